@@ -23,8 +23,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8z1.so")
 LIB_CHECKED = os.path.join(PKG, "libfp8z1_checked.so")
-SOURCES = ["layout.cpp", "fold.cu", "norm.cu", "step.cu", "step_full.cu", "step_pad.cu", "mx.cu"]
-HEADERS = ["internal.h", "checked.cuh", "update.cuh", "step_args.h", "step_kernel.cuh"]
+SOURCES = ["layout.cpp", "fold.cu", "norm.cu", "step.cu", "step_full.cu", "step_pad.cu", "mx.cu", "embed.cu", "ffn.cu",
+           "distill.cu"]
+HEADERS = ["internal.h", "checked.cuh", "update.cuh", "step_args.h", "step_kernel.cuh", "ops_common.cuh"]
+PUBLIC = ["fp8z1.h", "fp8z1_ops.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -54,7 +56,7 @@ def _stale(checked: bool) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [os.path.join(INCLUDE, "fp8z1.h")]
+    deps = [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [os.path.join(INCLUDE, h) for h in PUBLIC]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -34,6 +34,9 @@ LAYOUT_HOST_ONLY = 1
 DEVSTATUS_BADPTR = 1
 BUILD_CHECKED = 1
 
+F32, BF16 = 0, 1  # element types of the model operators' activations
+DISTILL_MAX_TOP = 1024
+
 OK, EINVAL, EALIGN, ENOMEM, ECUDA, ENODEV = 0, -1, -2, -3, -4, -5
 
 
@@ -72,6 +75,10 @@ class fp8z1_step_scalars(C.Structure):
 class fp8z1_loss_scaler(C.Structure):
     _fields_ = [("scale", C.c_float), ("step", C.c_int64), ("good_steps", C.c_int32),
                 ("growth_interval", C.c_int32)]
+
+
+class fp8z1_ffn_dims(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("tokens", "hidden", "inner", "experts")]
 
 
 BLOCK_DTYPE = np.dtype([("src_offset", "<i8"), ("param", "<i4"), ("expert", "<i4"),
@@ -127,6 +134,19 @@ _SIGS = {
     "fp8z1_checked_misses": (C.c_int, [C.POINTER(C.c_uint64)]),
     "fp8z1_checked_set_lut_entry": (C.c_int, [_P, C.c_int64, _P]),
     "fp8z1_norm_reset": (C.c_int, [_P, _P, _P]),
+    "fp8z1_embed": (C.c_int, [C.c_int64, C.c_int64, _P, _P, _P, C.c_int32, C.c_int64, C.c_float, _P, C.c_int32,
+                              C.c_int64, _P]),
+    "fp8z1_embed_grad_workspace": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.POINTER(C.c_int64)]),
+    "fp8z1_embed_grad": (C.c_int, [C.c_int64, C.c_int64, _P, C.c_int32, C.c_int64, C.c_float, _P, C.c_int32,
+                                   C.c_int64, _P, _P, _P]),
+    "fp8z1_ffn_sizes": (C.c_int, [C.POINTER(fp8z1_ffn_dims), C.POINTER(C.c_int64), C.POINTER(C.c_int64),
+                                  C.POINTER(C.c_int64)]),
+    "fp8z1_ffn_forward": (C.c_int, [C.POINTER(fp8z1_ffn_dims), _P, C.c_int64, _P, _P, _P, _P, _P, _P, C.c_int64, _P,
+                                    _P, _P]),
+    "fp8z1_ffn_backward": (C.c_int, [C.POINTER(fp8z1_ffn_dims), _P, C.c_int64, _P, C.c_int64, _P, _P, _P, _P, _P, _P,
+                                     _P, C.c_int64, _P, _P, _P, _P]),
+    "fp8z1_distill": (C.c_int, [_P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, _P, _P, C.c_int64, C.c_float, _P, _P,
+                                _P, C.c_int64, _P]),
     "fp8z1_strerror": (C.c_char_p, [C.c_int]),
 }
 
@@ -497,3 +517,55 @@ def fp8z1_clip_coef(sumsq: float, max_norm: float, loss_scale: float):
 
 def fp8z1_scaler_update(scaler: fp8z1_loss_scaler, found_inf: int):
     _check(lib().fp8z1_scaler_update(C.byref(scaler), int(found_inf)), "fp8z1_scaler_update")
+
+
+# ---- model operators (include/fp8z1_ops.h) -----------------------------------
+
+
+def fp8z1_embed(vocab: int, dim: int, codes, scales, ids, id_bytes: int, tokens: int, alpha: float, out,
+                out_type: int, ld_out: int, stream=None):
+    _check(lib().fp8z1_embed(int(vocab), int(dim), _ptr(codes), _ptr(scales), _ptr(ids), int(id_bytes), int(tokens),
+                             float(alpha), _ptr(out), int(out_type), int(ld_out), _stream(stream)), "fp8z1_embed")
+
+
+def fp8z1_embed_grad_workspace(vocab: int, dim: int, tokens: int) -> int:
+    n = C.c_int64()
+    _check(lib().fp8z1_embed_grad_workspace(int(vocab), int(dim), int(tokens), C.byref(n)),
+           "fp8z1_embed_grad_workspace")
+    return n.value
+
+
+def fp8z1_embed_grad(vocab: int, dim: int, ids, id_bytes: int, tokens: int, alpha: float, dy, dy_type: int,
+                     ld_dy: int, d_table, workspace, stream=None):
+    _check(lib().fp8z1_embed_grad(int(vocab), int(dim), _ptr(ids), int(id_bytes), int(tokens), float(alpha), _ptr(dy),
+                                  int(dy_type), int(ld_dy), _ptr(d_table), _ptr(workspace), _stream(stream)),
+           "fp8z1_embed_grad")
+
+
+def fp8z1_ffn_sizes(dims: fp8z1_ffn_dims):
+    """(saved, forward workspace, backward workspace) bytes."""
+    a, b, c = C.c_int64(), C.c_int64(), C.c_int64()
+    _check(lib().fp8z1_ffn_sizes(C.byref(dims), C.byref(a), C.byref(b), C.byref(c)), "fp8z1_ffn_sizes")
+    return a.value, b.value, c.value
+
+
+def fp8z1_ffn_forward(dims: fp8z1_ffn_dims, x, ld_x: int, d_offsets, gate_up, gate_up_scale, down, down_scale, y,
+                      ld_y: int, saved, workspace, stream=None):
+    _check(lib().fp8z1_ffn_forward(C.byref(dims), _ptr(x), int(ld_x), _ptr(d_offsets), _ptr(gate_up),
+                                   _ptr(gate_up_scale), _ptr(down), _ptr(down_scale), _ptr(y), int(ld_y), _ptr(saved),
+                                   _ptr(workspace), _stream(stream)), "fp8z1_ffn_forward")
+
+
+def fp8z1_ffn_backward(dims: fp8z1_ffn_dims, dy, ld_dy: int, x, ld_x: int, d_offsets, gate_up, gate_up_scale, down,
+                       down_scale, saved, dx, ld_dx: int, d_gate_up, d_down, workspace, stream=None):
+    _check(lib().fp8z1_ffn_backward(C.byref(dims), _ptr(dy), int(ld_dy), _ptr(x), int(ld_x), _ptr(d_offsets),
+                                    _ptr(gate_up), _ptr(gate_up_scale), _ptr(down), _ptr(down_scale), _ptr(saved),
+                                    _ptr(dx), int(ld_dx), _ptr(d_gate_up), _ptr(d_down), _ptr(workspace),
+                                    _stream(stream)), "fp8z1_ffn_backward")
+
+
+def fp8z1_distill(logits, type_: int, ld: int, rows: int, vocab: int, teacher_ids, teacher_logits, top: int,
+                  temperature: float, row_weight, loss, dlogits, ld_d: int, stream=None):
+    _check(lib().fp8z1_distill(_ptr(logits), int(type_), int(ld), int(rows), int(vocab), _ptr(teacher_ids),
+                               _ptr(teacher_logits), int(top), float(temperature), _ptr(row_weight), _ptr(loss),
+                               _ptr(dlogits), int(ld_d), _stream(stream)), "fp8z1_distill")
