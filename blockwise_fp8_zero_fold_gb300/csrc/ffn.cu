@@ -1,23 +1,55 @@
-// Gated feed-forward block on FP8 weights, forward and backward.
-#include "ops_common.cuh"
+// Gated feed-forward block on FP8 weights: entry points, the regrouping of
+// token rows into tiles, and the elementwise kernels between the products
+// (ffn_gemm.cu: products with FP8 weights; ffn_wgrad.cu: weight gradients).
+//
+// Forward:  plan, split x, gate_up (+ silu, product, encode), down.
+// Backward: plan, split dy, dh, the activation's backward with its encodings,
+//           FP16 copies of x and dy, dx, d_gate_up, d_down.
+#include <mutex>
+
+#include "ffn.cuh"
+
+namespace fp8z1 {
+namespace ffn {
+
+int tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+               const uint64_t* strides, const uint32_t* box)
+{
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return Encode(nullptr);
+        return reinterpret_cast<Encode>(fn);
+    }();
+    if (!encode) return FP8Z1_ECUDA;
+    cuuint64_t d[5], st[5];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        one[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return encode(map, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? FP8Z1_OK
+               : FP8Z1_ECUDA;
+}
+
+}  // namespace ffn
+}  // namespace fp8z1
 
 namespace {
 
 using namespace fp8z1;
-
-constexpr int kTile = 64, kStep = 16;
-
-// An FP8 weight [E, R, C] and its block scales.
-struct Weight {
-    const uint8_t* codes;
-    const float* scale;
-    int64_t R, C;
-    __device__ __forceinline__ float at(int64_t e, int64_t r, int64_t c) const
-    {
-        const int64_t sr = (R + 127) / 128, sc = (C + 127) / 128;
-        return e4m3_value(codes[(e * R + r) * C + c]) * scale[(e * sr + r / 128) * sc + c / 128];
-    }
-};
+using namespace fp8z1::ffn;
 
 struct Runs {
     const int32_t* offsets;  // NULL: one expert with every row
@@ -30,133 +62,210 @@ struct Runs {
     }
 };
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
-
-// D[m, n] = sum_k A(m, k) B(k, n) over a 64 x 64 tile; 256 threads, 4 x 4 each.
-template <class A, class B, class Out>
-__device__ __forceinline__ void product(int64_t m0, int64_t M, int64_t n0, int64_t N, int64_t K, const A& a,
-                                        const B& b, const Out& out)
+// The tiles of every expert.  Rows two experts claim (a table that does not
+// ascend) are bounded too: the launch holds at most `most` tiles.
+__global__ void __launch_bounds__(1024) plan_kernel(Runs runs, PlanBuffers p, int64_t most, Peaks* clear,
+                                                    const Peaks* from)
 {
-    __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-            const int k = i % kStep, m = i / kStep;
-            sa[k][m] = m0 + m < M && k0 + k < K ? a(m0 + m, k0 + k) : 0.0f;
-            const int n = i % kTile, kk = i / kTile;
-            sb[kk][n] = n0 + n < N && k0 + kk < K ? b(k0 + kk, n0 + n) : 0.0f;
-        }
+    __shared__ int32_t sums[1024];
+    const int e = threadIdx.x, n = (int)runs.experts;
+    int64_t lo = 0, hi = 0;
+    if (e < n) runs.get(e, lo, hi);
+    const int64_t mine = (hi - lo + kRows - 1) / kRows;
+    // a table that does not ascend could name more than `most` tiles: every expert's share ends there
+    sums[e] = (int32_t)min(mine, most);
+    __syncthreads();
+    for (int o = 1; o < 1024; o <<= 1) {
+        const int32_t add = e >= o ? sums[e - o] : 0;
         __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kStep; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
+        sums[e] = (int32_t)min((int64_t)sums[e] + add, most);
         __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m < M && n < N) out(m, n, acc[i][j]);
+    const int32_t first = e ? sums[e - 1] : 0, last = sums[e];
+    if (e < n) {
+        p.start[e] = first;
+        p.tokens[e] = (int32_t)min(hi - lo, (int64_t)(last - first) * kRows);
+        if (clear) {
+            Peaks c = {};
+            if (from) c = Peaks{from[e].x, from[e].gate, from[e].up, 0, 0, {0, 0, 0}};
+            clear[e] = c;
         }
+    }
+    if (e == n - 1) {
+        p.start[n] = last;
+        *p.n_tiles = last;
+    }
+    const int32_t total = sums[n - 1];
+    for (int32_t t = threadIdx.x; t < total; t += 1024) {
+        int a = 0, b = n - 1;  // the first expert whose tiles end after t
+        while (a < b) {
+            const int mid = (a + b) / 2;
+            if (sums[mid] > t)
+                b = mid;
+            else
+                a = mid + 1;
+        }
+        int64_t l, h;
+        runs.get(a, l, h);
+        const int64_t token0 = l + (int64_t)(t - (a ? sums[a - 1] : 0)) * kRows;
+        p.tiles[t] = Tile{a, (int32_t)token0, (int32_t)min(h - token0, (int64_t)kRows), 0};
+    }
 }
 
-using bf16 = __nv_bfloat16;
-
-// rows [lo, hi) x columns: gu = x gate_up
-__global__ void gate_up_kernel(Runs runs, const bf16* x, int64_t ld, Weight w, float* gu)
+__device__ __forceinline__ float2 bf16_pair(uint32_t two)
 {
-    int64_t lo, hi;
-    runs.get(blockIdx.z, lo, hi);
-    const int64_t m0 = (int64_t)blockIdx.y * kTile, e = blockIdx.z;
-    if (m0 >= hi - lo) return;
-    product(m0, hi - lo, (int64_t)blockIdx.x * kTile, w.C, w.R,
-            [&](int64_t m, int64_t k) { return to_float(x[(lo + m) * ld + k]); },
-            [&](int64_t k, int64_t n) { return w.at(e, k, n); },
-            [&](int64_t m, int64_t n, float v) { gu[(lo + m) * w.C + n] = v; });
+    return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
 }
 
-// y = (silu(g) * u) down; rows of no expert get zeros from expert 0's CTAs
-__global__ void down_kernel(Runs runs, const float* gu, Weight w, bf16* y, int64_t ld)
+// Rows of BF16 activations to FP8 pairs in the tiles' order (a warp a row,
+// 16 lanes a block of 128), with each expert's peak; rows of no expert are
+// zeroed in `rest`.
+__global__ void __launch_bounds__(256) split_kernel(Runs runs, Plan plan, const bf16* x, int64_t ld, int64_t H,
+                                                    Pairs out, int64_t rows, Peaks* peaks, bool dy, bf16* rest,
+                                                    int64_t ld_rest)
 {
-    int64_t lo, hi;
-    runs.get(blockIdx.z, lo, hi);
-    const int64_t m0 = (int64_t)blockIdx.y * kTile, e = blockIdx.z, F = w.R;
-    if (m0 >= hi - lo) return;
-    product(m0, hi - lo, (int64_t)blockIdx.x * kTile, w.C, F,
-            [&](int64_t m, int64_t k) {
-                const float* p = gu + (lo + m) * 2 * F;
-                return silu(p[k]) * p[F + k];
-            },
-            [&](int64_t k, int64_t n) { return w.at(e, k, n); },
-            [&](int64_t m, int64_t n, float v) { y[(lo + m) * ld + n] = __float2bfloat16_rn(v); });
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t n_rows = (int64_t)*plan.n_tiles * kRows;
+    if (rest) {
+        int64_t lo, hi;
+        runs.get(runs.experts - 1, lo, hi);
+        for (int64_t r = hi + warp; r < runs.tokens; r += (int64_t)gridDim.x * 8)
+            for (int64_t c = lane * 8; c < H; c += 256)
+                *reinterpret_cast<uint4*>(rest + r * ld_rest + c) = make_uint4(0, 0, 0, 0);
+    }
+    if (warp >= n_rows) return;
+    const Tile t = plan.tiles[warp / kRows];
+    const int r = (int)(warp % kRows);
+    const bf16* src = x + (int64_t)(t.token0 + r) * ld;
+    float top = 0.0f;
+    for (int64_t c = lane * 8; c < out.pitch; c += 256) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < t.rows && c < H) v = __ldg(reinterpret_cast<const uint4*>(src + c));
+        const float2 f[4] = {bf16_pair(v.x), bf16_pair(v.y), bf16_pair(v.z), bf16_pair(v.w)};
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
+        top = fmaxf(top, amax);
+        const unsigned live = __activemask();  // pitch is a multiple of 128: 16 lanes are in or out together
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(live, amax, o));
+        const PairScale ps = pair_scale(amax);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pair_encode(f[i].x, f[i].y, ps.up, hi[i], lo[i]);
+        *reinterpret_cast<uint2*>(out.hi + warp * out.pitch + c) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *reinterpret_cast<uint2*>(out.lo + warp * out.pitch + c) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        if ((lane & 15) == 0) out.scale[c / kBlock * rows + warp] = ps.down;
+    }
+    if (peaks && r < t.rows) {
+        const uint32_t p = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        if (lane == 0) atomicMax(dy ? &peaks[t.expert].dy : &peaks[t.expert].x, p);
+    }
 }
 
-__global__ void zero_rest_kernel(Runs runs, bf16* y, int64_t ld, int64_t cols)
+__device__ __forceinline__ uint32_t half_pair(float a, float b)
 {
-    int64_t lo, hi;
-    runs.get(runs.experts - 1, lo, hi);
-    for (int64_t r = hi + blockIdx.x; r < runs.tokens; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < cols; c += blockDim.x) y[r * ld + c] = __float2bfloat16_rn(0.0f);
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// dgu = [dg | du] from dh = dy down^T
-__global__ void dgu_kernel(Runs runs, const bf16* dy, int64_t ld, Weight w, const float* gu, float* dgu)
+// Rows of x and dy to FP16 in the tiles' order, each expert's at its power of two.
+__global__ void __launch_bounds__(256) halves_kernel(Plan plan, const bf16* x, int64_t ld_x, const bf16* dy,
+                                                     int64_t ld_dy, int64_t H, int64_t pitch, __half* x16,
+                                                     __half* dy16, const Peaks* peaks)
 {
-    int64_t lo, hi;
-    runs.get(blockIdx.z, lo, hi);
-    const int64_t m0 = (int64_t)blockIdx.y * kTile, e = blockIdx.z, F = w.R;
-    if (m0 >= hi - lo) return;
-    product(m0, hi - lo, (int64_t)blockIdx.x * kTile, F, w.C,
-            [&](int64_t m, int64_t k) { return to_float(dy[(lo + m) * ld + k]); },
-            [&](int64_t k, int64_t n) { return w.at(e, n, k); },
-            [&](int64_t m, int64_t n, float dh) {
-                const int64_t at = (lo + m) * 2 * F + n;
-                const float g = gu[at], u = gu[at + F], s = 1.0f / (1.0f + expf(-g));
-                dgu[at] = dh * u * s * (1.0f + g * (1.0f - s));
-                dgu[at + F] = dh * (g * s);
-            });
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (warp >= (int64_t)*plan.n_tiles * kRows) return;
+    const Tile t = plan.tiles[warp / kRows];
+    const int r = (int)(warp % kRows);
+    const Peaks p = peaks[t.expert];
+    const Pow2 fx = pow2(x_shift(p)), fd = pow2(dy_shift(p));
+    const bf16* sx = x + (int64_t)(t.token0 + r) * ld_x;
+    const bf16* sd = dy + (int64_t)(t.token0 + r) * ld_dy;
+    for (int64_t c = lane * 8; c < pitch; c += 256) {
+        uint4 vx = make_uint4(0, 0, 0, 0), vd = vx;
+        if (r < t.rows && c < H) {
+            vx = __ldg(reinterpret_cast<const uint4*>(sx + c));
+            vd = __ldg(reinterpret_cast<const uint4*>(sd + c));
+        }
+        const uint32_t wx[4] = {vx.x, vx.y, vx.z, vx.w}, wd[4] = {vd.x, vd.y, vd.z, vd.w};
+        uint32_t ox[4], od[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = bf16_pair(wx[i]), b = bf16_pair(wd[i]);
+            ox[i] = half_pair(fx.times(a.x), fx.times(a.y));
+            od[i] = half_pair(fd.times(b.x), fd.times(b.y));
+        }
+        *reinterpret_cast<uint4*>(x16 + warp * pitch + c) = make_uint4(ox[0], ox[1], ox[2], ox[3]);
+        *reinterpret_cast<uint4*>(dy16 + warp * pitch + c) = make_uint4(od[0], od[1], od[2], od[3]);
+    }
 }
 
-__global__ void dx_kernel(Runs runs, const float* dgu, Weight w, bf16* dx, int64_t ld)
+// v as two FP16 numbers, four at a time
+__device__ __forceinline__ void store_halves(__half* hi, __half* lo, const Pow2& f, const float4& v)
 {
-    int64_t lo, hi;
-    runs.get(blockIdx.z, lo, hi);
-    const int64_t m0 = (int64_t)blockIdx.y * kTile, e = blockIdx.z;
-    if (m0 >= hi - lo) return;
-    product(m0, hi - lo, (int64_t)blockIdx.x * kTile, w.R, w.C,
-            [&](int64_t m, int64_t k) { return dgu[(lo + m) * w.C + k]; },
-            [&](int64_t k, int64_t n) { return w.at(e, n, k); },
-            [&](int64_t m, int64_t n, float v) { dx[(lo + m) * ld + n] = __float2bfloat16_rn(v); });
+    const float a = f.times(v.x), b = f.times(v.y), c = f.times(v.z), d = f.times(v.w);
+    const __half2 h0 = __floats2half2_rn(a, b), h1 = __floats2half2_rn(c, d);
+    *reinterpret_cast<uint2*>(hi) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+    const float2 g0 = __half22float2(h0), g1 = __half22float2(h1);
+    *reinterpret_cast<uint2*>(lo) = make_uint2(half_pair(a - g0.x, b - g0.y), half_pair(c - g1.x, d - g1.y));
 }
 
-__global__ void d_gate_up_kernel(Runs runs, const bf16* x, int64_t ld, const float* dgu, float* out, int64_t H,
-                                 int64_t F2)
+// dg, du and h of 32 rows x 128 columns: read with lanes along rows (as the
+// products wrote them), turned in shared memory, written with lanes along
+// columns: [dg | du] as FP8 pairs for dx and as FP16 pairs for d_gate_up, h as
+// FP16 pairs for d_down.
+constexpr int kActPitch = 132;
+__global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float* gu, const float* dh, int64_t F,
+                                                         int64_t rows, Pairs pairs, __half* dgu_hi, __half* dgu_lo,
+                                                         __half* h_hi, __half* h_lo, const Peaks* peaks)
 {
-    int64_t lo, hi;
-    runs.get(blockIdx.z, lo, hi);
-    float* o = out + blockIdx.z * H * F2;
-    product((int64_t)blockIdx.y * kTile, H, (int64_t)blockIdx.x * kTile, F2, hi - lo,
-            [&](int64_t m, int64_t k) { return to_float(x[(lo + k) * ld + m]); },
-            [&](int64_t k, int64_t n) { return dgu[(lo + k) * F2 + n]; },
-            [&](int64_t m, int64_t n, float v) { o[m * F2 + n] = v; });
-}
-
-__global__ void d_down_kernel(Runs runs, const float* gu, const bf16* dy, int64_t ld, float* out, int64_t F,
-                              int64_t H)
-{
-    int64_t lo, hi;
-    runs.get(blockIdx.z, lo, hi);
-    float* o = out + blockIdx.z * F * H;
-    product((int64_t)blockIdx.y * kTile, F, (int64_t)blockIdx.x * kTile, H, hi - lo,
-            [&](int64_t m, int64_t k) {
-                const float* p = gu + (lo + k) * 2 * F;
-                return silu(p[m]) * p[F + m];
-            },
-            [&](int64_t k, int64_t n) { return to_float(dy[(lo + k) * ld + n]); },
-            [&](int64_t m, int64_t n, float v) { o[m * H + n] = v; });
+    extern __shared__ float act[];  // [3][32][kActPitch]
+    const int64_t tile = blockIdx.x >> 2;
+    if (tile >= *plan.n_tiles) return;
+    const int quarter = blockIdx.x & 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t f0 = (int64_t)blockIdx.y * 128;
+    const float* pg = gu + (tile * 2 * F + f0) * kRows + quarter * 32 + lane;
+    const float* pu = pg + F * kRows;
+    const float* pd = dh + (tile * F + f0) * kRows + quarter * 32 + lane;
+#pragma unroll 8
+    for (int i = 0; i < 16; ++i) {
+        const int c = warp * 16 + i;
+        const float g = __ldcs(pg + c * kRows), u = __ldcs(pu + c * kRows), d = __ldcs(pd + c * kRows);
+        const float s = 1.0f / (1.0f + expf(-g)), a = g * s;
+        float* o = act + lane * kActPitch + c;
+        o[0] = d * u * s * (1.0f + g * (1.0f - s));
+        o[32 * kActPitch] = d * a;
+        o[64 * kActPitch] = a * u;
+    }
+    __syncthreads();
+    const Peaks p = peaks[plan.tiles[tile].expert];
+    const Pow2 fg = pow2(dgu_shift(p)), fh = pow2(h_shift(p));
+    for (int r = warp; r < 32; r += 8) {
+        const int64_t at = tile * kRows + quarter * 32 + r;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float4 v = *reinterpret_cast<const float4*>(act + (half * 32 + r) * kActPitch + lane * 4);
+            const int64_t col = half * F + f0 + lane * 4;
+            store_halves(dgu_hi + at * 2 * F + col, dgu_lo + at * 2 * F + col, fg, v);
+            if (pairs.hi) {
+                float amax = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+                amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+                const PairScale ps = pair_scale(amax);
+                uint32_t h0, l0, h1, l1;
+                pair_encode(v.x, v.y, ps.up, h0, l0);
+                pair_encode(v.z, v.w, ps.up, h1, l1);
+                *reinterpret_cast<uint32_t*>(pairs.hi + at * pairs.pitch + col) = h0 | h1 << 16;
+                *reinterpret_cast<uint32_t*>(pairs.lo + at * pairs.pitch + col) = l0 | l1 << 16;
+                if (lane == 0) pairs.scale[(half * F + f0) / kBlock * rows + at] = ps.down;
+            }
+        }
+        const float4 v = *reinterpret_cast<const float4*>(act + (64 + r) * kActPitch + lane * 4);
+        store_halves(h_hi + at * F + f0 + lane * 4, h_lo + at * F + f0 + lane * 4, fh, v);
+    }
 }
 
 int check_dims(const fp8z1_ffn_dims* d)
@@ -183,85 +292,128 @@ int check_weights(const fp8z1_ffn_dims* d, const int32_t* off, const uint8_t* gu
                : FP8Z1_EALIGN;
 }
 
-unsigned tiles(int64_t n) { return (unsigned)ceil_div(n, kTile); }
+Dims dims_of(const fp8z1_ffn_dims* d) { return Dims{d->tokens, d->hidden, d->inner, d->experts}; }
 
 }  // namespace
 
-extern "C" int fp8z1_ffn_sizes(const fp8z1_ffn_dims* d, int64_t* saved_bytes, int64_t* forward_bytes,
+extern "C" int fp8z1_ffn_sizes(const fp8z1_ffn_dims* dims, int64_t* saved_bytes, int64_t* forward_bytes,
                                int64_t* backward_bytes)
 {
-    const int st = check_dims(d);
+    const int st = check_dims(dims);
     if (st != FP8Z1_OK) return st;
     if (!saved_bytes || !forward_bytes || !backward_bytes) return FP8Z1_EINVAL;
-    *saved_bytes = *forward_bytes = *backward_bytes = align256(d->tokens * 2 * d->inner * 4) + 256;
+    const Dims d = dims_of(dims);
+    Cut saved(nullptr), forward(nullptr), backward(nullptr);
+    Saved().cut(saved, d);
+    Forward().cut(forward, d);
+    Backward().cut(backward, d);
+    *saved_bytes = saved.at;
+    *forward_bytes = forward.at;
+    *backward_bytes = backward.at;
     return FP8Z1_OK;
 }
 
-extern "C" int fp8z1_ffn_forward(const fp8z1_ffn_dims* d, const void* x, int64_t ld_x, const int32_t* d_offsets,
+extern "C" int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int64_t ld_x, const int32_t* d_offsets,
                                  const uint8_t* gate_up, const float* gate_up_scale, const uint8_t* down,
                                  const float* down_scale, void* y, int64_t ld_y, void* saved, void* workspace,
                                  void* stream)
 {
-    int st = check_dims(d);
+    int st = check_dims(dims);
     if (st != FP8Z1_OK) return st;
-    if (d->tokens == 0) return FP8Z1_OK;
-    if ((st = check_weights(d, d_offsets, gate_up, gate_up_scale, down, down_scale)) != FP8Z1_OK) return st;
-    if ((st = check_rows(x, ld_x, d->hidden)) != FP8Z1_OK || (st = check_rows(y, ld_y, d->hidden)) != FP8Z1_OK) return st;
+    if ((st = check_weights(dims, d_offsets, gate_up, gate_up_scale, down, down_scale)) != FP8Z1_OK) return st;
+    const Dims d = dims_of(dims);
+    if (d.T == 0) return FP8Z1_OK;
+    if ((st = check_rows(x, ld_x, d.H)) != FP8Z1_OK || (st = check_rows(y, ld_y, d.H)) != FP8Z1_OK) return st;
     if (!workspace) return FP8Z1_EINVAL;
     if (!aligned(saved, 256) || !aligned(workspace, 256)) return FP8Z1_EALIGN;
-    NvtxRange r("fp8z1_ffn_forward");
+    NvtxRange range("fp8z1_ffn_forward");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Runs runs{d_offsets, d->tokens, d->experts};
-    const Weight wgu{gate_up, gate_up_scale, d->hidden, 2 * d->inner}, wd{down, down_scale, d->inner, d->hidden};
-    float* gu = static_cast<float*>(saved ? saved : workspace);
-    const unsigned E = (unsigned)d->experts, mt = tiles(d->tokens);
+    const Runs runs{d_offsets, d.T, d.E};
+    const Weight wgu{gate_up, gate_up_scale, d.H, 2 * d.F}, wd{down, down_scale, d.F, d.H};
+    Cut cw(workspace), cs(saved);
+    Forward f;
+    f.cut(cw, d);
+    Saved keep = {};
+    if (saved) keep.cut(cs, d);
+    const Plan plan = f.plan.plan();
+    const unsigned row_ctas = (unsigned)ceil_div(d.rows(), 8);
     count_launch();
-    gate_up_kernel<<<dim3(tiles(wgu.C), mt, E), 256, 0, s>>>(runs, static_cast<const bf16*>(x), ld_x, wgu, gu);
+    plan_kernel<<<1, 1024, 0, s>>>(runs, f.plan, d.tiles(), keep.peaks, nullptr);
     count_launch();
-    down_kernel<<<dim3(tiles(wd.C), mt, E), 256, 0, s>>>(runs, gu, wd, static_cast<bf16*>(y), ld_y);
-    count_launch();
-    zero_rest_kernel<<<64, 256, 0, s>>>(runs, static_cast<bf16*>(y), ld_y, d->hidden);
-    return launch_status();
+    split_kernel<<<row_ctas, 256, 0, s>>>(runs, plan, static_cast<const bf16*>(x), ld_x, d.H, f.x, d.rows(), keep.peaks,
+                                          false, static_cast<bf16*>(y), ld_y);
+    if ((st = launch_status()) != FP8Z1_OK ||
+        (st = launch_gate_up(d, plan, f.x, wgu, f.h, keep.gu, keep.peaks, s)) != FP8Z1_OK)
+        return st;
+    return launch_down(d, plan, f.h, wd, static_cast<bf16*>(y), ld_y, s);
 }
 
-extern "C" int fp8z1_ffn_backward(const fp8z1_ffn_dims* d, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
-                                  const int32_t* d_offsets, const uint8_t* gate_up, const float* gate_up_scale,
-                                  const uint8_t* down, const float* down_scale, const void* saved, void* dx,
-                                  int64_t ld_dx, float* d_gate_up, float* d_down, void* workspace, void* stream)
+extern "C" int fp8z1_ffn_backward(const fp8z1_ffn_dims* dims, const void* dy, int64_t ld_dy, const void* x,
+                                  int64_t ld_x, const int32_t* d_offsets, const uint8_t* gate_up,
+                                  const float* gate_up_scale, const uint8_t* down, const float* down_scale,
+                                  const void* saved, void* dx, int64_t ld_dx, float* d_gate_up, float* d_down,
+                                  void* workspace, void* stream)
 {
-    int st = check_dims(d);
+    int st = check_dims(dims);
     if (st != FP8Z1_OK) return st;
-    if ((st = check_weights(d, d_offsets, gate_up, gate_up_scale, down, down_scale)) != FP8Z1_OK) return st;
+    if ((st = check_weights(dims, d_offsets, gate_up, gate_up_scale, down, down_scale)) != FP8Z1_OK) return st;
     if (!d_gate_up || !d_down) return FP8Z1_EINVAL;
     if (!aligned(d_gate_up, 16) || !aligned(d_down, 16)) return FP8Z1_EALIGN;
-    if (d->tokens > 0) {
-        if ((st = check_rows(x, ld_x, d->hidden)) != FP8Z1_OK || (st = check_rows(dy, ld_dy, d->hidden)) != FP8Z1_OK ||
-            (dx && (st = check_rows(dx, ld_dx, d->hidden)) != FP8Z1_OK))
-            return st;
-        if (!saved || !workspace) return FP8Z1_EINVAL;
-        if (!aligned(saved, 256) || !aligned(workspace, 256)) return FP8Z1_EALIGN;
-    }
-    NvtxRange r("fp8z1_ffn_backward");
+    const Dims d = dims_of(dims);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Runs runs{d_offsets, d->tokens, d->experts};
-    const Weight wgu{gate_up, gate_up_scale, d->hidden, 2 * d->inner}, wd{down, down_scale, d->inner, d->hidden};
-    const float* gu = static_cast<const float*>(saved);
-    float* dgu = static_cast<float*>(workspace);
-    const bf16 *xb = static_cast<const bf16*>(x), *dyb = static_cast<const bf16*>(dy);
-    const unsigned E = (unsigned)d->experts, mt = tiles(d->tokens);
-    if (d->tokens > 0) {
-        count_launch();
-        dgu_kernel<<<dim3(tiles(d->inner), mt, E), 256, 0, s>>>(runs, dyb, ld_dy, wd, gu, dgu);
-        if (dx) {
-            count_launch();
-            dx_kernel<<<dim3(tiles(d->hidden), mt, E), 256, 0, s>>>(runs, dgu, wgu, static_cast<bf16*>(dx), ld_dx);
-            count_launch();
-            zero_rest_kernel<<<64, 256, 0, s>>>(runs, static_cast<bf16*>(dx), ld_dx, d->hidden);
-        }
+    if (d.T == 0) {
+        if (cudaMemsetAsync(d_gate_up, 0, (size_t)(d.E * d.H * 2 * d.F) * 4, s) != cudaSuccess ||
+            cudaMemsetAsync(d_down, 0, (size_t)(d.E * d.F * d.H) * 4, s) != cudaSuccess)
+            return FP8Z1_ECUDA;
+        return FP8Z1_OK;
     }
+    if ((st = check_rows(x, ld_x, d.H)) != FP8Z1_OK || (st = check_rows(dy, ld_dy, d.H)) != FP8Z1_OK ||
+        (dx && (st = check_rows(dx, ld_dx, d.H)) != FP8Z1_OK))
+        return st;
+    if (!saved || !workspace) return FP8Z1_EINVAL;
+    if (!aligned(saved, 256) || !aligned(workspace, 256)) return FP8Z1_EALIGN;
+    NvtxRange range("fp8z1_ffn_backward");
+    const Runs runs{d_offsets, d.T, d.E};
+    const Weight wgu{gate_up, gate_up_scale, d.H, 2 * d.F}, wd{down, down_scale, d.F, d.H};
+    Cut cw(workspace), cs(const_cast<void*>(saved));
+    Backward b;
+    b.cut(cw, d);
+    Saved keep;
+    keep.cut(cs, d);
+    const Plan plan = b.plan.plan();
+    const bf16 *xb = static_cast<const bf16*>(x), *dyb = static_cast<const bf16*>(dy);
+    const unsigned row_ctas = (unsigned)ceil_div(d.rows(), 8);
     count_launch();
-    d_gate_up_kernel<<<dim3(tiles(wgu.C), tiles(wgu.R), E), 256, 0, s>>>(runs, xb, ld_x, dgu, d_gate_up, wgu.R, wgu.C);
+    plan_kernel<<<1, 1024, 0, s>>>(runs, b.plan, d.tiles(), b.peaks, keep.peaks);
     count_launch();
-    d_down_kernel<<<dim3(tiles(wd.C), tiles(wd.R), E), 256, 0, s>>>(runs, gu, dyb, ld_dy, d_down, wd.R, wd.C);
-    return launch_status();
+    split_kernel<<<row_ctas, 256, 0, s>>>(runs, plan, dyb, ld_dy, d.H, b.dy, d.rows(), b.peaks, true,
+                                          static_cast<bf16*>(dx), ld_dx);
+    if ((st = launch_status()) != FP8Z1_OK || (st = launch_dh(d, plan, b.dy, wd, b.dh, b.peaks, s)) != FP8Z1_OK)
+        return st;
+    Pairs pairs = b.dgu;
+    if (!dx) pairs.hi = nullptr;
+    constexpr int kActSmem = 3 * 32 * kActPitch * 4;
+    if (cudaFuncSetAttribute(activation_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kActSmem) != cudaSuccess)
+        return FP8Z1_ECUDA;
+    count_launch();
+    activation_kernel<<<dim3((unsigned)(d.tiles() * 4), (unsigned)(d.F / 128)), 256, kActSmem, s>>>(
+        plan, keep.gu, b.dh, d.F, d.rows(), pairs, b.dgu_hi, b.dgu_lo, b.h_hi, b.h_lo, b.peaks);
+    count_launch();
+    halves_kernel<<<row_ctas, 256, 0, s>>>(plan, xb, ld_x, dyb, ld_dy, d.H, d.Hp(), b.x16, b.dy16, b.peaks);
+    if ((st = launch_status()) != FP8Z1_OK) return st;
+    if (dx && (st = launch_dx(d, plan, b.dgu, wgu, static_cast<bf16*>(dx), ld_dx, s)) != FP8Z1_OK) return st;
+    if ((st = launch_d_gate_up(d, plan, b, b.peaks, d_gate_up, s)) != FP8Z1_OK) return st;
+    return launch_d_down(d, plan, b, b.peaks, d_down, s);
+}
+
+extern "C" int fp8z1_ffn_timeouts(uint32_t* count)
+{
+    if (!count) return FP8Z1_EINVAL;
+    unsigned a = 0, b = 0;
+    const int st = take_timeouts_gemm(&a);
+    if (st != FP8Z1_OK) return st;
+    const int st2 = take_timeouts_wgrad(&b);
+    if (st2 != FP8Z1_OK) return st2;
+    *count = a + b;
+    return FP8Z1_OK;
 }

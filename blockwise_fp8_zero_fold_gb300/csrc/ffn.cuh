@@ -1,0 +1,226 @@
+// The gated feed-forward block's buffers, shared by its translation units.
+//
+// Token rows are regrouped so that every expert starts a tile of 128 rows:
+// tile t of the launch holds rows [token0, token0 + rows) of its expert, and
+// row r of it is row 128 t + r of every internal buffer (rows past the
+// expert's end are zeros).  The tensor core products then never read another
+// expert's rows.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "ops_common.cuh"
+#include "tc.cuh"
+
+namespace fp8z1 {
+namespace ffn {
+
+constexpr int kRows = 128;      // token rows of a tile
+constexpr int kBlock = 128;     // the scale blocks' side, and a K step of the FP8 products
+
+struct Tile {
+    int32_t expert, token0, rows, pad;
+};
+
+// Per expert: the bits of the largest magnitudes (as non-negative floats).
+struct Peaks {
+    uint32_t x, gate, up, dy, dh;
+    uint32_t pad[3];
+};
+
+// Which rows belong to whom; written by the plan kernel.
+struct Plan {
+    const int32_t* n_tiles;
+    const int32_t* start;   // [experts + 1] first tile of each expert
+    const int32_t* tokens;  // [experts] rows of each
+    const Tile* tiles;      // [n_tiles]
+};
+
+// FP8 pairs: value = (hi + lo) * scale[k / 128][row]
+struct Pairs {
+    uint8_t *hi, *lo;  // [rows, pitch]
+    float* scale;      // [pitch / 128, rows]
+    int64_t pitch;
+};
+
+struct Dims {
+    int64_t T, H, F, E;
+    int64_t tiles() const { return T / kRows + (E < T ? E : T); }  // at most
+    int64_t rows() const { return tiles() * kRows; }
+    int64_t Hp() const { return (H + 127) / 128 * 128; }
+};
+
+// Buffers cut from one allocation, 256 bytes apart.
+struct Cut {
+    char* base;
+    int64_t at = 0;
+    explicit Cut(void* p) : base(static_cast<char*>(p)) {}
+    template <class T>
+    T* take(int64_t n)
+    {
+        T* p = base ? reinterpret_cast<T*>(base + at) : nullptr;
+        at += align256(n * (int64_t)sizeof(T));
+        return p;
+    }
+};
+
+struct PlanBuffers {
+    int32_t *n_tiles, *start, *tokens;
+    Tile* tiles;
+    void cut(Cut& c, const Dims& d)
+    {
+        n_tiles = c.take<int32_t>(1);
+        start = c.take<int32_t>(d.E + 1);
+        tokens = c.take<int32_t>(d.E);
+        tiles = c.take<Tile>(d.tiles());
+    }
+    Plan plan() const { return Plan{n_tiles, start, tokens, tiles}; }
+};
+
+inline Pairs cut_pairs(Cut& c, int64_t rows, int64_t pitch)
+{
+    Pairs p;
+    p.hi = c.take<uint8_t>(rows * pitch);
+    p.lo = c.take<uint8_t>(rows * pitch);
+    p.scale = c.take<float>(rows * (pitch / kBlock));
+    p.pitch = pitch;
+    return p;
+}
+
+// What a forward pass keeps: g | u in FP32 as [tile][column of 2F][row of 128]
+// (a warp's 32 rows are consecutive), and each expert's peaks.
+struct Saved {
+    Peaks* peaks;
+    float* gu;
+    void cut(Cut& c, const Dims& d)
+    {
+        peaks = c.take<Peaks>(d.E);
+        gu = c.take<float>(d.rows() * 2 * d.F);
+    }
+};
+
+struct Forward {
+    PlanBuffers plan;
+    Pairs x, h;
+    void cut(Cut& c, const Dims& d)
+    {
+        plan.cut(c, d);
+        x = cut_pairs(c, d.rows(), d.Hp());
+        h = cut_pairs(c, d.rows(), d.F);
+    }
+};
+
+struct Backward {
+    PlanBuffers plan;
+    Peaks* peaks;
+    Pairs dy, dgu;
+    float* dh;           // [tile][column of F][row of 128]
+    __half *x16, *dy16;  // [rows, Hp]
+    __half *h_hi, *h_lo;      // [rows, F]
+    __half *dgu_hi, *dgu_lo;  // [rows, 2F]
+    void cut(Cut& c, const Dims& d)
+    {
+        plan.cut(c, d);
+        peaks = c.take<Peaks>(d.E);
+        dy = cut_pairs(c, d.rows(), d.Hp());
+        dgu = cut_pairs(c, d.rows(), 2 * d.F);
+        dh = c.take<float>(d.rows() * d.F);
+        x16 = c.take<__half>(d.rows() * d.Hp());
+        dy16 = c.take<__half>(d.rows() * d.Hp());
+        h_hi = c.take<__half>(d.rows() * d.F);
+        h_lo = c.take<__half>(d.rows() * d.F);
+        dgu_hi = c.take<__half>(d.rows() * 2 * d.F);
+        dgu_lo = c.take<__half>(d.rows() * 2 * d.F);
+    }
+};
+
+struct Weight {
+    const uint8_t* codes;
+    const float* scale;
+    int64_t R, C;  // of one expert
+};
+
+using bf16 = __nv_bfloat16;
+
+// An FP8 pair carries BF16's 8 significant bits: hi = e4m3(v), lo = e5m2(v - hi),
+// for v scaled by a power of two so that the largest of its 128 lies in
+// [128, 256).  hi leaves at most 8 units of a BF16 value's last place, and
+// E5M2's 3 bits hold every number of units up to 8: a BF16 value down to 2^-13
+// of the largest one is held exactly, a smaller one to 2^-21 of it.  (With lo
+// in E4M3 the exact range ended at 2^-10 and the rest at 2^-18: an outlier
+// channel 300 times the others then cost the weight gradients 2.4e-5.)  Any
+// other FP32 value is held to BF16's 2^-8.
+struct PairScale {
+    float up, down;  // multiply by `up` to encode, by `down` to decode
+};
+__device__ __forceinline__ PairScale pair_scale(float amax)
+{
+    uint32_t e = __float_as_uint(amax) >> 23;  // amax >= 0
+    e = min(max(e, 8u), 254u);
+    return PairScale{__uint_as_float((261u - e) << 23), __uint_as_float((e - 7u) << 23)};
+}
+__device__ __forceinline__ uint32_t e5m2x2(float lo, float hi)
+{
+    unsigned short r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// v's pair as two codes each for (a, b): bits 0-15 of hi and lo.  Infinities
+// become NaN (E4M3 has none).
+__device__ __forceinline__ void pair_encode(float a, float b, float up, uint32_t& hi, uint32_t& lo)
+{
+    a = fmaf(a, up, a - a);
+    b = fmaf(b, up, b - b);
+    hi = e4m3x2(a, b);
+    const float2 h = e4m3x2_decode(hi);
+    lo = e5m2x2(a - h.x, b - h.y);
+}
+
+// 2^k as two factors, for |k| <= 252
+struct Pow2 {
+    float a, b;
+    __device__ __forceinline__ float times(float v) const { return v * a * b; }
+};
+__device__ __forceinline__ Pow2 pow2(int k)
+{
+    k = min(max(k, -252), 252);
+    const int h = k / 2;
+    return Pow2{__uint_as_float((uint32_t)(127 + h) << 23), __uint_as_float((uint32_t)(127 + k - h) << 23)};
+}
+// floor(log2) of a positive float's bits (-127 for 0 and subnormals, 128 for inf)
+__device__ __forceinline__ int exponent(uint32_t bits) { return (int)(bits >> 23) - 127; }
+
+// The powers of two that bring an expert's FP16 operands below 2^15.
+//   |x| < 2^(ex + 1);  |dg| <= 1.1 |dh u| and |du| <= |dh g|;  |h| <= |g u|.
+__device__ __forceinline__ int x_shift(const Peaks& p) { return 14 - exponent(p.x); }
+__device__ __forceinline__ int dy_shift(const Peaks& p) { return 14 - exponent(p.dy); }
+__device__ __forceinline__ int dgu_shift(const Peaks& p)
+{
+    return 12 - exponent(p.dh) - max(exponent(p.gate), exponent(p.up));
+}
+__device__ __forceinline__ int h_shift(const Peaks& p) { return 13 - exponent(p.gate) - exponent(p.up); }
+
+// ---- launches (each returns a status) -------------------------------------------
+
+// The FP8 products of one K-blocked shape; see ffn_gemm.cu.
+int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w, const Pairs& h, float* gu,
+                   Peaks* peaks, cudaStream_t s);
+int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, cudaStream_t s);
+int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, float* dh, Peaks* peaks, cudaStream_t s);
+int launch_dx(const Dims& d, const Plan& p, const Pairs& dgu, const Weight& w, bf16* dx, int64_t ld, cudaStream_t s);
+// The weight gradients; see ffn_wgrad.cu.
+int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
+int launch_d_down(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
+
+// A tensor map over `rank` dimensions (innermost first; strides in bytes of
+// dimensions 1..), 128-byte swizzle.  Returns a status.
+int tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+               const uint64_t* strides, const uint32_t* box);
+
+// Waits that ran out in each translation unit's kernels on the current device
+// since the last call (synchronous).  Returns a status.
+int take_timeouts_gemm(unsigned* n);
+int take_timeouts_wgrad(unsigned* n);
+
+}  // namespace ffn
+}  // namespace fp8z1

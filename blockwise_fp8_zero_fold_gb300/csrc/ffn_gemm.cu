@@ -1,0 +1,428 @@
+// The four products of token rows with FP8 weights:
+//
+//   gate_up  g | u = x [Wg | Wu], then h = silu(g) u, encoded for the next product
+//   down     y = h Wd
+//   dh       dh = dy Wd^T
+//   dx       dx = [dg | du] [Wg | Wu]^T
+//
+// A row operand a is a pair of FP8 numbers at a power of two per (row, 128 of
+// k): a = 2^s (hi + lo), E4M3 and E5M2, which carries BF16's 8 bits exactly, so
+// the FP8 codes of a weight enter the tensor cores as they are:
+//
+//   sum_k a_k w_k c_kn = sum over blocks b of  2^s_b c_bn  sum_{k in b} (hi + lo)_k w_kn.
+//
+// Two FP8 products cost what one BF16 product does, and no weight is
+// converted.  The inner sums are exact products accumulated in FP32 in tensor
+// memory, 128 of k at a time; epilogue warps scale each and add it to the
+// tile's sums in registers (FP32) while the next 128 are multiplied.
+//
+// A CTA owns 128 rows x 256 columns.  Warp 0 issues TMA copies of K steps
+// (64 KB: the rows' hi and lo, 256 weight columns) three steps ahead, warp 1
+// the products into one of two 256-column accumulators, 8 warps add up.
+// CTAs are persistent; tiles run expert by expert, a column's row tiles next
+// to each other, so that an expert's codes are read from memory once.
+#include "ffn.cuh"
+
+namespace fp8z1 {
+namespace ffn {
+namespace {
+
+using namespace tc;
+
+__device__ unsigned g_timeouts;
+
+enum Mode { kGateUp, kDown, kDh, kDx };
+
+constexpr int kCols = 256;   // columns of a tile, in two chunks of 128
+constexpr int kStages = 3;
+constexpr int kThreads = 384;
+constexpr uint32_t kOperand = 128 * 128;          // bytes of a 128 x 128 operand tile
+constexpr uint32_t kStageBytes = 4 * kOperand;    // hi, lo, two chunks of the weight
+constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 4096;
+
+struct Args {
+    Plan plan;
+    const float* a_scale;  // [K / 128, rows]
+    const float* b_scale;  // [E, ceil(R / 128), ceil(C / 128)]
+    int64_t rows;          // of the row operands (pitch of a_scale)
+    int64_t F;
+    int64_t N;             // columns of the result (kGateUp: F pairs)
+    int32_t n_tiles;       // column tiles
+    int32_t k_blocks;
+    int32_t sr, sc;        // the scale grid of an expert
+    Pairs h;               // kGateUp
+    float* gu;             // kGateUp (NULL: not kept), [tile][2F][128]
+    float* dh;             // kDh, [tile][F][128]
+    Peaks* peaks;          // kGateUp (NULL: not kept), kDh
+    bf16* out;             // kDown, kDx
+    int64_t ld;
+};
+
+struct Work {
+    int32_t tile, expert, token0, rows, n;
+};
+
+// The i-th tile of the launch, expert by expert, column by column.
+__device__ __forceinline__ Work work_at(const Args& a, int64_t i)
+{
+    const int32_t t = (int32_t)(i / a.n_tiles);
+    const int32_t e = a.plan.tiles[t].expert;
+    const int32_t first = a.plan.start[e], count = a.plan.start[e + 1] - first;
+    const int64_t local = i - (int64_t)first * a.n_tiles;
+    Work w;
+    w.n = (int32_t)(local / count);
+    w.tile = first + (int32_t)(local - (int64_t)w.n * count);
+    const Tile tile = a.plan.tiles[w.tile];
+    w.expert = e;
+    w.token0 = tile.token0;
+    w.rows = tile.rows;
+    return w;
+}
+
+template <int kMode>
+__device__ __forceinline__ int chunk_column(const Args& a, const Work& w, int c)
+{
+    return kMode == kGateUp ? (int)(c * a.F) + w.n * 128 : w.n * kCols + c * 128;
+}
+
+// The scale of weight block (k block, column chunk c); 0 past the columns.
+template <int kMode>
+__device__ __forceinline__ float b_scale(const Args& a, const Work& w, int kb, int c)
+{
+    const int n = chunk_column<kMode>(a, w, c) >> 7;
+    const float* s = a.b_scale + (int64_t)w.expert * a.sr * a.sc;
+    if (kMode == kGateUp || kMode == kDown) return n < a.sc ? __ldg(s + (int64_t)kb * a.sc + n) : 0.0f;
+    return n < a.sr ? __ldg(s + (int64_t)n * a.sc + kb) : 0.0f;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ CUtensorMap map_lo,
+            const __grid_constant__ CUtensorMap map_w, const __grid_constant__ Args a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+    const uint32_t extra = base + kStages * kStageBytes;
+    // extra: full[3], empty[3], accumulator ready[2], free[2], tensor memory base, exchange, its amax[2][2][128]
+    const uint32_t bar_full = extra, bar_empty = extra + 32, bar_acc = extra + 64, bar_free = extra + 80,
+                   bar_exchange = extra + 104;
+    uint8_t* extra_ptr = smem_raw + (extra - smem_addr(smem_raw));
+    volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(extra_ptr + 96);
+    float* exchange = reinterpret_cast<float*>(extra_ptr + 128);  // [2][2][128]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(bar_full + 8 * i, 1);
+            bar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(bar_acc + 8 * i, 1);
+            bar_init(bar_free + 8 * i, 256);
+        }
+        bar_init(bar_exchange, 256);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+        prefetch_map(&map_hi);
+        prefetch_map(&map_lo);
+        prefetch_map(&map_w);
+    }
+    if (warp == 2) tmem_alloc<512>(extra + 96);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_at;
+    const int64_t total = (int64_t)*a.plan.n_tiles * a.n_tiles;
+    bool ok = true;
+
+    if (warp < 4) {
+        regs_less<56>();
+        if (warp == 0 && lane == 0) {
+            // TMA: K steps of every tile, kStages ahead
+            int64_t it = 0;
+            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+                const Work w = work_at(a, i);
+                const int c0 = chunk_column<kMode>(a, w, 0), c1 = chunk_column<kMode>(a, w, 1);
+                for (int kb = 0; kb < a.k_blocks; ++kb, ++it) {
+                    const int s = (int)(it % kStages);
+                    if (it >= kStages && !bar_wait(bar_empty + 8 * s, (uint32_t)(it / kStages - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = bar_full + 8 * s, dst = base + s * kStageBytes;
+                    bar_expect(full, kStageBytes);
+                    load_2d(dst, &map_hi, full, kb * 128, w.tile * kRows);
+                    load_2d(dst + kOperand, &map_lo, full, kb * 128, w.tile * kRows);
+                    if (kMode == kGateUp || kMode == kDown) {
+                        load_3d(dst + 2 * kOperand, &map_w, full, c0, kb * 128, w.expert);
+                        load_3d(dst + 3 * kOperand, &map_w, full, c1, kb * 128, w.expert);
+                    } else {
+                        load_3d(dst + 2 * kOperand, &map_w, full, kb * 128, c0, w.expert);
+                        load_3d(dst + 3 * kOperand, &map_w, full, kb * 128, c1, w.expert);
+                    }
+                }
+            }
+            // the copies in flight land before the CTA ends, whatever became of the other warps
+            for (int64_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+                ok &= bar_wait(bar_full + 8 * (j % kStages), (uint32_t)(j / kStages) & 1);
+        } else if (warp == 1 && lane == 0) {
+            constexpr bool kMnMajor = kMode == kGateUp || kMode == kDown;
+            constexpr uint32_t idesc[2] = {instruction(kRows, kCols, false, kMnMajor),
+                                           instruction(kRows, kCols, false, kMnMajor, true)};
+            int64_t it = 0;
+            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x)
+                for (int kb = 0; kb < a.k_blocks; ++kb, ++it) {
+                    const int s = (int)(it % kStages), acc = (int)(it & 1);
+                    if ((it >= 2 && !bar_wait(bar_free + 8 * acc, (uint32_t)(it / 2 - 1) & 1)) ||
+                        !bar_wait(bar_full + 8 * s, (uint32_t)(it / kStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint32_t src = base + s * kStageBytes, d = tmem + acc * kCols;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t da = operand(src + t * kOperand + k * 32, 1024, 16);
+                            // N-major: 8 k are 1024 bytes, the second chunk of 128 columns follows the first;
+                            // K-major: 8 columns are 1024 bytes
+                            const uint64_t db = kMnMajor ? operand(src + 2 * kOperand + k * 4096, 1024, kOperand)
+                                                         : operand(src + 2 * kOperand + k * 32, 1024, 16);
+                            mma_f8(d, da, db, idesc[t], t + k > 0);
+                        }
+                    commit(bar_empty + 8 * s);
+                    commit(bar_acc + 8 * acc);
+                }
+            // the products in flight end before the tensor memory is freed
+            if (it > 0) ok &= bar_wait(bar_acc + 8 * ((it - 1) & 1), (uint32_t)((it - 1) / 2) & 1);
+        }
+    } else {
+        regs_more<224>();
+        const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+        int64_t it = 0;
+        int parity = 0;
+        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x, parity ^= 1) {
+            const Work w = work_at(a, i);
+            const int64_t at = (int64_t)w.tile * kRows + row;  // row of the internal buffers
+            float sum[2][64];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < 64; ++j) sum[c][j] = 0.0f;
+            float sa = a.a_scale[at], s0 = b_scale<kMode>(a, w, 0, 0), s1 = b_scale<kMode>(a, w, 0, 1);
+            for (int kb = 0; kb < a.k_blocks; ++kb, ++it) {
+                const int acc = (int)(it & 1);
+                const float f[2] = {sa * s0, sa * s1};
+                if (kb + 1 < a.k_blocks) {  // the next step's scales, ahead of the wait
+                    sa = a.a_scale[(int64_t)(kb + 1) * a.rows + at];
+                    s0 = b_scale<kMode>(a, w, kb + 1, 0);
+                    s1 = b_scale<kMode>(a, w, kb + 1, 1);
+                }
+                // a warp's lanes agree on the outcome: the loads below are warp-wide
+                ok = __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc, (uint32_t)(it / 2) & 1));
+                if (!ok) break;
+                fence_after();
+                const uint32_t t = tmem + acc * kCols + lanes + group * 64;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t r[32];
+                        tmem_load(t + c * 128 + q * 32, r);
+                        tmem_wait();
+                        if (c == 1 && q == 1) {
+                            fence_before();
+                            bar_arrive(bar_free + 8 * acc);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            sum[c][q * 32 + j] = fmaf(__uint_as_float(r[j]), f[c], sum[c][q * 32 + j]);
+                    }
+            }
+            if (!ok) break;
+            if constexpr (kMode == kGateUp) {
+                const int n0 = w.n * 128 + group * 64;
+                float amax = 0.0f, top_g = 0.0f, top_u = 0.0f;
+                if (a.gu) {
+                    float* g = a.gu + ((int64_t)w.tile * 2 * a.F + n0) * kRows + row;
+                    float* u = g + a.F * kRows;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) {
+                        __stcs(g + j * kRows, sum[0][j]);
+                        __stcs(u + j * kRows, sum[1][j]);
+                        top_g = fmaxf(top_g, fabsf(sum[0][j]));
+                        top_u = fmaxf(top_u, fabsf(sum[1][j]));
+                    }
+                    const uint32_t pg = __reduce_max_sync(0xffffffffu, abs_bits(top_g));
+                    const uint32_t pu = __reduce_max_sync(0xffffffffu, abs_bits(top_u));
+                    if (lane == 0) {
+                        atomicMax(&a.peaks[w.expert].gate, pg);
+                        atomicMax(&a.peaks[w.expert].up, pu);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 64; ++j) {
+                    const float g = sum[0][j];
+                    sum[0][j] = __fdividef(g, 1.0f + __expf(-g)) * sum[1][j];
+                    if (g < -80.0f) sum[0][j] = g * expf(g) * sum[1][j];  // 1 + exp(-g) past the quick quotient
+                    amax = fmaxf(amax, fabsf(sum[0][j]));
+                }
+                // the largest of the row's 128 columns: the other 64 are the other group's
+                exchange[(parity * 2 + group) * 128 + row] = amax;
+                bar_arrive(bar_exchange);
+                ok = __all_sync(0xffffffffu, bar_wait(bar_exchange, parity));
+                if (!ok) break;
+                amax = fmaxf(amax, exchange[(parity * 2 + (group ^ 1)) * 128 + row]);
+                const PairScale ps = pair_scale(amax);
+                if (group == 0) a.h.scale[(int64_t)w.n * a.rows + at] = ps.down;
+                uint4* hi = reinterpret_cast<uint4*>(a.h.hi + at * a.h.pitch + n0);
+                uint4* lo = reinterpret_cast<uint4*>(a.h.lo + at * a.h.pitch + n0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t vh[4], vl[4];
+#pragma unroll
+                    for (int i2 = 0; i2 < 4; ++i2) {
+                        const float* v = &sum[0][q * 16 + i2 * 4];
+                        uint32_t h0, l0, h1, l1;
+                        pair_encode(v[0], v[1], ps.up, h0, l0);
+                        pair_encode(v[2], v[3], ps.up, h1, l1);
+                        vh[i2] = h0 | h1 << 16;
+                        vl[i2] = l0 | l1 << 16;
+                    }
+                    hi[q] = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+                    lo[q] = make_uint4(vl[0], vl[1], vl[2], vl[3]);
+                }
+            } else if constexpr (kMode == kDh) {
+                float top = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int64_t n0 = (int64_t)w.n * kCols + c * 128 + group * 64;
+                    if (n0 >= a.N) continue;  // F is a multiple of 128: a chunk is in or out whole
+                    float* o = a.dh + ((int64_t)w.tile * a.F + n0) * kRows + row;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) {
+                        __stcs(o + j * kRows, sum[c][j]);
+                        top = fmaxf(top, fabsf(sum[c][j]));
+                    }
+                }
+                const uint32_t p = __reduce_max_sync(0xffffffffu, abs_bits(top));
+                if (lane == 0) atomicMax(&a.peaks[w.expert].dh, p);
+            } else {
+                if (row < w.rows) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int64_t n0 = (int64_t)w.n * kCols + c * 128 + group * 64;
+                        bf16* o = a.out + (int64_t)(w.token0 + row) * a.ld + n0;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            if (n0 + q * 8 >= a.N) break;  // N is a multiple of 16
+                            uint32_t v[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __nv_bfloat162 two =
+                                    __floats2bfloat162_rn(sum[c][q * 8 + 2 * j], sum[c][q * 8 + 2 * j + 1]);
+                                v[j] = *reinterpret_cast<const uint32_t*>(&two);
+                            }
+                            *reinterpret_cast<uint4*>(o + q * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (!ok) atomicAdd(&g_timeouts, 1u);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 2) tmem_free<512>(tmem);
+}
+
+template <int kMode>
+int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a, cudaStream_t s)
+{
+    CUtensorMap hi, lo, wm;
+    const uint64_t rdims[2] = {(uint64_t)rows.pitch, (uint64_t)d.rows()}, rstride[1] = {(uint64_t)rows.pitch};
+    const uint32_t rbox[2] = {128, 128};
+    const uint64_t wdims[3] = {(uint64_t)w.C, (uint64_t)w.R, (uint64_t)d.E},
+                   wstride[2] = {(uint64_t)w.C, (uint64_t)(w.C * w.R)};
+    const uint32_t wbox[3] = {128, 128, 1};
+    int st;
+    if ((st = tensor_map(&hi, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, rows.hi, rdims, rstride, rbox)) != FP8Z1_OK ||
+        (st = tensor_map(&lo, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, rows.lo, rdims, rstride, rbox)) != FP8Z1_OK ||
+        (st = tensor_map(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w.codes, wdims, wstride, wbox)) != FP8Z1_OK)
+        return st;
+    a.a_scale = rows.scale;
+    a.b_scale = w.scale;
+    a.rows = d.rows();
+    a.F = d.F;
+    a.n_tiles = (int32_t)(kMode == kGateUp ? d.F / 128 : ceil_div(a.N, kCols));
+    a.k_blocks = (int32_t)ceil_div(K, kBlock);
+    a.sr = (int32_t)ceil_div(w.R, 128);
+    a.sc = (int32_t)ceil_div(w.C, 128);
+    const int sms = sm_count_here();
+    if (sms < 1 || cudaFuncSetAttribute(gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        return FP8Z1_ECUDA;
+    const int64_t most = d.tiles() * a.n_tiles;
+    count_launch();
+    gemm_kernel<kMode><<<(unsigned)(most < sms ? most : sms), kThreads, kSmem, s>>>(hi, lo, wm, a);
+    return launch_status();
+}
+
+}  // namespace
+
+int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w, const Pairs& h, float* gu,
+                   Peaks* peaks, cudaStream_t s)
+{
+    Args a = {};
+    a.plan = p;
+    a.N = d.F;
+    a.h = h;
+    a.gu = gu;
+    a.peaks = peaks;
+    return launch<kGateUp>(d, x, d.H, w, a, s);
+}
+
+int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, cudaStream_t s)
+{
+    Args a = {};
+    a.plan = p;
+    a.N = d.H;
+    a.out = y;
+    a.ld = ld;
+    return launch<kDown>(d, h, d.F, w, a, s);
+}
+
+int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, float* dh, Peaks* peaks, cudaStream_t s)
+{
+    Args a = {};
+    a.plan = p;
+    a.N = d.F;
+    a.dh = dh;
+    a.peaks = peaks;
+    return launch<kDh>(d, dy, d.H, w, a, s);
+}
+
+int launch_dx(const Dims& d, const Plan& p, const Pairs& dgu, const Weight& w, bf16* dx, int64_t ld, cudaStream_t s)
+{
+    Args a = {};
+    a.plan = p;
+    a.N = d.H;
+    a.out = dx;
+    a.ld = ld;
+    return launch<kDx>(d, dgu, 2 * d.F, w, a, s);
+}
+
+int take_timeouts_gemm(unsigned* n)
+{
+    const unsigned zero = 0;
+    return cudaMemcpyFromSymbol(n, g_timeouts, 4) == cudaSuccess && cudaMemcpyToSymbol(g_timeouts, &zero, 4) == cudaSuccess
+               ? FP8Z1_OK
+               : FP8Z1_ECUDA;
+}
+
+}  // namespace ffn
+}  // namespace fp8z1

@@ -1,0 +1,289 @@
+// The weight gradients: sums over an expert's token rows,
+//
+//   d_gate_up[h, c] = sum_t x[t, h] dgu[t, c]        d_down[f, h] = sum_t h[t, f] dy[t, h]
+//
+// in FP32 accuracy.  x and dy are BF16 values and fit FP16 exactly (8
+// significant bits; every expert's operand is brought below 2^15 by one power
+// of two, so FP16's 40 binades hold everything down to 2^-40 of the largest);
+// dgu and h are FP32 and enter as two FP16 numbers, hi = f16(v), lo = f16(v -
+// hi), 22 bits.  Two FP16 products with FP32 accumulators then cost twice one
+// BF16 product and keep FP32's accuracy; one BF16 product would lose 16 bits
+// of it, and the optimizer's grads are FP32.
+//
+// A CTA owns 128 x 256 of a gradient: 128 columns of the two-term operand (the
+// lanes of tensor memory), 256 of the other.  Both are row-major over tokens,
+// that is M- and N-major to the tensor cores.  The pipeline is ffn_gemm.cu's:
+// TMA steps of 64 token rows (64 KB), products into two accumulators, each
+// 128 rows added up in registers.  The last step issues only the 16-row
+// products that hold rows; rows past an expert's end are zeros.
+//
+// Bound by the FP32 gradients written (4 bytes an element) up to about 250
+// tokens an expert, by the tensor cores above.
+#include "ffn.cuh"
+
+namespace fp8z1 {
+namespace ffn {
+namespace {
+
+using namespace tc;
+
+__device__ unsigned g_timeouts;
+
+constexpr int kCols = 256;
+constexpr int kStep = 64;  // token rows of a stage
+constexpr int kStages = 3;
+constexpr int kThreads = 384;
+constexpr uint32_t kChunk = 64 * kStep * 2;     // bytes of 64 columns of a stage
+constexpr uint32_t kStageBytes = 8 * kChunk;    // hi: 2 chunks, lo: 2, the other operand: 4
+constexpr uint32_t kSmem = kStages * kStageBytes + 8 * 4096 + 1024 + 256;
+
+struct Args {
+    Plan plan;
+    const Peaks* peaks;
+    float* out;        // kTransposed: [E, N, M]
+    int64_t M, N;      // columns of the two-term operand, of the other
+    int32_t m_tiles, n_tiles, experts;
+};
+
+// kTransposed: the two-term operand's columns are the gradient's columns
+// (d_gate_up), else its rows (d_down).
+template <bool kTransposed>
+__global__ void __launch_bounds__(kThreads, 1)
+wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ CUtensorMap map_lo,
+             const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_out,
+             const __grid_constant__ Args a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+    const uint32_t staging = base + kStages * kStageBytes, extra = staging + 8 * 4096;
+    const uint32_t bar_full = extra, bar_empty = extra + 32, bar_acc = extra + 64, bar_free = extra + 80;
+    volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem_raw + (extra + 96 - smem_addr(smem_raw)));
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(bar_full + 8 * i, 1);
+            bar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(bar_acc + 8 * i, 1);
+            bar_init(bar_free + 8 * i, 256);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+        prefetch_map(&map_hi);
+        prefetch_map(&map_lo);
+        prefetch_map(&map_b);
+    }
+    if (warp == 2) tmem_alloc<512>(extra + 96);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_at;
+    const int64_t per = (int64_t)a.m_tiles * a.n_tiles, total = per * a.experts;
+    bool ok = true;
+
+    if (warp < 4) {
+        regs_less<56>();
+        if (warp == 0 && lane == 0) {
+            int64_t it = 0;
+            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+                const int e = (int)(i / per), local = (int)(i - e * per);
+                const int m = local % a.m_tiles, n = local / a.m_tiles;
+                const int row0 = a.plan.start[e] * kRows, steps = (a.plan.tokens[e] + kStep - 1) / kStep;
+                for (int k = 0; k < steps; ++k, ++it) {
+                    const int s = (int)(it % kStages);
+                    if (it >= kStages && !bar_wait(bar_empty + 8 * s, (uint32_t)(it / kStages - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = bar_full + 8 * s, dst = base + s * kStageBytes;
+                    bar_expect(full, kStageBytes);
+                    load_3d(dst, &map_hi, full, 0, row0 + k * kStep, m * 2);
+                    load_3d(dst + 2 * kChunk, &map_lo, full, 0, row0 + k * kStep, m * 2);
+                    load_3d(dst + 4 * kChunk, &map_b, full, 0, row0 + k * kStep, n * 4);
+                }
+            }
+            for (int64_t j = it > kStages ? it - kStages : 0; j < it; ++j)
+                ok &= bar_wait(bar_full + 8 * (j % kStages), (uint32_t)(j / kStages) & 1);
+        } else if (warp == 1 && lane == 0) {
+            constexpr uint32_t idesc = instruction(128, kCols, true, true);
+            int64_t it = 0, sums = 0;
+            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+                const int tokens = a.plan.tokens[(int)(i / per)];
+                for (int t0 = 0; t0 < tokens && ok; t0 += 2 * kStep, ++sums) {
+                    const int acc = (int)(sums & 1);
+                    const uint32_t d = tmem + acc * kCols;
+                    if (sums >= 2 && !bar_wait(bar_free + 8 * acc, (uint32_t)(sums / 2 - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    for (int sub = 0; sub < 2 && t0 + sub * kStep < tokens; ++sub, ++it) {
+                        const int s = (int)(it % kStages);
+                        if (!bar_wait(bar_full + 8 * s, (uint32_t)(it / kStages) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_after();
+                        const uint32_t src = base + s * kStageBytes;
+                        const int left = tokens - t0 - sub * kStep, steps = left >= kStep ? 4 : (left + 15) / 16;
+                        for (int k = 0; k < steps; ++k) {
+                            // 8 rows are 1024 bytes; the next 64 columns follow a chunk later
+                            const uint64_t db = operand(src + 4 * kChunk + k * 2048, 1024, kChunk);
+                            mma_f16(d, operand(src + k * 2048, 1024, kChunk), db, idesc, sub + k > 0);
+                            mma_f16(d, operand(src + 2 * kChunk + k * 2048, 1024, kChunk), db, idesc, true);
+                        }
+                        commit(bar_empty + 8 * s);
+                    }
+                    if (ok) commit(bar_acc + 8 * acc);
+                }
+            }
+            // every product issued ends before the tensor memory is freed
+            if (sums > 0) ok &= bar_wait(bar_acc + 8 * ((sums - 1) & 1), (uint32_t)((sums - 1) / 2) & 1);
+        }
+    } else {
+        regs_more<224>();
+        const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16, mine = staging + (warp - 4) * 4096;
+        int64_t sums = 0;
+        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+            const int e = (int)(i / per), local = (int)(i - e * per);
+            const int m = local % a.m_tiles, n = local / a.m_tiles;
+            const int tokens = a.plan.tokens[e];
+            float sum[2][64];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < 64; ++j) sum[c][j] = 0.0f;
+            for (int t0 = 0; t0 < tokens; t0 += 2 * kStep, ++sums) {
+                const int acc = (int)(sums & 1);
+                ok = __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc, (uint32_t)(sums / 2) & 1));
+                if (!ok) break;
+                fence_after();
+                const uint32_t t = tmem + acc * kCols + lanes + group * 64;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t r[32];
+                        tmem_load(t + c * 128 + q * 32, r);
+                        tmem_wait();
+                        if (c == 1 && q == 1) {
+                            fence_before();
+                            bar_arrive(bar_free + 8 * acc);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c][q * 32 + j] += __uint_as_float(r[j]);
+                    }
+            }
+            if (!ok) break;
+            const Peaks p = a.peaks[e];
+            const Pow2 f = pow2(kTransposed ? -(x_shift(p) + dgu_shift(p)) : -(dy_shift(p) + h_shift(p)));
+            if constexpr (kTransposed) {
+                // lanes are consecutive columns of the gradient
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int64_t n0 = (int64_t)n * kCols + c * 128 + group * 64;
+                    float* o = a.out + ((int64_t)e * a.N + n0) * a.M + m * 128 + row;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (n0 + j < a.N) __stcs(o + j * a.M, f.times(sum[c][j]));
+                }
+            } else {
+                // lanes are rows: 32 x 32 pieces turn in shared memory and leave by TMA
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if (lane == 0) store_wait_read<0>();
+                        __syncwarp();
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
+                            const float* x = &sum[c][q * 32 + v * 4];
+                            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             mine + lane * 128 + ((v ^ (lane & 7)) << 4)),
+                                         "f"(f.times(x[0])), "f"(f.times(x[1])), "f"(f.times(x[2])), "f"(f.times(x[3]))
+                                         : "memory");
+                        }
+                        fence_async();
+                        __syncwarp();
+                        const int n0 = n * kCols + c * 128 + group * 64 + q * 32;
+                        if (lane == 0 && n0 < a.N) {
+                            store_3d(&map_out, mine, n0, m * 128 + (warp & 3) * 32, e);
+                            store_commit();
+                        }
+                    }
+            }
+        }
+        if (!kTransposed && lane == 0) store_wait_all();
+    }
+    if (!ok) atomicAdd(&g_timeouts, 1u);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 2) tmem_free<512>(tmem);
+}
+
+// [rows, pitch] FP16 as {64, rows, pitch / 64}
+int map_f16(CUtensorMap* map, const __half* p, int64_t rows, int64_t pitch, uint32_t chunks)
+{
+    const uint64_t dims[3] = {64, (uint64_t)rows, (uint64_t)(pitch / 64)}, strides[2] = {(uint64_t)pitch * 2, 128};
+    const uint32_t box[3] = {64, kStep, chunks};
+    return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dims, strides, box);
+}
+
+template <bool kTransposed>
+int launch(const Dims& d, const Plan& p, const Peaks* peaks, const __half* hi, const __half* lo, int64_t M,
+           const __half* b, float* out, cudaStream_t s)
+{
+    CUtensorMap mh, ml, mb, mo;
+    const uint64_t odims[3] = {(uint64_t)d.H, (uint64_t)d.F, (uint64_t)d.E},
+                   ostride[2] = {(uint64_t)d.H * 4, (uint64_t)(d.H * d.F) * 4};
+    const uint32_t obox[3] = {32, 32, 1};
+    int st;
+    if ((st = map_f16(&mh, hi, d.rows(), M, 2)) != FP8Z1_OK || (st = map_f16(&ml, lo, d.rows(), M, 2)) != FP8Z1_OK ||
+        (st = map_f16(&mb, b, d.rows(), d.Hp(), 4)) != FP8Z1_OK ||
+        (st = kTransposed ? (mo = mb, FP8Z1_OK)
+                          : tensor_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, out, odims, ostride, obox)) != FP8Z1_OK)
+        return st;
+    Args a = {};
+    a.plan = p;
+    a.peaks = peaks;
+    a.out = out;
+    a.M = M;
+    a.N = d.H;
+    a.m_tiles = (int32_t)(M / 128);
+    a.n_tiles = (int32_t)ceil_div(d.H, kCols);
+    a.experts = (int32_t)d.E;
+    const int sms = sm_count_here();
+    if (sms < 1 || cudaFuncSetAttribute(wgrad_kernel<kTransposed>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+                       cudaSuccess)
+        return FP8Z1_ECUDA;
+    const int64_t total = (int64_t)a.m_tiles * a.n_tiles * d.E;
+    count_launch();
+    wgrad_kernel<kTransposed><<<(unsigned)(total < sms ? total : sms), kThreads, kSmem, s>>>(mh, ml, mb, mo, a);
+    return launch_status();
+}
+
+}  // namespace
+
+int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s)
+{
+    return launch<true>(d, p, peaks, b.dgu_hi, b.dgu_lo, 2 * d.F, b.x16, out, s);
+}
+
+int launch_d_down(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s)
+{
+    return launch<false>(d, p, peaks, b.h_hi, b.h_lo, d.F, b.dy16, out, s);
+}
+
+int take_timeouts_wgrad(unsigned* n)
+{
+    const unsigned zero = 0;
+    return cudaMemcpyFromSymbol(n, g_timeouts, 4) == cudaSuccess && cudaMemcpyToSymbol(g_timeouts, &zero, 4) == cudaSuccess
+               ? FP8Z1_OK
+               : FP8Z1_ECUDA;
+}
+
+}  // namespace ffn
+}  // namespace fp8z1

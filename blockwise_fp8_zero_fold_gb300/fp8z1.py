@@ -145,6 +145,7 @@ _SIGS = {
                                     _P, _P]),
     "fp8z1_ffn_backward": (C.c_int, [C.POINTER(fp8z1_ffn_dims), _P, C.c_int64, _P, C.c_int64, _P, _P, _P, _P, _P, _P,
                                      _P, C.c_int64, _P, _P, _P, _P]),
+    "fp8z1_ffn_timeouts": (C.c_int, [C.POINTER(C.c_uint32)]),
     "fp8z1_distill": (C.c_int, [_P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, _P, _P, C.c_int64, C.c_float, _P, _P,
                                 _P, C.c_int64, _P]),
     "fp8z1_strerror": (C.c_char_p, [C.c_int]),
@@ -562,6 +563,14 @@ def fp8z1_ffn_backward(dims: fp8z1_ffn_dims, dy, ld_dy: int, x, ld_x: int, d_off
                                     _ptr(gate_up), _ptr(gate_up_scale), _ptr(down), _ptr(down_scale), _ptr(saved),
                                     _ptr(dx), int(ld_dx), _ptr(d_gate_up), _ptr(d_down), _ptr(workspace),
                                     _stream(stream)), "fp8z1_ffn_backward")
+
+
+def fp8z1_ffn_timeouts() -> int:
+    """Threads of the feed-forward kernels that gave up waiting since the last
+    call (synchronous; 0 in all normal use)."""
+    n = C.c_uint32()
+    _check(lib().fp8z1_ffn_timeouts(C.byref(n)), "fp8z1_ffn_timeouts")
+    return n.value
 
 
 def fp8z1_distill(logits, type_: int, ld: int, rows: int, vocab: int, teacher_ids, teacher_logits, top: int,

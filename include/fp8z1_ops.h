@@ -110,6 +110,13 @@ int fp8z1_ffn_backward(const fp8z1_ffn_dims* dims, const void* dy, int64_t ld_dy
                        const uint8_t* down, const float* down_scale, const void* saved, void* dx, int64_t ld_dx,
                        float* d_gate_up, float* d_down, void* workspace, void* stream);
 
+/* The feed-forward kernels' warps wait for one another on barriers in shared
+ * memory, four seconds at most: a wait that runs out ends its CTA, whose results
+ * are then incomplete.  Reads and clears the number of threads that gave up on
+ * the current device since the last call (synchronous; 0 in all normal use).
+ * Errors: EINVAL (null), ECUDA. */
+int fp8z1_ffn_timeouts(uint32_t* count);
+
 /* ---- distillation ----------------------------------------------------------------- */
 
 /* Row r's loss against the teacher's `top` listed logits, at temperature tau:

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from blockwise_fp8_zero_fold_gb300 import fp8z1 as F
 from blockwise_fp8_zero_fold_gb300 import ops
 from tests import _ops as R
 from tests._gpu import lib  # noqa: F401
@@ -11,6 +12,13 @@ pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("lib")]
 # Weight gradients are FP32 sums of FP32 products.  With sums over up to 2^14 terms, whose roundings (2^-24 each)
 # add up like a random walk, in at most three products in a row: 2^-24 * 2^7 * 1.3 = 1e-5 of the norm.
 GRAD_TOL = 1e-5
+
+
+@pytest.fixture(autouse=True)
+def _no_timeouts():
+    """No wait inside the kernels ran out."""
+    yield
+    assert F.fp8z1_ffn_timeouts() == 0
 
 
 def gen(seed):
