@@ -1,95 +1,582 @@
 // Distillation loss against a teacher's top logits, and its gradient.
+//
+//   q_j = exp2((z_j - m) k) / sum,  k = log2(e) / tau,  m the row's maximum,
+//   loss = tau^2 sum_k p_k (log p_k - log q_{id_k}),
+//   dz_j = w tau (q_j - sum of the p listed for j).
+//
+// Bound by memory: the logits are read from it once and the gradient written
+// once.  A row is read twice, for its maximum and sum and, backwards, for the
+// gradient; the second time it comes from L2.
+//
+// A row belongs to a CTA of 4 to 16 warps, or to a cluster of up to 8 of them,
+// each with a slice.  A thread has eight vectors of 16 bytes on their way and joins them, four at a
+// time, to a running maximum and the sum of exponentials in reference to it;
+// the warps' pairs are joined through distributed shared memory in a fixed
+// order, so results repeat bit for bit.  One warp of a CTA has the teacher's
+// entries, a long chain of small steps beside the others' loads: the softmax,
+// the student's logits behind the ids, repeated ids added up; then the loss and,
+// over the dense gradient w tau q_j, the listed elements.
+//
+#include <cooperative_groups.h>
+
 #include "ops_common.cuh"
+#include "tc.cuh"
 
 namespace {
 
 using namespace fp8z1;
+namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
-
-__device__ float block_sum(float v, float* tmp)
+__device__ __forceinline__ float exp2_fast(float x)
 {
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = tmp[0];
-    for (int i = 1; i < kThreads / 32; ++i) v += tmp[i];
-    return v;
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-__device__ float block_max(float v, float* tmp)
-{
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = tmp[0];
-    for (int i = 1; i < kThreads / 32; ++i) v = fmaxf(v, tmp[i]);
-    return v;
-}
-
-// One CTA per row.
 template <class T>
-__global__ void distill_kernel(const T* logits, int64_t ld, int64_t vocab, const int32_t* ids, const float* teacher,
-                               int top, float tau, const float* weight, float* loss, T* dlogits, int64_t ld_d)
-{
-    __shared__ float tmp[kThreads / 32];
-    __shared__ int32_t id[FP8Z1_DISTILL_MAX_TOP];
-    __shared__ float p[FP8Z1_DISTILL_MAX_TOP];
-    const int64_t r = blockIdx.x;
-    const T* z = logits + r * ld;
-    T* dz = dlogits ? dlogits + r * ld_d : nullptr;
-    const float w = weight ? weight[r] : 1.0f;
-    float tmax = -INFINITY;
-    int any = 0;
-    for (int k = threadIdx.x; k < top; k += kThreads) {
-        const int32_t j = ids[r * top + k];
-        const float t = teacher[r * top + k];
-        const bool there = j >= 0 && j < vocab && t != -INFINITY;
-        id[k] = there ? j : -1;
-        p[k] = there ? t / tau : -INFINITY;
-        any |= there;
-        tmax = fmaxf(tmax, p[k]);
+struct Vec {
+    static constexpr int n = 16 / sizeof(T);
+    uint4 v;
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
-    any = __syncthreads_or(any);
-    if (w == 0.0f || !any) {
-        if (threadIdx.x == 0) loss[r] = 0.0f;
-        if (dz)
-            for (int64_t j = threadIdx.x; j < vocab; j += kThreads) dz[j] = from_float<T>(0.0f);
+    // the largest element (NaN ignored)
+    __device__ __forceinline__ float largest() const
+    {
+        if constexpr (sizeof(T) == 4) return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3)));
+        const auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(two(v.x), two(v.y)), __hmax2(two(v.z), two(v.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+};
+
+template <class T>
+__device__ __forceinline__ uint4 pack(const float (&f)[Vec<T>::n])
+{
+    if constexpr (sizeof(T) == 4)
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 two = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&two);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// 16 bytes of a row from element `at` (a multiple of the vector from the
+// aligned address below the row's start, so `at` may be negative); elements
+// outside [0, n) read as -inf and are not touched.
+template <class T>
+__device__ __forceinline__ uint4 load_vec(const T* z, int64_t at, int64_t n)
+{
+    constexpr int kN = Vec<T>::n;
+    if (at >= 0 && at + kN <= n) return __ldcs(reinterpret_cast<const uint4*>(z + at));
+    float f[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) f[i] = at + i >= 0 && at + i < n ? to_float(z[at + i]) : -INFINITY;
+    return pack<T>(f);
+}
+
+template <class T>
+__device__ __forceinline__ void store_vec(T* z, int64_t at, int64_t n, bool whole, const float (&f)[Vec<T>::n])
+{
+    constexpr int kN = Vec<T>::n;
+    if (whole && at >= 0 && at + kN <= n) {
+        __stcs(reinterpret_cast<uint4*>(z + at), pack<T>(f));
         return;
     }
-    tmax = block_max(tmax, tmp);
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+        if (at + i >= 0 && at + i < n) z[at + i] = from_float<T>(f[i]);
+}
+
+// Exponents are taken in the log2 domain as fma(z, k, -m k), one rounding of
+// the whole.  m k is rounded first, but alike wherever m is the reference, so
+// the shares e / sum do not see it.  A maximum so large that m k could
+// overflow (a row of nothing but a mask's lowest value) takes (z - m) k.
+struct Base {  // of a launch
+    float k, limit;
+    __device__ __forceinline__ explicit Base(float tau)
+    {
+        k = 1.4426950408889634f / tau;
+        limit = 1e37f / fmaxf(k, 1.0f);
+    }
+};
+struct Scale {
+    float k, m, mk;
+    bool plain;
+    __device__ __forceinline__ Scale(const Base& b, float top) : k(b.k)
+    {
+        m = top == -INFINITY ? 0.0f : top;
+        plain = fabsf(m) <= b.limit;
+        mk = m * k;
+    }
+    __device__ __forceinline__ float of(float z) const
+    {
+        return exp2_fast(plain ? fmaf(z, k, -mk) : (z - m) * k);
+    }
+};
+
+// A maximum and the sum of the exponentials in reference to it.
+struct __align__(8) Sum {
+    float m, s;
+};
+// `part`'s sum in reference to another maximum; 0 for an empty part
+__device__ __forceinline__ float in_reference(const Sum& part, const Scale& to)
+{
+    const float d = to.plain ? part.m * to.k - to.mk : (part.m - to.m) * to.k;
+    return part.m == -INFINITY ? part.s * 0.0f : part.s * exp2_fast(d);
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v)
+{
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+template <class T>
+struct Args {
+    const T* logits;
+    int64_t ld, rows, vocab;
+    const int32_t* ids;
+    const float* teacher;
+    int32_t top;
+    float tau;
+    const float* weight;
+    float* loss;
+    T* dlogits;
+    int64_t ld_d;
+    int64_t slice;     // vectors of a CTA
+};
+
+// A CTA's part of a row.  Vector v of the row holds elements v kN - shift ..;
+// the CTA has vectors [rank slice, (rank + 1) slice), elements [first, end).
+template <class T>
+struct Slice {
+    const T* z;
+    T* dz;
+    int64_t first, end;
+    bool same;  // the gradient's row starts alike
+    __device__ __forceinline__ Slice(const Args<T>& a, int64_t r, int rank)
+    {
+        z = a.logits + r * a.ld;
+        dz = a.dlogits ? a.dlogits + r * a.ld_d : nullptr;
+        const int shift = (int)(reinterpret_cast<uintptr_t>(z) % 16 / sizeof(T));
+        same = dz && reinterpret_cast<uintptr_t>(dz) % 16 == reinterpret_cast<uintptr_t>(z) % 16;
+        first = (int64_t)rank * a.slice * Vec<T>::n - shift;
+        end = min(first + a.slice * Vec<T>::n, a.vocab);
+    }
+};
+
+// The teacher's entries of one row, in shared memory.
+struct Lists {
+    // All of them: p (0: absent) and the student's logit.
+    float *p, *zk;
+    // Those of the CTA's slice (first all of them): id, p of all an id's repeats at the first one and -1 at the
+    // others, the student's logit.
+    int32_t* id;
+    float *own_p, *own_z;
+};
+__host__ __device__ __forceinline__ int64_t list_entries(int64_t top) { return (top + 3) / 4 * 4; }
+constexpr int kListBytes = 20;  // an entry
+__device__ __forceinline__ Lists lists_at(uint8_t* smem, int top)
+{
+    const int n = (int)list_entries(top);
+    float* f = reinterpret_cast<float*>(smem);
+    return Lists{f, f + n, reinterpret_cast<int32_t*>(f + 2 * n), f + 3 * n, f + 4 * n};
+}
+
+struct Entries {
+    float p_logp;  // the sum of p log p
+    int32_t any;
+    int32_t own;   // entries of the CTA's slice
+};
+
+// One warp fills the lists of row r, for the slice [first, end).
+template <class T>
+__device__ __forceinline__ Entries fill_lists(const Args<T>& a, int64_t r, const T* z, int64_t first, int64_t end,
+                                              const Lists& l)
+{
+    const int lane = threadIdx.x & 31;
+    constexpr float kLog2e = 1.4426950408889634f;
+    float top = -INFINITY;
+    bool any = false;
+#pragma unroll 4
+    for (int i = lane; i < a.top; i += 32) {
+        const int32_t j = __ldg(a.ids + r * a.top + i);
+        const float t = __ldg(a.teacher + r * a.top + i);
+        const bool there = j >= 0 && j < a.vocab && t != -INFINITY;
+        l.id[i] = there ? j : -1;
+        l.p[i] = there ? t / a.tau : -INFINITY;
+        l.zk[i] = there ? to_float(z[j]) : 0.0f;
+        any |= there;
+        top = fmaxf(top, l.p[i]);
+    }
+    Entries e = {0.0f, __any_sync(0xffffffffu, any), 0};
+    if (!e.any) return e;
+    top = warp_max(top);
     float mass = 0.0f;
-    for (int k = threadIdx.x; k < top; k += kThreads) mass += id[k] < 0 ? 0.0f : expf(p[k] - tmax);
-    mass = block_sum(mass, tmp);
-    float zmax = -INFINITY;
-    for (int64_t j = threadIdx.x; j < vocab; j += kThreads) zmax = fmaxf(zmax, to_float(z[j]));
-    zmax = block_max(zmax, tmp);
-    if (zmax == -INFINITY) zmax = 0.0f;
-    float total = 0.0f;
-    for (int64_t j = threadIdx.x; j < vocab; j += kThreads) total += expf((to_float(z[j]) - zmax) / tau);
-    total = block_sum(total, tmp);
-    float l = 0.0f;
+    for (int i = lane; i < a.top; i += 32)
+        if (l.id[i] >= 0) mass += exp2_fast((l.p[i] - top) * kLog2e);
+    mass = warp_sum(mass);
+    const float log_mass = logf(mass), by = 1.0f / mass;
+    for (int i0 = 0; i0 < a.top; i0 += 32) {
+        const int i = i0 + lane;
+        int32_t j = -1;
+        float p = 0.0f, zk = 0.0f;
+        if (i < a.top && l.id[i] >= 0) {
+            j = l.id[i];
+            zk = l.zk[i];
+            const float logp = l.p[i] - top - log_mass;
+            p = exp2_fast((l.p[i] - top) * kLog2e) * by;
+            // an entry too small to count: 0 log 0 = 0, whatever the student's logit
+            if (p != 0.0f) e.p_logp = fmaf(p, logp, e.p_logp);
+        }
+        if (i < a.top) l.p[i] = p;
+        // the slice's entries move to the front of theirs
+        const bool mine = j >= 0 && j >= first && j < end;
+        const unsigned group = __ballot_sync(0xffffffffu, mine);
+        if (mine) {
+            const int at = e.own + __popc(group & ((1u << lane) - 1));
+            l.id[at] = j;
+            l.own_p[at] = p;
+            l.own_z[at] = zk;
+        }
+        e.own += __popc(group);
+        __syncwarp();
+    }
+    e.p_logp = warp_sum(e.p_logp);
+    if (e.own + lane < list_entries(e.own)) l.id[e.own + lane] = -1;
+    __syncwarp();
+    // repeats of an id, at its first entry
+    for (int i0 = 0; i0 < e.own; i0 += 32) {
+        const int i = i0 + lane;
+        const int32_t j = i < e.own ? l.id[i] : -2;
+        int same = 0, before = 0;
+        const int4* ids = reinterpret_cast<const int4*>(l.id);
+#pragma unroll 2
+        for (int o = 0; o < e.own; o += 4) {
+            const int4 q = ids[o >> 2];
+            const int hits = (q.x == j) + (q.y == j) + (q.z == j) + (q.w == j);
+            same += hits;
+            // entries before i: whole groups of 4, and i's own group up to i
+            before += o + 4 <= i ? hits
+                                 : o > i ? 0 : (q.x == j && o < i) + (q.y == j && o + 1 < i) + (q.z == j && o + 2 < i);
+        }
+        float sum = i < e.own ? l.own_p[i] : 0.0f;
+        if (same > 1 && before == 0) {
+            sum = 0.0f;
+            for (int o = i; o < e.own; ++o)  // its repeats come later; their p is not read again after this group
+                if (l.id[o] == j) sum += l.own_p[o];
+        }
+        __syncwarp();
+        if (i < e.own) l.own_p[i] = before == 0 ? sum : -1.0f;
+        __syncwarp();
+    }
+    return e;
+}
+
+// The loss of a row of maximum m and sum `total`, by one warp:
+//   log p - log q = log p - (z - m) / tau + log total, and the p add up to 1.
+template <class T>
+__device__ __forceinline__ void write_loss(const Args<T>& a, int64_t r, const Lists& l, const Entries& e, float m,
+                                           float total)
+{
+    float pz = 0.0f;
+    if (e.any)
+        for (int i = threadIdx.x & 31; i < a.top; i += 32)
+            if (l.p[i] != 0.0f) pz = fmaf(l.p[i], l.zk[i] - m, pz);
+    pz = warp_sum(pz);
     // a row of -inf alone has q = 0: its log q is z = -inf, not -inf - -inf
-    const float log_total = total == 0.0f ? 0.0f : logf(total), log_mass = logf(mass);
-    for (int k = threadIdx.x; k < top; k += kThreads) {
-        if (id[k] < 0) continue;
-        const float lp = p[k] - tmax - log_mass;
-        const float pk = expf(lp);
-        l += pk * (lp - ((to_float(z[id[k]]) - zmax) / tau - log_total));
-        p[k] = pk;
+    const float log_total = total == 0.0f ? 0.0f : logf(total);
+    if ((threadIdx.x & 31) == 0) a.loss[r] = e.any ? a.tau * a.tau * (e.p_logp - pz / a.tau + log_total) : 0.0f;
+}
+
+// The listed elements of a slice, over its dense gradient, by one warp.
+template <class T>
+__device__ __forceinline__ void write_listed(const Lists& l, int own, T* dz, const Scale& sc, float q, float by)
+{
+    for (int i = threadIdx.x & 31; i < own; i += 32)
+        if (!(l.own_p[i] < 0.0f)) dz[l.id[i]] = from_float<T>(sc.of(l.own_z[i]) * q - l.own_p[i] * by);
+}
+
+__device__ __forceinline__ float inverse(float total)
+{
+    return total > 0.0f ? 1.0f / total : total;  // 0 and NaN stay so
+}
+
+// Maximum and sum of kHold vectors, joined to `mine`.
+template <class T, int kHold>
+__device__ __forceinline__ void add_vecs(const Vec<T> (&x)[kHold], const Base& k, Sum& mine)
+{
+    float m = x[0].largest();
+#pragma unroll
+    for (int j = 1; j < kHold; ++j) m = fmaxf(m, x[j].largest());
+    m = fmaxf(m, mine.m);
+    const Scale sc(k, m);
+    float s[2] = {in_reference(mine, sc), 0.0f};
+    if (sc.plain) {
+#pragma unroll
+        for (int j = 0; j < kHold; ++j)
+#pragma unroll
+            for (int i = 0; i < Vec<T>::n; ++i) s[i & 1] += exp2_fast(fmaf(x[j].get(i), sc.k, -sc.mk));
+    } else {
+#pragma unroll
+        for (int j = 0; j < kHold; ++j)
+#pragma unroll
+            for (int i = 0; i < Vec<T>::n; ++i) s[i & 1] += exp2_fast((x[j].get(i) - sc.m) * sc.k);
     }
-    l = block_sum(l, tmp);
-    if (threadIdx.x == 0) loss[r] = tau * tau * l;
-    if (!dz) return;
-    const float inv = total > 0.0f ? 1.0f / total : (total == 0.0f ? 0.0f : total);
-    for (int64_t j = threadIdx.x; j < vocab; j += kThreads) {
-        float d = expf((to_float(z[j]) - zmax) / tau) * inv;
-        for (int k = 0; k < top; ++k)
-            if (id[k] == j) d -= p[k];
-        dz[j] = from_float<T>(w * tau * d);
+    mine = Sum{m, s[0] + s[1]};
+}
+
+// One vector, any elements of it.
+template <class T>
+__device__ __forceinline__ void add_vec(const Vec<T>& x, const Base& k, Sum& mine)
+{
+    const float m = fmaxf(mine.m, x.largest());
+    const Scale sc(k, m);
+    float s = in_reference(mine, sc);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::n; ++i) s += sc.of(x.get(i));
+    mine = Sum{m, s};
+}
+
+// The sum over a warp's lanes.
+__device__ __forceinline__ Sum warp_join(const Sum& mine, const Base& k)
+{
+    const float m = warp_max(mine.m);
+    return Sum{m, warp_sum(in_reference(mine, Scale(k, m)))};
+}
+// The row's, from the `n` pairs its cluster's warps left; every lane gets it.
+__device__ __forceinline__ Sum row_join(const Sum* parts, int n, const Base& k)
+{
+    const int lane = threadIdx.x & 31;
+    float top = -INFINITY;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, parts[i].m);
+    const Scale sc(k, warp_max(top));
+    float s = 0.0f;
+    for (int i = lane; i < n; i += 32) s += in_reference(parts[i], sc);
+    return Sum{sc.m, warp_sum(s)};
+}
+
+template <class T>
+__device__ __forceinline__ void dense(const Vec<T>& x, const Scale& sc, float q, float (&f)[Vec<T>::n])
+{
+#pragma unroll
+    for (int i = 0; i < Vec<T>::n; ++i) f[i] = sc.of(x.get(i)) * q;
+}
+
+constexpr int kHold = 4;  // vectors a thread joins at once
+
+// kHold vectors a thread apart, from p on (or back, with a negative step).
+template <class T, int kStep>
+__device__ __forceinline__ void load_some(Vec<T> (&x)[kHold], const T* p)
+{
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) x[j].v = *reinterpret_cast<const uint4*>(p + j * kStep * Vec<T>::n);
+}
+template <class T, int kStep>
+__device__ __forceinline__ void store_some(const Vec<T> (&x)[kHold], T* p, const Scale& sc, float q)
+{
+    constexpr int kN = Vec<T>::n;
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) {
+        float f[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) f[i] = exp2_fast(fmaf(x[j].get(i), sc.k, -sc.mk)) * q;
+        __stcs(reinterpret_cast<uint4*>(p + j * kStep * kN), pack<T>(f));
     }
+}
+
+template <class T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) row_kernel(const Args<T> a)
+{
+    constexpr int kN = Vec<T>::n, kReaders = kThreads - 32, kWarps = kReaders / 32;
+    constexpr int64_t kBatch = (int64_t)kHold * kReaders * kN;  // elements
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ Sum parts[8 * kWarps];
+    __shared__ Entries entries;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Base k(a.tau);
+    const Lists l = lists_at(smem, a.top);
+    const int64_t r = blockIdx.x / ranks;
+    const Slice<T> s(a, r, rank);
+    const float w = a.weight ? __ldg(a.weight + r) : 1.0f;
+    auto clear = [&]() {
+        const float zero[kN] = {};
+        if (rank == 0 && tid == 0) a.loss[r] = 0.0f;
+        if (s.dz)
+            for (int64_t at = s.first + (int64_t)tid * kN; at < s.end; at += kThreads * kN)
+                store_vec(s.dz, at, s.end, s.same, zero);
+    };
+    if (w == 0.0f) return clear();  // the same in every CTA of the cluster
+    // the slice's vectors [0, vecs), those inside the row whole [f0, f1): the others are the row's first and last
+    const int vecs = s.end > s.first ? (int)((s.end - s.first + kN - 1) / kN) : 0;
+    const int f0 = s.first < 0 ? 1 : 0, f1 = s.end > s.first ? (int)((s.end - s.first) / kN) : 0;
+    const bool head = tid == 0 && f0 && vecs, tail = tid == 0 && f1 < vecs && (f1 || !f0);
+    const int64_t tail_at = s.first + (int64_t)f1 * kN;
+    // this thread's whole vectors: `share` of them, kReaders apart
+    const int share = f1 - f0 > tid ? (f1 - f0 - 1 - tid) / kReaders + 1 : 0, batches = share / kHold;
+    const T* const z0 = s.z + s.first + (int64_t)(f0 + tid) * kN;
+    if (warp == kWarps) {
+        const Entries e = fill_lists(a, r, s.z, s.first, s.end, l);
+        if (lane == 0) entries = e;
+    } else {
+        Sum mine = {-INFINITY, 0.0f};
+        Vec<T> x[kHold], y[kHold];
+        const T* p = z0;
+        if (batches > 0) load_some<T, kReaders>(x, p);
+        if (head) add_vec(Vec<T>{load_vec(s.z, s.first, s.end)}, k, mine);
+        if (tail) add_vec(Vec<T>{load_vec(s.z, tail_at, s.end)}, k, mine);
+        for (int b = 0; b < batches; b += 2, p += 2 * kBatch) {
+            if (b + 1 < batches) load_some<T, kReaders>(y, p + kBatch);
+            add_vecs<T, kHold>(x, k, mine);
+            if (b + 2 < batches) load_some<T, kReaders>(x, p + 2 * kBatch);
+            if (b + 1 < batches) add_vecs<T, kHold>(y, k, mine);
+        }
+        // the last few
+        p = z0 + batches * kBatch;
+        const int left = share - batches * kHold;
+#pragma unroll
+        for (int j = 0; j < kHold - 1; ++j)
+            if (j < left) x[j].v = *reinterpret_cast<const uint4*>(p + j * kReaders * kN);
+#pragma unroll
+        for (int j = 0; j < kHold - 1; ++j)
+            if (j < left) add_vec(x[j], k, mine);
+        mine = warp_join(mine, k);
+        if (lane < ranks) *cluster.map_shared_rank(&parts[rank * kWarps + warp], lane) = mine;
+    }
+    // Every warp's pair is here, and every CTA has read the listed logits, which the gradient may overwrite.
+    __syncwarp();
+    cluster.sync();
+    const Entries e = entries;
+    if (!e.any) return clear();
+    const Sum row = row_join(parts, ranks * kWarps, k);
+    const Scale sc(k, row.m);
+    const float q = inverse(row.s) * (w * a.tau);
+    if (warp == kWarps && rank == 0) write_loss(a, r, l, e, row.m, row.s);
+    if (!s.dz) return;
+    if (warp < kWarps) {
+        float f[kN];
+        if (s.same && sc.plain) {
+            // backwards: the vectors read last are the likeliest to be in L2 still
+            T* const d0 = s.dz + s.first + (int64_t)(f0 + tid) * kN;
+            for (int v = share - 1; v >= batches * kHold; --v) {
+                const Vec<T> x{*reinterpret_cast<const uint4*>(z0 + (int64_t)v * kReaders * kN)};
+#pragma unroll
+                for (int i = 0; i < kN; ++i) f[i] = exp2_fast(fmaf(x.get(i), sc.k, -sc.mk)) * q;
+                __stcs(reinterpret_cast<uint4*>(d0 + (int64_t)v * kReaders * kN), pack<T>(f));
+            }
+            Vec<T> x[kHold], y[kHold];
+            const T* p = z0 + (batches - 1) * kBatch;
+            T* o = d0 + (batches - 1) * kBatch;
+            if (batches > 0) load_some<T, kReaders>(x, p);
+            for (int b = batches; b > 0; b -= 2, p -= 2 * kBatch, o -= 2 * kBatch) {
+                if (b > 1) load_some<T, kReaders>(y, p - kBatch);
+                store_some<T, kReaders>(x, o, sc, q);
+                if (b > 2) load_some<T, kReaders>(x, p - 2 * kBatch);
+                if (b > 1) store_some<T, kReaders>(y, o - kBatch, sc, q);
+            }
+        } else {
+            for (int v = f0 + tid; v < f1; v += kReaders) {
+                const int64_t at = s.first + (int64_t)v * kN;
+                dense(Vec<T>{*reinterpret_cast<const uint4*>(s.z + at)}, sc, q, f);
+                store_vec(s.dz, at, s.end, s.same, f);
+            }
+        }
+        if (head) {
+            dense(Vec<T>{load_vec(s.z, s.first, s.end)}, sc, q, f);
+            store_vec(s.dz, s.first, s.end, false, f);
+        }
+        if (tail) {
+            dense(Vec<T>{load_vec(s.z, tail_at, s.end)}, sc, q, f);
+            store_vec(s.dz, tail_at, s.end, false, f);
+        }
+    }
+    __syncthreads();  // the dense gradient, before the listed elements of the slice
+    if (warp == kWarps) write_listed(l, e.own, s.dz, sc, q, w * a.tau);
+}
+
+template <class T>
+int launch_clusters(void (*kernel)(const Args<T>), const Args<T>& a, int64_t clusters, int ranks, int threads,
+                    int64_t smem, cudaStream_t s)
+{
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)ranks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.gridDim = dim3((unsigned)(clusters * ranks));
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = (size_t)smem;
+    c.stream = s;
+    c.attrs = &at;
+    c.numAttrs = ranks > 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return FP8Z1_ECUDA;
+    count_launch();
+    if (cudaLaunchKernelEx(&c, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return FP8Z1_ECUDA;
+    }
+    return launch_status();
+}
+
+template <class T, int kThreads>
+int launch_rows(Args<T> a, int ranks, cudaStream_t s)
+{
+    // rows beyond the grid's reach go in further launches
+    const int64_t most = (int64_t)1 << 24;
+    const Args<T> all = a;
+    for (int64_t r = 0; r < all.rows; r += most) {
+        a.rows = all.rows - r < most ? all.rows - r : most;
+        a.logits = all.logits + r * all.ld;
+        a.ids = all.ids + r * all.top;
+        a.teacher = all.teacher + r * all.top;
+        a.weight = all.weight ? all.weight + r : nullptr;
+        a.loss = all.loss + r;
+        a.dlogits = all.dlogits ? all.dlogits + r * all.ld_d : nullptr;
+        const int st = launch_clusters<T>(row_kernel<T, kThreads>, a, a.rows, ranks, kThreads,
+                                          list_entries(a.top) * kListBytes, s);
+        if (st != FP8Z1_OK) return st;
+    }
+    return FP8Z1_OK;
+}
+
+template <class T>
+int launch(Args<T> a, cudaStream_t s)
+{
+    constexpr int kN = Vec<T>::n;
+    // the most vectors a row spans, whatever its alignment
+    const int64_t vecs = ceil_div(a.vocab + kN - 1, kN);
+    // few rows are spread over more CTAs, down to 16 KB slices, while that still leaves SMs idle
+    int ranks = 1;
+    while (ranks < 8 && a.rows * ranks * 2 <= 152 && vecs > ranks * 2 * 1024) ranks *= 2;
+    a.slice = ceil_div(vecs, ranks);
+    // A CTA's fixed chain of steps is about 7 us: short rows go to small CTAs, of which an SM holds many.  Long ones
+    // to few: their gradient is read again from L2, where eight 256 KB rows an SM would not fit (4096 rows of 131072
+    // BF16 logits took 411 us at two rows an SM, 443 at four, 511 at eight; 8192 rows of 16384 took 264, 169, 118).
+    // The loss alone reads once, and four rows an SM do best (172 us against 189 at two).
+    const int64_t bytes = a.slice * 16;
+    if (bytes <= 48 * 1024) return launch_rows<T, 128>(a, ranks, s);
+    if (bytes <= 128 * 1024 || (!a.dlogits && bytes <= 1024 * 1024)) return launch_rows<T, 256>(a, ranks, s);
+    return launch_rows<T, 512>(a, ranks, s);
 }
 
 }  // namespace
@@ -110,16 +597,12 @@ extern "C" int fp8z1_distill(const void* logits, int32_t type, int64_t ld, int64
         !aligned(row_weight, 4) || !aligned(loss, 4))
         return FP8Z1_EALIGN;
     if (rows == 0) return FP8Z1_OK;
-    NvtxRange r("fp8z1_distill");
+    NvtxRange range("fp8z1_distill");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    count_launch();
     if (type == FP8Z1_F32)
-        distill_kernel<float><<<(unsigned)rows, kThreads, 0, s>>>(
-            static_cast<const float*>(logits), ld, vocab, teacher_ids, teacher_logits, (int)top, temperature,
-            row_weight, loss, static_cast<float*>(dlogits), ld_d);
-    else
-        distill_kernel<__nv_bfloat16><<<(unsigned)rows, kThreads, 0, s>>>(
-            static_cast<const __nv_bfloat16*>(logits), ld, vocab, teacher_ids, teacher_logits, (int)top, temperature,
-            row_weight, loss, static_cast<__nv_bfloat16*>(dlogits), ld_d);
-    return launch_status();
+        return launch<float>({static_cast<const float*>(logits), ld, rows, vocab, teacher_ids, teacher_logits,
+                              (int32_t)top, temperature, row_weight, loss, static_cast<float*>(dlogits), ld_d, 0}, s);
+    return launch<__nv_bfloat16>({static_cast<const __nv_bfloat16*>(logits), ld, rows, vocab, teacher_ids,
+                                  teacher_logits, (int32_t)top, temperature, row_weight, loss,
+                                  static_cast<__nv_bfloat16*>(dlogits), ld_d, 0}, s);
 }

@@ -1,4 +1,4 @@
-// The sm_103a pieces the gated feed-forward kernels are built from: mbarriers,
+// The sm_103a pieces the operators are built from: mbarriers,
 // TMA tile copies, tcgen05 matrix products and tensor memory.
 #pragma once
 
@@ -30,12 +30,15 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// how long one try may suspend its thread before it returns
+constexpr uint32_t kSuspendNs = 20000;
+
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
                  : "=r"(ok)
-                 : "r"(bar), "r"(parity)
+                 : "r"(bar), "r"(parity), "r"(kSuspendNs)
                  : "memory");
     return ok != 0;
 }
@@ -62,6 +65,52 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
     }
 }
 
+// Arrives on CTA `rank`'s barrier at this CTA's address `bar`, for the order of
+// what this thread has read alone: writes are not released (a release to the
+// cluster would wait for every global store in flight).
+__device__ __forceinline__ void bar_arrive_at(uint32_t bar, uint32_t rank)
+{
+    asm volatile(
+        "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, %1; mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a]; }" ::"r"(
+            bar),
+        "r"(rank)
+        : "memory");
+}
+
+// Two floats to CTA `rank`'s shared memory at this CTA's address `dst` (8-byte
+// aligned), counted as 8 bytes on its barrier at `bar`.
+__device__ __forceinline__ void send_pair(uint32_t dst, uint32_t rank, float x, float y, uint32_t bar)
+{
+    const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+    asm volatile(
+        "{ .reg .b32 a, b; mapa.shared::cluster.u32 a, %0, %1; mapa.shared::cluster.u32 b, %3, %1;\n"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [a], %2, [b]; }" ::"r"(dst),
+        "r"(rank), "l"(v), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ bool bar_try_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    if (bar_try_cluster(bar, parity)) return true;
+    const uint64_t t0 = now_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (bar_try_cluster(bar, parity)) return true;
+        if (now_ns() - t0 > kWaitNs) return false;
+    }
+}
+
 // ---- TMA ----------------------------------------------------------------------
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
@@ -84,6 +133,14 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, ui
             dst),
         "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
+}
+
+// `bytes` (a multiple of 16) from a 16-byte aligned address
+__device__ __forceinline__ void load_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 __device__ __forceinline__ void store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z)
