@@ -13,7 +13,7 @@ namespace fp8z1 {
 namespace ffn {
 
 int tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
-               const uint64_t* strides, const uint32_t* box)
+               const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle)
 {
     typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -37,7 +37,7 @@ int tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void*
         if (i + 1 < rank) st[i] = strides[i];
     }
     return encode(map, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? FP8Z1_OK
                : FP8Z1_ECUDA;

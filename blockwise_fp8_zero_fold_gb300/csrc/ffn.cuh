@@ -184,7 +184,7 @@ struct Pow2 {
 __device__ __forceinline__ Pow2 pow2(int k)
 {
     k = min(max(k, -252), 252);
-    const int h = k / 2;
+    const int h = min(max(k, -126), 126);  // b is 1 unless k leaves FP32's exponents
     return Pow2{__uint_as_float((uint32_t)(127 + h) << 23), __uint_as_float((uint32_t)(127 + k - h) << 23)};
 }
 // floor(log2) of a positive float's bits (-127 for 0 and subnormals, 128 for inf)
@@ -213,9 +213,9 @@ int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, const Peak
 int launch_d_down(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
 
 // A tensor map over `rank` dimensions (innermost first; strides in bytes of
-// dimensions 1..), 128-byte swizzle.  Returns a status.
+// dimensions 1..).  Returns a status.
 int tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
-               const uint64_t* strides, const uint32_t* box);
+               const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // Waits that ran out in each translation unit's kernels on the current device
 // since the last call (synchronous).  Returns a status.

@@ -227,21 +227,23 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 if (!ok) break;
                 fence_after();
                 const uint32_t t = tmem + acc * kCols + lanes + group * 64;
+                // columns 64 group + {0, 32, 128, 160} ..; each load is under way while the one before is added
+                uint32_t r[2][32];
+                tmem_load(t, r[0]);
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t r[32];
-                        tmem_load(t + c * 128 + q * 32, r);
-                        tmem_wait();
-                        if (c == 1 && q == 1) {
-                            fence_before();
-                            bar_arrive(bar_free + 8 * acc);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            sum[c][q * 32 + j] = fmaf(__uint_as_float(r[j]), f[c], sum[c][q * 32 + j]);
+                for (int q = 0; q < 4; ++q) {
+                    tmem_wait(r[q & 1]);
+                    if (q < 3) {
+                        tmem_load(t + (q + 1) / 2 * 128 + (q + 1) % 2 * 32, r[(q + 1) & 1]);
+                    } else {
+                        fence_before();
+                        bar_arrive(bar_free + 8 * acc);
                     }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        sum[q / 2][q % 2 * 32 + j] =
+                            fmaf(__uint_as_float(r[q & 1][j]), f[q / 2], sum[q / 2][q % 2 * 32 + j]);
+                }
             }
             if (!ok) break;
             if constexpr (kMode == kGateUp) {

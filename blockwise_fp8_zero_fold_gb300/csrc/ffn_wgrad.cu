@@ -14,7 +14,7 @@
 // lanes of tensor memory), 256 of the other.  Both are row-major over tokens,
 // that is M- and N-major to the tensor cores.  The pipeline is ffn_gemm.cu's:
 // TMA steps of 64 token rows (64 KB), products into two accumulators, each
-// 128 rows added up in registers.  The last step issues only the 16-row
+// 512 rows added up in registers.  The last step issues only the 16-row
 // products that hold rows; rows past an expert's end are zeros.
 //
 // Bound by the FP32 gradients written (4 bytes an element) up to about 250
@@ -32,6 +32,7 @@ __device__ unsigned g_timeouts;
 constexpr int kCols = 256;
 constexpr int kStep = 64;  // token rows of a stage
 constexpr int kStages = 3;
+constexpr int kAdd = 8;    // stages added up in tensor memory before they go to the registers' sums
 constexpr int kThreads = 384;
 constexpr uint32_t kChunk = 64 * kStep * 2;     // bytes of 64 columns of a stage
 constexpr uint32_t kStageBytes = 8 * kChunk;    // hi: 2 chunks, lo: 2, the other operand: 4
@@ -111,14 +112,14 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
             int64_t it = 0, sums = 0;
             for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
                 const int tokens = a.plan.tokens[(int)(i / per)];
-                for (int t0 = 0; t0 < tokens && ok; t0 += 2 * kStep, ++sums) {
+                for (int t0 = 0; t0 < tokens && ok; t0 += kAdd * kStep, ++sums) {
                     const int acc = (int)(sums & 1);
                     const uint32_t d = tmem + acc * kCols;
                     if (sums >= 2 && !bar_wait(bar_free + 8 * acc, (uint32_t)(sums / 2 - 1) & 1)) {
                         ok = false;
                         break;
                     }
-                    for (int sub = 0; sub < 2 && t0 + sub * kStep < tokens; ++sub, ++it) {
+                    for (int sub = 0; sub < kAdd && t0 + sub * kStep < tokens; ++sub, ++it) {
                         const int s = (int)(it % kStages);
                         if (!bar_wait(bar_full + 8 * s, (uint32_t)(it / kStages) & 1)) {
                             ok = false;
@@ -150,69 +151,82 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
             const int e = (int)(i / per), local = (int)(i - e * per);
             const int m = local % a.m_tiles, n = local / a.m_tiles;
             const int tokens = a.plan.tokens[e];
+            const Peaks p = a.peaks[e];
+            const Pow2 f = pow2(kTransposed ? -(x_shift(p) + dgu_shift(p)) : -(dy_shift(p) + h_shift(p)));
             float sum[2][64];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int j = 0; j < 64; ++j) sum[c][j] = 0.0f;
-            for (int t0 = 0; t0 < tokens; t0 += 2 * kStep, ++sums) {
+            for (int t0 = 0; t0 < tokens; t0 += kAdd * kStep, ++sums) {
                 const int acc = (int)(sums & 1);
                 ok = __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc, (uint32_t)(sums / 2) & 1));
                 if (!ok) break;
                 fence_after();
                 const uint32_t t = tmem + acc * kCols + lanes + group * 64;
+                uint32_t r[2][32];
+                tmem_load(t, r[0]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    tmem_wait(r[q & 1]);
+                    if (q < 3) {
+                        tmem_load(t + (q + 1) / 2 * 128 + (q + 1) % 2 * 32, r[(q + 1) & 1]);
+                    } else {
+                        fence_before();
+                        bar_arrive(bar_free + 8 * acc);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        sum[q / 2][q % 2 * 32 + j] =
+                            fmaf(__uint_as_float(r[q & 1][j]), f.a, sum[q / 2][q % 2 * 32 + j]);
+                }
+            }
+            if (!ok) break;
+            if (f.b != 1.0f)  // a power of two beyond FP32's exponents
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t r[32];
-                        tmem_load(t + c * 128 + q * 32, r);
-                        tmem_wait();
-                        if (c == 1 && q == 1) {
-                            fence_before();
-                            bar_arrive(bar_free + 8 * acc);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[c][q * 32 + j] += __uint_as_float(r[j]);
-                    }
-            }
-            if (!ok) break;
-            const Peaks p = a.peaks[e];
-            const Pow2 f = pow2(kTransposed ? -(x_shift(p) + dgu_shift(p)) : -(dy_shift(p) + h_shift(p)));
+                    for (int j = 0; j < 64; ++j) sum[c][j] *= f.b;
             if constexpr (kTransposed) {
                 // lanes are consecutive columns of the gradient
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int64_t n0 = (int64_t)n * kCols + c * 128 + group * 64;
                     float* o = a.out + ((int64_t)e * a.N + n0) * a.M + m * 128 + row;
+                    if (n0 + 64 <= a.N) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
-                        if (n0 + j < a.N) __stcs(o + j * a.M, f.times(sum[c][j]));
+                        for (int j = 0; j < 64; ++j, o += a.M) __stcs(o, sum[c][j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j, o += a.M)
+                            if (n0 + j < a.N) __stcs(o, sum[c][j]);
+                    }
                 }
             } else {
-                // lanes are rows: 32 x 32 pieces turn in shared memory and leave by TMA
+                // lanes are rows: pieces of 32 rows x 16 columns turn in shared memory and leave by TMA, one
+                // being read while the next is written
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t buf = mine + (q & 1) * 2048;
+                    if (lane == 0) store_wait_read<1>();
+                    __syncwarp();
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        if (lane == 0) store_wait_read<0>();
-                        __syncwarp();
-#pragma unroll
-                        for (int v = 0; v < 8; ++v) {
-                            const float* x = &sum[c][q * 32 + v * 4];
-                            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             mine + lane * 128 + ((v ^ (lane & 7)) << 4)),
-                                         "f"(f.times(x[0])), "f"(f.times(x[1])), "f"(f.times(x[2])), "f"(f.times(x[3]))
-                                         : "memory");
-                        }
-                        fence_async();
-                        __syncwarp();
-                        const int n0 = n * kCols + c * 128 + group * 64 + q * 32;
-                        if (lane == 0 && n0 < a.N) {
-                            store_3d(&map_out, mine, n0, m * 128 + (warp & 3) * 32, e);
-                            store_commit();
-                        }
+                    for (int v = 0; v < 4; ++v) {
+                        const float* x = &sum[q / 4][q % 4 * 16 + v * 4];
+                        // 64-byte swizzle: 16-byte units of a row change places with bits 1-2 of the row
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         buf + lane * 64 + ((v ^ (lane >> 1 & 3)) << 4)),
+                                     "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3])
+                                     : "memory");
                     }
+                    fence_async();
+                    __syncwarp();
+                    const int n0 = n * kCols + q / 4 * 128 + group * 64 + q % 4 * 16;
+                    if (lane == 0) {
+                        if (n0 < a.N) store_3d(&map_out, buf, n0, m * 128 + (warp & 3) * 32, e);
+                        store_commit();
+                    }
+                }
             }
         }
         if (!kTransposed && lane == 0) store_wait_all();
@@ -239,12 +253,13 @@ int launch(const Dims& d, const Plan& p, const Peaks* peaks, const __half* hi, c
     CUtensorMap mh, ml, mb, mo;
     const uint64_t odims[3] = {(uint64_t)d.H, (uint64_t)d.F, (uint64_t)d.E},
                    ostride[2] = {(uint64_t)d.H * 4, (uint64_t)(d.H * d.F) * 4};
-    const uint32_t obox[3] = {32, 32, 1};
+    const uint32_t obox[3] = {16, 32, 1};
     int st;
     if ((st = map_f16(&mh, hi, d.rows(), M, 2)) != FP8Z1_OK || (st = map_f16(&ml, lo, d.rows(), M, 2)) != FP8Z1_OK ||
         (st = map_f16(&mb, b, d.rows(), d.Hp(), 4)) != FP8Z1_OK ||
         (st = kTransposed ? (mo = mb, FP8Z1_OK)
-                          : tensor_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, out, odims, ostride, obox)) != FP8Z1_OK)
+                          : tensor_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, out, odims, ostride, obox,
+                                       CU_TENSOR_MAP_SWIZZLE_64B)) != FP8Z1_OK)
         return st;
     Args a = {};
     a.plan = p;

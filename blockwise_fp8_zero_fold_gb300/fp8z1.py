@@ -521,48 +521,72 @@ def fp8z1_scaler_update(scaler: fp8z1_loss_scaler, found_inf: int):
 
 
 # ---- model operators (include/fp8z1_ops.h) -----------------------------------
+# These calls repeat at the rate of a model's layers: the arguments go to ctypes
+# as they are (its argument types check and convert them), tensors by address.
+
+_ops = {}
+
+
+def _op(name: str):
+    f = _ops.get(name)
+    if f is None:
+        f = _ops[name] = getattr(lib(), name)
+    return f
+
+
+def _at(x):
+    """A tensor's address (None and ints pass)."""
+    return x.data_ptr() if hasattr(x, "data_ptr") else _ptr(x)
 
 
 def fp8z1_embed(vocab: int, dim: int, codes, scales, ids, id_bytes: int, tokens: int, alpha: float, out,
                 out_type: int, ld_out: int, stream=None):
-    _check(lib().fp8z1_embed(int(vocab), int(dim), _ptr(codes), _ptr(scales), _ptr(ids), int(id_bytes), int(tokens),
-                             float(alpha), _ptr(out), int(out_type), int(ld_out), _stream(stream)), "fp8z1_embed")
+    st = _op("fp8z1_embed")(vocab, dim, _at(codes), _at(scales), _at(ids), id_bytes, tokens, alpha, _at(out),
+                            out_type, ld_out, _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_embed")
 
 
 def fp8z1_embed_grad_workspace(vocab: int, dim: int, tokens: int) -> int:
     n = C.c_int64()
-    _check(lib().fp8z1_embed_grad_workspace(int(vocab), int(dim), int(tokens), C.byref(n)),
-           "fp8z1_embed_grad_workspace")
+    st = _op("fp8z1_embed_grad_workspace")(vocab, dim, tokens, n)
+    if st:
+        raise Fp8z1Error(st, "fp8z1_embed_grad_workspace")
     return n.value
 
 
 def fp8z1_embed_grad(vocab: int, dim: int, ids, id_bytes: int, tokens: int, alpha: float, dy, dy_type: int,
                      ld_dy: int, d_table, workspace, stream=None):
-    _check(lib().fp8z1_embed_grad(int(vocab), int(dim), _ptr(ids), int(id_bytes), int(tokens), float(alpha), _ptr(dy),
-                                  int(dy_type), int(ld_dy), _ptr(d_table), _ptr(workspace), _stream(stream)),
-           "fp8z1_embed_grad")
+    st = _op("fp8z1_embed_grad")(vocab, dim, _at(ids), id_bytes, tokens, alpha, _at(dy), dy_type, ld_dy,
+                                 _at(d_table), _at(workspace), _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_embed_grad")
 
 
 def fp8z1_ffn_sizes(dims: fp8z1_ffn_dims):
     """(saved, forward workspace, backward workspace) bytes."""
     a, b, c = C.c_int64(), C.c_int64(), C.c_int64()
-    _check(lib().fp8z1_ffn_sizes(C.byref(dims), C.byref(a), C.byref(b), C.byref(c)), "fp8z1_ffn_sizes")
+    st = _op("fp8z1_ffn_sizes")(dims, a, b, c)
+    if st:
+        raise Fp8z1Error(st, "fp8z1_ffn_sizes")
     return a.value, b.value, c.value
 
 
 def fp8z1_ffn_forward(dims: fp8z1_ffn_dims, x, ld_x: int, d_offsets, gate_up, gate_up_scale, down, down_scale, y,
                       ld_y: int, saved, workspace, stream=None):
-    _check(lib().fp8z1_ffn_forward(C.byref(dims), _ptr(x), int(ld_x), _ptr(d_offsets), _ptr(gate_up),
-                                   _ptr(gate_up_scale), _ptr(down), _ptr(down_scale), _ptr(y), int(ld_y), _ptr(saved),
-                                   _ptr(workspace), _stream(stream)), "fp8z1_ffn_forward")
+    st = _op("fp8z1_ffn_forward")(dims, _at(x), ld_x, _at(d_offsets), _at(gate_up), _at(gate_up_scale), _at(down),
+                                  _at(down_scale), _at(y), ld_y, _at(saved), _at(workspace), _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_ffn_forward")
 
 
 def fp8z1_ffn_backward(dims: fp8z1_ffn_dims, dy, ld_dy: int, x, ld_x: int, d_offsets, gate_up, gate_up_scale, down,
                        down_scale, saved, dx, ld_dx: int, d_gate_up, d_down, workspace, stream=None):
-    _check(lib().fp8z1_ffn_backward(C.byref(dims), _ptr(dy), int(ld_dy), _ptr(x), int(ld_x), _ptr(d_offsets),
-                                    _ptr(gate_up), _ptr(gate_up_scale), _ptr(down), _ptr(down_scale), _ptr(saved),
-                                    _ptr(dx), int(ld_dx), _ptr(d_gate_up), _ptr(d_down), _ptr(workspace),
-                                    _stream(stream)), "fp8z1_ffn_backward")
+    st = _op("fp8z1_ffn_backward")(dims, _at(dy), ld_dy, _at(x), ld_x, _at(d_offsets), _at(gate_up),
+                                   _at(gate_up_scale), _at(down), _at(down_scale), _at(saved), _at(dx), ld_dx,
+                                   _at(d_gate_up), _at(d_down), _at(workspace), _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_ffn_backward")
 
 
 def fp8z1_ffn_timeouts() -> int:
@@ -575,6 +599,7 @@ def fp8z1_ffn_timeouts() -> int:
 
 def fp8z1_distill(logits, type_: int, ld: int, rows: int, vocab: int, teacher_ids, teacher_logits, top: int,
                   temperature: float, row_weight, loss, dlogits, ld_d: int, stream=None):
-    _check(lib().fp8z1_distill(_ptr(logits), int(type_), int(ld), int(rows), int(vocab), _ptr(teacher_ids),
-                               _ptr(teacher_logits), int(top), float(temperature), _ptr(row_weight), _ptr(loss),
-                               _ptr(dlogits), int(ld_d), _stream(stream)), "fp8z1_distill")
+    st = _op("fp8z1_distill")(_at(logits), type_, ld, rows, vocab, _at(teacher_ids), _at(teacher_logits), top,
+                              temperature, _at(row_weight), _at(loss), _at(dlogits), ld_d, _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_distill")

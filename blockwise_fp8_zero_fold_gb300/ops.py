@@ -20,83 +20,87 @@ do not fit raise ValueError, what the library refuses raises Fp8z1Error.
 """
 from __future__ import annotations
 
-import ctypes as C
-from typing import Optional, Tuple
+from typing import Optional
 
 import torch
 
 from . import fp8z1 as F
 
+# The calls are small next to a few microseconds of kernel, so the checks here
+# build no message, wrapper or list before something is wrong.
+
 _TYPES = {torch.float32: F.F32, torch.bfloat16: F.BF16}
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_device = torch._C._cuda_getDevice
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+def _bad(what: str):
+    raise ValueError(what)
 
 
-def _stream_of(device, stream):
-    """(torch stream to enqueue on, whether it is not the current one)"""
+def _begin(dev: int, stream):
+    """(raw stream to enqueue on, the torch stream when it is not the current one)"""
+    if dev < 0:
+        _bad("the operators need CUDA tensors")
+    if dev != _device():
+        _bad("the tensors are not on the current device")
+    now = _raw_stream(dev)
     if stream is None:
-        return torch.cuda.current_stream(device), False
-    _need(isinstance(stream, torch.cuda.Stream), "stream must be a torch.cuda.Stream or None")
-    return stream, stream != torch.cuda.current_stream(device)
+        return now, None
+    if not isinstance(stream, torch.cuda.Stream) or stream.device.index != dev:
+        _bad("stream must be a torch.cuda.Stream of the tensors' device")
+    return stream.cuda_stream, stream if stream.cuda_stream != now else None
 
 
-class _Call:
-    """Allocations of one call: on its stream, so that their reuse is ordered."""
-
-    def __init__(self, device, stream):
-        _need(device.type == "cuda", "the operators need CUDA tensors")
-        self.device = device
-        self.stream, self.other = _stream_of(device, stream)
-        _need(self.stream.device == device, f"a stream of {self.stream.device} for tensors on {device}")
-
-    def empty(self, shape, dtype):
-        if not self.other:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        t.record_stream(self.stream)
-        return t
-
-    def bytes(self, n):
-        return self.empty((max(1, int(n)),), torch.uint8)
-
-    def out(self, given, shape, dtype, what):
-        if given is None:
-            return self.empty(shape, dtype)
-        _need(tuple(given.shape) == tuple(shape) and given.dtype == dtype and given.device == self.device,
-              f"{what} must be {dtype} of shape {tuple(shape)} on {self.device}")
-        return given
+def _new(shape, dtype, dev: int, other):
+    """A tensor of one call: on its stream, so that its memory is not reused early."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if other is not None:
+        t.record_stream(other)
+    return t
 
 
-def _on(device, *tensors):
+def _given(t: torch.Tensor, shape, dtype, dev: int, what: str):
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        _bad(f"{what} must be {dtype} of shape {tuple(shape)} on the inputs' device")
+    return t
+
+
+def _same_device(dev: int, *tensors):
     for t in tensors:
-        _need(t is None or t.device == device, f"a tensor on {t.device if t is not None else None}, others on {device}")
+        if t is not None and t.get_device() != dev:
+            _bad("the tensors are on several devices")
 
 
-def _rows(t: torch.Tensor, what: str):
-    """The row stride of a 2-D tensor whose rows are dense."""
-    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1), f"{what} must be 2-D with dense rows")
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
-    _need(ld >= t.shape[1], f"{what}'s rows must not overlap")
+def _rows(t: torch.Tensor, what: str) -> int:
+    """The row stride of a 2-D tensor whose rows are dense and apart."""
+    n, cols = t.shape
+    ld, one = t.stride()
+    if cols > 1 and one != 1:
+        _bad(f"{what}'s rows must be dense")
+    if n <= 1:
+        return ld if ld > cols else cols
+    if ld < cols:
+        _bad(f"{what}'s rows must not overlap")
     return ld
 
 
-def _fp8_weight(codes: torch.Tensor, scale: torch.Tensor, what: str) -> Tuple[int, int, int]:
+def _fp8_weight(codes: torch.Tensor, scale: torch.Tensor, what: str):
     """(E, R, C) of an FP8 weight after checking its codes and block scales."""
-    _need(codes.dim() in (2, 3) and codes.is_contiguous(), f"{what} must be contiguous [E, R, C] or [R, C] codes")
-    _need(codes.dtype == torch.uint8 or codes.dtype == torch.float8_e4m3fn, f"{what} must hold E4M3 codes (uint8)")
-    e, r, c = ((1,) + tuple(codes.shape))[-3:]
-    grid = (e, -(-r // F.TILE), -(-c // F.TILE))
-    _need(scale.dtype == torch.float32 and scale.is_contiguous() and scale.numel() == grid[0] * grid[1] * grid[2]
-          and tuple(scale.shape[-2:]) == grid[1:], f"{what}'s scales must be contiguous float32 {grid}")
+    shape = codes.shape
+    if len(shape) == 2:
+        e, (r, c) = 1, shape
+    elif len(shape) == 3:
+        e, r, c = shape
+    else:
+        _bad(f"{what} must be [E, R, C] or [R, C] codes")
+    if codes.dtype not in (torch.uint8, torch.float8_e4m3fn) or not codes.is_contiguous():
+        _bad(f"{what} must be contiguous E4M3 codes (uint8)")
+    if (scale.dtype != torch.float32 or scale.shape[-2:] != ((r + 127) // 128, (c + 127) // 128)
+            or scale.numel() != e * ((r + 127) // 128) * ((c + 127) // 128) or not scale.is_contiguous()):
+        _bad(f"{what}'s scales must be contiguous float32 [E, ceil(R/128), ceil(C/128)]")
     return e, r, c
-
-
-def _ids(ids: torch.Tensor) -> int:
-    _need(ids.dtype in (torch.int32, torch.int64) and ids.is_contiguous(), "ids must be contiguous int32 or int64")
-    return ids.element_size()
 
 
 # ---- embedding -----------------------------------------------------------------
@@ -106,16 +110,27 @@ def embed(ids: torch.Tensor, table: torch.Tensor, scale: torch.Tensor, *, alpha:
           dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``alpha * table[ids]``, [*ids.shape, dim]; rows of ids outside the table are zero."""
     e, vocab, dim = _fp8_weight(table, scale, "the table")
-    _need(e == 1, "an embedding table is [vocab, dim]")
-    _need(dtype in _TYPES, f"no embedding output of {dtype}")
-    nbytes = _ids(ids)
-    call = _Call(ids.device, stream)
-    _on(ids.device, table, scale)
-    n = ids.numel()
-    out = call.out(out, tuple(ids.shape) + (dim,), dtype, "out")
-    _need(out.dim() == 2 or out.is_contiguous(), "out must be contiguous")
-    ld = _rows(out, "out") if out.dim() == 2 else dim
-    F.fp8z1_embed(vocab, dim, table, scale, ids, nbytes, n, alpha, out, _TYPES[dtype], ld, call.stream)
+    nbytes, kind = _ID_BYTES.get(ids.dtype), _TYPES.get(dtype)
+    if e != 1:
+        _bad("an embedding table is [vocab, dim]")
+    if nbytes is None or not ids.is_contiguous():
+        _bad("ids must be contiguous int32 or int64")
+    if kind is None:
+        _bad(f"no embedding output of {dtype}")
+    dev = ids.get_device()
+    raw, other = _begin(dev, stream)
+    _same_device(dev, table, scale)
+    shape = ids.shape + (dim,)
+    ld = dim
+    if out is None:
+        out = _new(shape, dtype, dev, other)
+    else:
+        _given(out, shape, dtype, dev, "out")
+        if out.dim() == 2:
+            ld = _rows(out, "out")
+        elif not out.is_contiguous():
+            _bad("out must be contiguous")
+    F.fp8z1_embed(vocab, dim, table, scale, ids, nbytes, ids.numel(), alpha, out, kind, ld, raw)
     return out
 
 
@@ -123,18 +138,28 @@ def embed_grad(ids: torch.Tensor, dy: torch.Tensor, vocab: int, *, alpha: float 
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The FP32 [vocab, dim] gradient of ``embed``'s table from ``dy``
     [*ids.shape, dim] (every row written; repeatable bit for bit)."""
-    nbytes = _ids(ids)
-    _need(dy.dtype in _TYPES, f"no gradient of {dy.dtype}")
-    _need(dy.dim() >= 1 and tuple(dy.shape[:-1]) == tuple(ids.shape), "dy must be [*ids.shape, dim]")
+    nbytes, kind = _ID_BYTES.get(ids.dtype), _TYPES.get(dy.dtype)
+    if nbytes is None or not ids.is_contiguous():
+        _bad("ids must be contiguous int32 or int64")
+    if kind is None:
+        _bad(f"no gradient of {dy.dtype}")
+    if dy.dim() < 1 or dy.shape[:-1] != ids.shape:
+        _bad("dy must be [*ids.shape, dim]")
     dim, n = dy.shape[-1], ids.numel()
-    call = _Call(ids.device, stream)
-    _on(ids.device, dy)
-    _need(dy.dim() == 2 or dy.is_contiguous(), "dy must be contiguous")
-    ld = _rows(dy, "dy") if dy.dim() == 2 else dim
-    out = call.out(out, (vocab, dim), torch.float32, "out")
-    _need(out.is_contiguous(), "out must be contiguous")
-    ws = call.bytes(F.fp8z1_embed_grad_workspace(vocab, dim, n))
-    F.fp8z1_embed_grad(vocab, dim, ids, nbytes, n, alpha, dy, _TYPES[dy.dtype], ld, out, ws, call.stream)
+    dev = ids.get_device()
+    raw, other = _begin(dev, stream)
+    _same_device(dev, dy)
+    ld = dim
+    if dy.dim() == 2:
+        ld = _rows(dy, "dy")
+    elif not dy.is_contiguous():
+        _bad("dy must be contiguous")
+    if out is None:
+        out = _new((vocab, dim), torch.float32, dev, other)
+    elif not _given(out, (vocab, dim), torch.float32, dev, "out").is_contiguous():
+        _bad("out must be contiguous")
+    ws = _new(F.fp8z1_embed_grad_workspace(vocab, dim, n), torch.uint8, dev, other)
+    F.fp8z1_embed_grad(vocab, dim, ids, nbytes, n, alpha, dy, kind, ld, out, ws, raw)
     return out
 
 
@@ -144,15 +169,16 @@ def embed_grad(ids: torch.Tensor, dy: torch.Tensor, vocab: int, *, alpha: float 
 def _ffn_dims(x, gate_up, gate_up_scale, down, down_scale, offsets):
     e, h, f2 = _fp8_weight(gate_up, gate_up_scale, "gate_up")
     e2, f, h2 = _fp8_weight(down, down_scale, "down")
-    _need(e == e2 and h == h2 and f2 == 2 * f, f"gate_up [{e}, {h}, {f2}] and down [{e2}, {f}, {h2}] do not match: "
-          "[E, hidden, 2 inner] and [E, inner, hidden]")
-    _need(x.dim() == 2 and x.shape[1] == h and x.dtype == torch.bfloat16, f"x must be bfloat16 [tokens, {h}]")
-    if offsets is not None:
-        _need(offsets.dtype == torch.int32 and offsets.is_contiguous() and tuple(offsets.shape) == (e + 1,),
-              f"offsets must be contiguous int32 [{e + 1}]")
-    else:
-        _need(e == 1, "several experts need offsets")
-    _on(x.device, gate_up, gate_up_scale, down, down_scale, offsets)
+    if e != e2 or h != h2 or f2 != 2 * f:
+        _bad(f"gate_up [{e}, {h}, {f2}] and down [{e2}, {f}, {h2}] do not match: [E, hidden, 2 inner] and "
+             "[E, inner, hidden]")
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != h:
+        _bad(f"x must be bfloat16 [tokens, {h}]")
+    if offsets is None:
+        if e != 1:
+            _bad("several experts need offsets")
+    elif offsets.dtype != torch.int32 or offsets.shape != (e + 1,) or not offsets.is_contiguous():
+        _bad(f"offsets must be contiguous int32 [{e + 1}]")
     return F.fp8z1_ffn_dims(x.shape[0], h, f, e)
 
 
@@ -164,14 +190,19 @@ def ffn_forward(x: torch.Tensor, gate_up: torch.Tensor, gate_up_scale: torch.Ten
     [offsets[e], offsets[e + 1])).  With ``save`` also the buffer that
     ``ffn_backward`` reads: (y, saved)."""
     dims = _ffn_dims(x, gate_up, gate_up_scale, down, down_scale, offsets)
-    call = _Call(x.device, stream)
-    y = call.out(out, tuple(x.shape), torch.bfloat16, "out")
+    dev = x.get_device()
+    raw, other = _begin(dev, stream)
+    _same_device(dev, gate_up, gate_up_scale, down, down_scale, offsets)
+    if out is None:
+        out = _new(x.shape, torch.bfloat16, dev, other)
+    else:
+        _given(out, x.shape, torch.bfloat16, dev, "out")
     saved_bytes, forward_bytes, _ = F.fp8z1_ffn_sizes(dims)
-    saved = call.bytes(saved_bytes) if save else None
-    ws = call.bytes(forward_bytes)
-    F.fp8z1_ffn_forward(dims, x, _rows(x, "x"), offsets, gate_up, gate_up_scale, down, down_scale, y, _rows(y, "out"),
-                        saved, ws, call.stream)
-    return (y, saved) if save else y
+    saved = _new(saved_bytes, torch.uint8, dev, other) if save else None
+    ws = _new(forward_bytes, torch.uint8, dev, other)
+    F.fp8z1_ffn_forward(dims, x, _rows(x, "x"), offsets, gate_up, gate_up_scale, down, down_scale, out,
+                        _rows(out, "out"), saved, ws, raw)
+    return (out, saved) if save else out
 
 
 def ffn_backward(dy: torch.Tensor, x: torch.Tensor, saved: torch.Tensor, gate_up: torch.Tensor,
@@ -182,49 +213,65 @@ def ffn_backward(dy: torch.Tensor, x: torch.Tensor, saved: torch.Tensor, gate_up
     arguments: dx bfloat16 (None without ``need_dx``), the weight gradients
     FP32 in the weights' shapes."""
     dims = _ffn_dims(x, gate_up, gate_up_scale, down, down_scale, offsets)
-    _need(dy.dtype == torch.bfloat16 and tuple(dy.shape) == tuple(x.shape), "dy must be bfloat16 of x's shape")
-    call = _Call(x.device, stream)
-    _on(x.device, dy, saved)
+    if dy.dtype != torch.bfloat16 or dy.shape != x.shape:
+        _bad("dy must be bfloat16 of x's shape")
+    dev = x.get_device()
+    raw, other = _begin(dev, stream)
+    _same_device(dev, dy, saved, gate_up, gate_up_scale, down, down_scale, offsets)
     saved_bytes, _, backward_bytes = F.fp8z1_ffn_sizes(dims)
-    _need(saved.dtype == torch.uint8 and saved.numel() >= saved_bytes, "saved is not from ffn_forward of these sizes")
-    dx = call.empty(tuple(x.shape), torch.bfloat16) if need_dx else None
-    d_gate_up = call.out(d_gate_up, tuple(gate_up.shape), torch.float32, "d_gate_up")
-    d_down = call.out(d_down, tuple(down.shape), torch.float32, "d_down")
-    _need(d_gate_up.is_contiguous() and d_down.is_contiguous(), "the weight gradients must be contiguous")
-    ws = call.bytes(backward_bytes)
+    if saved.dtype != torch.uint8 or saved.numel() < saved_bytes:
+        _bad("saved is not from ffn_forward of these sizes")
+    dx = _new(x.shape, torch.bfloat16, dev, other) if need_dx else None
+    grads = []
+    for given, w, what in ((d_gate_up, gate_up, "d_gate_up"), (d_down, down, "d_down")):
+        if given is None:
+            given = _new(w.shape, torch.float32, dev, other)
+        elif not _given(given, w.shape, torch.float32, dev, what).is_contiguous():
+            _bad(f"{what} must be contiguous")
+        grads.append(given)
+    ws = _new(backward_bytes, torch.uint8, dev, other)
     F.fp8z1_ffn_backward(dims, dy, _rows(dy, "dy"), x, _rows(x, "x"), offsets, gate_up, gate_up_scale, down,
-                         down_scale, saved, dx, _rows(dx, "dx") if need_dx else 0, d_gate_up, d_down, ws, call.stream)
-    return dx, d_gate_up, d_down
+                         down_scale, saved, dx, _rows(dx, "dx") if need_dx else 0, grads[0], grads[1], ws, raw)
+    return dx, grads[0], grads[1]
 
 
 # ---- distillation --------------------------------------------------------------------
 
 
-def _distill(logits, teacher_ids, teacher_logits, temperature, row_weight, dlogits, call):
-    _need(logits.dtype in _TYPES, f"no logits of {logits.dtype}")
-    ld = _rows(logits, "logits")
+def _distill(logits, teacher_ids, teacher_logits, temperature, row_weight, grad, out, stream):
+    kind = _TYPES.get(logits.dtype)
+    if kind is None or logits.dim() != 2:
+        _bad("logits must be float32 or bfloat16 [rows, vocab]")
     rows, vocab = logits.shape
-    _need(teacher_ids.dtype == torch.int32 and teacher_ids.dim() == 2 and teacher_ids.shape[0] == rows
-          and teacher_ids.is_contiguous(), "teacher_ids must be contiguous int32 [rows, top]")
-    _need(teacher_logits.dtype == torch.float32 and teacher_logits.shape == teacher_ids.shape
-          and teacher_logits.is_contiguous(), "teacher_logits must be contiguous float32 of teacher_ids' shape")
-    if row_weight is not None:
-        _need(row_weight.dtype == torch.float32 and row_weight.is_contiguous() and tuple(row_weight.shape) == (rows,),
-              "row_weight must be contiguous float32 [rows]")
-    _on(logits.device, teacher_ids, teacher_logits, row_weight)
-    loss = call.empty((rows,), torch.float32)
-    F.fp8z1_distill(logits, _TYPES[logits.dtype], ld, rows, vocab, teacher_ids, teacher_logits, teacher_ids.shape[1],
-                    temperature, row_weight, loss, dlogits, 0 if dlogits is None else _rows(dlogits, "dlogits"),
-                    call.stream)
-    return loss
+    shape = teacher_ids.shape
+    if teacher_ids.dtype != torch.int32 or len(shape) != 2 or shape[0] != rows or not teacher_ids.is_contiguous():
+        _bad("teacher_ids must be contiguous int32 [rows, top]")
+    if teacher_logits.dtype != torch.float32 or teacher_logits.shape != shape or not teacher_logits.is_contiguous():
+        _bad("teacher_logits must be contiguous float32 of teacher_ids' shape")
+    if row_weight is not None and (row_weight.dtype != torch.float32 or row_weight.shape != (rows,)
+                                   or not row_weight.is_contiguous()):
+        _bad("row_weight must be contiguous float32 [rows]")
+    dev = logits.get_device()
+    raw, other = _begin(dev, stream)
+    _same_device(dev, teacher_ids, teacher_logits, row_weight)
+    ld, ld_d = _rows(logits, "logits"), 0
+    if grad:
+        if out is None:
+            out = _new(logits.shape, logits.dtype, dev, other)
+            ld_d = vocab
+        else:
+            ld_d = _rows(_given(out, logits.shape, logits.dtype, dev, "out"), "out")
+    loss = _new(rows, torch.float32, dev, other)
+    F.fp8z1_distill(logits, kind, ld, rows, vocab, teacher_ids, teacher_logits, shape[1], temperature, row_weight,
+                    loss, out, ld_d, raw)
+    return loss, out
 
 
 def distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, *,
                  temperature: float = 1.0, row_weight: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Each row's ``temperature^2 * KL(p || q)`` against the teacher's listed
     logits, float32 [rows] (0 in rows of weight 0 or without a teacher entry)."""
-    call = _Call(logits.device, stream)
-    return _distill(logits, teacher_ids, teacher_logits, temperature, row_weight, None, call)
+    return _distill(logits, teacher_ids, teacher_logits, temperature, row_weight, False, None, stream)[0]
 
 
 def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, *,
@@ -233,6 +280,4 @@ def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_l
     """(loss, dlogits): ``distill_loss`` and the gradient of
     ``(row_weight * loss).sum()`` in the logits' type.  ``out`` may be
     ``logits`` itself."""
-    call = _Call(logits.device, stream)
-    d = call.out(out, tuple(logits.shape), logits.dtype, "out")
-    return _distill(logits, teacher_ids, teacher_logits, temperature, row_weight, d, call), d
+    return _distill(logits, teacher_ids, teacher_logits, temperature, row_weight, True, out, stream)
