@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Runs runs, PlanBuffers p, in
     const int e = threadIdx.x, n = (int)runs.experts;
     int64_t lo = 0, hi = 0;
     if (e < n) runs.get(e, lo, hi);
-    const int64_t mine = (hi - lo + kRows - 1) / kRows;
+    const int64_t mine = (hi - lo + 2 * kRows - 1) / (2 * kRows) * 2;
     // a table that does not ascend could name more than `most` tiles: every expert's share ends there
     sums[e] = (int32_t)min(mine, most);
     __syncthreads();
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Runs runs, PlanBuffers p, in
         }
         int64_t l, h;
         runs.get(a, l, h);
-        const int64_t token0 = l + (int64_t)(t - (a ? sums[a - 1] : 0)) * kRows;
+        const int64_t token0 = min(l + (int64_t)(t - (a ? sums[a - 1] : 0)) * kRows, h);
         p.tiles[t] = Tile{a, (int32_t)token0, (int32_t)min(h - token0, (int64_t)kRows), 0};
     }
 }

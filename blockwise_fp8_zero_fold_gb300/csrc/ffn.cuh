@@ -1,10 +1,9 @@
 // The gated feed-forward block's buffers, shared by its translation units.
 //
-// Token rows are regrouped so that every expert starts a tile of 128 rows:
-// tile t of the launch holds rows [token0, token0 + rows) of its expert, and
-// row r of it is row 128 t + r of every internal buffer (rows past the
-// expert's end are zeros).  The tensor core products then never read another
-// expert's rows.
+// Token rows are regrouped so that every expert starts a pair of tiles of 128
+// rows (a pair of CTAs multiplies 256): tile t of the launch holds rows [token0,
+// token0 + rows) of its expert, and row r of it is row 128 t + r of every
+// internal buffer.  A pair's second tile may hold none.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -31,7 +30,7 @@ struct Peaks {
 // Which rows belong to whom; written by the plan kernel.
 struct Plan {
     const int32_t* n_tiles;
-    const int32_t* start;   // [experts + 1] first tile of each expert
+    const int32_t* start;   // [experts + 1] first tile of each expert (even)
     const int32_t* tokens;  // [experts] rows of each
     const Tile* tiles;      // [n_tiles]
 };
@@ -45,7 +44,7 @@ struct Pairs {
 
 struct Dims {
     int64_t T, H, F, E;
-    int64_t tiles() const { return T / kRows + (E < T ? E : T); }  // at most
+    int64_t tiles() const { return 2 * (T / (2 * kRows) + (E < T ? E : T)); }  // at most
     int64_t rows() const { return tiles() * kRows; }
     int64_t Hp() const { return (H + 127) / 128 * 128; }
 };
@@ -211,6 +210,44 @@ int launch_dx(const Dims& d, const Plan& p, const Pairs& dgu, const Weight& w, b
 // The weight gradients; see ffn_wgrad.cu.
 int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
 int launch_d_down(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
+
+// Launches a persistent kernel of one CTA an SM and two a cluster: as many
+// pairs as run at once, `most` at most.
+template <auto kKernel, class... P>
+int launch_pairs(int threads, uint32_t smem, int64_t most, cudaStream_t s, const P&... args)
+{
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    // what the device holds at once, asked once for each kernel and device
+    static std::atomic<int> holds[16];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FP8Z1_ECUDA;
+    int n = dev < 16 ? holds[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        c.gridDim = dim3(2);
+        if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kKernel, &c) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            return FP8Z1_ECUDA;
+        }
+        if (dev < 16) holds[dev].store(n, std::memory_order_relaxed);
+    }
+    c.gridDim = dim3((unsigned)((most < n ? most : n) * 2));
+    count_launch();
+    if (cudaLaunchKernelEx(&c, kKernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return FP8Z1_ECUDA;
+    }
+    return launch_status();
+}
 
 // A tensor map over `rank` dimensions (innermost first; strides in bytes of
 // dimensions 1..).  Returns a status.

@@ -16,9 +16,11 @@
 // memory, 128 of k at a time; epilogue warps scale each and add it to the
 // tile's sums in registers (FP32) while the next 128 are multiplied.
 //
-// A CTA owns 128 rows x 256 columns.  Warp 0 issues TMA copies of K steps
-// (64 KB: the rows' hi and lo, 256 weight columns) three steps ahead, warp 1
-// the products into one of two 256-column accumulators, 8 warps add up.
+// A pair of CTAs owns 256 rows x 256 columns, each the sums of its 128 rows.
+// In each, warp 0 issues TMA copies of K steps (48 KB: the rows' hi and lo, 128
+// weight columns) four steps ahead and 16 warps add up; warp 1 of the first
+// issues the products of both into one of two 256-column accumulators.
+//
 // CTAs are persistent; tiles run expert by expert, a column's row tiles next
 // to each other, so that an expert's codes are read from memory once.
 #include "ffn.cuh"
@@ -34,11 +36,11 @@ __device__ unsigned g_timeouts;
 enum Mode { kGateUp, kDown, kDh, kDx };
 
 constexpr int kCols = 256;   // columns of a tile, in two chunks of 128
-constexpr int kStages = 3;
-constexpr int kThreads = 384;
+constexpr int kStages = 4;
+constexpr int kThreads = 640;  // 4 warps that feed, 16 that add up
 constexpr uint32_t kOperand = 128 * 128;          // bytes of a 128 x 128 operand tile
-constexpr uint32_t kStageBytes = 4 * kOperand;    // hi, lo, two chunks of the weight
-constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 4096;
+constexpr uint32_t kStageBytes = 3 * kOperand;    // hi, lo, this CTA's half of the weight columns
+constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 4096 + 512;
 
 struct Args {
     Plan plan;
@@ -50,6 +52,7 @@ struct Args {
     int32_t n_tiles;       // column tiles
     int32_t k_blocks;
     int32_t sr, sc;        // the scale grid of an expert
+    int32_t b_step;        // from one K block's scale to the next
     Pairs h;               // kGateUp
     float* gu;             // kGateUp (NULL: not kept), [tile][2F][128]
     float* dh;             // kDh, [tile][F][128]
@@ -62,16 +65,17 @@ struct Work {
     int32_t tile, expert, token0, rows, n;
 };
 
-// The i-th tile of the launch, expert by expert, column by column.
-__device__ __forceinline__ Work work_at(const Args& a, int64_t i)
+// The i-th pair of tiles of the launch, expert by expert, column by column, and
+// the tile of CTA `rank`.
+__device__ __forceinline__ Work work_at(const Args& a, int64_t i, int rank)
 {
-    const int32_t t = (int32_t)(i / a.n_tiles);
+    const int32_t t = (int32_t)(i / a.n_tiles) * 2;
     const int32_t e = a.plan.tiles[t].expert;
-    const int32_t first = a.plan.start[e], count = a.plan.start[e + 1] - first;
-    const int64_t local = i - (int64_t)first * a.n_tiles;
+    const int32_t first = a.plan.start[e], pairs = (a.plan.start[e + 1] - first) / 2;
+    const int64_t local = i - (int64_t)(first / 2) * a.n_tiles;
     Work w;
-    w.n = (int32_t)(local / count);
-    w.tile = first + (int32_t)(local - (int64_t)w.n * count);
+    w.n = (int32_t)(local / pairs);
+    w.tile = first + (int32_t)(local - (int64_t)w.n * pairs) * 2 + rank;
     const Tile tile = a.plan.tiles[w.tile];
     w.expert = e;
     w.token0 = tile.token0;
@@ -85,14 +89,22 @@ __device__ __forceinline__ int chunk_column(const Args& a, const Work& w, int c)
     return kMode == kGateUp ? (int)(c * a.F) + w.n * 128 : w.n * kCols + c * 128;
 }
 
-// The scale of weight block (k block, column chunk c); 0 past the columns.
+// The scales of weight column chunk c, K block by K block b_step apart (a chunk
+// past the columns: any of the expert's, its sums are not stored).
 template <int kMode>
-__device__ __forceinline__ float b_scale(const Args& a, const Work& w, int kb, int c)
+__device__ __forceinline__ const float* b_scale(const Args& a, const Work& w, int c)
 {
     const int n = chunk_column<kMode>(a, w, c) >> 7;
     const float* s = a.b_scale + (int64_t)w.expert * a.sr * a.sc;
-    if (kMode == kGateUp || kMode == kDown) return n < a.sc ? __ldg(s + (int64_t)kb * a.sc + n) : 0.0f;
-    return n < a.sr ? __ldg(s + (int64_t)n * a.sc + kb) : 0.0f;
+    if (kMode == kGateUp || kMode == kDown) return s + min(n, a.sc - 1);
+    return s + (int64_t)min(n, a.sr - 1) * a.sc;
+}
+// Stays where it is, ahead of its use.
+__device__ __forceinline__ float load_ahead(const float* p)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -105,14 +117,15 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     const uint32_t extra = base + kStages * kStageBytes;
-    // extra: full[3], empty[3], accumulator ready[2], free[2], tensor memory base, exchange, its amax[2][2][128]
-    const uint32_t bar_full = extra, bar_empty = extra + 32, bar_acc = extra + 64, bar_free = extra + 80,
-                   bar_exchange = extra + 104;
+    // extra: full[4], empty[4], accumulators ready[2], free[2], tensor memory base, exchange, its amax[2][4][128]
+    const uint32_t bar_full = extra, bar_empty = extra + 32, bar_acc = extra + 64, bar_free = extra + 96,
+                   bar_exchange = extra + 136;
     uint8_t* extra_ptr = smem_raw + (extra - smem_addr(smem_raw));
-    volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(extra_ptr + 96);
-    float* exchange = reinterpret_cast<float*>(extra_ptr + 128);  // [2][2][128]
+    volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(extra_ptr + 128);
+    float* exchange = reinterpret_cast<float*>(extra_ptr + 256);  // [2][4][128]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(bar_full + 8 * i, 1);
@@ -120,145 +133,166 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(bar_acc + 8 * i, 1);
-            bar_init(bar_free + 8 * i, 256);
+            bar_init(bar_free + 8 * i, 32);  // the adding warps of both CTAs
         }
-        bar_init(bar_exchange, 256);
+        bar_init(bar_exchange, 512);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
         prefetch_map(&map_hi);
         prefetch_map(&map_lo);
         prefetch_map(&map_w);
     }
-    if (warp == 2) tmem_alloc<512>(extra + 96);
+    if (warp == 2) tmem_alloc<512>(extra + 128);
     fence_before();
     __syncthreads();
+    __syncwarp();
+    cluster_sync();  // the other CTA counts on this one's barriers from here on
     fence_after();
     const uint32_t tmem = *tmem_at;
-    const int64_t total = (int64_t)*a.plan.n_tiles * a.n_tiles;
+    const int64_t total = (int64_t)(*a.plan.n_tiles / 2) * a.n_tiles;
+    const int64_t i0 = blockIdx.x / 2, step = gridDim.x / 2;
     bool ok = true;
 
     if (warp < 4) {
-        regs_less<56>();
+        regs_less<48>();
         if (warp == 0 && lane == 0) {
             // TMA: K steps of every tile, kStages ahead
-            int64_t it = 0;
-            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
-                const Work w = work_at(a, i);
-                const int c0 = chunk_column<kMode>(a, w, 0), c1 = chunk_column<kMode>(a, w, 1);
-                for (int kb = 0; kb < a.k_blocks; ++kb, ++it) {
-                    const int s = (int)(it % kStages);
-                    if (it >= kStages && !bar_wait(bar_empty + 8 * s, (uint32_t)(it / kStages - 1) & 1)) {
+            Turn<kStages> turn;
+            for (int64_t i = i0; i < total && ok; i += step) {
+                const Work w = work_at(a, i, rank);
+                const int c = chunk_column<kMode>(a, w, rank);
+                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next()) {
+                    if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t full = bar_full + 8 * s, dst = base + s * kStageBytes;
-                    bar_expect(full, kStageBytes);
+                    // both CTAs' copies are counted in the first one, whose thread multiplies
+                    if (rank == 0) bar_expect(bar_full + 8 * turn.slot, 2 * kStageBytes);
+                    const uint32_t full = first_of_pair(bar_full + 8 * turn.slot), dst = base + turn.slot * kStageBytes;
                     load_2d(dst, &map_hi, full, kb * 128, w.tile * kRows);
                     load_2d(dst + kOperand, &map_lo, full, kb * 128, w.tile * kRows);
-                    if (kMode == kGateUp || kMode == kDown) {
-                        load_3d(dst + 2 * kOperand, &map_w, full, c0, kb * 128, w.expert);
-                        load_3d(dst + 3 * kOperand, &map_w, full, c1, kb * 128, w.expert);
-                    } else {
-                        load_3d(dst + 2 * kOperand, &map_w, full, kb * 128, c0, w.expert);
-                        load_3d(dst + 3 * kOperand, &map_w, full, kb * 128, c1, w.expert);
-                    }
+                    if (kMode == kGateUp || kMode == kDown)
+                        load_3d(dst + 2 * kOperand, &map_w, full, c, kb * 128, w.expert);
+                    else
+                        load_3d(dst + 2 * kOperand, &map_w, full, kb * 128, c, w.expert);
                 }
             }
-            // the copies in flight land before the CTA ends, whatever became of the other warps
-            for (int64_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-                ok &= bar_wait(bar_full + 8 * (j % kStages), (uint32_t)(j / kStages) & 1);
-        } else if (warp == 1 && lane == 0) {
+            // the copies in flight are read before the CTA ends, whatever became of the other warps
+            for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
             constexpr bool kMnMajor = kMode == kGateUp || kMode == kDown;
-            constexpr uint32_t idesc[2] = {instruction(kRows, kCols, false, kMnMajor),
-                                           instruction(kRows, kCols, false, kMnMajor, true)};
-            int64_t it = 0;
-            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x)
-                for (int kb = 0; kb < a.k_blocks; ++kb, ++it) {
-                    const int s = (int)(it % kStages), acc = (int)(it & 1);
-                    if ((it >= 2 && !bar_wait(bar_free + 8 * acc, (uint32_t)(it / 2 - 1) & 1)) ||
-                        !bar_wait(bar_full + 8 * s, (uint32_t)(it / kStages) & 1)) {
+            constexpr uint32_t idesc[2] = {instruction(kCols, false, kMnMajor),
+                                           instruction(kCols, false, kMnMajor, true)};
+            Turn<kStages> turn;
+            Turn<2> acc;
+            for (int64_t i = i0; i < total && ok; i += step)
+                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next(), acc.next()) {
+                    if (!bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) ||
+                        !bar_wait(bar_full + 8 * turn.slot, turn.phase)) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint32_t src = base + s * kStageBytes, d = tmem + acc * kCols;
+                    const uint32_t src = base + turn.slot * kStageBytes, d = tmem + acc.slot * kCols;
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint64_t da = operand(src + t * kOperand + k * 32, 1024, 16);
-                            // N-major: 8 k are 1024 bytes, the second chunk of 128 columns follows the first;
-                            // K-major: 8 columns are 1024 bytes
+                            // N-major: 8 k are 1024 bytes (all 128 columns); K-major: 8 columns are
                             const uint64_t db = kMnMajor ? operand(src + 2 * kOperand + k * 4096, 1024, kOperand)
                                                          : operand(src + 2 * kOperand + k * 32, 1024, 16);
                             mma_f8(d, da, db, idesc[t], t + k > 0);
                         }
-                    commit(bar_empty + 8 * s);
-                    commit(bar_acc + 8 * acc);
+                    commit(bar_empty + 8 * turn.slot);
+                    commit(bar_acc + 8 * acc.slot);
                 }
-            // the products in flight end before the tensor memory is freed
-            if (it > 0) ok &= bar_wait(bar_acc + 8 * ((it - 1) & 1), (uint32_t)((it - 1) / 2) & 1);
+            // every product issued ends, and its sums are read, before the tensor memory is freed
+            for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
         }
     } else {
-        regs_more<224>();
+        regs_more<104>();
         const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
-        int64_t it = 0;
+        Turn<2> acc;
         int parity = 0;
-        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x, parity ^= 1) {
-            const Work w = work_at(a, i);
+        for (int64_t i = i0; i < total && ok; i += step) {
+            const Work w = work_at(a, i, rank);
             const int64_t at = (int64_t)w.tile * kRows + row;  // row of the internal buffers
-            float sum[2][64];
+            uint64_t sums2[2][16];  // pairs of columns
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int j = 0; j < 64; ++j) sum[c][j] = 0.0f;
-            float sa = a.a_scale[at], s0 = b_scale<kMode>(a, w, 0, 0), s1 = b_scale<kMode>(a, w, 0, 1);
-            for (int kb = 0; kb < a.k_blocks; ++kb, ++it) {
-                const int acc = (int)(it & 1);
-                const float f[2] = {sa * s0, sa * s1};
-                if (kb + 1 < a.k_blocks) {  // the next step's scales, ahead of the wait
-                    sa = a.a_scale[(int64_t)(kb + 1) * a.rows + at];
-                    s0 = b_scale<kMode>(a, w, kb + 1, 0);
-                    s1 = b_scale<kMode>(a, w, kb + 1, 1);
+                for (int j = 0; j < 16; ++j) sums2[c][j] = 0;
+            // The factors of step kb are loaded two steps ahead: a load is as long as a step.
+            const float* pa = a.a_scale + at;
+            const float *pb0 = b_scale<kMode>(a, w, 0), *pb1 = b_scale<kMode>(a, w, 1);
+            float sa[2], s0[2], s1[2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                if (kb < a.k_blocks) {
+                    sa[kb] = load_ahead(pa + (int64_t)kb * a.rows);
+                    s0[kb] = load_ahead(pb0 + kb * a.b_step);
+                    s1[kb] = load_ahead(pb1 + kb * a.b_step);
                 }
+            auto add = [&](int kb, float& va, float& v0, float& v1) {
                 // a warp's lanes agree on the outcome: the loads below are warp-wide
-                ok = __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc, (uint32_t)(it / 2) & 1));
-                if (!ok) break;
+                ok = __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc.slot, acc.phase));
+                if (!ok) return;
                 fence_after();
-                const uint32_t t = tmem + acc * kCols + lanes + group * 64;
-                // columns 64 group + {0, 32, 128, 160} ..; each load is under way while the one before is added
-                uint32_t r[2][32];
-                tmem_load(t, r[0]);
+                const uint64_t f[2] = {pair(va * v0, va * v0), pair(va * v1, va * v1)};
+                if (kb + 2 < a.k_blocks) {
+                    va = load_ahead(pa + (int64_t)(kb + 2) * a.rows);
+                    v0 = load_ahead(pb0 + (kb + 2) * a.b_step);
+                    v1 = load_ahead(pb1 + (kb + 2) * a.b_step);
+                }
+                const uint32_t t = tmem + acc.slot * kCols + lanes + group * 32;
+                // columns 32 group + {0, 16, 128, 144} ..
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    tmem_wait(r[q & 1]);
-                    if (q < 3) {
-                        tmem_load(t + (q + 1) / 2 * 128 + (q + 1) % 2 * 32, r[(q + 1) & 1]);
-                    } else {
+                    uint32_t r[16];
+                    tmem_load(t + q / 2 * 128 + q % 2 * 16, r);
+                    tmem_wait(r);
+                    if (q == 3) {
                         fence_before();
-                        bar_arrive(bar_free + 8 * acc);
+                        __syncwarp();
+                        if (lane == 0) bar_arrive_pair(first_of_pair(bar_free + 8 * acc.slot));
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        sum[q / 2][q % 2 * 32 + j] =
-                            fmaf(__uint_as_float(r[q & 1][j]), f[q / 2], sum[q / 2][q % 2 * 32 + j]);
+                    for (int j = 0; j < 8; ++j)
+                        sums2[q / 2][q % 2 * 8 + j] =
+                            fma_pair(pair(r[2 * j], r[2 * j + 1]), f[q / 2], sums2[q / 2][q % 2 * 8 + j]);
                 }
+                acc.next();
+            };
+            for (int kb = 0; kb < a.k_blocks && ok; kb += 2) {
+                add(kb, sa[0], s0[0], s1[0]);
+                if (kb + 1 < a.k_blocks && ok) add(kb + 1, sa[1], s0[1], s1[1]);
             }
             if (!ok) break;
+            float sum[2][32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float2 v = unpair(sums2[c][j]);
+                    sum[c][2 * j] = v.x;
+                    sum[c][2 * j + 1] = v.y;
+                }
             if constexpr (kMode == kGateUp) {
-                const int n0 = w.n * 128 + group * 64;
+                const int n0 = w.n * 128 + group * 32;
                 float amax = 0.0f, top_g = 0.0f, top_u = 0.0f;
                 if (a.gu) {
                     float* g = a.gu + ((int64_t)w.tile * 2 * a.F + n0) * kRows + row;
                     float* u = g + a.F * kRows;
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
+                    for (int j = 0; j < 32; ++j) {
                         __stcs(g + j * kRows, sum[0][j]);
                         __stcs(u + j * kRows, sum[1][j]);
                         top_g = fmaxf(top_g, fabsf(sum[0][j]));
                         top_u = fmaxf(top_u, fabsf(sum[1][j]));
                     }
+                    if (row >= w.rows) top_g = top_u = 0.0f;
                     const uint32_t pg = __reduce_max_sync(0xffffffffu, abs_bits(top_g));
                     const uint32_t pu = __reduce_max_sync(0xffffffffu, abs_bits(top_u));
                     if (lane == 0) {
@@ -267,24 +301,26 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 64; ++j) {
+                for (int j = 0; j < 32; ++j) {
                     const float g = sum[0][j];
                     sum[0][j] = __fdividef(g, 1.0f + __expf(-g)) * sum[1][j];
                     if (g < -80.0f) sum[0][j] = g * expf(g) * sum[1][j];  // 1 + exp(-g) past the quick quotient
                     amax = fmaxf(amax, fabsf(sum[0][j]));
                 }
-                // the largest of the row's 128 columns: the other 64 are the other group's
-                exchange[(parity * 2 + group) * 128 + row] = amax;
+                // the largest of the row's 128 columns, 32 each of the four groups
+                exchange[(parity * 4 + group) * 128 + row] = amax;
                 bar_arrive(bar_exchange);
                 ok = __all_sync(0xffffffffu, bar_wait(bar_exchange, parity));
                 if (!ok) break;
-                amax = fmaxf(amax, exchange[(parity * 2 + (group ^ 1)) * 128 + row]);
+#pragma unroll
+                for (int o = 0; o < 4; ++o) amax = fmaxf(amax, exchange[(parity * 4 + o) * 128 + row]);
+                parity ^= 1;
                 const PairScale ps = pair_scale(amax);
                 if (group == 0) a.h.scale[(int64_t)w.n * a.rows + at] = ps.down;
                 uint4* hi = reinterpret_cast<uint4*>(a.h.hi + at * a.h.pitch + n0);
                 uint4* lo = reinterpret_cast<uint4*>(a.h.lo + at * a.h.pitch + n0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 2; ++q) {
                     uint32_t vh[4], vl[4];
 #pragma unroll
                     for (int i2 = 0; i2 < 4; ++i2) {
@@ -302,25 +338,25 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 float top = 0.0f;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int64_t n0 = (int64_t)w.n * kCols + c * 128 + group * 64;
+                    const int64_t n0 = (int64_t)w.n * kCols + c * 128 + group * 32;
                     if (n0 >= a.N) continue;  // F is a multiple of 128: a chunk is in or out whole
                     float* o = a.dh + ((int64_t)w.tile * a.F + n0) * kRows + row;
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
+                    for (int j = 0; j < 32; ++j) {
                         __stcs(o + j * kRows, sum[c][j]);
                         top = fmaxf(top, fabsf(sum[c][j]));
                     }
                 }
-                const uint32_t p = __reduce_max_sync(0xffffffffu, abs_bits(top));
+                const uint32_t p = __reduce_max_sync(0xffffffffu, abs_bits(row < w.rows ? top : 0.0f));
                 if (lane == 0) atomicMax(&a.peaks[w.expert].dh, p);
             } else {
                 if (row < w.rows) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int64_t n0 = (int64_t)w.n * kCols + c * 128 + group * 64;
+                        const int64_t n0 = (int64_t)w.n * kCols + c * 128 + group * 32;
                         bf16* o = a.out + (int64_t)(w.token0 + row) * a.ld + n0;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
+                        for (int q = 0; q < 4; ++q) {
                             if (n0 + q * 8 >= a.N) break;  // N is a multiple of 16
                             uint32_t v[4];
 #pragma unroll
@@ -339,6 +375,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     if (!ok) atomicAdd(&g_timeouts, 1u);
     fence_before();
     __syncthreads();
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while the other may still write to it
     fence_after();
     if (warp == 2) tmem_free<512>(tmem);
 }
@@ -365,13 +403,8 @@ int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a,
     a.k_blocks = (int32_t)ceil_div(K, kBlock);
     a.sr = (int32_t)ceil_div(w.R, 128);
     a.sc = (int32_t)ceil_div(w.C, 128);
-    const int sms = sm_count_here();
-    if (sms < 1 || cudaFuncSetAttribute(gemm_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-        return FP8Z1_ECUDA;
-    const int64_t most = d.tiles() * a.n_tiles;
-    count_launch();
-    gemm_kernel<kMode><<<(unsigned)(most < sms ? most : sms), kThreads, kSmem, s>>>(hi, lo, wm, a);
-    return launch_status();
+    a.b_step = kMode == kGateUp || kMode == kDown ? a.sc : 1;
+    return launch_pairs<gemm_kernel<kMode>>(kThreads, kSmem, d.tiles() / 2 * a.n_tiles, s, hi, lo, wm, a);
 }
 
 }  // namespace

@@ -10,12 +10,13 @@
 // BF16 product and keep FP32's accuracy; one BF16 product would lose 16 bits
 // of it, and the optimizer's grads are FP32.
 //
-// A CTA owns 128 x 256 of a gradient: 128 columns of the two-term operand (the
-// lanes of tensor memory), 256 of the other.  Both are row-major over tokens,
-// that is M- and N-major to the tensor cores.  The pipeline is ffn_gemm.cu's:
-// TMA steps of 64 token rows (64 KB), products into two accumulators, each
-// 512 rows added up in registers.  The last step issues only the 16-row
-// products that hold rows; rows past an expert's end are zeros.
+// A pair of CTAs owns 256 x 256 of a gradient: each 128 columns of the two-term
+// operand (the lanes of its tensor memory), and the other operand's 256 columns
+// half and half.  Both operands are row-major over tokens, that is M- and
+// N-major to the tensor cores.  The pipeline is ffn_gemm.cu's: TMA steps of 64
+// token rows (48 KB a CTA), products into two accumulators, each 512 rows added
+// up in registers.  The last step issues only the 16-row products that hold
+// rows; rows past an expert's end are zeros.
 //
 // Bound by the FP32 gradients written (4 bytes an element) up to about 250
 // tokens an expert, by the tensor cores above.
@@ -31,12 +32,12 @@ __device__ unsigned g_timeouts;
 
 constexpr int kCols = 256;
 constexpr int kStep = 64;  // token rows of a stage
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr int kAdd = 8;    // stages added up in tensor memory before they go to the registers' sums
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;  // 4 warps that feed, 16 that add up
 constexpr uint32_t kChunk = 64 * kStep * 2;     // bytes of 64 columns of a stage
-constexpr uint32_t kStageBytes = 8 * kChunk;    // hi: 2 chunks, lo: 2, the other operand: 4
-constexpr uint32_t kSmem = kStages * kStageBytes + 8 * 4096 + 1024 + 256;
+constexpr uint32_t kStageBytes = 6 * kChunk;    // hi: 2 chunks, lo: 2, half of the other operand: 2
+constexpr uint32_t kSmem = kStages * kStageBytes + 16 * 2048 + 1024 + 256;
 
 struct Args {
     Plan plan;
@@ -56,11 +57,12 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
-    const uint32_t staging = base + kStages * kStageBytes, extra = staging + 8 * 4096;
+    const uint32_t staging = base + kStages * kStageBytes, extra = staging + 16 * 2048;
     const uint32_t bar_full = extra, bar_empty = extra + 32, bar_acc = extra + 64, bar_free = extra + 80;
     volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem_raw + (extra + 96 - smem_addr(smem_raw)));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(bar_full + 8 * i, 1);
@@ -68,7 +70,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(bar_acc + 8 * i, 1);
-            bar_init(bar_free + 8 * i, 256);
+            bar_init(bar_free + 8 * i, 32);  // the adding warps of both CTAs
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
@@ -79,54 +81,54 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
     if (warp == 2) tmem_alloc<512>(extra + 96);
     fence_before();
     __syncthreads();
+    __syncwarp();
+    cluster_sync();  // the other CTA counts on this one's barriers from here on
     fence_after();
     const uint32_t tmem = *tmem_at;
-    const int64_t per = (int64_t)a.m_tiles * a.n_tiles, total = per * a.experts;
+    const int m_pairs = (a.m_tiles + 1) / 2;
+    const int64_t per = (int64_t)m_pairs * a.n_tiles, total = per * a.experts;
+    const int64_t i0 = blockIdx.x / 2, step = gridDim.x / 2;
     bool ok = true;
 
     if (warp < 4) {
-        regs_less<56>();
+        regs_less<48>();
         if (warp == 0 && lane == 0) {
-            int64_t it = 0;
-            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+            Turn<kStages> turn;
+            for (int64_t i = i0; i < total && ok; i += step) {
                 const int e = (int)(i / per), local = (int)(i - e * per);
-                const int m = local % a.m_tiles, n = local / a.m_tiles;
+                const int m = local % m_pairs * 2 + rank, n = local / m_pairs;
                 const int row0 = a.plan.start[e] * kRows, steps = (a.plan.tokens[e] + kStep - 1) / kStep;
-                for (int k = 0; k < steps; ++k, ++it) {
-                    const int s = (int)(it % kStages);
-                    if (it >= kStages && !bar_wait(bar_empty + 8 * s, (uint32_t)(it / kStages - 1) & 1)) {
+                for (int k = 0; k < steps; ++k, turn.next()) {
+                    if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t full = bar_full + 8 * s, dst = base + s * kStageBytes;
-                    bar_expect(full, kStageBytes);
+                    // both CTAs' copies are counted in the first one, whose thread multiplies
+                    if (rank == 0) bar_expect(bar_full + 8 * turn.slot, 2 * kStageBytes);
+                    const uint32_t full = first_of_pair(bar_full + 8 * turn.slot), dst = base + turn.slot * kStageBytes;
                     load_3d(dst, &map_hi, full, 0, row0 + k * kStep, m * 2);
                     load_3d(dst + 2 * kChunk, &map_lo, full, 0, row0 + k * kStep, m * 2);
-                    load_3d(dst + 4 * kChunk, &map_b, full, 0, row0 + k * kStep, n * 4);
+                    load_3d(dst + 4 * kChunk, &map_b, full, 0, row0 + k * kStep, n * 4 + rank * 2);
                 }
             }
-            for (int64_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-                ok &= bar_wait(bar_full + 8 * (j % kStages), (uint32_t)(j / kStages) & 1);
-        } else if (warp == 1 && lane == 0) {
-            constexpr uint32_t idesc = instruction(128, kCols, true, true);
-            int64_t it = 0, sums = 0;
-            for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+            // the copies in flight are read before the CTA ends, whatever became of the other warps
+            for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = instruction(kCols, true, true);
+            Turn<kStages> turn;
+            Turn<2> acc;
+            for (int64_t i = i0; i < total && ok; i += step) {
                 const int tokens = a.plan.tokens[(int)(i / per)];
-                for (int t0 = 0; t0 < tokens && ok; t0 += kAdd * kStep, ++sums) {
-                    const int acc = (int)(sums & 1);
-                    const uint32_t d = tmem + acc * kCols;
-                    if (sums >= 2 && !bar_wait(bar_free + 8 * acc, (uint32_t)(sums / 2 - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    for (int sub = 0; sub < kAdd && t0 + sub * kStep < tokens; ++sub, ++it) {
-                        const int s = (int)(it % kStages);
-                        if (!bar_wait(bar_full + 8 * s, (uint32_t)(it / kStages) & 1)) {
+                for (int t0 = 0; t0 < tokens && ok; t0 += kAdd * kStep, acc.next()) {
+                    const uint32_t d = tmem + acc.slot * kCols;
+                    ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1);
+                    for (int sub = 0; sub < kAdd && t0 + sub * kStep < tokens && ok; ++sub, turn.next()) {
+                        if (!bar_wait(bar_full + 8 * turn.slot, turn.phase)) {
                             ok = false;
                             break;
                         }
                         fence_after();
-                        const uint32_t src = base + s * kStageBytes;
+                        const uint32_t src = base + turn.slot * kStageBytes;
                         const int left = tokens - t0 - sub * kStep, steps = left >= kStep ? 4 : (left + 15) / 16;
                         for (int k = 0; k < steps; ++k) {
                             // 8 rows are 1024 bytes; the next 64 columns follow a chunk later
@@ -134,85 +136,93 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                             mma_f16(d, operand(src + k * 2048, 1024, kChunk), db, idesc, sub + k > 0);
                             mma_f16(d, operand(src + 2 * kChunk + k * 2048, 1024, kChunk), db, idesc, true);
                         }
-                        commit(bar_empty + 8 * s);
+                        commit(bar_empty + 8 * turn.slot);
                     }
-                    if (ok) commit(bar_acc + 8 * acc);
+                    if (ok) commit(bar_acc + 8 * acc.slot);
                 }
             }
-            // every product issued ends before the tensor memory is freed
-            if (sums > 0) ok &= bar_wait(bar_acc + 8 * ((sums - 1) & 1), (uint32_t)((sums - 1) / 2) & 1);
+            // every product issued ends, and its sums are read, before the tensor memory is freed
+            for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
         }
     } else {
-        regs_more<224>();
+        regs_more<104>();
         const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16, mine = staging + (warp - 4) * 4096;
-        int64_t sums = 0;
-        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16, mine = staging + (warp - 4) * 2048;
+        Turn<2> acc;
+        for (int64_t i = i0; i < total && ok; i += step) {
             const int e = (int)(i / per), local = (int)(i - e * per);
-            const int m = local % a.m_tiles, n = local / a.m_tiles;
+            const int m = local % m_pairs * 2 + rank, n = local / m_pairs;
             const int tokens = a.plan.tokens[e];
             const Peaks p = a.peaks[e];
             const Pow2 f = pow2(kTransposed ? -(x_shift(p) + dgu_shift(p)) : -(dy_shift(p) + h_shift(p)));
-            float sum[2][64];
+            const uint64_t fa = pair(f.a, f.a);
+            uint64_t sums2[2][16];  // pairs of columns
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int j = 0; j < 64; ++j) sum[c][j] = 0.0f;
-            for (int t0 = 0; t0 < tokens; t0 += kAdd * kStep, ++sums) {
-                const int acc = (int)(sums & 1);
-                ok = __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc, (uint32_t)(sums / 2) & 1));
+                for (int j = 0; j < 16; ++j) sums2[c][j] = 0;
+            for (int t0 = 0; t0 < tokens; t0 += kAdd * kStep, acc.next()) {
+                ok = __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc.slot, acc.phase));
                 if (!ok) break;
                 fence_after();
-                const uint32_t t = tmem + acc * kCols + lanes + group * 64;
-                uint32_t r[2][32];
-                tmem_load(t, r[0]);
+                const uint32_t t = tmem + acc.slot * kCols + lanes + group * 32;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    tmem_wait(r[q & 1]);
-                    if (q < 3) {
-                        tmem_load(t + (q + 1) / 2 * 128 + (q + 1) % 2 * 32, r[(q + 1) & 1]);
-                    } else {
+                    uint32_t r[16];
+                    tmem_load(t + q / 2 * 128 + q % 2 * 16, r);
+                    tmem_wait(r);
+                    if (q == 3) {
                         fence_before();
-                        bar_arrive(bar_free + 8 * acc);
+                        __syncwarp();
+                        if (lane == 0) bar_arrive_pair(first_of_pair(bar_free + 8 * acc.slot));
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        sum[q / 2][q % 2 * 32 + j] =
-                            fmaf(__uint_as_float(r[q & 1][j]), f.a, sum[q / 2][q % 2 * 32 + j]);
+                    for (int j = 0; j < 8; ++j)
+                        sums2[q / 2][q % 2 * 8 + j] =
+                            fma_pair(pair(r[2 * j], r[2 * j + 1]), fa, sums2[q / 2][q % 2 * 8 + j]);
                 }
             }
             if (!ok) break;
+            if (m >= a.m_tiles) continue;  // an odd last tile's other half
+            float sum[2][32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float2 v = unpair(sums2[c][j]);
+                    sum[c][2 * j] = v.x;
+                    sum[c][2 * j + 1] = v.y;
+                }
             if (f.b != 1.0f)  // a power of two beyond FP32's exponents
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) sum[c][j] *= f.b;
+                    for (int j = 0; j < 32; ++j) sum[c][j] *= f.b;
             if constexpr (kTransposed) {
                 // lanes are consecutive columns of the gradient
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int64_t n0 = (int64_t)n * kCols + c * 128 + group * 64;
+                    const int64_t n0 = (int64_t)n * kCols + c * 128 + group * 32;
                     float* o = a.out + ((int64_t)e * a.N + n0) * a.M + m * 128 + row;
-                    if (n0 + 64 <= a.N) {
+                    if (n0 + 32 <= a.N) {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j, o += a.M) __stcs(o, sum[c][j]);
+                        for (int j = 0; j < 32; ++j, o += a.M) __stcs(o, sum[c][j]);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j, o += a.M)
+                        for (int j = 0; j < 32; ++j, o += a.M)
                             if (n0 + j < a.N) __stcs(o, sum[c][j]);
                     }
                 }
             } else {
-                // lanes are rows: pieces of 32 rows x 16 columns turn in shared memory and leave by TMA, one
-                // being read while the next is written
+                // lanes are rows: pieces of 32 rows x 16 columns turn in shared memory and leave by TMA
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const uint32_t buf = mine + (q & 1) * 2048;
-                    if (lane == 0) store_wait_read<1>();
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t buf = mine;
+                    if (lane == 0) store_wait_read<0>();
                     __syncwarp();
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
-                        const float* x = &sum[q / 4][q % 4 * 16 + v * 4];
+                        const float* x = &sum[q / 2][q % 2 * 16 + v * 4];
                         // 64-byte swizzle: 16-byte units of a row change places with bits 1-2 of the row
                         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
                                          buf + lane * 64 + ((v ^ (lane >> 1 & 3)) << 4)),
@@ -221,7 +231,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                     }
                     fence_async();
                     __syncwarp();
-                    const int n0 = n * kCols + q / 4 * 128 + group * 64 + q % 4 * 16;
+                    const int n0 = n * kCols + q / 2 * 128 + group * 32 + q % 2 * 16;
                     if (lane == 0) {
                         if (n0 < a.N) store_3d(&map_out, buf, n0, m * 128 + (warp & 3) * 32, e);
                         store_commit();
@@ -234,15 +244,17 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
     if (!ok) atomicAdd(&g_timeouts, 1u);
     fence_before();
     __syncthreads();
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while the other may still write to it
     fence_after();
     if (warp == 2) tmem_free<512>(tmem);
 }
 
-// [rows, pitch] FP16 as {64, rows, pitch / 64}
-int map_f16(CUtensorMap* map, const __half* p, int64_t rows, int64_t pitch, uint32_t chunks)
+// [rows, pitch] FP16 as {64, rows, pitch / 64}, fetched 128 columns at a time
+int map_f16(CUtensorMap* map, const __half* p, int64_t rows, int64_t pitch)
 {
     const uint64_t dims[3] = {64, (uint64_t)rows, (uint64_t)(pitch / 64)}, strides[2] = {(uint64_t)pitch * 2, 128};
-    const uint32_t box[3] = {64, kStep, chunks};
+    const uint32_t box[3] = {64, kStep, 2};
     return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dims, strides, box);
 }
 
@@ -255,8 +267,8 @@ int launch(const Dims& d, const Plan& p, const Peaks* peaks, const __half* hi, c
                    ostride[2] = {(uint64_t)d.H * 4, (uint64_t)(d.H * d.F) * 4};
     const uint32_t obox[3] = {16, 32, 1};
     int st;
-    if ((st = map_f16(&mh, hi, d.rows(), M, 2)) != FP8Z1_OK || (st = map_f16(&ml, lo, d.rows(), M, 2)) != FP8Z1_OK ||
-        (st = map_f16(&mb, b, d.rows(), d.Hp(), 4)) != FP8Z1_OK ||
+    if ((st = map_f16(&mh, hi, d.rows(), M)) != FP8Z1_OK || (st = map_f16(&ml, lo, d.rows(), M)) != FP8Z1_OK ||
+        (st = map_f16(&mb, b, d.rows(), d.Hp())) != FP8Z1_OK ||
         (st = kTransposed ? (mo = mb, FP8Z1_OK)
                           : tensor_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, out, odims, ostride, obox,
                                        CU_TENSOR_MAP_SWIZZLE_64B)) != FP8Z1_OK)
@@ -270,14 +282,8 @@ int launch(const Dims& d, const Plan& p, const Peaks* peaks, const __half* hi, c
     a.m_tiles = (int32_t)(M / 128);
     a.n_tiles = (int32_t)ceil_div(d.H, kCols);
     a.experts = (int32_t)d.E;
-    const int sms = sm_count_here();
-    if (sms < 1 || cudaFuncSetAttribute(wgrad_kernel<kTransposed>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
-                       cudaSuccess)
-        return FP8Z1_ECUDA;
-    const int64_t total = (int64_t)a.m_tiles * a.n_tiles * d.E;
-    count_launch();
-    wgrad_kernel<kTransposed><<<(unsigned)(total < sms ? total : sms), kThreads, kSmem, s>>>(mh, ml, mb, mo, a);
-    return launch_status();
+    const int64_t total = (int64_t)((a.m_tiles + 1) / 2) * a.n_tiles * d.E;
+    return launch_pairs<wgrad_kernel<kTransposed>>(kThreads, kSmem, total, s, mh, ml, mb, mo, a);
 }
 
 }  // namespace

@@ -111,6 +111,46 @@ __device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity)
     }
 }
 
+// The cluster address of this CTA's address `a` in the pair's first CTA.
+__device__ __forceinline__ uint32_t first_of_pair(uint32_t a)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+    return r;
+}
+// An arrival on a barrier at a cluster address, after this thread's tensor
+// memory loads (no write to memory is released: see bar_arrive_at).
+__device__ __forceinline__ void bar_arrive_pair(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Every thread of the cluster's CTAs.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// The next of kSlots slots used in turn, and the parity of its use: a consumer
+// waits for `phase` of "full", a producer for `phase ^ 1` of "empty" (which a new
+// barrier has behind it).
+template <int kSlots>
+struct Turn {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 // ---- TMA ----------------------------------------------------------------------
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
@@ -118,10 +158,13 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// Tiles to this CTA's shared memory, counted on a barrier of either CTA of the
+// pair (`bar` is a cluster address, of first_of_pair).
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            dst),
         "l"(map), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
@@ -129,7 +172,7 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, ui
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
             dst),
         "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
@@ -160,31 +203,41 @@ __device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.w
 // this thread's shared memory writes, before a TMA copy reads them
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// ---- tcgen05 -------------------------------------------------------------------
+// ---- tcgen05, by pairs of CTAs ---------------------------------------------------
+//
+// A pair multiplies 256 rows by up to 256 columns: each CTA holds 128 rows of
+// the first operand, half the columns of the second and the sums of its rows.
+// The first CTA's thread issues for both.
 
+// By one warp of each CTA.
 template <int kCols>
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_out)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_out), "n"(kCols)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_out), "n"(kCols)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 template <int kCols>
 __device__ __forceinline__ void tmem_free(uint32_t taddr)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols) : "memory");
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Arrives on `bar` once every matrix product this thread issued has finished.
+// Arrives on the barriers at this offset of both CTAs once every product this
+// thread issued has finished.
 __device__ __forceinline__ void commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
 }
 
-// Shared memory operand, 128-byte swizzle (atoms of 8 rows x 128 bytes).
+// Shared memory operand (at the same offset in both CTAs), 128-byte swizzle
+// (atoms of 8 rows x 128 bytes).
 //   K-major (a row is 128 bytes of k): group_stride = bytes between groups of
 //     8 rows of the M or N index; chunk_stride unused.
 //   M/N-major (a row is 128 bytes of the M or N index): group_stride = bytes
@@ -195,19 +248,19 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t group_stride
            (uint64_t)(group_stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// Instruction descriptor: FP32 accumulator, operand formats E4M3 (f8f6f4) or
-// F16 (f16), both encoded 0, the first operand E5M2 instead with `a_e5m2`;
-// `mn_major` bits say which operands are M/N-major.
-__host__ __device__ constexpr uint32_t instruction(int m, int n, bool a_mn_major, bool b_mn_major, bool a_e5m2 = false)
+// Instruction descriptor of 256 rows x `n` columns: FP32 sums, operand formats
+// E4M3 (f8f6f4) or F16 (f16), both encoded 0, the first operand E5M2 instead
+// with `a_e5m2`; `mn_major` bits say which operands are M/N-major.
+__host__ __device__ constexpr uint32_t instruction(int n, bool a_mn_major, bool b_mn_major, bool a_e5m2 = false)
 {
-    return 1u << 4 | (a_e5m2 ? 1u << 7 : 0u) | (a_mn_major ? 1u << 15 : 0u) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
-           (uint32_t)(m >> 4) << 24;
+    return 1u << 4 | (a_e5m2 ? 1u << 7 : 0u) | (a_mn_major ? 1u << 15 : 0u) | (b_mn_major ? 1u << 16 : 0u) |
+           (uint32_t)(n >> 3) << 17 | (256u >> 4) << 24;
 }
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
@@ -215,30 +268,27 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 
-// 32 columns of this warp's 32 lanes: r[i] = tensor memory (lane, column + i).
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32])
+// 16 columns of this warp's 32 lanes: r[i] = tensor memory (lane, column + i).
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
 // The loads before this are done; `r` is one of them, so that no use of it moves up.
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 template <int kRegs>
@@ -250,6 +300,28 @@ template <int kRegs>
 __device__ __forceinline__ void regs_more()
 {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// Two FP32 numbers in one register pair, and their multiply-add in one
+// instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b)
+{
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(a), "r"(b));
+    return p;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float2 unpair(uint64_t p)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
 }  // namespace tc
