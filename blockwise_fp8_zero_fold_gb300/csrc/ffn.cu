@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Runs runs, PlanBuffers p, in
     const int e = threadIdx.x, n = (int)runs.experts;
     int64_t lo = 0, hi = 0;
     if (e < n) runs.get(e, lo, hi);
-    const int64_t mine = (hi - lo + 2 * kRows - 1) / (2 * kRows) * 2;
+    const int64_t mine = (hi - lo + kRows - 1) / kRows;
     // a table that does not ascend could name more than `most` tiles: every expert's share ends there
     sums[e] = (int32_t)min(mine, most);
     __syncthreads();
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Runs runs, PlanBuffers p, in
         }
         int64_t l, h;
         runs.get(a, l, h);
-        const int64_t token0 = min(l + (int64_t)(t - (a ? sums[a - 1] : 0)) * kRows, h);
+        const int64_t token0 = l + (int64_t)(t - (a ? sums[a - 1] : 0)) * kRows;
         p.tiles[t] = Tile{a, (int32_t)token0, (int32_t)min(h - token0, (int64_t)kRows), 0};
     }
 }
@@ -137,11 +137,12 @@ __global__ void __launch_bounds__(256) split_kernel(Runs runs, Plan plan, const 
     if (warp >= n_rows) return;
     const Tile t = plan.tiles[warp / kRows];
     const int r = (int)(warp % kRows);
+    if (r >= t.rows) return;
     const bf16* src = x + (int64_t)(t.token0 + r) * ld;
     float top = 0.0f;
     for (int64_t c = lane * 8; c < out.pitch; c += 256) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < t.rows && c < H) v = __ldg(reinterpret_cast<const uint4*>(src + c));
+        if (c < H) v = __ldg(reinterpret_cast<const uint4*>(src + c));
         const float2 f[4] = {bf16_pair(v.x), bf16_pair(v.y), bf16_pair(v.z), bf16_pair(v.w)};
         float amax = 0.0f;
 #pragma unroll
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(256) split_kernel(Runs runs, Plan plan, const 
         *reinterpret_cast<uint2*>(out.lo + warp * out.pitch + c) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         if ((lane & 15) == 0) out.scale[c / kBlock * rows + warp] = ps.down;
     }
-    if (peaks && r < t.rows) {
+    if (peaks) {
         const uint32_t p = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
         if (lane == 0) atomicMax(dy ? &peaks[t.expert].dy : &peaks[t.expert].x, p);
     }
@@ -180,6 +181,7 @@ __global__ void __launch_bounds__(256) halves_kernel(Plan plan, const bf16* x, i
     if (warp >= (int64_t)*plan.n_tiles * kRows) return;
     const Tile t = plan.tiles[warp / kRows];
     const int r = (int)(warp % kRows);
+    if (r >= (t.rows + 15) / 16 * 16) return;  // zeros to the next multiple of 16, which is what is multiplied
     const Peaks p = peaks[t.expert];
     const Pow2 fx = pow2(x_shift(p)), fd = pow2(dy_shift(p));
     const bf16* sx = x + (int64_t)(t.token0 + r) * ld_x;
@@ -227,6 +229,10 @@ __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float*
     const int64_t tile = blockIdx.x >> 2;
     if (tile >= *plan.n_tiles) return;
     const int quarter = blockIdx.x & 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Tile t = plan.tiles[tile];
+    const int rows_here = min(t.rows - quarter * 32, 32);  // of this CTA's 32
+    if (rows_here <= 0) return;
+    const bool there = lane < rows_here;
     const int64_t f0 = (int64_t)blockIdx.y * 128;
     const float* pg = gu + (tile * 2 * F + f0) * kRows + quarter * 32 + lane;
     const float* pu = pg + F * kRows;
@@ -234,7 +240,12 @@ __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float*
 #pragma unroll 8
     for (int i = 0; i < 16; ++i) {
         const int c = warp * 16 + i;
-        const float g = __ldcs(pg + c * kRows), u = __ldcs(pu + c * kRows), d = __ldcs(pd + c * kRows);
+        float g = 0.0f, u = 0.0f, d = 0.0f;
+        if (there) {
+            g = __ldcs(pg + c * kRows);
+            u = __ldcs(pu + c * kRows);
+            d = __ldcs(pd + c * kRows);
+        }
         const float s = 1.0f / (1.0f + expf(-g)), a = g * s;
         float* o = act + lane * kActPitch + c;
         o[0] = d * u * s * (1.0f + g * (1.0f - s));
@@ -242,9 +253,10 @@ __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float*
         o[64 * kActPitch] = a * u;
     }
     __syncthreads();
-    const Peaks p = peaks[plan.tiles[tile].expert];
+    const Peaks p = peaks[t.expert];
     const Pow2 fg = pow2(dgu_shift(p)), fh = pow2(h_shift(p));
-    for (int r = warp; r < 32; r += 8) {
+    // zeros to the next multiple of 16, which is what the weight gradients multiply
+    for (int r = warp; r < (rows_here + 15) / 16 * 16; r += 8) {
         const int64_t at = tile * kRows + quarter * 32 + r;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {

@@ -1,9 +1,10 @@
 // The gated feed-forward block's buffers, shared by its translation units.
 //
-// Token rows are regrouped so that every expert starts a pair of tiles of 128
-// rows (a pair of CTAs multiplies 256): tile t of the launch holds rows [token0,
-// token0 + rows) of its expert, and row r of it is row 128 t + r of every
-// internal buffer.  A pair's second tile may hold none.
+// Token rows are regrouped so that every expert starts a tile of 128 rows:
+// tile t of the launch holds rows [token0, token0 + rows) of its expert, and row
+// r of it is row 128 t + r of every internal buffer.  Rows of a tile past its
+// own are multiplied like the others and stored nowhere; in the operands of the
+// weight gradients they are zeros.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -30,7 +31,7 @@ struct Peaks {
 // Which rows belong to whom; written by the plan kernel.
 struct Plan {
     const int32_t* n_tiles;
-    const int32_t* start;   // [experts + 1] first tile of each expert (even)
+    const int32_t* start;   // [experts + 1] first tile of each expert
     const int32_t* tokens;  // [experts] rows of each
     const Tile* tiles;      // [n_tiles]
 };
@@ -44,7 +45,7 @@ struct Pairs {
 
 struct Dims {
     int64_t T, H, F, E;
-    int64_t tiles() const { return 2 * (T / (2 * kRows) + (E < T ? E : T)); }  // at most
+    int64_t tiles() const { return T / kRows + (E < T ? E : T); }  // at most
     int64_t rows() const { return tiles() * kRows; }
     int64_t Hp() const { return (H + 127) / 128 * 128; }
 };
@@ -211,36 +212,36 @@ int launch_dx(const Dims& d, const Plan& p, const Pairs& dgu, const Weight& w, b
 int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
 int launch_d_down(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
 
-// Launches a persistent kernel of one CTA an SM and two a cluster: as many
-// pairs as run at once, `most` at most.
+// Launches a persistent kernel of one CTA an SM, in clusters of one or two: as
+// many as run at once, `most` at most.
 template <auto kKernel, class... P>
-int launch_pairs(int threads, uint32_t smem, int64_t most, cudaStream_t s, const P&... args)
+int launch_clusters(int threads, uint32_t smem, int cluster, int64_t most, cudaStream_t s, const P&... args)
 {
     cudaLaunchConfig_t c = {};
     cudaLaunchAttribute at = {};
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 2;
+    at.val.clusterDim.x = (unsigned)cluster;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     c.blockDim = dim3((unsigned)threads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
     c.attrs = &at;
     c.numAttrs = 1;
-    // what the device holds at once, asked once for each kernel and device
-    static std::atomic<int> holds[16];
+    // what the device holds at once, asked once for each kernel, device and cluster size
+    static std::atomic<int> holds[16][2];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FP8Z1_ECUDA;
-    int n = dev < 16 ? holds[dev].load(std::memory_order_relaxed) : 0;
+    int n = dev < 16 ? holds[dev][cluster - 1].load(std::memory_order_relaxed) : 0;
     if (n == 0) {
-        c.gridDim = dim3(2);
+        c.gridDim = dim3((unsigned)cluster);
         if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, kKernel, &c) != cudaSuccess || n < 1) {
             cudaGetLastError();
             return FP8Z1_ECUDA;
         }
-        if (dev < 16) holds[dev].store(n, std::memory_order_relaxed);
+        if (dev < 16) holds[dev][cluster - 1].store(n, std::memory_order_relaxed);
     }
-    c.gridDim = dim3((unsigned)((most < n ? most : n) * 2));
+    c.gridDim = dim3((unsigned)((most < n ? most : n) * cluster));
     count_launch();
     if (cudaLaunchKernelEx(&c, kKernel, args...) != cudaSuccess) {
         cudaGetLastError();

@@ -16,10 +16,13 @@
 // memory, 128 of k at a time; epilogue warps scale each and add it to the
 // tile's sums in registers (FP32) while the next 128 are multiplied.
 //
-// A pair of CTAs owns 256 rows x 256 columns, each the sums of its 128 rows.
-// In each, warp 0 issues TMA copies of K steps (48 KB: the rows' hi and lo, 128
-// weight columns) four steps ahead and 16 warps add up; warp 1 of the first
-// issues the products of both into one of two 256-column accumulators.
+// A CTA owns 128 rows x 256 columns.  Warp 0 issues TMA copies of K steps (64
+// KB: the rows' hi and lo, 256 weight columns) three steps ahead, warp 1 the
+// products into one of two 256-column accumulators, 16 warps add up.  Two CTAs
+// of a cluster take neighbouring column tiles of the same rows, and one fetches
+// their hi, the other their lo for both.  (Pairs of CTAs with 256 rows were as
+// fast on full tiles and lost a quarter on experts of 100 to 400 rows; transposed
+// products of 128 columns, whose time follows an expert's rows, lost half.)
 //
 // CTAs are persistent; tiles run expert by expert, a column's row tiles next
 // to each other, so that an expert's codes are read from memory once.
@@ -36,11 +39,11 @@ __device__ unsigned g_timeouts;
 enum Mode { kGateUp, kDown, kDh, kDx };
 
 constexpr int kCols = 256;   // columns of a tile, in two chunks of 128
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kThreads = 640;  // 4 warps that feed, 16 that add up
 constexpr uint32_t kOperand = 128 * 128;          // bytes of a 128 x 128 operand tile
-constexpr uint32_t kStageBytes = 3 * kOperand;    // hi, lo, this CTA's half of the weight columns
-constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 4096 + 512;
+constexpr uint32_t kStageBytes = 4 * kOperand;    // hi, lo, two chunks of the weight
+constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 256 + 4096 + 4096;  // stages, barriers, exchange, factors
 
 struct Args {
     Plan plan;
@@ -49,7 +52,8 @@ struct Args {
     int64_t rows;          // of the row operands (pitch of a_scale)
     int64_t F;
     int64_t N;             // columns of the result (kGateUp: F pairs)
-    int32_t n_tiles;       // column tiles
+    int32_t n_groups;      // groups of column tiles
+    int32_t cluster;       // CTAs of a cluster: 1 or 2
     int32_t k_blocks;
     int32_t sr, sc;        // the scale grid of an expert
     int32_t b_step;        // from one K block's scale to the next
@@ -65,17 +69,18 @@ struct Work {
     int32_t tile, expert, token0, rows, n;
 };
 
-// The i-th pair of tiles of the launch, expert by expert, column by column, and
-// the tile of CTA `rank`.
+// The i-th group of column tiles (one, or a cluster's two) of the launch, expert
+// by expert, column by column, and the tile of CTA `rank`.
 __device__ __forceinline__ Work work_at(const Args& a, int64_t i, int rank)
 {
-    const int32_t t = (int32_t)(i / a.n_tiles) * 2;
+    const int32_t t = (int32_t)(i / a.n_groups);
     const int32_t e = a.plan.tiles[t].expert;
-    const int32_t first = a.plan.start[e], pairs = (a.plan.start[e + 1] - first) / 2;
-    const int64_t local = i - (int64_t)(first / 2) * a.n_tiles;
+    const int32_t first = a.plan.start[e], count = a.plan.start[e + 1] - first;
+    const int64_t local = i - (int64_t)first * a.n_groups;
     Work w;
-    w.n = (int32_t)(local / pairs);
-    w.tile = first + (int32_t)(local - (int64_t)w.n * pairs) * 2 + rank;
+    const int32_t group = (int32_t)(local / count);
+    w.n = group * a.cluster + rank;
+    w.tile = first + (int32_t)(local - (int64_t)group * count);
     const Tile tile = a.plan.tiles[w.tile];
     w.expert = e;
     w.token0 = tile.token0;
@@ -99,14 +104,6 @@ __device__ __forceinline__ const float* b_scale(const Args& a, const Work& w, in
     if (kMode == kGateUp || kMode == kDown) return s + min(n, a.sc - 1);
     return s + (int64_t)min(n, a.sr - 1) * a.sc;
 }
-// Stays where it is, ahead of its use.
-__device__ __forceinline__ float load_ahead(const float* p)
-{
-    float v;
-    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    return v;
-}
-
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 template <int kMode>
@@ -117,9 +114,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     const uint32_t extra = base + kStages * kStageBytes;
-    // extra: full[4], empty[4], accumulators ready[2], free[2], tensor memory base, exchange, its amax[2][4][128]
+    // extra: full[3], empty[3], accumulators ready[2], free[2], tensor memory base, exchange, factors ready[4],
+    // read[4]; the amax exchange [2][4][128]; the factors [4][2][128]
     const uint32_t bar_full = extra, bar_empty = extra + 32, bar_acc = extra + 64, bar_free = extra + 96,
-                   bar_exchange = extra + 136;
+                   bar_exchange = extra + 136, bar_factors = extra + 144, bar_read = extra + 176,
+                   factors = extra + 256 + 4096;
     uint8_t* extra_ptr = smem_raw + (extra - smem_addr(smem_raw));
     volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(extra_ptr + 128);
     float* exchange = reinterpret_cast<float*>(extra_ptr + 256);  // [2][4][128]
@@ -129,28 +128,32 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(bar_full + 8 * i, 1);
-            bar_init(bar_empty + 8 * i, 1);
+            bar_init(bar_empty + 8 * i, a.cluster);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(bar_acc + 8 * i, 1);
-            bar_init(bar_free + 8 * i, 32);  // the adding warps of both CTAs
+            bar_init(bar_free + 8 * i, 16);  // the adding warps
         }
         bar_init(bar_exchange, 512);
+        for (int i = 0; i < 4; ++i) {
+            bar_init(bar_factors + 8 * i, 64);
+            bar_init(bar_read + 8 * i, 16);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
         prefetch_map(&map_hi);
         prefetch_map(&map_lo);
         prefetch_map(&map_w);
     }
-    if (warp == 2) tmem_alloc<512>(extra + 128);
+    if (warp == 2) tmem_alloc<1, 512>(extra + 128);
     fence_before();
     __syncthreads();
     __syncwarp();
-    cluster_sync();  // the other CTA counts on this one's barriers from here on
+    cluster_sync();  // the other CTA may write to this one's stages and barriers from here on
     fence_after();
     const uint32_t tmem = *tmem_at;
-    const int64_t total = (int64_t)(*a.plan.n_tiles / 2) * a.n_tiles;
-    const int64_t i0 = blockIdx.x / 2, step = gridDim.x / 2;
+    const int64_t total = (int64_t)*a.plan.n_tiles * a.n_groups;
+    const int64_t i0 = blockIdx.x / a.cluster, step = gridDim.x / a.cluster;
     bool ok = true;
 
     if (warp < 4) {
@@ -160,29 +163,37 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             Turn<kStages> turn;
             for (int64_t i = i0; i < total && ok; i += step) {
                 const Work w = work_at(a, i, rank);
-                const int c = chunk_column<kMode>(a, w, rank);
+                const int c0 = chunk_column<kMode>(a, w, 0), c1 = chunk_column<kMode>(a, w, 1), y = w.tile * kRows;
                 for (int kb = 0; kb < a.k_blocks; ++kb, turn.next()) {
                     if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
                         ok = false;
                         break;
                     }
-                    // both CTAs' copies are counted in the first one, whose thread multiplies
-                    if (rank == 0) bar_expect(bar_full + 8 * turn.slot, 2 * kStageBytes);
-                    const uint32_t full = first_of_pair(bar_full + 8 * turn.slot), dst = base + turn.slot * kStageBytes;
-                    load_2d(dst, &map_hi, full, kb * 128, w.tile * kRows);
-                    load_2d(dst + kOperand, &map_lo, full, kb * 128, w.tile * kRows);
-                    if (kMode == kGateUp || kMode == kDown)
-                        load_3d(dst + 2 * kOperand, &map_w, full, c, kb * 128, w.expert);
-                    else
-                        load_3d(dst + 2 * kOperand, &map_w, full, kb * 128, c, w.expert);
+                    const uint32_t full = bar_full + 8 * turn.slot, dst = base + turn.slot * kStageBytes;
+                    bar_expect(full, kStageBytes);
+                    if (a.cluster == 1) {
+                        load_2d(dst, &map_hi, full, kb * 128, y);
+                        load_2d(dst + kOperand, &map_lo, full, kb * 128, y);
+                    } else if (rank == 0) {
+                        load_2d_both(dst, &map_hi, full, kb * 128, y);
+                    } else {
+                        load_2d_both(dst + kOperand, &map_lo, full, kb * 128, y);
+                    }
+                    if (kMode == kGateUp || kMode == kDown) {
+                        load_3d(dst + 2 * kOperand, &map_w, full, c0, kb * 128, w.expert);
+                        load_3d(dst + 3 * kOperand, &map_w, full, c1, kb * 128, w.expert);
+                    } else {
+                        load_3d(dst + 2 * kOperand, &map_w, full, kb * 128, c0, w.expert);
+                        load_3d(dst + 3 * kOperand, &map_w, full, kb * 128, c1, w.expert);
+                    }
                 }
             }
             // the copies in flight are read before the CTA ends, whatever became of the other warps
             for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && lane == 0) {
             constexpr bool kMnMajor = kMode == kGateUp || kMode == kDown;
-            constexpr uint32_t idesc[2] = {instruction(kCols, false, kMnMajor),
-                                           instruction(kCols, false, kMnMajor, true)};
+            constexpr uint32_t idesc[2] = {instruction(128, kCols, false, kMnMajor),
+                                           instruction(128, kCols, false, kMnMajor, true)};
             Turn<kStages> turn;
             Turn<2> acc;
             for (int64_t i = i0; i < total && ok; i += step)
@@ -199,22 +210,50 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint64_t da = operand(src + t * kOperand + k * 32, 1024, 16);
-                            // N-major: 8 k are 1024 bytes (all 128 columns); K-major: 8 columns are
+                            // N-major: 8 k are 1024 bytes, the second chunk of 128 columns follows the first;
+                            // K-major: 8 columns are 1024 bytes
                             const uint64_t db = kMnMajor ? operand(src + 2 * kOperand + k * 4096, 1024, kOperand)
                                                          : operand(src + 2 * kOperand + k * 32, 1024, 16);
                             mma_f8(d, da, db, idesc[t], t + k > 0);
                         }
-                    commit(bar_empty + 8 * turn.slot);
+                    if (a.cluster == 1)
+                        commit(bar_empty + 8 * turn.slot);
+                    else
+                        commit_both<1>(bar_empty + 8 * turn.slot);
                     commit(bar_acc + 8 * acc.slot);
                 }
             // every product issued ends, and its sums are read, before the tensor memory is freed
             for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
+        } else if (warp >= 2) {
+            // the factors of each step, 2^s_b c_bn of both chunks for two rows a thread
+            Turn<4> turn;
+            const int mine = threadIdx.x - 64;
+            for (int64_t i = i0; i < total && ok; i += step) {
+                const Work w = work_at(a, i, rank);
+                const float* pa = a.a_scale + (int64_t)w.tile * kRows + mine;
+                const float *p0 = b_scale<kMode>(a, w, 0), *p1 = b_scale<kMode>(a, w, 1);
+                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next()) {
+                    const float va = pa[(int64_t)kb * a.rows], vb = pa[(int64_t)kb * a.rows + 64], v0 = p0[kb * a.b_step],
+                                v1 = p1[kb * a.b_step];
+                    if (!bar_wait(bar_read + 8 * turn.slot, turn.phase ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t f = factors + turn.slot * 1024 + mine * 4;
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f), "f"(va * v0) : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f + 256), "f"(vb * v0) : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f + 512), "f"(va * v1) : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f + 768), "f"(vb * v1) : "memory");
+                    bar_arrive(bar_factors + 8 * turn.slot);
+                }
+            }
         }
     } else {
         regs_more<104>();
         const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
         Turn<2> acc;
+        Turn<4> turn;
         int parity = 0;
         for (int64_t i = i0; i < total && ok; i += step) {
             const Work w = work_at(a, i, rank);
@@ -224,28 +263,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) sums2[c][j] = 0;
-            // The factors of step kb are loaded two steps ahead: a load is as long as a step.
-            const float* pa = a.a_scale + at;
-            const float *pb0 = b_scale<kMode>(a, w, 0), *pb1 = b_scale<kMode>(a, w, 1);
-            float sa[2], s0[2], s1[2];
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-                if (kb < a.k_blocks) {
-                    sa[kb] = load_ahead(pa + (int64_t)kb * a.rows);
-                    s0[kb] = load_ahead(pb0 + kb * a.b_step);
-                    s1[kb] = load_ahead(pb1 + kb * a.b_step);
-                }
-            auto add = [&](int kb, float& va, float& v0, float& v1) {
+            for (int kb = 0; kb < a.k_blocks; ++kb, acc.next(), turn.next()) {
                 // a warp's lanes agree on the outcome: the loads below are warp-wide
-                ok = __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc.slot, acc.phase));
-                if (!ok) return;
+                ok = __all_sync(0xffffffffu, bar_wait(bar_factors + 8 * turn.slot, turn.phase) &&
+                                                 bar_wait(bar_acc + 8 * acc.slot, acc.phase));
+                if (!ok) break;
                 fence_after();
-                const uint64_t f[2] = {pair(va * v0, va * v0), pair(va * v1, va * v1)};
-                if (kb + 2 < a.k_blocks) {
-                    va = load_ahead(pa + (int64_t)(kb + 2) * a.rows);
-                    v0 = load_ahead(pb0 + (kb + 2) * a.b_step);
-                    v1 = load_ahead(pb1 + (kb + 2) * a.b_step);
-                }
+                float f0, f1;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f0) : "r"(factors + turn.slot * 1024 + row * 4));
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f1) : "r"(factors + turn.slot * 1024 + 512 + row * 4));
+                const uint64_t f[2] = {pair(f0, f0), pair(f1, f1)};
                 const uint32_t t = tmem + acc.slot * kCols + lanes + group * 32;
                 // columns 32 group + {0, 16, 128, 144} ..
 #pragma unroll
@@ -256,20 +283,19 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     if (q == 3) {
                         fence_before();
                         __syncwarp();
-                        if (lane == 0) bar_arrive_pair(first_of_pair(bar_free + 8 * acc.slot));
+                        if (lane == 0) {
+                            bar_arrive(bar_free + 8 * acc.slot);
+                            bar_arrive(bar_read + 8 * turn.slot);
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         sums2[q / 2][q % 2 * 8 + j] =
                             fma_pair(pair(r[2 * j], r[2 * j + 1]), f[q / 2], sums2[q / 2][q % 2 * 8 + j]);
                 }
-                acc.next();
-            };
-            for (int kb = 0; kb < a.k_blocks && ok; kb += 2) {
-                add(kb, sa[0], s0[0], s1[0]);
-                if (kb + 1 < a.k_blocks && ok) add(kb + 1, sa[1], s0[1], s1[1]);
             }
             if (!ok) break;
+            if (w.n * (kMode == kGateUp ? 128 : kCols) >= a.N) continue;  // past the last column tile of the group
             float sum[2][32];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -378,7 +404,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     __syncwarp();
     cluster_sync();  // no CTA leaves while the other may still write to it
     fence_after();
-    if (warp == 2) tmem_free<512>(tmem);
+    if (warp == 2) tmem_free<1, 512>(tmem);
 }
 
 template <int kMode>
@@ -399,12 +425,14 @@ int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a,
     a.b_scale = w.scale;
     a.rows = d.rows();
     a.F = d.F;
-    a.n_tiles = (int32_t)(kMode == kGateUp ? d.F / 128 : ceil_div(a.N, kCols));
+    const int64_t n_tiles = kMode == kGateUp ? d.F / 128 : ceil_div(a.N, kCols);
+    a.cluster = n_tiles % 2 == 0 || n_tiles > 8 ? 2 : 1;  // an odd tile's neighbour multiplies for nothing
+    a.n_groups = (int32_t)ceil_div(n_tiles, a.cluster);
     a.k_blocks = (int32_t)ceil_div(K, kBlock);
     a.sr = (int32_t)ceil_div(w.R, 128);
     a.sc = (int32_t)ceil_div(w.C, 128);
     a.b_step = kMode == kGateUp || kMode == kDown ? a.sc : 1;
-    return launch_pairs<gemm_kernel<kMode>>(kThreads, kSmem, d.tiles() / 2 * a.n_tiles, s, hi, lo, wm, a);
+    return launch_clusters<gemm_kernel<kMode>>(kThreads, kSmem, a.cluster, d.tiles() * a.n_groups, s, hi, lo, wm, a);
 }
 
 }  // namespace

@@ -78,7 +78,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
         prefetch_map(&map_lo);
         prefetch_map(&map_b);
     }
-    if (warp == 2) tmem_alloc<512>(extra + 96);
+    if (warp == 2) tmem_alloc<2, 512>(extra + 96);
     fence_before();
     __syncthreads();
     __syncwarp();
@@ -106,15 +106,15 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                     // both CTAs' copies are counted in the first one, whose thread multiplies
                     if (rank == 0) bar_expect(bar_full + 8 * turn.slot, 2 * kStageBytes);
                     const uint32_t full = first_of_pair(bar_full + 8 * turn.slot), dst = base + turn.slot * kStageBytes;
-                    load_3d(dst, &map_hi, full, 0, row0 + k * kStep, m * 2);
-                    load_3d(dst + 2 * kChunk, &map_lo, full, 0, row0 + k * kStep, m * 2);
-                    load_3d(dst + 4 * kChunk, &map_b, full, 0, row0 + k * kStep, n * 4 + rank * 2);
+                    load_3d_pair(dst, &map_hi, full, 0, row0 + k * kStep, m * 2);
+                    load_3d_pair(dst + 2 * kChunk, &map_lo, full, 0, row0 + k * kStep, m * 2);
+                    load_3d_pair(dst + 4 * kChunk, &map_b, full, 0, row0 + k * kStep, n * 4 + rank * 2);
                 }
             }
             // the copies in flight are read before the CTA ends, whatever became of the other warps
             for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
         } else if (warp == 1 && lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = instruction(kCols, true, true);
+            constexpr uint32_t idesc = instruction(256, kCols, true, true);
             Turn<kStages> turn;
             Turn<2> acc;
             for (int64_t i = i0; i < total && ok; i += step) {
@@ -133,12 +133,12 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                         for (int k = 0; k < steps; ++k) {
                             // 8 rows are 1024 bytes; the next 64 columns follow a chunk later
                             const uint64_t db = operand(src + 4 * kChunk + k * 2048, 1024, kChunk);
-                            mma_f16(d, operand(src + k * 2048, 1024, kChunk), db, idesc, sub + k > 0);
-                            mma_f16(d, operand(src + 2 * kChunk + k * 2048, 1024, kChunk), db, idesc, true);
+                            mma_f16_pair(d, operand(src + k * 2048, 1024, kChunk), db, idesc, sub + k > 0);
+                            mma_f16_pair(d, operand(src + 2 * kChunk + k * 2048, 1024, kChunk), db, idesc, true);
                         }
-                        commit(bar_empty + 8 * turn.slot);
+                        commit_both<2>(bar_empty + 8 * turn.slot);
                     }
-                    if (ok) commit(bar_acc + 8 * acc.slot);
+                    if (ok) commit_both<2>(bar_acc + 8 * acc.slot);
                 }
             }
             // every product issued ends, and its sums are read, before the tensor memory is freed
@@ -247,7 +247,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
     __syncwarp();
     cluster_sync();  // no CTA leaves while the other may still write to it
     fence_after();
-    if (warp == 2) tmem_free<512>(tmem);
+    if (warp == 2) tmem_free<2, 512>(tmem);
 }
 
 // [rows, pitch] FP16 as {64, rows, pitch / 64}, fetched 128 columns at a time
@@ -283,7 +283,7 @@ int launch(const Dims& d, const Plan& p, const Peaks* peaks, const __half* hi, c
     a.n_tiles = (int32_t)ceil_div(d.H, kCols);
     a.experts = (int32_t)d.E;
     const int64_t total = (int64_t)((a.m_tiles + 1) / 2) * a.n_tiles * d.E;
-    return launch_pairs<wgrad_kernel<kTransposed>>(kThreads, kSmem, total, s, mh, ml, mb, mo, a);
+    return launch_clusters<wgrad_kernel<kTransposed>>(kThreads, kSmem, 2, total, s, mh, ml, mb, mo, a);
 }
 
 }  // namespace

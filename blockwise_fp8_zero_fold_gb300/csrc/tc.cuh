@@ -158,18 +158,38 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// Tiles to this CTA's shared memory, counted on a barrier of either CTA of the
-// pair (`bar` is a cluster address, of first_of_pair).
+// Tiles to this CTA's shared memory.
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-            dst),
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
         "l"(map), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
 
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// The same to both CTAs of a cluster, at this CTA's offsets of the destination
+// and the barrier.
+__device__ __forceinline__ void load_2d_both(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(
+            dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "h"((uint16_t)3)
+        : "memory");
+}
+
+// To this CTA's shared memory, counted on a barrier of either CTA of a pair
+// (`bar` is a cluster address, of first_of_pair).
+__device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z)
 {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
@@ -203,41 +223,62 @@ __device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.w
 // this thread's shared memory writes, before a TMA copy reads them
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// ---- tcgen05, by pairs of CTAs ---------------------------------------------------
+// ---- tcgen05 -----------------------------------------------------------------------
 //
-// A pair multiplies 256 rows by up to 256 columns: each CTA holds 128 rows of
-// the first operand, half the columns of the second and the sums of its rows.
-// The first CTA's thread issues for both.
+// kGroup 1: a CTA multiplies 128 rows by up to 256 columns by itself.  kGroup 2:
+// a pair of CTAs 256 rows by up to 256 columns; each holds 128 rows of the first
+// operand, half the columns of the second and the sums of its rows, and the
+// first CTA's thread issues for both.
 
-// By one warp of each CTA.
-template <int kCols>
+// By one warp of the CTA (of each CTA).
+template <int kGroup, int kCols>
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_out)
 {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_out), "n"(kCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    if constexpr (kGroup == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_out), "n"(kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_out), "n"(kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
 }
-template <int kCols>
+template <int kGroup, int kCols>
 __device__ __forceinline__ void tmem_free(uint32_t taddr)
 {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols) : "memory");
+    if constexpr (kGroup == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols) : "memory");
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Arrives on the barriers at this offset of both CTAs once every product this
-// thread issued has finished.
+// Arrives on `bar` once every product this thread issued has finished.
 __device__ __forceinline__ void commit(uint32_t bar)
 {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// The same on the barriers at this offset of both CTAs of the cluster.
+template <int kGroup>
+__device__ __forceinline__ void commit_both(uint32_t bar)
+{
+    if constexpr (kGroup == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
 }
 
-// Shared memory operand (at the same offset in both CTAs), 128-byte swizzle
-// (atoms of 8 rows x 128 bytes).
+// Shared memory operand (of a pair: at the same offset in both CTAs), 128-byte
+// swizzle (atoms of 8 rows x 128 bytes).
 //   K-major (a row is 128 bytes of k): group_stride = bytes between groups of
 //     8 rows of the M or N index; chunk_stride unused.
 //   M/N-major (a row is 128 bytes of the M or N index): group_stride = bytes
@@ -248,24 +289,25 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t group_stride
            (uint64_t)(group_stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// Instruction descriptor of 256 rows x `n` columns: FP32 sums, operand formats
-// E4M3 (f8f6f4) or F16 (f16), both encoded 0, the first operand E5M2 instead
-// with `a_e5m2`; `mn_major` bits say which operands are M/N-major.
-__host__ __device__ constexpr uint32_t instruction(int n, bool a_mn_major, bool b_mn_major, bool a_e5m2 = false)
+// Instruction descriptor of m rows x n columns: FP32 sums, operand formats E4M3
+// (f8f6f4) or F16 (f16), both encoded 0, the first operand E5M2 instead with
+// `a_e5m2`; `mn_major` bits say which operands are M/N-major.
+__host__ __device__ constexpr uint32_t instruction(int m, int n, bool a_mn_major, bool b_mn_major, bool a_e5m2 = false)
 {
     return 1u << 4 | (a_e5m2 ? 1u << 7 : 0u) | (a_mn_major ? 1u << 15 : 0u) | (b_mn_major ? 1u << 16 : 0u) |
-           (uint32_t)(n >> 3) << 17 | (256u >> 4) << 24;
+           (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
 
+// By one CTA.
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
-
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+// By a pair.
+__device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
         "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
