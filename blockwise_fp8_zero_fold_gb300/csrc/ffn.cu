@@ -2,7 +2,8 @@
 // token rows into tiles, and the elementwise kernels between the products
 // (ffn_gemm.cu: products with FP8 weights; ffn_wgrad.cu: weight gradients).
 //
-// Forward:  plan, split x, gate_up (+ silu, product, encode), down.
+// Forward:  plan, split x, gate_up (+ silu, product, encode), down; with few
+//           tokens y comes from matrix-vector products (ffn_gemv.cu).
 // Backward: plan, split dy, dh, the activation's backward with its encodings,
 //           FP16 copies of x and dy, dx, d_gate_up, d_down.
 #include <mutex>
@@ -50,17 +51,6 @@ namespace {
 
 using namespace fp8z1;
 using namespace fp8z1::ffn;
-
-struct Runs {
-    const int32_t* offsets;  // NULL: one expert with every row
-    int64_t tokens, experts;
-    // rows [lo, hi) of expert e, inside [0, tokens] whatever the table holds
-    __device__ __forceinline__ void get(int64_t e, int64_t& lo, int64_t& hi) const
-    {
-        lo = offsets ? min(max((int64_t)offsets[e], (int64_t)0), tokens) : 0;
-        hi = offsets ? min(max((int64_t)offsets[e + 1], lo), tokens) : tokens;
-    }
-};
 
 // The tiles of every expert.  Rows two experts claim (a table that does not
 // ascend) are bounded too: the launch holds at most `most` tiles.
@@ -345,6 +335,10 @@ extern "C" int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int6
     Cut cw(workspace), cs(saved);
     Forward f;
     f.cut(cw, d);
+    if (few_tokens(d)) {  // y is the same whether the call saves or not
+        st = launch_gemv(d, runs, static_cast<const bf16*>(x), ld_x, wgu, wd, f.part, static_cast<bf16*>(y), ld_y, s);
+        if (st != FP8Z1_OK || !saved) return st;
+    }
     Saved keep = {};
     if (saved) keep.cut(cs, d);
     const Plan plan = f.plan.plan();
@@ -357,7 +351,8 @@ extern "C" int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int6
     if ((st = launch_status()) != FP8Z1_OK ||
         (st = launch_gate_up(d, plan, f.x, wgu, f.h, keep.gu, keep.peaks, s)) != FP8Z1_OK)
         return st;
-    return launch_down(d, plan, f.h, wd, static_cast<bf16*>(y), ld_y, s);
+    if (few_tokens(d)) return FP8Z1_OK;
+    return launch_down(d, plan, f.h, wd, static_cast<bf16*>(y), ld_y, f.part, s);
 }
 
 extern "C" int fp8z1_ffn_backward(const fp8z1_ffn_dims* dims, const void* dy, int64_t ld_dy, const void* x,

@@ -43,6 +43,17 @@ struct Pairs {
     int64_t pitch;
 };
 
+struct Runs {
+    const int32_t* offsets;  // NULL: one expert with every row
+    int64_t tokens, experts;
+    // rows [lo, hi) of expert e, inside [0, tokens] whatever the table holds
+    __device__ __forceinline__ void get(int64_t e, int64_t& lo, int64_t& hi) const
+    {
+        lo = offsets ? min(max((int64_t)offsets[e], (int64_t)0), tokens) : 0;
+        hi = offsets ? min(max((int64_t)offsets[e + 1], lo), tokens) : tokens;
+    }
+};
+
 struct Dims {
     int64_t T, H, F, E;
     int64_t tiles() const { return T / kRows + (E < T ? E : T); }  // at most
@@ -99,12 +110,28 @@ struct Saved {
     }
 };
 
+// Whether the forward pass is matrix-vector products; see ffn_gemv.cu.
+bool few_tokens(const Dims& d);
+
+// CTAs along K of the down product: its column tiles are few (16 for 4096
+// columns), and with one row tile or two they would leave most SMs without work.
+inline int32_t down_splits(const Dims& d)
+{
+    if (d.T == 0) return 1;
+    const int64_t tiles = d.tiles() * ceil_div(d.H, 256), blocks = d.F / kBlock;
+    int64_t n = 128 / tiles;
+    if (n > blocks / 4) n = blocks / 4;
+    return (int32_t)(n < 1 ? 1 : n > 16 ? 16 : n);
+}
+
 struct Forward {
     PlanBuffers plan;
+    float* part;  // [splits, rows, H] when the down product is split; [T, F], few tokens
     Pairs x, h;
     void cut(Cut& c, const Dims& d)
     {
         plan.cut(c, d);
+        part = c.take<float>(few_tokens(d) ? d.T * d.F : down_splits(d) > 1 ? down_splits(d) * d.rows() * d.H : 0);
         x = cut_pairs(c, d.rows(), d.Hp());
         h = cut_pairs(c, d.rows(), d.F);
     }
@@ -205,9 +232,13 @@ __device__ __forceinline__ int h_shift(const Peaks& p) { return 13 - exponent(p.
 // The FP8 products of one K-blocked shape; see ffn_gemm.cu.
 int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w, const Pairs& h, float* gu,
                    Peaks* peaks, cudaStream_t s);
-int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, cudaStream_t s);
+int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, float* part,
+                cudaStream_t s);
 int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, float* dh, Peaks* peaks, cudaStream_t s);
 int launch_dx(const Dims& d, const Plan& p, const Pairs& dgu, const Weight& w, bf16* dx, int64_t ld, cudaStream_t s);
+// y of a few tokens (h: FP32 [T, F]); see ffn_gemv.cu.
+int launch_gemv(const Dims& d, const Runs& runs, const bf16* x, int64_t ld_x, const Weight& wgu, const Weight& wd, float* h,
+                bf16* y, int64_t ld_y, cudaStream_t s);
 // The weight gradients; see ffn_wgrad.cu.
 int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
 int launch_d_down(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);

@@ -36,7 +36,9 @@ using namespace tc;
 
 __device__ unsigned g_timeouts;
 
-enum Mode { kGateUp, kDown, kDh, kDx };
+// kPart: down with K split over several CTAs, FP32 partial sums
+enum Mode { kGateUp, kDown, kDh, kDx, kPart };
+__host__ __device__ constexpr bool n_major(int mode) { return mode == kGateUp || mode == kDown || mode == kPart; }
 
 constexpr int kCols = 256;   // columns of a tile, in two chunks of 128
 constexpr int kStages = 3;
@@ -54,6 +56,7 @@ struct Args {
     int64_t N;             // columns of the result (kGateUp: F pairs)
     int32_t n_groups;      // groups of column tiles
     int32_t cluster;       // CTAs of a cluster: 1 or 2
+    int32_t splits;        // kPart: CTAs (clusters) along K, else 1
     int32_t k_blocks;
     int32_t sr, sc;        // the scale grid of an expert
     int32_t b_step;        // from one K block's scale to the next
@@ -63,24 +66,29 @@ struct Args {
     Peaks* peaks;          // kGateUp (NULL: not kept), kDh
     bf16* out;             // kDown, kDx
     int64_t ld;
+    float* part;           // kPart, [splits, rows, N]
 };
 
 struct Work {
     int32_t tile, expert, token0, rows, n;
+    int32_t split, k0, k1;  // K blocks
 };
 
 // The i-th group of column tiles (one, or a cluster's two) of the launch, expert
 // by expert, column by column, and the tile of CTA `rank`.
 __device__ __forceinline__ Work work_at(const Args& a, int64_t i, int rank)
 {
-    const int32_t t = (int32_t)(i / a.n_groups);
+    const int32_t per = a.n_groups * a.splits, t = (int32_t)(i / per);
     const int32_t e = a.plan.tiles[t].expert;
     const int32_t first = a.plan.start[e], count = a.plan.start[e + 1] - first;
-    const int64_t local = i - (int64_t)first * a.n_groups;
+    const int64_t local = i - (int64_t)first * per;
     Work w;
-    const int32_t group = (int32_t)(local / count);
+    const int32_t column = (int32_t)(local / count), group = column / a.splits;
+    w.split = column - group * a.splits;
+    w.k0 = (int32_t)((int64_t)a.k_blocks * w.split / a.splits);
+    w.k1 = (int32_t)((int64_t)a.k_blocks * (w.split + 1) / a.splits);
     w.n = group * a.cluster + rank;
-    w.tile = first + (int32_t)(local - (int64_t)group * count);
+    w.tile = first + (int32_t)(local - (int64_t)column * count);
     const Tile tile = a.plan.tiles[w.tile];
     w.expert = e;
     w.token0 = tile.token0;
@@ -101,7 +109,7 @@ __device__ __forceinline__ const float* b_scale(const Args& a, const Work& w, in
 {
     const int n = chunk_column<kMode>(a, w, c) >> 7;
     const float* s = a.b_scale + (int64_t)w.expert * a.sr * a.sc;
-    if (kMode == kGateUp || kMode == kDown) return s + min(n, a.sc - 1);
+    if (n_major(kMode)) return s + min(n, a.sc - 1);
     return s + (int64_t)min(n, a.sr - 1) * a.sc;
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -152,7 +160,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     cluster_sync();  // the other CTA may write to this one's stages and barriers from here on
     fence_after();
     const uint32_t tmem = *tmem_at;
-    const int64_t total = (int64_t)*a.plan.n_tiles * a.n_groups;
+    const int64_t total = (int64_t)*a.plan.n_tiles * a.n_groups * a.splits;
     const int64_t i0 = blockIdx.x / a.cluster, step = gridDim.x / a.cluster;
     bool ok = true;
 
@@ -164,7 +172,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             for (int64_t i = i0; i < total && ok; i += step) {
                 const Work w = work_at(a, i, rank);
                 const int c0 = chunk_column<kMode>(a, w, 0), c1 = chunk_column<kMode>(a, w, 1), y = w.tile * kRows;
-                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next()) {
+                for (int kb = w.k0; kb < w.k1; ++kb, turn.next()) {
                     if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
                         ok = false;
                         break;
@@ -179,7 +187,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     } else {
                         load_2d_both(dst + kOperand, &map_lo, full, kb * 128, y);
                     }
-                    if (kMode == kGateUp || kMode == kDown) {
+                    if (n_major(kMode)) {
                         load_3d(dst + 2 * kOperand, &map_w, full, c0, kb * 128, w.expert);
                         load_3d(dst + 3 * kOperand, &map_w, full, c1, kb * 128, w.expert);
                     } else {
@@ -191,13 +199,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             // the copies in flight are read before the CTA ends, whatever became of the other warps
             for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
         } else if (warp == 1 && lane == 0) {
-            constexpr bool kMnMajor = kMode == kGateUp || kMode == kDown;
+            constexpr bool kMnMajor = n_major(kMode);
             constexpr uint32_t idesc[2] = {instruction(128, kCols, false, kMnMajor),
                                            instruction(128, kCols, false, kMnMajor, true)};
             Turn<kStages> turn;
             Turn<2> acc;
-            for (int64_t i = i0; i < total && ok; i += step)
-                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next(), acc.next()) {
+            for (int64_t i = i0; i < total && ok; i += step) {
+                const Work w = work_at(a, i, rank);
+                for (int kb = w.k0; kb < w.k1; ++kb, turn.next(), acc.next()) {
                     if (!bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) ||
                         !bar_wait(bar_full + 8 * turn.slot, turn.phase)) {
                         ok = false;
@@ -222,6 +231,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                         commit_both<1>(bar_empty + 8 * turn.slot);
                     commit(bar_acc + 8 * acc.slot);
                 }
+            }
             // every product issued ends, and its sums are read, before the tensor memory is freed
             for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
         } else if (warp >= 2) {
@@ -232,7 +242,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 const Work w = work_at(a, i, rank);
                 const float* pa = a.a_scale + (int64_t)w.tile * kRows + mine;
                 const float *p0 = b_scale<kMode>(a, w, 0), *p1 = b_scale<kMode>(a, w, 1);
-                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next()) {
+                for (int kb = w.k0; kb < w.k1; ++kb, turn.next()) {
                     const float va = pa[(int64_t)kb * a.rows], vb = pa[(int64_t)kb * a.rows + 64], v0 = p0[kb * a.b_step],
                                 v1 = p1[kb * a.b_step];
                     if (!bar_wait(bar_read + 8 * turn.slot, turn.phase ^ 1)) {
@@ -263,7 +273,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) sums2[c][j] = 0;
-            for (int kb = 0; kb < a.k_blocks; ++kb, acc.next(), turn.next()) {
+            for (int kb = w.k0; kb < w.k1; ++kb, acc.next(), turn.next()) {
                 // a warp's lanes agree on the outcome: the loads below are warp-wide
                 ok = __all_sync(0xffffffffu, bar_wait(bar_factors + 8 * turn.slot, turn.phase) &&
                                                  bar_wait(bar_acc + 8 * acc.slot, acc.phase));
@@ -360,6 +370,19 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     hi[q] = make_uint4(vh[0], vh[1], vh[2], vh[3]);
                     lo[q] = make_uint4(vl[0], vl[1], vl[2], vl[3]);
                 }
+            } else if constexpr (kMode == kPart) {
+                if (row < w.rows)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int64_t n0 = (int64_t)w.n * kCols + c * 128 + group * 32;
+                        float* o = a.part + ((int64_t)w.split * a.rows + at) * a.N + n0;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            if (n0 + q * 4 >= a.N) break;
+                            *reinterpret_cast<float4*>(o + q * 4) =
+                                make_float4(sum[c][q * 4], sum[c][q * 4 + 1], sum[c][q * 4 + 2], sum[c][q * 4 + 3]);
+                        }
+                    }
             } else if constexpr (kMode == kDh) {
                 float top = 0.0f;
 #pragma unroll
@@ -407,6 +430,26 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     if (warp == 2) tmem_free<1, 512>(tmem);
 }
 
+// y of the partial sums, in the order of the splits.
+__global__ void __launch_bounds__(256) join_kernel(Plan plan, const float* part, int64_t rows, int64_t N, int splits,
+                                                   bf16* out, int64_t ld)
+{
+    if (blockIdx.x / kRows >= *plan.n_tiles) return;
+    const Tile t = plan.tiles[blockIdx.x / kRows];
+    const int r = blockIdx.x % kRows;
+    const int64_t n = (int64_t)(blockIdx.y * 256 + threadIdx.x) * 4;
+    if (r >= t.rows || n >= N) return;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(part + ((int64_t)k * rows + blockIdx.x) * N + n);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(out + (int64_t)(t.token0 + r) * ld + n);
+    o[0] = __floats2bfloat162_rn(s.x, s.y);
+    o[1] = __floats2bfloat162_rn(s.z, s.w);
+}
+
 template <int kMode>
 int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a, cudaStream_t s)
 {
@@ -428,11 +471,12 @@ int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a,
     const int64_t n_tiles = kMode == kGateUp ? d.F / 128 : ceil_div(a.N, kCols);
     a.cluster = n_tiles % 2 == 0 || n_tiles > 8 ? 2 : 1;  // an odd tile's neighbour multiplies for nothing
     a.n_groups = (int32_t)ceil_div(n_tiles, a.cluster);
+    if (kMode != kPart) a.splits = 1;
     a.k_blocks = (int32_t)ceil_div(K, kBlock);
     a.sr = (int32_t)ceil_div(w.R, 128);
     a.sc = (int32_t)ceil_div(w.C, 128);
-    a.b_step = kMode == kGateUp || kMode == kDown ? a.sc : 1;
-    return launch_clusters<gemm_kernel<kMode>>(kThreads, kSmem, a.cluster, d.tiles() * a.n_groups, s, hi, lo, wm, a);
+    a.b_step = n_major(kMode) ? a.sc : 1;
+    return launch_clusters<gemm_kernel<kMode>>(kThreads, kSmem, a.cluster, d.tiles() * a.n_groups * a.splits, s, hi, lo, wm, a);
 }
 
 }  // namespace
@@ -449,14 +493,23 @@ int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w
     return launch<kGateUp>(d, x, d.H, w, a, s);
 }
 
-int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, cudaStream_t s)
+int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, float* part,
+                cudaStream_t s)
 {
     Args a = {};
     a.plan = p;
     a.N = d.H;
     a.out = y;
     a.ld = ld;
-    return launch<kDown>(d, h, d.F, w, a, s);
+    a.splits = down_splits(d);
+    if (a.splits == 1) return launch<kDown>(d, h, d.F, w, a, s);
+    a.part = part;
+    const int st = launch<kPart>(d, h, d.F, w, a, s);
+    if (st != FP8Z1_OK) return st;
+    count_launch();
+    join_kernel<<<dim3((unsigned)d.rows(), (unsigned)ceil_div(d.H, 1024)), 256, 0, s>>>(p, part, d.rows(), d.H, a.splits,
+                                                                                       y, ld);
+    return launch_status();
 }
 
 int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, float* dh, Peaks* peaks, cudaStream_t s)

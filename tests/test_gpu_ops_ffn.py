@@ -95,6 +95,21 @@ def test_few_tokens(tokens, experts):
         assert torch.equal(ops.ffn_forward(x, *w), y)
 
 
+@pytest.mark.parametrize("counts,hidden,inner", [
+    ([0, 2, 0, 1], 528, 256), ([0] * 900 + [3, 0, 1], 64, 128), ([0] * 31 + [1], 144, 128), ([9, 0, 0, 5, 1] + [0] * 15 + [2] * 12, 528, 256),
+    ([1] * 64, 64, 128), ([4], 7168, 2048), ([3], 16, 128), ([2], 2064, 1152), ([100], 528, 2048), ([60, 0, 3], 2064, 4096),
+])
+def test_few_tokens_spread_unevenly(counts, hidden, inner):
+    """A few tokens on some of many experts, with rows of no expert; products split along inner."""
+    x, dy, w, off = make(counts, hidden, inner, 5, rest=1 if len(counts) > 1 else 0)
+    n = sum(counts)
+    y = ops.ffn_forward(x, *w, offsets=off)
+    assert not y[n:].any()
+    check(x[:n], dy[:n], w, off, (y[:n], None, None, None))
+    assert torch.equal(y, ops.ffn_forward(x, *w, offsets=off))
+    assert torch.equal(y, ops.ffn_forward(x, *w, offsets=off, save=True)[0]), "y depends on save"
+
+
 def test_full_widths_of_the_expert_workload():
     """hidden 7168, inner 2048: three experts of the MoE configuration's widths."""
     x, dy, w, off = make([150, 0, 75], 7168, 2048, 4)
