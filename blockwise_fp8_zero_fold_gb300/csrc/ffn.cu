@@ -107,9 +107,10 @@ __device__ __forceinline__ float2 bf16_pair(uint32_t two)
     return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
 }
 
-// Rows of BF16 activations to FP8 pairs in the tiles' order (a warp a row,
-// 16 lanes a block of 128), with each expert's peak; rows of no expert are
-// zeroed in `rest`.
+// Rows of BF16 activations to FP8 pairs in the tiles' order (a warp kRowColumns
+// of a row: with one row of 7168, a warp for all of it took 21 us; 16 lanes a block
+// of 128), with each expert's peak; rows of no expert are zeroed in `rest`.
+constexpr int kRowColumns = 1024;
 __global__ void __launch_bounds__(256) split_kernel(Runs runs, Plan plan, const bf16* x, int64_t ld, int64_t H,
                                                     Pairs out, int64_t rows, Peaks* peaks, bool dy, bf16* rest,
                                                     int64_t ld_rest)
@@ -117,11 +118,12 @@ __global__ void __launch_bounds__(256) split_kernel(Runs runs, Plan plan, const 
     const int lane = threadIdx.x & 31;
     const int64_t warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int64_t n_rows = (int64_t)*plan.n_tiles * kRows;
+    const int64_t c0 = (int64_t)blockIdx.y * kRowColumns, c1 = min(c0 + kRowColumns, out.pitch);
     if (rest) {
         int64_t lo, hi;
         runs.get(runs.experts - 1, lo, hi);
         for (int64_t r = hi + warp; r < runs.tokens; r += (int64_t)gridDim.x * 8)
-            for (int64_t c = lane * 8; c < H; c += 256)
+            for (int64_t c = c0 + lane * 8; c < min(c1, H); c += 256)
                 *reinterpret_cast<uint4*>(rest + r * ld_rest + c) = make_uint4(0, 0, 0, 0);
     }
     if (warp >= n_rows) return;
@@ -130,7 +132,8 @@ __global__ void __launch_bounds__(256) split_kernel(Runs runs, Plan plan, const 
     if (r >= t.rows) return;
     const bf16* src = x + (int64_t)(t.token0 + r) * ld;
     float top = 0.0f;
-    for (int64_t c = lane * 8; c < out.pitch; c += 256) {
+#pragma unroll
+    for (int64_t c = c0 + lane * 8; c < c1; c += 256) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (c < H) v = __ldg(reinterpret_cast<const uint4*>(src + c));
         const float2 f[4] = {bf16_pair(v.x), bf16_pair(v.y), bf16_pair(v.z), bf16_pair(v.w)};
@@ -176,7 +179,9 @@ __global__ void __launch_bounds__(256) halves_kernel(Plan plan, const bf16* x, i
     const Pow2 fx = pow2(x_shift(p)), fd = pow2(dy_shift(p));
     const bf16* sx = x + (int64_t)(t.token0 + r) * ld_x;
     const bf16* sd = dy + (int64_t)(t.token0 + r) * ld_dy;
-    for (int64_t c = lane * 8; c < pitch; c += 256) {
+    const int64_t c0 = (int64_t)blockIdx.y * kRowColumns, c1 = min(c0 + kRowColumns, pitch);
+#pragma unroll
+    for (int64_t c = c0 + lane * 8; c < c1; c += 256) {
         uint4 vx = make_uint4(0, 0, 0, 0), vd = vx;
         if (r < t.rows && c < H) {
             vx = __ldg(reinterpret_cast<const uint4*>(sx + c));
@@ -236,9 +241,11 @@ __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float*
             u = __ldcs(pu + c * kRows);
             d = __ldcs(pd + c * kRows);
         }
-        const float s = 1.0f / (1.0f + expf(-g)), a = g * s;
+        // the sigmoid and its complement, by exp(-|g|) <= 1: neither overflows nor cancels
+        const float e = expf(-fabsf(g)), big = __fdividef(1.0f, 1.0f + e), small = e * big;
+        const float s = g < 0.0f ? small : big, rest = g < 0.0f ? big : small, a = g * s;
         float* o = act + lane * kActPitch + c;
-        o[0] = d * u * s * (1.0f + g * (1.0f - s));
+        o[0] = d * u * s * (1.0f + g * rest);
         o[32 * kActPitch] = d * a;
         o[64 * kActPitch] = a * u;
     }
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float*
 int check_dims(const fp8z1_ffn_dims* d)
 {
     if (!d || d->tokens < 0 || d->tokens > kMaxRows || d->hidden < 16 || d->hidden % 16 ||
-        d->hidden >= (int64_t)1 << 24 || d->inner < 128 || d->inner % 128 || d->inner >= (int64_t)1 << 24 ||
+        d->hidden >= (int64_t)1 << 24 || d->inner < 128 || d->inner % 128 || d->inner >= (int64_t)1 << 23 ||
         d->experts < 1 || d->experts > 1024)
         return FP8Z1_EINVAL;
     return FP8Z1_OK;
@@ -342,14 +349,14 @@ extern "C" int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int6
     Saved keep = {};
     if (saved) keep.cut(cs, d);
     const Plan plan = f.plan.plan();
-    const unsigned row_ctas = (unsigned)ceil_div(d.rows(), 8);
+    const dim3 row_ctas((unsigned)ceil_div(d.rows(), 8), (unsigned)ceil_div(d.Hp(), kRowColumns));
     count_launch();
     plan_kernel<<<1, 1024, 0, s>>>(runs, f.plan, d.tiles(), keep.peaks, nullptr);
     count_launch();
     split_kernel<<<row_ctas, 256, 0, s>>>(runs, plan, static_cast<const bf16*>(x), ld_x, d.H, f.x, d.rows(), keep.peaks,
                                           false, static_cast<bf16*>(y), ld_y);
     if ((st = launch_status()) != FP8Z1_OK ||
-        (st = launch_gate_up(d, plan, f.x, wgu, f.h, keep.gu, keep.peaks, s)) != FP8Z1_OK)
+        (st = launch_gate_up(d, plan, f.x, wgu, f.h, keep.gu, keep.peaks, f.part, s)) != FP8Z1_OK)
         return st;
     if (few_tokens(d)) return FP8Z1_OK;
     return launch_down(d, plan, f.h, wd, static_cast<bf16*>(y), ld_y, f.part, s);
@@ -389,7 +396,7 @@ extern "C" int fp8z1_ffn_backward(const fp8z1_ffn_dims* dims, const void* dy, in
     keep.cut(cs, d);
     const Plan plan = b.plan.plan();
     const bf16 *xb = static_cast<const bf16*>(x), *dyb = static_cast<const bf16*>(dy);
-    const unsigned row_ctas = (unsigned)ceil_div(d.rows(), 8);
+    const dim3 row_ctas((unsigned)ceil_div(d.rows(), 8), (unsigned)ceil_div(d.Hp(), kRowColumns));
     count_launch();
     plan_kernel<<<1, 1024, 0, s>>>(runs, b.plan, d.tiles(), b.peaks, keep.peaks);
     count_launch();

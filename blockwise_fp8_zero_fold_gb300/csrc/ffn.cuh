@@ -7,6 +7,7 @@
 // weight gradients they are zeros.
 #pragma once
 
+#include <algorithm>
 #include <cuda_fp16.h>
 
 #include "ops_common.cuh"
@@ -113,25 +114,32 @@ struct Saved {
 // Whether the forward pass is matrix-vector products; see ffn_gemv.cu.
 bool few_tokens(const Dims& d);
 
-// CTAs along K of the down product: its column tiles are few (16 for 4096
-// columns), and with one row tile or two they would leave most SMs without work.
-inline int32_t down_splits(const Dims& d)
+// CTAs along K of a forward product with N columns (gate_up: 2F) and K rows.  With
+// few tiles of 128 x 256 most SMs would have no work, and one CTA takes 0.8 us for
+// 128 rows of codes from memory: parts of at least 512 rows, for about 128 CTAs.
+// (6 tokens of 7168 x 2048: gate_up 59 us whole.)
+inline int32_t k_splits(const Dims& d, int64_t N, int64_t K)
 {
     if (d.T == 0) return 1;
-    const int64_t tiles = d.tiles() * ceil_div(d.H, 256), blocks = d.F / kBlock;
-    int64_t n = 128 / tiles;
-    if (n > blocks / 4) n = blocks / 4;
+    int64_t n = 128 / (d.tiles() * ceil_div(N, 256));
+    if (n > K / (4 * kBlock)) n = K / (4 * kBlock);
     return (int32_t)(n < 1 ? 1 : n > 16 ? 16 : n);
+}
+inline int64_t part_floats(const Dims& d, int64_t N, int64_t K)
+{
+    const int64_t n = k_splits(d, N, K);
+    return n > 1 ? n * d.rows() * N : 0;
 }
 
 struct Forward {
     PlanBuffers plan;
-    float* part;  // [splits, rows, H] when the down product is split; [T, F], few tokens
+    float* part;  // a split product's sums, [splits, rows, N]; few tokens: h, [T, F]
     Pairs x, h;
     void cut(Cut& c, const Dims& d)
     {
         plan.cut(c, d);
-        part = c.take<float>(few_tokens(d) ? d.T * d.F : down_splits(d) > 1 ? down_splits(d) * d.rows() * d.H : 0);
+        part = c.take<float>(
+            std::max<int64_t>({few_tokens(d) ? d.T * d.F : 0, part_floats(d, 2 * d.F, d.H), part_floats(d, d.H, d.F)}));
         x = cut_pairs(c, d.rows(), d.Hp());
         h = cut_pairs(c, d.rows(), d.F);
     }
@@ -231,7 +239,7 @@ __device__ __forceinline__ int h_shift(const Peaks& p) { return 13 - exponent(p.
 
 // The FP8 products of one K-blocked shape; see ffn_gemm.cu.
 int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w, const Pairs& h, float* gu,
-                   Peaks* peaks, cudaStream_t s);
+                   Peaks* peaks, float* part, cudaStream_t s);
 int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, float* part,
                 cudaStream_t s);
 int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, float* dh, Peaks* peaks, cudaStream_t s);

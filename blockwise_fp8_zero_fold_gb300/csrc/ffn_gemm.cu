@@ -36,7 +36,7 @@ using namespace tc;
 
 __device__ unsigned g_timeouts;
 
-// kPart: down with K split over several CTAs, FP32 partial sums
+// kPart: gate_up or down with K split over several CTAs, FP32 partial sums
 enum Mode { kGateUp, kDown, kDh, kDx, kPart };
 __host__ __device__ constexpr bool n_major(int mode) { return mode == kGateUp || mode == kDown || mode == kPart; }
 
@@ -111,6 +111,13 @@ __device__ __forceinline__ const float* b_scale(const Args& a, const Work& w, in
     const float* s = a.b_scale + (int64_t)w.expert * a.sr * a.sc;
     if (n_major(kMode)) return s + min(n, a.sc - 1);
     return s + (int64_t)min(n, a.sr - 1) * a.sc;
+}
+// g / (1 + exp(-g)) by t = exp(-|g|) <= 1: nothing overflows, and no branch (the
+// branch's code, 32 times a row, cost a small product 10 us of instruction fetches)
+__device__ __forceinline__ float silu(float g)
+{
+    const float t = __expf(-fabsf(g));
+    return g * __fdividef(g < 0.0f ? t : 1.0f, 1.0f + t);
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
@@ -338,9 +345,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 }
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    const float g = sum[0][j];
-                    sum[0][j] = __fdividef(g, 1.0f + __expf(-g)) * sum[1][j];
-                    if (g < -80.0f) sum[0][j] = g * expf(g) * sum[1][j];  // 1 + exp(-g) past the quick quotient
+                    sum[0][j] = silu(sum[0][j]) * sum[1][j];
                     amax = fmaxf(amax, fabsf(sum[0][j]));
                 }
                 // the largest of the row's 128 columns, 32 each of the four groups
@@ -450,6 +455,55 @@ __global__ void __launch_bounds__(256) join_kernel(Plan plan, const float* part,
     o[1] = __floats2bfloat162_rn(s.z, s.w);
 }
 
+// h of the partial sums of gate and up, as pairs (a warp 128 columns of a row), and
+// what the gate_up product's own epilogue keeps.
+__global__ void __launch_bounds__(256) join_gate_kernel(Plan plan, const float* part, int64_t rows, int64_t F, int splits,
+                                                        Pairs h, float* gu, Peaks* peaks)
+{
+    if (blockIdx.x / kRows >= *plan.n_tiles) return;
+    const Tile t = plan.tiles[blockIdx.x / kRows];
+    const int r = blockIdx.x % kRows, lane = threadIdx.x & 31;
+    const int64_t block = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5), n = block * 128 + lane * 4;
+    if (r >= t.rows || n >= F) return;
+    float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) {
+        const float* p = part + ((int64_t)k * rows + blockIdx.x) * 2 * F + n;
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + F);
+        g.x += a.x, g.y += a.y, g.z += a.z, g.w += a.w;
+        u.x += b.x, u.y += b.y, u.z += b.z, u.w += b.w;
+    }
+    const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
+    float v[4], amax = 0.0f, top_g = 0.0f, top_u = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = silu(gs[j]) * us[j];
+        amax = fmaxf(amax, fabsf(v[j]));
+        top_g = fmaxf(top_g, fabsf(gs[j]));
+        top_u = fmaxf(top_u, fabsf(us[j]));
+        if (gu) {
+            float* o = gu + ((int64_t)(blockIdx.x / kRows) * 2 * F + n + j) * kRows + r;
+            o[0] = gs[j];
+            o[F * kRows] = us[j];
+        }
+    }
+    const PairScale ps = pair_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, abs_bits(amax))));
+    uint32_t h0, l0, h1, l1;
+    pair_encode(v[0], v[1], ps.up, h0, l0);
+    pair_encode(v[2], v[3], ps.up, h1, l1);
+    *reinterpret_cast<uint32_t*>(h.hi + (int64_t)blockIdx.x * h.pitch + n) = h0 | h1 << 16;
+    *reinterpret_cast<uint32_t*>(h.lo + (int64_t)blockIdx.x * h.pitch + n) = l0 | l1 << 16;
+    if (lane == 0) h.scale[block * rows + blockIdx.x] = ps.down;
+    if (gu) {
+        const uint32_t pg = __reduce_max_sync(0xffffffffu, abs_bits(top_g));
+        const uint32_t pu = __reduce_max_sync(0xffffffffu, abs_bits(top_u));
+        if (lane == 0) {
+            atomicMax(&peaks[t.expert].gate, pg);
+            atomicMax(&peaks[t.expert].up, pu);
+        }
+    }
+}
+
 template <int kMode>
 int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a, cudaStream_t s)
 {
@@ -482,7 +536,7 @@ int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a,
 }  // namespace
 
 int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w, const Pairs& h, float* gu,
-                   Peaks* peaks, cudaStream_t s)
+                   Peaks* peaks, float* part, cudaStream_t s)
 {
     Args a = {};
     a.plan = p;
@@ -490,7 +544,16 @@ int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w
     a.h = h;
     a.gu = gu;
     a.peaks = peaks;
-    return launch<kGateUp>(d, x, d.H, w, a, s);
+    a.splits = k_splits(d, 2 * d.F, d.H);
+    if (a.splits == 1) return launch<kGateUp>(d, x, d.H, w, a, s);
+    a.N = 2 * d.F;
+    a.part = part;
+    const int st = launch<kPart>(d, x, d.H, w, a, s);
+    if (st != FP8Z1_OK) return st;
+    count_launch();
+    join_gate_kernel<<<dim3((unsigned)d.rows(), (unsigned)ceil_div(d.F, 1024)), 256, 0, s>>>(p, part, d.rows(), d.F,
+                                                                                            a.splits, h, gu, peaks);
+    return launch_status();
 }
 
 int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, float* part,
@@ -501,7 +564,7 @@ int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, b
     a.N = d.H;
     a.out = y;
     a.ld = ld;
-    a.splits = down_splits(d);
+    a.splits = k_splits(d, d.H, d.F);
     if (a.splits == 1) return launch<kDown>(d, h, d.F, w, a, s);
     a.part = part;
     const int st = launch<kPart>(d, h, d.F, w, a, s);
