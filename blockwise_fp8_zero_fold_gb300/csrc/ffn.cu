@@ -57,6 +57,7 @@ using namespace fp8z1::ffn;
 __global__ void __launch_bounds__(1024) plan_kernel(Runs runs, PlanBuffers p, int64_t most, Peaks* clear,
                                                     const Peaks* from)
 {
+    next_may_start();
     __shared__ int32_t sums[1024];
     const int e = threadIdx.x, n = (int)runs.experts;
     int64_t lo = 0, hi = 0;
@@ -115,6 +116,8 @@ __global__ void __launch_bounds__(256) split_kernel(Runs runs, Plan plan, const 
                                                     Pairs out, int64_t rows, Peaks* peaks, bool dy, bf16* rest,
                                                     int64_t ld_rest)
 {
+    next_may_start();
+    after_previous();
     const int lane = threadIdx.x & 31;
     const int64_t warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int64_t n_rows = (int64_t)*plan.n_tiles * kRows;
@@ -169,6 +172,8 @@ __global__ void __launch_bounds__(256) halves_kernel(Plan plan, const bf16* x, i
                                                      int64_t ld_dy, int64_t H, int64_t pitch, __half* x16,
                                                      __half* dy16, const Peaks* peaks)
 {
+    next_may_start();
+    after_previous();
     const int lane = threadIdx.x & 31;
     const int64_t warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (warp >= (int64_t)*plan.n_tiles * kRows) return;
@@ -221,6 +226,8 @@ __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float*
                                                          __half* h_hi, __half* h_lo, const Peaks* peaks)
 {
     extern __shared__ float act[];  // [3][32][kActPitch]
+    next_may_start();
+    after_previous();
     const int64_t tile = blockIdx.x >> 2;
     if (tile >= *plan.n_tiles) return;
     const int quarter = blockIdx.x & 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -352,10 +359,9 @@ extern "C" int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int6
     const dim3 row_ctas((unsigned)ceil_div(d.rows(), 8), (unsigned)ceil_div(d.Hp(), kRowColumns));
     count_launch();
     plan_kernel<<<1, 1024, 0, s>>>(runs, f.plan, d.tiles(), keep.peaks, nullptr);
-    count_launch();
-    split_kernel<<<row_ctas, 256, 0, s>>>(runs, plan, static_cast<const bf16*>(x), ld_x, d.H, f.x, d.rows(), keep.peaks,
-                                          false, static_cast<bf16*>(y), ld_y);
     if ((st = launch_status()) != FP8Z1_OK ||
+        (st = launch_after(split_kernel, row_ctas, 256, 0, s, runs, plan, static_cast<const bf16*>(x), ld_x, d.H, f.x,
+                           d.rows(), keep.peaks, false, static_cast<bf16*>(y), ld_y)) != FP8Z1_OK ||
         (st = launch_gate_up(d, plan, f.x, wgu, f.h, keep.gu, keep.peaks, f.part, s)) != FP8Z1_OK)
         return st;
     if (few_tokens(d)) return FP8Z1_OK;
@@ -399,22 +405,21 @@ extern "C" int fp8z1_ffn_backward(const fp8z1_ffn_dims* dims, const void* dy, in
     const dim3 row_ctas((unsigned)ceil_div(d.rows(), 8), (unsigned)ceil_div(d.Hp(), kRowColumns));
     count_launch();
     plan_kernel<<<1, 1024, 0, s>>>(runs, b.plan, d.tiles(), b.peaks, keep.peaks);
-    count_launch();
-    split_kernel<<<row_ctas, 256, 0, s>>>(runs, plan, dyb, ld_dy, d.H, b.dy, d.rows(), b.peaks, true,
-                                          static_cast<bf16*>(dx), ld_dx);
-    if ((st = launch_status()) != FP8Z1_OK || (st = launch_dh(d, plan, b.dy, wd, b.dh, b.peaks, s)) != FP8Z1_OK)
+    if ((st = launch_status()) != FP8Z1_OK ||
+        (st = launch_after(split_kernel, row_ctas, 256, 0, s, runs, plan, dyb, ld_dy, d.H, b.dy, d.rows(), b.peaks, true,
+                           static_cast<bf16*>(dx), ld_dx)) != FP8Z1_OK ||
+        (st = launch_dh(d, plan, b.dy, wd, b.dh, b.peaks, s)) != FP8Z1_OK)
         return st;
     Pairs pairs = b.dgu;
     if (!dx) pairs.hi = nullptr;
     constexpr int kActSmem = 3 * 32 * kActPitch * 4;
     if (cudaFuncSetAttribute(activation_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kActSmem) != cudaSuccess)
         return FP8Z1_ECUDA;
-    count_launch();
-    activation_kernel<<<dim3((unsigned)(d.tiles() * 4), (unsigned)(d.F / 128)), 256, kActSmem, s>>>(
-        plan, keep.gu, b.dh, d.F, d.rows(), pairs, b.dgu_hi, b.dgu_lo, b.h_hi, b.h_lo, b.peaks);
-    count_launch();
-    halves_kernel<<<row_ctas, 256, 0, s>>>(plan, xb, ld_x, dyb, ld_dy, d.H, d.Hp(), b.x16, b.dy16, b.peaks);
-    if ((st = launch_status()) != FP8Z1_OK) return st;
+    if ((st = launch_after(activation_kernel, dim3((unsigned)(d.tiles() * 4), (unsigned)(d.F / 128)), 256, kActSmem, s, plan,
+                           keep.gu, b.dh, d.F, d.rows(), pairs, b.dgu_hi, b.dgu_lo, b.h_hi, b.h_lo, b.peaks)) != FP8Z1_OK ||
+        (st = launch_after(halves_kernel, row_ctas, 256, 0, s, plan, xb, ld_x, dyb, ld_dy, d.H, d.Hp(), b.x16, b.dy16,
+                           b.peaks)) != FP8Z1_OK)
+        return st;
     if (dx && (st = launch_dx(d, plan, b.dgu, wgu, static_cast<bf16*>(dx), ld_dx, s)) != FP8Z1_OK) return st;
     if ((st = launch_d_gate_up(d, plan, b, b.peaks, d_gate_up, s)) != FP8Z1_OK) return st;
     return launch_d_down(d, plan, b, b.peaks, d_down, s);

@@ -251,20 +251,50 @@ int launch_gemv(const Dims& d, const Runs& runs, const bf16* x, int64_t ld_x, co
 int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
 int launch_d_down(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
 
-// Launches a persistent kernel of one CTA an SM, in clusters of one or two: as
+// A pass is a chain of short kernels: each may start while the one before it ends
+// (its launch and set-up cost 2 to 3 us otherwise) and touches memory only when
+// all that one wrote is there.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches a kernel that calls both, right behind another of the pass.
+template <class... A, class... P>
+int launch_after(void (*kernel)(A...), dim3 grid, int threads, uint32_t smem, cudaStream_t s, const P&... args)
+{
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = grid;
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    count_launch();
+    if (cudaLaunchKernelEx(&c, kernel, A(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return FP8Z1_ECUDA;
+    }
+    return launch_status();
+}
+
+// Launches, right behind another kernel of the pass, a persistent one of one CTA an SM, in clusters of one or two: as
 // many as run at once, `most` at most.
 template <auto kKernel, class... P>
 int launch_clusters(int threads, uint32_t smem, int cluster, int64_t most, cudaStream_t s, const P&... args)
 {
     cudaLaunchConfig_t c = {};
-    cudaLaunchAttribute at = {};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)cluster;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     c.blockDim = dim3((unsigned)threads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
-    c.attrs = &at;
+    c.attrs = at;
     c.numAttrs = 1;
     // what the device holds at once, asked once for each kernel, device and cluster size
     static std::atomic<int> holds[16][2];
@@ -281,6 +311,7 @@ int launch_clusters(int threads, uint32_t smem, int cluster, int64_t most, cudaS
         if (dev < 16) holds[dev][cluster - 1].store(n, std::memory_order_relaxed);
     }
     c.gridDim = dim3((unsigned)((most < n ? most : n) * cluster));
+    c.numAttrs = 2;
     count_launch();
     if (cudaLaunchKernelEx(&c, kKernel, args...) != cudaSuccess) {
         cudaGetLastError();

@@ -127,6 +127,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             const __grid_constant__ CUtensorMap map_w, const __grid_constant__ Args a)
 {
     extern __shared__ uint8_t smem_raw[];
+    next_may_start();
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     const uint32_t extra = base + kStages * kStageBytes;
     // extra: full[3], empty[3], accumulators ready[2], free[2], tensor memory base, exchange, factors ready[4],
@@ -166,6 +167,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     __syncwarp();
     cluster_sync();  // the other CTA may write to this one's stages and barriers from here on
     fence_after();
+    after_previous();
     const uint32_t tmem = *tmem_at;
     const int64_t total = (int64_t)*a.plan.n_tiles * a.n_groups * a.splits;
     const int64_t i0 = blockIdx.x / a.cluster, step = gridDim.x / a.cluster;
@@ -439,6 +441,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
 __global__ void __launch_bounds__(256) join_kernel(Plan plan, const float* part, int64_t rows, int64_t N, int splits,
                                                    bf16* out, int64_t ld)
 {
+    next_may_start();
+    after_previous();
     if (blockIdx.x / kRows >= *plan.n_tiles) return;
     const Tile t = plan.tiles[blockIdx.x / kRows];
     const int r = blockIdx.x % kRows;
@@ -460,6 +464,8 @@ __global__ void __launch_bounds__(256) join_kernel(Plan plan, const float* part,
 __global__ void __launch_bounds__(256) join_gate_kernel(Plan plan, const float* part, int64_t rows, int64_t F, int splits,
                                                         Pairs h, float* gu, Peaks* peaks)
 {
+    next_may_start();
+    after_previous();
     if (blockIdx.x / kRows >= *plan.n_tiles) return;
     const Tile t = plan.tiles[blockIdx.x / kRows];
     const int r = blockIdx.x % kRows, lane = threadIdx.x & 31;
@@ -550,10 +556,8 @@ int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w
     a.part = part;
     const int st = launch<kPart>(d, x, d.H, w, a, s);
     if (st != FP8Z1_OK) return st;
-    count_launch();
-    join_gate_kernel<<<dim3((unsigned)d.rows(), (unsigned)ceil_div(d.F, 1024)), 256, 0, s>>>(p, part, d.rows(), d.F,
-                                                                                            a.splits, h, gu, peaks);
-    return launch_status();
+    return launch_after(join_gate_kernel, dim3((unsigned)d.rows(), (unsigned)ceil_div(d.F, 1024)), 256, 0, s, p, part,
+                        d.rows(), d.F, a.splits, h, gu, peaks);
 }
 
 int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, float* part,
@@ -569,10 +573,8 @@ int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, b
     a.part = part;
     const int st = launch<kPart>(d, h, d.F, w, a, s);
     if (st != FP8Z1_OK) return st;
-    count_launch();
-    join_kernel<<<dim3((unsigned)d.rows(), (unsigned)ceil_div(d.H, 1024)), 256, 0, s>>>(p, part, d.rows(), d.H, a.splits,
-                                                                                       y, ld);
-    return launch_status();
+    return launch_after(join_kernel, dim3((unsigned)d.rows(), (unsigned)ceil_div(d.H, 1024)), 256, 0, s, p, part, d.rows(),
+                        d.H, a.splits, y, ld);
 }
 
 int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, float* dh, Peaks* peaks, cudaStream_t s)

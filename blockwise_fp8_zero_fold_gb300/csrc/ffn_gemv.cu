@@ -92,9 +92,9 @@ __global__ void __launch_bounds__(kThreads, resident(kMost)) gemv_kernel(const A
     if (there && hi > lo) load_rows<kDeep>(x, w, a.C, deep, rows);
     // the down product's CTAs may start beside the last of gate_up's: its first codes are on their way when h is there
     if (kGateUp)
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        next_may_start();
     else
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        after_previous();
     if (!kGateUp && blockIdx.y == 0 && rank == 0) {  // rows of no expert
         int64_t l, h;
         a.runs.get(a.runs.experts - 1, l, h);

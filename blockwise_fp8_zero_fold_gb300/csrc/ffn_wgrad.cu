@@ -56,6 +56,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
              const __grid_constant__ Args a)
 {
     extern __shared__ uint8_t smem_raw[];
+    next_may_start();
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     const uint32_t staging = base + kStages * kStageBytes, extra = staging + 16 * 2048;
     const uint32_t bar_full = extra, bar_empty = extra + 32, bar_acc = extra + 64, bar_free = extra + 80;
@@ -84,6 +85,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
     __syncwarp();
     cluster_sync();  // the other CTA counts on this one's barriers from here on
     fence_after();
+    after_previous();
     const uint32_t tmem = *tmem_at;
     const int m_pairs = (a.m_tiles + 1) / 2;
     const int64_t per = (int64_t)m_pairs * a.n_tiles, total = per * a.experts;
