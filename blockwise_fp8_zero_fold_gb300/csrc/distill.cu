@@ -20,7 +20,6 @@
 #include <cooperative_groups.h>
 
 #include "ops_common.cuh"
-#include "tc.cuh"
 
 namespace {
 

@@ -65,52 +65,6 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
     }
 }
 
-// Arrives on CTA `rank`'s barrier at this CTA's address `bar`, for the order of
-// what this thread has read alone: writes are not released (a release to the
-// cluster would wait for every global store in flight).
-__device__ __forceinline__ void bar_arrive_at(uint32_t bar, uint32_t rank)
-{
-    asm volatile(
-        "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, %1; mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a]; }" ::"r"(
-            bar),
-        "r"(rank)
-        : "memory");
-}
-
-// Two floats to CTA `rank`'s shared memory at this CTA's address `dst` (8-byte
-// aligned), counted as 8 bytes on its barrier at `bar`.
-__device__ __forceinline__ void send_pair(uint32_t dst, uint32_t rank, float x, float y, uint32_t bar)
-{
-    const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
-    asm volatile(
-        "{ .reg .b32 a, b; mapa.shared::cluster.u32 a, %0, %1; mapa.shared::cluster.u32 b, %3, %1;\n"
-        "st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [a], %2, [b]; }" ::"r"(dst),
-        "r"(rank), "l"(v), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ bool bar_try_cluster(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(kSuspendNs)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity)
-{
-    if (bar_try_cluster(bar, parity)) return true;
-    const uint64_t t0 = now_ns();
-    for (;;) {
-        for (int i = 0; i < 64; ++i)
-            if (bar_try_cluster(bar, parity)) return true;
-        if (now_ns() - t0 > kWaitNs) return false;
-    }
-}
-
 // The cluster address of this CTA's address `a` in the pair's first CTA.
 __device__ __forceinline__ uint32_t first_of_pair(uint32_t a)
 {
@@ -118,8 +72,9 @@ __device__ __forceinline__ uint32_t first_of_pair(uint32_t a)
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
     return r;
 }
-// An arrival on a barrier at a cluster address, after this thread's tensor
-// memory loads (no write to memory is released: see bar_arrive_at).
+// An arrival on a barrier at a cluster address, after this thread's tensor memory
+// loads.  Its writes are not released (a release to the cluster would wait for
+// every global store in flight).
 __device__ __forceinline__ void bar_arrive_pair(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -196,14 +151,6 @@ __device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* ma
             dst),
         "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
-}
-
-// `bytes` (a multiple of 16) from a 16-byte aligned address
-__device__ __forceinline__ void load_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
 }
 
 __device__ __forceinline__ void store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z)

@@ -43,8 +43,8 @@ extern "C" {
  * alignment of the element types; rows that are multiples of 16 elements on
  * 16-byte boundaries are read and written 16 bytes at a time.
  * tokens == 0 enqueues nothing.
- * Errors: EINVAL (null, vocab, dim < 1, tokens < 0 or >= 2^31, id_bytes,
- * out_type, ld_out < dim, alpha not finite), EALIGN, ECUDA. */
+ * Errors: EINVAL (null, vocab < 1 or >= 2^31, dim < 1 or > 2^23, tokens < 0 or
+ * > 2^30, id_bytes, out_type, ld_out < dim, alpha not finite), EALIGN, ECUDA. */
 int fp8z1_embed(int64_t vocab, int64_t dim, const uint8_t* codes, const float* scales, const void* ids,
                 int32_t id_bytes, int64_t tokens, float alpha, void* out, int32_t out_type, int64_t ld_out,
                 void* stream);
@@ -71,8 +71,8 @@ int fp8z1_embed_grad(int64_t vocab, int64_t dim, const void* ids, int32_t id_byt
  * [inner, hidden].  experts = 1 is a dense block. */
 typedef struct {
     int64_t tokens;  /* rows of x, 0 .. 2^30 */
-    int64_t hidden;  /* a multiple of 16 */
-    int64_t inner;   /* a multiple of 128 */
+    int64_t hidden;  /* a multiple of 16, below 2^24 */
+    int64_t inner;   /* a multiple of 128, below 2^23 */
     int64_t experts; /* 1 .. 1024 */
 } fp8z1_ffn_dims;
 
@@ -89,8 +89,9 @@ int fp8z1_ffn_sizes(const fp8z1_ffn_dims* dims, int64_t* saved_bytes, int64_t* f
  * `saved`: NULL, or fp8z1_ffn_sizes' saved_bytes for fp8z1_ffn_backward
  * (256-byte aligned, as `workspace`).
  * Accumulation is FP32; h is rounded to 8 significant bits (BF16's) between
- * the two products and y once at the end.  An infinity or NaN in a row of x
- * makes that row of y NaN.
+ * the two products (up to four tokens: not rounded) and y once at the end.  An
+ * infinity or NaN in a row of x leaves that row of y without finite numbers.
+ * y does not depend on `saved`; results repeat bit for bit.
  * Errors: EINVAL, EALIGN, ECUDA. */
 int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int64_t ld_x, const int32_t* d_offsets,
                       const uint8_t* gate_up, const float* gate_up_scale, const uint8_t* down,

@@ -163,6 +163,15 @@ def test_not_finite_rows_stay_in_their_rows_and_experts():
         assert not d_gu[1].isfinite().all() and not d_dn[1].isfinite().all()
 
 
+def test_not_finite_row_of_a_few_tokens():
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        x, dy, w, off = make([2, 0, 1], 304, 256, 3)
+        clean = ops.ffn_forward(x, *w, offsets=off)
+        x[1, 17] = bad
+        y = ops.ffn_forward(x, *w, offsets=off)
+        assert torch.equal(y[[0, 2]], clean[[0, 2]]) and not y[1].isfinite().any()
+
+
 def test_uneven_magnitudes():
     """Rows, columns and weight blocks of very different size: every row keeps its own accuracy, and the
     weight gradient that of its sums."""
