@@ -3,13 +3,15 @@
 //
 //   h = silu(x Wg) * (x Wu)   (FP32),   y = h Wd   (rounded to BF16 once)
 //
-// Bound by the codes read.  A cluster of up to 8 CTAs has 128 columns of a
-// product (gate_up: 128 gate columns and the up columns beside them), each CTA a
-// part of K; a thread has 16 neighbouring columns (16 bytes of a row), four rows
-// on their way while four are multiplied, and FP32 sums of up to 4 tokens.  Scale
-// blocks are 128 x 128, so a row's 16 columns share their scale: it goes to the
-// vector's element.  Sums are added over a CTA's threads and the cluster's CTAs
-// in a fixed order.
+// Bound by the codes read, and near it by their decoding.  A cluster of up to 8
+// CTAs has 128 or 64 columns of a product (gate_up: gate columns and the up columns
+// beside them), each CTA a part of K; a thread has 16 neighbouring columns (16 bytes
+// of a row), three or four rows on their way while as many are multiplied, and FP32
+// sums of up to 4 tokens.  Scale blocks are 128 x 128, so a row's 16 columns share
+// their scale: it goes to the vector's element.  Sums are added over a CTA's threads
+// and the cluster's CTAs in a fixed order.  The second product's codes are on their
+// way before h is there.  One token of 4096 x 14336 takes 47 us, 26 at the rate of a
+// copy.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -23,10 +25,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256, kMostSplit = 8, kTokens = 4, kHold = 4;
+constexpr int kThreads = 256, kMostSplit = 8, kTokens = 4;  // kernels for 1 token and for up to 4
 constexpr int kMostSlice = 8192;  // of K, a CTA's
-// CTAs of an SM: a token has 16 sums a thread
-constexpr int resident(int tokens) { return tokens == 1 ? 3 : 2; }
+// CTAs of an SM, for which a token's 16 sums a thread leave registers, and rows on
+// their way.  (One token of 4096 x 14336: 52 us with 3 CTAs and 4 rows, 47 with 4
+// and 3, 51 with 5 and 2.)
+__host__ __device__ constexpr int resident(int tokens) { return tokens == 1 ? 4 : 2; }
+__host__ __device__ constexpr int hold(int tokens) { return tokens == 1 ? 3 : 4; }
 
 struct Args {
     Runs runs;
@@ -44,8 +49,8 @@ struct Args {
     int64_t ld_y;
 };
 
-// Four rows' codes of a thread's columns.
-template <int kStep>
+// kHold rows' codes of a thread's columns.
+template <int kStep, int kHold>
 __device__ __forceinline__ void load_rows(uint4 (&c)[kHold], const uint8_t* w, int64_t C, int k, int n)
 {
 #pragma unroll
@@ -60,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, resident(kMost)) gemv_kernel(const A
 {
     using T = std::conditional_t<kGateUp, bf16, float>;  // the vectors' type
     constexpr int kHalf = kOut / 16, kAcross = kGateUp ? 2 * kHalf : kHalf, kDeep = kThreads / kAcross;
-    constexpr int kCols = kAcross * 16, kWarps = kThreads / 32;
+    constexpr int kCols = kAcross * 16, kWarps = kThreads / 32, kHold = hold(kMost);
     extern __shared__ __align__(16) uint8_t smem[];  // scales [2][slice / 128], then vectors [kMost][slice]
     __shared__ float sums[kWarps][kMost][kCols];
     cg::cluster_group cluster = cg::this_cluster();
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, resident(kMost)) gemv_kernel(const A
     if (e < a.runs.experts) a.runs.get(e, lo, hi);
     const uint8_t* w = a.w + (e * a.K + k0) * a.C + col + (half ? a.N : 0);
     uint4 x[kHold], y[kHold];
-    if (there && hi > lo) load_rows<kDeep>(x, w, a.C, deep, rows);
+    if (there && hi > lo) load_rows<kDeep, kHold>(x, w, a.C, deep, rows);
     // the down product's CTAs may start beside the last of gate_up's: its first codes are on their way when h is there
     if (kGateUp)
         next_may_start();
@@ -157,9 +162,9 @@ __global__ void __launch_bounds__(kThreads, resident(kMost)) gemv_kernel(const A
     };
     if (there)
         for (int k = deep; k < rows; k += 2 * kHold * kDeep) {
-            load_rows<kDeep>(y, w, a.C, k + kHold * kDeep, rows);
+            load_rows<kDeep, kHold>(y, w, a.C, k + kHold * kDeep, rows);
             multiply(x, k);
-            load_rows<kDeep>(x, w, a.C, k + 2 * kHold * kDeep, rows);
+            load_rows<kDeep, kHold>(x, w, a.C, k + 2 * kHold * kDeep, rows);
             multiply(y, k + kHold * kDeep);
         }
     // over the warp's rows, the CTA's warps, the cluster's CTAs
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, resident(kMost)) gemv_kernel(const A
 }
 
 // The time of a launch by its rounds of CTAs, in rows of 64 columns; a CTA's fixed
-// steps are worth 512 rows.
+// steps are worth 1024 rows.
 struct Shape {
     double time;
     int32_t split, slice;
@@ -217,7 +222,7 @@ Shape shape(int64_t K, int64_t N, int64_t runs, int out, int resident)
     for (int n = 1; n <= kMostSplit; ++n) {
         const int64_t slice = ceil_div(ceil_div(K, n), 128) * 128;
         if (slice > kMostSlice || (n > 1 && slice < 256)) continue;
-        const double t = (double)ceil_div(groups * n, 152 * resident) * (double)((slice + 512) * out / 64);
+        const double t = (double)ceil_div(groups * n, 152 * resident) * (double)((slice + 1024) * out / 64);
         if (t < best.time) best = {t, n, (int32_t)slice};
     }
     return best;
@@ -276,8 +281,8 @@ int launch(const Args& a, cudaStream_t s)
 
 bool few_tokens(const Dims& d)
 {
-    // the slices of the vectors fit shared memory.  (61 tokens over 27 of 32 experts took 0.47 ms this way and 0.28 ms
-    // on the tensor cores; one token of a dense block 0.073 and 0.103.)
+    // the slices of the vectors fit shared memory.  (One token of 4096 x 14336: 47 us, 79 on the tensor cores; four: 82
+    // and 79, and 33 and 41 at 7168 x 2048; 61 tokens over 27 of 32 experts: 466 and 264.)
     return d.T <= kTokens && (d.H > d.F ? d.H : d.F) <= kMostSplit * kMostSlice;
 }
 
