@@ -45,7 +45,9 @@ constexpr int kStages = 3;
 constexpr int kThreads = 640;  // 4 warps that feed, 16 that add up
 constexpr uint32_t kOperand = 128 * 128;          // bytes of a 128 x 128 operand tile
 constexpr uint32_t kStageBytes = 4 * kOperand;    // hi, lo, two chunks of the weight
-constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 256 + 4096 + 4096;  // stages, barriers, exchange, factors
+constexpr int kStagePitch = 48;                     // of a row's 32 bytes on their way out
+// stages, barriers, exchange, factors, rows on their way out
+constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 256 + 4096 + 4096 + 16 * 32 * kStagePitch;
 
 struct Args {
     Plan plan;
@@ -112,6 +114,23 @@ __device__ __forceinline__ const float* b_scale(const Args& a, const Work& w, in
     if (n_major(kMode)) return s + min(n, a.sc - 1);
     return s + (int64_t)min(n, a.sr - 1) * a.sc;
 }
+// 32 bytes of each of a warp's 32 rows, a lane's own in v[2], through shared memory:
+// two lanes store a row's, so that a sector is written whole and an instruction
+// touches 16 lines, not 32.
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint4 (&v)[2], uint8_t* to, int64_t pitch,
+                                           int rows)
+{
+    *reinterpret_cast<uint4*>(stage + lane * kStagePitch) = v[0];
+    *reinterpret_cast<uint4*>(stage + lane * kStagePitch + 16) = v[1];
+    __syncwarp();
+#pragma unroll
+    for (int r = lane >> 1; r < 32; r += 16)
+        if (r < rows)
+            *reinterpret_cast<uint4*>(to + r * pitch + (lane & 1) * 16) =
+                *reinterpret_cast<const uint4*>(stage + r * kStagePitch + (lane & 1) * 16);
+    __syncwarp();
+}
+
 // g / (1 + exp(-g)) by t = exp(-|g|) <= 1: nothing overflows, and no branch (the
 // branch's code, 32 times a row, cost a small product 10 us of instruction fetches)
 __device__ __forceinline__ float silu(float g)
@@ -271,6 +290,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
         regs_more<104>();
         const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+        uint8_t* stage = extra_ptr + 256 + 4096 + 4096 + (warp - 4) * 32 * kStagePitch;
         Turn<2> acc;
         Turn<4> turn;
         int parity = 0;
@@ -360,8 +380,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 parity ^= 1;
                 const PairScale ps = pair_scale(amax);
                 if (group == 0) a.h.scale[(int64_t)w.n * a.rows + at] = ps.down;
-                uint4* hi = reinterpret_cast<uint4*>(a.h.hi + at * a.h.pitch + n0);
-                uint4* lo = reinterpret_cast<uint4*>(a.h.lo + at * a.h.pitch + n0);
+                uint4 hi[2], lo[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t vh[4], vl[4];
@@ -377,6 +396,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     hi[q] = make_uint4(vh[0], vh[1], vh[2], vh[3]);
                     lo[q] = make_uint4(vl[0], vl[1], vl[2], vl[3]);
                 }
+                const int64_t first = (at - lane) * a.h.pitch + n0;
+                store_rows(stage, lane, hi, a.h.hi + first, a.h.pitch, 32);
+                store_rows(stage, lane, lo, a.h.lo + first, a.h.pitch, 32);
             } else if constexpr (kMode == kPart) {
                 if (row < w.rows)
 #pragma unroll
@@ -406,23 +428,23 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 const uint32_t p = __reduce_max_sync(0xffffffffu, abs_bits(row < w.rows ? top : 0.0f));
                 if (lane == 0) atomicMax(&a.peaks[w.expert].dh, p);
             } else {
-                if (row < w.rows) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int64_t n0 = (int64_t)w.n * kCols + c * 128 + group * 32;
-                        bf16* o = a.out + (int64_t)(w.token0 + row) * a.ld + n0;
+                for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (n0 + q * 8 >= a.N) break;  // N is a multiple of 16
-                            uint32_t v[4];
+                    for (int q = 0; q < 2; ++q) {
+                        const int64_t n0 = (int64_t)w.n * kCols + c * 128 + group * 32 + q * 16;
+                        if (n0 >= a.N) break;  // N is a multiple of 16
+                        uint32_t v[8];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const __nv_bfloat162 two =
-                                    __floats2bfloat162_rn(sum[c][q * 8 + 2 * j], sum[c][q * 8 + 2 * j + 1]);
-                                v[j] = *reinterpret_cast<const uint32_t*>(&two);
-                            }
-                            *reinterpret_cast<uint4*>(o + q * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+                        for (int j = 0; j < 8; ++j) {
+                            const __nv_bfloat162 two =
+                                __floats2bfloat162_rn(sum[c][q * 16 + 2 * j], sum[c][q * 16 + 2 * j + 1]);
+                            v[j] = *reinterpret_cast<const uint32_t*>(&two);
                         }
+                        const uint4 out[2] = {make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7])};
+                        store_rows(stage, lane, out,
+                                   reinterpret_cast<uint8_t*>(a.out + (int64_t)(w.token0 + row - lane) * a.ld + n0),
+                                   a.ld * 2, w.rows - (row - lane));
                     }
                 }
             }
