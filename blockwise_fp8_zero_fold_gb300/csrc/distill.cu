@@ -6,18 +6,21 @@
 //
 // Bound by memory: the logits are read from it once and the gradient written
 // once.  A row is read twice, for its maximum and sum and, backwards, for the
-// gradient; the second time it comes from L2.
+// gradient; the second time it comes from L2, and a long row's first 92 KB from
+// shared memory.  4096 rows of 131072 BF16 logits take 362 us with the gradient
+// (5.9 TB/s) and 166 without (6.5).
 //
 // A row belongs to a CTA of 4 to 16 warps, or to a cluster of up to 8 of them,
-// each with a slice.  A thread has eight vectors of 16 bytes on their way and joins them, four at a
-// time, to a running maximum and the sum of exponentials in reference to it;
-// the warps' pairs are joined through distributed shared memory in a fixed
-// order, so results repeat bit for bit.  One warp of a CTA has the teacher's
+// each with a slice.  A thread has eight vectors of 16 bytes on their way and
+// joins them, four at a time, to a running maximum and the sum of exponentials in
+// reference to it; the warps' pairs are joined through distributed shared memory
+// in a fixed order, so results repeat bit for bit.  One warp of a CTA has the teacher's
 // entries, a long chain of small steps beside the others' loads: the softmax,
 // the student's logits behind the ids, repeated ids added up; then the loss and,
 // over the dense gradient w tau q_j, the listed elements.
-//
 #include <cooperative_groups.h>
+
+#include <algorithm>
 
 #include "ops_common.cuh"
 
@@ -160,6 +163,7 @@ struct Args {
     T* dlogits;
     int64_t ld_d;
     int64_t slice;     // vectors of a CTA
+    int32_t kept;      // the first batches of a slice that stay in shared memory for the gradient
 };
 
 // A CTA's part of a row.  Vector v of the row holds elements v kN - shift ..;
@@ -433,6 +437,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) row_kernel(const Ar
     // this thread's whole vectors: `share` of them, kReaders apart
     const int share = f1 - f0 > tid ? (f1 - f0 - 1 - tid) / kReaders + 1 : 0, batches = share / kHold;
     const T* const z0 = s.z + s.first + (int64_t)(f0 + tid) * kN;
+    uint4* const kept = reinterpret_cast<uint4*>(smem + list_entries(a.top) * kListBytes) + tid;
+    auto keep = [&](const Vec<T>(&v)[kHold], int b) {
+        if (b < a.kept)
+#pragma unroll
+            for (int j = 0; j < kHold; ++j) kept[(b * kHold + j) * kReaders] = v[j].v;
+    };
+    auto again = [&](Vec<T>(&v)[kHold], int b, const T* p) {
+        if (b >= a.kept) return load_some<T, kReaders>(v, p);
+#pragma unroll
+        for (int j = 0; j < kHold; ++j) v[j].v = kept[(b * kHold + j) * kReaders];
+    };
     if (warp == kWarps) {
         const Entries e = fill_lists(a, r, s.z, s.first, s.end, l);
         if (lane == 0) entries = e;
@@ -445,9 +460,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) row_kernel(const Ar
         if (tail) add_vec(Vec<T>{load_vec(s.z, tail_at, s.end)}, k, mine);
         for (int b = 0; b < batches; b += 2, p += 2 * kBatch) {
             if (b + 1 < batches) load_some<T, kReaders>(y, p + kBatch);
+            keep(x, b);
             add_vecs<T, kHold>(x, k, mine);
             if (b + 2 < batches) load_some<T, kReaders>(x, p + 2 * kBatch);
-            if (b + 1 < batches) add_vecs<T, kHold>(y, k, mine);
+            if (b + 1 < batches) {
+                keep(y, b + 1);
+                add_vecs<T, kHold>(y, k, mine);
+            }
         }
         // the last few
         p = z0 + batches * kBatch;
@@ -485,11 +504,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) row_kernel(const Ar
             Vec<T> x[kHold], y[kHold];
             const T* p = z0 + (batches - 1) * kBatch;
             T* o = d0 + (batches - 1) * kBatch;
-            if (batches > 0) load_some<T, kReaders>(x, p);
+            if (batches > 0) again(x, batches - 1, p);
             for (int b = batches; b > 0; b -= 2, p -= 2 * kBatch, o -= 2 * kBatch) {
-                if (b > 1) load_some<T, kReaders>(y, p - kBatch);
+                if (b > 1) again(y, b - 2, p - kBatch);
                 store_some<T, kReaders>(x, o, sc, q);
-                if (b > 2) load_some<T, kReaders>(x, p - 2 * kBatch);
+                if (b > 2) again(x, b - 3, p - 2 * kBatch);
                 if (b > 1) store_some<T, kReaders>(y, o - kBatch, sc, q);
             }
         } else {
@@ -540,6 +559,13 @@ int launch_clusters(void (*kernel)(const Args<T>), const Args<T>& a, int64_t clu
 template <class T, int kThreads>
 int launch_rows(Args<T> a, int ranks, cudaStream_t s)
 {
+    // Long rows keep the first of their batches in shared memory, as many as leave room for the SM's other CTA: the
+    // gradient reads them last, when a row's worth of every CTA and the gradient's lines have passed through L2.  (4096
+    // rows of 131072 BF16 logits: 362 us, 408 without; 8192 rows of 16384: 139 and 117, 1001 of 50001 FP32: 83 and 80.)
+    constexpr int64_t kBatchBytes = (int64_t)kHold * (kThreads - 32) * 16, kCtas = 1024 / kThreads;
+    const int64_t lists = list_entries(a.top) * kListBytes, room = 227 * 1024 / kCtas - 2048 - lists;
+    const bool leave_l2 = a.slice * 16 * kCtas * 152 > (int64_t)64 << 20;
+    a.kept = a.dlogits && leave_l2 ? (int32_t)std::min<int64_t>(room / kBatchBytes, a.slice * 16 / kBatchBytes) : 0;
     // rows beyond the grid's reach go in further launches
     const int64_t most = (int64_t)1 << 24;
     const Args<T> all = a;
@@ -552,7 +578,7 @@ int launch_rows(Args<T> a, int ranks, cudaStream_t s)
         a.loss = all.loss + r;
         a.dlogits = all.dlogits ? all.dlogits + r * all.ld_d : nullptr;
         const int st = launch_clusters<T>(row_kernel<T, kThreads>, a, a.rows, ranks, kThreads,
-                                          list_entries(a.top) * kListBytes, s);
+                                          lists + a.kept * kBatchBytes, s);
         if (st != FP8Z1_OK) return st;
     }
     return FP8Z1_OK;
@@ -569,8 +595,8 @@ int launch(Args<T> a, cudaStream_t s)
     while (ranks < 8 && a.rows * ranks * 2 <= 152 && vecs > ranks * 2 * 1024) ranks *= 2;
     a.slice = ceil_div(vecs, ranks);
     // A CTA's fixed chain of steps is about 7 us: short rows go to small CTAs, of which an SM holds many.  Long ones
-    // to few: their gradient is read again from L2, where eight 256 KB rows an SM would not fit (4096 rows of 131072
-    // BF16 logits took 411 us at two rows an SM, 443 at four, 511 at eight; 8192 rows of 16384 took 264, 169, 118).
+    // to few: they are read again from L2, where eight 256 KB rows an SM would not fit (4096 rows of 131072 BF16
+    // logits took 411 us at two rows an SM, 443 at four, 511 at eight; 8192 rows of 16384 took 264, 169, 118).
     // The loss alone reads once, and four rows an SM do best (172 us against 189 at two).
     const int64_t bytes = a.slice * 16;
     if (bytes <= 48 * 1024) return launch_rows<T, 128>(a, ranks, s);

@@ -53,6 +53,18 @@ def test_loss_and_gradient(rows, vocab, top, dtype, tau):
     assert d3 is z and torch.equal(z, d) and torch.equal(loss3, loss)
 
 
+@pytest.mark.parametrize("vocab,top,dtype", [(131072, 64, torch.bfloat16), (150001, 1024, torch.bfloat16),
+                                             (65537, 5, torch.float32), (57344, 33, torch.float32)])
+def test_many_long_rows(vocab, top, dtype):
+    """Rows of a CTA each, the first part of which stays in shared memory; the gradient in the logits' place."""
+    z, ids, t, w = make(81, vocab, top, dtype, vocab)
+    keep = z.clone()
+    loss, d = ops.distill_loss_grad(z, ids, t, row_weight=w, out=z)
+    check(keep, ids, t, w, 1.0, loss, d)
+    again = ops.distill_loss_grad(keep, ids, t, row_weight=w)
+    assert torch.equal(loss, again[0]) and torch.equal(d, again[1])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("vocab,lo", [(1000, 0), (1000, 1), (1000, 3), (33333, 5)])
 def test_strided_and_unaligned_rows(dtype, vocab, lo):
