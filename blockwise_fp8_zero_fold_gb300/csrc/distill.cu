@@ -10,7 +10,7 @@
 // shared memory.  4096 rows of 131072 BF16 logits take 362 us with the gradient
 // (5.9 TB/s) and 166 without (6.5).
 //
-// A row belongs to a CTA of 4 to 16 warps, or to a cluster of up to 8 of them,
+// A row belongs to a CTA of 2 to 16 warps, or to a cluster of up to 8 of them,
 // each with a slice.  A thread has eight vectors of 16 bytes on their way and
 // joins them, four at a time, to a running maximum and the sum of exponentials in
 // reference to it; the warps' pairs are joined through distributed shared memory
@@ -597,8 +597,11 @@ int launch(Args<T> a, cudaStream_t s)
     // A CTA's fixed chain of steps is about 7 us: short rows go to small CTAs, of which an SM holds many.  Long ones
     // to few: they are read again from L2, where eight 256 KB rows an SM would not fit (4096 rows of 131072 BF16
     // logits took 411 us at two rows an SM, 443 at four, 511 at eight; 8192 rows of 16384 took 264, 169, 118).
-    // The loss alone reads once, and four rows an SM do best (172 us against 189 at two).
+    // Rows of a few KB are that chain alone: 65536 of 2048 took 468 us in CTAs of 128 threads, 334 in 64; 16384 of 8192
+    // 164 and 147.  (With fewer rows than run at once in 128 threads, more threads a row end sooner.)  The loss alone
+    // reads once, and four rows an SM do best (172 us against 189 at two).
     const int64_t bytes = a.slice * 16;
+    if (bytes <= 24 * 1024 && a.rows * ranks > 152 * 8) return launch_rows<T, 64>(a, ranks, s);
     if (bytes <= 48 * 1024) return launch_rows<T, 128>(a, ranks, s);
     if (bytes <= 128 * 1024 || (!a.dlogits && bytes <= 1024 * 1024)) return launch_rows<T, 256>(a, ranks, s);
     return launch_rows<T, 512>(a, ranks, s);

@@ -31,8 +31,8 @@ def test_gradients_of_the_whole_step():
     q = (torch.cat(out) @ w[0][0].T).log_softmax(1)
     p = t_logits[ids].double().log_softmax(1)
     want = (p.exp() * (p - q.gather(1, t_ids[ids].long()))).sum(1).mean()
-    assert abs(float(loss) - float(want)) <= 6 * 2.0**-9 * abs(float(want))
     want.backward()
+    assert abs(float(loss) - want.item()) <= 6 * 2.0**-9 * abs(want.item())
     for got, ref in zip(s.grads, w):
         ref = ref.grad * scale
         assert float((got.double() - ref).norm()) <= 6 * 2.0**-9 * float(ref.norm())
