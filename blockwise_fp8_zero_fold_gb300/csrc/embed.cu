@@ -11,9 +11,16 @@
 // columns to a CTA, which adds up runs of equal ids in registers.  A run inside
 // one chunk is written at once; one that crosses chunks leaves a partial sum in
 // each, and a last kernel adds those up in order.  Nothing depends on the order
-// in which CTAs run: no atomics on floating point.  The table is cleared by the
-// CTAs beside the sorting ones in the first launch, which hides the sort behind
-// the clearing (2.1 GB of a 131072 x 4096 table).
+// in which CTAs run: no atomics on floating point.
+//
+// Nearly all of the time is the table's zeros.  Up to 16384 tokens one CTA sorts
+// while the others clear as much as takes that long; what is left of a large table
+// is cleared beside the sums, by CTAs that look up which of their rows have a
+// token and leave those out.  131072 x 4096 with 16384 tokens: 377 us, 6.1 TB/s
+// (412 with all of it cleared beside the sort); with 2000 tokens 323 (359); with
+// 40000, sorted in passes, 523 (598).
+#include <algorithm>
+
 #include "ops_common.cuh"
 
 namespace {
@@ -389,7 +396,36 @@ struct Runs {
     float* table;
     int64_t dim;
     float alpha;
+    int64_t chunks;
+    // rows [uncleared, vocab) hold no zeros yet: CTAs behind the chunks' have rows_each of them and clear what has no token
+    int64_t uncleared, vocab, rows_each;
 };
+
+constexpr int kMostRowsEach = 128;
+
+__device__ __forceinline__ void clear_unnamed_rows(const Runs& r)
+{
+    __shared__ bool named[kMostRowsEach];
+    const int64_t r0 = r.uncleared + ((blockIdx.x - r.chunks) * gridDim.y + blockIdx.y) * r.rows_each;
+    const int n = (int)max(min(r.rows_each, r.vocab - r0), (int64_t)0);
+    if ((int)threadIdx.x < n) {
+        int64_t a = 0, b = *r.s.n_real, end = b;
+        const uint32_t row = (uint32_t)(r0 + threadIdx.x);
+        while (a < b) {
+            const int64_t m = (a + b) / 2;
+            if (r.s.key[m] < row)
+                a = m + 1;
+            else
+                b = m;
+        }
+        named[threadIdx.x] = a < end && r.s.key[a] == row;
+    }
+    __syncthreads();
+    for (int i = 0; i < n; ++i)
+        if (!named[i])
+            for (int64_t d = threadIdx.x * 4; d < r.dim; d += kSumThreads * 4)
+                __stcs(reinterpret_cast<float4*>(r.table + (r0 + i) * r.dim + d), make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+}
 
 // Columns of a thread: 8 of aligned rows, 1 of others.
 template <class T, int kCols>
@@ -430,6 +466,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(Runs r, const T* __res
 {
     __shared__ uint32_t key[kChunk + 2];
     __shared__ int32_t token[kChunk];
+    if constexpr (kCols == 8)
+        if (blockIdx.x >= r.chunks) return clear_unnamed_rows(r);
     const int64_t c = blockIdx.x, p0 = c * kChunk, real = *r.s.n_real;
     if (p0 >= real) return;
     const int n = (int)min((int64_t)kChunk, real - p0);
@@ -517,9 +555,10 @@ __global__ void __launch_bounds__(kSumThreads) join_kernel(Runs r)
 template <class T, int kCols>
 int launch_sums(const Runs& r, const T* dy, int64_t ld, int64_t tokens, cudaStream_t s)
 {
-    const dim3 grid((unsigned)ceil_div(tokens, kChunk), (unsigned)ceil_div(r.dim, kSumThreads * kCols));
+    const dim3 grid((unsigned)r.chunks, (unsigned)ceil_div(r.dim, kSumThreads * kCols));
+    const int64_t clearing = ceil_div(ceil_div(r.vocab - r.uncleared, r.rows_each), grid.y);
     count_launch();
-    sum_kernel<T, kCols><<<grid, kSumThreads, 0, s>>>(r, dy, ld);
+    sum_kernel<T, kCols><<<dim3((unsigned)(r.chunks + clearing), grid.y), kSumThreads, 0, s>>>(r, dy, ld);
     if (tokens > kChunk) {
         count_launch();
         join_kernel<kCols><<<grid, kSumThreads, 0, s>>>(r);
@@ -568,6 +607,9 @@ struct Space {
         bytes = at;
     }
 };
+
+// bytes cleared in the time of a sort of up to 2048 and of up to 16384 tokens
+constexpr int64_t kClearFew = (int64_t)128 << 20, kClearMany = (int64_t)400 << 20;
 
 constexpr int sort_smem(int items) { return kBins * kSortWarps * 2 + items * kSortThreads * 6; }
 
@@ -629,17 +671,27 @@ extern "C" int fp8z1_embed_grad(int64_t vocab, int64_t dim, const void* ids, int
     Space w(workspace, dim, tokens);
     const int sms = sm_count_here();
     if (sms < 1) return FP8Z1_ECUDA;
+    const int esz = dy_type == FP8Z1_F32 ? 4 : 2;
+    const bool wide = dim % 8 == 0 && aligned(dy, 16) && ld_dy * esz % 16 == 0 && aligned(d_table, 16);
+    // What is cleared while one CTA sorts (the passes of a larger sort are short launches that it would delay); the rest
+    // beside the sums, where rows that get one are left out.
+    int64_t first = vocab;
+    if (wide) {
+        const int64_t beside =
+            tokens <= 2 * kSortThreads ? kClearFew : tokens <= 16 * kSortThreads ? kClearMany : 0;
+        if (beside / (dim * 4) < vocab) first = beside / (dim * 4);
+    }
     // CTAs that clear: 64 KB each at least, two for every SM at most
-    const int64_t wanted = ceil_div(n_table, 16384);
+    const int64_t n_first = first * dim, wanted = ceil_div(n_first, 16384);
     const unsigned clear_ctas = (unsigned)(wanted < 2 * sms ? wanted : 2 * sms);
     int bits = 1;  // of the keys 0 .. vocab
     while (vocab >> bits) ++bits;
     const int passes = (bits + 7) / 8;
     Sorted sorted{w.key[0], w.token[0], w.n_real};
     if (tokens <= 2 * kSortThreads) {
-        st = sort_small<2>(i, tokens, vocab, passes, sorted, d_table, n_table, clear_ctas, s);
+        st = sort_small<2>(i, tokens, vocab, passes, sorted, d_table, n_first, clear_ctas, s);
     } else if (tokens <= 16 * kSortThreads) {
-        st = sort_small<16>(i, tokens, vocab, passes, sorted, d_table, n_table, clear_ctas, s);
+        st = sort_small<16>(i, tokens, vocab, passes, sorted, d_table, n_first, clear_ctas, s);
     } else {
         const int64_t tiles = ceil_div(tokens, kSortTile);
         Pass p = {i, nullptr, nullptr, w.key[0], w.token[0], tokens, vocab, w.counts, tiles, 0};
@@ -663,9 +715,9 @@ extern "C" int fp8z1_embed_grad(int64_t vocab, int64_t dim, const void* ids, int
         st = launch_status();
     }
     if (st != FP8Z1_OK) return st;
-    const Runs r{sorted, w.partial, d_table, dim, alpha};
-    const int esz = dy_type == FP8Z1_F32 ? 4 : 2;
-    const bool wide = dim % 8 == 0 && aligned(dy, 16) && ld_dy * esz % 16 == 0 && aligned(d_table, 16);
+    // half a megabyte of rows for a clearing CTA
+    const int64_t each = std::max<int64_t>(std::min<int64_t>((1 << 19) / (dim * 4), kMostRowsEach), 1);
+    const Runs r{sorted, w.partial, d_table, dim, alpha, ceil_div(tokens, kChunk), first, vocab, each};
     if (dy_type == FP8Z1_F32) {
         const float* p = static_cast<const float*>(dy);
         return wide ? launch_sums<float, 8>(r, p, ld_dy, tokens, s) : launch_sums<float, 1>(r, p, ld_dy, tokens, s);

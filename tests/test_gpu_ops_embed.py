@@ -87,6 +87,24 @@ def test_gradient(vocab, dim, tokens, dtype, id_type):
     assert torch.equal(got, ops.embed_grad(ids, dy, vocab, alpha=1.5)), "the gradient does not repeat bit for bit"
 
 
+@pytest.mark.parametrize("vocab,dim,tokens", [(70001, 512, 700), (70001, 512, 1), (30000, 4096, 5000), (9001, 64, 20000), (3, 40, 17000)])
+def test_gradient_of_large_tables(vocab, dim, tokens):
+    """Tables cleared beside the sums: every row without a token is zero, the others are not touched by it."""
+    g = gen(vocab + tokens)
+    ids = (torch.rand(tokens, generator=g, device="cuda").pow(3) * (vocab + 1)).long() - 1  # -1 too; common and rare ids
+    ids[-1] = vocab - 1
+    dy = torch.randn(tokens, dim, generator=g, device="cuda")
+    out = torch.full((vocab, dim), 7.0, device="cuda")
+    got = ops.embed_grad(ids, dy, vocab, out=out)
+    real = ids >= 0
+    want = torch.zeros(vocab, dim, dtype=torch.float64, device="cuda").index_add_(0, ids[real], dy[real].double())
+    mag = torch.zeros(vocab, dim, dtype=torch.float64, device="cuda").index_add_(0, ids[real], dy[real].double().abs())
+    n = torch.bincount(ids[real], minlength=vocab)[:, None]
+    assert ((got.double() - want).abs() <= (n + 1) * 2.0**-24 * mag).all()
+    again = ops.embed_grad(ids, dy, vocab, out=torch.full_like(out, float("nan")))
+    assert torch.equal(got, again)
+
+
 def test_gradient_of_no_tokens_and_strided_rows():
     g = gen(5)
     none = torch.full((40,), -1, device="cuda")
