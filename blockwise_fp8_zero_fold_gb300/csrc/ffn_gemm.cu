@@ -26,6 +26,13 @@
 //
 // CTAs are persistent; tiles run expert by expert, a column's row tiles next
 // to each other, so that an expert's codes are read from memory once.
+//
+// Bound by the tensor cores from some 100 rows an expert: 8192 tokens over 31
+// experts of 7168 x 2048 take 0.46 ms (gate_up), 0.24 (down), 0.23 (dh) and 0.42
+// (dx), 1040 TFLOP/s of BF16 products, 1350 with the padded rows.  A tile's end
+// (4 to 6 us, SiLU and encoding a third of it) is hidden by no more than the two
+// accumulators and costs 14 % of that.  With fewer rows bound by the codes read:
+// 61 tokens over 27 experts at 6.1 TB/s while every SM has a tile.
 #include "ffn.cuh"
 
 namespace fp8z1 {
