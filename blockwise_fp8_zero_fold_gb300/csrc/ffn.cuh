@@ -279,7 +279,7 @@ int launch_after(void (*kernel)(A...), dim3 grid, int threads, uint32_t smem, cu
     return launch_status();
 }
 
-// Launches, right behind another kernel of the pass, a persistent one of one CTA an SM, in clusters of one or two: as
+// Launches, right behind another kernel of the pass, a persistent one of one CTA an SM, in clusters of one, two or four: as
 // many as run at once, `most` at most.
 template <auto kKernel, class... P>
 int launch_clusters(int threads, uint32_t smem, int cluster, int64_t most, cudaStream_t s, const P&... args)
@@ -297,7 +297,7 @@ int launch_clusters(int threads, uint32_t smem, int cluster, int64_t most, cudaS
     c.attrs = at;
     c.numAttrs = 1;
     // what the device holds at once, asked once for each kernel, device and cluster size
-    static std::atomic<int> holds[16][2];
+    static std::atomic<int> holds[16][4];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FP8Z1_ECUDA;
     int n = dev < 16 ? holds[dev][cluster - 1].load(std::memory_order_relaxed) : 0;

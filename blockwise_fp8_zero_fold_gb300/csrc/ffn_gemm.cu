@@ -263,7 +263,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     if (a.cluster == 1)
                         commit(bar_empty + 8 * turn.slot);
                     else
-                        commit_both<1>(bar_empty + 8 * turn.slot);
+                        commit_to<1>(bar_empty + 8 * turn.slot, 3);
                     commit(bar_acc + 8 * acc.slot);
                 }
             }

@@ -18,10 +18,17 @@
 // up in registers.  The last step issues only the 16-row products that hold
 // rows; rows past an expert's end are zeros.
 //
+// A stage is 48 KB for 0.54 us of products, more than L2 delivers to every SM at
+// once: two pairs of a cluster take neighbouring column tiles of the same 256
+// columns, and one fetches their hi, the other their lo for both (32 KB a CTA).  A
+// GB300 holds 36 such clusters, 144 CTAs of 152, and still gains: 2051 tokens of
+// 4096 x 14336 take 790 us for both gradients, 930 by single pairs; 8192 tokens over
+// 31 experts of 7168 x 2048, which wait for their stores, the same 1170.
+//
 // Bound by the FP32 gradients written (4 bytes an element) up to about 250
 // tokens an expert, by the tensor cores above: 8192 tokens over 31 experts of 7168 x
-// 2048 take 770 us (d_gate_up) and 400 (d_down), 1250 TFLOP/s of FP16 products;
-// four experts of 512 keep the tensor cores busy 65 to 71 % of the time.
+// 2048 take 770 us (d_gate_up) and 400 (d_down), 4.8 TB/s written; 2051 tokens of a
+// dense block 1520 TFLOP/s of FP16 products.
 #include "ffn.cuh"
 
 namespace fp8z1 {
@@ -49,7 +56,8 @@ struct Args {
     const Peaks* peaks;
     float* out;        // kTransposed: [E, N, M]
     int64_t M, N;      // columns of the two-term operand, of the other
-    int32_t m_tiles, n_tiles, experts;
+    int32_t m_tiles, n_groups, experts;
+    int32_t pairs;     // of a cluster, 1 or 2, on neighbouring column tiles of the same rows
 };
 
 // kTransposed: the two-term operand's columns are the gradient's columns
@@ -68,11 +76,12 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
     volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem_raw + (extra + 96 - smem_addr(smem_raw)));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank();
+    const int rank = (int)cluster_rank(), sub = rank & 1;  // of the cluster, of the pair
+    const uint32_t both = 3u << (rank & 2), all = a.pairs == 2 ? 15u : 3u;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(bar_full + 8 * i, 1);
-            bar_init(bar_empty + 8 * i, 1);
+            bar_init(bar_empty + 8 * i, a.pairs);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(bar_acc + 8 * i, 1);
@@ -93,8 +102,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
     after_previous();
     const uint32_t tmem = *tmem_at;
     const int m_pairs = (a.m_tiles + 1) / 2;
-    const int64_t per = (int64_t)m_pairs * a.n_tiles, total = per * a.experts;
-    const int64_t i0 = blockIdx.x / 2, step = gridDim.x / 2;
+    const int64_t per = (int64_t)m_pairs * a.n_groups, total = per * a.experts;
+    const int64_t i0 = blockIdx.x / (2 * a.pairs), step = gridDim.x / (2 * a.pairs);
     bool ok = true;
 
     if (warp < 4) {
@@ -103,7 +112,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
             Turn<kStages> turn;
             for (int64_t i = i0; i < total && ok; i += step) {
                 const int e = (int)(i / per), local = (int)(i - e * per);
-                const int m = local % m_pairs * 2 + rank, n = local / m_pairs;
+                const int m = local % m_pairs * 2 + sub, n = local / m_pairs * a.pairs + rank / 2;
                 const int row0 = a.plan.start[e] * kRows, steps = (a.plan.tokens[e] + kStep - 1) / kStep;
                 for (int k = 0; k < steps; ++k, turn.next()) {
                     if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
@@ -111,16 +120,24 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                         break;
                     }
                     // both CTAs' copies are counted in the first one, whose thread multiplies
-                    if (rank == 0) bar_expect(bar_full + 8 * turn.slot, 2 * kStageBytes);
-                    const uint32_t full = first_of_pair(bar_full + 8 * turn.slot), dst = base + turn.slot * kStageBytes;
-                    load_3d_pair(dst, &map_hi, full, 0, row0 + k * kStep, m * 2);
-                    load_3d_pair(dst + 2 * kChunk, &map_lo, full, 0, row0 + k * kStep, m * 2);
-                    load_3d_pair(dst + 4 * kChunk, &map_b, full, 0, row0 + k * kStep, n * 4 + rank * 2);
+                    if (sub == 0) bar_expect(bar_full + 8 * turn.slot, 2 * kStageBytes);
+                    const uint32_t full = first_of_pair(bar_full + 8 * turn.slot, rank), dst = base + turn.slot * kStageBytes;
+                    if (a.pairs == 1) {
+                        load_3d_pair(dst, &map_hi, full, 0, row0 + k * kStep, m * 2);
+                        load_3d_pair(dst + 2 * kChunk, &map_lo, full, 0, row0 + k * kStep, m * 2);
+                    } else {  // the CTA two further on has the same rows: one fetches their hi, the other their lo for both
+                        const uint32_t mask = 5u << sub;
+                        if (rank < 2)
+                            load_3d_pairs(dst, &map_hi, full, 0, row0 + k * kStep, m * 2, mask);
+                        else
+                            load_3d_pairs(dst + 2 * kChunk, &map_lo, full, 0, row0 + k * kStep, m * 2, mask);
+                    }
+                    load_3d_pair(dst + 4 * kChunk, &map_b, full, 0, row0 + k * kStep, n * 4 + sub * 2);
                 }
             }
             // the copies in flight are read before the CTA ends, whatever became of the other warps
             for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && lane == 0 && sub == 0) {
             constexpr uint32_t idesc = instruction(256, kCols, true, true);
             Turn<kStages> turn;
             Turn<2> acc;
@@ -143,9 +160,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                             mma_f16_pair(d, operand(src + k * 2048, 1024, kChunk), db, idesc, sub + k > 0);
                             mma_f16_pair(d, operand(src + 2 * kChunk + k * 2048, 1024, kChunk), db, idesc, true);
                         }
-                        commit_both<2>(bar_empty + 8 * turn.slot);
+                        commit_to<2>(bar_empty + 8 * turn.slot, all);
                     }
-                    if (ok) commit_both<2>(bar_acc + 8 * acc.slot);
+                    if (ok) commit_to<2>(bar_acc + 8 * acc.slot, both);
                 }
             }
             // every product issued ends, and its sums are read, before the tensor memory is freed
@@ -158,7 +175,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
         Turn<2> acc;
         for (int64_t i = i0; i < total && ok; i += step) {
             const int e = (int)(i / per), local = (int)(i - e * per);
-            const int m = local % m_pairs * 2 + rank, n = local / m_pairs;
+            const int m = local % m_pairs * 2 + sub, n = local / m_pairs * a.pairs + rank / 2;
             const int tokens = a.plan.tokens[e];
             const Peaks p = a.peaks[e];
             const Pow2 f = pow2(kTransposed ? -(x_shift(p) + dgu_shift(p)) : -(dy_shift(p) + h_shift(p)));
@@ -181,7 +198,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                     if (q == 3) {
                         fence_before();
                         __syncwarp();
-                        if (lane == 0) bar_arrive_pair(first_of_pair(bar_free + 8 * acc.slot));
+                        if (lane == 0) bar_arrive_pair(first_of_pair(bar_free + 8 * acc.slot, rank));
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -287,10 +304,12 @@ int launch(const Dims& d, const Plan& p, const Peaks* peaks, const __half* hi, c
     a.M = M;
     a.N = d.H;
     a.m_tiles = (int32_t)(M / 128);
-    a.n_tiles = (int32_t)ceil_div(d.H, kCols);
+    const int32_t n_tiles = (int32_t)ceil_div(d.H, kCols);
+    a.pairs = n_tiles % 2 == 0 ? 2 : 1;
+    a.n_groups = n_tiles / a.pairs;
     a.experts = (int32_t)d.E;
-    const int64_t total = (int64_t)((a.m_tiles + 1) / 2) * a.n_tiles * d.E;
-    return launch_clusters<wgrad_kernel<kTransposed>>(kThreads, kSmem, 2, total, s, mh, ml, mb, mo, a);
+    const int64_t total = (int64_t)((a.m_tiles + 1) / 2) * a.n_groups * d.E;
+    return launch_clusters<wgrad_kernel<kTransposed>>(kThreads, kSmem, 2 * a.pairs, total, s, mh, ml, mb, mo, a);
 }
 
 }  // namespace

@@ -65,11 +65,12 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
     }
 }
 
-// The cluster address of this CTA's address `a` in the pair's first CTA.
-__device__ __forceinline__ uint32_t first_of_pair(uint32_t a)
+// The cluster address of this CTA's address `a` in the first CTA of its pair
+// (ranks 2 i and 2 i + 1).
+__device__ __forceinline__ uint32_t first_of_pair(uint32_t a, uint32_t rank)
 {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank & ~1u));
     return r;
 }
 // An arrival on a barrier at a cluster address, after this thread's tensor memory
@@ -153,6 +154,18 @@ __device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* ma
         : "memory");
 }
 
+// The same to the CTAs of `mask`, at this CTA's offset of the destination, counted
+// in the first CTA of each one's pair.
+__device__ __forceinline__ void load_3d_pairs(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                              uint32_t mask)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(
+            dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "h"((uint16_t)mask)
+        : "memory");
+}
+
 __device__ __forceinline__ void store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z)
 {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
@@ -208,19 +221,19 @@ __device__ __forceinline__ void commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// The same on the barriers at this offset of both CTAs of the cluster.
+// The same on the barriers at this offset of the cluster's CTAs of `mask`.
 template <int kGroup>
-__device__ __forceinline__ void commit_both(uint32_t bar)
+__device__ __forceinline__ void commit_to(uint32_t bar, uint32_t mask)
 {
     if constexpr (kGroup == 2)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"((uint16_t)3)
+            "h"((uint16_t)mask)
             : "memory");
     else
         asm volatile(
             "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"((uint16_t)3)
+            "h"((uint16_t)mask)
             : "memory");
 }
 
