@@ -31,7 +31,9 @@
 // experts of 7168 x 2048 take 0.46 ms (gate_up), 0.24 (down), 0.23 (dh) and 0.42
 // (dx), 1040 TFLOP/s of BF16 products, 1350 with the padded rows.  A tile's end
 // (4 to 6 us, SiLU and encoding a third of it) is hidden by no more than the two
-// accumulators and costs 14 % of that.  With fewer rows bound by the codes read:
+// accumulators and costs 14 % of that; reading the sums of every 128 of k out of
+// tensor memory costs about as much (1750 TFLOP/s without).  Sharing the codes as
+// well, by clusters of 2 x 2 tiles, gained nothing.  With fewer rows bound by the codes read:
 // 61 tokens over 27 experts at 6.1 TB/s while every SM has a tile.
 #include "ffn.cuh"
 

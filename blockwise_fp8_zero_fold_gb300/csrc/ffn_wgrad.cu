@@ -22,13 +22,13 @@
 // once: two pairs of a cluster take neighbouring column tiles of the same 256
 // columns, and one fetches their hi, the other their lo for both (32 KB a CTA).  A
 // GB300 holds 36 such clusters, 144 CTAs of 152, and still gains: 2051 tokens of
-// 4096 x 14336 take 790 us for both gradients, 930 by single pairs; 8192 tokens over
-// 31 experts of 7168 x 2048, which wait for their stores, the same 1170.
+// 4096 x 14336 take 545 us (d_gate_up) and 280 (d_down), 640 and 300 by single
+// pairs; 8192 tokens over 31 experts of 7168 x 2048, which wait for their stores,
+// the same 770 and 400.
 //
 // Bound by the FP32 gradients written (4 bytes an element) up to about 250
-// tokens an expert, by the tensor cores above: 8192 tokens over 31 experts of 7168 x
-// 2048 take 770 us (d_gate_up) and 400 (d_down), 4.8 TB/s written; 2051 tokens of a
-// dense block 1520 TFLOP/s of FP16 products.
+// tokens an expert, by the tensor cores above: the experts' gradients are written at
+// 4.8 TB/s, the dense block's multiplied at 1750 TFLOP/s (FP16 products).
 #include "ffn.cuh"
 
 namespace fp8z1 {
