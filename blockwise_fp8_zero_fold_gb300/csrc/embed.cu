@@ -21,6 +21,7 @@
 // (412 with all of it cleared beside the sort); with 2000 tokens 323 (359); with
 // 40000, sorted in passes, 523 (598).
 #include <algorithm>
+#include <type_traits>
 
 #include "ops_common.cuh"
 
@@ -609,8 +610,14 @@ struct Space {
     }
 };
 
-// bytes cleared in the time of a sort of up to 2048 and of up to 16384 tokens
-constexpr int64_t kClearFew = (int64_t)128 << 20, kClearMany = (int64_t)400 << 20;
+// Keys of a thread of the one sorting CTA: 2048 tokens take 10 to 15 us to sort (two
+// and three passes), 4096 13 to 20, 8192 21 to 33, 16384 40 to 63; and the bytes that
+// the other CTAs clear in about that time.
+constexpr int sort_items(int64_t tokens)
+{
+    return tokens <= 2 * kSortThreads ? 2 : tokens <= 4 * kSortThreads ? 4 : tokens <= 8 * kSortThreads ? 8 : 16;
+}
+constexpr int64_t cleared_beside(int items) { return (int64_t)(64 + 21 * items) << 20; }
 
 constexpr int sort_smem(int items) { return kBins * kSortWarps * 2 + items * kSortThreads * 6; }
 
@@ -678,8 +685,7 @@ extern "C" int fp8z1_embed_grad(int64_t vocab, int64_t dim, const void* ids, int
     // beside the sums, where rows that get one are left out.
     int64_t first = vocab;
     if (wide) {
-        const int64_t beside =
-            tokens <= 2 * kSortThreads ? kClearFew : tokens <= 16 * kSortThreads ? kClearMany : 0;
+        const int64_t beside = tokens <= 16 * kSortThreads ? cleared_beside(sort_items(tokens)) : 0;
         if (beside / (dim * 4) < vocab) first = beside / (dim * 4);
     }
     // CTAs that clear: 64 KB each at least, two for every SM at most
@@ -689,10 +695,16 @@ extern "C" int fp8z1_embed_grad(int64_t vocab, int64_t dim, const void* ids, int
     while (vocab >> bits) ++bits;
     const int passes = (bits + 7) / 8;
     Sorted sorted{w.key[0], w.token[0], w.n_real};
-    if (tokens <= 2 * kSortThreads) {
-        st = sort_small<2>(i, tokens, vocab, passes, sorted, d_table, n_first, clear_ctas, s);
-    } else if (tokens <= 16 * kSortThreads) {
-        st = sort_small<16>(i, tokens, vocab, passes, sorted, d_table, n_first, clear_ctas, s);
+    if (tokens <= 16 * kSortThreads) {
+        const auto sort = [&](auto kItems) {
+            return sort_small<decltype(kItems)::value>(i, tokens, vocab, passes, sorted, d_table, n_first, clear_ctas, s);
+        };
+        switch (sort_items(tokens)) {
+            case 2: st = sort(std::integral_constant<int, 2>{}); break;
+            case 4: st = sort(std::integral_constant<int, 4>{}); break;
+            case 8: st = sort(std::integral_constant<int, 8>{}); break;
+            default: st = sort(std::integral_constant<int, 16>{});
+        }
     } else {
         const int64_t tiles = ceil_div(tokens, kSortTile);
         Pass p = {i, nullptr, nullptr, w.key[0], w.token[0], tokens, vocab, w.counts, tiles, 0};
