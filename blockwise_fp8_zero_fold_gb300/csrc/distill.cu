@@ -531,9 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) row_kernel(const Ar
     if (warp == kWarps) write_listed(l, e.own, s.dz, sc, q, w * a.tau);
 }
 
-template <class T>
-int launch_clusters(void (*kernel)(const Args<T>), const Args<T>& a, int64_t clusters, int ranks, int threads,
-                    int64_t smem, cudaStream_t s)
+constexpr int kMostSmem = 112 * 1024;  // two CTAs of 512 threads an SM
+
+template <auto kKernel, class T>
+int launch_clusters(const Args<T>& a, int64_t clusters, int ranks, int threads, int64_t smem, cudaStream_t s)
 {
     cudaLaunchConfig_t c = {};
     cudaLaunchAttribute at = {};
@@ -546,10 +547,9 @@ int launch_clusters(void (*kernel)(const Args<T>), const Args<T>& a, int64_t clu
     c.stream = s;
     c.attrs = &at;
     c.numAttrs = ranks > 1;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return FP8Z1_ECUDA;
+    if (smem > 40 * 1024 && !allow_smem<kKernel>(kMostSmem)) return FP8Z1_ECUDA;
     count_launch();
-    if (cudaLaunchKernelEx(&c, kernel, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&c, kKernel, a) != cudaSuccess) {
         cudaGetLastError();
         return FP8Z1_ECUDA;
     }
@@ -563,8 +563,8 @@ int launch_rows(Args<T> a, int ranks, cudaStream_t s)
     // gradient reads them last, when a row's worth of every CTA and the gradient's lines have passed through L2.  (4096
     // rows of 131072 BF16 logits: 362 us, 408 without; 8192 rows of 16384: 139 and 117, 1001 of 50001 FP32: 83 and 80.)
     constexpr int64_t kBatchBytes = (int64_t)kHold * (kThreads - 32) * 16, kCtas = 1024 / kThreads;
-    const int64_t lists = list_entries(a.top) * kListBytes, room = 227 * 1024 / kCtas - 2048 - lists;
-    const bool leave_l2 = a.slice * 16 * kCtas * 152 > (int64_t)64 << 20;
+    const int64_t lists = list_entries(a.top) * kListBytes, room = kMostSmem - lists;
+    const bool leave_l2 = kCtas == 2 && a.slice * 16 * kCtas * 152 > (int64_t)64 << 20;
     a.kept = a.dlogits && leave_l2 ? (int32_t)std::min<int64_t>(room / kBatchBytes, a.slice * 16 / kBatchBytes) : 0;
     // rows beyond the grid's reach go in further launches
     const int64_t most = (int64_t)1 << 24;
@@ -577,8 +577,7 @@ int launch_rows(Args<T> a, int ranks, cudaStream_t s)
         a.weight = all.weight ? all.weight + r : nullptr;
         a.loss = all.loss + r;
         a.dlogits = all.dlogits ? all.dlogits + r * all.ld_d : nullptr;
-        const int st = launch_clusters<T>(row_kernel<T, kThreads>, a, a.rows, ranks, kThreads,
-                                          lists + a.kept * kBatchBytes, s);
+        const int st = launch_clusters<row_kernel<T, kThreads>>(a, a.rows, ranks, kThreads, lists + a.kept * kBatchBytes, s);
         if (st != FP8Z1_OK) return st;
     }
     return FP8Z1_OK;

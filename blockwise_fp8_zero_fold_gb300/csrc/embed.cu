@@ -625,9 +625,7 @@ template <int kItems>
 int sort_small(Ids ids, int64_t tokens, int64_t vocab, int passes, const Sorted& out, float* table, int64_t n_table,
                unsigned clear_ctas, cudaStream_t s)
 {
-    if (cudaFuncSetAttribute(sort_small_kernel<kItems>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sort_smem(kItems)) != cudaSuccess)
-        return FP8Z1_ECUDA;
+    if (!allow_smem<sort_small_kernel<kItems>>(sort_smem(kItems))) return FP8Z1_ECUDA;
     count_launch();
     sort_small_kernel<kItems><<<1 + clear_ctas, kSortThreads, sort_smem(kItems), s>>>(
         ids, (int32_t)tokens, vocab, passes, out, table, n_table);

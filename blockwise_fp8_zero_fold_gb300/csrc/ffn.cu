@@ -423,8 +423,7 @@ extern "C" int fp8z1_ffn_backward(const fp8z1_ffn_dims* dims, const void* dy, in
     Pairs pairs = b.dgu;
     if (!dx) pairs.hi = nullptr;
     constexpr int kActSmem = 3 * 32 * kActPitch * 4;
-    if (cudaFuncSetAttribute(activation_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kActSmem) != cudaSuccess)
-        return FP8Z1_ECUDA;
+    if (!allow_smem<activation_kernel>(kActSmem)) return FP8Z1_ECUDA;
     if ((st = launch_after(activation_kernel, dim3((unsigned)(d.tiles() * 4), (unsigned)(d.F / 128)), 256, kActSmem, s, plan,
                            keep.gu, b.dh, d.F, d.rows(), pairs, b.dgu_hi, b.dgu_lo, b.h_hi, b.h_lo, b.peaks)) != FP8Z1_OK ||
         (st = launch_after(halves_kernel, row_ctas, 256, 0, s, plan, xb, ld_x, dyb, ld_dy, d.H, d.Hp(), b.x16, b.dy16,

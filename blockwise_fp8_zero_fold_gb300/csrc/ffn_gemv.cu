@@ -248,16 +248,7 @@ int launch(Args a, const Shape& shape, int64_t runs, cudaStream_t s)
     c.stream = s;
     c.attrs = at;
     c.numAttrs = kGateUp ? 1 : 2;
-    // the most this kernel is launched with, set once for each device
-    static std::atomic<uint32_t> set{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return FP8Z1_ECUDA;
-    if (dev > 31 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kMostSlice * (kMost * (int)sizeof(T) + 1)) != cudaSuccess)
-            return FP8Z1_ECUDA;
-        if (dev < 32) set.fetch_or(1u << dev, std::memory_order_relaxed);
-    }
+    if (!allow_smem<gemv_kernel<kGateUp, kOut, kMost>>(kMostSlice * (kMost * (int)sizeof(T) + 1))) return FP8Z1_ECUDA;
     count_launch();
     if (cudaLaunchKernelEx(&c, kernel, a) != cudaSuccess) {
         cudaGetLastError();

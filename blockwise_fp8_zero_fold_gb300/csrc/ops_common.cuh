@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "fp8z1_ops.h"
 #include "internal.h"
 #include "update.cuh"
@@ -31,6 +33,23 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x)
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t code) { return e4m3x2_decode(code).x; }
+
+// Lets kKernel take up to `bytes` (always the same) of dynamic shared memory on the
+// current device; asked once for each, as the question costs as much as a launch.
+template <auto kKernel>
+bool allow_smem(int bytes)
+{
+    static std::atomic<uint32_t> asked{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < 32 && asked.load(std::memory_order_relaxed) >> dev & 1) return true;
+    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    if (dev < 32) asked.fetch_or(1u << dev, std::memory_order_relaxed);
+    return true;
+}
 
 // The SM count of the current device (0 when it cannot be read).
 inline int sm_count_here()
