@@ -405,7 +405,8 @@ __device__ __forceinline__ void store_some(const Vec<T> (&x)[kHold], T* p, const
     }
 }
 
-template <class T, int kThreads>
+// kKeep: whether the first batches of a slice stay in shared memory.
+template <class T, int kThreads, bool kKeep>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) row_kernel(const Args<T> a)
 {
     constexpr int kN = Vec<T>::n, kReaders = kThreads - 32, kWarps = kReaders / 32;
@@ -439,14 +440,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) row_kernel(const Ar
     const T* const z0 = s.z + s.first + (int64_t)(f0 + tid) * kN;
     uint4* const kept = reinterpret_cast<uint4*>(smem + list_entries(a.top) * kListBytes) + tid;
     auto keep = [&](const Vec<T>(&v)[kHold], int b) {
-        if (b < a.kept)
+        if constexpr (kKeep) {
+            if (b >= a.kept) return;
 #pragma unroll
             for (int j = 0; j < kHold; ++j) kept[(b * kHold + j) * kReaders] = v[j].v;
+        }
     };
     auto again = [&](Vec<T>(&v)[kHold], int b, const T* p) {
-        if (b >= a.kept) return load_some<T, kReaders>(v, p);
+        if constexpr (kKeep) {
+            if (b < a.kept) {
 #pragma unroll
-        for (int j = 0; j < kHold; ++j) v[j].v = kept[(b * kHold + j) * kReaders];
+                for (int j = 0; j < kHold; ++j) v[j].v = kept[(b * kHold + j) * kReaders];
+                return;
+            }
+        }
+        load_some<T, kReaders>(v, p);
     };
     if (warp == kWarps) {
         const Entries e = fill_lists(a, r, s.z, s.first, s.end, l);
@@ -556,16 +564,12 @@ int launch_clusters(const Args<T>& a, int64_t clusters, int ranks, int threads, 
     return launch_status();
 }
 
-template <class T, int kThreads>
+template <class T, int kThreads, bool kKeep = false>
 int launch_rows(Args<T> a, int ranks, cudaStream_t s)
 {
-    // Long rows keep the first of their batches in shared memory, as many as leave room for the SM's other CTA: the
-    // gradient reads them last, when a row's worth of every CTA and the gradient's lines have passed through L2.  (4096
-    // rows of 131072 BF16 logits: 362 us, 408 without; 8192 rows of 16384: 139 and 117, 1001 of 50001 FP32: 83 and 80.)
-    constexpr int64_t kBatchBytes = (int64_t)kHold * (kThreads - 32) * 16, kCtas = 1024 / kThreads;
-    const int64_t lists = list_entries(a.top) * kListBytes, room = kMostSmem - lists;
-    const bool leave_l2 = kCtas == 2 && a.slice * 16 * kCtas * 152 > (int64_t)64 << 20;
-    a.kept = a.dlogits && leave_l2 ? (int32_t)std::min<int64_t>(room / kBatchBytes, a.slice * 16 / kBatchBytes) : 0;
+    constexpr int64_t kBatchBytes = (int64_t)kHold * (kThreads - 32) * 16;
+    const int64_t lists = list_entries(a.top) * kListBytes;
+    a.kept = kKeep ? (int32_t)std::min<int64_t>((kMostSmem - lists) / kBatchBytes, a.slice * 16 / kBatchBytes) : 0;
     // rows beyond the grid's reach go in further launches
     const int64_t most = (int64_t)1 << 24;
     const Args<T> all = a;
@@ -577,7 +581,7 @@ int launch_rows(Args<T> a, int ranks, cudaStream_t s)
         a.weight = all.weight ? all.weight + r : nullptr;
         a.loss = all.loss + r;
         a.dlogits = all.dlogits ? all.dlogits + r * all.ld_d : nullptr;
-        const int st = launch_clusters<row_kernel<T, kThreads>>(a, a.rows, ranks, kThreads, lists + a.kept * kBatchBytes, s);
+        const int st = launch_clusters<row_kernel<T, kThreads, kKeep>>(a, a.rows, ranks, kThreads, lists + a.kept * kBatchBytes, s);
         if (st != FP8Z1_OK) return st;
     }
     return FP8Z1_OK;
@@ -603,6 +607,10 @@ int launch(Args<T> a, cudaStream_t s)
     if (bytes <= 24 * 1024 && a.rows * ranks > 152 * 8) return launch_rows<T, 64>(a, ranks, s);
     if (bytes <= 48 * 1024) return launch_rows<T, 128>(a, ranks, s);
     if (bytes <= 128 * 1024 || (!a.dlogits && bytes <= 1024 * 1024)) return launch_rows<T, 256>(a, ranks, s);
+    // Long rows keep the first of their batches in shared memory, as many as leave room for the SM's other CTA: the
+    // gradient reads them last, when a row's worth of every CTA and the gradient's lines have passed through L2.  (4096
+    // rows of 131072 BF16 logits: 362 us, 408 without; 1001 of 50001 FP32: 83 and 80.)
+    if (a.dlogits && bytes * 2 * 152 > (int64_t)64 << 20) return launch_rows<T, 512, true>(a, ranks, s);
     return launch_rows<T, 512>(a, ranks, s);
 }
 
