@@ -14,9 +14,11 @@ Each is one call of libfp8z1.so's entry point of the same name (include/
 fp8z1_ops.h has the formulas); this module checks the tensors, allocates
 outputs and workspaces through torch and enqueues on ``stream`` (a
 ``torch.cuda.Stream``; None is torch's current stream).  With a ``stream``
-that is not current, the outputs and workspaces are marked as used there; the
-inputs' memory is the caller's to keep until the work is done.  Tensors that
-do not fit raise ValueError, what the library refuses raises Fp8z1Error.
+that is not current, the outputs and workspaces are allocated as that stream's
+and the outputs marked as used on the current one too; the order of the two
+streams, and the inputs' memory until the work is done, are the caller's to
+see to.  Tensors that do not fit raise ValueError, what the library refuses
+raises Fp8z1Error.
 """
 from __future__ import annotations
 
@@ -53,11 +55,20 @@ def _begin(dev: int, stream):
     return stream.cuda_stream, stream if stream.cuda_stream != now else None
 
 
+def _scratch(shape, dtype, dev: int, other):
+    """Memory of one call, from the pool of the stream that the call is enqueued on.  (The current stream's
+    pool may give out a block that the current stream's kernels still use: in order there, not on ``other``.)"""
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(other):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _new(shape, dtype, dev: int, other):
-    """A tensor of one call: on its stream, so that its memory is not reused early."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
+    """An output: the same, and kept until what the caller's stream does with it is done."""
+    t = _scratch(shape, dtype, dev, other)
     if other is not None:
-        t.record_stream(other)
+        t.record_stream(torch.cuda.current_stream(dev))
     return t
 
 
@@ -158,7 +169,7 @@ def embed_grad(ids: torch.Tensor, dy: torch.Tensor, vocab: int, *, alpha: float 
         out = _new((vocab, dim), torch.float32, dev, other)
     elif not _given(out, (vocab, dim), torch.float32, dev, "out").is_contiguous():
         _bad("out must be contiguous")
-    ws = _new(F.fp8z1_embed_grad_workspace(vocab, dim, n), torch.uint8, dev, other)
+    ws = _scratch(F.fp8z1_embed_grad_workspace(vocab, dim, n), torch.uint8, dev, other)
     F.fp8z1_embed_grad(vocab, dim, ids, nbytes, n, alpha, dy, kind, ld, out, ws, raw)
     return out
 
@@ -199,7 +210,7 @@ def ffn_forward(x: torch.Tensor, gate_up: torch.Tensor, gate_up_scale: torch.Ten
         _given(out, x.shape, torch.bfloat16, dev, "out")
     saved_bytes, forward_bytes, _ = F.fp8z1_ffn_sizes(dims)
     saved = _new(saved_bytes, torch.uint8, dev, other) if save else None
-    ws = _new(forward_bytes, torch.uint8, dev, other)
+    ws = _scratch(forward_bytes, torch.uint8, dev, other)
     F.fp8z1_ffn_forward(dims, x, _rows(x, "x"), offsets, gate_up, gate_up_scale, down, down_scale, out,
                         _rows(out, "out"), saved, ws, raw)
     return (out, saved) if save else out
@@ -229,7 +240,7 @@ def ffn_backward(dy: torch.Tensor, x: torch.Tensor, saved: torch.Tensor, gate_up
         elif not _given(given, w.shape, torch.float32, dev, what).is_contiguous():
             _bad(f"{what} must be contiguous")
         grads.append(given)
-    ws = _new(backward_bytes, torch.uint8, dev, other)
+    ws = _scratch(backward_bytes, torch.uint8, dev, other)
     F.fp8z1_ffn_backward(dims, dy, _rows(dy, "dy"), x, _rows(x, "x"), offsets, gate_up, gate_up_scale, down,
                          down_scale, saved, dx, _rows(dx, "dx") if need_dx else 0, grads[0], grads[1], ws, raw)
     return dx, grads[0], grads[1]
