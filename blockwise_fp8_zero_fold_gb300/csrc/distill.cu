@@ -99,42 +99,47 @@ __device__ __forceinline__ void store_vec(T* z, int64_t at, int64_t n, bool whol
         if (at + i >= 0 && at + i < n) z[at + i] = from_float<T>(f[i]);
 }
 
-// Exponents are taken in the log2 domain as fma(z, k, -m k), one rounding of
-// the whole.  m k is rounded first, but alike wherever m is the reference, so
-// the shares e / sum do not see it.  A maximum so large that m k could
-// overflow (a row of nothing but a mask's lowest value) takes (z - m) k.
+// Exponents are taken in the log2 domain as fma(z, k, -mk), one rounding of the
+// whole, with mk the rounded m k: the reference is mk / k, and what it differs from
+// m by, rest() in the log2 domain, is the same for all that is added up and comes
+// off the sum's logarithm at the end.  From |m k| = 2^22 on (a row, or a thread's part
+// of one, of nothing but a mask's value) the rest could leave FP32's exponents, and
+// (z - m) k is taken, whose reference is m itself.
 struct Base {  // of a launch
     float k, limit;
     __device__ __forceinline__ explicit Base(float tau)
     {
         k = 1.4426950408889634f / tau;
-        limit = 1e37f / fmaxf(k, 1.0f);
+        limit = 4194304.0f / k;
     }
 };
-struct Scale {
-    float k, m, mk;
+struct Scale : Base {
+    float m, mk;
     bool plain;
-    __device__ __forceinline__ Scale(const Base& b, float top) : k(b.k)
+    __device__ __forceinline__ Scale(const Base& b, float top) : Base(b)
     {
         m = top == -INFINITY ? 0.0f : top;
-        plain = fabsf(m) <= b.limit;
+        plain = fabsf(m) <= limit;
         mk = m * k;
     }
     __device__ __forceinline__ float of(float z) const
     {
         return exp2_fast(plain ? fmaf(z, k, -mk) : (z - m) * k);
     }
+    __device__ __forceinline__ float rest() const { return plain ? fmaf(m, k, -mk) : 0.0f; }
 };
 
 // A maximum and the sum of the exponentials in reference to it.
 struct __align__(8) Sum {
     float m, s;
 };
-// `part`'s sum in reference to another maximum; 0 for an empty part
+// `part`'s sum in reference to another, no smaller maximum; 0 for an empty part
 __device__ __forceinline__ float in_reference(const Sum& part, const Scale& to)
 {
-    const float d = to.plain ? part.m * to.k - to.mk : (part.m - to.m) * to.k;
-    return part.m == -INFINITY ? part.s * 0.0f : part.s * exp2_fast(d);
+    if (to.plain && fabsf(part.m) <= to.limit) return part.s * exp2_fast(part.m * to.k - to.mk);
+    if (part.m == -INFINITY) return part.s * 0.0f;
+    const Scale from(to, part.m);
+    return part.s * exp2_fast((part.m - to.m) * to.k + (to.rest() - from.rest()));
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -293,19 +298,19 @@ __device__ __forceinline__ Entries fill_lists(const Args<T>& a, int64_t r, const
     return e;
 }
 
-// The loss of a row of maximum m and sum `total`, by one warp:
-//   log p - log q = log p - (z - m) / tau + log total, and the p add up to 1.
+// The loss of a row of reference `sc` and sum `total`, by one warp:
+//   log p - log q = log p - (z - m) / tau + log (total / 2^rest), and the p add up to 1.
 template <class T>
-__device__ __forceinline__ void write_loss(const Args<T>& a, int64_t r, const Lists& l, const Entries& e, float m,
+__device__ __forceinline__ void write_loss(const Args<T>& a, int64_t r, const Lists& l, const Entries& e, const Scale& sc,
                                            float total)
 {
     float pz = 0.0f;
     if (e.any)
         for (int i = threadIdx.x & 31; i < a.top; i += 32)
-            if (l.p[i] != 0.0f) pz = fmaf(l.p[i], l.zk[i] - m, pz);
+            if (l.p[i] != 0.0f) pz = fmaf(l.p[i], l.zk[i] - sc.m, pz);
     pz = warp_sum(pz);
     // a row of -inf alone has q = 0: its log q is z = -inf, not -inf - -inf
-    const float log_total = total == 0.0f ? 0.0f : logf(total);
+    const float log_total = total == 0.0f ? 0.0f : fmaf(sc.rest(), -0.6931471805599453f, logf(total));
     if ((threadIdx.x & 31) == 0) a.loss[r] = e.any ? a.tau * a.tau * (e.p_logp - pz / a.tau + log_total) : 0.0f;
 }
 
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) row_kernel(const Ar
     const Sum row = row_join(parts, ranks * kWarps, k);
     const Scale sc(k, row.m);
     const float q = inverse(row.s) * (w * a.tau);
-    if (warp == kWarps && rank == 0) write_loss(a, r, l, e, row.m, row.s);
+    if (warp == kWarps && rank == 0) write_loss(a, r, l, e, sc, row.s);
     if (!s.dz) return;
     if (warp < kWarps) {
         float f[kN];
