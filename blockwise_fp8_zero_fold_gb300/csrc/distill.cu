@@ -229,7 +229,7 @@ __device__ __forceinline__ Entries fill_lists(const Args<T>& a, int64_t r, const
         const float t = __ldg(a.teacher + r * a.top + i);
         const bool there = j >= 0 && j < a.vocab && t != -INFINITY;
         l.id[i] = there ? j : -1;
-        l.p[i] = there ? t / a.tau : -INFINITY;
+        l.p[i] = there ? t : -INFINITY;
         l.zk[i] = there ? to_float(z[j]) : 0.0f;
         any |= there;
         top = fmaxf(top, l.p[i]);
@@ -239,7 +239,12 @@ __device__ __forceinline__ Entries fill_lists(const Args<T>& a, int64_t r, const
     top = warp_max(top);
     float mass = 0.0f;
     for (int i = lane; i < a.top; i += 32)
-        if (l.id[i] >= 0) mass += exp2_fast((l.p[i] - top) * kLog2e);
+        if (l.id[i] >= 0) {
+            // the difference first: a mask's lowest value by a temperature below 1 would be -inf
+            const float t = (l.p[i] - top) / a.tau;
+            l.p[i] = t;
+            mass += exp2_fast(t * kLog2e);
+        }
     mass = warp_sum(mass);
     const float log_mass = logf(mass), by = 1.0f / mass;
     for (int i0 = 0; i0 < a.top; i0 += 32) {
@@ -249,8 +254,8 @@ __device__ __forceinline__ Entries fill_lists(const Args<T>& a, int64_t r, const
         if (i < a.top && l.id[i] >= 0) {
             j = l.id[i];
             zk = l.zk[i];
-            const float logp = l.p[i] - top - log_mass;
-            p = exp2_fast((l.p[i] - top) * kLog2e) * by;
+            const float logp = l.p[i] - log_mass;
+            p = exp2_fast(l.p[i] * kLog2e) * by;
             // an entry too small to count: 0 log 0 = 0, whatever the student's logit
             if (p != 0.0f) e.p_logp = fmaf(p, logp, e.p_logp);
         }
