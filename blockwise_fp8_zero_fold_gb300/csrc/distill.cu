@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) row_kernel(const Ar
                 store_vec(s.dz, at, s.end, s.same, zero);
     };
     if (w == 0.0f) return clear();  // the same in every CTA of the cluster
+    if (ranks > 1) cluster.sync();  // every CTA has started: the others may write to it
     // the slice's vectors [0, vecs), those inside the row whole [f0, f1): the others are the row's first and last
     const int vecs = s.end > s.first ? (int)((s.end - s.first + kN - 1) / kN) : 0;
     const int f0 = s.first < 0 ? 1 : 0, f1 = s.end > s.first ? (int)((s.end - s.first) / kN) : 0;

@@ -70,3 +70,22 @@ def test_beside_a_read_of_memory_that_is_freed(name):
     call(s)
     torch.cuda.synchronize()
     assert all((k == 7).all() for k in kept)
+
+
+def test_clusters_that_start_one_by_one():
+    """A row over several CTAs while other kernels hold most of the SMs: no CTA writes to one that has not started."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    z = torch.randn(5, 131_072, generator=g, device="cuda")
+    ids = torch.randint(131_072, (5, 16), generator=g, device="cuda", dtype=torch.int32)
+    t = torch.randn(5, 16, generator=g, device="cuda")
+    want = ops.distill_loss_grad(z, ids, t)
+    a = torch.randn(2048, 2048, generator=g, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = []
+    for _ in range(100):
+        with torch.cuda.stream(s):
+            a @ a
+        got.append(ops.distill_loss_grad(z, ids, t))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for pair in got for x, y in zip(pair, want))
