@@ -280,15 +280,15 @@ int launch_after(void (*kernel)(A...), dim3 grid, int threads, uint32_t smem, cu
     return launch_status();
 }
 
-// Launches, right behind another kernel of the pass, a persistent one of one CTA an SM, in clusters of one, two or four: as
-// many as run at once, `most` at most.
-template <auto kKernel, class... P>
-int launch_clusters(int threads, uint32_t smem, int cluster, int64_t most, cudaStream_t s, const P&... args)
+// Launches, right behind another kernel of the pass, a persistent one of one CTA an SM, in clusters of kCluster: as many as
+// run at once, `most` at most.
+template <auto kKernel, int kCluster, class... P>
+int launch_persistent(int threads, uint32_t smem, int64_t most, cudaStream_t s, const P&... args)
 {
     cudaLaunchConfig_t c = {};
     cudaLaunchAttribute at[2] = {};
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)cluster;
+    at[0].val.clusterDim.x = kCluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
@@ -297,21 +297,21 @@ int launch_clusters(int threads, uint32_t smem, int cluster, int64_t most, cudaS
     c.stream = s;
     c.attrs = at;
     c.numAttrs = 1;
-    // what the device holds at once, asked once for each kernel, device and cluster size
-    static std::atomic<int> holds[16][4];
+    // what the device holds at once, asked once for each kernel and device
+    static std::atomic<int> holds[16];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FP8Z1_ECUDA;
-    int n = dev < 16 ? holds[dev][cluster - 1].load(std::memory_order_relaxed) : 0;
+    int n = dev < 16 ? holds[dev].load(std::memory_order_relaxed) : 0;
     if (n == 0) {
-        c.gridDim = dim3((unsigned)cluster);
+        c.gridDim = dim3(kCluster);
         if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, kKernel, &c) != cudaSuccess || n < 1) {
             cudaGetLastError();
             return FP8Z1_ECUDA;
         }
-        if (dev < 16) holds[dev][cluster - 1].store(n, std::memory_order_relaxed);
+        if (dev < 16) holds[dev].store(n, std::memory_order_relaxed);
     }
-    c.gridDim = dim3((unsigned)((most < n ? most : n) * cluster));
+    c.gridDim = dim3((unsigned)((most < n ? most : n) * kCluster));
     c.numAttrs = 2;
     count_launch();
     if (cudaLaunchKernelEx(&c, kKernel, args...) != cudaSuccess) {

@@ -18,10 +18,8 @@
 //
 // A CTA owns 128 rows x 256 columns.  Warp 0 issues TMA copies of K steps (64
 // KB: the rows' hi and lo, 256 weight columns) three steps ahead, warp 1 the
-// products into one of two 256-column accumulators, 16 warps add up.  Two CTAs
-// of a cluster take neighbouring column tiles of the same rows, and one fetches
-// their hi, the other their lo for both.  (Pairs of CTAs with 256 rows were as
-// fast on full tiles and lost a quarter on experts of 100 to 400 rows; transposed
+// products into one of two 256-column accumulators, 16 warps add up.  (Pairs of
+// CTAs with 256 rows lost a quarter on experts of 100 to 400 rows; transposed
 // products of 128 columns, whose time follows an expert's rows, lost half.)
 //
 // CTAs are persistent; tiles run expert by expert, a column's row tiles next
@@ -65,9 +63,8 @@ struct Args {
     int64_t rows;          // of the row operands (pitch of a_scale)
     int64_t F;
     int64_t N;             // columns of the result (kGateUp: F pairs)
-    int32_t n_groups;      // groups of column tiles
-    int32_t cluster;       // CTAs of a cluster: 1 or 2
-    int32_t splits;        // kPart: CTAs (clusters) along K, else 1
+    int32_t n_tiles;       // column tiles
+    int32_t splits;        // kPart: CTAs along K, else 1
     int32_t k_blocks;
     int32_t sr, sc;        // the scale grid of an expert
     int32_t b_step;        // from one K block's scale to the next
@@ -85,20 +82,19 @@ struct Work {
     int32_t split, k0, k1;  // K blocks
 };
 
-// The i-th group of column tiles (one, or a cluster's two) of the launch, expert
-// by expert, column by column, and the tile of CTA `rank`.
-__device__ __forceinline__ Work work_at(const Args& a, int64_t i, int rank)
+// The i-th tile of the launch, expert by expert, column by column.
+__device__ __forceinline__ Work work_at(const Args& a, int64_t i)
 {
-    const int32_t per = a.n_groups * a.splits, t = (int32_t)(i / per);
+    const int32_t per = a.n_tiles * a.splits, t = (int32_t)(i / per);
     const int32_t e = a.plan.tiles[t].expert;
     const int32_t first = a.plan.start[e], count = a.plan.start[e + 1] - first;
     const int64_t local = i - (int64_t)first * per;
     Work w;
-    const int32_t column = (int32_t)(local / count), group = column / a.splits;
-    w.split = column - group * a.splits;
+    const int32_t column = (int32_t)(local / count);
+    w.n = column / a.splits;
+    w.split = column - w.n * a.splits;
     w.k0 = (int32_t)((int64_t)a.k_blocks * w.split / a.splits);
     w.k1 = (int32_t)((int64_t)a.k_blocks * (w.split + 1) / a.splits);
-    w.n = group * a.cluster + rank;
     w.tile = first + (int32_t)(local - (int64_t)column * count);
     const Tile tile = a.plan.tiles[w.tile];
     w.expert = e;
@@ -168,11 +164,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     float* exchange = reinterpret_cast<float*>(extra_ptr + 256);  // [2][4][128]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(bar_full + 8 * i, 1);
-            bar_init(bar_empty + 8 * i, a.cluster);
+            bar_init(bar_empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(bar_acc + 8 * i, 1);
@@ -193,12 +188,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     fence_before();
     __syncthreads();
     __syncwarp();
-    cluster_sync();  // the other CTA may write to this one's stages and barriers from here on
     fence_after();
     after_previous();
     const uint32_t tmem = *tmem_at;
-    const int64_t total = (int64_t)*a.plan.n_tiles * a.n_groups * a.splits;
-    const int64_t i0 = blockIdx.x / a.cluster, step = gridDim.x / a.cluster;
+    const int64_t total = (int64_t)*a.plan.n_tiles * a.n_tiles * a.splits, i0 = blockIdx.x, step = gridDim.x;
     bool ok = true;
 
     if (warp < 4) {
@@ -207,7 +200,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             // TMA: K steps of every tile, kStages ahead
             Turn<kStages> turn;
             for (int64_t i = i0; i < total && ok; i += step) {
-                const Work w = work_at(a, i, rank);
+                const Work w = work_at(a, i);
                 const int c0 = chunk_column<kMode>(a, w, 0), c1 = chunk_column<kMode>(a, w, 1), y = w.tile * kRows;
                 for (int kb = w.k0; kb < w.k1; ++kb, turn.next()) {
                     if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
@@ -216,14 +209,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     }
                     const uint32_t full = bar_full + 8 * turn.slot, dst = base + turn.slot * kStageBytes;
                     bar_expect(full, kStageBytes);
-                    if (a.cluster == 1) {
-                        load_2d(dst, &map_hi, full, kb * 128, y);
-                        load_2d(dst + kOperand, &map_lo, full, kb * 128, y);
-                    } else if (rank == 0) {
-                        load_2d_both(dst, &map_hi, full, kb * 128, y);
-                    } else {
-                        load_2d_both(dst + kOperand, &map_lo, full, kb * 128, y);
-                    }
+                    load_2d(dst, &map_hi, full, kb * 128, y);
+                    load_2d(dst + kOperand, &map_lo, full, kb * 128, y);
                     if (n_major(kMode)) {
                         load_3d(dst + 2 * kOperand, &map_w, full, c0, kb * 128, w.expert);
                         load_3d(dst + 3 * kOperand, &map_w, full, c1, kb * 128, w.expert);
@@ -242,7 +229,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             Turn<kStages> turn;
             Turn<2> acc;
             for (int64_t i = i0; i < total && ok; i += step) {
-                const Work w = work_at(a, i, rank);
+                const Work w = work_at(a, i);
                 for (int kb = w.k0; kb < w.k1; ++kb, turn.next(), acc.next()) {
                     if (!bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) ||
                         !bar_wait(bar_full + 8 * turn.slot, turn.phase)) {
@@ -262,10 +249,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                                                          : operand(src + 2 * kOperand + k * 32, 1024, 16);
                             mma_f8(d, da, db, idesc[t], t + k > 0);
                         }
-                    if (a.cluster == 1)
-                        commit(bar_empty + 8 * turn.slot);
-                    else
-                        commit_to<1>(bar_empty + 8 * turn.slot, 3);
+                    commit(bar_empty + 8 * turn.slot);
                     commit(bar_acc + 8 * acc.slot);
                 }
             }
@@ -276,7 +260,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             Turn<4> turn;
             const int mine = threadIdx.x - 64;
             for (int64_t i = i0; i < total && ok; i += step) {
-                const Work w = work_at(a, i, rank);
+                const Work w = work_at(a, i);
                 const float* pa = a.a_scale + (int64_t)w.tile * kRows + mine;
                 const float *p0 = b_scale<kMode>(a, w, 0), *p1 = b_scale<kMode>(a, w, 1);
                 for (int kb = w.k0; kb < w.k1; ++kb, turn.next()) {
@@ -304,7 +288,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
         Turn<4> turn;
         int parity = 0;
         for (int64_t i = i0; i < total && ok; i += step) {
-            const Work w = work_at(a, i, rank);
+            const Work w = work_at(a, i);
             const int64_t at = (int64_t)w.tile * kRows + row;  // row of the internal buffers
             uint64_t sums2[2][16];  // pairs of columns
 #pragma unroll
@@ -343,7 +327,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 }
             }
             if (!ok) break;
-            if (w.n * (kMode == kGateUp ? 128 : kCols) >= a.N) continue;  // past the last column tile of the group
             float sum[2][32];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -463,7 +446,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     fence_before();
     __syncthreads();
     __syncwarp();
-    cluster_sync();  // no CTA leaves while the other may still write to it
     fence_after();
     if (warp == 2) tmem_free<1, 512>(tmem);
 }
@@ -559,15 +541,13 @@ int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a,
     a.b_scale = w.scale;
     a.rows = d.rows();
     a.F = d.F;
-    const int64_t n_tiles = kMode == kGateUp ? d.F / 128 : ceil_div(a.N, kCols);
-    a.cluster = n_tiles % 2 == 0 || n_tiles > 8 ? 2 : 1;  // an odd tile's neighbour multiplies for nothing
-    a.n_groups = (int32_t)ceil_div(n_tiles, a.cluster);
+    a.n_tiles = (int32_t)(kMode == kGateUp ? d.F / 128 : ceil_div(a.N, kCols));
     if (kMode != kPart) a.splits = 1;
     a.k_blocks = (int32_t)ceil_div(K, kBlock);
     a.sr = (int32_t)ceil_div(w.R, 128);
     a.sc = (int32_t)ceil_div(w.C, 128);
     a.b_step = n_major(kMode) ? a.sc : 1;
-    return launch_clusters<gemm_kernel<kMode>>(kThreads, kSmem, a.cluster, d.tiles() * a.n_groups * a.splits, s, hi, lo, wm, a);
+    return launch_persistent<gemm_kernel<kMode>, 1>(kThreads, kSmem, d.tiles() * a.n_tiles * a.splits, s, hi, lo, wm, a);
 }
 
 }  // namespace

@@ -16,15 +16,8 @@
 // N-major to the tensor cores.  The pipeline is ffn_gemm.cu's: TMA steps of 64
 // token rows (48 KB a CTA), products into two accumulators, each 256 rows added
 // up in registers.  The last step issues only the 16-row products that hold
-// rows; rows past an expert's end are zeros.
-//
-// A stage is 48 KB for 0.54 us of products, more than L2 delivers to every SM at
-// once: two pairs of a cluster take neighbouring column tiles of the same 256
-// columns, and one fetches their hi, the other their lo for both (32 KB a CTA).  A
-// GB300 holds 36 such clusters, 144 CTAs of 152, and still gains: 2051 tokens of
-// 4096 x 14336 take 545 us (d_gate_up) and 280 (d_down), 640 and 300 by single
-// pairs; 8192 tokens over 31 experts of 7168 x 2048, which wait for their stores,
-// the same 770 and 400.
+// rows; rows past an expert's end are zeros.  A stage is 48 KB for 0.54 us of
+// products, more than L2 delivers to every SM at once.
 //
 // Bound by the FP32 gradients written (4 bytes an element) up to about 250
 // tokens an expert, by the tensor cores above: the experts' gradients are written at
@@ -56,8 +49,7 @@ struct Args {
     const Peaks* peaks;
     float* out;        // kTransposed: [E, N, M]
     int64_t M, N;      // columns of the two-term operand, of the other
-    int32_t m_tiles, n_groups, experts;
-    int32_t pairs;     // of a cluster, 1 or 2, on neighbouring column tiles of the same rows
+    int32_t m_tiles, n_tiles, experts;
 };
 
 // kTransposed: the two-term operand's columns are the gradient's columns
@@ -76,12 +68,11 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
     volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem_raw + (extra + 96 - smem_addr(smem_raw)));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank(), sub = rank & 1;  // of the cluster, of the pair
-    const uint32_t both = 3u << (rank & 2), all = a.pairs == 2 ? 15u : 3u;
+    const int sub = (int)cluster_rank();  // of the pair
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(bar_full + 8 * i, 1);
-            bar_init(bar_empty + 8 * i, a.pairs);
+            bar_init(bar_empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(bar_acc + 8 * i, 1);
@@ -102,8 +93,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
     after_previous();
     const uint32_t tmem = *tmem_at;
     const int m_pairs = (a.m_tiles + 1) / 2;
-    const int64_t per = (int64_t)m_pairs * a.n_groups, total = per * a.experts;
-    const int64_t i0 = blockIdx.x / (2 * a.pairs), step = gridDim.x / (2 * a.pairs);
+    const int64_t per = (int64_t)m_pairs * a.n_tiles, total = per * a.experts;
+    const int64_t i0 = blockIdx.x / 2, step = gridDim.x / 2;
     bool ok = true;
 
     if (warp < 4) {
@@ -112,7 +103,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
             Turn<kStages> turn;
             for (int64_t i = i0; i < total && ok; i += step) {
                 const int e = (int)(i / per), local = (int)(i - e * per);
-                const int m = local % m_pairs * 2 + sub, n = local / m_pairs * a.pairs + rank / 2;
+                const int m = local % m_pairs * 2 + sub, n = local / m_pairs;
                 const int row0 = a.plan.start[e] * kRows, steps = (a.plan.tokens[e] + kStep - 1) / kStep;
                 for (int k = 0; k < steps; ++k, turn.next()) {
                     if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
@@ -121,17 +112,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                     }
                     // both CTAs' copies are counted in the first one, whose thread multiplies
                     if (sub == 0) bar_expect(bar_full + 8 * turn.slot, 2 * kStageBytes);
-                    const uint32_t full = first_of_pair(bar_full + 8 * turn.slot, rank), dst = base + turn.slot * kStageBytes;
-                    if (a.pairs == 1) {
-                        load_3d_pair(dst, &map_hi, full, 0, row0 + k * kStep, m * 2);
-                        load_3d_pair(dst + 2 * kChunk, &map_lo, full, 0, row0 + k * kStep, m * 2);
-                    } else {  // the CTA two further on has the same rows: one fetches their hi, the other their lo for both
-                        const uint32_t mask = 5u << sub;
-                        if (rank < 2)
-                            load_3d_pairs(dst, &map_hi, full, 0, row0 + k * kStep, m * 2, mask);
-                        else
-                            load_3d_pairs(dst + 2 * kChunk, &map_lo, full, 0, row0 + k * kStep, m * 2, mask);
-                    }
+                    const uint32_t full = first_of_pair(bar_full + 8 * turn.slot), dst = base + turn.slot * kStageBytes;
+                    load_3d_pair(dst, &map_hi, full, 0, row0 + k * kStep, m * 2);
+                    load_3d_pair(dst + 2 * kChunk, &map_lo, full, 0, row0 + k * kStep, m * 2);
                     load_3d_pair(dst + 4 * kChunk, &map_b, full, 0, row0 + k * kStep, n * 4 + sub * 2);
                 }
             }
@@ -160,9 +143,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                             mma_f16_pair(d, operand(src + k * 2048, 1024, kChunk), db, idesc, sub + k > 0);
                             mma_f16_pair(d, operand(src + 2 * kChunk + k * 2048, 1024, kChunk), db, idesc, true);
                         }
-                        commit_to<2>(bar_empty + 8 * turn.slot, all);
+                        commit_pair(bar_empty + 8 * turn.slot);
                     }
-                    if (ok) commit_to<2>(bar_acc + 8 * acc.slot, both);
+                    if (ok) commit_pair(bar_acc + 8 * acc.slot);
                 }
             }
             // every product issued ends, and its sums are read, before the tensor memory is freed
@@ -175,7 +158,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
         Turn<2> acc;
         for (int64_t i = i0; i < total && ok; i += step) {
             const int e = (int)(i / per), local = (int)(i - e * per);
-            const int m = local % m_pairs * 2 + sub, n = local / m_pairs * a.pairs + rank / 2;
+            const int m = local % m_pairs * 2 + sub, n = local / m_pairs;
             const int tokens = a.plan.tokens[e];
             const Peaks p = a.peaks[e];
             const Pow2 f = pow2(kTransposed ? -(x_shift(p) + dgu_shift(p)) : -(dy_shift(p) + h_shift(p)));
@@ -198,7 +181,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                     if (q == 3) {
                         fence_before();
                         __syncwarp();
-                        if (lane == 0) bar_arrive_pair(first_of_pair(bar_free + 8 * acc.slot, rank));
+                        if (lane == 0) bar_arrive_pair(first_of_pair(bar_free + 8 * acc.slot));
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -304,12 +287,10 @@ int launch(const Dims& d, const Plan& p, const Peaks* peaks, const __half* hi, c
     a.M = M;
     a.N = d.H;
     a.m_tiles = (int32_t)(M / 128);
-    const int32_t n_tiles = (int32_t)ceil_div(d.H, kCols);
-    a.pairs = n_tiles % 2 == 0 ? 2 : 1;
-    a.n_groups = n_tiles / a.pairs;
+    a.n_tiles = (int32_t)ceil_div(d.H, kCols);
     a.experts = (int32_t)d.E;
-    const int64_t total = (int64_t)((a.m_tiles + 1) / 2) * a.n_groups * d.E;
-    return launch_clusters<wgrad_kernel<kTransposed>>(kThreads, kSmem, 2 * a.pairs, total, s, mh, ml, mb, mo, a);
+    const int64_t total = (int64_t)((a.m_tiles + 1) / 2) * a.n_tiles * d.E;
+    return launch_persistent<wgrad_kernel<kTransposed>, 2>(kThreads, kSmem, total, s, mh, ml, mb, mo, a);
 }
 
 }  // namespace

@@ -65,12 +65,11 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
     }
 }
 
-// The cluster address of this CTA's address `a` in the first CTA of its pair
-// (ranks 2 i and 2 i + 1).
-__device__ __forceinline__ uint32_t first_of_pair(uint32_t a, uint32_t rank)
+// The cluster address of this CTA's address `a` in the first CTA of its pair.
+__device__ __forceinline__ uint32_t first_of_pair(uint32_t a)
 {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank & ~1u));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
     return r;
 }
 // An arrival on a barrier at a cluster address, after this thread's tensor memory
@@ -132,17 +131,6 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, ui
         : "memory");
 }
 
-// The same to both CTAs of a cluster, at this CTA's offsets of the destination
-// and the barrier.
-__device__ __forceinline__ void load_2d_both(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(
-            dst),
-        "l"(map), "r"(bar), "r"(x), "r"(y), "h"((uint16_t)3)
-        : "memory");
-}
-
 // To this CTA's shared memory, counted on a barrier of either CTA of a pair
 // (`bar` is a cluster address, of first_of_pair).
 __device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z)
@@ -151,18 +139,6 @@ __device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* ma
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
             dst),
         "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
-// The same to the CTAs of `mask`, at this CTA's offset of the destination, counted
-// in the first CTA of each one's pair.
-__device__ __forceinline__ void load_3d_pairs(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
-                                              uint32_t mask)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(
-            dst),
-        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "h"((uint16_t)mask)
         : "memory");
 }
 
@@ -221,20 +197,13 @@ __device__ __forceinline__ void commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// The same on the barriers at this offset of the cluster's CTAs of `mask`.
-template <int kGroup>
-__device__ __forceinline__ void commit_to(uint32_t bar, uint32_t mask)
+// The same, of a pair's products, on the barriers at this offset of both its CTAs.
+__device__ __forceinline__ void commit_pair(uint32_t bar)
 {
-    if constexpr (kGroup == 2)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"((uint16_t)mask)
-            : "memory");
-    else
-        asm volatile(
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"((uint16_t)mask)
-            : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
 }
 
 // Shared memory operand (of a pair: at the same offset in both CTAs), 128-byte
