@@ -6,7 +6,7 @@
 //           tokens y comes from matrix-vector products (ffn_gemv.cu).
 // Backward: plan, split dy, dh, the activation's backward with its encodings,
 //           FP16 copies of x and dy, dx, d_gate_up, d_down.
-#include <mutex>
+#include <cooperative_groups.h>
 
 #include "ffn.cuh"
 
@@ -51,6 +51,7 @@ namespace {
 
 using namespace fp8z1;
 using namespace fp8z1::ffn;
+namespace cg = cooperative_groups;
 
 // The tiles of every expert.  Rows two experts claim (a table that does not
 // ascend) are bounded too: the launch holds at most `most` tiles.
@@ -77,9 +78,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Runs runs, PlanBuffers p, in
         p.start[e] = first;
         p.tokens[e] = (int32_t)min(hi - lo, (int64_t)(last - first) * kRows);
         if (clear) {
-            Peaks c = {};
-            if (from) c = Peaks{from[e].x, from[e].gate, from[e].up, 0, 0, {0, 0, 0}};
-            clear[e] = c;
+            clear[e] = Peaks{from ? from[e].x : 0, 0};
         }
     }
     if (e == n - 1) {
@@ -87,6 +86,20 @@ __global__ void __launch_bounds__(1024) plan_kernel(Runs runs, PlanBuffers p, in
         *p.n_tiles = last;
     }
     const int32_t total = sums[n - 1];
+    // an expert's tiles two by two: half as many pairs as tiles, and half of one more where their number is odd
+    __shared__ int32_t odd_of_warp[32], pair_start[1024];
+    if (p.pairs) {
+        const unsigned odd = __ballot_sync(0xffffffffu, (last - first) & 1);
+        if ((e & 31) == 0) odd_of_warp[e >> 5] = __popc(odd);
+        __syncthreads();
+        if (e < n) {
+            int32_t odds = __popc(odd & ((1u << (e & 31)) - 1));
+            for (int w = 0; w < e >> 5; ++w) odds += odd_of_warp[w];
+            p.pair_start[e] = pair_start[e] = (first + odds) / 2;
+            if (e == n - 1) *p.n_pairs = (last + odds + (last - first & 1)) / 2;
+        }
+        __syncthreads();
+    }
     for (int32_t t = threadIdx.x; t < total; t += 1024) {
         int a = 0, b = n - 1;  // the first expert whose tiles end after t
         while (a < b) {
@@ -98,8 +111,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(Runs runs, PlanBuffers p, in
         }
         int64_t l, h;
         runs.get(a, l, h);
-        const int64_t token0 = l + (int64_t)(t - (a ? sums[a - 1] : 0)) * kRows;
+        const int32_t local = t - (a ? sums[a - 1] : 0);
+        const int64_t token0 = l + (int64_t)local * kRows;
         p.tiles[t] = Tile{a, (int32_t)token0, (int32_t)min(h - token0, (int64_t)kRows), 0};
+        if (p.pairs && local % 2 == 0) p.pairs[pair_start[a] + local / 2] = 2 * t + (t + 1 < sums[a]);
     }
 }
 
@@ -190,7 +205,7 @@ __global__ void __launch_bounds__(256) halves_kernel(Plan plan, const bf16* x, i
     const int r = (int)(warp % kRows);
     if (r >= (t.rows + 15) / 16 * 16) return;  // zeros to the next multiple of 16, which is what is multiplied
     const Peaks p = peaks[t.expert];
-    const Pow2 fx = pow2(x_shift(p)), fd = pow2(dy_shift(p));
+    const Pow2 fx = pow2(peak_shift(p.x)), fd = pow2(peak_shift(p.dy));
     const bf16* sx = x + (int64_t)(t.token0 + r) * ld_x;
     const bf16* sd = dy + (int64_t)(t.token0 + r) * ld_dy;
     const int64_t c0 = (int64_t)blockIdx.y * kRowColumns, c1 = min(c0 + kRowColumns, pitch);
@@ -214,36 +229,45 @@ __global__ void __launch_bounds__(256) halves_kernel(Plan plan, const bf16* x, i
     }
 }
 
-// v as two FP16 numbers, four at a time
-__device__ __forceinline__ void store_halves(__half* hi, __half* lo, const Pow2& f, const float4& v)
+// v times f as two FP16 numbers, four at a time
+__device__ __forceinline__ void store_halves(__half* hi, __half* lo, const float4& f, const float4& v)
 {
-    const float a = f.times(v.x), b = f.times(v.y), c = f.times(v.z), d = f.times(v.w);
+    const float a = f.x * v.x, b = f.y * v.y, c = f.z * v.z, d = f.w * v.w;
     const __half2 h0 = __floats2half2_rn(a, b), h1 = __floats2half2_rn(c, d);
     *reinterpret_cast<uint2*>(hi) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
     const float2 g0 = __half22float2(h0), g1 = __half22float2(h1);
     *reinterpret_cast<uint2*>(lo) = make_uint2(half_pair(a - g0.x, b - g0.y), half_pair(c - g1.x, d - g1.y));
 }
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // dg, du and h of 32 rows x 128 columns: read with lanes along rows (as the
 // products wrote them), turned in shared memory, written with lanes along
 // columns: [dg | du] as FP8 pairs for dx and as FP16 pairs for d_gate_up, h as
-// FP16 pairs for d_down.  Bound by memory, 28 bytes an element: 8192 rows of 2048
-// take 99 us, 4.7 TB/s.
+// FP16 pairs for d_down.  The eight CTAs of two tiles are a cluster: a column's power
+// of two is that of its largest number in all 256 rows.  Bound by memory, 28 bytes an
+// element: 8192 rows of 2048 take 99 us, 4.7 TB/s.
 constexpr int kActPitch = 132;
+constexpr int kActSmem = (3 * 32 * kActPitch + 3 * 128) * 4;
 __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float* gu, const float* dh, int64_t F,
                                                          int64_t rows, Pairs pairs, __half* dgu_hi, __half* dgu_lo,
-                                                         __half* h_hi, __half* h_lo, const Peaks* peaks)
+                                                         __half* h_hi, __half* h_lo, float* factors)
 {
-    extern __shared__ float act[];  // [3][32][kActPitch]
+    extern __shared__ __align__(16) float act[];  // [3][32][kActPitch], then the columns' powers of two
+    __shared__ uint32_t mine[3 * 128];                 // this CTA's largest numbers of the columns (bits)
+    __shared__ __align__(16) uint8_t peaks[8][3 * 128];  // the exponents of every CTA's
     next_may_start();
     after_previous();
-    const int64_t tile = blockIdx.x >> 2;
-    if (tile >= *plan.n_tiles) return;
-    const int quarter = blockIdx.x & 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Tile t = plan.tiles[tile];
-    const int rows_here = min(t.rows - quarter * 32, 32);  // of this CTA's 32
-    if (rows_here <= 0) return;
+    const int64_t pair = blockIdx.x >> 3;
+    if (pair >= *plan.n_pairs) return;  // with the whole cluster
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_arrive();  // this CTA has started: the others may write to it
+    const int rank = (int)cluster.block_rank();
+    const int second = blockIdx.x >> 2 & 1, quarter = blockIdx.x & 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t first_tile = plan.pairs[pair];
+    const int64_t tile = (first_tile >> 1) + second;
+    // of this CTA's 32 rows; it may have none
+    const int rows_here = second && !(first_tile & 1) ? 0 : min(plan.tiles[tile].rows - quarter * 32, 32);
     const bool there = lane < rows_here;
     const int64_t f0 = (int64_t)blockIdx.y * 128;
     const float* pg = gu + (tile * 2 * F + f0) * kRows + quarter * 32 + lane;
@@ -262,13 +286,45 @@ __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float*
         const float e = expf(-fabsf(g)), big = __fdividef(1.0f, 1.0f + e), small = e * big;
         const float s = g < 0.0f ? small : big, rest = g < 0.0f ? big : small, a = g * s;
         float* o = act + lane * kActPitch + c;
-        o[0] = d * u * s * (1.0f + g * rest);
-        o[32 * kActPitch] = d * a;
-        o[64 * kActPitch] = a * u;
+        const float dg = d * u * s * (1.0f + g * rest), du = d * a, h = a * u;
+        o[0] = dg;
+        o[32 * kActPitch] = du;
+        o[64 * kActPitch] = h;
+        const uint32_t p0 = __reduce_max_sync(0xffffffffu, abs_bits(dg)), p1 = __reduce_max_sync(0xffffffffu, abs_bits(du)),
+                       p2 = __reduce_max_sync(0xffffffffu, abs_bits(h));
+        if (lane == 0) mine[c] = p0, mine[128 + c] = p1, mine[256 + c] = p2;
+    }
+    __syncwarp();
+    cluster.barrier_wait();
+    if (lane < 24) {  // the warp's 16 columns of one of the three, to one of the CTAs
+        const int at = lane % 3 * 128 + warp * 16;
+        uint32_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[j] |= mine[at + 4 * j + k] >> 23 << (8 * k);
+        }
+        *reinterpret_cast<uint4*>(cluster.map_shared_rank(&peaks[rank][at], lane / 3)) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    __syncwarp();
+    cluster.sync();
+    float* up = act + 3 * 32 * kActPitch;
+    if (threadIdx.x < 96) {  // four columns of one of the three
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m = __vmaxu4(m, *reinterpret_cast<const uint32_t*>(&peaks[q][threadIdx.x * 4]));
+        const ColumnScale x = column_scale(m & 255), y = column_scale(m >> 8 & 255), z = column_scale(m >> 16 & 255),
+                          w = column_scale(m >> 24);
+        *reinterpret_cast<float4*>(up + threadIdx.x * 4) = make_float4(x.up, y.up, z.up, w.up);
+        if (rank == 0)
+            *reinterpret_cast<float4*>(factors + (pair * 3 + threadIdx.x / 32) * F + f0 + lane * 4) =
+                make_float4(x.down, y.down, z.down, w.down);
     }
     __syncthreads();
-    const Peaks p = peaks[t.expert];
-    const Pow2 fg = pow2(dgu_shift(p)), fh = pow2(h_shift(p));
+    const float4 fg = *reinterpret_cast<const float4*>(up + lane * 4),
+                 fu = *reinterpret_cast<const float4*>(up + 128 + lane * 4),
+                 fh = *reinterpret_cast<const float4*>(up + 256 + lane * 4);
     // zeros to the next multiple of 16, which is what the weight gradients multiply
     for (int r = warp; r < (rows_here + 15) / 16 * 16; r += 8) {
         const int64_t at = tile * kRows + quarter * 32 + r;
@@ -276,7 +332,7 @@ __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float*
         for (int half = 0; half < 2; ++half) {
             const float4 v = *reinterpret_cast<const float4*>(act + (half * 32 + r) * kActPitch + lane * 4);
             const int64_t col = half * F + f0 + lane * 4;
-            store_halves(dgu_hi + at * 2 * F + col, dgu_lo + at * 2 * F + col, fg, v);
+            store_halves(dgu_hi + at * 2 * F + col, dgu_lo + at * 2 * F + col, half ? fu : fg, v);
             if (pairs.hi) {
                 float amax = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
                 amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
@@ -372,7 +428,7 @@ extern "C" int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int6
     if ((st = launch_status()) != FP8Z1_OK ||
         (st = launch_after(split_kernel, row_ctas, 256, 0, s, runs, plan, static_cast<const bf16*>(x), ld_x, d.H, f.x,
                            d.rows(), keep.peaks, false, static_cast<bf16*>(y), ld_y)) != FP8Z1_OK ||
-        (st = launch_gate_up(d, plan, f.x, wgu, f.h, keep.gu, keep.peaks, f.part, s)) != FP8Z1_OK)
+        (st = launch_gate_up(d, plan, f.x, wgu, f.h, keep.gu, f.part, s)) != FP8Z1_OK)
         return st;
     if (few_tokens(d)) return FP8Z1_OK;
     return launch_down(d, plan, f.h, wd, static_cast<bf16*>(y), ld_y, f.part, s);
@@ -418,20 +474,20 @@ extern "C" int fp8z1_ffn_backward(const fp8z1_ffn_dims* dims, const void* dy, in
     if ((st = launch_status()) != FP8Z1_OK ||
         (st = launch_after(split_kernel, row_ctas, 256, 0, s, runs, plan, dyb, ld_dy, d.H, b.dy, d.rows(), b.peaks, true,
                            static_cast<bf16*>(dx), ld_dx)) != FP8Z1_OK ||
-        (st = launch_dh(d, plan, b.dy, wd, b.dh, b.peaks, s)) != FP8Z1_OK)
+        (st = launch_dh(d, plan, b.dy, wd, b.dh, s)) != FP8Z1_OK)
         return st;
     Pairs pairs = b.dgu;
     if (!dx) pairs.hi = nullptr;
-    constexpr int kActSmem = 3 * 32 * kActPitch * 4;
     if (!allow_smem<activation_kernel>(kActSmem)) return FP8Z1_ECUDA;
-    if ((st = launch_after(activation_kernel, dim3((unsigned)(d.tiles() * 4), (unsigned)(d.F / 128)), 256, kActSmem, s, plan,
-                           keep.gu, b.dh, d.F, d.rows(), pairs, b.dgu_hi, b.dgu_lo, b.h_hi, b.h_lo, b.peaks)) != FP8Z1_OK ||
+    if ((st = launch_after<8>(activation_kernel, dim3((unsigned)(d.pairs() * 8), (unsigned)(d.F / 128)), 256, kActSmem, s,
+                              plan, keep.gu, b.dh, d.F, d.rows(), pairs, b.dgu_hi, b.dgu_lo, b.h_hi, b.h_lo,
+                              b.factors)) != FP8Z1_OK ||
         (st = launch_after(halves_kernel, row_ctas, 256, 0, s, plan, xb, ld_x, dyb, ld_dy, d.H, d.Hp(), b.x16, b.dy16,
                            b.peaks)) != FP8Z1_OK)
         return st;
     if (dx && (st = launch_dx(d, plan, b.dgu, wgu, static_cast<bf16*>(dx), ld_dx, s)) != FP8Z1_OK) return st;
-    if ((st = launch_d_gate_up(d, plan, b, b.peaks, d_gate_up, s)) != FP8Z1_OK) return st;
-    return launch_d_down(d, plan, b, b.peaks, d_down, s);
+    if ((st = launch_d_gate_up(d, plan, b, d_gate_up, s)) != FP8Z1_OK) return st;
+    return launch_d_down(d, plan, b, d_down, s);
 }
 
 extern "C" int fp8z1_ffn_timeouts(uint32_t* count)

@@ -25,8 +25,7 @@ struct Tile {
 
 // Per expert: the bits of the largest magnitudes (as non-negative floats).
 struct Peaks {
-    uint32_t x, gate, up, dy, dh;
-    uint32_t pad[3];
+    uint32_t x, dy;
 };
 
 // Which rows belong to whom; written by the plan kernel.
@@ -35,6 +34,10 @@ struct Plan {
     const int32_t* start;   // [experts + 1] first tile of each expert
     const int32_t* tokens;  // [experts] rows of each
     const Tile* tiles;      // [n_tiles]
+    // An expert's tiles two by two, as the weight gradients add them up (backward).
+    const int32_t* n_pairs;
+    const int32_t* pair_start;  // [experts] first pair of each
+    const int32_t* pairs;       // [n_pairs] twice the first tile, and 1 when there is a second
 };
 
 // FP8 pairs: value = (hi + lo) * scale[k / 128][row]
@@ -58,6 +61,7 @@ struct Runs {
 struct Dims {
     int64_t T, H, F, E;
     int64_t tiles() const { return T / kRows + (E < T ? E : T); }  // at most
+    int64_t pairs() const { return (tiles() + (E < tiles() ? E : tiles())) / 2; }  // at most: an odd tile each
     int64_t rows() const { return tiles() * kRows; }
     int64_t Hp() const { return (H + 127) / 128 * 128; }
 };
@@ -79,14 +83,20 @@ struct Cut {
 struct PlanBuffers {
     int32_t *n_tiles, *start, *tokens;
     Tile* tiles;
-    void cut(Cut& c, const Dims& d)
+    int32_t *n_pairs, *pair_start, *pairs;  // NULL in a forward pass
+    void cut(Cut& c, const Dims& d, bool backward)
     {
         n_tiles = c.take<int32_t>(1);
         start = c.take<int32_t>(d.E + 1);
         tokens = c.take<int32_t>(d.E);
         tiles = c.take<Tile>(d.tiles());
+        n_pairs = pair_start = pairs = nullptr;
+        if (!backward) return;
+        n_pairs = c.take<int32_t>(1);
+        pair_start = c.take<int32_t>(d.E);
+        pairs = c.take<int32_t>(d.pairs());
     }
-    Plan plan() const { return Plan{n_tiles, start, tokens, tiles}; }
+    Plan plan() const { return Plan{n_tiles, start, tokens, tiles, n_pairs, pair_start, pairs}; }
 };
 
 inline Pairs cut_pairs(Cut& c, int64_t rows, int64_t pitch)
@@ -100,7 +110,7 @@ inline Pairs cut_pairs(Cut& c, int64_t rows, int64_t pitch)
 }
 
 // What a forward pass keeps: g | u in FP32 as [tile][column of 2F][row of 128]
-// (a warp's 32 rows are consecutive), and each expert's peaks.
+// (a warp's 32 rows are consecutive), and each expert's peak of x.
 struct Saved {
     Peaks* peaks;
     float* gu;
@@ -137,7 +147,7 @@ struct Forward {
     Pairs x, h;
     void cut(Cut& c, const Dims& d)
     {
-        plan.cut(c, d);
+        plan.cut(c, d, false);
         part = c.take<float>(
             std::max<int64_t>({few_tokens(d) ? d.T * d.F : 0, part_floats(d, 2 * d.F, d.H), part_floats(d, d.H, d.F)}));
         x = cut_pairs(c, d.rows(), d.Hp());
@@ -153,9 +163,10 @@ struct Backward {
     __half *x16, *dy16;  // [rows, Hp]
     __half *h_hi, *h_lo;      // [rows, F]
     __half *dgu_hi, *dgu_lo;  // [rows, 2F]
+    float* factors;           // [pairs of tiles][3F], of the columns of dg, du, h: see column_scale
     void cut(Cut& c, const Dims& d)
     {
-        plan.cut(c, d);
+        plan.cut(c, d, true);
         peaks = c.take<Peaks>(d.E);
         dy = cut_pairs(c, d.rows(), d.Hp());
         dgu = cut_pairs(c, d.rows(), 2 * d.F);
@@ -166,6 +177,7 @@ struct Backward {
         h_lo = c.take<__half>(d.rows() * d.F);
         dgu_hi = c.take<__half>(d.rows() * 2 * d.F);
         dgu_lo = c.take<__half>(d.rows() * 2 * d.F);
+        factors = c.take<float>(d.pairs() * 3 * d.F);
     }
 };
 
@@ -226,31 +238,41 @@ __device__ __forceinline__ Pow2 pow2(int k)
 // floor(log2) of a positive float's bits (-127 for 0 and subnormals, 128 for inf)
 __device__ __forceinline__ int exponent(uint32_t bits) { return (int)(bits >> 23) - 127; }
 
-// The powers of two that bring an expert's FP16 operands below 2^15.
-//   |x| < 2^(ex + 1);  |dg| <= 1.1 |dh u| and |du| <= |dh g|;  |h| <= |g u|.
-__device__ __forceinline__ int x_shift(const Peaks& p) { return 14 - exponent(p.x); }
-__device__ __forceinline__ int dy_shift(const Peaks& p) { return 14 - exponent(p.dy); }
-__device__ __forceinline__ int dgu_shift(const Peaks& p)
+// The FP16 operands of the weight gradients lie below 2^15.  x and dy take one power
+// of two for an expert: 2^shift to encode, 2^exponent to decode numbers of 2^14.
+__device__ __forceinline__ int peak_exponent(uint32_t bits) { return max(exponent(bits), -126); }
+__device__ __forceinline__ int peak_shift(uint32_t bits) { return 14 - peak_exponent(bits); }
+__device__ __forceinline__ float peak_factor(uint32_t bits)
 {
-    return 12 - exponent(p.dh) - max(exponent(p.gate), exponent(p.up));
+    return __uint_as_float((uint32_t)(127 + min(peak_exponent(bits), 127)) << 23);
 }
-__device__ __forceinline__ int h_shift(const Peaks& p) { return 13 - exponent(p.gate) - exponent(p.up); }
+// dg, du and h take one for every column of a pair of tiles, from its largest number there: an
+// element keeps 22 bits, or what lies above 2^-40 of that number, whatever the other
+// columns hold.  `down` brings products with numbers of 2^14 back to numbers of 1.
+struct ColumnScale {
+    float up, down;
+};
+__device__ __forceinline__ ColumnScale column_scale(uint32_t exponent)  // the bits of it, 127 for [1, 2)
+{
+    const int shift = min(141 - (int)exponent, 112);
+    return ColumnScale{__uint_as_float((uint32_t)(127 + shift) << 23), __uint_as_float((uint32_t)(113 - shift) << 23)};
+}
 
 // ---- launches (each returns a status) -------------------------------------------
 
 // The FP8 products of one K-blocked shape; see ffn_gemm.cu.
-int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w, const Pairs& h, float* gu,
-                   Peaks* peaks, float* part, cudaStream_t s);
+int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w, const Pairs& h, float* gu, float* part,
+                   cudaStream_t s);
 int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, float* part,
                 cudaStream_t s);
-int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, float* dh, Peaks* peaks, cudaStream_t s);
+int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, float* dh, cudaStream_t s);
 int launch_dx(const Dims& d, const Plan& p, const Pairs& dgu, const Weight& w, bf16* dx, int64_t ld, cudaStream_t s);
 // y of a few tokens (h: FP32 [T, F]); see ffn_gemv.cu.
 int launch_gemv(const Dims& d, const Runs& runs, const bf16* x, int64_t ld_x, const Weight& wgu, const Weight& wd, float* h,
                 bf16* y, int64_t ld_y, cudaStream_t s);
 // The weight gradients; see ffn_wgrad.cu.
-int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
-int launch_d_down(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s);
+int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, float* out, cudaStream_t s);
+int launch_d_down(const Dims& d, const Plan& p, const Backward& b, float* out, cudaStream_t s);
 
 // A pass is a chain of short kernels: each may start while the one before it ends
 // (its launch and set-up cost 2 to 3 us otherwise) and touches memory only when
@@ -258,20 +280,23 @@ int launch_d_down(const Dims& d, const Plan& p, const Backward& b, const Peaks* 
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Launches a kernel that calls both, right behind another of the pass.
-template <class... A, class... P>
+// Launches a kernel that calls both, right behind another of the pass, in clusters of kCluster CTAs.
+template <int kCluster = 1, class... A, class... P>
 int launch_after(void (*kernel)(A...), dim3 grid, int threads, uint32_t smem, cudaStream_t s, const P&... args)
 {
     cudaLaunchConfig_t c = {};
-    cudaLaunchAttribute at = {};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kCluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     c.gridDim = grid;
     c.blockDim = dim3((unsigned)threads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
-    c.attrs = &at;
-    c.numAttrs = 1;
+    c.attrs = at;
+    c.numAttrs = kCluster > 1 ? 2 : 1;
     count_launch();
     if (cudaLaunchKernelEx(&c, kernel, A(args)...) != cudaSuccess) {
         cudaGetLastError();

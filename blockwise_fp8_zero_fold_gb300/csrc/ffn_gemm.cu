@@ -71,7 +71,6 @@ struct Args {
     Pairs h;               // kGateUp
     float* gu;             // kGateUp (NULL: not kept), [tile][2F][128]
     float* dh;             // kDh, [tile][F][128]
-    Peaks* peaks;          // kGateUp (NULL: not kept), kDh
     bf16* out;             // kDown, kDx
     int64_t ld;
     float* part;           // kPart, [splits, rows, N]
@@ -338,7 +337,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 }
             if constexpr (kMode == kGateUp) {
                 const int n0 = w.n * 128 + group * 32;
-                float amax = 0.0f, top_g = 0.0f, top_u = 0.0f;
+                float amax = 0.0f;
                 if (a.gu) {
                     float* g = a.gu + ((int64_t)w.tile * 2 * a.F + n0) * kRows + row;
                     float* u = g + a.F * kRows;
@@ -346,15 +345,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     for (int j = 0; j < 32; ++j) {
                         __stcs(g + j * kRows, sum[0][j]);
                         __stcs(u + j * kRows, sum[1][j]);
-                        top_g = fmaxf(top_g, fabsf(sum[0][j]));
-                        top_u = fmaxf(top_u, fabsf(sum[1][j]));
-                    }
-                    if (row >= w.rows) top_g = top_u = 0.0f;
-                    const uint32_t pg = __reduce_max_sync(0xffffffffu, abs_bits(top_g));
-                    const uint32_t pu = __reduce_max_sync(0xffffffffu, abs_bits(top_u));
-                    if (lane == 0) {
-                        atomicMax(&a.peaks[w.expert].gate, pg);
-                        atomicMax(&a.peaks[w.expert].up, pu);
                     }
                 }
 #pragma unroll
@@ -405,20 +395,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                         }
                     }
             } else if constexpr (kMode == kDh) {
-                float top = 0.0f;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int64_t n0 = (int64_t)w.n * kCols + c * 128 + group * 32;
                     if (n0 >= a.N) continue;  // F is a multiple of 128: a chunk is in or out whole
                     float* o = a.dh + ((int64_t)w.tile * a.F + n0) * kRows + row;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        __stcs(o + j * kRows, sum[c][j]);
-                        top = fmaxf(top, fabsf(sum[c][j]));
-                    }
+                    for (int j = 0; j < 32; ++j) __stcs(o + j * kRows, sum[c][j]);
                 }
-                const uint32_t p = __reduce_max_sync(0xffffffffu, abs_bits(row < w.rows ? top : 0.0f));
-                if (lane == 0) atomicMax(&a.peaks[w.expert].dh, p);
             } else {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -475,7 +459,7 @@ __global__ void __launch_bounds__(256) join_kernel(Plan plan, const float* part,
 // h of the partial sums of gate and up, as pairs (a warp 128 columns of a row), and
 // what the gate_up product's own epilogue keeps.
 __global__ void __launch_bounds__(256) join_gate_kernel(Plan plan, const float* part, int64_t rows, int64_t F, int splits,
-                                                        Pairs h, float* gu, Peaks* peaks)
+                                                        Pairs h, float* gu)
 {
     next_may_start();
     after_previous();
@@ -493,13 +477,11 @@ __global__ void __launch_bounds__(256) join_gate_kernel(Plan plan, const float* 
         u.x += b.x, u.y += b.y, u.z += b.z, u.w += b.w;
     }
     const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
-    float v[4], amax = 0.0f, top_g = 0.0f, top_u = 0.0f;
+    float v[4], amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         v[j] = silu(gs[j]) * us[j];
         amax = fmaxf(amax, fabsf(v[j]));
-        top_g = fmaxf(top_g, fabsf(gs[j]));
-        top_u = fmaxf(top_u, fabsf(us[j]));
         if (gu) {
             float* o = gu + ((int64_t)(blockIdx.x / kRows) * 2 * F + n + j) * kRows + r;
             o[0] = gs[j];
@@ -513,14 +495,6 @@ __global__ void __launch_bounds__(256) join_gate_kernel(Plan plan, const float* 
     *reinterpret_cast<uint32_t*>(h.hi + (int64_t)blockIdx.x * h.pitch + n) = h0 | h1 << 16;
     *reinterpret_cast<uint32_t*>(h.lo + (int64_t)blockIdx.x * h.pitch + n) = l0 | l1 << 16;
     if (lane == 0) h.scale[block * rows + blockIdx.x] = ps.down;
-    if (gu) {
-        const uint32_t pg = __reduce_max_sync(0xffffffffu, abs_bits(top_g));
-        const uint32_t pu = __reduce_max_sync(0xffffffffu, abs_bits(top_u));
-        if (lane == 0) {
-            atomicMax(&peaks[t.expert].gate, pg);
-            atomicMax(&peaks[t.expert].up, pu);
-        }
-    }
 }
 
 template <int kMode>
@@ -552,15 +526,14 @@ int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a,
 
 }  // namespace
 
-int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w, const Pairs& h, float* gu,
-                   Peaks* peaks, float* part, cudaStream_t s)
+int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w, const Pairs& h, float* gu, float* part,
+                   cudaStream_t s)
 {
     Args a = {};
     a.plan = p;
     a.N = d.F;
     a.h = h;
     a.gu = gu;
-    a.peaks = peaks;
     a.splits = k_splits(d, 2 * d.F, d.H);
     if (a.splits == 1) return launch<kGateUp>(d, x, d.H, w, a, s);
     a.N = 2 * d.F;
@@ -568,7 +541,7 @@ int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w
     const int st = launch<kPart>(d, x, d.H, w, a, s);
     if (st != FP8Z1_OK) return st;
     return launch_after(join_gate_kernel, dim3((unsigned)d.rows(), (unsigned)ceil_div(d.F, 1024)), 256, 0, s, p, part,
-                        d.rows(), d.F, a.splits, h, gu, peaks);
+                        d.rows(), d.F, a.splits, h, gu);
 }
 
 int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, bf16* y, int64_t ld, float* part,
@@ -588,13 +561,12 @@ int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, b
                         d.H, a.splits, y, ld);
 }
 
-int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, float* dh, Peaks* peaks, cudaStream_t s)
+int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, float* dh, cudaStream_t s)
 {
     Args a = {};
     a.plan = p;
     a.N = d.F;
     a.dh = dh;
-    a.peaks = peaks;
     return launch<kDh>(d, dy, d.H, w, a, s);
 }
 

@@ -4,9 +4,11 @@
 //
 // in FP32 accuracy.  x and dy are BF16 values and fit FP16 exactly (8
 // significant bits; every expert's operand is brought below 2^15 by one power
-// of two, so FP16's 40 binades hold everything down to 2^-40 of the largest);
+// of two, and FP16 holds such a number whole down to 2^-32 of the largest);
 // dgu and h are FP32 and enter as two FP16 numbers, hi = f16(v), lo = f16(v -
-// hi), 22 bits.  Two FP16 products with FP32 accumulators then cost twice one
+// hi), 22 bits, every column of two tiles' 256 rows at its own power of two, so
+// that a column of small numbers (a gate that is shut) keeps its bits beside
+// large ones.  Two FP16 products with FP32 accumulators then cost twice one
 // BF16 product and keep FP32's accuracy; one BF16 product would lose 16 bits
 // of it, and the optimizer's grads are FP32.
 //
@@ -14,8 +16,8 @@
 // operand (the lanes of its tensor memory), and the other operand's 256 columns
 // half and half.  Both operands are row-major over tokens, that is M- and
 // N-major to the tensor cores.  The pipeline is ffn_gemm.cu's: TMA steps of 64
-// token rows (48 KB a CTA), products into two accumulators, each 256 rows added
-// up in registers.  The last step issues only the 16-row products that hold
+// token rows (48 KB a CTA), products into two accumulators, each two tiles' 256
+// rows scaled and added up in registers.  The last step issues only the 16-row products that hold
 // rows; rows past an expert's end are zeros.  A stage is 48 KB for 0.54 us of
 // products, more than L2 delivers to every SM at once.
 //
@@ -35,10 +37,12 @@ __device__ unsigned g_timeouts;
 constexpr int kCols = 256;
 constexpr int kStep = 64;  // token rows of a stage
 constexpr int kStages = 4;
-// Stages added up in tensor memory before they go to the registers' sums.  Its adds
-// do not round to nearest: sums of 256 rows there leave 7e-7 of the gradient's norm,
-// of 512 1.3e-6 at the same speed.
-constexpr int kAdd = 4;
+// Stages added up in tensor memory before they go to the registers' sums: two tiles' rows,
+// which share their columns' powers of two.  (Tensor memory's adds do not round to
+// nearest: sums of 256 rows there leave 7e-7 of the gradient's norm, of 512 1.3e-6.  Powers
+// of two and sums of 128 rows let the products run only 256 rows ahead of a tile's stores:
+// 300 tokens of 4096 x 14336 then took 290 + 96 us.)
+constexpr int kAdd = 2 * kRows / kStep;
 constexpr int kThreads = 640;  // 4 warps that feed, 16 that add up
 constexpr uint32_t kChunk = 64 * kStep * 2;     // bytes of 64 columns of a stage
 constexpr uint32_t kStageBytes = 6 * kChunk;    // hi: 2 chunks, lo: 2, half of the other operand: 2
@@ -46,7 +50,9 @@ constexpr uint32_t kSmem = kStages * kStageBytes + 16 * 2048 + 1024 + 256;
 
 struct Args {
     Plan plan;
-    const Peaks* peaks;
+    const uint32_t* peaks;  // of x or dy, a Peaks apart
+    const float* factors;   // of the two-term operand's columns, [pairs of tiles][pitch]
+    int64_t pitch;
     float* out;        // kTransposed: [E, N, M]
     int64_t M, N;      // columns of the two-term operand, of the other
     int32_t m_tiles, n_tiles, experts;
@@ -160,9 +166,10 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
             const int e = (int)(i / per), local = (int)(i - e * per);
             const int m = local % m_pairs * 2 + sub, n = local / m_pairs;
             const int tokens = a.plan.tokens[e];
-            const Peaks p = a.peaks[e];
-            const Pow2 f = pow2(kTransposed ? -(x_shift(p) + dgu_shift(p)) : -(dy_shift(p) + h_shift(p)));
-            const uint64_t fa = pair(f.a, f.a);
+            const float* factor = a.factors + a.plan.pair_start[e] * a.pitch + m * 128 + row;
+            // plain loads: they stay ahead of the waits
+            float next = tokens && m < a.m_tiles ? *factor : 0.0f;
+            const uint32_t peak = a.peaks[e * (int)(sizeof(Peaks) / 4)];
             uint64_t sums2[2][16];  // pairs of columns
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -172,6 +179,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                 ok = __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc.slot, acc.phase));
                 if (!ok) break;
                 fence_after();
+                const uint64_t f = pair(next, next);
+                if (t0 + kAdd * kStep < tokens && m < a.m_tiles) next = *(factor += a.pitch);
                 const uint32_t t = tmem + acc.slot * kCols + lanes + group * 32;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -186,25 +195,21 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         sums2[q / 2][q % 2 * 8 + j] =
-                            fma_pair(pair(r[2 * j], r[2 * j + 1]), fa, sums2[q / 2][q % 2 * 8 + j]);
+                            fma_pair(pair(r[2 * j], r[2 * j + 1]), f, sums2[q / 2][q % 2 * 8 + j]);
                 }
             }
             if (!ok) break;
             if (m >= a.m_tiles) continue;  // an odd last tile's other half
+            const float last = peak_factor(peak);
             float sum[2][32];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float2 v = unpair(sums2[c][j]);
-                    sum[c][2 * j] = v.x;
-                    sum[c][2 * j + 1] = v.y;
+                    sum[c][2 * j] = v.x * last;
+                    sum[c][2 * j + 1] = v.y * last;
                 }
-            if (f.b != 1.0f)  // a power of two beyond FP32's exponents
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) sum[c][j] *= f.b;
             if constexpr (kTransposed) {
                 // lanes are consecutive columns of the gradient
 #pragma unroll
@@ -266,8 +271,8 @@ int map_f16(CUtensorMap* map, const __half* p, int64_t rows, int64_t pitch)
 }
 
 template <bool kTransposed>
-int launch(const Dims& d, const Plan& p, const Peaks* peaks, const __half* hi, const __half* lo, int64_t M,
-           const __half* b, float* out, cudaStream_t s)
+int launch(const Dims& d, const Plan& p, const uint32_t* peaks, const float* factors, const __half* hi, const __half* lo,
+           int64_t M, const __half* b, float* out, cudaStream_t s)
 {
     CUtensorMap mh, ml, mb, mo;
     const uint64_t odims[3] = {(uint64_t)d.H, (uint64_t)d.F, (uint64_t)d.E},
@@ -283,6 +288,8 @@ int launch(const Dims& d, const Plan& p, const Peaks* peaks, const __half* hi, c
     Args a = {};
     a.plan = p;
     a.peaks = peaks;
+    a.factors = factors;
+    a.pitch = 3 * d.F;
     a.out = out;
     a.M = M;
     a.N = d.H;
@@ -295,14 +302,14 @@ int launch(const Dims& d, const Plan& p, const Peaks* peaks, const __half* hi, c
 
 }  // namespace
 
-int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s)
+int launch_d_gate_up(const Dims& d, const Plan& p, const Backward& b, float* out, cudaStream_t s)
 {
-    return launch<true>(d, p, peaks, b.dgu_hi, b.dgu_lo, 2 * d.F, b.x16, out, s);
+    return launch<true>(d, p, &b.peaks->x, b.factors, b.dgu_hi, b.dgu_lo, 2 * d.F, b.x16, out, s);
 }
 
-int launch_d_down(const Dims& d, const Plan& p, const Backward& b, const Peaks* peaks, float* out, cudaStream_t s)
+int launch_d_down(const Dims& d, const Plan& p, const Backward& b, float* out, cudaStream_t s)
 {
-    return launch<false>(d, p, peaks, b.h_hi, b.h_lo, d.F, b.dy16, out, s);
+    return launch<false>(d, p, &b.peaks->dy, b.factors + 2 * d.F, b.h_hi, b.h_lo, d.F, b.dy16, out, s);
 }
 
 int take_timeouts_wgrad(unsigned* n)

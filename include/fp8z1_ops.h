@@ -104,7 +104,9 @@ int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int64_t ld_x, c
  *   d_gate_up = x^T [dg | du],  d_down = h^T dy,  FP32 [E, R, C] row-major: the
  * optimizer's grads.  Every element is written (zeros for an expert without
  * tokens; dx = 0 in rows of no expert).  dy, dx as x above; d_gate_up and
- * d_down 16-byte aligned.  The weight gradients carry FP32 accuracy.
+ * d_down 16-byte aligned.  The weight gradients carry FP32 accuracy, every column
+ * of d_gate_up and row of d_down relative to its own size; of x and dy, elements
+ * below 2^-32 of the expert's largest lose bits there.
  * Errors: EINVAL, EALIGN, ECUDA. */
 int fp8z1_ffn_backward(const fp8z1_ffn_dims* dims, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
                        const int32_t* d_offsets, const uint8_t* gate_up, const float* gate_up_scale,
