@@ -166,7 +166,16 @@ __global__ void __launch_bounds__(256) split_kernel(Runs runs, Plan plan, const 
         float amax = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
-        top = fmaxf(top, amax);
+        // the expert's peak is that of its finite numbers: an infinity stays one in FP16, the others keep their bits
+        if (amax == INFINITY) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (fabsf(f[j].x) < INFINITY) top = fmaxf(top, fabsf(f[j].x));
+                if (fabsf(f[j].y) < INFINITY) top = fmaxf(top, fabsf(f[j].y));
+            }
+        } else {
+            top = fmaxf(top, amax);
+        }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if (c >= out.pitch) continue;

@@ -23,7 +23,7 @@ struct Tile {
     int32_t expert, token0, rows, pad;
 };
 
-// Per expert: the bits of the largest magnitudes (as non-negative floats).
+// Per expert: the bits of the largest finite magnitudes (as non-negative floats).
 struct Peaks {
     uint32_t x, dy;
 };
