@@ -8,6 +8,8 @@
 //           FP16 copies of x and dy, dx, d_gate_up, d_down.
 #include <cooperative_groups.h>
 
+#include <mutex>
+
 #include "ffn.cuh"
 
 namespace fp8z1 {
@@ -502,11 +504,31 @@ extern "C" int fp8z1_ffn_backward(const fp8z1_ffn_dims* dims, const void* dy, in
 extern "C" int fp8z1_ffn_timeouts(uint32_t* count)
 {
     if (!count) return FP8Z1_EINVAL;
+    // the devices' counters only grow, so that no count is lost between a read and a reset
+    static std::mutex lock;
+    static uint32_t seen[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return FP8Z1_ECUDA;
+    std::lock_guard<std::mutex> hold(lock);
     unsigned a = 0, b = 0;
-    const int st = take_timeouts_gemm(&a);
-    if (st != FP8Z1_OK) return st;
-    const int st2 = take_timeouts_wgrad(&b);
-    if (st2 != FP8Z1_OK) return st2;
-    *count = a + b;
+    int st = read_timeouts_gemm(&a);
+    if (st == FP8Z1_OK) st = read_timeouts_wgrad(&b);
+    if (st != FP8Z1_OK) {
+        cudaGetLastError();
+        return st;
+    }
+    *count = a + b - seen[dev];
+    seen[dev] = a + b;
     return FP8Z1_OK;
+}
+
+extern "C" int fp8z1_checked_ffn_stall(uint32_t kernels)
+{
+#if FP8Z1_CHECKED
+    const int st = stall_gemm(kernels & 31);
+    return st == FP8Z1_OK ? stall_wgrad(kernels >> 5) : st;
+#else
+    (void)kernels;
+    return FP8Z1_EINVAL;
+#endif
 }

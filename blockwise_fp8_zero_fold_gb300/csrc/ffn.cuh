@@ -352,9 +352,13 @@ int tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void*
                const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // Waits that ran out in each translation unit's kernels on the current device
-// since the last call (synchronous).  Returns a status.
-int take_timeouts_gemm(unsigned* n);
-int take_timeouts_wgrad(unsigned* n);
+// (synchronous).  Returns a status.
+int read_timeouts_gemm(unsigned* n);
+int read_timeouts_wgrad(unsigned* n);
+#if FP8Z1_CHECKED
+int stall_gemm(unsigned kernels);
+int stall_wgrad(unsigned kernels);
+#endif
 
 }  // namespace ffn
 }  // namespace fp8z1

@@ -42,6 +42,9 @@ namespace {
 using namespace tc;
 
 __device__ unsigned g_timeouts;
+#if FP8Z1_CHECKED
+__device__ unsigned g_stall;  // bit kMode: that kernel's first CTA does not announce its first sums
+#endif
 
 // kPart: gate_up or down with K split over several CTAs, FP32 partial sums
 enum Mode { kGateUp, kDown, kDh, kDx, kPart };
@@ -249,6 +252,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                             mma_f8(d, da, db, idesc[t], t + k > 0);
                         }
                     commit(bar_empty + 8 * turn.slot);
+#if FP8Z1_CHECKED
+                    if (g_stall >> kMode & 1 && blockIdx.x == 0 && i == i0 && kb == w.k0) continue;
+#endif
                     commit(bar_acc + 8 * acc.slot);
                 }
             }
@@ -286,7 +292,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
         Turn<2> acc;
         Turn<4> turn;
         int parity = 0;
-        for (int64_t i = i0; i < total && ok; i += step) {
+        bool together = true;  // kGateUp: with the other warps of the row
+        for (int64_t i = i0; i < total; i += step) {
             const Work w = work_at(a, i);
             const int64_t at = (int64_t)w.tile * kRows + row;  // row of the internal buffers
             uint64_t sums2[2][16];  // pairs of columns
@@ -296,8 +303,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 for (int j = 0; j < 16; ++j) sums2[c][j] = 0;
             for (int kb = w.k0; kb < w.k1; ++kb, acc.next(), turn.next()) {
                 // a warp's lanes agree on the outcome: the loads below are warp-wide
-                ok = __all_sync(0xffffffffu, bar_wait(bar_factors + 8 * turn.slot, turn.phase) &&
-                                                 bar_wait(bar_acc + 8 * acc.slot, acc.phase));
+                ok = ok && __all_sync(0xffffffffu, bar_wait(bar_factors + 8 * turn.slot, turn.phase) &&
+                                                       bar_wait(bar_acc + 8 * acc.slot, acc.phase));
                 if (!ok) break;
                 fence_after();
                 float f0, f1;
@@ -325,7 +332,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                             fma_pair(pair(r[2 * j], r[2 * j + 1]), f[q / 2], sums2[q / 2][q % 2 * 8 + j]);
                 }
             }
-            if (!ok) break;
+            // a wait ran out: this tile and the CTA's further ones are NaN, which reaches all that is made of them
+            if (!ok)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sums2[j / 16][j % 16] = pair(NAN, NAN);
             float sum[2][32];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -353,13 +363,19 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     amax = fmaxf(amax, fabsf(sum[0][j]));
                 }
                 // the largest of the row's 128 columns, 32 each of the four groups
-                exchange[(parity * 4 + group) * 128 + row] = amax;
-                bar_arrive(bar_exchange);
-                ok = __all_sync(0xffffffffu, bar_wait(bar_exchange, parity));
-                if (!ok) break;
+                if (together) {
+                    exchange[(parity * 4 + group) * 128 + row] = amax;
+                    bar_arrive(bar_exchange);
+                    together = __all_sync(0xffffffffu, bar_wait(bar_exchange, parity));
+                }
+                if (together) {
 #pragma unroll
-                for (int o = 0; o < 4; ++o) amax = fmaxf(amax, exchange[(parity * 4 + o) * 128 + row]);
-                parity ^= 1;
+                    for (int o = 0; o < 4; ++o) amax = fmaxf(amax, exchange[(parity * 4 + o) * 128 + row]);
+                    parity ^= 1;
+                } else {
+                    ok = false;
+                    amax = INFINITY;  // the row's 128 numbers become NaN
+                }
                 const PairScale ps = pair_scale(amax);
                 if (group == 0) a.h.scale[(int64_t)w.n * a.rows + at] = ps.down;
                 uint4 hi[2], lo[2];
@@ -580,13 +596,17 @@ int launch_dx(const Dims& d, const Plan& p, const Pairs& dgu, const Weight& w, b
     return launch<kDx>(d, dgu, 2 * d.F, w, a, s);
 }
 
-int take_timeouts_gemm(unsigned* n)
+int read_timeouts_gemm(unsigned* n)
 {
-    const unsigned zero = 0;
-    return cudaMemcpyFromSymbol(n, g_timeouts, 4) == cudaSuccess && cudaMemcpyToSymbol(g_timeouts, &zero, 4) == cudaSuccess
-               ? FP8Z1_OK
-               : FP8Z1_ECUDA;
+    return cudaMemcpyFromSymbol(n, g_timeouts, 4) == cudaSuccess ? FP8Z1_OK : FP8Z1_ECUDA;
 }
+
+#if FP8Z1_CHECKED
+int stall_gemm(unsigned kernels)
+{
+    return cudaMemcpyToSymbol(g_stall, &kernels, 4) == cudaSuccess ? FP8Z1_OK : FP8Z1_ECUDA;
+}
+#endif
 
 }  // namespace ffn
 }  // namespace fp8z1

@@ -33,6 +33,9 @@ namespace {
 using namespace tc;
 
 __device__ unsigned g_timeouts;
+#if FP8Z1_CHECKED
+__device__ unsigned g_stall;  // bit kTransposed: that kernel's first pair does not announce its first sums
+#endif
 
 constexpr int kCols = 256;
 constexpr int kStep = 64;  // token rows of a stage
@@ -151,6 +154,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                         }
                         commit_pair(bar_empty + 8 * turn.slot);
                     }
+#if FP8Z1_CHECKED
+                    if (g_stall >> kTransposed & 1 && blockIdx.x == 0 && i == i0 && t0 == 0) continue;
+#endif
                     if (ok) commit_pair(bar_acc + 8 * acc.slot);
                 }
             }
@@ -162,7 +168,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
         const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16, mine = staging + (warp - 4) * 2048;
         Turn<2> acc;
-        for (int64_t i = i0; i < total && ok; i += step) {
+        for (int64_t i = i0; i < total; i += step) {
             const int e = (int)(i / per), local = (int)(i - e * per);
             const int m = local % m_pairs * 2 + sub, n = local / m_pairs;
             const int tokens = a.plan.tokens[e];
@@ -176,7 +182,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
 #pragma unroll
                 for (int j = 0; j < 16; ++j) sums2[c][j] = 0;
             for (int t0 = 0; t0 < tokens; t0 += kAdd * kStep, acc.next()) {
-                ok = __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc.slot, acc.phase));
+                ok = ok && __all_sync(0xffffffffu, bar_wait(bar_acc + 8 * acc.slot, acc.phase));
                 if (!ok) break;
                 fence_after();
                 const uint64_t f = pair(next, next);
@@ -198,7 +204,10 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                             fma_pair(pair(r[2 * j], r[2 * j + 1]), f, sums2[q / 2][q % 2 * 8 + j]);
                 }
             }
-            if (!ok) break;
+            // a wait ran out: this tile and the pair's further ones are NaN
+            if (!ok)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sums2[j / 16][j % 16] = pair(NAN, NAN);
             if (m >= a.m_tiles) continue;  // an odd last tile's other half
             const float last = peak_factor(peak);
             float sum[2][32];
@@ -312,13 +321,17 @@ int launch_d_down(const Dims& d, const Plan& p, const Backward& b, float* out, c
     return launch<false>(d, p, &b.peaks->dy, b.factors + 2 * d.F, b.h_hi, b.h_lo, d.F, b.dy16, out, s);
 }
 
-int take_timeouts_wgrad(unsigned* n)
+int read_timeouts_wgrad(unsigned* n)
 {
-    const unsigned zero = 0;
-    return cudaMemcpyFromSymbol(n, g_timeouts, 4) == cudaSuccess && cudaMemcpyToSymbol(g_timeouts, &zero, 4) == cudaSuccess
-               ? FP8Z1_OK
-               : FP8Z1_ECUDA;
+    return cudaMemcpyFromSymbol(n, g_timeouts, 4) == cudaSuccess ? FP8Z1_OK : FP8Z1_ECUDA;
 }
+
+#if FP8Z1_CHECKED
+int stall_wgrad(unsigned kernels)
+{
+    return cudaMemcpyToSymbol(g_stall, &kernels, 4) == cudaSuccess ? FP8Z1_OK : FP8Z1_ECUDA;
+}
+#endif
 
 }  // namespace ffn
 }  // namespace fp8z1

@@ -50,18 +50,25 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
-// Every wait ends: after four seconds it gives up and returns false.  Its
-// kernel then drains its own copies, frees its tensor memory and returns.
+// Every wait ends: after kWaitNs, and kWaitTries of up to kSuspendNs each (the clock
+// goes on while a process is paused or its context switched out, the tries do not), it
+// gives up and returns false.  A warp that adds up then stores NaN for what it could
+// not finish; the others drain their own copies, free tensor memory and return.
+#if FP8Z1_CHECKED
+constexpr uint64_t kWaitNs = 200000000ull;
+constexpr int kWaitTries = 5000;
+#else
 constexpr uint64_t kWaitNs = 4000000000ull;
+constexpr int kWaitTries = 100000;
+#endif
 
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity)
 {
     if (bar_try(bar, parity)) return true;
     const uint64_t t0 = now_ns();
-    for (;;) {
-        for (int i = 0; i < 64; ++i)
-            if (bar_try(bar, parity)) return true;
-        if (now_ns() - t0 > kWaitNs) return false;
+    for (int tries = 1;; ++tries) {
+        if (bar_try(bar, parity)) return true;
+        if (tries >= kWaitTries && tries % 64 == 0 && now_ns() - t0 > kWaitNs) return false;
     }
 }
 

@@ -146,6 +146,7 @@ _SIGS = {
     "fp8z1_ffn_backward": (C.c_int, [C.POINTER(fp8z1_ffn_dims), _P, C.c_int64, _P, C.c_int64, _P, _P, _P, _P, _P, _P,
                                      _P, C.c_int64, _P, _P, _P, _P]),
     "fp8z1_ffn_timeouts": (C.c_int, [C.POINTER(C.c_uint32)]),
+    "fp8z1_checked_ffn_stall": (C.c_int, [C.c_uint32]),
     "fp8z1_distill": (C.c_int, [_P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, _P, _P, C.c_int64, C.c_float, _P, _P,
                                 _P, C.c_int64, _P]),
     "fp8z1_strerror": (C.c_char_p, [C.c_int]),
@@ -595,6 +596,12 @@ def fp8z1_ffn_timeouts() -> int:
     n = C.c_uint32()
     _check(lib().fp8z1_ffn_timeouts(C.byref(n)), "fp8z1_ffn_timeouts")
     return n.value
+
+
+def fp8z1_checked_ffn_stall(kernels: int):
+    """Test hook of the checked library: these kernels' first CTA leaves its
+    first sums unannounced (0: none does)."""
+    _check(lib().fp8z1_checked_ffn_stall(kernels), "fp8z1_checked_ffn_stall")
 
 
 def fp8z1_distill(logits, type_: int, ld: int, rows: int, vocab: int, teacher_ids, teacher_logits, top: int,

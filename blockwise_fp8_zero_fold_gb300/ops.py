@@ -18,7 +18,9 @@ that is not current, the outputs and workspaces are allocated as that stream's
 and the outputs marked as used on the current one too; the order of the two
 streams, and the inputs' memory until the work is done, are the caller's to
 see to.  Tensors that do not fit raise ValueError, what the library refuses
-raises Fp8z1Error.
+raises Fp8z1Error.  Should a wait between the feed-forward kernels' warps ever
+run out, what it belongs to is NaN (``fp8z1.fp8z1_ffn_timeouts`` counts them);
+the optimizer skips a step with such gradients.
 """
 from __future__ import annotations
 

@@ -114,11 +114,20 @@ int fp8z1_ffn_backward(const fp8z1_ffn_dims* dims, const void* dy, int64_t ld_dy
                        float* d_gate_up, float* d_down, void* workspace, void* stream);
 
 /* The feed-forward kernels' warps wait for one another on barriers in shared
- * memory, four seconds at most: a wait that runs out ends its CTA, whose results
- * are then incomplete.  Reads and clears the number of threads that gave up on
- * the current device since the last call (synchronous; 0 in all normal use).
- * Errors: EINVAL (null), ECUDA. */
+ * memory, and every wait ends: one that has not been answered after four seconds
+ * and 100000 tries (a paused process does not run out of tries) gives up, and what
+ * its CTA could not finish is NaN, in y, dx, the weight gradients or `saved`; a
+ * NaN gradient sets the step's found_inf.  Reads and clears the number of threads
+ * that gave up on the current device since the last call (synchronous; 0 in all
+ * normal use).  Errors: EINVAL (null), ECUDA. */
 int fp8z1_ffn_timeouts(uint32_t* count);
+
+/* Test hook of a checked build (whose waits give up after 0.2 seconds): from the
+ * next call on, the first CTA of the kernels of `kernels` does not announce its
+ * first sums, so that the waits for them run out.  Bits: 1 gate_up, 2 down, 4 dh,
+ * 8 dx, 16 a product split along K, 32 d_down, 64 d_gate_up; 0 ends it.
+ * Synchronous.  Errors: EINVAL (a release build), ECUDA. */
+int fp8z1_checked_ffn_stall(uint32_t kernels);
 
 /* ---- distillation ----------------------------------------------------------------- */
 
