@@ -92,8 +92,8 @@ def _rows(t: torch.Tensor, what: str) -> int:
     ld, one = t.stride()
     if cols > 1 and one != 1:
         _bad(f"{what}'s rows must be dense")
-    if n <= 1:
-        return ld if ld > cols else cols
+    if n <= 1:  # a single row's stride is whatever it was cut from, and no alignment is asked of it
+        return cols
     if ld < cols:
         _bad(f"{what}'s rows must not overlap")
     return ld
