@@ -190,23 +190,23 @@ struct Weight {
 using bf16 = __nv_bfloat16;
 
 // An FP8 pair carries BF16's 8 significant bits: hi = e4m3(v), lo = e5m2(v - hi),
-// for v scaled by a power of two so that the largest of its 128 lies in
-// [128, 256).  hi leaves at most 8 units of a BF16 value's last place, and
-// E5M2's 3 bits hold every number of units up to 8: a BF16 value down to 2^-13
-// of the largest one is held exactly, a smaller one to 2^-21 of it.  (With lo
-// in E4M3 the exact range ended at 2^-10 and the rest at 2^-18: an outlier
-// channel 300 times the others then cost the weight gradients 2.4e-5.)  Any
-// other FP32 value is held to BF16's 2^-8.
+// for v scaled by a power of two so that the largest of its 128 lies in (224, 448],
+// the top of E4M3.  hi leaves at most 8 units of a BF16 value's last place, and
+// E5M2's 3 bits hold every number of units up to 8: a BF16 value down to 2^-13.8
+// of the largest one is held exactly, a smaller one to 2^-21.8 of it.  (An outlier
+// channel 300 times the others needs that range: with the largest in [128, 256) one
+// gate in 10^4 was off by 2^-16 of its terms and a weight gradient that hung on it by
+// 6e-5; with lo in E4M3 the exact range would end at 2^-10.)  Any other FP32 value is
+// held to BF16's 2^-8.
 struct PairScale {
     float up, down;  // multiply by `up` to encode, by `down` to decode
 };
 __device__ __forceinline__ PairScale pair_scale(float amax)
 {
-    uint32_t e = __float_as_uint(amax) >> 23;  // amax >= 0
-    const bool finite = e < 255;
-    e = min(max(e, 8u), 254u);
+    const uint32_t bits = __float_as_uint(amax);  // amax >= 0
+    const uint32_t e = min(max((bits + 0x1fffffu) >> 23, 9u), 255u);  // one more from 1.75 times a power of two on
     // an infinity makes its 128 values NaN (E4M3 has none)
-    return PairScale{__uint_as_float(finite ? (261u - e) << 23 : 0x7fffffffu), __uint_as_float((e - 7u) << 23)};
+    return PairScale{__uint_as_float(bits < 0x7f800000u ? (262u - e) << 23 : 0x7fffffffu), __uint_as_float((e - 8u) << 23)};
 }
 // v's pair as two codes each for (a, b): bits 0-15 of hi and lo.  FP16 on the way
 // holds more bits than the pair does, down to 2^-32 of the largest value, and takes

@@ -89,8 +89,9 @@ int fp8z1_ffn_sizes(const fp8z1_ffn_dims* dims, int64_t* saved_bytes, int64_t* f
  * `saved`: NULL, or fp8z1_ffn_sizes' saved_bytes for fp8z1_ffn_backward
  * (256-byte aligned, as `workspace`).
  * Accumulation is FP32; h is rounded to 8 significant bits (BF16's) between
- * the two products (up to four tokens: not rounded) and y once at the end.  An
- * infinity or NaN in a row of x leaves that row of y without finite numbers.
+ * the two products (up to four tokens: not rounded) and y once at the end.   x is
+ * held exactly down to 2^-13 of the largest of its 128 neighbours, to 2^-21 of
+ * that below.  An infinity or NaN in a row of x leaves that row of y without finite numbers.
  * y does not depend on `saved`; results repeat bit for bit.
  * Errors: EINVAL, EALIGN, ECUDA. */
 int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int64_t ld_x, const int32_t* d_offsets,
