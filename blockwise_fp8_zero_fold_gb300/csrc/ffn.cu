@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256) split_kernel(Runs runs, Plan plan, const 
         const PairScale ps = pair_scale(amax);
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pair_encode(f[j].x, f[j].y, ps.up, hi[j], lo[j]);
+        for (int j = 0; j < 4; ++j) pair_encode<Lo::kE5M2>(f[j].x, f[j].y, ps.up, hi[j], lo[j]);
         *reinterpret_cast<uint2*>(out.hi + warp * out.pitch + c) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
         *reinterpret_cast<uint2*>(out.lo + warp * out.pitch + c) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         if ((lane & 15) == 0) out.scale[c / kBlock * rows + warp] = ps.down;
@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float*
                 amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
                 const PairScale ps = pair_scale(amax);
                 uint32_t h0, l0, h1, l1;
-                pair_encode(v.x, v.y, ps.up, h0, l0);
-                pair_encode(v.z, v.w, ps.up, h1, l1);
+                pair_encode<Lo::kE4M3>(v.x, v.y, ps.up, h0, l0);
+                pair_encode<Lo::kE4M3>(v.z, v.w, ps.up, h1, l1);
                 *reinterpret_cast<uint32_t*>(pairs.hi + at * pairs.pitch + col) = h0 | h1 << 16;
                 *reinterpret_cast<uint32_t*>(pairs.lo + at * pairs.pitch + col) = l0 | l1 << 16;
                 if (lane == 0) pairs.scale[(half * F + f0) / kBlock * rows + at] = ps.down;

@@ -40,7 +40,7 @@ struct Plan {
     const int32_t* pairs;       // [n_pairs] twice the first tile, and 1 when there is a second
 };
 
-// FP8 pairs: value = (hi + lo) * scale[k / 128][row]
+// FP8 pairs: value = (hi + lo) * scale[k / 128][row]; see pair_encode
 struct Pairs {
     uint8_t *hi, *lo;  // [rows, pitch]
     float* scale;      // [pitch / 128, rows]
@@ -189,15 +189,22 @@ struct Weight {
 
 using bf16 = __nv_bfloat16;
 
-// An FP8 pair carries BF16's 8 significant bits: hi = e4m3(v), lo = e5m2(v - hi),
-// for v scaled by a power of two so that the largest of its 128 lies in (224, 448],
-// the top of E4M3.  hi leaves at most 8 units of a BF16 value's last place, and
-// E5M2's 3 bits hold every number of units up to 8: a BF16 value down to 2^-13.8
-// of the largest one is held exactly, a smaller one to 2^-21.8 of it.  (An outlier
-// channel 300 times the others needs that range: with the largest in [128, 256) one
-// gate in 10^4 was off by 2^-16 of its terms and a weight gradient that hung on it by
-// 6e-5; with lo in E4M3 the exact range would end at 2^-10.)  Any other FP32 value is
-// held to BF16's 2^-8.
+// An FP8 pair: hi = e4m3(v), lo = v - hi, for v scaled by a power of two so that the
+// largest of its 128 lies in (224, 448], the top of E4M3.  hi leaves at most 8 units of a
+// BF16 value's last place.
+//
+// x and dy are BF16 values, and their lo is E5M2, whose 3 bits hold every number of
+// units up to 8: a value down to 2^-13.8 of the largest one is held exactly, a smaller one
+// to 2^-21.8 of it.  (An outlier channel 300 times the others needs that range: with the
+// largest in [128, 256) one gate in 10^4 was off by 2^-16 of its terms and a weight gradient
+// that hung on it by 6e-5; with lo in E4M3 the exact range would end at 2^-10.)
+//
+// h, dg and du are FP32 and rounded by their pair on the way to the second product (to y,
+// to dx), as a BF16 activation between two products would be.  Their lo is E4M3, of 4
+// bits: values are held to 2^-9 of themselves, twice as fine as BF16's 2^-8, or to 2^-17.8
+// of the largest: y and dx, rounded to BF16, are off by 1.8e-3 of their norm (2.1e-3 with
+// two roundings of BF16's, 1.66e-3 with the last alone).  A third FP8 term would hold 12
+// bits and make these products half as long again.
 struct PairScale {
     float up, down;  // multiply by `up` to encode, by `down` to decode
 };
@@ -208,9 +215,11 @@ __device__ __forceinline__ PairScale pair_scale(float amax)
     // an infinity makes its 128 values NaN (E4M3 has none)
     return PairScale{__uint_as_float(bits < 0x7f800000u ? (262u - e) << 23 : 0x7fffffffu), __uint_as_float((e - 8u) << 23)};
 }
+enum class Lo { kE5M2, kE4M3 };
 // v's pair as two codes each for (a, b): bits 0-15 of hi and lo.  FP16 on the way
 // holds more bits than the pair does, down to 2^-32 of the largest value, and takes
 // half the instructions of FP32.
+template <Lo kLo>
 __device__ __forceinline__ void pair_encode(float a, float b, float up, uint32_t& hi, uint32_t& lo)
 {
     const __half2 v = __floats2half2_rn(a * up, b * up);
@@ -219,7 +228,10 @@ __device__ __forceinline__ void pair_encode(float a, float b, float up, uint32_t
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(*reinterpret_cast<const uint32_t*>(&v)));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
     const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
+    if constexpr (kLo == Lo::kE5M2)
+        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
+    else
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
     hi = h;
     lo = l;
 }

@@ -6,8 +6,8 @@
 //   dx       dx = [dg | du] [Wg | Wu]^T
 //
 // A row operand a is a pair of FP8 numbers at a power of two per (row, 128 of
-// k): a = 2^s (hi + lo), E4M3 and E5M2, which carries BF16's 8 bits exactly, so
-// the FP8 codes of a weight enter the tensor cores as they are:
+// k): a = 2^s (hi + lo), which carries x's and dy's 8 bits exactly and 9 of h's, dg's
+// and du's, so the FP8 codes of a weight enter the tensor cores as they are:
 //
 //   sum_k a_k w_k c_kn = sum over blocks b of  2^s_b c_bn  sum_{k in b} (hi + lo)_k w_kn.
 //
@@ -66,6 +66,7 @@ struct Args {
     int64_t rows;          // of the row operands (pitch of a_scale)
     int64_t F;
     int64_t N;             // columns of the result (kGateUp: F pairs)
+    uint32_t idesc[2];     // of the products with hi, with lo
     int32_t n_tiles;       // column tiles
     int32_t splits;        // kPart: CTAs along K, else 1
     int32_t k_blocks;
@@ -226,8 +227,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
         } else if (warp == 1 && lane == 0) {
             constexpr bool kMnMajor = n_major(kMode);
-            constexpr uint32_t idesc[2] = {instruction(128, kCols, false, kMnMajor),
-                                           instruction(128, kCols, false, kMnMajor, true)};
             Turn<kStages> turn;
             Turn<2> acc;
             for (int64_t i = i0; i < total && ok; i += step) {
@@ -249,7 +248,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                             // K-major: 8 columns are 1024 bytes
                             const uint64_t db = kMnMajor ? operand(src + 2 * kOperand + k * 4096, 1024, kOperand)
                                                          : operand(src + 2 * kOperand + k * 32, 1024, 16);
-                            mma_f8(d, da, db, idesc[t], t + k > 0);
+                            mma_f8(d, da, db, a.idesc[t], t + k > 0);
                         }
                     commit(bar_empty + 8 * turn.slot);
 #if FP8Z1_CHECKED
@@ -386,8 +385,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                     for (int i2 = 0; i2 < 4; ++i2) {
                         const float* v = &sum[0][q * 16 + i2 * 4];
                         uint32_t h0, l0, h1, l1;
-                        pair_encode(v[0], v[1], ps.up, h0, l0);
-                        pair_encode(v[2], v[3], ps.up, h1, l1);
+                        pair_encode<Lo::kE4M3>(v[0], v[1], ps.up, h0, l0);
+                        pair_encode<Lo::kE4M3>(v[2], v[3], ps.up, h1, l1);
                         vh[i2] = h0 | h1 << 16;
                         vl[i2] = l0 | l1 << 16;
                     }
@@ -506,15 +505,15 @@ __global__ void __launch_bounds__(256) join_gate_kernel(Plan plan, const float* 
     }
     const PairScale ps = pair_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, abs_bits(amax))));
     uint32_t h0, l0, h1, l1;
-    pair_encode(v[0], v[1], ps.up, h0, l0);
-    pair_encode(v[2], v[3], ps.up, h1, l1);
+    pair_encode<Lo::kE4M3>(v[0], v[1], ps.up, h0, l0);
+    pair_encode<Lo::kE4M3>(v[2], v[3], ps.up, h1, l1);
     *reinterpret_cast<uint32_t*>(h.hi + (int64_t)blockIdx.x * h.pitch + n) = h0 | h1 << 16;
     *reinterpret_cast<uint32_t*>(h.lo + (int64_t)blockIdx.x * h.pitch + n) = l0 | l1 << 16;
     if (lane == 0) h.scale[block * rows + blockIdx.x] = ps.down;
 }
 
 template <int kMode>
-int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a, cudaStream_t s)
+int launch(const Dims& d, const Pairs& rows, Lo lo_format, int64_t K, const Weight& w, Args a, cudaStream_t s)
 {
     CUtensorMap hi, lo, wm;
     const uint64_t rdims[2] = {(uint64_t)rows.pitch, (uint64_t)d.rows()}, rstride[1] = {(uint64_t)rows.pitch};
@@ -527,6 +526,7 @@ int launch(const Dims& d, const Pairs& rows, int64_t K, const Weight& w, Args a,
         (st = tensor_map(&lo, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, rows.lo, rdims, rstride, rbox)) != FP8Z1_OK ||
         (st = tensor_map(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, w.codes, wdims, wstride, wbox)) != FP8Z1_OK)
         return st;
+    for (int t = 0; t < 2; ++t) a.idesc[t] = instruction(128, kCols, false, n_major(kMode), t && lo_format == Lo::kE5M2);
     a.a_scale = rows.scale;
     a.b_scale = w.scale;
     a.rows = d.rows();
@@ -551,10 +551,10 @@ int launch_gate_up(const Dims& d, const Plan& p, const Pairs& x, const Weight& w
     a.h = h;
     a.gu = gu;
     a.splits = k_splits(d, 2 * d.F, d.H);
-    if (a.splits == 1) return launch<kGateUp>(d, x, d.H, w, a, s);
+    if (a.splits == 1) return launch<kGateUp>(d, x, Lo::kE5M2, d.H, w, a, s);
     a.N = 2 * d.F;
     a.part = part;
-    const int st = launch<kPart>(d, x, d.H, w, a, s);
+    const int st = launch<kPart>(d, x, Lo::kE5M2, d.H, w, a, s);
     if (st != FP8Z1_OK) return st;
     return launch_after(join_gate_kernel, dim3((unsigned)d.rows(), (unsigned)ceil_div(d.F, 1024)), 256, 0, s, p, part,
                         d.rows(), d.F, a.splits, h, gu);
@@ -569,9 +569,9 @@ int launch_down(const Dims& d, const Plan& p, const Pairs& h, const Weight& w, b
     a.out = y;
     a.ld = ld;
     a.splits = k_splits(d, d.H, d.F);
-    if (a.splits == 1) return launch<kDown>(d, h, d.F, w, a, s);
+    if (a.splits == 1) return launch<kDown>(d, h, Lo::kE4M3, d.F, w, a, s);
     a.part = part;
-    const int st = launch<kPart>(d, h, d.F, w, a, s);
+    const int st = launch<kPart>(d, h, Lo::kE4M3, d.F, w, a, s);
     if (st != FP8Z1_OK) return st;
     return launch_after(join_kernel, dim3((unsigned)d.rows(), (unsigned)ceil_div(d.H, 1024)), 256, 0, s, p, part, d.rows(),
                         d.H, a.splits, y, ld);
@@ -583,7 +583,7 @@ int launch_dh(const Dims& d, const Plan& p, const Pairs& dy, const Weight& w, fl
     a.plan = p;
     a.N = d.F;
     a.dh = dh;
-    return launch<kDh>(d, dy, d.H, w, a, s);
+    return launch<kDh>(d, dy, Lo::kE5M2, d.H, w, a, s);
 }
 
 int launch_dx(const Dims& d, const Plan& p, const Pairs& dgu, const Weight& w, bf16* dx, int64_t ld, cudaStream_t s)
@@ -593,7 +593,7 @@ int launch_dx(const Dims& d, const Plan& p, const Pairs& dgu, const Weight& w, b
     a.N = d.H;
     a.out = dx;
     a.ld = ld;
-    return launch<kDx>(d, dgu, 2 * d.F, w, a, s);
+    return launch<kDx>(d, dgu, Lo::kE4M3, 2 * d.F, w, a, s);
 }
 
 int read_timeouts_gemm(unsigned* n)

@@ -88,10 +88,12 @@ int fp8z1_ffn_sizes(const fp8z1_ffn_dims* dims, int64_t* saved_bytes, int64_t* f
  * 16-byte aligned, ld_x, ld_y multiples of 8.  gate_up, down: 16-byte aligned.
  * `saved`: NULL, or fp8z1_ffn_sizes' saved_bytes for fp8z1_ffn_backward
  * (256-byte aligned, as `workspace`).
- * Accumulation is FP32; h is rounded to 8 significant bits (BF16's) between
- * the two products (up to four tokens: not rounded) and y once at the end.   x is
- * held exactly down to 2^-13 of the largest of its 128 neighbours, to 2^-21 of
- * that below.  An infinity or NaN in a row of x leaves that row of y without finite numbers.
+ * Accumulation is FP32; h is rounded between the two products, to 9 significant
+ * bits (BF16 has 8) or 2^-17 of the largest of its 128 neighbours, and y once at
+ * the end.  (Up to four tokens keep h in FP32: a token's y may change in its last
+ * place when a fifth joins.)  x is held exactly down to 2^-13 of the largest of
+ * its 128 neighbours, to 2^-21 of that below.  An infinity or NaN in a row of x
+ * leaves that row of y without finite numbers.
  * y does not depend on `saved`; results repeat bit for bit.
  * Errors: EINVAL, EALIGN, ECUDA. */
 int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int64_t ld_x, const int32_t* d_offsets,
@@ -101,7 +103,8 @@ int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int64_t ld_x, c
 /* The gradients of sum(dy * y), from the same x, offsets and weights and the
  * buffer that forward pass filled:
  *   dh = dy Wd^T,  dg = dh * u * s (1 + g (1 - s)),  du = dh * silu(g),  s = sigmoid(g),
- *   dx = [dg | du] gate_up^T (BF16; NULL leaves it out),
+ *   dx = [dg | du] gate_up^T (BF16; NULL leaves it out; dg and du rounded for
+ *        it as h is for y),
  *   d_gate_up = x^T [dg | du],  d_down = h^T dy,  FP32 [E, R, C] row-major: the
  * optimizer's grads.  Every element is written (zeros for an expert without
  * tokens; dx = 0 in rows of no expert).  dy, dx as x above; d_gate_up and
