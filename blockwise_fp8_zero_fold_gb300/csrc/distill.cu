@@ -619,9 +619,10 @@ int launch(Args<T> a, cudaStream_t s)
     if (bytes <= 48 * 1024) return launch_rows<T, 128>(a, ranks, s);
     if (bytes <= 128 * 1024 || (!a.dlogits && bytes <= 1024 * 1024)) return launch_rows<T, 256>(a, ranks, s);
     // Long rows keep the first of their batches in shared memory, as many as leave room for the SM's other CTA: the
-    // gradient reads them last, when a row's worth of every CTA and the gradient's lines have passed through L2.  (4096
-    // rows of 131072 BF16 logits: 362 us, 408 without; 1001 of 50001 FP32: 83 and 80.)
-    if (a.dlogits && bytes * 2 * 152 > (int64_t)64 << 20) return launch_rows<T, 512, true>(a, ranks, s);
+    // gradient reads them last, when a row's worth of every CTA and the gradient's lines have passed through L2.  Kept
+    // and not, 4000 rows of BF16 logits took 223 and 221 us at 160 KB a row, 246 and 258 at 184, 286 and 319 at 216, 353
+    // and 399 at 256; 1000 of FP32 64 and 62, 72 and 72, 80 and 87, 98 and 104.
+    if (a.dlogits && bytes > 176 * 1024) return launch_rows<T, 512, true>(a, ranks, s);
     return launch_rows<T, 512>(a, ranks, s);
 }
 
