@@ -272,9 +272,14 @@ int launch(const Args& a, cudaStream_t s)
 
 bool few_tokens(const Dims& d)
 {
-    // the slices of the vectors fit shared memory.  (One token of 4096 x 14336: 47 us, 79 on the tensor cores; four: 82
-    // and 79, and 33 and 41 at 7168 x 2048; 61 tokens over 27 of 32 experts: 466 and 264.)
-    return d.T <= kTokens && (d.H > d.F ? d.H : d.F) <= kMostSplit * kMostSlice;
+    // The slices of the vectors have to fit shared memory.  One token's products are read; more tokens multiply every
+    // decoded code again, which the tensor cores do not notice.  Here and there, us, by the multiplications: 264 M (three
+    // tokens of 7168 x 4096) 40 and 41, 277 M (four of 4096 x 5632) 38 and 40, 302 M (three of 4096 x 8192) 42 and 43,
+    // 352 M (four of 7168 x 4096, of 2048 x 14336; two of 4096 x 14336) 46 and 41, 46 and 44, 60 and 60, 705 M (four of
+    // 4096 x 14336) 79 and 60.  One token of 4096 x 14336 44 and 59, of 7168 x 18432 80 and 94; four over 32 experts of
+    // 7168 x 2048, mostly one each, 51 and 55.
+    return d.T <= kTokens && (d.H > d.F ? d.H : d.F) <= kMostSplit * kMostSlice &&
+           (d.T == 1 || d.T * 3 * d.H * d.F <= (int64_t)5 << 26);
 }
 
 int launch_gemv(const Dims& d, const Runs& runs, const bf16* x, int64_t ld_x, const Weight& wgu, const Weight& wd, float* h,

@@ -90,10 +90,10 @@ int fp8z1_ffn_sizes(const fp8z1_ffn_dims* dims, int64_t* saved_bytes, int64_t* f
  * (256-byte aligned, as `workspace`).
  * Accumulation is FP32; h is rounded between the two products, to 9 significant
  * bits (BF16 has 8) or 2^-17 of the largest of its 128 neighbours, and y once at
- * the end.  (Up to four tokens keep h in FP32: a token's y may change in its last
- * place when a fifth joins.)  x is held exactly down to 2^-13 of the largest of
- * its 128 neighbours, to 2^-21 of that below.  An infinity or NaN in a row of x
- * leaves that row of y without finite numbers.
+ * the end.  (One token, and up to four of small blocks, keep h in FP32: a token's y
+ * may change in its last place when others join.)  x is held exactly down to
+ * 2^-13 of the largest of its 128 neighbours, to 2^-21 of that below.  An infinity
+ * or NaN in a row of x leaves that row of y without finite numbers.
  * y does not depend on `saved`; results repeat bit for bit.
  * Errors: EINVAL, EALIGN, ECUDA. */
 int fp8z1_ffn_forward(const fp8z1_ffn_dims* dims, const void* x, int64_t ld_x, const int32_t* d_offsets,
