@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(Runs runs, PlanBuffers p, in
         p.start[e] = first;
         p.tokens[e] = (int32_t)min(hi - lo, (int64_t)(last - first) * kRows);
         if (clear) {
-            clear[e] = Peaks{from ? from[e].x : 0, 0};
+            clear[e] = Peaks{from ? from[e].x : 0, 0, {}};
         }
     }
     if (e == n - 1) {
