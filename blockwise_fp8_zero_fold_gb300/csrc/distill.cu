@@ -7,8 +7,8 @@
 // Bound by memory: the logits are read from it once and the gradient written
 // once.  A row is read twice, for its maximum and sum and, backwards, for the
 // gradient; the second time it comes from L2, and a long row's first 92 KB from
-// shared memory.  4096 rows of 131072 BF16 logits take 362 us with the gradient
-// (5.9 TB/s) and 166 without (6.5).
+// shared memory.  4096 rows of 131072 BF16 logits take 361 us with the gradient
+// (5.9 TB/s) and 164 without (6.5).
 //
 // A row belongs to a CTA of 2 to 16 warps, or to a cluster of up to 8 of them,
 // each with a slice.  A thread has eight vectors of 16 bytes on their way and
@@ -606,16 +606,16 @@ int launch(Args<T> a, cudaStream_t s)
     const int64_t vecs = ceil_div(a.vocab + kN - 1, kN);
     // few rows are spread over more CTAs, down to 16 KB slices, while that still leaves SMs idle
     int ranks = 1;
-    while (ranks < 8 && a.rows * ranks * 2 <= 152 && vecs > ranks * 2 * 1024) ranks *= 2;
+    while (ranks < 8 && a.rows * ranks * 2 <= kSms && vecs > ranks * 2 * 1024) ranks *= 2;
     a.slice = ceil_div(vecs, ranks);
     // A CTA's fixed chain of steps is about 7 us: short rows go to small CTAs, of which an SM holds many.  Long ones
-    // to few: they are read again from L2, where eight 256 KB rows an SM would not fit (4096 rows of 131072 BF16
-    // logits took 411 us at two rows an SM, 443 at four, 511 at eight; 8192 rows of 16384 took 264, 169, 118).
-    // Rows of a few KB are that chain alone: 65536 of 2048 took 468 us in CTAs of 128 threads, 334 in 64; 16384 of 8192
-    // 164 and 147.  (With fewer rows than run at once in 128 threads, more threads a row end sooner.)  The loss alone
-    // reads once, and four rows an SM do best (172 us against 189 at two).
+    // to few: they are read again from L2, where eight 256 KB rows an SM would not fit.  At two, four and eight rows an
+    // SM (CTAs of 512, 256 and 128 threads, nothing kept), BF16, 64 entries: 4096 rows of 131072 take 408, 450 and 479
+    // us, of 65536 188, 204 and 230, of 32768 116, 100 and 108; 8192 rows of 16384 240, 154 and 118.  Rows of a few KB
+    // are that chain alone: 65536 of 2048 take 470 us in CTAs of 128 threads, 331 in 64; 16384 of 8192 161 and 140 (120
+    // and 132 with 8 entries).  The loss alone reads once, and four rows an SM do best (164 us for 131072, 173 at two).
     const int64_t bytes = a.slice * 16;
-    if (bytes <= 24 * 1024 && a.rows * ranks > 152 * 8) return launch_rows<T, 64>(a, ranks, s);
+    if (bytes <= 24 * 1024 && a.rows * ranks > kSms * 8) return launch_rows<T, 64>(a, ranks, s);
     if (bytes <= 48 * 1024) return launch_rows<T, 128>(a, ranks, s);
     if (bytes <= 128 * 1024 || (!a.dlogits && bytes <= 1024 * 1024)) return launch_rows<T, 256>(a, ranks, s);
     // Long rows keep the first of their batches in shared memory, as many as leave room for the SM's other CTA: the

@@ -17,9 +17,9 @@
 // Nearly all of the time is the table's zeros.  Up to 16384 tokens one CTA sorts
 // while the others clear as much as takes that long; what is left of a large table
 // is cleared beside the sums, by CTAs that look up which of their rows have a
-// token and leave those out.  131072 x 4096 with 16384 tokens: 377 us, 6.1 TB/s
-// (412 with all of it cleared beside the sort); with 2000 tokens 323 (359); with
-// 40000, sorted in passes, 523 (598).
+// token and leave those out.  131072 x 4096 with 16384 tokens: 360 us, 6.3 TB/s
+// (412 with all of it cleared beside the sort); with 2000 tokens 322 (359); with
+// 40000, sorted in passes, 503 (598).
 #include <algorithm>
 #include <type_traits>
 
@@ -113,7 +113,7 @@ int launch_embed(int64_t vocab, int64_t dim, const uint8_t* codes, const float* 
         ceil_div(dim, 8 * kEmbedThreads) <= 65535) {
         const unsigned slices = (unsigned)ceil_div(dim, 8 * kEmbedThreads);
         // 4 tokens a thread once that still leaves several CTAs for every SM
-        if (tokens * slices >= 4 * 152 * 8)
+        if (tokens * slices >= 4 * kSms * 8)
             embed_kernel<T, 4><<<dim3((unsigned)ceil_div(tokens, 4), slices), kEmbedThreads, 0, s>>>(
                 vocab, dim, codes, scales, ids, tokens, alpha, out, ld);
         else

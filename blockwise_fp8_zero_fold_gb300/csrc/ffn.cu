@@ -128,7 +128,7 @@ __device__ __forceinline__ float2 bf16_pair(uint32_t two)
 // Rows of BF16 activations to FP8 pairs in the tiles' order (a warp kRowColumns
 // of a row: with one row of 7168, a warp for all of it took 21 us; 16 lanes a block
 // of 128), with each expert's peak; rows of no expert are zeroed in `rest`.  8192
-// rows of 7168: 42 us, 5.7 TB/s (55 with a load at a time).
+// rows of 7168: 42 us, 5.6 TB/s (55 with a load at a time).
 constexpr int kRowColumns = 1024;
 __global__ void __launch_bounds__(256) split_kernel(Runs runs, Plan plan, const bf16* x, int64_t ld, int64_t H,
                                                     Pairs out, int64_t rows, Peaks* peaks, bool dy, bf16* rest,
@@ -202,7 +202,7 @@ __device__ __forceinline__ uint32_t half_pair(float a, float b)
 }
 
 // Rows of x and dy to FP16 in the tiles' order, each expert's at its power of two.
-// Bound by memory: 8192 rows of 7168 take 72 us, 6.5 TB/s.
+// Bound by memory: 8192 rows of 7168 take 78 us, 6.0 TB/s.
 __global__ void __launch_bounds__(256) halves_kernel(Plan plan, const bf16* x, int64_t ld_x, const bf16* dy,
                                                      int64_t ld_dy, int64_t H, int64_t pitch, __half* x16,
                                                      __half* dy16, const Peaks* peaks)
@@ -257,7 +257,9 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // columns: [dg | du] as FP8 pairs for dx and as FP16 pairs for d_gate_up, h as
 // FP16 pairs for d_down.  The eight CTAs of two tiles are a cluster: a column's power
 // of two is that of its largest number in all 256 rows.  Bound by memory, 28 bytes an
-// element: 8192 rows of 2048 take 99 us, 4.7 TB/s.
+// element: 8192 rows of 2048 take 127 us, 3.7 TB/s (100 with one power of two for an
+// expert, known beforehand).  The peaks go through 32-bit words: stores of bytes in the
+// load loop kept later loads behind them (302 us for 215 at 2051 rows of 14336).
 constexpr int kActPitch = 132;
 constexpr int kActSmem = (3 * 32 * kActPitch + 3 * 128) * 4;
 __global__ void __launch_bounds__(256) activation_kernel(Plan plan, const float* gu, const float* dh, int64_t F,

@@ -26,13 +26,13 @@
 // to each other, so that an expert's codes are read from memory once.
 //
 // Bound by the tensor cores from some 100 rows an expert: 8192 tokens over 31
-// experts of 7168 x 2048 take 0.46 ms (gate_up), 0.24 (down), 0.23 (dh) and 0.42
-// (dx), 1040 TFLOP/s of BF16 products, 1350 with the padded rows.  A tile's end
-// (4 to 6 us, SiLU and encoding a third of it) is hidden by no more than the two
-// accumulators and costs 14 % of that; reading the sums of every 128 of k out of
-// tensor memory costs about as much (1750 TFLOP/s without).  Sharing the codes as
-// well, by clusters of 2 x 2 tiles, gained nothing.  With fewer rows bound by the codes read:
-// 61 tokens over 27 experts at 6.1 TB/s while every SM has a tile.
+// experts of 7168 x 2048 take 0.42 ms (gate_up), 0.22 (down), 0.22 (dh) and 0.38
+// (dx), 1170 TFLOP/s of BF16 products, 1520 with the padded rows; 2051 of 4096 x 14336
+// 0.35, 0.16, 0.17 and 0.31, 1460.  A tile's end (SiLU, encoding, stores) is hidden by no
+// more than the two accumulators: forward passes without it took 6 and 8 % less; without
+// reading the sums of every 128 of k out of tensor memory they took the same.  With few
+// rows bound by the codes read: 61 tokens over 27 experts, 1.19 GB in 260 us, 432 column
+// tiles in three rounds of 152 CTAs.
 #include "ffn.cuh"
 
 namespace fp8z1 {

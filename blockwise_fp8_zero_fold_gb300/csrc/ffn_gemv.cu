@@ -3,15 +3,16 @@
 //
 //   h = silu(x Wg) * (x Wu)   (FP32),   y = h Wd   (rounded to BF16 once)
 //
-// Bound by the codes read, and near it by their decoding.  A cluster of up to 8
+// Bound by the codes read and by their decoding, neither alone: one token of 4096 x
+// 14336 takes 43 us, 26 at the rate of a copy, with half the issue slots decoding and DRAM
+// at 53 % in the first product and 38 % in the second, whose start overlaps.  A cluster of up to 8
 // CTAs has 128 or 64 columns of a product (gate_up: gate columns and the up columns
 // beside them), each CTA a part of K; a thread has 16 neighbouring columns (16 bytes
 // of a row), three or four rows on their way while as many are multiplied, and FP32
 // sums of up to 4 tokens.  Scale blocks are 128 x 128, so a row's 16 columns share
 // their scale: it goes to the vector's element.  Sums are added over a CTA's threads
 // and the cluster's CTAs in a fixed order.  The second product's codes are on their
-// way before h is there.  One token of 4096 x 14336 takes 47 us, 26 at the rate of a
-// copy.
+// way before h is there.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -28,8 +29,8 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 256, kMostSplit = 8, kTokens = 4;  // kernels for 1 token and for up to 4
 constexpr int kMostSlice = 8192;  // of K, a CTA's
 // CTAs of an SM, for which a token's 16 sums a thread leave registers, and rows on
-// their way.  (One token of 4096 x 14336: 52 us with 3 CTAs and 4 rows, 47 with 4
-// and 3, 51 with 5 and 2.)
+// their way.  (One token of 4096 x 14336: 48 us with 3 CTAs and 4 rows, 44 with 4
+// and 3, 48 with 5 and 2.)
 __host__ __device__ constexpr int resident(int tokens) { return tokens == 1 ? 4 : 2; }
 __host__ __device__ constexpr int hold(int tokens) { return tokens == 1 ? 3 : 4; }
 
@@ -222,7 +223,7 @@ Shape shape(int64_t K, int64_t N, int64_t runs, int out, int resident)
     for (int n = 1; n <= kMostSplit; ++n) {
         const int64_t slice = ceil_div(ceil_div(K, n), 128) * 128;
         if (slice > kMostSlice || (n > 1 && slice < 256)) continue;
-        const double t = (double)ceil_div(groups * n, 152 * resident) * (double)((slice + 1024) * out / 64);
+        const double t = (double)ceil_div(groups * n, kSms * resident) * (double)((slice + 1024) * out / 64);
         if (t < best.time) best = {t, n, (int32_t)slice};
     }
     return best;

@@ -22,8 +22,9 @@
 // products, more than L2 delivers to every SM at once.
 //
 // Bound by the FP32 gradients written (4 bytes an element) up to about 250
-// tokens an expert, by the tensor cores above: the experts' gradients are written at
-// 4.8 TB/s, the dense block's multiplied at 1750 TFLOP/s (FP16 products).
+// tokens an expert, by the tensor cores and what feeds them above: 8192 tokens over 31
+// experts of 7168 x 2048 take 800 us (d_gate_up) and 400 (d_down), 4.7 TB/s of stores;
+// 2051 of 4096 x 14336 640 and 295, 1550 TFLOP/s of FP16 products.
 #include "ffn.cuh"
 
 namespace fp8z1 {

@@ -13,6 +13,7 @@
 namespace fp8z1 {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int kSms = 152;  // of a GB300: rules that choose by size go by it (results do not)
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t align256(int64_t n) { return (n + 255) & ~(int64_t)255; }

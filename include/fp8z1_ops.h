@@ -40,8 +40,9 @@ extern "C" {
  * `tokens` integers of `id_bytes` (4 or 8) bytes, signed; an id outside
  * [0, vocab) is no token and gives a row of zeros.  `codes`: [vocab, dim].
  * `out`: rows of `dim` elements, ld_out >= dim apart.  Any dim >= 1 and any
- * alignment of the element types; rows that are multiples of 16 elements on
- * 16-byte boundaries are read and written 16 bytes at a time.
+ * alignment of the element types; rows of a multiple of 8 elements, codes on
+ * 8-byte and `out` on 16-byte boundaries, are read 8 and written 16 bytes at a
+ * time.
  * tokens == 0 enqueues nothing.
  * Errors: EINVAL (null, vocab < 1 or >= 2^31, dim < 1 or > 2^23, tokens < 0 or
  * > 2^30, id_bytes, out_type, ld_out < dim, alpha not finite), EALIGN, ECUDA. */
