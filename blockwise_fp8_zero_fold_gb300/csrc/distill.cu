@@ -316,7 +316,7 @@ __device__ __forceinline__ void write_loss(const Args<T>& a, int64_t r, const Li
     pz = warp_sum(pz);
     // a row of -inf alone has q = 0: its log q is z = -inf, not -inf - -inf
     const float log_total = total == 0.0f ? 0.0f : fmaf(sc.rest(), -0.6931471805599453f, logf(total));
-    if ((threadIdx.x & 31) == 0) a.loss[r] = e.any ? a.tau * a.tau * (e.p_logp - pz / a.tau + log_total) : 0.0f;
+    if ((threadIdx.x & 31) == 0) a.loss[r] = e.any ? a.tau * (a.tau * (e.p_logp + log_total) - pz) : 0.0f;
 }
 
 // The listed elements of a slice, over its dense gradient, by one warp.

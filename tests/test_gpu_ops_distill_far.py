@@ -67,3 +67,18 @@ def test_a_mask_beside_ordinary_logits():
     size = w.cpu().double()[:, None]
     q = wd / torch.where(size == 0, torch.ones_like(size), size)
     assert ((d.cpu().double() - wd).abs() <= 1e-5 * (q.abs() + 2e-2) * size).all()
+
+
+def test_a_listed_id_masked_by_the_lowest_value():
+    """Its loss is tau (m - z) p, within FP32 where (m - z) / tau is not."""
+    lowest, tau = torch.finfo(torch.float32).min, 0.3
+    z = torch.randn(2, 500, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    z[0, 7] = lowest
+    ids = torch.tensor([[7, 3], [7, 3]], dtype=torch.int32, device="cuda")
+    t = torch.tensor([[1.0, 1.0]] * 2, device="cuda")
+    loss, d = ops.distill_loss_grad(z, ids, t, temperature=tau)
+    want, wd = R.distill(z, ids, t, tau, None)
+    assert want.isfinite().all() and want[0] > 1e37
+    # the listed entries' p are 1/2 each: four roundings of 2^-23, and LOSS_TOL for the ordinary row
+    assert ((loss.cpu().double() - want).abs() <= tau * tau * LOSS_TOL / tau + 2.0**-21 * want.abs()).all()
+    assert ((d.cpu().double() - wd).abs() <= 1e-5 * tau * (wd.abs() / tau + 2e-2)).all()
