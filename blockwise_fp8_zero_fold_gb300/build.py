@@ -24,7 +24,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8z1.so")
 LIB_CHECKED = os.path.join(PKG, "libfp8z1_checked.so")
 SOURCES = ["layout.cpp", "fold.cu", "norm.cu", "step.cu", "step_full.cu", "step_pad.cu", "mx.cu", "embed.cu", "ffn.cu",
-           "ffn_gemm.cu", "ffn_gemv.cu", "ffn_wgrad.cu", "distill.cu"]
+           "ffn_gemm.cu", "ffn_gemv.cu", "ffn_wgrad.cu", "distill.cu", "rms_norm.cu", "route.cu"]
 HEADERS = ["internal.h", "checked.cuh", "update.cuh", "step_args.h", "step_kernel.cuh", "ops_common.cuh",
            "ffn.cuh", "tc.cuh"]
 PUBLIC = ["fp8z1.h", "fp8z1_ops.h"]

@@ -149,6 +149,18 @@ _SIGS = {
     "fp8z1_checked_ffn_stall": (C.c_int, [C.c_uint32]),
     "fp8z1_distill": (C.c_int, [_P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, _P, _P, C.c_int64, C.c_float, _P, _P,
                                 _P, C.c_int64, _P]),
+    "fp8z1_rms_norm": (C.c_int, [C.c_int64, C.c_int64, _P, C.c_int32, C.c_int64, _P, C.c_int64, _P, C.c_float, _P,
+                                 C.c_int64, _P, C.c_int64, _P, _P, _P]),
+    "fp8z1_rms_norm_grad_workspace": (C.c_int, [C.c_int64, C.c_int64, C.POINTER(C.c_int64)]),
+    "fp8z1_rms_norm_grad": (C.c_int, [C.c_int64, C.c_int64, _P, C.c_int32, C.c_int64, _P, C.c_int64, _P, C.c_float, _P,
+                                      C.c_int64, _P, C.c_int64, _P, _P, _P]),
+    "fp8z1_route": (C.c_int, [_P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, _P, _P, _P]),
+    "fp8z1_dispatch": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.c_int64, _P, C.c_int32, C.c_int64, _P, _P, _P,
+                                 C.c_int64, _P]),
+    "fp8z1_combine": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, _P, C.c_int32, C.c_int64, _P, _P, _P, C.c_int64, _P,
+                                C.c_int64, _P]),
+    "fp8z1_combine_grad": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.c_int64, _P, C.c_int32, C.c_int64, _P, C.c_int64,
+                                     _P, _P, _P, _P, C.c_int64, _P, _P]),
     "fp8z1_strerror": (C.c_char_p, [C.c_int]),
 }
 
@@ -610,3 +622,57 @@ def fp8z1_distill(logits, type_: int, ld: int, rows: int, vocab: int, teacher_id
                               temperature, _at(row_weight), _at(loss), _at(dlogits), ld_d, _stream(stream))
     if st:
         raise Fp8z1Error(st, "fp8z1_distill")
+
+
+def fp8z1_rms_norm(rows: int, dim: int, x, type_: int, ld_x: int, residual, ld_r: int, weight, eps: float, total,
+                   ld_total: int, y, ld_y: int, codes, scales, stream=None):
+    st = _op("fp8z1_rms_norm")(rows, dim, _at(x), type_, ld_x, _at(residual), ld_r, _at(weight), eps, _at(total), ld_total,
+                               _at(y), ld_y, _at(codes), _at(scales), _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_rms_norm")
+
+
+def fp8z1_rms_norm_grad_workspace(rows: int, dim: int) -> int:
+    n = C.c_int64()
+    st = _op("fp8z1_rms_norm_grad_workspace")(rows, dim, n)
+    if st:
+        raise Fp8z1Error(st, "fp8z1_rms_norm_grad_workspace")
+    return n.value
+
+
+def fp8z1_rms_norm_grad(rows: int, dim: int, dy, type_: int, ld_dy: int, total, ld_total: int, weight, eps: float,
+                        d_total, ld_dt: int, dx, ld_dx: int, d_weight, workspace, stream=None):
+    st = _op("fp8z1_rms_norm_grad")(rows, dim, _at(dy), type_, ld_dy, _at(total), ld_total, _at(weight), eps, _at(d_total),
+                                    ld_dt, _at(dx), ld_dx, _at(d_weight), _at(workspace), _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_rms_norm_grad")
+
+
+def fp8z1_route(ids, id_bytes: int, tokens: int, top: int, experts: int, offsets, place, stream=None):
+    st = _op("fp8z1_route")(_at(ids), id_bytes, tokens, top, experts, _at(offsets), _at(place), _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_route")
+
+
+def fp8z1_dispatch(tokens: int, top: int, experts: int, dim: int, x, type_: int, ld_x: int, offsets, place, rows,
+                   ld_rows: int, stream=None):
+    st = _op("fp8z1_dispatch")(tokens, top, experts, dim, _at(x), type_, ld_x, _at(offsets), _at(place), _at(rows), ld_rows,
+                               _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_dispatch")
+
+
+def fp8z1_combine(tokens: int, top: int, dim: int, rows, type_: int, ld_rows: int, place, weight, residual,
+                  ld_residual: int, y, ld_y: int, stream=None):
+    st = _op("fp8z1_combine")(tokens, top, dim, _at(rows), type_, ld_rows, _at(place), _at(weight), _at(residual),
+                              ld_residual, _at(y), ld_y, _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_combine")
+
+
+def fp8z1_combine_grad(tokens: int, top: int, experts: int, dim: int, dy, type_: int, ld_dy: int, rows, ld_rows: int,
+                       offsets, place, weight, d_rows, ld_d: int, d_weight, stream=None):
+    st = _op("fp8z1_combine_grad")(tokens, top, experts, dim, _at(dy), type_, ld_dy, _at(rows), ld_rows, _at(offsets),
+                                   _at(place), _at(weight), _at(d_rows), ld_d, _at(d_weight), _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_combine_grad")

@@ -8,7 +8,11 @@ FP32 [E, R, C] weight gradients, which ``ShardOptimizer.step`` reads:
   embed, embed_grad          rows of an FP8 table, and the table's gradient;
   ffn_forward, ffn_backward  the gated feed-forward block of each expert;
   distill_loss, distill_loss_grad
-                             distillation from a teacher's top logits.
+                             distillation from a teacher's top logits;
+  rms_norm, rms_norm_fp8, rms_norm_grad
+                             root-mean-square norm, the residual added first;
+  route, dispatch, combine, dispatch_grad, combine_grad
+                             tokens sorted by expert for ``ffn_forward``, and back.
 
 Each is one call of libfp8z1.so's entry point of the same name (include/
 fp8z1_ops.h has the formulas); this module checks the tensors, allocates
@@ -24,7 +28,7 @@ the optimizer skips a step with such gradients.
 """
 from __future__ import annotations
 
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -97,6 +101,16 @@ def _rows(t: torch.Tensor, what: str) -> int:
     if ld < cols:
         _bad(f"{what}'s rows must not overlap")
     return ld
+
+
+def _rows_of(t: torch.Tensor, what: str):
+    """(rows, row stride) of [*, dim]: a 2-D tensor of any row stride, or contiguous."""
+    if t.dim() == 2:
+        return t.shape[0], _rows(t, what)
+    if t.dim() < 1 or not t.is_contiguous():
+        _bad(f"{what} must be contiguous, or 2-D")
+    dim = t.shape[-1]
+    return (t.numel() // dim if dim else 0), dim
 
 
 def _fp8_weight(codes: torch.Tensor, scale: torch.Tensor, what: str):
@@ -294,3 +308,206 @@ def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_l
     ``(row_weight * loss).sum()`` in the logits' type.  ``out`` may be
     ``logits`` itself."""
     return _distill(logits, teacher_ids, teacher_logits, temperature, row_weight, True, out, stream)
+
+
+# ---- root-mean-square norm -------------------------------------------------------------
+
+
+def _norm(x, weight, residual, eps, fp8, out, total, stream):
+    kind, shape = _TYPES.get(x.dtype), x.shape
+    if kind is None or x.dim() < 1:
+        _bad("x must be float32 or bfloat16 [*, dim]")
+    dim = shape[-1]
+    if weight.dtype != torch.float32 or weight.shape != (dim,) or not weight.is_contiguous():
+        _bad(f"weight must be contiguous float32 [{dim}]")
+    rows, ld_x = _rows_of(x, "x")
+    dev = x.get_device()
+    raw, other = _begin(dev, stream)
+    _same_device(dev, weight)
+    ld_r = ld_t = ld_y = 0
+    if residual is not None:
+        ld_r = _rows_of(_given(residual, shape, x.dtype, dev, "residual"), "residual")[1]
+        if total is None:
+            total = _new(shape, x.dtype, dev, other)
+        ld_t = _rows_of(_given(total, shape, x.dtype, dev, "total"), "total")[1]
+    elif total is not None:
+        _bad("total is the sum with a residual")
+    scale = None
+    if fp8:
+        codes = out = _new(shape, torch.float8_e4m3fn, dev, other)
+        scale = _new(shape[:-1] + ((dim + 127) // 128,), torch.float32, dev, other)
+        y = None
+    else:
+        if out is None:
+            out = _new(shape, x.dtype, dev, other)
+        y, codes = _given(out, shape, x.dtype, dev, "out"), None
+        ld_y = _rows_of(y, "out")[1]
+    F.fp8z1_rms_norm(rows, dim, x, kind, ld_x, residual, ld_r, weight, eps, total, ld_t, y, ld_y, codes, scale, raw)
+    return out, scale, total
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             out: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None, stream=None):
+    """``s * (mean(s^2) + eps)^-1/2 * weight`` of each row s of ``x`` (float32 or
+    bfloat16 [*, dim]; weight float32 [dim]), in x's type.  With ``residual``
+    s = x + residual, and the result is (y, s); ``total`` takes s (it may be
+    ``x`` or ``residual`` itself, as ``out`` may)."""
+    y, _, total = _norm(x, weight, residual, eps, False, out, total, stream)
+    return y if residual is None else (y, total)
+
+
+def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 total: Optional[torch.Tensor] = None, stream=None):
+    """``rms_norm`` in 8 bits: (codes, scale), E4M3 codes (float8_e4m3fn) and a float32
+    scale for every 128 columns, [*, ceil(dim / 128)]; with ``residual`` (codes,
+    scale, s)."""
+    codes, scale, total = _norm(x, weight, residual, eps, True, None, total, stream)
+    return (codes, scale) if residual is None else (codes, scale, total)
+
+
+def rms_norm_grad(dy: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6,
+                  d_total: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                  d_weight: Optional[torch.Tensor] = None, stream=None):
+    """(dx, d_weight) of ``rms_norm`` from the rows that it normed (its ``total``, or x):
+    dx in their type, which is the residual's gradient too, with ``d_total`` (what
+    reaches the sum past the norm) added; d_weight float32 [dim]."""
+    kind, shape = _TYPES.get(total.dtype), total.shape
+    if kind is None or total.dim() < 1:
+        _bad("total must be float32 or bfloat16 [*, dim]")
+    dim = shape[-1]
+    if weight.dtype != torch.float32 or weight.shape != (dim,) or not weight.is_contiguous():
+        _bad(f"weight must be contiguous float32 [{dim}]")
+    rows, ld_s = _rows_of(total, "total")
+    dev = total.get_device()
+    raw, other = _begin(dev, stream)
+    _same_device(dev, weight)
+    ld_dy = _rows_of(_given(dy, shape, total.dtype, dev, "dy"), "dy")[1]
+    ld_t = 0
+    if d_total is not None:
+        ld_t = _rows_of(_given(d_total, shape, total.dtype, dev, "d_total"), "d_total")[1]
+    if dx is None:
+        dx = _new(shape, total.dtype, dev, other)
+    ld_dx = _rows_of(_given(dx, shape, total.dtype, dev, "dx"), "dx")[1]
+    if d_weight is None:
+        d_weight = _new((dim,), torch.float32, dev, other)
+    elif not _given(d_weight, (dim,), torch.float32, dev, "d_weight").is_contiguous():
+        _bad("d_weight must be contiguous")
+    ws = _scratch(F.fp8z1_rms_norm_grad_workspace(rows, dim), torch.uint8, dev, other)
+    F.fp8z1_rms_norm_grad(rows, dim, dy, kind, ld_dy, total, ld_s, weight, eps, d_total, ld_t, dx, ld_dx, d_weight, ws,
+                          raw)
+    return dx, d_weight
+
+
+# ---- routing --------------------------------------------------------------------------
+
+
+class Route(NamedTuple):
+    """Where tokens' rows go: expert e has rows [offsets[e], offsets[e + 1]) of
+    tokens * top (int32 [experts + 1], as ``ffn_forward`` takes them), and choice j of
+    token t row place[t, j] (int32 [tokens, top], -1: none)."""
+    offsets: torch.Tensor
+    place: torch.Tensor
+
+
+def route(ids: torch.Tensor, experts: int, *, stream=None) -> Route:
+    """Sorts the choices ids[t, j] (int32 or int64 [tokens, top], or [tokens]) by
+    expert, each expert's in the order of the choices; an id outside [0, experts)
+    is no choice."""
+    nbytes = _ID_BYTES.get(ids.dtype)
+    if nbytes is None or ids.dim() not in (1, 2) or not ids.is_contiguous():
+        _bad("ids must be contiguous int32 or int64 [tokens, top]")
+    tokens, top = ids.shape if ids.dim() == 2 else (ids.shape[0], 1)
+    dev = ids.get_device()
+    raw, other = _begin(dev, stream)
+    if not 1 <= experts <= 1024:
+        _bad("experts must be 1 to 1024")
+    offsets = _new(experts + 1, torch.int32, dev, other)
+    place = _new((tokens, top), torch.int32, dev, other)
+    F.fp8z1_route(ids, nbytes, tokens, top, experts, offsets, place, raw)
+    return Route(offsets, place)
+
+
+def _route_dims(r: Route, dev: int):
+    offsets, place = r
+    if place.dtype != torch.int32 or place.dim() != 2 or not place.is_contiguous():
+        _bad("place must be contiguous int32 [tokens, top]")
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
+        _bad("offsets must be contiguous int32 [experts + 1]")
+    _same_device(dev, offsets, place)
+    return place.shape[0], place.shape[1], offsets.shape[0] - 1
+
+
+def _plain_rows(t: torch.Tensor, rows: int, what: str):
+    """(type, dim, row stride) of float32 or bfloat16 [rows, dim]."""
+    kind = _TYPES.get(t.dtype)
+    if kind is None or t.dim() != 2 or t.shape[0] != rows:
+        _bad(f"{what} must be float32 or bfloat16 [{rows}, dim]")
+    return kind, t.shape[1], _rows(t, what)
+
+
+def _choice_weight(weight, shape):
+    if weight.dtype != torch.float32 or weight.shape != shape or not weight.is_contiguous():
+        _bad(f"weight must be contiguous float32 {tuple(shape)}")
+
+
+def dispatch(x: torch.Tensor, r: Route, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The experts' rows, [tokens * top, dim]: row place[t, j] is x[t] (float32 or
+    bfloat16 [tokens, dim]); rows of no choice, behind the last expert's, are zero."""
+    dev = x.get_device()
+    tokens, top, experts = _route_dims(r, dev)
+    kind, dim, ld = _plain_rows(x, tokens, "x")
+    raw, other = _begin(dev, stream)
+    if out is None:
+        out = _new((tokens * top, dim), x.dtype, dev, other)
+    ld_o = _rows(_given(out, (tokens * top, dim), x.dtype, dev, "out"), "out")
+    F.fp8z1_dispatch(tokens, top, experts, dim, x, kind, ld, r.offsets, r.place, out, ld_o, raw)
+    return out
+
+
+def combine(rows: torch.Tensor, r: Route, weight: Optional[torch.Tensor] = None, *,
+            residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Each token's ``residual + sum_j weight[t, j] * rows[place[t, j]]``, [tokens, dim] in
+    the rows' type (rounded once; weight float32 [tokens, top], None for 1).  ``out``
+    may be ``residual`` itself."""
+    dev = rows.get_device()
+    tokens, top, _ = _route_dims(r, dev)
+    kind, dim, ld = _plain_rows(rows, tokens * top, "rows")
+    if weight is not None:
+        _choice_weight(weight, r.place.shape)
+    raw, other = _begin(dev, stream)
+    _same_device(dev, weight)
+    shape, ld_r = (tokens, dim), 0
+    if residual is not None:
+        ld_r = _rows(_given(residual, shape, rows.dtype, dev, "residual"), "residual")
+    if out is None:
+        out = _new(shape, rows.dtype, dev, other)
+    ld_y = _rows(_given(out, shape, rows.dtype, dev, "out"), "out")
+    F.fp8z1_combine(tokens, top, dim, rows, kind, ld, r.place, weight, residual, ld_r, out, ld_y, raw)
+    return out
+
+
+def dispatch_grad(d_rows: torch.Tensor, r: Route, *, add: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``dispatch``'s gradient, the sum of each token's rows of ``d_rows``; ``add``
+    (what reaches x otherwise) joins it."""
+    return combine(d_rows, r, residual=add, out=out, stream=stream)
+
+
+def combine_grad(dy: torch.Tensor, rows: torch.Tensor, r: Route, weight: torch.Tensor, *,
+                 out: Optional[torch.Tensor] = None, stream=None):
+    """(d_rows, d_weight) of ``combine``: d_rows in the rows' type (zero in rows of no
+    choice), d_weight float32 [tokens, top] (0 where there is no row)."""
+    dev = rows.get_device()
+    tokens, top, experts = _route_dims(r, dev)
+    kind, dim, ld = _plain_rows(rows, tokens * top, "rows")
+    _choice_weight(weight, r.place.shape)
+    raw, other = _begin(dev, stream)
+    _same_device(dev, weight)
+    ld_dy = _rows(_given(dy, (tokens, dim), rows.dtype, dev, "dy"), "dy")
+    if out is None:
+        out = _new(rows.shape, rows.dtype, dev, other)
+    ld_d = _rows(_given(out, rows.shape, rows.dtype, dev, "out"), "out")
+    d_weight = _new((tokens, top), torch.float32, dev, other)
+    F.fp8z1_combine_grad(tokens, top, experts, dim, dy, kind, ld_dy, rows, ld, r.offsets, r.place, weight, out, ld_d,
+                         d_weight, raw)
+    return out, d_weight

@@ -6,7 +6,10 @@
  *   embedding   rows of an FP8 table, scaled; the table's gradient;
  *   gated FFN   (silu(x Wg) * (x Wu)) Wd of each expert on its own tokens,
  *               forward and backward;
- *   distillation  loss against a teacher's top logits, and its gradient.
+ *   distillation  loss against a teacher's top logits, and its gradient;
+ *   RMS norm    of rows, the residual added first, in 16, 32 or 8 bits; its gradient;
+ *   routing     tokens sorted by expert, their rows gathered and joined again,
+ *               and the gradients of both.
  *
  * Conventions, beside those of fp8z1.h (status codes, streams, no work
  * enqueued by a rejected call, no exception across the ABI):
@@ -156,6 +159,77 @@ int fp8z1_checked_ffn_stall(uint32_t kernels);
 int fp8z1_distill(const void* logits, int32_t type, int64_t ld, int64_t rows, int64_t vocab,
                   const int32_t* teacher_ids, const float* teacher_logits, int64_t top, float temperature,
                   const float* row_weight, float* loss, void* dlogits, int64_t ld_d, void* stream);
+
+/* ---- root-mean-square norm --------------------------------------------------------- */
+
+/* Row by row, in FP32:
+ *   s = x + residual, rounded to `type` and written to `total` (without a residual s = x),
+ *   y = s * (mean_j s_j^2 + eps)^-1/2 * weight,
+ * y rounded once: to `type` in `y`, and to E4M3 in `codes` ([rows, dim], dense) with a
+ * scale for every 128 columns in `scales` ([rows, ceil(dim / 128)], dense): max |y| / 448 of
+ * the 128, 1 where that is 0; a value is its code times its scale.  `y` or `codes` may be
+ * NULL (codes and scales together), not both.
+ * x, residual, total, y: `type`, rows of `dim` elements, ld >= dim apart; total and y may be
+ * x or residual themselves.  weight: FP32 [dim].  Any alignment of the element types;
+ * dim and strides of whole 16 bytes on 16-byte boundaries are moved 8 elements at a time.
+ * No row is too large: squares beyond FP32 are summed scaled down.  An infinity or NaN
+ * leaves its row without finite numbers (but 0 where a finite element meets an infinity's norm).
+ * rows == 0 enqueues nothing.
+ * Errors: EINVAL (null, rows < 0 or > 2^30, dim outside 1 .. 16384, type, strides, eps outside
+ * 1e-20 .. 1e20, residual without total or total without residual), EALIGN, ECUDA. */
+int fp8z1_rms_norm(int64_t rows, int64_t dim, const void* x, int32_t type, int64_t ld_x, const void* residual,
+                   int64_t ld_r, const float* weight, float eps, void* total, int64_t ld_total, void* y, int64_t ld_y,
+                   uint8_t* codes, float* scales, void* stream);
+
+/* Bytes of workspace fp8z1_rms_norm_grad needs.  Host only. */
+int fp8z1_rms_norm_grad_workspace(int64_t rows, int64_t dim, int64_t* bytes);
+
+/* The gradients of sum(dy * y) from the rows s that were normed (`total`, or x itself):
+ *   g = dy * weight,  h = s * rstd,  dx = rstd * (g - h * mean_j(g_j h_j)) + d_total,
+ *   d_weight = sum over the rows of dy * h   (FP32 [dim], every element written).
+ * dx is the gradient of x and of the residual; d_total (NULL: none) is what reaches s past the
+ * norm.  dy, total, d_total, dx: `type`; dx may be dy or d_total itself.  Sums are FP32 in a
+ * fixed order: results repeat bit for bit.
+ * Errors: as fp8z1_rms_norm; EALIGN (workspace: 256 bytes). */
+int fp8z1_rms_norm_grad(int64_t rows, int64_t dim, const void* dy, int32_t type, int64_t ld_dy, const void* total,
+                        int64_t ld_total, const float* weight, float eps, const void* d_total, int64_t ld_dt, void* dx,
+                        int64_t ld_dx, float* d_weight, void* workspace, void* stream);
+
+/* ---- routing ------------------------------------------------------------------------- */
+
+/* Sorts the choices (t, j), 0 <= t < tokens, 0 <= j < top, by their expert ids[t, j]
+ * (`id_bytes` 4 or 8, signed; an id outside [0, experts) is no choice):
+ *   offsets [experts + 1]: expert e has rows [offsets[e], offsets[e + 1]) (as
+ *     fp8z1_ffn_forward takes them, over tokens * top rows);
+ *   place [tokens, top]: the row of choice (t, j), -1 where there is none.
+ * An expert's rows are in the order of the choices; an expert may be chosen twice by a
+ * token and has two rows then.  tokens == 0 writes the offsets alone.
+ * Errors: EINVAL (null, tokens < 0, tokens * top > 2^30, top outside 1 .. 64, experts
+ * outside 1 .. 1024, id_bytes), EALIGN, ECUDA. */
+int fp8z1_route(const void* ids, int32_t id_bytes, int64_t tokens, int64_t top, int64_t experts, int32_t* offsets,
+                int32_t* place, void* stream);
+
+/* rows[place[t, j]] = x[t], bit for bit; rows from offsets[experts] to tokens * top are
+ * cleared.  x: [tokens, dim], rows: [tokens * top, dim], both `type`.  tokens == 0 enqueues
+ * nothing.  Errors: EINVAL (as fp8z1_route, dim outside 1 .. 2^23, type, strides), EALIGN, ECUDA. */
+int fp8z1_dispatch(int64_t tokens, int64_t top, int64_t experts, int64_t dim, const void* x, int32_t type, int64_t ld_x,
+                   const int32_t* offsets, const int32_t* place, void* rows, int64_t ld_rows, void* stream);
+
+/* y[t] = residual[t] + sum_j weight[t, j] * rows[place[t, j]] over the choices that have a
+ * row, in FP32 in the order of j, the residual last, rounded once to `type`.  weight: FP32
+ * [tokens, top], NULL for 1 (which is fp8z1_dispatch's gradient); residual NULL: none; y may
+ * be residual itself.  Errors: as fp8z1_dispatch. */
+int fp8z1_combine(int64_t tokens, int64_t top, int64_t dim, const void* rows, int32_t type, int64_t ld_rows,
+                  const int32_t* place, const float* weight, const void* residual, int64_t ld_residual, void* y,
+                  int64_t ld_y, void* stream);
+
+/* The gradients of sum(dy * y) of fp8z1_combine:
+ *   d_rows[place[t, j]] = weight[t, j] * dy[t]  (rows from offsets[experts] on are cleared),
+ *   d_weight[t, j] = sum over the columns of dy[t] * rows[place[t, j]], FP32, 0 without a row.
+ * The residual's is dy.  Results repeat bit for bit.  Errors: as fp8z1_dispatch. */
+int fp8z1_combine_grad(int64_t tokens, int64_t top, int64_t experts, int64_t dim, const void* dy, int32_t type,
+                       int64_t ld_dy, const void* rows, int64_t ld_rows, const int32_t* offsets, const int32_t* place,
+                       const float* weight, void* d_rows, int64_t ld_d, float* d_weight, void* stream);
 
 #ifdef __cplusplus
 }
