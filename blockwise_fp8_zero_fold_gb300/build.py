@@ -24,9 +24,10 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8z1.so")
 LIB_CHECKED = os.path.join(PKG, "libfp8z1_checked.so")
 SOURCES = ["layout.cpp", "fold.cu", "norm.cu", "step.cu", "step_full.cu", "step_pad.cu", "mx.cu", "embed.cu", "ffn.cu",
-           "ffn_gemm.cu", "ffn_gemv.cu", "ffn_wgrad.cu", "distill.cu", "rms_norm.cu", "route.cu"]
+           "ffn_gemm.cu", "ffn_gemv.cu", "ffn_wgrad.cu", "distill.cu", "rms_norm.cu", "route.cu",
+           "linear.cu", "linear_gemm.cu", "linear_wgrad.cu"]
 HEADERS = ["internal.h", "checked.cuh", "update.cuh", "step_args.h", "step_kernel.cuh", "ops_common.cuh",
-           "ffn.cuh", "tc.cuh"]
+           "ffn.cuh", "linear.cuh", "tc.cuh"]
 PUBLIC = ["fp8z1.h", "fp8z1_ops.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

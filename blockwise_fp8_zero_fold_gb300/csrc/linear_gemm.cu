@@ -1,0 +1,750 @@
+// The products of rows with an FP8 weight, y = act(x w + bias) + residual.
+//
+// A row is one FP8 number an element with a scale for every 128 (8-bit rows), or a pair
+// of them (BF16 rows: E4M3 and E5M2 hold their 8 bits; FP32 rows, rounded to 9 bits: E4M3
+// twice), so the weight's codes enter the tensor cores as they are:
+//
+//   sum_k x_k w_kn = sum over blocks b of 128 of k  s_b c_bn  sum_{k in b} (hi + lo)_k w_kn.
+//
+// The inner sums are exact products accumulated in FP32 in tensor memory; other
+// warps scale each block's and add it to the tile's sums in registers while the
+// next is multiplied.
+//
+// Many rows: a pair of CTAs has 256 rows x 256 columns, each the sums of 128 rows and half
+// the weight's columns in shared memory, as a CTA alone would need 96 bytes of operands a
+// clock for 8-bit rows, more than L2 delivers to every SM at once.
+//
+// Few rows: the weight's columns take the rows' place, 128 to a CTA, and 16 to 128 rows of x
+// the columns': the products' time follows the rows, and the codes are what is read.  K is
+// split over a cluster's CTAs, whose sums are added in shared memory in their order.
+#include <cooperative_groups.h>
+
+#include "linear.cuh"
+
+namespace fp8z1 {
+namespace linear {
+namespace {
+
+using namespace tc;
+using ffn::after_previous;
+using ffn::next_may_start;
+namespace cg = cooperative_groups;
+
+__device__ unsigned g_timeouts;
+#if FP8Z1_CHECKED
+__device__ unsigned g_stall;  // bit 0: many rows, 1: few rows: the first CTA does not announce its first sums
+#endif
+
+constexpr uint32_t kOperand = 128 * 128;  // bytes of a 128 x 128 operand tile
+constexpr int kStagePitch = 48;           // of a row's 32 bytes on their way out
+
+struct Args {
+    Out o;
+    const float* a_scale;
+    int64_t scale_row, scale_block;
+    const float* b_scale;
+    int32_t b_col, b_step;  // strides of b_scale: a block of columns, a block of k
+    int32_t b_cols;         // blocks of columns
+    int32_t k_blocks;
+    uint32_t idesc[2];      // of the products with hi, with lo
+    int32_t m_tiles, n_tiles;
+    int32_t splits;         // few rows: CTAs of a cluster
+};
+
+// ---- what becomes of the sums -----------------------------------------------------------
+
+// 16 neighbouring columns of a row a lane (a warp: 32 rows).  `rows`: how many of the warp's
+// rows exist, `row` and `n0` the lane's row and first column.
+__device__ __forceinline__ void finish(const Out& o, float (&v)[16], int64_t row, int lane, int rows, int64_t n0, uint8_t* stage)
+{
+    const bool here = lane < rows, whole = n0 + 16 <= o.N;
+    if (o.bias)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (n0 + j < o.N) v[j] += __ldg(o.bias + n0 + j);
+    if (o.pre && here) {
+        float* p = o.pre + row * o.N + n0;
+        if (whole && o.vec_pre) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (n0 + j < o.N) p[j] = v[j];
+        }
+    }
+    if (o.act != FP8Z1_ACT_NONE)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = activate(v[j], o.act);
+    if (o.residual && here) {
+        const bf16* p = o.residual + row * o.ld_r + n0;
+        if (whole && o.vec_r) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 u = *reinterpret_cast<const uint4*>(p + 8 * h);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[8 * h + 2 * j] += __uint_as_float(w[j] << 16);
+                    v[8 * h + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (n0 + j < o.N) v[j] += to_float(p[j]);
+        }
+    }
+    if (!whole || !o.vec_y) {
+        if (!here) return;
+        if (o.f32) {
+            float* p = static_cast<float*>(o.y) + row * o.ld_y + n0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (n0 + j < o.N) p[j] = v[j];
+        } else {
+            bf16* p = static_cast<bf16*>(o.y) + row * o.ld_y + n0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (n0 + j < o.N) p[j] = __float2bfloat16_rn(v[j]);
+        }
+        return;
+    }
+    // 32 bytes of each row through shared memory: two lanes store a row's, a sector is written whole
+    const int64_t first = row - lane;
+    uint8_t* to;
+    int64_t pitch;
+    if (o.f32) {
+        to = reinterpret_cast<uint8_t*>(static_cast<float*>(o.y) + first * o.ld_y + n0);
+        pitch = o.ld_y * 4;
+    } else {
+        to = reinterpret_cast<uint8_t*>(static_cast<bf16*>(o.y) + first * o.ld_y + n0);
+        pitch = o.ld_y * 2;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint4 w[2];
+        if (o.f32) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                w[q] = make_uint4(__float_as_uint(v[8 * h + 4 * q]), __float_as_uint(v[8 * h + 4 * q + 1]),
+                                  __float_as_uint(v[8 * h + 4 * q + 2]), __float_as_uint(v[8 * h + 4 * q + 3]));
+        } else {
+            if (h) break;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t u[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __nv_bfloat162 two = __floats2bfloat162_rn(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]);
+                    u[j] = *reinterpret_cast<const uint32_t*>(&two);
+                }
+                w[q] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+        }
+        *reinterpret_cast<uint4*>(stage + lane * kStagePitch) = w[0];
+        *reinterpret_cast<uint4*>(stage + lane * kStagePitch + 16) = w[1];
+        __syncwarp();
+#pragma unroll
+        for (int r = lane >> 1; r < 32; r += 16)
+            if (r < rows)
+                *reinterpret_cast<uint4*>(to + r * pitch + 32 * h + (lane & 1) * 16) =
+                    *reinterpret_cast<const uint4*>(stage + r * kStagePitch + (lane & 1) * 16);
+        __syncwarp();
+    }
+}
+
+// ---- many rows ------------------------------------------------------------------------------
+
+constexpr int kCols = 256;
+constexpr int kManyThreads = 640;  // 4 warps that feed, 16 that add up
+template <int kTerms>
+struct Many {
+    static constexpr int kStages = kTerms == 2 ? 4 : 6;
+    static constexpr uint32_t kStageBytes = (kTerms + 1) * kOperand;  // hi, lo, half of the weight's columns
+    // stages, barriers, factors, rows on their way out
+    static constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 256 + 4096 + 16 * 32 * kStagePitch;
+};
+
+template <int kTerms, bool kKMajor>
+__global__ void __launch_bounds__(kManyThreads, 1)
+many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ CUtensorMap map_lo,
+            const __grid_constant__ CUtensorMap map_w, const __grid_constant__ Args a)
+{
+    constexpr int kStages = Many<kTerms>::kStages;
+    constexpr uint32_t kStageBytes = Many<kTerms>::kStageBytes;
+    extern __shared__ uint8_t smem_raw[];
+    next_may_start();
+    const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+    const uint32_t extra = base + kStages * kStageBytes;
+    // extra: full, empty [kStages], accumulators ready, free [2], factors ready, read [4], tensor memory base; factors
+    // [4][2][128]; rows on their way out
+    const uint32_t bar_full = extra, bar_empty = extra + 48, bar_acc = extra + 96, bar_free = extra + 112,
+                   bar_factors = extra + 128, bar_read = extra + 160, factors = extra + 256;
+    uint8_t* extra_ptr = smem_raw + (extra - smem_addr(smem_raw));
+    volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(extra_ptr + 192);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = (int)cluster_rank();  // of the pair
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(bar_full + 8 * i, 1);
+            bar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(bar_acc + 8 * i, 1);
+            bar_init(bar_free + 8 * i, 32);  // the adding warps of both CTAs
+        }
+        for (int i = 0; i < 4; ++i) {
+            bar_init(bar_factors + 8 * i, 64);
+            bar_init(bar_read + 8 * i, 16);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+        prefetch_map(&map_hi);
+        if (kTerms == 2) prefetch_map(&map_lo);
+        prefetch_map(&map_w);
+    }
+    if (warp == 2) tmem_alloc<2, 512>(extra + 192);
+    fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();  // the other CTA counts on this one's barriers from here on
+    fence_after();
+    after_previous();
+    const uint32_t tmem = *tmem_at;
+    const int64_t total = (int64_t)a.m_tiles * a.n_tiles, i0 = blockIdx.x / 2, step = gridDim.x / 2;
+    bool ok = true;
+
+    if (warp < 4) {
+        regs_less<48>();
+        if (warp == 0 && lane == 0) {
+            Turn<kStages> turn;
+            for (int64_t i = i0; i < total && ok; i += step) {
+                const int n = (int)(i / a.m_tiles), m = (int)(i - (int64_t)n * a.m_tiles);
+                const int row = m * 256 + sub * 128, col = n * kCols + sub * 128;
+                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next()) {
+                    if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    // both CTAs' copies are counted in the first one, whose thread multiplies
+                    if (sub == 0) bar_expect(bar_full + 8 * turn.slot, 2 * kStageBytes);
+                    const uint32_t full = first_of_pair(bar_full + 8 * turn.slot), dst = base + turn.slot * kStageBytes;
+                    load_2d_pair(dst, &map_hi, full, kb * 128, row);
+                    if (kTerms == 2) load_2d_pair(dst + kOperand, &map_lo, full, kb * 128, row);
+                    if (kKMajor)
+                        load_2d_pair(dst + kTerms * kOperand, &map_w, full, kb * 128, col);
+                    else
+                        load_2d_pair(dst + kTerms * kOperand, &map_w, full, col, kb * 128);
+                }
+            }
+            // the copies in flight are read before the CTA ends, whatever became of the other warps
+            for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
+        } else if (warp == 1 && lane == 0 && sub == 0) {
+            Turn<kStages> turn;
+            Turn<2> acc;
+            for (int64_t i = i0; i < total && ok; i += step) {
+                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next(), acc.next()) {
+                    if (!bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) ||
+                        !bar_wait(bar_full + 8 * turn.slot, turn.phase)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint32_t src = base + turn.slot * kStageBytes, d = tmem + acc.slot * kCols;
+#pragma unroll
+                    for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint64_t da = operand(src + t * kOperand + k * 32, 1024, 16);
+                            // K-major: 8 columns are 1024 bytes; N-major: 8 k are
+                            const uint64_t db = operand(src + kTerms * kOperand + k * (kKMajor ? 32 : 4096), 1024, 16);
+                            mma_f8_pair(d, da, db, a.idesc[t], t + k > 0);
+                        }
+                    commit_pair(bar_empty + 8 * turn.slot);
+#if FP8Z1_CHECKED
+                    if (g_stall & 1 && blockIdx.x == 0 && i == i0 && kb == 0) continue;
+#endif
+                    commit_pair(bar_acc + 8 * acc.slot);
+                }
+            }
+            // every product issued ends, and its sums are read, before the tensor memory is freed
+            for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
+        } else if (warp >= 2) {
+            // the factors of each step, s_b c_bn of both chunks of 128 columns for two rows a thread
+            Turn<4> turn;
+            const int mine = threadIdx.x - 64;
+            for (int64_t i = i0; i < total && ok; i += step) {
+                const int n = (int)(i / a.m_tiles), m = (int)(i - (int64_t)n * a.m_tiles);
+                const int64_t row = (int64_t)m * 256 + sub * 128 + mine;  // rows and columns past the end: any others' scales
+                const float* pa = a.a_scale + min(row, a.o.T - 1) * a.scale_row;
+                const float* pb = a.a_scale + min(row + 64, a.o.T - 1) * a.scale_row;
+                const float* p0 = a.b_scale + (int64_t)min(n * 2, a.b_cols - 1) * a.b_col;
+                const float* p1 = a.b_scale + (int64_t)min(n * 2 + 1, a.b_cols - 1) * a.b_col;
+                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next()) {
+                    const float va = pa[kb * a.scale_block], vb = pb[kb * a.scale_block], v0 = p0[(int64_t)kb * a.b_step],
+                                v1 = p1[(int64_t)kb * a.b_step];
+                    if (!bar_wait(bar_read + 8 * turn.slot, turn.phase ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t f = factors + turn.slot * 1024 + mine * 4;
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f), "f"(va * v0) : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f + 256), "f"(vb * v0) : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f + 512), "f"(va * v1) : "memory");
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f + 768), "f"(vb * v1) : "memory");
+                    bar_arrive(bar_factors + 8 * turn.slot);
+                }
+            }
+        }
+    } else {
+        regs_more<104>();
+        const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+        uint8_t* stage = extra_ptr + 256 + 4096 + (warp - 4) * 32 * kStagePitch;
+        Turn<2> acc;
+        Turn<4> turn;
+        for (int64_t i = i0; i < total; i += step) {
+            const int n = (int)(i / a.m_tiles), m = (int)(i - (int64_t)n * a.m_tiles);
+            uint64_t sums2[2][16];  // pairs of columns
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sums2[c][j] = 0;
+            for (int kb = 0; kb < a.k_blocks; ++kb, acc.next(), turn.next()) {
+                // a warp's lanes agree on the outcome: the loads below are warp-wide
+                ok = ok && __all_sync(0xffffffffu, bar_wait(bar_factors + 8 * turn.slot, turn.phase) &&
+                                                       bar_wait(bar_acc + 8 * acc.slot, acc.phase));
+                if (!ok) break;
+                fence_after();
+                float f0, f1;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f0) : "r"(factors + turn.slot * 1024 + row * 4));
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f1) : "r"(factors + turn.slot * 1024 + 512 + row * 4));
+                const uint64_t f[2] = {pair(f0, f0), pair(f1, f1)};
+                const uint32_t t = tmem + acc.slot * kCols + lanes + group * 32;
+                // columns 32 group + {0, 16, 128, 144} ..
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t r[16];
+                    tmem_load(t + q / 2 * 128 + q % 2 * 16, r);
+                    tmem_wait(r);
+                    if (q == 3) {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            bar_arrive_pair(first_of_pair(bar_free + 8 * acc.slot));
+                            bar_arrive(bar_read + 8 * turn.slot);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        sums2[q / 2][q % 2 * 8 + j] =
+                            fma_pair(pair(r[2 * j], r[2 * j + 1]), f[q / 2], sums2[q / 2][q % 2 * 8 + j]);
+                }
+            }
+            // a wait ran out: this tile and the pair's further ones are NaN
+            if (!ok)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sums2[j / 16][j % 16] = pair(NAN, NAN);
+            const int64_t at = (int64_t)m * 256 + sub * 128 + row;
+            const int rows = (int)min(max(a.o.T - (at - lane), (int64_t)0), (int64_t)32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t n0 = (int64_t)n * kCols + q / 2 * 128 + group * 32 + q % 2 * 16;
+                if (n0 >= a.o.N || rows == 0) continue;  // with the whole warp
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 two = unpair(sums2[q / 2][q % 2 * 8 + j]);
+                    v[2 * j] = two.x;
+                    v[2 * j + 1] = two.y;
+                }
+                finish(a.o, v, at, lane, rows, n0, stage);
+            }
+        }
+    }
+    if (!ok) atomicAdd(&g_timeouts, 1u);
+    fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while the other may still write to it
+    fence_after();
+    if (warp == 2) tmem_free<2, 512>(tmem);
+}
+
+// ---- few rows ---------------------------------------------------------------------------------
+
+// kN rows of x; 4 warps feed, 4 or (from 64 rows) 8 add up.  Two CTAs share an SM up to 64 rows.
+template <int kTerms, int kN>
+struct Few {
+    static constexpr int kGroups = kN >= 64 ? 2 : 1, kMine = kN / kGroups;  // rows of an adding warp
+    static constexpr int kThreads = 128 + 128 * kGroups;
+    static constexpr uint32_t kRowBytes = kN * 128;  // of a term
+    static constexpr uint32_t kStageBytes = kOperand + kTerms * kRowBytes;
+    static constexpr int kResident = kN <= 64 ? 2 : 1;
+    static constexpr int kStages = kN <= 64 ? (int)(100 * 1024 / kStageBytes) : 4;
+    static constexpr uint32_t kAt = 256, kSmem = kStages * kStageBytes + 1024 + kAt + 4 * kN * 4;
+    static constexpr int kTmem = 2 * kN < 32 ? 32 : 2 * kN;
+    static_assert(kStages >= 3 && kStages <= 6 && kStages * kStageBytes >= kN * 512, "the sums of a split fit the stages");
+};
+
+template <int kTerms, int kN, bool kKMajor>
+__global__ void __launch_bounds__(Few<kTerms, kN>::kThreads, Few<kTerms, kN>::kResident)
+few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ CUtensorMap map_lo,
+           const __grid_constant__ CUtensorMap map_w, const __grid_constant__ Args a)
+{
+    using S = Few<kTerms, kN>;
+    constexpr int kStages = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    next_may_start();
+    const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+    const uint32_t extra = base + kStages * S::kStageBytes;
+    // extra: full, empty [kStages], accumulators ready, free [2], factors ready, read [4], tensor memory base, whether
+    // a wait ran out; factors [4][kN]
+    const uint32_t bar_full = extra, bar_empty = extra + 48, bar_acc = extra + 96, bar_free = extra + 112,
+                   bar_factors = extra + 128, bar_read = extra + 160, factors = extra + S::kAt;
+    uint8_t* extra_ptr = smem_raw + (extra - smem_addr(smem_raw));
+    volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(extra_ptr + 192);
+    uint32_t* failed = reinterpret_cast<uint32_t*>(extra_ptr + 196);
+    float* sums_at = reinterpret_cast<float*>(extra_ptr - kStages * S::kStageBytes);  // [kN][128], over the stages
+    cg::cluster_group cluster = cg::this_cluster();
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = a.splits > 1 ? (int)cluster.block_rank() : 0;
+    const int n = blockIdx.x / a.splits;
+    const int token0 = blockIdx.y * kN;
+    const int k0 = a.k_blocks * split / a.splits, k1 = a.k_blocks * (split + 1) / a.splits;
+    if (threadIdx.x == 0) {
+        *failed = 0;
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(bar_full + 8 * i, 1);
+            bar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(bar_acc + 8 * i, 1);
+            bar_init(bar_free + 8 * i, 4 * S::kGroups);
+        }
+        for (int i = 0; i < 4; ++i) {
+            bar_init(bar_factors + 8 * i, 64);
+            bar_init(bar_read + 8 * i, 4 * S::kGroups);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+        prefetch_map(&map_hi);
+        if (kTerms == 2) prefetch_map(&map_lo);
+        prefetch_map(&map_w);
+    }
+    if (warp == 2) tmem_alloc<1, S::kTmem>(extra + 192);
+    fence_before();
+    __syncthreads();
+    __syncwarp();
+    fence_after();
+    const uint32_t tmem = *tmem_at;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            auto codes = [&](int kb, uint32_t full, uint32_t dst) {
+                if (kKMajor)
+                    load_2d(dst, &map_w, full, kb * 128, n * 128);
+                else
+                    load_2d(dst, &map_w, full, n * 128, kb * 128);
+            };
+            // the first codes are on their way before the kernel ahead has ended: it does not write them
+            const int ahead = min(kStages, k1 - k0);
+            for (int i = 0; i < ahead; ++i) {
+                bar_expect(bar_full + 8 * i, S::kStageBytes);
+                codes(k0 + i, bar_full + 8 * i, base + i * S::kStageBytes);
+            }
+            after_previous();
+            Turn<kStages> turn;
+            for (int kb = k0; kb < k1; ++kb, turn.next()) {
+                const uint32_t full = bar_full + 8 * turn.slot, dst = base + turn.slot * S::kStageBytes;
+                if (kb >= k0 + ahead) {
+                    if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    bar_expect(full, S::kStageBytes);
+                    codes(kb, full, dst);
+                }
+                load_2d(dst + kOperand, &map_hi, full, kb * 128, token0);
+                if (kTerms == 2) load_2d(dst + kOperand + S::kRowBytes, &map_lo, full, kb * 128, token0);
+            }
+            // the copies in flight are read before the CTA ends, whatever became of the other warps
+            for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            Turn<kStages> turn;
+            Turn<2> acc;
+            for (int kb = k0; kb < k1; ++kb, turn.next(), acc.next()) {
+                if (!bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) || !bar_wait(bar_full + 8 * turn.slot, turn.phase)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const uint32_t src = base + turn.slot * S::kStageBytes, d = tmem + acc.slot * kN;
+#pragma unroll
+                for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t da = operand(src + k * (kKMajor ? 32 : 4096), 1024, 16);
+                        const uint64_t db = operand(src + kOperand + t * S::kRowBytes + k * 32, 1024, 16);
+                        mma_f8(d, da, db, a.idesc[t], t + k > 0);
+                    }
+                commit(bar_empty + 8 * turn.slot);
+#if FP8Z1_CHECKED
+                if (g_stall & 2 && blockIdx.x + blockIdx.y == 0 && kb == k0) continue;
+#endif
+                commit(bar_acc + 8 * acc.slot);
+            }
+            // every product issued ends, and its sums are read, before the tensor memory is freed
+            for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
+        }
+    } else if (warp < 4) {
+        after_previous();
+        Turn<4> turn;
+        const int mine = threadIdx.x - 64;
+        constexpr int kEach = kN <= 64 ? 1 : 2;
+        const float* pb = a.b_scale + (int64_t)n * a.b_col;
+        for (int kb = k0; kb < k1; ++kb, turn.next()) {
+            const float c = pb[(int64_t)kb * a.b_step];
+            float v[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int64_t row = min((int64_t)token0 + min(mine + 64 * i, kN - 1), a.o.T - 1);
+                v[i] = a.a_scale[row * a.scale_row + kb * a.scale_block];
+            }
+            if (!bar_wait(bar_read + 8 * turn.slot, turn.phase ^ 1)) {
+                ok = false;
+                break;
+            }
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (mine + 64 * i < kN)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(factors + (turn.slot * kN + mine + 64 * i) * 4), "f"(v[i] * c)
+                                 : "memory");
+            bar_arrive(bar_factors + 8 * turn.slot);
+        }
+    }
+    const int adder = threadIdx.x - 128, group = adder >> 7, out = adder & 127;  // the sums' column of y in this CTA
+    float sums[S::kMine];
+    if (warp >= 4) {
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+        Turn<2> acc;
+        Turn<4> turn;
+#pragma unroll
+        for (int j = 0; j < S::kMine; ++j) sums[j] = 0.0f;
+        for (int kb = k0; kb < k1; ++kb, acc.next(), turn.next()) {
+            ok = ok && __all_sync(0xffffffffu, bar_wait(bar_factors + 8 * turn.slot, turn.phase) &&
+                                                   bar_wait(bar_acc + 8 * acc.slot, acc.phase));
+            if (!ok) break;
+            fence_after();
+            const uint32_t t = tmem + acc.slot * kN + lanes + group * S::kMine;
+            const uint32_t f = factors + (turn.slot * kN + group * S::kMine) * 4;
+#pragma unroll
+            for (int q = 0; q < S::kMine / 16; ++q) {
+                uint32_t r[16];
+                tmem_load(t + q * 16, r);
+                tmem_wait(r);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    float4 s;
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(s.x), "=f"(s.y), "=f"(s.z), "=f"(s.w)
+                                 : "r"(f + (q * 16 + j) * 4));
+                    sums[q * 16 + j] = __fmaf_rn(__uint_as_float(r[j]), s.x, sums[q * 16 + j]);
+                    sums[q * 16 + j + 1] = __fmaf_rn(__uint_as_float(r[j + 1]), s.y, sums[q * 16 + j + 1]);
+                    sums[q * 16 + j + 2] = __fmaf_rn(__uint_as_float(r[j + 2]), s.z, sums[q * 16 + j + 2]);
+                    sums[q * 16 + j + 3] = __fmaf_rn(__uint_as_float(r[j + 3]), s.w, sums[q * 16 + j + 3]);
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(bar_free + 8 * acc.slot);
+                bar_arrive(bar_read + 8 * turn.slot);
+            }
+        }
+    }
+    if (!ok) {
+        atomicAdd(&g_timeouts, 1u);
+        *failed = 1;
+    }
+    const Out& o = a.o;
+    const int64_t col = (int64_t)n * 128 + out;
+    const float bias = warp >= 4 && o.bias && col < o.N ? __ldg(o.bias + col) : 0.0f;
+    // row `j` of the CTA's; neighbouring lanes are neighbouring columns
+    auto store = [&](int j, float z) {
+        const int64_t row = token0 + j;
+        if (row >= o.T || col >= o.N) return;
+        z += bias;
+        if (o.pre) o.pre[row * o.N + col] = z;
+        float v = activate(z, o.act);
+        if (o.residual) v += to_float(o.residual[row * o.ld_r + col]);
+        if (o.f32)
+            static_cast<float*>(o.y)[row * o.ld_y + col] = v;
+        else
+            static_cast<bf16*>(o.y)[row * o.ld_y + col] = __float2bfloat16_rn(v);
+    };
+    if (a.splits > 1) {
+        // every stage has been read: the last sums came after the last product
+        if (warp >= 4)
+#pragma unroll
+            for (int j = 0; j < S::kMine; ++j) sums_at[(group * S::kMine + j) * 128 + out] = sums[j];
+        cluster.sync();
+        if (warp >= 4) {
+            bool whole = true;
+            for (int q = 0; q < a.splits; ++q) whole &= *cluster.map_shared_rank(failed, q) == 0;
+            const int rows = (int)min((int64_t)kN, o.T - token0);
+            for (int j = split + group * a.splits; j < rows; j += S::kGroups * a.splits) {
+                float z = 0.0f;
+#pragma unroll 4
+                for (int q = 0; q < a.splits; ++q) z += cluster.map_shared_rank(sums_at, q)[j * 128 + out];
+                store(j, whole ? z : NAN);
+            }
+        }
+        cluster.sync();  // no CTA leaves before its sums are read
+    } else {
+        __syncthreads();  // `failed` is set
+        if (warp >= 4) {
+            const bool whole = *failed == 0;
+#pragma unroll
+            for (int j = 0; j < S::kMine; ++j) store(group * S::kMine + j, whole ? sums[j] : NAN);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    __syncwarp();
+    fence_after();
+    if (warp == 2) tmem_free<1, S::kTmem>(tmem);
+}
+
+// ---- launches -----------------------------------------------------------------------------------
+
+// Tiles of `box_rows` rows x 128 bytes of row-major bytes.
+int map_bytes(CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t cols, int64_t pitch, int box_rows)
+{
+    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, stride[1] = {(uint64_t)pitch};
+    const uint32_t box[2] = {128, (uint32_t)box_rows};
+    return ffn::tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p, dims, stride, box);
+}
+
+int maps(CUtensorMap* hi, CUtensorMap* lo, CUtensorMap* wm, const Rows& x, const Weight& w, int64_t K, int box_rows)
+{
+    // bytes of a row behind its K (a pair's padding is zeros, of 8-bit rows the map ends there)
+    const int64_t cols = x.lo ? x.pitch : K;
+    int st = map_bytes(hi, x.hi, x.T, cols, x.pitch, box_rows);
+    if (st != FP8Z1_OK) return st;
+    if ((st = map_bytes(lo, x.lo ? x.lo : x.hi, x.T, cols, x.pitch, box_rows)) != FP8Z1_OK) return st;
+    return map_bytes(wm, w.codes, w.R, w.C, w.C, 128);
+}
+
+template <int kTerms, bool kKMajor>
+int launch_many(const Rows& x, const Weight& w, Args a, cudaStream_t s)
+{
+    CUtensorMap hi, lo, wm;
+    const int st = maps(&hi, &lo, &wm, x, w, w.K(), 128);
+    if (st != FP8Z1_OK) return st;
+    a.m_tiles = (int32_t)ceil_div(x.T, 256);
+    a.n_tiles = (int32_t)ceil_div(a.o.N, kCols);
+    for (int t = 0; t < 2; ++t)
+        a.idesc[t] = instruction_of(256, kCols, false, !kKMajor, t && x.lo_format == Lo::kE5M2, 0);
+    return ffn::launch_persistent<many_kernel<kTerms, kKMajor>, 2>(kManyThreads, Many<kTerms>::kSmem,
+                                                                    (int64_t)a.m_tiles * a.n_tiles, s, hi, lo, wm, a);
+}
+
+// CTAs along K: as few rounds of K steps as the SMs' CTAs need, a CTA's start and end worth 4 of them.
+int splits_of(int64_t groups, int64_t slots, int64_t k_blocks)
+{
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int n = 1; n <= 8 && n <= k_blocks; n *= 2) {
+        const int64_t t = ceil_div(groups * n, slots) * (ceil_div(k_blocks, n) + 4);
+        if (t < least) least = t, best = n;
+    }
+    return best;
+}
+
+template <int kTerms, int kN, bool kKMajor>
+int launch_few(const Rows& x, const Weight& w, Args a, cudaStream_t s)
+{
+    using S = Few<kTerms, kN>;
+    CUtensorMap hi, lo, wm;
+    const int st = maps(&hi, &lo, &wm, x, w, w.K(), kN);
+    if (st != FP8Z1_OK) return st;
+    a.n_tiles = (int32_t)ceil_div(a.o.N, 128);
+    a.m_tiles = (int32_t)ceil_div(x.T, kN);
+    a.splits = splits_of((int64_t)a.n_tiles * a.m_tiles, (int64_t)kSms * S::kResident, a.k_blocks);
+    for (int t = 0; t < 2; ++t)
+        a.idesc[t] = instruction_of(128, kN, !kKMajor, false, 0, t && x.lo_format == Lo::kE5M2);
+    if (!allow_smem<few_kernel<kTerms, kN, kKMajor>>((int)S::kSmem)) return FP8Z1_ECUDA;
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)a.splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = dim3((unsigned)(a.n_tiles * a.splits), (unsigned)a.m_tiles);
+    c.blockDim = dim3(S::kThreads);
+    c.dynamicSmemBytes = S::kSmem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = x.lo ? 2 : 1;  // 8-bit rows are the caller's: no kernel of this call goes ahead
+    count_launch();
+    if (cudaLaunchKernelEx(&c, few_kernel<kTerms, kN, kKMajor>, hi, lo, wm, a) != cudaSuccess) {
+        cudaGetLastError();
+        return FP8Z1_ECUDA;
+    }
+    return launch_status();
+}
+
+template <int kTerms, bool kKMajor>
+int launch(const Rows& x, const Weight& w, const Args& a, cudaStream_t s)
+{
+    if (x.T <= 16) return launch_few<kTerms, 16, kKMajor>(x, w, a, s);
+    if (x.T <= 32) return launch_few<kTerms, 32, kKMajor>(x, w, a, s);
+    if (x.T <= 64) return launch_few<kTerms, 64, kKMajor>(x, w, a, s);
+    // 128 columns by 128 rows a CTA while that leaves no SM twice as much to do as pairs of 256 x 256 would
+    const int64_t few = ceil_div(x.T, 128) * ceil_div(a.o.N, 128);
+    if (x.T <= 128 || few <= 2 * kSms) return launch_few<kTerms, 128, kKMajor>(x, w, a, s);
+    return launch_many<kTerms, kKMajor>(x, w, a, s);
+}
+
+}  // namespace
+
+int launch_product(const Rows& x, const Weight& w, const Out& o, cudaStream_t s)
+{
+    Args a = {};
+    a.o = o;
+    a.a_scale = x.scale;
+    a.scale_row = x.scale_row;
+    a.scale_block = x.scale_block;
+    a.b_scale = w.scale;
+    const int32_t sc = (int32_t)ceil_div(w.C, 128);
+    a.b_col = w.k_major ? sc : 1;
+    a.b_step = w.k_major ? 1 : sc;
+    a.b_cols = (int32_t)ceil_div(o.N, 128);
+    a.k_blocks = (int32_t)ceil_div(w.K(), kBlock);
+    a.splits = 1;
+    if (x.lo) return w.k_major ? launch<2, true>(x, w, a, s) : launch<2, false>(x, w, a, s);
+    return w.k_major ? launch<1, true>(x, w, a, s) : launch<1, false>(x, w, a, s);
+}
+
+int read_timeouts_product(unsigned* n)
+{
+    return cudaMemcpyFromSymbol(n, g_timeouts, 4) == cudaSuccess ? FP8Z1_OK : FP8Z1_ECUDA;
+}
+
+#if FP8Z1_CHECKED
+int stall_product(unsigned kernels)
+{
+    return cudaMemcpyToSymbol(g_stall, &kernels, 4) == cudaSuccess ? FP8Z1_OK : FP8Z1_ECUDA;
+}
+#endif
+
+}  // namespace linear
+}  // namespace fp8z1

@@ -52,6 +52,9 @@ bool allow_smem(int bytes)
     return true;
 }
 
+// out[c] = sum over i < n of part[i, c], [n, cols] FP32, in a fixed order (rms_norm.cu).
+int launch_column_sum(const float* part, int n, int64_t cols, float* out, cudaStream_t s);
+
 // The SM count of the current device (0 when it cannot be read).
 inline int sm_count_here()
 {

@@ -287,20 +287,21 @@ __global__ void __launch_bounds__(kWarpRow ? 256 : 512) norm_grad_kernel(const G
 }
 
 // The sums of `n` rows of partial sums: 32 columns a CTA, 32 threads a column, in a fixed order.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int n, int dim, float* out)
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int n, int64_t dim, float* out)
 {
     __shared__ float sums[32][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t c0 = (int64_t)blockIdx.x * 32, c = c0 + x;
     float s = 0.0f;
     if (c < dim)
 #pragma unroll 8
-        for (int i = y; i < n; i += 32) s += part[(int64_t)i * dim + c];
+        for (int i = y; i < n; i += 32) s += part[i * dim + c];
     sums[y][x] = s;
     __syncthreads();
     s = sums[x][y];  // the warp's column
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (x == 0 && blockIdx.x * 32 + y < dim) out[blockIdx.x * 32 + y] = s;
+    if (x == 0 && c0 + y < dim) out[c0 + y] = s;
 }
 
 int check(int64_t rows, int64_t dim, int32_t type, float eps)
@@ -376,6 +377,14 @@ int64_t grad_ctas(int64_t rows, int64_t dim)
 }
 
 }  // namespace
+
+int launch_column_sum(const float* part, int n, int64_t cols, float* out, cudaStream_t s)
+{
+    count_launch();
+    column_sum_kernel<<<(unsigned)ceil_div(cols, 32), 1024, 0, s>>>(part, n, cols, out);
+    return launch_status();
+}
+
 }  // namespace fp8z1
 
 using namespace fp8z1;
@@ -438,7 +447,5 @@ extern "C" int fp8z1_rms_norm_grad(int64_t rows, int64_t dim, const void* dy, in
     const GradArgs a = {rows, (int)dim, eps, 1.0f / (float)dim, ld_dy, ld_total, ld_dt, ld_dx, dy, total, d_total, weight,
                         dx, static_cast<float*>(workspace)};
     if ((st = by_shape<Grad>(type, vec, each, threads == 32, a, threads, ctas, s)) != FP8Z1_OK) return st;
-    count_launch();
-    column_sum_kernel<<<(unsigned)ceil_div(dim, 32), 1024, 0, s>>>(a.part, (int)ctas, (int)dim, d_weight);
-    return launch_status();
+    return launch_column_sum(a.part, (int)ctas, dim, d_weight, s);
 }

@@ -34,7 +34,8 @@ LAYOUT_HOST_ONLY = 1
 DEVSTATUS_BADPTR = 1
 BUILD_CHECKED = 1
 
-F32, BF16 = 0, 1  # element types of the model operators' activations
+F32, BF16, E4M3 = 0, 1, 2  # element types of the model operators' activations
+ACT_NONE, ACT_SILU, ACT_GELU_TANH = 0, 1, 2
 DISTILL_MAX_TOP = 1024
 
 OK, EINVAL, EALIGN, ENOMEM, ECUDA, ENODEV = 0, -1, -2, -3, -4, -5
@@ -79,6 +80,11 @@ class fp8z1_loss_scaler(C.Structure):
 
 class fp8z1_ffn_dims(C.Structure):
     _fields_ = [(n, C.c_int64) for n in ("tokens", "hidden", "inner", "experts")]
+
+
+class fp8z1_linear_dims(C.Structure):
+    _fields_ = ([(n, C.c_int64) for n in ("tokens", "rows", "cols")]
+                + [(n, C.c_int32) for n in ("transposed", "activation", "x_type", "y_type")])
 
 
 BLOCK_DTYPE = np.dtype([("src_offset", "<i8"), ("param", "<i4"), ("expert", "<i4"),
@@ -161,6 +167,13 @@ _SIGS = {
                                 C.c_int64, _P]),
     "fp8z1_combine_grad": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.c_int64, _P, C.c_int32, C.c_int64, _P, C.c_int64,
                                      _P, _P, _P, _P, C.c_int64, _P, _P]),
+    "fp8z1_linear_sizes": (C.c_int, [C.POINTER(fp8z1_linear_dims), C.POINTER(C.c_int64), C.POINTER(C.c_int64)]),
+    "fp8z1_linear": (C.c_int, [C.POINTER(fp8z1_linear_dims), _P, C.c_int64, _P, _P, _P, _P, _P, C.c_int64, _P, C.c_int64,
+                               _P, _P, _P]),
+    "fp8z1_linear_grad": (C.c_int, [C.POINTER(fp8z1_linear_dims), _P, C.c_int64, _P, C.c_int64, _P, _P, _P, _P, C.c_int64,
+                                    _P, _P, _P, _P]),
+    "fp8z1_linear_timeouts": (C.c_int, [C.POINTER(C.c_uint32)]),
+    "fp8z1_checked_linear_stall": (C.c_int, [C.c_uint32]),
     "fp8z1_strerror": (C.c_char_p, [C.c_int]),
 }
 
@@ -676,3 +689,41 @@ def fp8z1_combine_grad(tokens: int, top: int, experts: int, dim: int, dy, type_:
                                    _at(place), _at(weight), _at(d_rows), ld_d, _at(d_weight), _stream(stream))
     if st:
         raise Fp8z1Error(st, "fp8z1_combine_grad")
+
+
+def fp8z1_linear_sizes(dims: fp8z1_linear_dims):
+    """(forward, backward) workspace bytes."""
+    a, b = C.c_int64(), C.c_int64()
+    st = _op("fp8z1_linear_sizes")(dims, a, b)
+    if st:
+        raise Fp8z1Error(st, "fp8z1_linear_sizes")
+    return a.value, b.value
+
+
+def fp8z1_linear(dims: fp8z1_linear_dims, x, ld_x: int, x_scale, codes, scales, bias, residual, ld_residual: int, y,
+                 ld_y: int, pre, workspace, stream=None):
+    st = _op("fp8z1_linear")(dims, _at(x), ld_x, _at(x_scale), _at(codes), _at(scales), _at(bias), _at(residual),
+                             ld_residual, _at(y), ld_y, _at(pre), _at(workspace), _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_linear")
+
+
+def fp8z1_linear_grad(dims: fp8z1_linear_dims, dy, ld_dy: int, x, ld_x: int, codes, scales, pre, dx, ld_dx: int, d_weight,
+                      d_bias, workspace, stream=None):
+    st = _op("fp8z1_linear_grad")(dims, _at(dy), ld_dy, _at(x), ld_x, _at(codes), _at(scales), _at(pre), _at(dx), ld_dx,
+                                  _at(d_weight), _at(d_bias), _at(workspace), _stream(stream))
+    if st:
+        raise Fp8z1Error(st, "fp8z1_linear_grad")
+
+
+def fp8z1_linear_timeouts() -> int:
+    """Threads of the product's kernels that gave up waiting since the last call
+    (synchronous; 0 in all normal use)."""
+    n = C.c_uint32()
+    _check(lib().fp8z1_linear_timeouts(C.byref(n)), "fp8z1_linear_timeouts")
+    return n.value
+
+
+def fp8z1_checked_linear_stall(kernels: int):
+    """Test hook of the checked library, as ``fp8z1_checked_ffn_stall``."""
+    _check(lib().fp8z1_checked_linear_stall(kernels), "fp8z1_checked_linear_stall")

@@ -12,7 +12,8 @@ FP32 [E, R, C] weight gradients, which ``ShardOptimizer.step`` reads:
   rms_norm, rms_norm_fp8, rms_norm_grad
                              root-mean-square norm, the residual added first;
   route, dispatch, combine, dispatch_grad, combine_grad
-                             tokens sorted by expert for ``ffn_forward``, and back.
+                             tokens sorted by expert for ``ffn_forward``, and back;
+  linear, linear_grad        a matrix product with bias, activation and residual.
 
 Each is one call of libfp8z1.so's entry point of the same name (include/
 fp8z1_ops.h has the formulas); this module checks the tensors, allocates
@@ -22,9 +23,10 @@ that is not current, the outputs and workspaces are allocated as that stream's
 and the outputs marked as used on the current one too; the order of the two
 streams, and the inputs' memory until the work is done, are the caller's to
 see to.  Tensors that do not fit raise ValueError, what the library refuses
-raises Fp8z1Error.  Should a wait between the feed-forward kernels' warps ever
-run out, what it belongs to is NaN (``fp8z1.fp8z1_ffn_timeouts`` counts them);
-the optimizer skips a step with such gradients.
+raises Fp8z1Error.  Should a wait between the warps of a matrix product's
+kernel ever run out, what it belongs to is NaN (``fp8z1.fp8z1_ffn_timeouts`` and
+``fp8z1_linear_timeouts`` count them); the optimizer skips a step with such
+gradients.
 """
 from __future__ import annotations
 
@@ -511,3 +513,105 @@ def combine_grad(dy: torch.Tensor, rows: torch.Tensor, r: Route, weight: torch.T
     F.fp8z1_combine_grad(tokens, top, experts, dim, dy, kind, ld_dy, rows, ld, r.offsets, r.place, weight, out, ld_d,
                          d_weight, raw)
     return out, d_weight
+
+
+# ---- matrix product ---------------------------------------------------------------------
+
+_ACTS = {None: F.ACT_NONE, "silu": F.ACT_SILU, "gelu_tanh": F.ACT_GELU_TANH}
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _linear_dims(x, weight, scale, transposed, activation, y_type):
+    """(dims, width of x, width of y)"""
+    e, r, c = _fp8_weight(weight, scale, "the weight")
+    if e != 1:
+        _bad("a product's weight is [rows, cols]")
+    act, kind = _ACTS.get(activation, -1), _TYPES.get(y_type)
+    if act < 0:
+        _bad(f"no activation {activation!r}: None, 'silu' or 'gelu_tanh'")
+    if kind is None:
+        _bad(f"no product of {y_type}")
+    inner, outer = (c, r) if transposed else (r, c)
+    if x.dim() != 2 or x.shape[1] != inner:
+        _bad(f"x must be [tokens, {inner}]")
+    x_type = F.E4M3 if x.dtype in _CODES else F.BF16 if x.dtype == torch.bfloat16 else _bad("x must be bfloat16 or E4M3 codes")
+    return F.fp8z1_linear_dims(x.shape[0], r, c, 1 if transposed else 0, act, x_type, kind), inner, outer
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor, *, x_scale: Optional[torch.Tensor] = None,
+           bias: Optional[torch.Tensor] = None, activation: Optional[str] = None, residual: Optional[torch.Tensor] = None,
+           transposed: bool = False, dtype: torch.dtype = torch.bfloat16, save: bool = False,
+           out: Optional[torch.Tensor] = None, stream=None):
+    """``act(x w + bias) + residual`` with an FP8 weight [rows, cols] (cols a multiple of
+    16), or ``x w^T`` with ``transposed``, in float32 or bfloat16.  ``x``: bfloat16
+    [tokens, width], or E4M3 codes with ``x_scale`` as ``rms_norm_fp8`` gives them
+    (width a multiple of 16 then).  ``bias`` float32, ``residual`` bfloat16;
+    ``activation`` None, "silu" or "gelu_tanh".  With ``save`` also z = x w + bias,
+    float32, which ``linear_grad`` reads where there is an activation: (y, z)."""
+    dims, inner, outer = _linear_dims(x, weight, weight_scale, transposed, activation, dtype)
+    tokens = x.shape[0]
+    fp8 = dims.x_type == F.E4M3
+    if fp8 != (x_scale is not None):
+        _bad("E4M3 codes need x_scale, bfloat16 rows have none")
+    if fp8 and (x_scale.dtype != torch.float32 or x_scale.shape != (tokens, (inner + 127) // 128)
+                or not x_scale.is_contiguous()):
+        _bad("x_scale must be contiguous float32 [tokens, ceil(width / 128)]")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (outer,) or not bias.is_contiguous()):
+        _bad(f"bias must be contiguous float32 [{outer}]")
+    dev = x.get_device()
+    raw, other = _begin(dev, stream)
+    _same_device(dev, weight, weight_scale, x_scale, bias)
+    shape, ld_x, ld_r = (tokens, outer), _rows(x, "x"), 0
+    if fp8 and tokens == 1:
+        ld_x = (inner + 15) // 16 * 16  # a single row's stride is whatever it was cut from
+    if residual is not None:
+        ld_r = _rows(_given(residual, shape, torch.bfloat16, dev, "residual"), "residual")
+    if out is None:
+        out = _new(shape, dtype, dev, other)
+    ld_y = _rows(_given(out, shape, dtype, dev, "out"), "out")
+    pre = _new(shape, torch.float32, dev, other) if save else None
+    ws = _scratch(F.fp8z1_linear_sizes(dims)[0], torch.uint8, dev, other)
+    F.fp8z1_linear(dims, x, ld_x, x_scale, weight, weight_scale, bias, residual, ld_r, out, ld_y, pre, ws, raw)
+    return (out, pre) if save else out
+
+
+def linear_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor, *,
+                activation: Optional[str] = None, pre: Optional[torch.Tensor] = None, transposed: bool = False,
+                bias: bool = False, need_dx: bool = True, need_weight: bool = True,
+                d_weight: Optional[torch.Tensor] = None, d_bias: Optional[torch.Tensor] = None, stream=None):
+    """(dx, d_weight, d_bias) of ``linear`` for bfloat16 ``x`` and dy in its result's type: dx
+    bfloat16 (None without ``need_dx``), d_weight float32 in the weight's shape (None
+    without ``need_weight``), d_bias float32 (None without ``bias``).  ``pre``: z of
+    ``linear(..., save=True)``, with an activation.  The residual's gradient is dy."""
+    dims, inner, outer = _linear_dims(x, weight, weight_scale, transposed, activation, dy.dtype)
+    tokens = x.shape[0]
+    if dims.x_type != F.BF16:
+        _bad("the gradients need bfloat16 x")
+    if dy.shape != (tokens, outer):
+        _bad(f"dy must be [{tokens}, {outer}]")
+    if activation is None:
+        pre = None
+    elif pre is None or pre.dtype != torch.float32 or pre.shape != dy.shape or not pre.is_contiguous():
+        _bad("pre must be contiguous float32 of dy's shape, from linear(..., save=True)")
+    dev = x.get_device()
+    raw, other = _begin(dev, stream)
+    _same_device(dev, dy, weight, weight_scale, pre)
+    if not (need_dx or need_weight or bias):
+        _bad("no gradient is wanted")
+    dx = _new(x.shape, torch.bfloat16, dev, other) if need_dx else None
+    if not need_weight:
+        d_weight = None
+    elif d_weight is None:
+        d_weight = _new(weight.shape, torch.float32, dev, other)
+    elif not _given(d_weight, weight.shape, torch.float32, dev, "d_weight").is_contiguous():
+        _bad("d_weight must be contiguous")
+    if not bias:
+        d_bias = None
+    elif d_bias is None:
+        d_bias = _new((outer,), torch.float32, dev, other)
+    elif not _given(d_bias, (outer,), torch.float32, dev, "d_bias").is_contiguous():
+        _bad("d_bias must be contiguous")
+    ws = _scratch(F.fp8z1_linear_sizes(dims)[1], torch.uint8, dev, other)
+    F.fp8z1_linear_grad(dims, dy, _rows(dy, "dy"), x, _rows(x, "x"), weight, weight_scale, pre, dx,
+                        _rows(dx, "dx") if need_dx else 0, d_weight, d_bias, ws, raw)
+    return dx, d_weight, d_bias

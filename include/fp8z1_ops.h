@@ -8,6 +8,7 @@
  *               forward and backward;
  *   distillation  loss against a teacher's top logits, and its gradient;
  *   RMS norm    of rows, the residual added first, in 16, 32 or 8 bits; its gradient;
+ *   product     act(x W + bias) + residual, its gradients;
  *   routing     tokens sorted by expert, their rows gathered and joined again,
  *               and the gradients of both.
  *
@@ -35,6 +36,7 @@ extern "C" {
 /* element types of activations, logits and their gradients */
 #define FP8Z1_F32 0
 #define FP8Z1_BF16 1
+#define FP8Z1_E4M3 2 /* rows of codes with a scale for every 128 columns (fp8z1_linear's x) */
 
 /* ---- embedding -------------------------------------------------------------- */
 
@@ -230,6 +232,63 @@ int fp8z1_combine(int64_t tokens, int64_t top, int64_t dim, const void* rows, in
 int fp8z1_combine_grad(int64_t tokens, int64_t top, int64_t experts, int64_t dim, const void* dy, int32_t type,
                        int64_t ld_dy, const void* rows, int64_t ld_rows, const int32_t* offsets, const int32_t* place,
                        const float* weight, void* d_rows, int64_t ld_d, float* d_weight, void* stream);
+
+/* ---- matrix product ------------------------------------------------------------------- */
+
+/* activations: z; z sigmoid(z); z sigmoid(sqrt(8 / pi) (z + 0.044715 z^3)), GELU's tanh form */
+#define FP8Z1_ACT_NONE 0
+#define FP8Z1_ACT_SILU 1
+#define FP8Z1_ACT_GELU_TANH 2
+
+typedef struct {
+    int64_t tokens;     /* rows of x, 0 .. 2^30 */
+    int64_t rows, cols; /* of the FP8 weight w; cols a multiple of 16; both at most 2^22 */
+    int32_t transposed; /* 0: x w, x [tokens, rows], y [tokens, cols]; 1: x w^T, x [tokens, cols], y [tokens, rows] */
+    int32_t activation; /* FP8Z1_ACT_* */
+    int32_t x_type;     /* FP8Z1_BF16 or FP8Z1_E4M3 */
+    int32_t y_type;     /* FP8Z1_BF16 or FP8Z1_F32; dy's too */
+} fp8z1_linear_dims;
+
+/* Bytes of the workspaces of both directions (forward: 0 for E4M3 rows).  Host only.
+ * Errors: EINVAL. */
+int fp8z1_linear_sizes(const fp8z1_linear_dims* dims, int64_t* forward_bytes, int64_t* backward_bytes);
+
+/* z = x w + bias (or x w^T + bias),  y = act(z) + residual, rounded once to `y_type`.
+ * x: BF16 of any alignment and stride >= its width; or E4M3 codes, 16-byte aligned rows
+ * (ld_x a multiple of 16), with `x_scale`, FP32 [tokens, ceil(width / 128)] dense, as
+ * fp8z1_rms_norm writes them (x_scale is not read for BF16).  codes: 16-byte aligned.
+ * bias: FP32 [width of y] or NULL; residual: BF16 or NULL; pre: NULL, or FP32 [tokens, width of
+ * y] dense for z, which fp8z1_linear_grad reads.  y may be residual itself where both are BF16
+ * of one stride.  Sums are FP32 over exact products of the codes and x (BF16 x down to 2^-13
+ * of the largest of its 128 neighbours, to 2^-21 of that below); they repeat bit for
+ * bit, and may change in their last places when other rows join.  An infinity or NaN in a row
+ * of x leaves that row of y without finite numbers.  tokens == 0 enqueues nothing.
+ * Errors: EINVAL, EALIGN, ECUDA. */
+int fp8z1_linear(const fp8z1_linear_dims* dims, const void* x, int64_t ld_x, const float* x_scale, const uint8_t* codes,
+                 const float* scales, const float* bias, const void* residual, int64_t ld_residual, void* y, int64_t ld_y,
+                 float* pre, void* workspace, void* stream);
+
+/* The gradients of sum(dy * y) for BF16 x, dz = dy * act'(z):
+ *   dx = dz w^T (or dz w), BF16;  d_weight = x^T dz (or dz^T x), FP32 [rows, cols];  d_bias =
+ *   sum over the rows of dz, FP32.
+ * Each may be NULL, not all.  `pre`: z of the forward pass (not read without activation).
+ * The residual's gradient is dy.  dy of `y_type`, dx: any alignment and stride; d_weight 16-byte
+ * aligned.  dz is dy itself, exact, for BF16 dy without activation; else it is rounded for dx to 9
+ * significant bits (BF16 has 8) or 2^-17 of the largest of its 128 neighbours.  d_weight
+ * and d_bias carry FP32 accuracy, d_weight every column of dz relative to its own size (x: what
+ * lies above 2^-31 of the largest of 256 rows x 128 columns); every element is written.
+ * Errors: EINVAL (E4M3 x too), EALIGN (workspace: 256 bytes), ECUDA. */
+int fp8z1_linear_grad(const fp8z1_linear_dims* dims, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                      const uint8_t* codes, const float* scales, const float* pre, void* dx, int64_t ld_dx,
+                      float* d_weight, float* d_bias, void* workspace, void* stream);
+
+/* As fp8z1_ffn_timeouts, of the product's kernels (whose waits end as the
+ * feed-forward kernels' do, and leave NaN in y, dx or d_weight). */
+int fp8z1_linear_timeouts(uint32_t* count);
+
+/* As fp8z1_checked_ffn_stall.  Bits: 1 products of many rows, 2 of few, 4 d_weight, 8 d_weight of a
+ * transposed weight. */
+int fp8z1_checked_linear_stall(uint32_t kernels);
 
 #ifdef __cplusplus
 }
