@@ -13,6 +13,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ops_common.cuh"
 
@@ -26,10 +27,14 @@ constexpr int kMostExperts = 1024, kMostTop = 64;
 
 // ---- the sort -----------------------------------------------------------------------
 //
-// A cluster of CTAs, each warp a run of the choices, twice over: counts of every
-// expert in shared memory by warp, their sums over warps, CTAs and experts, then every
-// choice's row is its warp's next one of that expert.  Choices of one expert inside
-// 32 are ranked by a match of the lanes.
+// A cluster of CTAs, each warp a run of the choices: a choice's rank among those of its
+// expert in the warp (by a match of the lanes, 32 choices a step, and the warp's counts in
+// shared memory), the counts' sums over warps, CTAs and experts, and each choice's row is
+// what lies before its warp's and its rank.  Bound by latency: the choices of a warp's
+// first kHeld steps are on their way at once and stay in registers with their ranks, an
+// expert's counts are added by a warp with a lane for each.
+
+constexpr int kHeld = 16;
 
 struct SortArgs {
     const void* ids;
@@ -47,6 +52,17 @@ __device__ __forceinline__ int expert_of(const Id* ids, int64_t i, int64_t n, in
     return e >= 0 && e < (Id)experts ? (int)e : -1;
 }
 
+// The rank of each lane's choice among its expert's of the warp so far, which `mine` counts.
+__device__ __forceinline__ int rank_of(int e, int32_t* mine, int lane)
+{
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int rank = e < 0 ? 0 : mine[e] + __popc(same & ((1u << lane) - 1));
+    __syncwarp();
+    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    __syncwarp();
+    return rank;
+}
+
 template <class Id>
 __global__ void __launch_bounds__(1024) sort_kernel(const SortArgs a)
 {
@@ -59,34 +75,44 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortArgs a)
     int32_t* total = counts + warps * E;
     const Id* ids = static_cast<const Id*>(a.ids);
     const int64_t i0 = ((int64_t)rank * warps + warp) * a.per_warp, i1 = min(i0 + a.per_warp, a.n);
+    int held[kHeld], ranks[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+        held[k] = k * 32 < a.per_warp ? expert_of(ids, i0 + k * 32 + lane, a.n, E) : -1;
     for (int e = lane; e < E; e += 32) mine[e] = 0;
     __syncwarp();
-    for (int64_t i = i0; i < i1; i += 32) {
-        const int e = expert_of(ids, i + lane, a.n, E);
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        ranks[k] = 0;
+        if (i0 + k * 32 < i1) ranks[k] = rank_of(held[k], mine, lane);
+    }
+    for (int64_t i = i0 + kHeld * 32; i < i1; i += 32) {  // these ranks wait in `place`
+        const int rank_here = rank_of(expert_of(ids, i + lane, a.n, E), mine, lane);
+        if (i + lane < a.n) a.place[i + lane] = rank_here;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int32_t sum = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int32_t n = counts[w * E + e];
-            counts[w * E + e] = sum;
-            sum += n;
+    for (int e = warp; e < E; e += warps) {  // a lane a warp's counts: what lies before each of them
+        const int32_t n = lane < warps ? counts[lane * E + e] : 0;
+        int32_t sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += up;
         }
-        total[e] = sum;
+        if (lane < warps) counts[lane * E + e] = sum - n;
+        if (lane == 31) total[e] = sum;
     }
     if (ctas > 1)
         cluster.sync();
     else
         __syncthreads();
-    // 32 neighbouring experts a warp: what lies before each of them
+    // a thread an expert: what lies before it, of the experts ahead and of its own in the CTAs ahead
     int32_t before = 0;  // of all experts up to this round's first
     for (int e0 = 0; e0 < E; e0 += blockDim.x) {
         const int e = e0 + threadIdx.x;
         int32_t all = 0, ahead = 0;
         if (e < E)
+#pragma unroll 8
             for (int c = 0; c < ctas; ++c) {
                 const int32_t n = ctas > 1 ? cluster.map_shared_rank(total, c)[e] : total[e];
                 if (c < rank) ahead += n;
@@ -100,29 +126,27 @@ __global__ void __launch_bounds__(1024) sort_kernel(const SortArgs a)
         }
         if (lane == 31) scan[warp] = sum;
         __syncthreads();
-        int32_t start = before + sum - all, last = before;
-        for (int w = 0; w < warps; ++w) {
-            if (w < warp) start += scan[w];
-            last += scan[w];
-        }
-        before = last;
+        const int32_t part = lane < warps ? scan[lane] : 0;
+        const int32_t start = before + sum - all + (int32_t)__reduce_add_sync(0xffffffffu, lane < warp ? part : 0);
+        before += (int32_t)__reduce_add_sync(0xffffffffu, part);
         if (e < E) {
-            for (int w = 0; w < warps; ++w) counts[w * E + e] += start + ahead;
             if (rank == 0) a.offsets[e] = start;
             if (rank == 0 && e == E - 1) a.offsets[E] = start + all;
         }
-        __syncthreads();
+        if (ctas > 1)
+            cluster.sync();  // the totals have been read
+        else
+            __syncthreads();
+        if (e < E) total[e] = start + ahead;  // from here on the first row of the CTA's own
     }
-    for (int64_t i = i0; i < i1; i += 32) {
-        const int e = expert_of(ids, i + lane, a.n, E);
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        const int32_t at = e < 0 ? -1 : mine[e] + __popc(same & ((1u << lane) - 1));
-        if (i + lane < a.n) a.place[i + lane] = at;
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
-    }
-    if (ctas > 1) cluster.sync();  // no CTA leaves before its counts are read
+    __syncthreads();
+    auto place = [&](int64_t i, int e, int rank_here) {
+        if (i < a.n) a.place[i] = e < 0 ? -1 : total[e] + mine[e] + rank_here;
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+        if (i0 + k * 32 < i1) place(i0 + k * 32 + lane, held[k], ranks[k]);
+    for (int64_t i = i0 + kHeld * 32 + lane; i < i1; i += 32) place(i, expert_of(ids, i, a.n, E), a.place[i]);
 }
 
 // ---- rows ----------------------------------------------------------------------------
@@ -182,32 +206,56 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const RowArgs a)
     clear_rest(a, out, a.ld_out, a.cols);
 }
 
-// kN neighbouring elements
-template <class T, int kN>
-__device__ __forceinline__ void load(const T* p, float (&v)[kN])
-{
-    if constexpr (kN == 1) {
-        v[0] = to_float(*p);
-    } else if constexpr (sizeof(T) == 4) {
-        static_assert(kN == 4, "16 bytes");
-        const float4 f = *reinterpret_cast<const float4*>(p);
-        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-    } else {
-        static_assert(kN == 8, "16 bytes");
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// What a thread takes of a row at a time: 16 bytes, or (rows that do not lie on them) four
+// elements a CTA's width apart.  `left`: elements from its first to the row's end.
+template <class T, bool kVec>
+struct Piece;
+template <class T>
+struct Piece<T, false> {
+    static constexpr int kN = 4;
+    T raw[4];
+    __device__ __forceinline__ void load(const T* p, int64_t left)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((int)blockDim.x * i < left) raw[i] = p[blockDim.x * i];
+    }
+    __device__ __forceinline__ void get(float (&v)[4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = to_float(raw[i]);
+    }
+    static __device__ __forceinline__ void store(T* p, const float (&v)[4], int64_t left)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((int)blockDim.x * i < left) p[blockDim.x * i] = from_float<T>(v[i]);
+    }
+};
+template <>
+struct Piece<float, true> {
+    static constexpr int kN = 4;
+    float4 raw;
+    __device__ __forceinline__ void load(const float* p, int64_t) { raw = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = raw.x, v[1] = raw.y, v[2] = raw.z, v[3] = raw.w; }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[4], int64_t)
+    {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+};
+template <>
+struct Piece<bf16, true> {
+    static constexpr int kN = 8;
+    uint4 raw;
+    __device__ __forceinline__ void load(const bf16* p, int64_t) { raw = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-}
-template <class T, int kN>
-__device__ __forceinline__ void store(T* p, const float (&v)[kN])
-{
-    if constexpr (kN == 1) {
-        *p = from_float<T>(v[0]);
-    } else if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
+    static __device__ __forceinline__ void store(bf16* p, const float (&v)[8], int64_t)
+    {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -216,100 +264,144 @@ __device__ __forceinline__ void store(T* p, const float (&v)[kN])
         }
         *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-}
-
-// kN columns of a token a thread, the rows of kTogether choices on their way at once.
-constexpr int kTogether = 8;
-template <class T, int kN>
-__global__ void __launch_bounds__(256) combine_kernel(const RowArgs a)
+};
+// A thread's first element of a CTA's `part`-th width of pieces.
+template <class T, bool kVec>
+__device__ __forceinline__ int64_t first_of(int64_t part)
 {
-    const int64_t t = blockIdx.x, c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * kN;
-    if (c >= a.cols) return;
-    const T* rows = static_cast<const T*>(a.rows) + c;
-    float sum[kN] = {};
-    if (a.x) load<T, kN>(static_cast<const T*>(a.x) + t * a.ld_x + c, sum);
-    float add[kN] = {};  // the residual joins last
-#pragma unroll
-    for (int i = 0; i < kN; ++i) add[i] = sum[i], sum[i] = 0.0f;
-    for (int j0 = 0; j0 < a.top; j0 += kTogether) {
-        float v[kTogether][kN], w[kTogether];
-#pragma unroll
-        for (int j = 0; j < kTogether; ++j) {
-            w[j] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kN; ++i) v[j][i] = 0.0f;
-            if (j0 + j >= a.top) continue;
-            const int64_t r = row_of(a, t * a.top + j0 + j);
-            if (r < 0) continue;
-            w[j] = a.weight ? __ldg(a.weight + t * a.top + j0 + j) : 1.0f;
-            load<T, kN>(rows + r * a.ld_rows, v[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < kTogether; ++j)
-#pragma unroll
-            for (int i = 0; i < kN; ++i) sum[i] = __fmaf_rn(w[j], v[j][i], sum[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kN; ++i) sum[i] += add[i];
-    store<T, kN>(static_cast<T*>(a.y) + t * a.ld_y + c, sum);
+    return part * blockDim.x * Piece<T, kVec>::kN + threadIdx.x * (kVec ? Piece<T, kVec>::kN : 1);
 }
 
-// A CTA a token, kTogether choices at a time.
-template <class T, int kN>
+// The choices of token t: rows and weights in shared memory.
+struct Choices {
+    int32_t row[kMostTop];  // -1: none
+    float weight[kMostTop];
+};
+__device__ __forceinline__ void load_choices(Choices& c, const RowArgs& a, int64_t t)
+{
+    for (int j = threadIdx.x; j < a.top; j += blockDim.x) {
+        const int64_t r = row_of(a, t * a.top + j);
+        c.row[j] = (int32_t)r;
+        c.weight[j] = r < 0 ? 0.0f : a.weight ? __ldg(a.weight + t * a.top + j) : 1.0f;
+    }
+    __syncthreads();
+}
+
+// Calls f<how many>(first) for `top` choices, kMost, then 4, 2 and 1 at a time: so many rows are on their way at
+// once.  (Of single elements 4: 8 took 100 registers and 36 us for 3001 tokens' three rows of 1001 FP32.)
+template <int kMost, class F>
+__device__ __forceinline__ void by_parts(int top, F f)
+{
+    int j = 0;
+    for (; j + kMost <= top; j += kMost) f(std::integral_constant<int, kMost>(), j);
+    if (kMost > 4 && top & 4) f(std::integral_constant<int, 4>(), j), j += 4;
+    if (top & 2) f(std::integral_constant<int, 2>(), j), j += 2;
+    if (top & 1) f(std::integral_constant<int, 1>(), j);
+}
+
+// The pieces of kMany choices' rows from column c on.  The loads do not ask whether there is a row, so that
+// they go together: a choice without one reads row 0, which is not used.
+template <class T, bool kVec, int kMany>
+__device__ __forceinline__ void load_rows(Piece<T, kVec> (&v)[kMany], const Choices& choices, int j0, const T* rows, int64_t ld,
+                                          int64_t left)
+{
+#pragma unroll
+    for (int j = 0; j < kMany; ++j) v[j].load(rows + (int64_t)max(choices.row[j0 + j], 0) * ld, left);
+}
+
+// Parts of a token's columns are neighbouring CTAs'.
+template <class T, bool kVec>
+__global__ void __launch_bounds__(256) combine_kernel(const RowArgs a, int parts)
+{
+    using P = Piece<T, kVec>;
+    __shared__ Choices choices;
+    const int64_t t = blockIdx.x / parts;
+    load_choices(choices, a, t);
+    int64_t part = blockIdx.x % parts;
+    for (int64_t c = first_of<T, kVec>(part); c < a.cols; c = first_of<T, kVec>(part += parts)) {
+        const T* rows = static_cast<const T*>(a.rows) + c;
+        const int64_t left = a.cols - c;
+        float sum[P::kN] = {};
+        P add;
+        if (a.x) add.load(static_cast<const T*>(a.x) + t * a.ld_x + c, left);
+        by_parts<kVec ? 8 : 4>(a.top, [&](auto how_many, int j0) {
+            constexpr int many = decltype(how_many)::value;
+            P v[many];
+            load_rows(v, choices, j0, rows, a.ld_rows, left);
+#pragma unroll
+            for (int j = 0; j < many; ++j) {
+                if (choices.row[j0 + j] < 0) continue;
+                float f[P::kN];
+                v[j].get(f);
+                const float w = choices.weight[j0 + j];
+#pragma unroll
+                for (int i = 0; i < P::kN; ++i) sum[i] = __fmaf_rn(w, f[i], sum[i]);
+            }
+        });
+        if (a.x) {  // the residual joins last
+            float f[P::kN];
+            add.get(f);
+#pragma unroll
+            for (int i = 0; i < P::kN; ++i) sum[i] += f[i];
+        }
+        P::store(static_cast<T*>(a.y) + t * a.ld_y + c, sum, left);
+    }
+}
+
+// A CTA a token.
+template <class T, bool kVec>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a)
 {
-    __shared__ float sums[8][kTogether];
+    using P = Piece<T, kVec>;
+    __shared__ float sums[8][8];
+    __shared__ Choices choices;
     const int64_t t = blockIdx.x;
+    load_choices(choices, a, t);
     const T* dy = static_cast<const T*>(a.y) + t * a.ld_y;
-    const T* rows = static_cast<const T*>(a.rows);
     T* out = static_cast<T*>(a.out);
-    for (int j0 = 0; j0 < a.top; j0 += kTogether) {
-        float dot[kTogether] = {}, w[kTogether];
-        int64_t r[kTogether];
+    by_parts<kVec ? 8 : 4>(a.top, [&](auto how_many, int j0) {
+        constexpr int many = decltype(how_many)::value;
+        float dot[many];
 #pragma unroll
-        for (int j = 0; j < kTogether; ++j) {
-            r[j] = j0 + j < a.top ? row_of(a, t * a.top + j0 + j) : -1;
-            w[j] = r[j] >= 0 ? __ldg(a.weight + t * a.top + j0 + j) : 0.0f;
-        }
-        for (int64_t c = (int64_t)threadIdx.x * kN; c < a.cols; c += (int64_t)blockDim.x * kN) {
-            float d[kN], v[kTogether][kN];
-            load<T, kN>(dy + c, d);
+        for (int j = 0; j < many; ++j) dot[j] = 0.0f;
+        int64_t part = 0;
+        for (int64_t c = first_of<T, kVec>(0); c < a.cols; c = first_of<T, kVec>(++part)) {
+            const int64_t left = a.cols - c;
+            P v[many], raw;
+            raw.load(dy + c, left);
+            load_rows(v, choices, j0, static_cast<const T*>(a.rows) + c, a.ld_rows, left);
+            float d[P::kN];
+            raw.get(d);
 #pragma unroll
-            for (int j = 0; j < kTogether; ++j) {
-                if (r[j] >= 0) {
-                    load<T, kN>(rows + r[j] * a.ld_rows + c, v[j]);
-                } else {
+            for (int j = 0; j < many; ++j) {
+                const int32_t r = choices.row[j0 + j];
+                if (r < 0) continue;
+                const float w = choices.weight[j0 + j];
+                float f[P::kN], g[P::kN];
+                v[j].get(f);
 #pragma unroll
-                    for (int i = 0; i < kN; ++i) v[j][i] = 0.0f;
+                for (int i = 0; i < P::kN; ++i) {
+                    if (kVec || (int)blockDim.x * i < left) dot[j] = __fmaf_rn(d[i], f[i], dot[j]);
+                    g[i] = w * d[i];
                 }
-            }
-#pragma unroll
-            for (int j = 0; j < kTogether; ++j) {
-                if (r[j] < 0) continue;
-                float g[kN];
-#pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    dot[j] = __fmaf_rn(d[i], v[j][i], dot[j]);
-                    g[i] = w[j] * d[i];
-                }
-                store<T, kN>(out + r[j] * a.ld_out + c, g);
+                P::store(out + r * a.ld_out + c, g, left);
             }
         }
 #pragma unroll
-        for (int j = 0; j < kTogether; ++j)
+        for (int j = 0; j < many; ++j)
 #pragma unroll
             for (int o = 16; o; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
         __syncthreads();
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int j = 0; j < kTogether; ++j) sums[threadIdx.x >> 5][j] = dot[j];
+            for (int j = 0; j < many; ++j) sums[threadIdx.x >> 5][j] = dot[j];
         __syncthreads();
-        if (threadIdx.x < kTogether && j0 + threadIdx.x < a.top) {
+        if (threadIdx.x < many) {
             float s = 0.0f;
             for (int q = 0; q < (int)(blockDim.x >> 5); ++q) s += sums[q][threadIdx.x];
             a.d_weight[t * a.top + j0 + threadIdx.x] = s;
         }
-    }
+    });
     clear_rest(a, out, a.ld_out, a.cols);
 }
 
@@ -339,20 +431,24 @@ int launch_dispatch(RowArgs a, int64_t bytes, int64_t size, cudaStream_t s)
     return launch_status();
 }
 
-template <class T, int kN>
+template <class T, bool kVec>
 int launch_combine(const RowArgs& a, cudaStream_t s)
 {
+    constexpr int kN = Piece<T, kVec>::kN;
     const unsigned threads = threads_for(ceil_div(a.cols, kN));
+    // few tokens: their columns over more CTAs
+    const int64_t most = ceil_div(a.cols, (int64_t)threads * kN);
+    const int parts = (int)std::max<int64_t>(1, std::min(most, 4 * kSms / a.tokens));
     count_launch();
-    combine_kernel<T, kN><<<dim3((unsigned)a.tokens, (unsigned)ceil_div(ceil_div(a.cols, kN), threads)), threads, 0, s>>>(a);
+    combine_kernel<T, kVec><<<(unsigned)(a.tokens * parts), threads, 0, s>>>(a, parts);
     return launch_status();
 }
 
-template <class T, int kN>
+template <class T, bool kVec>
 int launch_combine_grad(const RowArgs& a, cudaStream_t s)
 {
     count_launch();
-    combine_grad_kernel<T, kN><<<(unsigned)a.tokens, threads_for(ceil_div(a.cols, kN)), 0, s>>>(a);
+    combine_grad_kernel<T, kVec><<<(unsigned)a.tokens, threads_for(ceil_div(a.cols, Piece<T, kVec>::kN)), 0, s>>>(a);
     return launch_status();
 }
 
@@ -372,8 +468,8 @@ extern "C" int fp8z1_route(const void* ids, int32_t id_bytes, int64_t tokens, in
     if (!offsets || (n && (!ids || !place)) || (id_bytes != 4 && id_bytes != 8)) return FP8Z1_EINVAL;
     if (!aligned(ids, id_bytes) || !aligned(offsets, 4) || !aligned(place, 4)) return FP8Z1_EALIGN;
     NvtxRange range("fp8z1_route");
-    // one CTA up to 8192 choices, then up to 8 CTAs of 32 warps
-    const int ctas = (int)std::min<int64_t>(8, std::max<int64_t>(1, ceil_div(n, 8192)));
+    // one CTA up to 4096 choices (a cluster's barriers cost as much as four steps), then up to 8 CTAs of 32 warps
+    const int ctas = (int)std::min<int64_t>(8, std::max<int64_t>(1, ceil_div(n, 4096)));
     const int warps = ctas > 1 ? 32 : (int)std::min<int64_t>(32, std::max<int64_t>(4, ceil_div(n, 64)));
     SortArgs a = {ids, n, (int32_t)experts, 0, offsets, place};
     a.per_warp = (int32_t)(ceil_div(ceil_div(n, (int64_t)ctas * warps), 32) * 32);
@@ -457,8 +553,8 @@ extern "C" int fp8z1_combine(int64_t tokens, int64_t top, int64_t dim, const voi
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = dim * size % 16 == 0 && fits(rows, ld_rows, size, 16) && fits(residual, ld_residual, size, 16) &&
                      fits(y, ld_y, size, 16);
-    if (type == FP8Z1_F32) return vec ? launch_combine<float, 4>(a, s) : launch_combine<float, 1>(a, s);
-    return vec ? launch_combine<bf16, 8>(a, s) : launch_combine<bf16, 1>(a, s);
+    if (type == FP8Z1_F32) return vec ? launch_combine<float, true>(a, s) : launch_combine<float, false>(a, s);
+    return vec ? launch_combine<bf16, true>(a, s) : launch_combine<bf16, false>(a, s);
 }
 
 extern "C" int fp8z1_combine_grad(int64_t tokens, int64_t top, int64_t experts, int64_t dim, const void* dy, int32_t type,
@@ -495,6 +591,6 @@ extern "C" int fp8z1_combine_grad(int64_t tokens, int64_t top, int64_t experts, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = dim * size % 16 == 0 && fits(dy, ld_dy, size, 16) && fits(rows, ld_rows, size, 16) &&
                      fits(d_rows, ld_d, size, 16);
-    if (type == FP8Z1_F32) return vec ? launch_combine_grad<float, 4>(a, s) : launch_combine_grad<float, 1>(a, s);
-    return vec ? launch_combine_grad<bf16, 8>(a, s) : launch_combine_grad<bf16, 1>(a, s);
+    if (type == FP8Z1_F32) return vec ? launch_combine_grad<float, true>(a, s) : launch_combine_grad<float, false>(a, s);
+    return vec ? launch_combine_grad<bf16, true>(a, s) : launch_combine_grad<bf16, false>(a, s);
 }
