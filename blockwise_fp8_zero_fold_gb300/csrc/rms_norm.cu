@@ -7,12 +7,14 @@
 // s is rounded to the rows' type, as the residual stream keeps it, and the norm is
 // that of the rounded row; sums, rstd, y before its one rounding and dw are FP32.
 //
-// A row is held in registers from its one read on: a warp's (8 rows a CTA) up to 1024
-// columns, a CTA's beyond.  Few rows are spread over more threads (8 elements each
-// for 32), as latency counts there.
+// A row is held in registers from its one read on, by a warp (8 rows a CTA) or by a CTA.  All
+// is bound by memory but for the smallest calls, which latency bounds.  The gradient of longer
+// rows: persistent CTAs whose rows come to shared memory as bulk copies ahead of their use, as
+// registers alone hold too few bytes under way (159 us for 8192 rows of 7168).
 #include <algorithm>
 
 #include "ops_common.cuh"
+#include "tc.cuh"
 
 namespace fp8z1 {
 namespace {
@@ -61,64 +63,108 @@ __device__ __forceinline__ void store8(bf16* p, const float* v)
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A thread's elements of a row (0 past its end), and back.
-template <int kE, bool kVec, class T>
-__device__ __forceinline__ void load_row(const T* p, int dim, int tid, int threads, float (&v)[kE])
-{
-    if constexpr (kVec) {
-#pragma unroll
-        for (int j = 0; j < kE; j += 8) {
-            const int c = column<true>(j, tid, threads);
-            float t[8] = {};
-            if (c < dim) load8(p + c, t);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[j + i] = t[i];
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kE; ++j) {
-            const int c = column<false>(j, tid, threads);
-            v[j] = c < dim ? to_float(p[c]) : 0.0f;
-        }
+// A thread's elements of a row as they were read.
+template <class T, int kE>
+struct Held;
+template <int kE>
+struct Held<float, kE> {
+    float raw[kE];
+    __device__ __forceinline__ float get(int j) const { return raw[j]; }
+    __device__ __forceinline__ void set(int j, float v) { raw[j] = v; }
+    __device__ __forceinline__ void set8(int j, const float* p)
+    {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        raw[j] = a.x, raw[j + 1] = a.y, raw[j + 2] = a.z, raw[j + 3] = a.w;
+        raw[j + 4] = b.x, raw[j + 5] = b.y, raw[j + 6] = b.z, raw[j + 7] = b.w;
     }
-}
-template <int kE, bool kVec, class T>
-__device__ __forceinline__ void store_row(T* p, int dim, int tid, int threads, const float (&v)[kE])
+};
+template <int kE>
+struct Held<bf16, kE> {
+    uint32_t raw[kE / 2] = {};
+    __device__ __forceinline__ float get(int j) const { return __uint_as_float(j & 1 ? raw[j / 2] & 0xffff0000u : raw[j / 2] << 16); }
+    __device__ __forceinline__ void set(int j, bf16 v)
+    {
+        const uint32_t b = *reinterpret_cast<const unsigned short*>(&v);
+        raw[j / 2] = j & 1 ? (raw[j / 2] & 0xffffu) | b << 16 : (raw[j / 2] & 0xffff0000u) | b;
+    }
+    __device__ __forceinline__ void set8(int j, const bf16* p)
+    {
+        const uint4 a = *reinterpret_cast<const uint4*>(p);
+        raw[j / 2] = a.x, raw[j / 2 + 1] = a.y, raw[j / 2 + 2] = a.z, raw[j / 2 + 3] = a.w;
+    }
+};
+
+// A thread's elements of a row, zeros past the end: all from p, or those of [lo, hi) from `here` in shared memory.
+template <int kE, bool kVec, bool kStaged, class T>
+__device__ __forceinline__ void hold(Held<T, kE>& v, const T* p, const T* here, int lo, int hi, int dim, int tid, int threads)
 {
 #pragma unroll
     for (int j = 0; j < kE; j += kVec ? 8 : 1) {
         const int c = column<kVec>(j, tid, threads);
-        if (c >= dim) continue;
-        if constexpr (kVec)
-            store8(p + c, &v[j]);
-        else
-            p[c] = from_float<T>(v[j]);
+        if constexpr (kVec) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v.set(j + i, from_float<T>(0.0f));
+            if (c < dim) v.set8(j, (kStaged ? here : p) + c);
+        } else {
+            T e = from_float<T>(0.0f);
+            if (kStaged && c >= lo && c < hi)
+                e = here[c];
+            else if (c < dim)
+                e = p[c];
+            v.set(j, e);
+        }
     }
 }
 
-// The sums of a and b over a row's threads, in a fixed order; every thread gets them.
-// `part`: two floats for each warp; a CTA's next use of it is a barrier away.
-template <bool kWarpRow>
-__device__ __forceinline__ float2 row_sum(float a, float b, float2* part)
+// kN neighbours (kVec: 8) or elements 32 apart from column c on, zeros past the end; and back.
+template <bool kVec>
+constexpr int kPiece = kVec ? 8 : 4;
+template <bool kVec, class T>
+__device__ __forceinline__ void load_piece(const T* p, int c, int dim, float (&v)[kPiece<kVec>])
+{
+    if constexpr (kVec) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        if (c < dim) load8(p + c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = c + 32 * i < dim ? to_float(p[c + 32 * i]) : 0.0f;
+    }
+}
+template <bool kVec, class T>
+__device__ __forceinline__ void store_piece(T* p, int c, int dim, const float (&v)[kPiece<kVec>])
+{
+    if constexpr (kVec) {
+        if (c < dim) store8(p + c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + 32 * i < dim) p[c + 32 * i] = from_float<T>(v[i]);
+    }
+}
+
+// The sum of a over a row's threads, in a fixed order; every thread gets it.  `part`: a float
+// for each warp of the CTA.
+__device__ __forceinline__ float2 warp_sum(float2 a)
 {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
     }
-    if constexpr (kWarpRow) return make_float2(a, b);
-    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-    __syncthreads();
-    if (lane == 0) part[threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    const float2 mine = lane < warps ? part[lane] : make_float2(0.0f, 0.0f);
-    a = mine.x, b = mine.y;
+    return a;
+}
+template <bool kWarpRow>
+__device__ __forceinline__ float row_sum(float a, float* part)
+{
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    return make_float2(a, b);
+    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if constexpr (kWarpRow) return a;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = part[0];
+    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) a += part[w];
+    return a;
 }
 
 // The squares of numbers beyond 2^60 or so leave FP32 in a sum of 16384.  Such a row is
@@ -138,70 +184,75 @@ struct Args {
     int groups;  // of 128 columns
 };
 
+// A row by a warp, or by a CTA.
 template <class T, int kE, bool kVec, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 256 : kE == 8 ? 1024 : 512) norm_kernel(const Args a)
+__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) norm_kernel(const Args a)
 {
-    __shared__ float2 part[32];
+    constexpr int kP = kPiece<kVec>;
+    __shared__ float part[2][32];
     const int threads = kWarpRow ? 32 : blockDim.x, tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
     const int64_t row = kWarpRow ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
     if (kWarpRow && row >= a.rows) return;
-    float v[kE];
-    load_row<kE, kVec>(static_cast<const T*>(a.x) + row * a.ld_x, a.dim, tid, threads, v);
+    Held<T, kE> s;
+    hold<kE, kVec, false, T>(s, static_cast<const T*>(a.x) + row * a.ld_x, nullptr, 0, 0, a.dim, tid, threads);
     if (a.r) {
-        float r[kE];
-        load_row<kE, kVec>(static_cast<const T*>(a.r) + row * a.ld_r, a.dim, tid, threads, r);
+        Held<T, kE> r;
+        hold<kE, kVec, false, T>(r, static_cast<const T*>(a.r) + row * a.ld_r, nullptr, 0, 0, a.dim, tid, threads);
 #pragma unroll
-        for (int j = 0; j < kE; ++j) v[j] = to_float(from_float<T>(v[j] + r[j]));
-        store_row<kE, kVec>(static_cast<T*>(a.total) + row * a.ld_t, a.dim, tid, threads, v);
+        for (int j = 0; j < kE; j += kP) {
+            float v[kP];
+#pragma unroll
+            for (int i = 0; i < kP; ++i) s.set(j + i, from_float<T>(s.get(j + i) + r.get(j + i))), v[i] = s.get(j + i);
+            store_piece<kVec>(static_cast<T*>(a.total) + row * a.ld_t, column<kVec>(j, tid, threads), a.dim, v);
+        }
     }
     float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kE; ++j) sum = __fmaf_rn(v[j], v[j], sum);
-    sum = row_sum<kWarpRow>(sum, 0.0f, part).x;
+    for (int j = 0; j < kE; ++j) sum = __fmaf_rn(s.get(j), s.get(j), sum);
+    sum = row_sum<kWarpRow>(sum, part[0]);
     float rstd = __frsqrt_rn(__fmaf_rn(sum, a.inv_dim, a.eps));
     if (sum > kHuge) {
         sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < kE; ++j) {
-            const float t = v[j] * kShrink;
+            const float t = s.get(j) * kShrink;
             sum = __fmaf_rn(t, t, sum);
         }
-        rstd = __frsqrt_rn(row_sum<kWarpRow>(sum, 0.0f, part).x * a.inv_dim) * kShrink;
+        rstd = __frsqrt_rn(row_sum<kWarpRow>(sum, part[1]) * a.inv_dim) * kShrink;
     }
-    {
-        float w[kE];
-        load_row<kE, kVec>(a.weight, a.dim, tid, threads, w);
-#pragma unroll
-        for (int j = 0; j < kE; ++j) v[j] = v[j] * rstd * w[j];
-    }
-    if (a.y) store_row<kE, kVec>(static_cast<T*>(a.y) + row * a.ld_y, a.dim, tid, threads, v);
-    if (!a.codes) return;
+    T* y = static_cast<T*>(a.y) + row * a.ld_y;
     uint8_t* codes = a.codes + row * a.dim;
     float* scales = a.scales + row * a.groups;
-    constexpr int kPart = kVec ? 8 : 4;
 #pragma unroll
-    for (int j = 0; j < kE; j += kPart) {
+    for (int j = 0; j < kE; j += kP) {
         const int c = column<kVec>(j, tid, threads);
+        float v[kP];
+        load_piece<kVec>(a.weight, c, a.dim, v);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) v[i] = s.get(j + i) * rstd * v[i];
+        if (a.y) store_piece<kVec>(y, c, a.dim, v);
+        if (!a.codes) continue;
         float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kPart; ++i) amax = fmaxf(amax, fabsf(v[j + i]));
-#pragma unroll
-        for (int o = kVec ? 8 : 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        float scale = __fdiv_rn(amax, 448.0f);
-        if (scale == 0.0f) scale = 1.0f;
+        for (int i = 0; i < kP; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        // of non-negative numbers, as integers: 16 lanes hold 128 columns, or all
+        const uint32_t lanes = kVec ? tid & 16 ? 0xffff0000u : 0xffffu : 0xffffffffu;
+        amax = __uint_as_float(__reduce_max_sync(lanes, __float_as_uint(amax)));
+        // one division for the 128: an element a rounding away from the middle of two codes may take the other.
+        // Below 2^-117 the reciprocal would leave FP32: such a group is 0.
+        const float scale = amax >= 0x1p-117f ? __fdiv_rn(amax, 448.0f) : 1.0f, up = __frcp_rn(scale);
         if constexpr (kVec) {
             if (c >= a.dim) continue;
             if ((tid & 15) == 0) scales[c >> 7] = scale;
             uint32_t two[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                two[i] = e4m3x2(__fdiv_rn(v[j + 2 * i], scale), __fdiv_rn(v[j + 2 * i + 1], scale));
+            for (int i = 0; i < 4; ++i) two[i] = e4m3x2(v[2 * i] * up, v[2 * i + 1] * up);
             *reinterpret_cast<uint2*>(codes + c) = make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
         } else {
             if ((tid & 31) == 0 && c < a.dim) scales[c >> 7] = scale;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (c + 32 * i < a.dim) codes[c + 32 * i] = (uint8_t)e4m3x2(__fdiv_rn(v[j + i], scale), 0.0f);
+                if (c + 32 * i < a.dim) codes[c + 32 * i] = (uint8_t)e4m3x2(v[i] * up, 0.0f);
         }
     }
 }
@@ -217,72 +268,240 @@ struct GradArgs {
     float* part;  // [CTAs, dim]
 };
 
-// dx of rows blockIdx.x, + gridDim.x, ...; the columns' sums of dy h over them stay in
-// registers and are written at the end (of 8 warps' rows in their order).
-template <class T, int kE, bool kVec, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 256 : 512) norm_grad_kernel(const GradArgs a)
+// dx of a row, and its part of d_weight, from what a thread holds of the normed row and dy; `w` the weight, `sums`
+// adds two numbers over the row's threads, `more` d_total's elements from a column on.
+template <class T, int kE, bool kVec, class F, class G>
+__device__ __forceinline__ void grad_row(const GradArgs& a, int64_t row, int tid, int threads, const Held<T, kE>& s, const Held<T, kE>& d,
+                                         const float* w, float (&dw)[kE], F sums, G more)
 {
-    __shared__ float2 part[32];
-    __shared__ float columns[kWarpRow ? 32 * kE : 1];
-    const int threads = kWarpRow ? 32 : blockDim.x, tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t first = kWarpRow ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
-    const int64_t step = (int64_t)gridDim.x * (kWarpRow ? 8 : 1);
+    constexpr int kP = kPiece<kVec>;
+    auto add = [&](float by) {
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < kE; j += kP) {
+            float wj[kP];
+            load_piece<kVec>(w, column<kVec>(j, tid, threads), a.dim, wj);
+#pragma unroll
+            for (int i = 0; i < kP; ++i) {
+                const float v = s.get(j + i) * by;
+                sum.x = __fmaf_rn(v, v, sum.x);
+                sum.y = __fmaf_rn(d.get(j + i) * wj[i], v, sum.y);
+            }
+        }
+        return sum;
+    };
+    float2 sum = sums(add(1.0f), 0);
+    float rstd = __frsqrt_rn(__fmaf_rn(sum.x, a.inv_dim, a.eps)), mean = sum.y * rstd * a.inv_dim;
+    if (sum.x > kHuge) {  // as the norm's
+        sum = sums(add(kShrink), 2);
+        const float r = __frsqrt_rn(sum.x * a.inv_dim);
+        rstd = r * kShrink;
+        mean = sum.y * r * a.inv_dim;
+    }
+    T* dx = static_cast<T*>(a.dx) + row * a.ld_dx;
+#pragma unroll
+    for (int j = 0; j < kE; j += kP) {
+        const int c = column<kVec>(j, tid, threads);
+        float v[kP];
+        load_piece<kVec>(w, c, a.dim, v);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            const float h = s.get(j + i) * rstd;
+            dw[j + i] = __fmaf_rn(d.get(j + i), h, dw[j + i]);
+            v[i] = rstd * __fmaf_rn(-h, mean, d.get(j + i) * v[i]);
+        }
+        if (a.d_total) more(c, v);
+        store_piece<kVec>(dx, c, a.dim, v);
+    }
+}
+
+// Rows of a warp each, 8 a CTA, + 8 gridDim.x ...: the columns' sums of dy h over them stay in
+// registers and are added at the end, in the order of the warps.
+template <class T, int kE, bool kVec>
+__global__ void __launch_bounds__(256) norm_grad_kernel(const GradArgs a)
+{
+    __shared__ float columns[32 * kE];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float dw[kE];
 #pragma unroll
     for (int j = 0; j < kE; ++j) dw[j] = 0.0f;
-    for (int64_t row = first; row < a.rows; row += step) {
-        float v[kE], d[kE], w[kE];
-        load_row<kE, kVec>(static_cast<const T*>(a.s) + row * a.ld_s, a.dim, tid, threads, v);
-        load_row<kE, kVec>(static_cast<const T*>(a.dy) + row * a.ld_dy, a.dim, tid, threads, d);
-        load_row<kE, kVec>(a.weight, a.dim, tid, threads, w);
-        float sum = 0.0f, dot = 0.0f;
+    for (int64_t row = (int64_t)blockIdx.x * 8 + warp; row < a.rows; row += (int64_t)gridDim.x * 8) {
+        Held<T, kE> s, d;
+        hold<kE, kVec, false, T>(s, static_cast<const T*>(a.s) + row * a.ld_s, nullptr, 0, 0, a.dim, lane, 32);
+        hold<kE, kVec, false, T>(d, static_cast<const T*>(a.dy) + row * a.ld_dy, nullptr, 0, 0, a.dim, lane, 32);
+        grad_row<T, kE, kVec>(
+            a, row, lane, 32, s, d, a.weight, dw, [](float2 v, int) { return warp_sum(v); },
+            [&](int c, float(&v)[kPiece<kVec>]) {
+                float t[kPiece<kVec>];
+                load_piece<kVec>(static_cast<const T*>(a.d_total) + row * a.ld_t, c, a.dim, t);
 #pragma unroll
-        for (int j = 0; j < kE; ++j) {
-            sum = __fmaf_rn(v[j], v[j], sum);
-            dot = __fmaf_rn(d[j] * w[j], v[j], dot);
-        }
-        const float2 both = row_sum<kWarpRow>(sum, dot, part);
-        float rstd = __frsqrt_rn(__fmaf_rn(both.x, a.inv_dim, a.eps)), mean = both.y * rstd * a.inv_dim;
-        if (both.x > kHuge) {  // as the norm's
-            sum = dot = 0.0f;
+                for (int i = 0; i < kPiece<kVec>; ++i) v[i] += t[i];
+            });
+    }
+    for (int q = 0; q < 8; ++q) {
+        if (warp == q)
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
-                const float t = v[j] * kShrink;
-                sum = __fmaf_rn(t, t, sum);
-                dot = __fmaf_rn(d[j] * w[j], t, dot);
+                const int c = column<kVec>(j, lane, 32);
+                columns[c] = q ? columns[c] + dw[j] : dw[j];
             }
-            const float2 again = row_sum<kWarpRow>(sum, dot, part);
-            const float r = __frsqrt_rn(again.x * a.inv_dim);
-            rstd = r * kShrink;
-            mean = again.y * r * a.inv_dim;
-        }
-#pragma unroll
-        for (int j = 0; j < kE; ++j) {
-            const float h = v[j] * rstd;
-            dw[j] = __fmaf_rn(d[j], h, dw[j]);
-            v[j] = rstd * __fmaf_rn(-h, mean, d[j] * w[j]);
-        }
-        if (a.d_total) {
-            load_row<kE, kVec>(static_cast<const T*>(a.d_total) + row * a.ld_t, a.dim, tid, threads, d);
-#pragma unroll
-            for (int j = 0; j < kE; ++j) v[j] += d[j];
-        }
-        store_row<kE, kVec>(static_cast<T*>(a.dx) + row * a.ld_dx, a.dim, tid, threads, v);
+        __syncthreads();
     }
-    float* out = a.part + (int64_t)blockIdx.x * a.dim;
-    if constexpr (kWarpRow) {
-        for (int q = 0; q < 8; ++q) {
-            if (threadIdx.x >> 5 == q)
+    for (int c = threadIdx.x; c < a.dim; c += 256) a.part[(int64_t)blockIdx.x * a.dim + c] = columns[c];
+}
+
+// ---- longer rows: on their way through shared memory ---------------------------------------
+//
+// A CTA's last warp copies its rows, a row of each input a stage, as soon as a stage has been read;
+// groups of the other warps take them in turn.  Bulk copies move whole 16 bytes on 16-byte
+// boundaries; what a row has before its first and behind its last such boundary is read where it lies.
+
+constexpr int kMostStages = 8, kMostGroups = 8;
+
+struct Ring {
+    const void* in[3];
+    int64_t ld[3];
+    int n;              // inputs
+    int stages, pitch;  // pitch: bytes of a row's place; no stages: rows too long for two are read where they lie
+    int groups, threads;  // threads of a group
+};
+
+template <class T>
+struct Span {  // of a row's elements in whole 16 bytes
+    int lo, hi;
+    __device__ __forceinline__ Span(const T* p, int dim)
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        lo = (int)((-at & 15) / sizeof(T));
+        hi = (int)((((at + dim * sizeof(T)) & ~(uintptr_t)15) - at) / sizeof(T));
+        if (hi < lo) hi = lo = 0;
+    }
+};
+
+// By one thread: the copies of a row's inputs to a stage, counted on its barrier.
+template <class T>
+__device__ __forceinline__ void fetch(const Ring& r, int64_t row, int dim, uint32_t stage, uint32_t bar)
+{
+    uint32_t bytes = 0;
 #pragma unroll
-                for (int j = 0; j < kE; ++j) {
-                    const int c = column<kVec>(j, tid, 32);
-                    columns[c] = q ? columns[c] + dw[j] : dw[j];
-                }
-            __syncthreads();
+    for (int k = 0; k < 3; ++k) {
+        if (k >= r.n) break;
+        const Span<T> s(static_cast<const T*>(r.in[k]) + row * r.ld[k], dim);
+        bytes += (uint32_t)(s.hi - s.lo) * sizeof(T);
+    }
+    tc::bar_expect(bar, bytes);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        if (k >= r.n) break;
+        const T* p = static_cast<const T*>(r.in[k]) + row * r.ld[k];
+        const Span<T> s(p, dim);
+        if (s.hi == s.lo) continue;
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         stage + k * r.pitch + (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15) + (uint32_t)(s.lo * sizeof(T))),
+                     "l"(p + s.lo), "r"((uint32_t)(s.hi - s.lo) * (uint32_t)sizeof(T)), "r"(bar)
+                     : "memory");
+    }
+}
+
+// What a thread takes of input k of the row in a stage.
+template <int kE, bool kVec, class T>
+__device__ __forceinline__ void take(Held<T, kE>& v, const Ring& r, const void* in, int64_t ld, int k, int64_t row, int dim,
+                                     const uint8_t* stage, int tid)
+{
+    const T* p = static_cast<const T*>(in) + row * ld;
+    const Span<T> s(p, dim);
+    if (r.stages)
+        hold<kE, kVec, true, T>(v, p, reinterpret_cast<const T*>(stage + k * r.pitch + (reinterpret_cast<uintptr_t>(p) & 15)), s.lo, s.hi,
+                                dim, tid, r.threads);
+    else
+        hold<kE, kVec, false, T>(v, p, nullptr, 0, 0, dim, tid, r.threads);
+}
+
+template <class T, int kE, bool kVec>
+__global__ void __launch_bounds__(512, 1) norm_grad_ring_kernel(const GradArgs a, const Ring r)
+{
+    extern __shared__ __align__(128) uint8_t smem[];  // full, empty [kMostStages], the weight, stages
+    __shared__ float2 part[kMostGroups][3][32];
+    const uint32_t bar_full = tc::smem_addr(smem), bar_empty = bar_full + 8 * kMostStages;
+    float* weight = reinterpret_cast<float*>(smem + 128);
+    uint8_t* stages = smem + 128 + (a.dim + 3) / 4 * 16;
+    const int stage_bytes = r.n * r.pitch, warps = r.threads >> 5;
+    const int group = threadIdx.x / r.threads, tid = threadIdx.x - group * r.threads;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < r.stages; ++i) {
+            tc::bar_init(bar_full + 8 * i, 1);
+            tc::bar_init(bar_empty + 8 * i, warps);
         }
-        for (int c = threadIdx.x; c < a.dim; c += 256) out[c] = columns[c];
-    } else {
-        store_row<kE, kVec>(out, a.dim, tid, threads, dw);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    for (int c = threadIdx.x; c < a.dim; c += blockDim.x) weight[c] = a.weight[c];
+    __syncthreads();
+    if (group == r.groups) {
+        if (tid != 0) return;
+        int slot = 0;
+        uint32_t phase = 0;
+        for (int64_t row = blockIdx.x; r.stages && row < a.rows; row += gridDim.x) {
+            if (!tc::bar_wait(bar_empty + 8 * slot, phase ^ 1)) break;  // the readers' waits run out too
+            fetch<T>(r, row, a.dim, tc::smem_addr(stages) + slot * stage_bytes, bar_full + 8 * slot);
+            if (++slot == r.stages) slot = 0, phase ^= 1;
+        }
+        return;
+    }
+    float dw[kE];
+#pragma unroll
+    for (int j = 0; j < kE; ++j) dw[j] = 0.0f;
+    int slot = group, odd = 0;
+    uint32_t phase = 0;
+    for (int64_t row = blockIdx.x + (int64_t)group * gridDim.x; row < a.rows; row += (int64_t)r.groups * gridDim.x) {
+        const bool ok = r.stages == 0 || tc::bar_wait(bar_full + 8 * slot, phase);
+        const uint8_t* stage = stages + slot * stage_bytes;
+        Held<T, kE> s, d;
+        take<kE, kVec, T>(s, r, a.s, a.ld_s, 0, row, a.dim, stage, tid);
+        take<kE, kVec, T>(d, r, a.dy, a.ld_dy, 1, row, a.dim, stage, tid);
+        auto sums = [&](float2 v, int again) {
+            v = warp_sum(v);
+            if (!ok) v.x = NAN;  // a copy that never came
+            // two rows' sums lie side by side: one barrier a row
+            float2* mine = part[group][again ? 2 : odd];
+            if ((tid & 31) == 0) mine[tid >> 5] = v;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(r.threads) : "memory");
+            v = mine[0];
+            for (int w = 1; w < warps; ++w) v.x += mine[w].x, v.y += mine[w].y;
+            return v;
+        };
+        const T* more = static_cast<const T*>(a.d_total) + row * a.ld_t;
+        const Span<T> span(more, a.dim);
+        const T* here = reinterpret_cast<const T*>(stage + 2 * r.pitch + (reinterpret_cast<uintptr_t>(more) & 15));
+        grad_row<T, kE, kVec>(a, row, tid, r.threads, s, d, weight, dw, sums, [&](int c, float(&v)[kPiece<kVec>]) {
+            float t[kPiece<kVec>];
+            if (!r.stages) {
+                load_piece<kVec>(more, c, a.dim, t);
+            } else if constexpr (kVec) {
+                load_piece<true>(here, c, a.dim, t);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = c + 32 * i;
+                    t[i] = 0.0f;
+                    if (e >= span.lo && e < span.hi)
+                        t[i] = to_float(here[e]);
+                    else if (e < a.dim)
+                        t[i] = to_float(more[e]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPiece<kVec>; ++i) v[i] += t[i];
+        });
+        __syncwarp();
+        if (r.stages && (tid & 31) == 0) tc::bar_arrive(bar_empty + 8 * slot);
+        odd ^= 1;
+        slot += r.groups;
+        if (slot >= r.stages) slot -= r.stages, phase ^= 1;
+    }
+#pragma unroll
+    for (int j = 0; j < kE; ++j) {
+        const int c = column<kVec>(j, tid, r.threads);
+        if (c < a.dim) a.part[((int64_t)blockIdx.x * r.groups + group) * a.dim + c] = dw[j];
     }
 }
 
@@ -315,66 +534,91 @@ int check(int64_t rows, int64_t dim, int32_t type, float eps)
 // Whether a buffer's rows can be taken 8 elements at a time.
 bool fits(const void* p, int64_t ld, int size) { return !p || (aligned(p, 16) && ld * size % 16 == 0); }
 
-// Threads of a row with 8 or 32 elements each.
-int threads_of(int64_t dim, int each)
+constexpr int kWarpDim = 1024;  // up to here a warp has a row
+
+// Threads of a CTA's row with so many elements each.
+int threads_of(int64_t dim, int each) { return (int)ceil_div(dim, each * 32) * 32; }
+// The gradient's ring: a CTA an SM of at most 16 warps, for 128 registers a thread; as many elements a thread as
+// they hold of three inputs and the weight's sums (groups of 28 warps at 8 elements took 120 us for XX).
+constexpr int kRingSmem = 224 * 1024;
+int ring_each(int64_t dim, int size) { return size == 2 || dim > 7680 ? 32 : 16; }
+int ring_groups(int64_t dim, int size) { return std::min(kMostGroups, std::max(1, 480 / threads_of(dim, ring_each(dim, size)))); }
+int shape_ring(Ring& r, int64_t dim, int size)  // bytes of shared memory
 {
-    int t = 32;
-    while ((int64_t)t * each < dim) t *= 2;
-    return t;
+    r.threads = threads_of(dim, ring_each(dim, size));
+    r.groups = ring_groups(dim, size);
+    r.pitch = (int)ceil_div(dim * size + 16, 16) * 16;
+    const int fixed = 128 + (int)ceil_div(dim, 4) * 16, stage = r.n * r.pitch;
+    r.stages = std::min(kMostStages, (kRingSmem - fixed - 6144) / stage);
+    if (r.stages < 2 || r.stages < r.groups || r.threads > 480) r.stages = 0;
+    return fixed + r.stages * stage;
 }
 
-template <template <class, int, bool, bool> class F, class... A>
-int by_shape(int32_t type, bool vec, int each, bool warp, const A&... args)
+// Calls f.template run<T, kE, kVec>() for the types and sizes of a call.
+template <int kLittle, int kMuch, class F>
+int by_shape(int32_t type, bool vec, int each, F f)
 {
-#define FP8Z1_CASE(T, E, V, W) \
-    if (each == E && vec == V && warp == W) return F<T, E, V, W>::run(args...);
-#define FP8Z1_CASES(T) \
-    FP8Z1_CASE(T, 8, true, true) FP8Z1_CASE(T, 8, true, false) FP8Z1_CASE(T, 8, false, true) \
-    FP8Z1_CASE(T, 8, false, false) FP8Z1_CASE(T, 32, true, true) FP8Z1_CASE(T, 32, true, false) \
-    FP8Z1_CASE(T, 32, false, true) FP8Z1_CASE(T, 32, false, false)
-    if (type == FP8Z1_F32) {
-        FP8Z1_CASES(float)
-    } else {
-        FP8Z1_CASES(bf16)
-    }
-#undef FP8Z1_CASES
-#undef FP8Z1_CASE
-    return FP8Z1_EINVAL;
+    if (type == FP8Z1_F32)
+        return each == kLittle ? (vec ? f.template run<float, kLittle, true>() : f.template run<float, kLittle, false>())
+                               : (vec ? f.template run<float, kMuch, true>() : f.template run<float, kMuch, false>());
+    return each == kLittle ? (vec ? f.template run<bf16, kLittle, true>() : f.template run<bf16, kLittle, false>())
+                           : (vec ? f.template run<bf16, kMuch, true>() : f.template run<bf16, kMuch, false>());
 }
 
-template <class T, int kE, bool kVec, bool kWarpRow>
-struct Norm {
-    static int run(const Args& a, int threads, cudaStream_t s)
+struct WarpRows {
+    const Args& a;
+    cudaStream_t s;
+    template <class T, int kE, bool kVec>
+    int run() const
     {
-        count_launch();
-        if (kWarpRow)
-            norm_kernel<T, kE, kVec, true><<<(unsigned)ceil_div(a.rows, 8), 256, 0, s>>>(a);
-        else
-            norm_kernel<T, kE, kVec, false><<<(unsigned)a.rows, threads, 0, s>>>(a);
+        norm_kernel<T, kE, kVec, true><<<(unsigned)ceil_div(a.rows, 8), 256, 0, s>>>(a);
+        return launch_status();
+    }
+};
+struct CtaRows {
+    const Args& a;
+    int threads;
+    cudaStream_t s;
+    template <class T, int kE, bool kVec>
+    int run() const
+    {
+        norm_kernel<T, kE, kVec, false><<<(unsigned)a.rows, threads, 0, s>>>(a);
+        return launch_status();
+    }
+};
+struct GradWarpRows {
+    const GradArgs& a;
+    unsigned ctas;
+    cudaStream_t s;
+    template <class T, int kE, bool kVec>
+    int run() const
+    {
+        norm_grad_kernel<T, kE, kVec><<<ctas, 256, 0, s>>>(a);
+        return launch_status();
+    }
+};
+struct GradRingRows {
+    const GradArgs& a;
+    const Ring& r;
+    int smem;
+    unsigned ctas;
+    cudaStream_t s;
+    template <class T, int kE, bool kVec>
+    int run() const
+    {
+        if (!allow_smem<norm_grad_ring_kernel<T, kE, kVec>>(kRingSmem - 6144)) return FP8Z1_ECUDA;
+        norm_grad_ring_kernel<T, kE, kVec><<<ctas, r.groups * r.threads + (r.stages ? 32 : 0), smem, s>>>(a, r);
         return launch_status();
     }
 };
 
-template <class T, int kE, bool kVec, bool kWarpRow>
-struct Grad {
-    static int run(const GradArgs& a, int threads, unsigned ctas, cudaStream_t s)
-    {
-        count_launch();
-        if constexpr (!kWarpRow && kE == 8)
-            return FP8Z1_EINVAL;  // not called: the gradient takes 32 elements a thread beyond a warp's
-        else
-            norm_grad_kernel<T, kE, kVec, kWarpRow><<<ctas, kWarpRow ? 256 : threads, 0, s>>>(a);
-        return launch_status();
-    }
-};
-
-// CTAs of the gradient: as many as run at once, each with a row at least.
+// CTAs of the gradient: as many as run at once, each with a row at least; and the rows of partial sums, at most.
 int64_t grad_ctas(int64_t rows, int64_t dim)
 {
-    const int threads = threads_of(dim, 32);
-    const int64_t most = (int64_t)kSms * (threads == 32 ? 2 : std::max(1, 512 / threads));
-    return std::max<int64_t>(1, std::min(most, threads == 32 ? ceil_div(rows, 8) : rows));
+    if (dim <= kWarpDim) return std::max<int64_t>(1, std::min<int64_t>(2 * kSms, ceil_div(rows, 8)));
+    return std::max<int64_t>(1, std::min<int64_t>(kSms, rows));
 }
+int64_t grad_parts(int64_t rows, int64_t dim) { return grad_ctas(rows, dim) * (dim <= kWarpDim ? 1 : std::max(ring_groups(dim, 2), ring_groups(dim, 4))); }
 
 }  // namespace
 
@@ -406,17 +650,20 @@ extern "C" int fp8z1_rms_norm(int64_t rows, int64_t dim, const void* x, int32_t 
     NvtxRange range("fp8z1_rms_norm");
     const bool vec = dim % 8 == 0 && fits(x, ld_x, size) && fits(residual, ld_r, size) && fits(total, ld_total, size) &&
                      fits(y, ld_y, size) && aligned(weight, 16) && aligned(codes, 8);
-    int each = 32, threads = threads_of(dim, 32);
-    if (dim <= 8192 && rows * threads < kSms * 512) each = 8, threads = threads_of(dim, 8);
     const Args a = {rows, (int)dim, eps, 1.0f / (float)dim, ld_x, ld_r, ld_total, ld_y, x, residual, weight, total, y,
                     codes, scales, (int)ceil_div(dim, 128)};
-    return by_shape<Norm>(type, vec, each, threads == 32, a, threads, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    count_launch();
+    if (dim <= 256 || (dim <= kWarpDim && rows > 8 * kSms)) return by_shape<8, 32>(type, vec, dim <= 256 ? 8 : 32, WarpRows{a, s});
+    // a row a CTA: few rows at 8 elements a thread, many at 32 (registers for eight CTAs' rows an SM)
+    const int each = dim <= 8192 && rows <= 4 * kSms ? 8 : 32;
+    return by_shape<8, 32>(type, vec, each, CtaRows{a, threads_of(dim, each), s});
 }
 
 extern "C" int fp8z1_rms_norm_grad_workspace(int64_t rows, int64_t dim, int64_t* bytes)
 {
     if (!bytes || check(rows, dim, FP8Z1_F32, 1.0f) != FP8Z1_OK) return FP8Z1_EINVAL;
-    *bytes = grad_ctas(rows, dim) * dim * 4;
+    *bytes = grad_parts(rows, dim) * dim * 4;
     return FP8Z1_OK;
 }
 
@@ -441,11 +688,26 @@ extern "C" int fp8z1_rms_norm_grad(int64_t rows, int64_t dim, const void* dy, in
     NvtxRange range("fp8z1_rms_norm_grad");
     const bool vec = dim % 8 == 0 && fits(dy, ld_dy, size) && fits(total, ld_total, size) && fits(d_total, ld_dt, size) &&
                      fits(dx, ld_dx, size) && aligned(weight, 16);
-    const int threads = threads_of(dim, 32);
-    const int each = dim <= 256 ? 8 : 32;
     const unsigned ctas = (unsigned)grad_ctas(rows, dim);
     const GradArgs a = {rows, (int)dim, eps, 1.0f / (float)dim, ld_dy, ld_total, ld_dt, ld_dx, dy, total, d_total, weight,
                         dx, static_cast<float*>(workspace)};
-    if ((st = by_shape<Grad>(type, vec, each, threads == 32, a, threads, ctas, s)) != FP8Z1_OK) return st;
-    return launch_column_sum(a.part, (int)ctas, dim, d_weight, s);
+    int parts = (int)ctas;
+    count_launch();
+    if (dim <= kWarpDim) {
+        st = by_shape<8, 32>(type, vec, dim <= 256 ? 8 : 32, GradWarpRows{a, ctas, s});
+    } else {
+        Ring r = {};
+        r.in[0] = total;
+        r.ld[0] = ld_total;
+        r.in[1] = dy;
+        r.ld[1] = ld_dy;
+        r.in[2] = d_total;
+        r.ld[2] = ld_dt;
+        r.n = d_total ? 3 : 2;
+        const int smem = shape_ring(r, dim, size);
+        parts *= r.groups;
+        st = by_shape<16, 32>(type, vec, ring_each(dim, size), GradRingRows{a, r, smem, ctas, s});
+    }
+    if (st != FP8Z1_OK) return st;
+    return launch_column_sum(a.part, parts, dim, d_weight, s);
 }

@@ -32,7 +32,7 @@ def make(rows, dim, dtype, seed, by=1.0):
 
 SHAPES = [(1, 1), (1, 7), (3, 8), (5, 64), (2, 127), (2, 128), (2, 129), (9, 255), (8, 256), (17, 257), (64, 1000), (33, 1024),
           (2, 1025), (7, 2048), (700, 520), (1, 7168), (2500, 304), (5, 4097), (3, 8192), (2, 8200), (2, 16384), (2, 16383),
-          (400, 7168), (5000, 72)]
+          (400, 7168), (5000, 72), (1300, 2049), (1900, 1032), (650, 8200), (620, 16383), (1500, 7168), (3000, 1100)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
