@@ -562,7 +562,12 @@ def _op(name: str):
 
 def _at(x):
     """A tensor's address (None and ints pass)."""
-    return x.data_ptr() if hasattr(x, "data_ptr") else _ptr(x)
+    if x is None:
+        return None
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return _ptr(x)
 
 
 def fp8z1_embed(vocab: int, dim: int, codes, scales, ids, id_bytes: int, tokens: int, alpha: float, out,

@@ -105,14 +105,20 @@ def _rows(t: torch.Tensor, what: str) -> int:
     return ld
 
 
-def _rows_of(t: torch.Tensor, what: str):
-    """(rows, row stride) of [*, dim]: a 2-D tensor of any row stride, or contiguous."""
-    if t.dim() == 2:
-        return t.shape[0], _rows(t, what)
-    if t.dim() < 1 or not t.is_contiguous():
+def _stride_of(t: torch.Tensor, dim: int, what: str) -> int:
+    """The row stride of [*, dim]: contiguous, or 2-D of any row stride."""
+    if t.is_contiguous():
+        return dim
+    if t.dim() != 2:
         _bad(f"{what} must be contiguous, or 2-D")
-    dim = t.shape[-1]
-    return (t.numel() // dim if dim else 0), dim
+    return _rows(t, what)
+
+
+def _fits(t: torch.Tensor, shape, dtype, dev: int, dim: int, what: str) -> int:
+    """The row stride of a tensor that has to be of this shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        _bad(f"{what} must be {dtype} of shape {tuple(shape)} on the inputs' device")
+    return dim if t.is_contiguous() else _stride_of(t, dim, what)
 
 
 def _fp8_weight(codes: torch.Tensor, scale: torch.Tensor, what: str):
@@ -316,35 +322,37 @@ def distill_loss_grad(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_l
 
 
 def _norm(x, weight, residual, eps, fp8, out, total, stream):
-    kind, shape = _TYPES.get(x.dtype), x.shape
-    if kind is None or x.dim() < 1:
+    shape, dtype = x.shape, x.dtype
+    kind = _TYPES.get(dtype)
+    if kind is None or not shape:
         _bad("x must be float32 or bfloat16 [*, dim]")
     dim = shape[-1]
     if weight.dtype != torch.float32 or weight.shape != (dim,) or not weight.is_contiguous():
         _bad(f"weight must be contiguous float32 [{dim}]")
-    rows, ld_x = _rows_of(x, "x")
+    ld_x = _stride_of(x, dim, "x")
     dev = x.get_device()
     raw, other = _begin(dev, stream)
-    _same_device(dev, weight)
-    ld_r = ld_t = ld_y = 0
+    if weight.get_device() != dev:
+        _bad("the tensors are on several devices")
+    ld_r, ld_t, ld_y, scale = 0, dim, dim, None
     if residual is not None:
-        ld_r = _rows_of(_given(residual, shape, x.dtype, dev, "residual"), "residual")[1]
+        ld_r = _fits(residual, shape, dtype, dev, dim, "residual")
         if total is None:
-            total = _new(shape, x.dtype, dev, other)
-        ld_t = _rows_of(_given(total, shape, x.dtype, dev, "total"), "total")[1]
+            total = _new(shape, dtype, dev, other)
+        else:
+            ld_t = _fits(total, shape, dtype, dev, dim, "total")
     elif total is not None:
         _bad("total is the sum with a residual")
-    scale = None
+    y = codes = None
     if fp8:
         codes = out = _new(shape, torch.float8_e4m3fn, dev, other)
-        scale = _new(shape[:-1] + ((dim + 127) // 128,), torch.float32, dev, other)
-        y = None
+        scale = _new((*shape[:-1], (dim + 127) // 128), torch.float32, dev, other)
+    elif out is None:
+        y = out = _new(shape, dtype, dev, other)
     else:
-        if out is None:
-            out = _new(shape, x.dtype, dev, other)
-        y, codes = _given(out, shape, x.dtype, dev, "out"), None
-        ld_y = _rows_of(y, "out")[1]
-    F.fp8z1_rms_norm(rows, dim, x, kind, ld_x, residual, ld_r, weight, eps, total, ld_t, y, ld_y, codes, scale, raw)
+        y, ld_y = out, _fits(out, shape, dtype, dev, dim, "out")
+    F.fp8z1_rms_norm(x.numel() // dim if dim else 0, dim, x, kind, ld_x, residual, ld_r, weight, eps, total, ld_t, y, ld_y,
+                     codes, scale, raw)
     return out, scale, total
 
 
@@ -373,27 +381,31 @@ def rms_norm_grad(dy: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, *
     """(dx, d_weight) of ``rms_norm`` from the rows that it normed (its ``total``, or x):
     dx in their type, which is the residual's gradient too, with ``d_total`` (what
     reaches the sum past the norm) added; d_weight float32 [dim]."""
-    kind, shape = _TYPES.get(total.dtype), total.shape
-    if kind is None or total.dim() < 1:
+    shape, dtype = total.shape, total.dtype
+    kind = _TYPES.get(dtype)
+    if kind is None or not shape:
         _bad("total must be float32 or bfloat16 [*, dim]")
     dim = shape[-1]
     if weight.dtype != torch.float32 or weight.shape != (dim,) or not weight.is_contiguous():
         _bad(f"weight must be contiguous float32 [{dim}]")
-    rows, ld_s = _rows_of(total, "total")
+    ld_s = _stride_of(total, dim, "total")
     dev = total.get_device()
     raw, other = _begin(dev, stream)
-    _same_device(dev, weight)
-    ld_dy = _rows_of(_given(dy, shape, total.dtype, dev, "dy"), "dy")[1]
-    ld_t = 0
+    if weight.get_device() != dev:
+        _bad("the tensors are on several devices")
+    ld_dy = _fits(dy, shape, dtype, dev, dim, "dy")
+    ld_t, ld_dx = 0, dim
     if d_total is not None:
-        ld_t = _rows_of(_given(d_total, shape, total.dtype, dev, "d_total"), "d_total")[1]
+        ld_t = _fits(d_total, shape, dtype, dev, dim, "d_total")
     if dx is None:
-        dx = _new(shape, total.dtype, dev, other)
-    ld_dx = _rows_of(_given(dx, shape, total.dtype, dev, "dx"), "dx")[1]
+        dx = _new(shape, dtype, dev, other)
+    else:
+        ld_dx = _fits(dx, shape, dtype, dev, dim, "dx")
     if d_weight is None:
         d_weight = _new((dim,), torch.float32, dev, other)
     elif not _given(d_weight, (dim,), torch.float32, dev, "d_weight").is_contiguous():
         _bad("d_weight must be contiguous")
+    rows = total.numel() // dim if dim else 0
     ws = _scratch(F.fp8z1_rms_norm_grad_workspace(rows, dim), torch.uint8, dev, other)
     F.fp8z1_rms_norm_grad(rows, dim, dy, kind, ld_dy, total, ld_s, weight, eps, d_total, ld_t, dx, ld_dx, d_weight, ws,
                           raw)
@@ -415,12 +427,11 @@ def route(ids: torch.Tensor, experts: int, *, stream=None) -> Route:
     """Sorts the choices ids[t, j] (int32 or int64 [tokens, top], or [tokens]) by
     expert, each expert's in the order of the choices; an id outside [0, experts)
     is no choice."""
-    nbytes = _ID_BYTES.get(ids.dtype)
-    if nbytes is None or ids.dim() not in (1, 2) or not ids.is_contiguous():
+    nbytes, shape = _ID_BYTES.get(ids.dtype), ids.shape
+    if nbytes is None or len(shape) not in (1, 2) or not ids.is_contiguous():
         _bad("ids must be contiguous int32 or int64 [tokens, top]")
-    tokens, top = ids.shape if ids.dim() == 2 else (ids.shape[0], 1)
-    dev = ids.get_device()
-    raw, other = _begin(dev, stream)
+    tokens, top = shape if len(shape) == 2 else (shape[0], 1)
+    raw, other = _begin(dev := ids.get_device(), stream)
     if not 1 <= experts <= 1024:
         _bad("experts must be 1 to 1024")
     offsets = _new(experts + 1, torch.int32, dev, other)
@@ -431,25 +442,28 @@ def route(ids: torch.Tensor, experts: int, *, stream=None) -> Route:
 
 def _route_dims(r: Route, dev: int):
     offsets, place = r
-    if place.dtype != torch.int32 or place.dim() != 2 or not place.is_contiguous():
+    shape, ends = place.shape, offsets.shape
+    if place.dtype != torch.int32 or len(shape) != 2 or not place.is_contiguous():
         _bad("place must be contiguous int32 [tokens, top]")
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 2 or not offsets.is_contiguous():
+    if offsets.dtype != torch.int32 or len(ends) != 1 or ends[0] < 2 or not offsets.is_contiguous():
         _bad("offsets must be contiguous int32 [experts + 1]")
-    _same_device(dev, offsets, place)
-    return place.shape[0], place.shape[1], offsets.shape[0] - 1
+    if offsets.get_device() != dev or place.get_device() != dev:
+        _bad("the tensors are on several devices")
+    return shape[0], shape[1], ends[0] - 1
 
 
 def _plain_rows(t: torch.Tensor, rows: int, what: str):
     """(type, dim, row stride) of float32 or bfloat16 [rows, dim]."""
-    kind = _TYPES.get(t.dtype)
-    if kind is None or t.dim() != 2 or t.shape[0] != rows:
+    kind, shape = _TYPES.get(t.dtype), t.shape
+    if kind is None or len(shape) != 2 or shape[0] != rows:
         _bad(f"{what} must be float32 or bfloat16 [{rows}, dim]")
-    return kind, t.shape[1], _rows(t, what)
+    dim = shape[1]
+    return kind, dim, dim if t.is_contiguous() else _rows(t, what)
 
 
-def _choice_weight(weight, shape):
-    if weight.dtype != torch.float32 or weight.shape != shape or not weight.is_contiguous():
-        _bad(f"weight must be contiguous float32 {tuple(shape)}")
+def _choice_weight(weight, shape, dev: int):
+    if weight.dtype != torch.float32 or weight.shape != shape or not weight.is_contiguous() or weight.get_device() != dev:
+        _bad(f"weight must be contiguous float32 {tuple(shape)} on the rows' device")
 
 
 def dispatch(x: torch.Tensor, r: Route, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -459,10 +473,12 @@ def dispatch(x: torch.Tensor, r: Route, *, out: Optional[torch.Tensor] = None, s
     tokens, top, experts = _route_dims(r, dev)
     kind, dim, ld = _plain_rows(x, tokens, "x")
     raw, other = _begin(dev, stream)
+    ld_o, shape = dim, (tokens * top, dim)
     if out is None:
-        out = _new((tokens * top, dim), x.dtype, dev, other)
-    ld_o = _rows(_given(out, (tokens * top, dim), x.dtype, dev, "out"), "out")
-    F.fp8z1_dispatch(tokens, top, experts, dim, x, kind, ld, r.offsets, r.place, out, ld_o, raw)
+        out = _new(shape, x.dtype, dev, other)
+    else:
+        ld_o = _fits(out, shape, x.dtype, dev, dim, "out")
+    F.fp8z1_dispatch(tokens, top, experts, dim, x, kind, ld, r[0], r[1], out, ld_o, raw)
     return out
 
 
@@ -475,16 +491,16 @@ def combine(rows: torch.Tensor, r: Route, weight: Optional[torch.Tensor] = None,
     tokens, top, _ = _route_dims(r, dev)
     kind, dim, ld = _plain_rows(rows, tokens * top, "rows")
     if weight is not None:
-        _choice_weight(weight, r.place.shape)
+        _choice_weight(weight, (tokens, top), dev)
     raw, other = _begin(dev, stream)
-    _same_device(dev, weight)
-    shape, ld_r = (tokens, dim), 0
+    shape, ld_r, ld_y = (tokens, dim), 0, dim
     if residual is not None:
-        ld_r = _rows(_given(residual, shape, rows.dtype, dev, "residual"), "residual")
+        ld_r = _fits(residual, shape, rows.dtype, dev, dim, "residual")
     if out is None:
         out = _new(shape, rows.dtype, dev, other)
-    ld_y = _rows(_given(out, shape, rows.dtype, dev, "out"), "out")
-    F.fp8z1_combine(tokens, top, dim, rows, kind, ld, r.place, weight, residual, ld_r, out, ld_y, raw)
+    else:
+        ld_y = _fits(out, shape, rows.dtype, dev, dim, "out")
+    F.fp8z1_combine(tokens, top, dim, rows, kind, ld, r[1], weight, residual, ld_r, out, ld_y, raw)
     return out
 
 
@@ -502,16 +518,16 @@ def combine_grad(dy: torch.Tensor, rows: torch.Tensor, r: Route, weight: torch.T
     dev = rows.get_device()
     tokens, top, experts = _route_dims(r, dev)
     kind, dim, ld = _plain_rows(rows, tokens * top, "rows")
-    _choice_weight(weight, r.place.shape)
+    _choice_weight(weight, (tokens, top), dev)
     raw, other = _begin(dev, stream)
-    _same_device(dev, weight)
-    ld_dy = _rows(_given(dy, (tokens, dim), rows.dtype, dev, "dy"), "dy")
+    ld_dy, ld_d = _fits(dy, (tokens, dim), rows.dtype, dev, dim, "dy"), dim
     if out is None:
         out = _new(rows.shape, rows.dtype, dev, other)
-    ld_d = _rows(_given(out, rows.shape, rows.dtype, dev, "out"), "out")
+    else:
+        ld_d = _fits(out, rows.shape, rows.dtype, dev, dim, "out")
     d_weight = _new((tokens, top), torch.float32, dev, other)
-    F.fp8z1_combine_grad(tokens, top, experts, dim, dy, kind, ld_dy, rows, ld, r.offsets, r.place, weight, out, ld_d,
-                         d_weight, raw)
+    F.fp8z1_combine_grad(tokens, top, experts, dim, dy, kind, ld_dy, rows, ld, r[0], r[1], weight, out, ld_d, d_weight,
+                         raw)
     return out, d_weight
 
 
@@ -522,20 +538,21 @@ _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _linear_dims(x, weight, scale, transposed, activation, y_type):
-    """(dims, width of x, width of y)"""
+    """(dims, width of x, width of y, row stride of x)"""
     e, r, c = _fp8_weight(weight, scale, "the weight")
+    act, kind, shape = _ACTS.get(activation, -1), _TYPES.get(y_type), x.shape
     if e != 1:
         _bad("a product's weight is [rows, cols]")
-    act, kind = _ACTS.get(activation, -1), _TYPES.get(y_type)
     if act < 0:
         _bad(f"no activation {activation!r}: None, 'silu' or 'gelu_tanh'")
     if kind is None:
         _bad(f"no product of {y_type}")
     inner, outer = (c, r) if transposed else (r, c)
-    if x.dim() != 2 or x.shape[1] != inner:
+    if len(shape) != 2 or shape[1] != inner:
         _bad(f"x must be [tokens, {inner}]")
-    x_type = F.E4M3 if x.dtype in _CODES else F.BF16 if x.dtype == torch.bfloat16 else _bad("x must be bfloat16 or E4M3 codes")
-    return F.fp8z1_linear_dims(x.shape[0], r, c, 1 if transposed else 0, act, x_type, kind), inner, outer
+    x_type = F.BF16 if x.dtype == torch.bfloat16 else F.E4M3 if x.dtype in _CODES else _bad("x must be bfloat16 or E4M3 codes")
+    dims = F.fp8z1_linear_dims(shape[0], r, c, 1 if transposed else 0, act, x_type, kind)
+    return dims, inner, outer, inner if x.is_contiguous() else _rows(x, "x")
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor, *, x_scale: Optional[torch.Tensor] = None,
@@ -548,29 +565,31 @@ def linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor, *,
     (width a multiple of 16 then).  ``bias`` float32, ``residual`` bfloat16;
     ``activation`` None, "silu" or "gelu_tanh".  With ``save`` also z = x w + bias,
     float32, which ``linear_grad`` reads where there is an activation: (y, z)."""
-    dims, inner, outer = _linear_dims(x, weight, weight_scale, transposed, activation, dtype)
+    dims, inner, outer, ld_x = _linear_dims(x, weight, weight_scale, transposed, activation, dtype)
     tokens = x.shape[0]
-    fp8 = dims.x_type == F.E4M3
-    if fp8 != (x_scale is not None):
-        _bad("E4M3 codes need x_scale, bfloat16 rows have none")
-    if fp8 and (x_scale.dtype != torch.float32 or x_scale.shape != (tokens, (inner + 127) // 128)
-                or not x_scale.is_contiguous()):
-        _bad("x_scale must be contiguous float32 [tokens, ceil(width / 128)]")
-    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (outer,) or not bias.is_contiguous()):
-        _bad(f"bias must be contiguous float32 [{outer}]")
     dev = x.get_device()
     raw, other = _begin(dev, stream)
+    if dims.x_type == F.E4M3:
+        if (x_scale is None or x_scale.dtype != torch.float32 or x_scale.shape != (tokens, (inner + 127) // 128)
+                or not x_scale.is_contiguous()):
+            _bad("E4M3 codes need x_scale, contiguous float32 [tokens, ceil(width / 128)]")
+        if tokens == 1:
+            ld_x = (inner + 15) // 16 * 16  # a single row's stride is whatever it was cut from
+    elif x_scale is not None:
+        _bad("bfloat16 rows have no x_scale")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (outer,) or not bias.is_contiguous()):
+        _bad(f"bias must be contiguous float32 [{outer}]")
     _same_device(dev, weight, weight_scale, x_scale, bias)
-    shape, ld_x, ld_r = (tokens, outer), _rows(x, "x"), 0
-    if fp8 and tokens == 1:
-        ld_x = (inner + 15) // 16 * 16  # a single row's stride is whatever it was cut from
+    shape, ld_r, ld_y = (tokens, outer), 0, outer
     if residual is not None:
-        ld_r = _rows(_given(residual, shape, torch.bfloat16, dev, "residual"), "residual")
+        ld_r = _fits(residual, shape, torch.bfloat16, dev, outer, "residual")
     if out is None:
         out = _new(shape, dtype, dev, other)
-    ld_y = _rows(_given(out, shape, dtype, dev, "out"), "out")
+    else:
+        ld_y = _fits(out, shape, dtype, dev, outer, "out")
     pre = _new(shape, torch.float32, dev, other) if save else None
-    ws = _scratch(F.fp8z1_linear_sizes(dims)[0], torch.uint8, dev, other)
+    size = F.fp8z1_linear_sizes(dims)[0]
+    ws = _scratch(size, torch.uint8, dev, other) if size else None
     F.fp8z1_linear(dims, x, ld_x, x_scale, weight, weight_scale, bias, residual, ld_r, out, ld_y, pre, ws, raw)
     return (out, pre) if save else out
 
@@ -583,7 +602,7 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, weight_
     bfloat16 (None without ``need_dx``), d_weight float32 in the weight's shape (None
     without ``need_weight``), d_bias float32 (None without ``bias``).  ``pre``: z of
     ``linear(..., save=True)``, with an activation.  The residual's gradient is dy."""
-    dims, inner, outer = _linear_dims(x, weight, weight_scale, transposed, activation, dy.dtype)
+    dims, inner, outer, ld_x = _linear_dims(x, weight, weight_scale, transposed, activation, dy.dtype)
     tokens = x.shape[0]
     if dims.x_type != F.BF16:
         _bad("the gradients need bfloat16 x")
@@ -612,6 +631,6 @@ def linear_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, weight_
     elif not _given(d_bias, (outer,), torch.float32, dev, "d_bias").is_contiguous():
         _bad("d_bias must be contiguous")
     ws = _scratch(F.fp8z1_linear_sizes(dims)[1], torch.uint8, dev, other)
-    F.fp8z1_linear_grad(dims, dy, _rows(dy, "dy"), x, _rows(x, "x"), weight, weight_scale, pre, dx,
-                        _rows(dx, "dx") if need_dx else 0, d_weight, d_bias, ws, raw)
+    F.fp8z1_linear_grad(dims, dy, outer if dy.is_contiguous() else _rows(dy, "dy"), x, ld_x, weight, weight_scale, pre, dx,
+                        inner, d_weight, d_bias, ws, raw)
     return dx, d_weight, d_bias
