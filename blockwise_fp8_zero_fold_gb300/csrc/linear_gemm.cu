@@ -184,8 +184,8 @@ many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     uint8_t* extra_ptr = smem_raw + (extra - smem_addr(smem_raw));
     volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(extra_ptr + 192);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sub = (int)cluster_rank();  // of the pair
+    const int warp = of_warp((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const int sub = blockIdx.x & 1;  // of the pair
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(bar_full + 8 * i, 1);
@@ -212,22 +212,24 @@ many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     cluster_sync();  // the other CTA counts on this one's barriers from here on
     fence_after();
     after_previous();
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = of_warp(*tmem_at);
     const int64_t total = (int64_t)a.m_tiles * a.n_tiles, i0 = blockIdx.x / 2, step = gridDim.x / 2;
     bool ok = true;
 
     if (warp < 4) {
         regs_less<48>();
-        if (warp == 0 && lane == 0) {
+        const bool one = one_lane();
+        if (warp == 0) {
             Turn<kStages> turn;
             for (int64_t i = i0; i < total && ok; i += step) {
                 const int n = (int)(i / a.m_tiles), m = (int)(i - (int64_t)n * a.m_tiles);
                 const int row = m * 256 + sub * 128, col = n * kCols + sub * 128;
                 for (int kb = 0; kb < a.k_blocks; ++kb, turn.next()) {
-                    if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
+                    if (!bar_wait_warp(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
                         ok = false;
                         break;
                     }
+                    if (!one) continue;
                     // both CTAs' copies are counted in the first one, whose thread multiplies
                     if (sub == 0) bar_expect(bar_full + 8 * turn.slot, 2 * kStageBytes);
                     const uint32_t full = first_of_pair(bar_full + 8 * turn.slot), dst = base + turn.slot * kStageBytes;
@@ -240,18 +242,19 @@ many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 }
             }
             // the copies in flight are read before the CTA ends, whatever became of the other warps
-            for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
-        } else if (warp == 1 && lane == 0 && sub == 0) {
+            for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait_warp(bar_empty + 8 * turn.slot, turn.phase ^ 1);
+        } else if (warp == 1 && sub == 0) {
             Turn<kStages> turn;
             Turn<2> acc;
             for (int64_t i = i0; i < total && ok; i += step) {
                 for (int kb = 0; kb < a.k_blocks; ++kb, turn.next(), acc.next()) {
-                    if (!bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) ||
-                        !bar_wait(bar_full + 8 * turn.slot, turn.phase)) {
+                    if (!bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1) ||
+                        !bar_wait_warp(bar_full + 8 * turn.slot, turn.phase)) {
                         ok = false;
                         break;
                     }
                     fence_after();
+                    if (!one) continue;
                     const uint32_t src = base + turn.slot * kStageBytes, d = tmem + acc.slot * kCols;
 #pragma unroll
                     for (int t = 0; t < kTerms; ++t)
@@ -270,7 +273,7 @@ many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 }
             }
             // every product issued ends, and its sums are read, before the tensor memory is freed
-            for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
+            for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
         } else if (warp >= 2) {
             // the factors of each step, s_b c_bn of both chunks of 128 columns for two rows a thread
             Turn<4> turn;
@@ -410,9 +413,8 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
     float* sums_at = reinterpret_cast<float*>(extra_ptr - kStages * S::kStageBytes);  // [kN][128], over the stages
     cg::cluster_group cluster = cg::this_cluster();
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = a.splits > 1 ? (int)cluster.block_rank() : 0;
-    const int n = blockIdx.x / a.splits;
+    const int warp = of_warp((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const int n = blockIdx.x / a.splits, split = blockIdx.x - n * a.splits;
     const int token0 = blockIdx.y * kN;
     const int k0 = a.k_blocks * split / a.splits, k1 = a.k_blocks * (split + 1) / a.splits;
     if (threadIdx.x == 0) {
@@ -440,69 +442,65 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
     __syncthreads();
     __syncwarp();
     fence_after();
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = of_warp(*tmem_at);
     bool ok = true;
 
     if (warp == 0) {
-        if (lane == 0) {
-            auto codes = [&](int kb, uint32_t full, uint32_t dst) {
-                if (kKMajor)
-                    load_2d(dst, &map_w, full, kb * 128, n * 128);
-                else
-                    load_2d(dst, &map_w, full, n * 128, kb * 128);
-            };
-            // the first codes are on their way before the kernel ahead has ended: it does not write them
-            const int ahead = min(kStages, k1 - k0);
-            for (int i = 0; i < ahead; ++i) {
-                bar_expect(bar_full + 8 * i, S::kStageBytes);
-                codes(k0 + i, bar_full + 8 * i, base + i * S::kStageBytes);
+        const bool one = one_lane();
+        auto codes = [&](int kb, uint32_t full, uint32_t dst) {
+            bar_expect(full, S::kStageBytes);
+            if (kKMajor)
+                load_2d(dst, &map_w, full, kb * 128, n * 128);
+            else
+                load_2d(dst, &map_w, full, n * 128, kb * 128);
+        };
+        // the first codes are on their way before the kernel ahead has ended: it does not write them
+        const int ahead = min(kStages, k1 - k0);
+        if (one)
+            for (int i = 0; i < ahead; ++i) codes(k0 + i, bar_full + 8 * i, base + i * S::kStageBytes);
+        after_previous();
+        Turn<kStages> turn;
+        for (int kb = k0; kb < k1; ++kb, turn.next()) {
+            const uint32_t full = bar_full + 8 * turn.slot, dst = base + turn.slot * S::kStageBytes;
+            if (kb >= k0 + ahead && !bar_wait_warp(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
+                ok = false;
+                break;
             }
-            after_previous();
-            Turn<kStages> turn;
-            for (int kb = k0; kb < k1; ++kb, turn.next()) {
-                const uint32_t full = bar_full + 8 * turn.slot, dst = base + turn.slot * S::kStageBytes;
-                if (kb >= k0 + ahead) {
-                    if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
-                        ok = false;
-                        break;
-                    }
-                    bar_expect(full, S::kStageBytes);
-                    codes(kb, full, dst);
-                }
-                load_2d(dst + kOperand, &map_hi, full, kb * 128, token0);
-                if (kTerms == 2) load_2d(dst + kOperand + S::kRowBytes, &map_lo, full, kb * 128, token0);
-            }
-            // the copies in flight are read before the CTA ends, whatever became of the other warps
-            for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
+            if (!one) continue;
+            if (kb >= k0 + ahead) codes(kb, full, dst);
+            load_2d(dst + kOperand, &map_hi, full, kb * 128, token0);
+            if (kTerms == 2) load_2d(dst + kOperand + S::kRowBytes, &map_lo, full, kb * 128, token0);
         }
+        // the copies in flight are read before the CTA ends, whatever became of the other warps
+        for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait_warp(bar_empty + 8 * turn.slot, turn.phase ^ 1);
     } else if (warp == 1) {
-        if (lane == 0) {
-            Turn<kStages> turn;
-            Turn<2> acc;
-            for (int kb = k0; kb < k1; ++kb, turn.next(), acc.next()) {
-                if (!bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) || !bar_wait(bar_full + 8 * turn.slot, turn.phase)) {
-                    ok = false;
-                    break;
-                }
-                fence_after();
-                const uint32_t src = base + turn.slot * S::kStageBytes, d = tmem + acc.slot * kN;
-#pragma unroll
-                for (int t = 0; t < kTerms; ++t)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint64_t da = operand(src + k * (kKMajor ? 32 : 4096), 1024, 16);
-                        const uint64_t db = operand(src + kOperand + t * S::kRowBytes + k * 32, 1024, 16);
-                        mma_f8(d, da, db, a.idesc[t], t + k > 0);
-                    }
-                commit(bar_empty + 8 * turn.slot);
-#if FP8Z1_CHECKED
-                if (g_stall & 2 && blockIdx.x + blockIdx.y == 0 && kb == k0) continue;
-#endif
-                commit(bar_acc + 8 * acc.slot);
+        const bool one = one_lane();
+        Turn<kStages> turn;
+        Turn<2> acc;
+        for (int kb = k0; kb < k1; ++kb, turn.next(), acc.next()) {
+            if (!bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1) || !bar_wait_warp(bar_full + 8 * turn.slot, turn.phase)) {
+                ok = false;
+                break;
             }
-            // every product issued ends, and its sums are read, before the tensor memory is freed
-            for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
+            fence_after();
+            if (!one) continue;
+            const uint32_t src = base + turn.slot * S::kStageBytes, d = tmem + acc.slot * kN;
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t da = operand(src + k * (kKMajor ? 32 : 4096), 1024, 16);
+                    const uint64_t db = operand(src + kOperand + t * S::kRowBytes + k * 32, 1024, 16);
+                    mma_f8(d, da, db, a.idesc[t], t + k > 0);
+                }
+            commit(bar_empty + 8 * turn.slot);
+#if FP8Z1_CHECKED
+            if (g_stall & 2 && blockIdx.x + blockIdx.y == 0 && kb == k0) continue;
+#endif
+            commit(bar_acc + 8 * acc.slot);
         }
+        // every product issued ends, and its sums are read, before the tensor memory is freed
+        for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
     } else if (warp < 4) {
         after_previous();
         Turn<4> turn;
@@ -589,6 +587,7 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
         else
             static_cast<bf16*>(o.y)[row * o.ld_y + col] = __float2bfloat16_rn(v);
     };
+    __syncwarp();
     if (a.splits > 1) {
         // every stage has been read: the last sums came after the last product
         if (warp >= 4)

@@ -66,8 +66,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
     const uint32_t bar_full = extra, bar_empty = extra + 48, bar_acc = extra + 96, bar_free = extra + 112;
     volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem_raw + (extra + 128 - smem_addr(smem_raw)));
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int sub = (int)cluster_rank();  // of the pair
+    const int warp = of_warp((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const int sub = blockIdx.x & 1;  // of the pair
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             bar_init(bar_full + 8 * i, 1);
@@ -90,22 +90,24 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
     cluster_sync();  // the other CTA counts on this one's barriers from here on
     fence_after();
     after_previous();
-    const uint32_t tmem = *tmem_at;
+    const uint32_t tmem = of_warp(*tmem_at);
     const int m_pairs = (a.m_tiles + 1) / 2;
     const int64_t total = (int64_t)m_pairs * a.n_tiles, i0 = blockIdx.x / 2, step = gridDim.x / 2;
     bool ok = true;
 
     if (warp < 4) {
         regs_less<48>();
-        if (warp == 0 && lane == 0) {
+        const bool one = one_lane();
+        if (warp == 0) {
             Turn<kStages> turn;
             for (int64_t i = i0; i < total && ok; i += step) {
                 const int n = (int)(i / m_pairs), m = (int)(i - (int64_t)n * m_pairs) * 2 + sub;
                 for (int t = 0; t < a.T; t += kStep, turn.next()) {
-                    if (!bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
+                    if (!bar_wait_warp(bar_empty + 8 * turn.slot, turn.phase ^ 1)) {
                         ok = false;
                         break;
                     }
+                    if (!one) continue;
                     // both CTAs' copies are counted in the first one, whose thread multiplies
                     if (sub == 0) bar_expect(bar_full + 8 * turn.slot, 2 * kStageBytes);
                     const uint32_t full = first_of_pair(bar_full + 8 * turn.slot), dst = base + turn.slot * kStageBytes;
@@ -118,8 +120,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
                 }
             }
             // the copies in flight are read before the CTA ends, whatever became of the other warps
-            for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait(bar_empty + 8 * turn.slot, turn.phase ^ 1);
-        } else if (warp == 1 && lane == 0 && sub == 0) {
+            for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait_warp(bar_empty + 8 * turn.slot, turn.phase ^ 1);
+        } else if (warp == 1 && sub == 0) {
             constexpr uint32_t format = kTerms == 2 ? 0 : 1;  // F16, BF16
             constexpr uint32_t idesc = instruction_of(256, kCols, true, true, format, format);
             Turn<kStages> turn;
@@ -127,13 +129,14 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
             for (int64_t i = i0; i < total && ok; i += step) {
                 for (int t0 = 0; t0 < a.T && ok; t0 += kTall, acc.next()) {
                     const uint32_t d = tmem + acc.slot * kCols;
-                    ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1);
+                    ok = bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1);
                     for (int s = 0; s < kAdd && t0 + s * kStep < a.T && ok; ++s, turn.next()) {
-                        if (!bar_wait(bar_full + 8 * turn.slot, turn.phase)) {
+                        if (!bar_wait_warp(bar_full + 8 * turn.slot, turn.phase)) {
                             ok = false;
                             break;
                         }
                         fence_after();
+                        if (!one) continue;
                         const uint32_t src = base + turn.slot * kStageBytes;
                         // 16 rows a product; rows past the end came as zeros
                         const int left = a.T - t0 - s * kStep, steps = left >= kStep ? 4 : (left + 15) / 16;
@@ -149,11 +152,11 @@ wgrad_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__
 #if FP8Z1_CHECKED
                     if (g_stall >> kTurned & 1 && blockIdx.x == 0 && i == i0 && t0 == 0) continue;
 #endif
-                    if (ok) commit_pair(bar_acc + 8 * acc.slot);
+                    if (ok && one) commit_pair(bar_acc + 8 * acc.slot);
                 }
             }
             // every product issued ends, and its sums are read, before the tensor memory is freed
-            for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
+            for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
         }
     } else {
         regs_more<104>();

@@ -98,6 +98,26 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+// One lane of a whole warp, and a value that its lanes share.  A warp that issues copies or products runs its
+// loop as a whole and lets one lane issue: what the instructions take is known to be the warp's then, and
+// goes to them as it is (from a loop of lane 0 alone a product's took some 50 clocks to issue, a step's end 400).
+__device__ __forceinline__ bool one_lane()
+{
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one != 0;
+}
+template <class T>
+__device__ __forceinline__ T of_warp(T v)
+{
+    return __shfl_sync(0xffffffffu, v, 0);
+}
+// A wait of a whole warp: the same outcome for its lanes.
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, bar_wait(bar, parity));
+}
+
 // The next of kSlots slots used in turn, and the parity of its use: a consumer
 // waits for `phase` of "full", a producer for `phase ^ 1` of "empty" (which a new
 // barrier has behind it).
