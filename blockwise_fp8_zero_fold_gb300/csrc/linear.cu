@@ -383,6 +383,7 @@ extern "C" int fp8z1_linear(const fp8z1_linear_dims* dims, const void* x, int64_
     o.vec_y = on16(y, ld_y, y_size);
     o.vec_r = on16(residual, ld_residual, 2);
     o.vec_pre = on16(pre, N, 4);
+    o.vec_bias = aligned(bias, 16);
     return launch_product(rows, Weight{codes, scales, d.R, d.C, d.k_major}, o, s);
 }
 

@@ -41,7 +41,7 @@ struct Out {
     int64_t ld_y;
     float* pre;            // z + bias, [T, N], or NULL
     bool f32;              // y's type
-    bool vec_y, vec_r, vec_pre;  // whole 16 bytes on 16-byte boundaries
+    bool vec_y, vec_r, vec_pre, vec_bias;  // whole 16 bytes on 16-byte boundaries
 };
 
 // z's factor in its activation, a sigmoid of c(z), by t = exp(-|c|) <= 1: nothing overflows.

@@ -53,104 +53,110 @@ struct Args {
 
 // ---- what becomes of the sums -----------------------------------------------------------
 
-// 16 neighbouring columns of a row a lane (a warp: 32 rows).  `rows`: how many of the warp's
-// rows exist, `row` and `n0` the lane's row and first column.
-__device__ __forceinline__ void finish(const Out& o, float (&v)[16], int64_t row, int lane, int rows, int64_t n0, uint8_t* stage)
+// 32 bytes of each of a warp's rows, a lane's own in w[2], through shared memory: two lanes store a row's, so that a
+// sector is written whole.
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, int rows, const uint4 (&w)[2], uint8_t* to, int64_t pitch)
 {
-    const bool here = lane < rows, whole = n0 + 16 <= o.N;
-    if (o.bias)
+    *reinterpret_cast<uint4*>(stage + lane * kStagePitch) = w[0];
+    *reinterpret_cast<uint4*>(stage + lane * kStagePitch + 16) = w[1];
+    __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (n0 + j < o.N) v[j] += __ldg(o.bias + n0 + j);
-    if (o.pre && here) {
-        float* p = o.pre + row * o.N + n0;
-        if (whole && o.vec_pre) {
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (n0 + j < o.N) p[j] = v[j];
-        }
-    }
-    if (o.act != FP8Z1_ACT_NONE)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = activate(v[j], o.act);
-    if (o.residual && here) {
-        const bf16* p = o.residual + row * o.ld_r + n0;
-        if (whole && o.vec_r) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 u = *reinterpret_cast<const uint4*>(p + 8 * h);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[8 * h + 2 * j] += __uint_as_float(w[j] << 16);
-                    v[8 * h + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (n0 + j < o.N) v[j] += to_float(p[j]);
-        }
-    }
-    if (!whole || !o.vec_y) {
-        if (!here) return;
-        if (o.f32) {
-            float* p = static_cast<float*>(o.y) + row * o.ld_y + n0;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (n0 + j < o.N) p[j] = v[j];
-        } else {
-            bf16* p = static_cast<bf16*>(o.y) + row * o.ld_y + n0;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (n0 + j < o.N) p[j] = __float2bfloat16_rn(v[j]);
-        }
-        return;
-    }
-    // 32 bytes of each row through shared memory: two lanes store a row's, a sector is written whole
-    const int64_t first = row - lane;
-    uint8_t* to;
-    int64_t pitch;
-    if (o.f32) {
-        to = reinterpret_cast<uint8_t*>(static_cast<float*>(o.y) + first * o.ld_y + n0);
-        pitch = o.ld_y * 4;
-    } else {
-        to = reinterpret_cast<uint8_t*>(static_cast<bf16*>(o.y) + first * o.ld_y + n0);
-        pitch = o.ld_y * 2;
-    }
+    for (int r = lane >> 1; r < 32; r += 16)
+        if (r < rows)
+            *reinterpret_cast<uint4*>(to + r * pitch + (lane & 1) * 16) =
+                *reinterpret_cast<const uint4*>(stage + r * kStagePitch + (lane & 1) * 16);
+    __syncwarp();
+}
+
+// 16 neighbouring columns of a row a lane (a warp: 32 rows, of which `rows` exist), from column n0 on; `first` the
+// warp's first row.  Eight at a time: the sums of the other columns wait in registers.
+__device__ __forceinline__ void finish(const Out& o, const uint64_t (&sums)[8], int64_t first, int lane, int rows, int64_t n0,
+                                       uint8_t* stage)
+{
+    const bool here = lane < rows, whole = n0 + 16 <= o.N, staged = whole && o.vec_y;
+    const int64_t row = first + lane;
+    uint4 w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        uint4 w[2];
-        if (o.f32) {
+        const int64_t c = n0 + 8 * h;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 two = unpair(sums[4 * h + j]);
+            v[2 * j] = two.x;
+            v[2 * j + 1] = two.y;
+        }
+        if (o.bias && whole && o.vec_bias) {
+            const float4 p = __ldg(reinterpret_cast<const float4*>(o.bias + c)), q = __ldg(reinterpret_cast<const float4*>(o.bias + c + 4));
+            v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w, v[4] += q.x, v[5] += q.y, v[6] += q.z, v[7] += q.w;
+        } else if (o.bias) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < o.N) v[j] += __ldg(o.bias + c + j);
+        }
+        if (o.pre && whole && o.vec_pre) {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                w[q] = make_uint4(__float_as_uint(v[8 * h + 4 * q]), __float_as_uint(v[8 * h + 4 * q + 1]),
-                                  __float_as_uint(v[8 * h + 4 * q + 2]), __float_as_uint(v[8 * h + 4 * q + 3]));
-        } else {
-            if (h) break;
+                w[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                                  __float_as_uint(v[4 * q + 3]));
+            store_rows(stage, lane, rows, w, reinterpret_cast<uint8_t*>(o.pre + first * o.N + c), o.N * 4);
+        } else if (o.pre && here) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t u[4];
+            for (int j = 0; j < 8; ++j)
+                if (c + j < o.N) o.pre[row * o.N + c + j] = v[j];
+        }
+        if (o.act != FP8Z1_ACT_NONE)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = activate(v[j], o.act);
+        if (o.residual && here) {
+            const bf16* p = o.residual + row * o.ld_r + c;
+            if (whole && o.vec_r) {
+                const uint4 u = *reinterpret_cast<const uint4*>(p);
+                const uint32_t r[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const __nv_bfloat162 two = __floats2bfloat162_rn(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]);
-                    u[j] = *reinterpret_cast<const uint32_t*>(&two);
+                    v[2 * j] += __uint_as_float(r[j] << 16);
+                    v[2 * j + 1] += __uint_as_float(r[j] & 0xffff0000u);
                 }
-                w[q] = make_uint4(u[0], u[1], u[2], u[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < o.N) v[j] += to_float(p[j]);
             }
         }
-        *reinterpret_cast<uint4*>(stage + lane * kStagePitch) = w[0];
-        *reinterpret_cast<uint4*>(stage + lane * kStagePitch + 16) = w[1];
-        __syncwarp();
+        if (!staged) {
+            if (here) {
 #pragma unroll
-        for (int r = lane >> 1; r < 32; r += 16)
-            if (r < rows)
-                *reinterpret_cast<uint4*>(to + r * pitch + 32 * h + (lane & 1) * 16) =
-                    *reinterpret_cast<const uint4*>(stage + r * kStagePitch + (lane & 1) * 16);
-        __syncwarp();
+                for (int j = 0; j < 8; ++j) {
+                    if (c + j >= o.N) break;
+                    if (o.f32)
+                        static_cast<float*>(o.y)[row * o.ld_y + c + j] = v[j];
+                    else
+                        static_cast<bf16*>(o.y)[row * o.ld_y + c + j] = __float2bfloat16_rn(v[j]);
+                }
+            }
+        } else if (o.f32) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                w[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                                  __float_as_uint(v[4 * q + 3]));
+            store_rows(stage, lane, rows, w, reinterpret_cast<uint8_t*>(static_cast<float*>(o.y) + first * o.ld_y + c), o.ld_y * 4);
+        } else {
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                u[j] = *reinterpret_cast<const uint32_t*>(&two);
+            }
+            // 16 bytes wait for the next
+            if (h == 0) {
+                *reinterpret_cast<uint4*>(stage + lane * kStagePitch + 32) = make_uint4(u[0], u[1], u[2], u[3]);
+            } else {
+                w[0] = *reinterpret_cast<const uint4*>(stage + lane * kStagePitch + 32);
+                w[1] = make_uint4(u[0], u[1], u[2], u[3]);
+                store_rows(stage, lane, rows, w, reinterpret_cast<uint8_t*>(static_cast<bf16*>(o.y) + first * o.ld_y + n0), o.ld_y * 2);
+            }
+        }
     }
 }
 
@@ -163,7 +169,7 @@ struct Many {
     static constexpr int kStages = kTerms == 2 ? 4 : 6;
     static constexpr uint32_t kStageBytes = (kTerms + 1) * kOperand;  // hi, lo, half of the weight's columns
     // stages, barriers, factors, rows on their way out
-    static constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 256 + 4096 + 16 * 32 * kStagePitch;
+    static constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 256 + 8192 + 16 * 32 * kStagePitch;
 };
 
 template <int kTerms, bool kKMajor>
@@ -177,10 +183,10 @@ many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
     next_may_start();
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     const uint32_t extra = base + kStages * kStageBytes;
-    // extra: full, empty [kStages], accumulators ready, free [2], factors ready, read [4], tensor memory base; factors
-    // [4][2][128]; rows on their way out
+    // extra: full, empty [kStages], accumulators ready, free [2], factors ready, read [2], tensor memory base; factors
+    // [2][4 steps][2][128]; rows on their way out
     const uint32_t bar_full = extra, bar_empty = extra + 48, bar_acc = extra + 96, bar_free = extra + 112,
-                   bar_factors = extra + 128, bar_read = extra + 160, factors = extra + 256;
+                   bar_factors = extra + 128, bar_read = extra + 144, factors = extra + 256;
     uint8_t* extra_ptr = smem_raw + (extra - smem_addr(smem_raw));
     volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(extra_ptr + 192);
 
@@ -195,8 +201,8 @@ many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             bar_init(bar_acc + 8 * i, 1);
             bar_init(bar_free + 8 * i, 32);  // the adding warps of both CTAs
         }
-        for (int i = 0; i < 4; ++i) {
-            bar_init(bar_factors + 8 * i, 64);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(bar_factors + 8 * i, 32);
             bar_init(bar_read + 8 * i, 16);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -243,60 +249,74 @@ many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
             }
             // the copies in flight are read before the CTA ends, whatever became of the other warps
             for (int j = 0; j < kStages; ++j, turn.next()) ok &= bar_wait_warp(bar_empty + 8 * turn.slot, turn.phase ^ 1);
-        } else if (warp == 1 && sub == 0) {
+        } else if (warp & 1 && sub == 0) {
+            // Two warps take the steps in turn, each with its accumulator: a step's barriers take one some 250 clocks,
+            // while the other's products run.  An even number of stages gives each warp stages of its own: one that the
+            // other has not seen filled would pass for filled again.
+            static_assert(kStages % 2 == 0, "stages of its own");
+            const int odd = warp >> 1;
             Turn<kStages> turn;
-            Turn<2> acc;
-            for (int64_t i = i0; i < total && ok; i += step) {
-                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next(), acc.next()) {
-                    if (!bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1) ||
-                        !bar_wait_warp(bar_full + 8 * turn.slot, turn.phase)) {
-                        ok = false;
-                        break;
-                    }
-                    fence_after();
-                    if (!one) continue;
-                    const uint32_t src = base + turn.slot * kStageBytes, d = tmem + acc.slot * kCols;
-#pragma unroll
-                    for (int t = 0; t < kTerms; ++t)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint64_t da = operand(src + t * kOperand + k * 32, 1024, 16);
-                            // K-major: 8 columns are 1024 bytes; N-major: 8 k are
-                            const uint64_t db = operand(src + kTerms * kOperand + k * (kKMajor ? 32 : 4096), 1024, 16);
-                            mma_f8_pair(d, da, db, a.idesc[t], t + k > 0);
-                        }
-                    commit_pair(bar_empty + 8 * turn.slot);
-#if FP8Z1_CHECKED
-                    if (g_stall & 1 && blockIdx.x == 0 && i == i0 && kb == 0) continue;
-#endif
-                    commit_pair(bar_acc + 8 * acc.slot);
+            if (odd) turn.next();
+            uint32_t phase = 0;
+            const int64_t count = (total > i0 ? (total - i0 + step - 1) / step : 0) * a.k_blocks;  // of all tiles
+            for (int64_t n = odd; n < count; n += 2, turn.next(), turn.next(), phase ^= 1) {
+                if (!bar_wait_warp(bar_full + 8 * turn.slot, turn.phase) || !bar_wait_warp(bar_free + 8 * odd, phase ^ 1)) {
+                    ok = false;
+                    break;
                 }
+                fence_after();
+                if (!one) continue;
+                const uint32_t src = base + turn.slot * kStageBytes, d = tmem + odd * kCols;
+#pragma unroll
+                for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t da = operand(src + t * kOperand + k * 32, 1024, 16);
+                        // K-major: 8 columns are 1024 bytes; N-major: 8 k are
+                        const uint64_t db = operand(src + kTerms * kOperand + k * (kKMajor ? 32 : 4096), 1024, 16);
+                        mma_f8_pair(d, da, db, a.idesc[t], t + k > 0);
+                    }
+                commit_pair(bar_empty + 8 * turn.slot);
+#if FP8Z1_CHECKED
+                if (g_stall & 1 && blockIdx.x == 0 && n == 0) continue;
+#endif
+                commit_pair(bar_acc + 8 * odd);
             }
             // every product issued ends, and its sums are read, before the tensor memory is freed
-            for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
-        } else if (warp >= 2) {
-            // the factors of each step, s_b c_bn of both chunks of 128 columns for two rows a thread
-            Turn<4> turn;
-            const int mine = threadIdx.x - 64;
+            ok = bar_wait_warp(bar_free + 8 * odd, phase ^ 1) && ok;
+        } else if (warp == 2) {
+            // the factors of four steps at a time, s_b c_bn of both chunks of 128 columns for four rows a thread
+            Turn<2> turn;
             for (int64_t i = i0; i < total && ok; i += step) {
                 const int n = (int)(i / a.m_tiles), m = (int)(i - (int64_t)n * a.m_tiles);
-                const int64_t row = (int64_t)m * 256 + sub * 128 + mine;  // rows and columns past the end: any others' scales
-                const float* pa = a.a_scale + min(row, a.o.T - 1) * a.scale_row;
-                const float* pb = a.a_scale + min(row + 64, a.o.T - 1) * a.scale_row;
+                const int64_t row = (int64_t)m * 256 + sub * 128 + lane;  // rows and columns past the end: any others' scales
+                const float* pa[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) pa[j] = a.a_scale + min(row + 32 * j, a.o.T - 1) * a.scale_row;
                 const float* p0 = a.b_scale + (int64_t)min(n * 2, a.b_cols - 1) * a.b_col;
                 const float* p1 = a.b_scale + (int64_t)min(n * 2 + 1, a.b_cols - 1) * a.b_col;
-                for (int kb = 0; kb < a.k_blocks; ++kb, turn.next()) {
-                    const float va = pa[kb * a.scale_block], vb = pb[kb * a.scale_block], v0 = p0[(int64_t)kb * a.b_step],
-                                v1 = p1[(int64_t)kb * a.b_step];
-                    if (!bar_wait(bar_read + 8 * turn.slot, turn.phase ^ 1)) {
+                for (int kb = 0; kb < a.k_blocks; kb += 4, turn.next()) {
+                    float v[4][4], c0[4], c1[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int64_t at = min(kb + k, a.k_blocks - 1);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[k][j] = pa[j][at * a.scale_block];
+                        c0[k] = p0[at * a.b_step];
+                        c1[k] = p1[at * a.b_step];
+                    }
+                    if (!bar_wait_warp(bar_read + 8 * turn.slot, turn.phase ^ 1)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t f = factors + turn.slot * 1024 + mine * 4;
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f), "f"(va * v0) : "memory");
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f + 256), "f"(vb * v0) : "memory");
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f + 512), "f"(va * v1) : "memory");
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(f + 768), "f"(vb * v1) : "memory");
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t f = factors + (turn.slot * 4 + k) * 1024 + (lane + 32 * j) * 4;
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(f), "f"(v[k][j] * c0[k]) : "memory");
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(f + 512), "f"(v[k][j] * c1[k]) : "memory");
+                        }
                     bar_arrive(bar_factors + 8 * turn.slot);
                 }
             }
@@ -305,65 +325,66 @@ many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
         regs_more<104>();
         const int group = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
-        uint8_t* stage = extra_ptr + 256 + 4096 + (warp - 4) * 32 * kStagePitch;
-        Turn<2> acc;
-        Turn<4> turn;
+        uint8_t* stage = extra_ptr + 256 + 8192 + (warp - 4) * 32 * kStagePitch;
+        const uint32_t bar_free_first = first_of_pair(bar_free);
+        Turn<2> acc, turn;
         for (int64_t i = i0; i < total; i += step) {
             const int n = (int)(i / a.m_tiles), m = (int)(i - (int64_t)n * a.m_tiles);
-            uint64_t sums2[2][16];  // pairs of columns
+            float sums[2][32];  // scalars: pairs for two additions an instruction cost the moves that made them (130 us for 120)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) sums2[c][j] = 0;
-            for (int kb = 0; kb < a.k_blocks; ++kb, acc.next(), turn.next()) {
+                for (int j = 0; j < 32; ++j) sums[c][j] = 0.0f;
+            bool ready = false;  // the step's sums are known to be there
+            for (int kb = 0; kb < a.k_blocks; ++kb) {
                 // a warp's lanes agree on the outcome: the loads below are warp-wide
-                ok = ok && __all_sync(0xffffffffu, bar_wait(bar_factors + 8 * turn.slot, turn.phase) &&
-                                                       bar_wait(bar_acc + 8 * acc.slot, acc.phase));
+                if ((kb & 3) == 0) ok = ok && bar_wait_warp(bar_factors + 8 * turn.slot, turn.phase);
+                const uint32_t at = factors + (turn.slot * 4 + (kb & 3)) * 1024 + row * 4;
+                float f[2];
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(at));
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[1]) : "r"(at + 512));
+                if (!ready) ok = ok && bar_wait_warp(bar_acc + 8 * acc.slot, acc.phase);
                 if (!ok) break;
                 fence_after();
-                float f0, f1;
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f0) : "r"(factors + turn.slot * 1024 + row * 4));
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f1) : "r"(factors + turn.slot * 1024 + 512 + row * 4));
-                const uint64_t f[2] = {pair(f0, f0), pair(f1, f1)};
-                const uint32_t t = tmem + acc.slot * kCols + lanes + group * 32;
-                // columns 32 group + {0, 16, 128, 144} ..
+                const uint32_t t = tmem + acc.slot * kCols + lanes + group * 32, free = bar_free_first + 8 * acc.slot;
+                acc.next();
+                bool next = false;
+                // columns 32 group + {0 .. 31, 128 .. 159}, 32 on their way at once
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t r[16];
-                    tmem_load(t + q / 2 * 128 + q % 2 * 16, r);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t r[32];
+                    tmem_load(t + c * 128, r);
                     tmem_wait(r);
-                    if (q == 3) {
+                    if (c) {
                         fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            bar_arrive_pair(first_of_pair(bar_free + 8 * acc.slot));
-                            bar_arrive(bar_read + 8 * turn.slot);
-                        }
+                        bar_arrive_pair_first(free, lane);
+                        // asked beside the additions: a wait takes some 130 clocks, and a step's chain is what bounds 8-bit rows
+                        next = bar_test(bar_acc + 8 * acc.slot, acc.phase);
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        sums2[q / 2][q % 2 * 8 + j] =
-                            fma_pair(pair(r[2 * j], r[2 * j + 1]), f[q / 2], sums2[q / 2][q % 2 * 8 + j]);
+                    for (int j = 0; j < 32; ++j) sums[c][j] = __fmaf_rn(__uint_as_float(r[j]), f[c], sums[c][j]);
+                }
+                ready = __all_sync(0xffffffffu, next);
+                if ((kb & 3) == 3 || kb + 1 == a.k_blocks) {
+                    if (lane == 0) bar_arrive(bar_read + 8 * turn.slot);
+                    turn.next();
                 }
             }
             // a wait ran out: this tile and the pair's further ones are NaN
             if (!ok)
 #pragma unroll
-                for (int j = 0; j < 32; ++j) sums2[j / 16][j % 16] = pair(NAN, NAN);
-            const int64_t at = (int64_t)m * 256 + sub * 128 + row;
-            const int rows = (int)min(max(a.o.T - (at - lane), (int64_t)0), (int64_t)32);
+                for (int j = 0; j < 64; ++j) sums[j / 32][j % 32] = NAN;
+            const int64_t first = (int64_t)m * 256 + sub * 128 + (warp & 3) * 32;  // row of the warp
+            const int rows = (int)min(max(a.o.T - first, (int64_t)0), (int64_t)32);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int64_t n0 = (int64_t)n * kCols + q / 2 * 128 + group * 32 + q % 2 * 16;
                 if (n0 >= a.o.N || rows == 0) continue;  // with the whole warp
-                float v[16];
+                uint64_t v[8];  // in pairs they need no registers of their own
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 two = unpair(sums2[q / 2][q % 2 * 8 + j]);
-                    v[2 * j] = two.x;
-                    v[2 * j + 1] = two.y;
-                }
-                finish(a.o, v, at, lane, rows, n0, stage);
+                for (int j = 0; j < 8; ++j) v[j] = pair(sums[q / 2][q % 2 * 16 + 2 * j], sums[q / 2][q % 2 * 16 + 2 * j + 1]);
+                finish(a.o, v, first, lane, rows, n0, stage);
             }
         }
     }
@@ -378,16 +399,16 @@ many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
 
 // ---- few rows ---------------------------------------------------------------------------------
 
-// kN rows of x; 4 warps feed, 4 or (from 64 rows) 8 add up.  Two CTAs share an SM up to 64 rows.
+// kN rows of x; 4 warps feed, 4 for each 32 rows add up.  Two CTAs share an SM up to 64 rows.
 template <int kTerms, int kN>
 struct Few {
-    static constexpr int kGroups = kN >= 64 ? 2 : 1, kMine = kN / kGroups;  // rows of an adding warp
+    static constexpr int kGroups = kN <= 32 ? 1 : kN / 32, kMine = kN / kGroups;  // rows of an adding warp
     static constexpr int kThreads = 128 + 128 * kGroups;
     static constexpr uint32_t kRowBytes = kN * 128;  // of a term
     static constexpr uint32_t kStageBytes = kOperand + kTerms * kRowBytes;
     static constexpr int kResident = kN <= 64 ? 2 : 1;
     static constexpr int kStages = kN <= 64 ? (int)(100 * 1024 / kStageBytes) : 4;
-    static constexpr uint32_t kAt = 256, kSmem = kStages * kStageBytes + 1024 + kAt + 4 * kN * 4;
+    static constexpr uint32_t kAt = 256, kSmem = kStages * kStageBytes + 1024 + kAt + 8 * kN * 4;
     static constexpr int kTmem = 2 * kN < 32 ? 32 : 2 * kN;
     static_assert(kStages >= 3 && kStages <= 6 && kStages * kStageBytes >= kN * 512, "the sums of a split fit the stages");
 };
@@ -403,10 +424,10 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
     next_may_start();
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
     const uint32_t extra = base + kStages * S::kStageBytes;
-    // extra: full, empty [kStages], accumulators ready, free [2], factors ready, read [4], tensor memory base, whether
-    // a wait ran out; factors [4][kN]
+    // extra: full, empty [kStages], accumulators ready, free [2], factors ready, read [2], tensor memory base, whether
+    // a wait ran out; factors [2][4 steps][kN]
     const uint32_t bar_full = extra, bar_empty = extra + 48, bar_acc = extra + 96, bar_free = extra + 112,
-                   bar_factors = extra + 128, bar_read = extra + 160, factors = extra + S::kAt;
+                   bar_factors = extra + 128, bar_read = extra + 144, factors = extra + S::kAt;
     uint8_t* extra_ptr = smem_raw + (extra - smem_addr(smem_raw));
     volatile uint32_t* tmem_at = reinterpret_cast<uint32_t*>(extra_ptr + 192);
     uint32_t* failed = reinterpret_cast<uint32_t*>(extra_ptr + 196);
@@ -427,8 +448,8 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
             bar_init(bar_acc + 8 * i, 1);
             bar_init(bar_free + 8 * i, 4 * S::kGroups);
         }
-        for (int i = 0; i < 4; ++i) {
-            bar_init(bar_factors + 8 * i, 64);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(bar_factors + 8 * i, 32);
             bar_init(bar_read + 8 * i, 4 * S::kGroups);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -478,7 +499,7 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
         Turn<kStages> turn;
         Turn<2> acc;
         for (int kb = k0; kb < k1; ++kb, turn.next(), acc.next()) {
-            if (!bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1) || !bar_wait_warp(bar_full + 8 * turn.slot, turn.phase)) {
+            if (!bar_wait_warp(bar_full + 8 * turn.slot, turn.phase) || !bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1)) {
                 ok = false;
                 break;
             }
@@ -501,29 +522,37 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
         }
         // every product issued ends, and its sums are read, before the tensor memory is freed
         for (int j = 0; j < 2; ++j, acc.next()) ok = bar_wait_warp(bar_free + 8 * acc.slot, acc.phase ^ 1) && ok;
-    } else if (warp < 4) {
+    } else if (warp == 2) {
         after_previous();
-        Turn<4> turn;
-        const int mine = threadIdx.x - 64;
-        constexpr int kEach = kN <= 64 ? 1 : 2;
+        // the factors of four steps at a time
+        Turn<2> turn;
+        constexpr int kEach = (kN + 31) / 32;
         const float* pb = a.b_scale + (int64_t)n * a.b_col;
-        for (int kb = k0; kb < k1; ++kb, turn.next()) {
-            const float c = pb[(int64_t)kb * a.b_step];
-            float v[kEach];
+        const float* pa[kEach];
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const int64_t row = min((int64_t)token0 + min(mine + 64 * i, kN - 1), a.o.T - 1);
-                v[i] = a.a_scale[row * a.scale_row + kb * a.scale_block];
+        for (int i = 0; i < kEach; ++i)
+            pa[i] = a.a_scale + min((int64_t)token0 + min(lane + 32 * i, kN - 1), a.o.T - 1) * a.scale_row;
+        for (int kb = k0; kb < k1; kb += 4, turn.next()) {
+            float c[4], v[4][kEach];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t at = min(kb + k, k1 - 1);
+                c[k] = pb[at * a.b_step];
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) v[k][i] = pa[i][at * a.scale_block];
             }
-            if (!bar_wait(bar_read + 8 * turn.slot, turn.phase ^ 1)) {
+            if (!bar_wait_warp(bar_read + 8 * turn.slot, turn.phase ^ 1)) {
                 ok = false;
                 break;
             }
 #pragma unroll
-            for (int i = 0; i < kEach; ++i)
-                if (mine + 64 * i < kN)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(factors + (turn.slot * kN + mine + 64 * i) * 4), "f"(v[i] * c)
-                                 : "memory");
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    if (lane + 32 * i < kN)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(factors + ((turn.slot * 4 + k) * kN + lane + 32 * i) * 4),
+                                     "f"(v[k][i] * c[k])
+                                     : "memory");
             bar_arrive(bar_factors + 8 * turn.slot);
         }
     }
@@ -531,39 +560,35 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
     float sums[S::kMine];
     if (warp >= 4) {
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
-        Turn<2> acc;
-        Turn<4> turn;
+        Turn<2> acc, turn;
 #pragma unroll
         for (int j = 0; j < S::kMine; ++j) sums[j] = 0.0f;
-        for (int kb = k0; kb < k1; ++kb, acc.next(), turn.next()) {
-            ok = ok && __all_sync(0xffffffffu, bar_wait(bar_factors + 8 * turn.slot, turn.phase) &&
-                                                   bar_wait(bar_acc + 8 * acc.slot, acc.phase));
+        for (int kb = k0; kb < k1; ++kb, acc.next()) {
+            const int k = (kb - k0) & 3;
+            if (k == 0) ok = ok && bar_wait_warp(bar_factors + 8 * turn.slot, turn.phase);
+            ok = ok && bar_wait_warp(bar_acc + 8 * acc.slot, acc.phase);
             if (!ok) break;
             fence_after();
-            const uint32_t t = tmem + acc.slot * kN + lanes + group * S::kMine;
-            const uint32_t f = factors + (turn.slot * kN + group * S::kMine) * 4;
-#pragma unroll
-            for (int q = 0; q < S::kMine / 16; ++q) {
-                uint32_t r[16];
-                tmem_load(t + q * 16, r);
-                tmem_wait(r);
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    float4 s;
-                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(s.x), "=f"(s.y), "=f"(s.z), "=f"(s.w)
-                                 : "r"(f + (q * 16 + j) * 4));
-                    sums[q * 16 + j] = __fmaf_rn(__uint_as_float(r[j]), s.x, sums[q * 16 + j]);
-                    sums[q * 16 + j + 1] = __fmaf_rn(__uint_as_float(r[j + 1]), s.y, sums[q * 16 + j + 1]);
-                    sums[q * 16 + j + 2] = __fmaf_rn(__uint_as_float(r[j + 2]), s.z, sums[q * 16 + j + 2]);
-                    sums[q * 16 + j + 3] = __fmaf_rn(__uint_as_float(r[j + 3]), s.w, sums[q * 16 + j + 3]);
-                }
-            }
+            const uint32_t f = factors + ((turn.slot * 4 + k) * kN + group * S::kMine) * 4;
+            uint32_t r[S::kMine];
+            tmem_load(tmem + acc.slot * kN + lanes + group * S::kMine, r);
+            tmem_wait(r);
             fence_before();
             __syncwarp();
-            if (lane == 0) {
-                bar_arrive(bar_free + 8 * acc.slot);
-                bar_arrive(bar_read + 8 * turn.slot);
+            if (lane == 0) bar_arrive(bar_free + 8 * acc.slot);
+#pragma unroll
+            for (int j = 0; j < S::kMine; j += 4) {
+                float4 s;
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(s.x), "=f"(s.y), "=f"(s.z), "=f"(s.w) : "r"(f + j * 4));
+                sums[j] = __fmaf_rn(__uint_as_float(r[j]), s.x, sums[j]);
+                sums[j + 1] = __fmaf_rn(__uint_as_float(r[j + 1]), s.y, sums[j + 1]);
+                sums[j + 2] = __fmaf_rn(__uint_as_float(r[j + 2]), s.z, sums[j + 2]);
+                sums[j + 3] = __fmaf_rn(__uint_as_float(r[j + 3]), s.w, sums[j + 3]);
+            }
+            if (k == 3 || kb + 1 == k1) {
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar_read + 8 * turn.slot);
+                turn.next();
             }
         }
     }
@@ -701,15 +726,25 @@ int launch_few(const Rows& x, const Weight& w, Args a, cudaStream_t s)
     return launch_status();
 }
 
+// Whether CTAs of 128 columns by 128 rows take less time than pairs with 256 x 256.  A step of K takes both about
+// as long, 0.7 us of BF16 rows and 0.48 of 8-bit ones, so the rounds of the SMs decide; a round's start and end are worth 4
+// and 6 steps.  Measured, us of few and many: 512 rows of 7168 x 4096 42 and 42, 256 29 and 41, 1001 82 and 46; 200 of
+// 4096 x 14336 59 and 30; 2051 of 4096 x 1024 31 and 32, x 2048 56 and 33.
+bool few_tiles(int64_t T, int64_t N, int64_t k_blocks)
+{
+    const int64_t tiles = ceil_div(T, 128) * ceil_div(N, 128);
+    const int n = splits_of(tiles, kSms, k_blocks);
+    return ceil_div(tiles * n, kSms) * (ceil_div(k_blocks, n) + 4) <
+           ceil_div(ceil_div(T, 256) * ceil_div(N, 256), kSms / 2) * (k_blocks + 6);
+}
+
 template <int kTerms, bool kKMajor>
 int launch(const Rows& x, const Weight& w, const Args& a, cudaStream_t s)
 {
     if (x.T <= 16) return launch_few<kTerms, 16, kKMajor>(x, w, a, s);
     if (x.T <= 32) return launch_few<kTerms, 32, kKMajor>(x, w, a, s);
     if (x.T <= 64) return launch_few<kTerms, 64, kKMajor>(x, w, a, s);
-    // 128 columns by 128 rows a CTA while that leaves no SM twice as much to do as pairs of 256 x 256 would
-    const int64_t few = ceil_div(x.T, 128) * ceil_div(a.o.N, 128);
-    if (x.T <= 128 || few <= 2 * kSms) return launch_few<kTerms, 128, kKMajor>(x, w, a, s);
+    if (x.T <= 128 || few_tiles(x.T, a.o.N, a.k_blocks)) return launch_few<kTerms, 128, kKMajor>(x, w, a, s);
     return launch_many<kTerms, kKMajor>(x, w, a, s);
 }
 

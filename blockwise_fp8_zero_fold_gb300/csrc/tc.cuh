@@ -43,6 +43,17 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
+// Whether a phase is over, without a wait.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ uint64_t now_ns()
 {
     uint64_t t;
@@ -85,6 +96,14 @@ __device__ __forceinline__ uint32_t first_of_pair(uint32_t a)
 __device__ __forceinline__ void bar_arrive_pair(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same by a warp's first lane, without a branch.
+__device__ __forceinline__ void bar_arrive_pair_first(uint32_t bar, int lane)
+{
+    asm volatile(
+        "{ .reg .pred p; setp.eq.s32 p, %1, 0; @p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0]; }" ::"r"(bar),
+        "r"(lane)
+        : "memory");
 }
 // Every thread of the cluster's CTAs.
 __device__ __forceinline__ void cluster_sync()
@@ -261,6 +280,13 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t group_stride
            (uint64_t)(group_stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// M/N-major with runs of 64 bytes in the 64-byte swizzle (atoms of 8 rows x 64 bytes), one run wide.
+__device__ __forceinline__ uint64_t operand_64(uint32_t addr, uint32_t group_stride)
+{
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(group_stride >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)4 << 61;
+}
+
 // Instruction descriptor of m rows x n columns: FP32 sums, operand formats E4M3
 // (f8f6f4) or F16 (f16), both encoded 0, the first operand E5M2 instead with
 // `a_e5m2`; `mn_major` bits say which operands are M/N-major.
@@ -316,6 +342,26 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// 32 columns.
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 template <int kRegs>
