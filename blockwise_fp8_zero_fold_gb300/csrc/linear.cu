@@ -4,6 +4,8 @@
 // Forward:  pairs of BF16 rows (8-bit rows go as they are), product.
 // Backward: dz = dy act'(z) to pairs, its columns' sums; dx, a product with the weight turned;
 //           d_weight, of dy and x as they lie when dz is dy in BF16, else of FP16 terms.
+#include <cooperative_groups.h>
+
 #include <mutex>
 
 #include "linear.cuh"
@@ -12,6 +14,7 @@ namespace fp8z1 {
 namespace linear {
 namespace {
 
+namespace cg = cooperative_groups;
 using ffn::after_previous;
 using ffn::ColumnScale;
 using ffn::Cut;
@@ -107,20 +110,27 @@ struct DzArgs {
     Backward b;  // what is not wanted is NULL
 };
 
-// dz of 256 rows x 128 columns, a warp 8 rows and a lane 4 columns of each, in registers
+// dz of 128 rows x 128 columns, a warp 8 rows and a lane 4 columns of each, in registers
 // from its one read on: pairs for dx (a row's 128 share a scale), FP16 terms for d_weight
-// (a column's 256 do), the columns' sums.  The terms: a column's largest number is brought to
-// 2^14, so that columns of small numbers keep their 22 bits beside large ones.
+// (a column's 256 do: two CTAs tell each other their largest), the columns' sums.  The terms: a
+// column's largest number is brought to 2^14, so that columns of small numbers keep their 22
+// bits beside large ones.  (256 rows by 1024 threads, one CTA an SM, loaded and stored by turns: XX.)
+constexpr int kDzRows = kTall / 2;
 template <class D, bool kAct, bool kTerms>
-__global__ void __launch_bounds__(1024) dz_kernel(const DzArgs a)
+__global__ void __launch_bounds__(512, 2) dz_kernel(const DzArgs a)
 {
     constexpr bool kExact = !kTerms;  // BF16 values
-    __shared__ uint32_t peaks[128];
-    __shared__ float sums[32][128];
+    __shared__ uint32_t peaks[2][128];  // of this CTA's rows, of the other's
+    __shared__ float sums[16][128];
     next_may_start();
+    cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t r0 = (int64_t)blockIdx.x * kTall + warp * 8, c = (int64_t)blockIdx.y * 128 + lane * 4;
-    if (kTerms && threadIdx.x < 128) peaks[threadIdx.x] = 0;
+    const int64_t r0 = (int64_t)blockIdx.x * kDzRows + warp * 8, c = (int64_t)blockIdx.y * 128 + lane * 4;
+    const bool terms = kTerms && a.b.dz_hi;
+    if (terms) {
+        if (threadIdx.x < 128) peaks[0][threadIdx.x] = 0;
+        cluster.barrier_arrive();  // this CTA has started: the other may write to it
+    }
     float v[8][4];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
@@ -157,46 +167,48 @@ __global__ void __launch_bounds__(1024) dz_kernel(const DzArgs a)
             for (int j = 0; j < 4; ++j) s[j] += v[r][j];
         *reinterpret_cast<float4*>(&sums[warp][lane * 4]) = make_float4(s[0], s[1], s[2], s[3]);
     }
-    if (kTerms) {
+    if (terms) {
+        __syncwarp();
+        cluster.barrier_wait();
+        uint32_t p[4] = {};
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = max(p[j], abs_bits(v[r][j]));
         __syncthreads();
-        if (a.b.dz_hi) {
-            uint32_t p[4] = {};
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) p[j] = max(p[j], abs_bits(v[r][j]));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) atomicMax(&peaks[lane * 4 + j], p[j]);  // the order leaves the largest as it is
-        }
+        for (int j = 0; j < 4; ++j) atomicMax(&peaks[0][lane * 4 + j], p[j]);  // the order leaves the largest as it is
     }
     __syncthreads();
+    if (terms && threadIdx.x < 128) cluster.map_shared_rank(&peaks[1][0], (int)cluster.block_rank() ^ 1)[threadIdx.x] = peaks[0][threadIdx.x];
     if (a.b.part && threadIdx.x < 128) {
         float s = 0.0f;
-#pragma unroll 8
-        for (int w = 0; w < 32; ++w) s += sums[w][threadIdx.x];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) s += sums[w][threadIdx.x];
         const int64_t col = (int64_t)blockIdx.y * 128 + threadIdx.x;
         if (col < a.N) a.b.part[(int64_t)blockIdx.x * a.N + col] = s;
     }
-    if (kTerms && a.b.dz_hi) {
-        float up[4], down[4];
+    if (!terms) return;
+    __syncwarp();
+    cluster.sync();
+    float up[4], down[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const ColumnScale s = ffn::column_scale(peaks[lane * 4 + j] >> 23);
-            up[j] = s.up, down[j] = s.down;
-        }
-        if (warp == 0)
-            *reinterpret_cast<float4*>(a.b.dz_factor + (int64_t)blockIdx.x * a.Np + c) = make_float4(down[0], down[1], down[2], down[3]);
+    for (int j = 0; j < 4; ++j) {
+        const ColumnScale s = ffn::column_scale(max(peaks[0][lane * 4 + j], peaks[1][lane * 4 + j]) >> 23);
+        up[j] = s.up, down[j] = s.down;
+    }
+    if (warp == 0 && !(blockIdx.x & 1))
+        *reinterpret_cast<float4*>(a.b.dz_factor + (int64_t)(blockIdx.x >> 1) * a.Np + c) = make_float4(down[0], down[1], down[2], down[3]);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            if (r0 + r >= a.T) break;
-            const int64_t at = (r0 + r) * a.Np + c;
-            const float f0 = v[r][0] * up[0], f1 = v[r][1] * up[1], f2 = v[r][2] * up[2], f3 = v[r][3] * up[3];
-            const __half2 h0 = __floats2half2_rn(f0, f1), h1 = __floats2half2_rn(f2, f3);
-            const float2 g0 = __half22float2(h0), g1 = __half22float2(h1);
-            *reinterpret_cast<uint2*>(a.b.dz_hi + at) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-            *reinterpret_cast<uint2*>(a.b.dz_lo + at) = make_uint2(half_pair(f0 - g0.x, f1 - g0.y), half_pair(f2 - g1.x, f3 - g1.y));
-        }
+    for (int r = 0; r < 8; ++r) {
+        if (r0 + r >= a.T) break;
+        const int64_t at = (r0 + r) * a.Np + c;
+        const float f0 = v[r][0] * up[0], f1 = v[r][1] * up[1], f2 = v[r][2] * up[2], f3 = v[r][3] * up[3];
+        const __half2 h0 = __floats2half2_rn(f0, f1), h1 = __floats2half2_rn(f2, f3);
+        const float2 g0 = __half22float2(h0), g1 = __half22float2(h1);
+        *reinterpret_cast<uint2*>(a.b.dz_hi + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+        *reinterpret_cast<uint2*>(a.b.dz_lo + at) = make_uint2(half_pair(f0 - g0.x, f1 - g0.y), half_pair(f2 - g1.x, f3 - g1.y));
     }
 }
 
@@ -278,7 +290,7 @@ void cut(Backward& b, Cut& c, const Dims& d)
     b.hi = c.take<uint8_t>(d.T * Np);
     b.lo = c.take<uint8_t>(d.T * Np);
     b.scale = c.take<float>(d.T * (Np / 128));
-    b.part = c.take<float>(tall * d.N());
+    b.part = c.take<float>(2 * tall * d.N());
     if (d.exact()) {
         b.x_copy = c.take<bf16>(d.T * Kp);
         b.dy_copy = c.take<bf16>(d.T * Np);
@@ -300,6 +312,27 @@ int check(const fp8z1_linear_dims* p, Dims& d)
         return FP8Z1_EINVAL;
     d = Dims{p->tokens, p->rows, p->cols, p->transposed == 1, p->activation, p->x_type, p->y_type};
     return FP8Z1_OK;
+}
+
+// The first kernel of its pass, in clusters of two.
+int launch_dz(void (*kernel)(DzArgs), dim3 grid, cudaStream_t s, const DzArgs& a)
+{
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at[1] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.gridDim = grid;
+    c.blockDim = dim3(512);
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    count_launch();
+    if (cudaLaunchKernelEx(&c, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return FP8Z1_ECUDA;
+    }
+    return launch_status();
 }
 
 bool on16(const void* p, int64_t ld, int size) { return aligned(p, 16) && ld * size % 16 == 0; }
@@ -415,7 +448,7 @@ extern "C" int fp8z1_linear_grad(const fp8z1_linear_dims* dims, const void* dy, 
     Backward b;
     Cut c(workspace);
     cut(b, c, d);
-    const dim3 tiles((unsigned)ceil_div(d.T, kTall), (unsigned)(d.Np() / 128));
+    const dim3 tall((unsigned)ceil_div(d.T, kTall), (unsigned)(d.Kp() / 128));
     DzArgs z = {};
     z.dy = dy;
     z.pre = pre;
@@ -431,14 +464,14 @@ extern "C" int fp8z1_linear_grad(const fp8z1_linear_dims* dims, const void* dy, 
     if (!d_bias) z.b.part = nullptr;
     if (!d_weight) z.b.dz_hi = z.b.dz_lo = nullptr;
     if (dx || d_bias || !d.exact()) {
-        count_launch();
+        const dim3 tiles(2 * tall.x, (unsigned)(d.Np() / 128));
         if (d.exact())
-            dz_kernel<bf16, false, false><<<tiles, 1024, 0, s>>>(z);
+            st = launch_dz(dz_kernel<bf16, false, false>, tiles, s, z);
         else if (d.y_type == FP8Z1_F32)
-            d.act ? dz_kernel<float, true, true><<<tiles, 1024, 0, s>>>(z) : dz_kernel<float, false, true><<<tiles, 1024, 0, s>>>(z);
+            st = d.act ? launch_dz(dz_kernel<float, true, true>, tiles, s, z) : launch_dz(dz_kernel<float, false, true>, tiles, s, z);
         else
-            dz_kernel<bf16, true, true><<<tiles, 1024, 0, s>>>(z);
-        if ((st = launch_status()) != FP8Z1_OK) return st;
+            st = launch_dz(dz_kernel<bf16, true, true>, tiles, s, z);
+        if (st != FP8Z1_OK) return st;
     }
     if (dx) {
         Rows rows = {};
@@ -488,13 +521,13 @@ extern "C" int fp8z1_linear_grad(const fp8z1_linear_dims* dims, const void* dy, 
                 g.dz = b.dy_copy;
                 g.ld_dz = d.Np();
             }
-        } else if ((st = ffn::launch_after(x16_kernel, dim3(tiles.x, (unsigned)(d.Kp() / 128)), 1024, 0, s, xb, ld_x, d.T, K,
+        } else if ((st = ffn::launch_after(x16_kernel, tall, 1024, 0, s, xb, ld_x, d.T, K,
                                            d.Kp(), aligned(x, 8) && ld_x % 4 == 0, b.x16, b.x_factor)) != FP8Z1_OK) {
             return st;
         }
         if ((st = launch_wgrad(g, s)) != FP8Z1_OK) return st;
     }
-    return d_bias ? launch_column_sum(b.part, (int)tiles.x, N, d_bias, s) : FP8Z1_OK;
+    return d_bias ? launch_column_sum(b.part, 2 * (int)tall.x, N, d_bias, s) : FP8Z1_OK;
 }
 
 extern "C" int fp8z1_linear_timeouts(uint32_t* count)

@@ -68,6 +68,21 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, int rows, c
     __syncwarp();
 }
 
+// 8 columns of each of a warp's rows, a lane's own in v, to rows of any alignment (of `cols` columns from here on):
+// eight lanes store a row's, so that an instruction touches a few sectors, not 32.
+template <class T>
+__device__ __forceinline__ void store_any(uint8_t* stage, int lane, int rows, const float (&v)[8], T* to, int64_t ld, int64_t cols)
+{
+    *reinterpret_cast<float4*>(stage + lane * kStagePitch) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(stage + lane * kStagePitch + 16) = make_float4(v[4], v[5], v[6], v[7]);
+    __syncwarp();
+    const int c = lane & 7;
+#pragma unroll
+    for (int r = lane >> 3; r < 32; r += 4)
+        if (r < rows && c < cols) to[r * ld + c] = from_float<T>(*reinterpret_cast<const float*>(stage + r * kStagePitch + c * 4));
+    __syncwarp();
+}
+
 // 16 neighbouring columns of a row a lane (a warp: 32 rows, of which `rows` exist), from column n0 on; `first` the
 // warp's first row.  Eight at a time: the sums of the other columns wait in registers.
 __device__ __forceinline__ void finish(const Out& o, const uint64_t (&sums)[8], int64_t first, int lane, int rows, int64_t n0,
@@ -100,10 +115,8 @@ __device__ __forceinline__ void finish(const Out& o, const uint64_t (&sums)[8], 
                 w[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
                                   __float_as_uint(v[4 * q + 3]));
             store_rows(stage, lane, rows, w, reinterpret_cast<uint8_t*>(o.pre + first * o.N + c), o.N * 4);
-        } else if (o.pre && here) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < o.N) o.pre[row * o.N + c + j] = v[j];
+        } else if (o.pre) {
+            store_any(stage, lane, rows, v, o.pre + first * o.N + c, o.N, o.N - c);
         }
         if (o.act != FP8Z1_ACT_NONE)
 #pragma unroll
@@ -125,16 +138,10 @@ __device__ __forceinline__ void finish(const Out& o, const uint64_t (&sums)[8], 
             }
         }
         if (!staged) {
-            if (here) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (c + j >= o.N) break;
-                    if (o.f32)
-                        static_cast<float*>(o.y)[row * o.ld_y + c + j] = v[j];
-                    else
-                        static_cast<bf16*>(o.y)[row * o.ld_y + c + j] = __float2bfloat16_rn(v[j]);
-                }
-            }
+            if (o.f32)
+                store_any(stage, lane, rows, v, static_cast<float*>(o.y) + first * o.ld_y + c, o.ld_y, o.N - c);
+            else
+                store_any(stage, lane, rows, v, static_cast<bf16*>(o.y) + first * o.ld_y + c, o.ld_y, o.N - c);
         } else if (o.f32) {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
