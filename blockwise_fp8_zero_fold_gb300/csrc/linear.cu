@@ -132,20 +132,40 @@ __global__ void __launch_bounds__(512, 2) dz_kernel(const DzArgs a)
         cluster.barrier_arrive();  // this CTA has started: the other may write to it
     }
     float v[8][4];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[r][j] = 0.0f;
-        if (r0 + r < a.T) load_some(static_cast<const D*>(a.dy) + (r0 + r) * a.ld, c, a.N, a.vec_dy, v[r]);
-    }
-    if (kAct)
+    if (kAct && sizeof(D) == 2 && a.vec_dy && a.vec_pre) {
+        // dy waits in its own 16 bits, so that the registers hold all rows' loads at once
+        uint2 d[8];
+        const bool in = c < a.N;  // rows of whole fours
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            float z[4] = {};
-            if (r0 + r < a.T) load_some(a.pre + (r0 + r) * a.N, c, a.N, a.vec_pre, z);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[r][j] *= slope(z[j], a.act);
+            const bool here = in && r0 + r < a.T;
+            d[r] = here ? __ldg(reinterpret_cast<const uint2*>(static_cast<const bf16*>(a.dy) + (r0 + r) * a.ld + c)) : make_uint2(0, 0);
+            const float4 z = here ? __ldg(reinterpret_cast<const float4*>(a.pre + (r0 + r) * a.N + c)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v[r][0] = z.x, v[r][1] = z.y, v[r][2] = z.z, v[r][3] = z.w;
         }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            v[r][0] = __uint_as_float(d[r].x << 16) * slope(v[r][0], a.act);
+            v[r][1] = __uint_as_float(d[r].x & 0xffff0000u) * slope(v[r][1], a.act);
+            v[r][2] = __uint_as_float(d[r].y << 16) * slope(v[r][2], a.act);
+            v[r][3] = __uint_as_float(d[r].y & 0xffff0000u) * slope(v[r][3], a.act);
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[r][j] = 0.0f;
+            if (r0 + r < a.T) load_some(static_cast<const D*>(a.dy) + (r0 + r) * a.ld, c, a.N, a.vec_dy, v[r]);
+        }
+        if (kAct)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                float z[4] = {};
+                if (r0 + r < a.T) load_some(a.pre + (r0 + r) * a.N, c, a.N, a.vec_pre, z);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[r][j] *= slope(z[j], a.act);
+            }
+    }
     if (a.b.hi)
 #pragma unroll
         for (int r = 0; r < 8; ++r) {

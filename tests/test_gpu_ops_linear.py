@@ -109,6 +109,19 @@ def test_larger_products(tokens, rows, cols, transposed, x):
     forward(s, transposed, None, False, True, F32)
 
 
+@pytest.mark.parametrize("x", ["bf16", "fp8"])
+@pytest.mark.parametrize("tokens", [257, 300, 320])
+def test_rows_beyond_whole_tiles(tokens, x):
+    """A few rows past 256 over many columns: those rows' result is the others' kind, in every form."""
+    for transposed in (False, True):
+        s = make(tokens, *((19712, 256) if transposed else (256, 19712)), transposed, tokens, x)
+        for pad, dtype in ((0, BF16), (3, F32)):
+            out = M.strided(torch.zeros(tokens, 19712, dtype=dtype, device="cuda"), pad)
+            y, pre = forward(s, transposed, "silu", True, True, dtype, save=True, out=out)
+            again, pre2 = forward(s, transposed, "silu", True, True, dtype, save=True)
+            assert torch.equal(y, again) and torch.equal(pre, pre2)
+
+
 @pytest.mark.parametrize("tokens", [3, 90, 800])
 @pytest.mark.parametrize("pad,at", [(8, 0), (1, 0), (0, 1), (5, 3)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
