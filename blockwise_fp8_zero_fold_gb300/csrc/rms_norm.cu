@@ -539,7 +539,8 @@ constexpr int kWarpDim = 1024;  // up to here a warp has a row
 // Threads of a CTA's row with so many elements each.
 int threads_of(int64_t dim, int each) { return (int)ceil_div(dim, each * 32) * 32; }
 // The gradient's ring: a CTA an SM of at most 16 warps, for 128 registers a thread; as many elements a thread as
-// they hold of three inputs and the weight's sums (groups of 28 warps at 8 elements took 120 us for XX).
+// they hold of three inputs and the weight's sums (groups of 28 warps at 8
+// elements took 120 us for 8192 rows of 7168, two of 14 at 16 with spilled registers 189, this 90).
 constexpr int kRingSmem = 224 * 1024;
 int ring_each(int64_t dim, int size) { return size == 2 || dim > 7680 ? 32 : 16; }
 int ring_groups(int64_t dim, int size) { return std::min(kMostGroups, std::max(1, 480 / threads_of(dim, ring_each(dim, size)))); }
@@ -641,7 +642,7 @@ extern "C" int fp8z1_rms_norm(int64_t rows, int64_t dim, const void* x, int32_t 
     if (st != FP8Z1_OK) return st;
     if (rows == 0) return FP8Z1_OK;
     if (!x || !weight || (!y && !codes) || !codes != !scales || !residual != !total || ld_x < dim ||
-        (residual && (ld_r < dim || ld_total < dim)) || (y && ld_y < dim))
+        (residual && (ld_r < dim || ld_total < dim)) || (y && (ld_y < dim || y == total)))
         return FP8Z1_EINVAL;
     const int size = type == FP8Z1_F32 ? 4 : 2;
     if (!aligned(x, size) || !aligned(residual, size) || !aligned(total, size) || !aligned(y, size) ||
@@ -654,10 +655,12 @@ extern "C" int fp8z1_rms_norm(int64_t rows, int64_t dim, const void* x, int32_t 
                     codes, scales, (int)ceil_div(dim, 128)};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     count_launch();
-    if (dim <= 256 || (dim <= kWarpDim && rows > 8 * kSms)) return by_shape<8, 32>(type, vec, dim <= 256 ? 8 : 32, WarpRows{a, s});
-    // a row a CTA: few rows at 8 elements a thread, many at 32 (registers for eight CTAs' rows an SM)
-    const int each = dim <= 8192 && rows <= 4 * kSms ? 8 : 32;
-    return by_shape<8, 32>(type, vec, each, CtaRows{a, threads_of(dim, each), s});
+    if (dim <= 256) return by_shape<8, 8>(type, vec, 8, WarpRows{a, s});
+    // 8 elements a thread while the SMs hold all rows' threads at once, 32 beyond: us at 7168 columns, BF16 to 8 bits, 304
+    // rows 4.7 (5.3 with 32), 608 7.8 (6.2), 4864 53 (42); at 1024 columns 2432 rows 4.7 (4.8), 4864 7.7 (6.5)
+    if (dim <= 8192 && rows * threads_of(dim, 8) <= 2048 * kSms) return by_shape<8, 8>(type, vec, 8, CtaRows{a, threads_of(dim, 8), s});
+    if (dim <= kWarpDim) return by_shape<32, 32>(type, vec, 32, WarpRows{a, s});
+    return by_shape<32, 32>(type, vec, 32, CtaRows{a, threads_of(dim, 32), s});
 }
 
 extern "C" int fp8z1_rms_norm_grad_workspace(int64_t rows, int64_t dim, int64_t* bytes)

@@ -168,17 +168,18 @@ int fp8z1_distill(const void* logits, int32_t type, int64_t ld, int64_t rows, in
  *   s = x + residual, rounded to `type` and written to `total` (without a residual s = x),
  *   y = s * (mean_j s_j^2 + eps)^-1/2 * weight,
  * y rounded once: to `type` in `y`, and to E4M3 in `codes` ([rows, dim], dense) with a
- * scale for every 128 columns in `scales` ([rows, ceil(dim / 128)], dense): max |y| / 448 of
- * the 128, 1 where that is 0; a value is its code times its scale.  `y` or `codes` may be
- * NULL (codes and scales together), not both.
+ * scale for every 128 columns in `scales` ([rows, ceil(dim / 128)], dense): c = max |y| / 448 of
+ * the 128, codes those of y times 1 / c in FP32; a value is its code times its scale.  128 numbers
+ * below 2^-117 are 0, with a scale of 1.  `y` or `codes` may be NULL (codes and scales together),
+ * not both.
  * x, residual, total, y: `type`, rows of `dim` elements, ld >= dim apart; total and y may be
- * x or residual themselves.  weight: FP32 [dim].  Any alignment of the element types;
+ * x or residual themselves, not each other.  weight: FP32 [dim].  Any alignment of the element types;
  * dim and strides of whole 16 bytes on 16-byte boundaries are moved 8 elements at a time.
  * No row is too large: squares beyond FP32 are summed scaled down.  An infinity or NaN
  * leaves its row without finite numbers (but 0 where a finite element meets an infinity's norm).
  * rows == 0 enqueues nothing.
  * Errors: EINVAL (null, rows < 0 or > 2^30, dim outside 1 .. 16384, type, strides, eps outside
- * 1e-20 .. 1e20, residual without total or total without residual), EALIGN, ECUDA. */
+ * 1e-20 .. 1e20, residual without total or total without residual, y == total), EALIGN, ECUDA. */
 int fp8z1_rms_norm(int64_t rows, int64_t dim, const void* x, int32_t type, int64_t ld_x, const void* residual,
                    int64_t ld_r, const float* weight, float eps, void* total, int64_t ld_total, void* y, int64_t ld_y,
                    uint8_t* codes, float* scales, void* stream);

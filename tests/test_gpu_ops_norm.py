@@ -171,12 +171,15 @@ def test_ends_of_the_range(dim):
 
 
 def test_tiny_results_in_8_bits():
-    """A group whose largest / 448 is no FP32 number has a scale of 1 and codes of 0."""
-    x = torch.ones(2, 256, device="cuda")
-    w = torch.full((256,), 1e-44, device="cuda")
-    w[128:] = 1.0
-    codes, scale = ops.rms_norm_fp8(x, w)
-    assert (scale[:, 0] == 1).all() and not codes[:, :128].float().any() and (codes[:, 128:].float() == 448).all()
+    """128 numbers below 2^-117 are 0, with a scale of 1; from there on they are held."""
+    x = torch.ones(2, 384, device="cuda")
+    w = torch.ones(384, device="cuda")
+    for tiny in (1e-44, 1e-38, 2.0**-117.1):
+        w[:128], w[256:] = tiny, 2.0**-116.9
+        codes, scale = ops.rms_norm_fp8(x, w)
+        assert (scale[:, 0] == 1).all() and not codes[:, :128].float().any() and (codes[:, 128:].float() == 448).all()
+        y = M.norm(x, w, EPS)["y"][:, 256:]
+        assert ((scale[:, 2:].double() * 448 - y).abs() <= 2.0**-21 * y).all()
 
 
 @pytest.mark.parametrize("shape", [(0, 64), (2, 0, 64), (2, 3, 64), (64,)])

@@ -28,7 +28,7 @@ def status(name, args):
     return getattr(F.lib(), name)(*args.values())
 
 
-NORM = dict(rows=2, dim=64, x=P, type=F.BF16, ld_x=64, r=P, ld_r=64, w=P, eps=1e-6, total=P, ld_t=64, y=P, ld_y=64, codes=P,
+NORM = dict(rows=2, dim=64, x=P, type=F.BF16, ld_x=64, r=P, ld_r=64, w=P, eps=1e-6, total=P, ld_t=64, y=P + 1024, ld_y=64, codes=P,
             scales=P, stream=None)
 
 
@@ -40,7 +40,7 @@ NORM = dict(rows=2, dim=64, x=P, type=F.BF16, ld_x=64, r=P, ld_r=64, w=P, eps=1e
     (dict(y=None, codes=None, scales=None), F.EINVAL), (dict(eps=0.0), F.EINVAL), (dict(eps=-1.0), F.EINVAL),
     (dict(eps=NAN), F.EINVAL), (dict(eps=INF), F.EINVAL), (dict(eps=1e-30), F.EINVAL), (dict(x=P + 1), F.EALIGN),
     (dict(r=P + 1), F.EALIGN), (dict(total=P + 1), F.EALIGN), (dict(y=P + 1), F.EALIGN), (dict(w=P + 2), F.EALIGN),
-    (dict(scales=P + 2), F.EALIGN), (dict(type=F.F32, x=P + 2), F.EALIGN),
+    (dict(scales=P + 2), F.EALIGN), (dict(type=F.F32, x=P + 2), F.EALIGN), (dict(y=P), F.EINVAL),  # y over the sum
     (dict(rows=0, x=None, w=None, r=None, total=None, y=None, codes=None, scales=None), F.OK)])
 def test_norm_refusals(change, want):
     assert status("fp8z1_rms_norm", {**NORM, **change}) == want
