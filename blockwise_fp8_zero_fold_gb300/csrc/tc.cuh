@@ -280,13 +280,6 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t group_stride
            (uint64_t)(group_stride >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// M/N-major with runs of 64 bytes in the 64-byte swizzle (atoms of 8 rows x 64 bytes), one run wide.
-__device__ __forceinline__ uint64_t operand_64(uint32_t addr, uint32_t group_stride)
-{
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(group_stride >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)4 << 61;
-}
-
 // Instruction descriptor of m rows x n columns: FP32 sums, operand formats E4M3
 // (f8f6f4) or F16 (f16), both encoded 0, the first operand E5M2 instead with
 // `a_e5m2`; `mn_major` bits say which operands are M/N-major.
