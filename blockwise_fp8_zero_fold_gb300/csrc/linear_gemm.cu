@@ -448,8 +448,9 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
     cg::cluster_group cluster = cg::this_cluster();
 
     const int warp = of_warp((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const int n = blockIdx.x / a.splits, split = blockIdx.x - n * a.splits;
-    const int token0 = blockIdx.y * kN;
+    // the rows' tiles outermost, in one dimension of the grid: another holds 65535
+    const int tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits, m = tile / a.n_tiles, n = tile - m * a.n_tiles;
+    const int token0 = m * kN;
     const int k0 = a.k_blocks * split / a.splits, k1 = a.k_blocks * (split + 1) / a.splits;
     if (threadIdx.x == 0) {
         *failed = 0;
@@ -529,7 +530,7 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
                 }
             commit(bar_empty + 8 * turn.slot);
 #if FP8Z1_CHECKED
-            if (g_stall & 2 && blockIdx.x + blockIdx.y == 0 && kb == k0) continue;
+            if (g_stall & 2 && blockIdx.x == 0 && kb == k0) continue;
 #endif
             commit(bar_acc + 8 * acc.slot);
         }
@@ -725,7 +726,7 @@ int launch_few(const Rows& x, const Weight& w, Args a, cudaStream_t s)
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
-    c.gridDim = dim3((unsigned)(a.n_tiles * a.splits), (unsigned)a.m_tiles);
+    c.gridDim = dim3((unsigned)((int64_t)a.n_tiles * a.splits * a.m_tiles));  // below 2^31: more than 128 columns take it for few rows alone
     c.blockDim = dim3(S::kThreads);
     c.dynamicSmemBytes = S::kSmem;
     c.stream = s;

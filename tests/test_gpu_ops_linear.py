@@ -301,6 +301,30 @@ def test_infinities_in_the_gradients():
         assert torch.equal(dw[k][:, n], want[1][k][:, n]) and torch.equal(db[n], want[2][n])
 
 
+def test_more_tiles_of_rows_than_a_grid_has_in_its_second_dimension():
+    """65537 tiles of 128 rows through a narrow weight, offsets past 2^31; all gradients."""
+    tokens, rows, cols = 65536 * 128 + 77, 272, 16
+    s = make(1, rows, cols, False, 5)
+    g = M.gen(6)
+    x = torch.randn((tokens, rows), generator=g, device="cuda", dtype=BF16)
+    dy = torch.randn((tokens, cols), generator=g, device="cuda", dtype=BF16)
+    y = ops.linear(x, s["codes"], s["scale"])
+    dx, dw, db = ops.linear_grad(dy, x, s["codes"], s["scale"], bias=True)
+    edges = [0, 65535 * 128, 2**31 // 384, 2**31 // rows, tokens - 300]
+    want_w, want_b = torch.zeros((rows, cols), dtype=torch.float64, device="cuda"), 0.0
+    for i in range(0, tokens, 1 << 19):
+        d = dy[i:i + (1 << 19)].double()
+        want_w += x[i:i + (1 << 19)].double().T @ d
+        want_b = want_b + d.sum(0)
+    for i in edges:
+        at = slice(max(i - 200, 0), i + 300)
+        v, d = x[at].double(), dy[at].double()
+        check(y[at], v @ s["w"], v.abs() @ s["w"].abs(), BF16)
+        check(dx[at], d @ s["w"].T, d.abs() @ s["w"].T.abs(), BF16)
+    # 32769 additions of 256 rows' sums round by 2^-24 of the sum so far, of either sign: 181 * 2^-24 = 1.1e-5 of the norm
+    assert rel(dw, want_w) <= 2e-5 and rel(db, want_b) <= 2e-5
+
+
 @pytest.mark.parametrize("transposed", [False, True])
 def test_no_tokens(transposed):
     s = make(0, 64, 32, transposed, 1)
