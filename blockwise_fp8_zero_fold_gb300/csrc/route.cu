@@ -509,6 +509,7 @@ extern "C" int fp8z1_dispatch(int64_t tokens, int64_t top, int64_t experts, int6
     if (!x || !offsets || !place || !rows || ld_x < dim || ld_rows < dim) return FP8Z1_EINVAL;
     const int64_t size = type == FP8Z1_F32 ? 4 : 2, bytes = dim * size;
     if (!aligned(x, size) || !aligned(rows, size) || !aligned(offsets, 4) || !aligned(place, 4)) return FP8Z1_EALIGN;
+    if (rows == x) return FP8Z1_EINVAL;  // tokens read what others have written
     NvtxRange range("fp8z1_dispatch");
     RowArgs a = {};
     a.tokens = tokens;
@@ -539,6 +540,7 @@ extern "C" int fp8z1_combine(int64_t tokens, int64_t top, int64_t dim, const voi
     const int64_t size = type == FP8Z1_F32 ? 4 : 2;
     if (!aligned(rows, size) || !aligned(residual, size) || !aligned(y, size) || !aligned(place, 4) || !aligned(weight, 4))
         return FP8Z1_EALIGN;
+    if (y == rows) return FP8Z1_EINVAL;  // tokens read what others have written
     NvtxRange range("fp8z1_combine");
     RowArgs a = {};
     a.tokens = tokens;
@@ -574,6 +576,7 @@ extern "C" int fp8z1_combine_grad(int64_t tokens, int64_t top, int64_t experts, 
     if (!aligned(dy, size) || !aligned(rows, size) || !aligned(d_rows, size) || !aligned(offsets, 4) || !aligned(place, 4) ||
         !aligned(weight, 4) || !aligned(d_weight, 4))
         return FP8Z1_EALIGN;
+    if (d_rows == dy) return FP8Z1_EINVAL;  // tokens read what others have written
     NvtxRange range("fp8z1_combine_grad");
     RowArgs a = {};
     a.tokens = tokens;

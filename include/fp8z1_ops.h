@@ -214,14 +214,15 @@ int fp8z1_route(const void* ids, int32_t id_bytes, int64_t tokens, int64_t top, 
 
 /* rows[place[t, j]] = x[t], bit for bit; rows from offsets[experts] to tokens * top are
  * cleared.  x: [tokens, dim], rows: [tokens * top, dim], both `type`.  tokens == 0 enqueues
- * nothing.  Errors: EINVAL (as fp8z1_route, dim outside 1 .. 2^23, type, strides), EALIGN, ECUDA. */
+ * nothing.  Errors: EINVAL (as fp8z1_route, dim outside 1 .. 2^23, type, strides, rows == x), EALIGN,
+ * ECUDA. */
 int fp8z1_dispatch(int64_t tokens, int64_t top, int64_t experts, int64_t dim, const void* x, int32_t type, int64_t ld_x,
                    const int32_t* offsets, const int32_t* place, void* rows, int64_t ld_rows, void* stream);
 
 /* y[t] = residual[t] + sum_j weight[t, j] * rows[place[t, j]] over the choices that have a
  * row, in FP32 in the order of j, the residual last, rounded once to `type`.  weight: FP32
  * [tokens, top], NULL for 1 (which is fp8z1_dispatch's gradient); residual NULL: none; y may
- * be residual itself.  Errors: as fp8z1_dispatch. */
+ * be residual itself, not rows (EINVAL).  Errors: as fp8z1_dispatch. */
 int fp8z1_combine(int64_t tokens, int64_t top, int64_t dim, const void* rows, int32_t type, int64_t ld_rows,
                   const int32_t* place, const float* weight, const void* residual, int64_t ld_residual, void* y,
                   int64_t ld_y, void* stream);
@@ -229,7 +230,7 @@ int fp8z1_combine(int64_t tokens, int64_t top, int64_t dim, const void* rows, in
 /* The gradients of sum(dy * y) of fp8z1_combine:
  *   d_rows[place[t, j]] = weight[t, j] * dy[t]  (rows from offsets[experts] on are cleared),
  *   d_weight[t, j] = sum over the columns of dy[t] * rows[place[t, j]], FP32, 0 without a row.
- * The residual's is dy.  Results repeat bit for bit.  Errors: as fp8z1_dispatch. */
+ * The residual's is dy.  Results repeat bit for bit.  Errors: as fp8z1_dispatch (d_rows == dy). */
 int fp8z1_combine_grad(int64_t tokens, int64_t top, int64_t experts, int64_t dim, const void* dy, int32_t type,
                        int64_t ld_dy, const void* rows, int64_t ld_rows, const int32_t* offsets, const int32_t* place,
                        const float* weight, void* d_rows, int64_t ld_d, float* d_weight, void* stream);

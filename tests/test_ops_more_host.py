@@ -114,6 +114,13 @@ def test_combine_grad_refusals(change, want):
     assert status("fp8z1_combine_grad", {**CGRAD, **change}) == want
 
 
+@pytest.mark.parametrize("name,args,out,given", [("fp8z1_dispatch", DISPATCH, "rows", "x"), ("fp8z1_combine", COMBINE, "y", "rows"),
+                                                 ("fp8z1_combine_grad", CGRAD, "d", "dy")])
+def test_rows_go_to_rows_of_their_own(name, args, out, given):
+    """Tokens would read what others have written, were the result its own input."""
+    assert args[out] == args[given] and status(name, args) == F.EINVAL
+
+
 DIMS = dict(tokens=4, rows=64, cols=32, transposed=0, activation=F.ACT_NONE, x_type=F.BF16, y_type=F.BF16)
 
 
