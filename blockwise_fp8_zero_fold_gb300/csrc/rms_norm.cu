@@ -14,7 +14,7 @@
 //
 // With rows of 7168 BF16: 16384 with a residual to 8 bits 133 us, 6.2 TB/s; 8192 forward 66 us, 7.1 TB/s,
 // their gradient 90 us, 5.2 TB/s, and 4 us for the columns' sums.  32 rows 3 us from a captured graph.  2003 rows of
-// 4097 FP32, single elements and no bulk copies: 14 and 35 us, the gradient at 2.8 TB/s, bound by its instructions.
+// 4097 FP32, single elements: 15 and 26 us, the gradient at 3.8 TB/s, bound by its instructions.
 #include <algorithm>
 
 #include "ops_common.cuh"
@@ -103,19 +103,26 @@ template <int kE, bool kVec, bool kStaged, class T>
 __device__ __forceinline__ void hold(Held<T, kE>& v, const T* p, const T* here, int lo, int hi, int dim, int tid, int threads)
 {
 #pragma unroll
-    for (int j = 0; j < kE; j += kVec ? 8 : 1) {
+    for (int j = 0; j < kE; j += kVec ? 8 : 4) {
         const int c = column<kVec>(j, tid, threads);
         if constexpr (kVec) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v.set(j + i, from_float<T>(0.0f));
             if (c < dim) v.set8(j, (kStaged ? here : p) + c);
+        } else if (kStaged && (c & ~31) >= lo && (c | 31) + 96 < hi) {  // the warp's 128
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v.set(j + i, here[c + 32 * i]);
         } else {
-            T e = from_float<T>(0.0f);
-            if (kStaged && c >= lo && c < hi)
-                e = here[c];
-            else if (c < dim)
-                e = p[c];
-            v.set(j, e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = c + 32 * i;
+                T e = from_float<T>(0.0f);
+                if (kStaged && d >= lo && d < hi)
+                    e = here[d];
+                else if (d < dim)
+                    e = p[d];
+                v.set(j + i, e);
+            }
         }
     }
 }
@@ -130,6 +137,9 @@ __device__ __forceinline__ void load_piece(const T* p, int c, int dim, float (&v
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.0f;
         if (c < dim) load8(p + c, v);
+    } else if ((c | 31) + 96 < dim) {  // the warp's 128
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = to_float(p[c + 32 * i]);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = c + 32 * i < dim ? to_float(p[c + 32 * i]) : 0.0f;
@@ -140,6 +150,9 @@ __device__ __forceinline__ void store_piece(T* p, int c, int dim, const float (&
 {
     if constexpr (kVec) {
         if (c < dim) store8(p + c, v);
+    } else if ((c | 31) + 96 < dim) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[c + 32 * i] = from_float<T>(v[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -421,8 +434,8 @@ __device__ __forceinline__ void take(Held<T, kE>& v, const Ring& r, const void* 
         hold<kE, kVec, false, T>(v, p, nullptr, 0, 0, dim, tid, r.threads);
 }
 
-template <class T, int kE, bool kVec>
-__global__ void __launch_bounds__(512, 1) norm_grad_ring_kernel(const GradArgs a, const Ring r)
+template <class T, int kE, bool kVec, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1) norm_grad_ring_kernel(const GradArgs a, const Ring r)
 {
     extern __shared__ __align__(128) uint8_t smem[];  // full, empty [kMostStages], the weight, stages
     __shared__ float2 part[kMostGroups][3][32];
@@ -542,16 +555,23 @@ constexpr int kWarpDim = 1024;  // up to here a warp has a row
 
 // Threads of a CTA's row with so many elements each.
 int threads_of(int64_t dim, int each) { return (int)ceil_div(dim, each * 32) * 32; }
-// The gradient's ring: a CTA an SM of at most 16 warps, for 128 registers a thread; as many elements a thread as
-// they hold of three inputs and the weight's sums (groups of 28 warps at 8
-// elements took 120 us for 8192 rows of 7168, two of 14 at 16 with spilled registers 189, this 90).
+// The gradient's ring: a CTA an SM, of 15 warps and the one that copies, for 128 registers a thread; as many elements a
+// thread as they hold of three inputs and the weight's sums (groups of 28 warps at 8 elements took 120 us for 8192 rows
+// of 7168 BF16, two of 14 at 16 with spilled registers 189, this 90).  Single elements 16, as 32 spill: 8192 rows of 7169
+// BF16 329 us, at 16 147.  19 warps and 96 registers where they hold two rows and 15 one: 2003 rows of 4097 FP32 33 us
+// for 38, 8192 of BF16 83 for 132; of other widths they spill (7169 FP32 187 for 128) or gain nothing.
 constexpr int kRingSmem = 224 * 1024;
-int ring_each(int64_t dim, int size) { return size == 2 || dim > 7680 ? 32 : 16; }
-int ring_groups(int64_t dim, int size) { return std::min(kMostGroups, std::max(1, 480 / threads_of(dim, ring_each(dim, size)))); }
-int shape_ring(Ring& r, int64_t dim, int size)  // bytes of shared memory
+int ring_each(int64_t dim, int size, bool vec) { return dim > 7680 || (size == 2 && vec) ? 32 : 16; }
+int ring_groups(int64_t dim, int each)
 {
-    r.threads = threads_of(dim, ring_each(dim, size));
-    r.groups = ring_groups(dim, size);
+    const int threads = threads_of(dim, each);
+    if (each == 16 && 480 / threads == 1 && 608 / threads == 2) return 2;
+    return std::min(kMostGroups, std::max(1, 480 / threads));
+}
+int shape_ring(Ring& r, int64_t dim, int size, int each)  // bytes of shared memory
+{
+    r.threads = threads_of(dim, each);
+    r.groups = ring_groups(dim, each);
     r.pitch = (int)ceil_div(dim * size + 16, 16) * 16;
     const int fixed = 128 + (int)ceil_div(dim, 4) * 16, stage = r.n * r.pitch;
     r.stages = std::min(kMostStages, (kRingSmem - fixed - 6144) / stage);
@@ -608,12 +628,19 @@ struct GradRingRows {
     int smem;
     unsigned ctas;
     cudaStream_t s;
+    template <class T, int kE, bool kVec, int kThreads>
+    int launch() const
+    {
+        if (!allow_smem<norm_grad_ring_kernel<T, kE, kVec, kThreads>>(kRingSmem - 6144)) return FP8Z1_ECUDA;
+        norm_grad_ring_kernel<T, kE, kVec, kThreads><<<ctas, r.groups * r.threads + (r.stages ? 32 : 0), smem, s>>>(a, r);
+        return launch_status();
+    }
     template <class T, int kE, bool kVec>
     int run() const
     {
-        if (!allow_smem<norm_grad_ring_kernel<T, kE, kVec>>(kRingSmem - 6144)) return FP8Z1_ECUDA;
-        norm_grad_ring_kernel<T, kE, kVec><<<ctas, r.groups * r.threads + (r.stages ? 32 : 0), smem, s>>>(a, r);
-        return launch_status();
+        if constexpr (kE == 16 && kVec && sizeof(T) == 2) return FP8Z1_EINVAL;  // 32 of these
+        else if constexpr (kE == 16) return r.groups * r.threads > 480 ? launch<T, kE, kVec, 640>() : launch<T, kE, kVec, 512>();
+        else return launch<T, kE, kVec, 512>();
     }
 };
 
@@ -623,7 +650,7 @@ int64_t grad_ctas(int64_t rows, int64_t dim)
     if (dim <= kWarpDim) return std::max<int64_t>(1, std::min<int64_t>(2 * kSms, ceil_div(rows, 8)));
     return std::max<int64_t>(1, std::min<int64_t>(kSms, rows));
 }
-int64_t grad_parts(int64_t rows, int64_t dim) { return grad_ctas(rows, dim) * (dim <= kWarpDim ? 1 : std::max(ring_groups(dim, 2), ring_groups(dim, 4))); }
+int64_t grad_parts(int64_t rows, int64_t dim) { return grad_ctas(rows, dim) * (dim <= kWarpDim ? 1 : std::max(ring_groups(dim, 16), ring_groups(dim, 32))); }
 
 }  // namespace
 
@@ -711,9 +738,9 @@ extern "C" int fp8z1_rms_norm_grad(int64_t rows, int64_t dim, const void* dy, in
         r.in[2] = d_total;
         r.ld[2] = ld_dt;
         r.n = d_total ? 3 : 2;
-        const int smem = shape_ring(r, dim, size);
+        const int each = ring_each(dim, size, vec), smem = shape_ring(r, dim, size, each);
         parts *= r.groups;
-        st = by_shape<16, 32>(type, vec, ring_each(dim, size), GradRingRows{a, r, smem, ctas, s});
+        st = by_shape<16, 32>(type, vec, each, GradRingRows{a, r, smem, ctas, s});
     }
     if (st != FP8Z1_OK) return st;
     return launch_column_sum(a.part, parts, dim, d_weight, s);

@@ -86,6 +86,14 @@ def test_gradient(rows, dim, dtype):
         assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,dim", [(1000, 3840), (1000, 3841), (901, 4096), (1201, 4097), (700, 4863), (700, 4864), (700, 4865),
+                                      (640, 7169), (900, 7680), (610, 7681)])
+def test_gradient_of_widths_that_take_other_threads(rows, dim, dtype):
+    """One row of a CTA under way or two, and widths on both sides."""
+    test_gradient(rows, dim, dtype)
+
+
 def test_gradient_against_differences():
     x, _, w, dy, _ = make(3, 200, F32, 5)
     dx, dw = ops.rms_norm_grad(dy, x, w, eps=EPS)
