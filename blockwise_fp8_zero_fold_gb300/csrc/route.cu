@@ -11,8 +11,8 @@
 // Sums are FP32 in the order of j (over columns: of the threads), without atomics.
 // All four are bound by the rows moved: a token's row is read once for all its choices.
 //
-// 8192 tokens of 7168 BF16, 8 of 32 experts each: dispatch 156 us, 6.8 TB/s; combine 196 us, 5.4 TB/s of rows that lie
-// apart (6.0 with a residual); its gradient 318 us, 6.3 TB/s; the sort of 65536 choices 11 us.  61 tokens: 5, 4 and 4 us.
+// 8192 tokens of 7168 BF16, 8 of 32 experts each: dispatch 156 us, 6.8 TB/s; combine 158 us, 6.7 TB/s, with a
+// residual 180, 6.5; its gradient 300 us, 6.7 TB/s; the sort of 65536 choices 11 us.  61 tokens: 5, 4 and 4 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -312,9 +312,12 @@ __device__ __forceinline__ void load_rows(Piece<T, kVec> (&v)[kMany], const Choi
     for (int j = 0; j < kMany; ++j) v[j].load(rows + (int64_t)max(choices.row[j0 + j], 0) * ld, left);
 }
 
-// Parts of a token's columns are neighbouring CTAs'.
-template <class T, bool kVec>
-__global__ void __launch_bounds__(256) combine_kernel(const RowArgs a, int parts)
+// Parts of a token's columns are neighbouring CTAs'.  A CTA waits for its choices, then for their rows: what its registers
+// leave to other CTAs pays.  us with a residual, 8192 tokens: BF16, eight rows on their way and 4 CTAs an SM, 8 choices of
+// 7168 180 (3 CTAs 193, 5 198); fewer choices four rows and 6, 2 of 5120 59 (63 with 4, 84 with eight rows).  FP32 8 CTAs, 2
+// of 5120 100 (104 to 118 with four rows and 5 or 8).
+template <class T, bool kVec, int kMost>
+__global__ void __launch_bounds__(256, !kVec ? 4 : sizeof(T) == 4 ? 8 : kMost == 8 ? 4 : 6) combine_kernel(const RowArgs a, int parts)
 {
     using P = Piece<T, kVec>;
     __shared__ Choices choices;
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a, int parts
         float sum[P::kN] = {};
         P add;
         if (a.x) add.load(static_cast<const T*>(a.x) + t * a.ld_x + c, left);
-        by_parts<kVec ? 8 : 4>(a.top, [&](auto how_many, int j0) {
+        by_parts<kMost>(a.top, [&](auto how_many, int j0) {
             constexpr int many = decltype(how_many)::value;
             P v[many];
             load_rows(v, choices, j0, rows, a.ld_rows, left);
@@ -351,9 +354,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const RowArgs a, int parts
     }
 }
 
-// A CTA a token.
-template <class T, bool kVec>
-__global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a)
+// A CTA a token.  As above: BF16, 8192 tokens, 8 choices of 7168 300 us with 3 CTAs an SM (2: 326, 4: 318), 2 of 5120
+// 87 with four rows and 5 (96 with 4, 115 with eight rows and 3).
+template <class T, bool kVec, int kMost>
+__global__ void __launch_bounds__(256, !kVec ? 4 : kMost == 8 ? 3 : 5) combine_grad_kernel(const RowArgs a)
 {
     using P = Piece<T, kVec>;
     __shared__ float sums[8][8];
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const RowArgs a)
     load_choices(choices, a, t);
     const T* dy = static_cast<const T*>(a.y) + t * a.ld_y;
     T* out = static_cast<T*>(a.out);
-    by_parts<kVec ? 8 : 4>(a.top, [&](auto how_many, int j0) {
+    by_parts<kMost>(a.top, [&](auto how_many, int j0) {
         constexpr int many = decltype(how_many)::value;
         float dot[many];
 #pragma unroll
@@ -420,7 +424,12 @@ int check(int64_t tokens, int64_t top, int64_t experts, int64_t dim, int32_t typ
     return check(tokens, top, experts);
 }
 
-unsigned threads_for(int64_t vectors) { return (unsigned)std::min<int64_t>(256, std::max<int64_t>(1, ceil_div(vectors, 32)) * 32); }
+// As many as go round a row's vectors evenly, at most 256.
+unsigned threads_for(int64_t vectors)
+{
+    const int64_t rounds = std::max<int64_t>(1, ceil_div(vectors, 256));
+    return (unsigned)(std::max<int64_t>(1, ceil_div(vectors, rounds * 32)) * 32);
+}
 
 template <class V>
 int launch_dispatch(RowArgs a, int64_t bytes, int64_t size, cudaStream_t s)
@@ -434,7 +443,7 @@ int launch_dispatch(RowArgs a, int64_t bytes, int64_t size, cudaStream_t s)
     return launch_status();
 }
 
-template <class T, bool kVec>
+template <class T, bool kVec, int kMost>
 int launch_combine(const RowArgs& a, cudaStream_t s)
 {
     constexpr int kN = Piece<T, kVec>::kN;
@@ -443,16 +452,28 @@ int launch_combine(const RowArgs& a, cudaStream_t s)
     const int64_t most = ceil_div(a.cols, (int64_t)threads * kN);
     const int parts = (int)std::max<int64_t>(1, std::min(most, 4 * kSms / a.tokens));
     count_launch();
-    combine_kernel<T, kVec><<<(unsigned)(a.tokens * parts), threads, 0, s>>>(a, parts);
+    combine_kernel<T, kVec, kVec && sizeof(T) == 4 ? 8 : kMost><<<(unsigned)(a.tokens * parts), threads, 0, s>>>(a, parts);
     return launch_status();
 }
 
-template <class T, bool kVec>
+template <class T, bool kVec, int kMost>
 int launch_combine_grad(const RowArgs& a, cudaStream_t s)
 {
     count_launch();
-    combine_grad_kernel<T, kVec><<<(unsigned)a.tokens, threads_for(ceil_div(a.cols, Piece<T, kVec>::kN)), 0, s>>>(a);
+    combine_grad_kernel<T, kVec, kMost><<<(unsigned)a.tokens, threads_for(ceil_div(a.cols, Piece<T, kVec>::kN)), 0, s>>>(a);
     return launch_status();
+}
+
+// Calls f for a call's type, pieces and rows on their way at once.
+template <class F>
+int by_type(int32_t type, bool vec, int64_t top, F f)
+{
+    const auto of = [&](auto t) {
+        using B = std::bool_constant<true>;
+        if (!vec) return f(t, std::bool_constant<false>(), std::integral_constant<int, 4>());
+        return top >= 8 ? f(t, B(), std::integral_constant<int, 8>()) : f(t, B(), std::integral_constant<int, 4>());
+    };
+    return type == FP8Z1_F32 ? of(float()) : of(bf16());
 }
 
 bool fits(const void* p, int64_t ld, int64_t size, int64_t bytes) { return !p || (aligned(p, bytes) && ld * size % bytes == 0); }
@@ -558,8 +579,7 @@ extern "C" int fp8z1_combine(int64_t tokens, int64_t top, int64_t dim, const voi
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = dim * size % 16 == 0 && fits(rows, ld_rows, size, 16) && fits(residual, ld_residual, size, 16) &&
                      fits(y, ld_y, size, 16);
-    if (type == FP8Z1_F32) return vec ? launch_combine<float, true>(a, s) : launch_combine<float, false>(a, s);
-    return vec ? launch_combine<bf16, true>(a, s) : launch_combine<bf16, false>(a, s);
+    return by_type(type, vec, top, [&](auto t, auto v, auto n) { return launch_combine<decltype(t), v(), n()>(a, s); });
 }
 
 extern "C" int fp8z1_combine_grad(int64_t tokens, int64_t top, int64_t experts, int64_t dim, const void* dy, int32_t type,
@@ -597,6 +617,5 @@ extern "C" int fp8z1_combine_grad(int64_t tokens, int64_t top, int64_t experts, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool vec = dim * size % 16 == 0 && fits(dy, ld_dy, size, 16) && fits(rows, ld_rows, size, 16) &&
                      fits(d_rows, ld_d, size, 16);
-    if (type == FP8Z1_F32) return vec ? launch_combine_grad<float, true>(a, s) : launch_combine_grad<float, false>(a, s);
-    return vec ? launch_combine_grad<bf16, true>(a, s) : launch_combine_grad<bf16, false>(a, s);
+    return by_type(type, vec, top, [&](auto t, auto v, auto n) { return launch_combine_grad<decltype(t), v(), n()>(a, s); });
 }
