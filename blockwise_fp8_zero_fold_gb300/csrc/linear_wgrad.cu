@@ -16,7 +16,7 @@
 // the gradient's norm) and then scaled and added in registers.
 //
 // 2051 rows to 4096 x 14336 of FP32 dz: 303 us, 1.6 PFLOP/s of FP16 products; the tensor cores are busy 89 % of
-// the time at 2048 rows and 7168 x 4096, 76 % with BF16 rows, whose half as many products share the same ends of tiles.
+// the time at 2048 rows and 7168 x 4096, 75 % with BF16 rows, whose half as many products share the same ends of tiles.
 #include "linear.cuh"
 
 namespace fp8z1 {
