@@ -75,8 +75,8 @@ struct Backward {
     float* dz_factor;      // [T / 256, Np]
     __half* x16;           // [T, Kp]
     float* x_factor;       // [T / 256, Kp / 128]
-    float* part;           // [T / 256, N] sums of dz's columns
-    bf16 *x_copy, *dy_copy;  // [T, rounded up to 8 columns]: where theirs do not lie on 16 bytes
+    float* part;           // [T / 128, N] sums of dz's columns
+    bf16 *x_copy, *dy_copy;  // [T, Kp], [T, Np]: where theirs do not lie on 16 bytes
 };
 
 // ---- launches (each returns a status) --------------------------------------------

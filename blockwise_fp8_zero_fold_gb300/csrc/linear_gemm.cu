@@ -18,9 +18,9 @@
 // the columns': the products' time follows the rows, and the codes are what is read.  K is
 // split over a cluster's CTAs, whose sums are added in shared memory in their order.
 //
-// Many rows: 4096 8-bit rows of 7168 x 4096 take 125 us, 1.9 PFLOP/s, 8192 212 us, 2.3 PFLOP/s; without the additions
-// 92 us, so they and the way from product to additions and back bound it, and 256 tiles are 3.4 rounds of 76 pairs.  2051
-// BF16 rows of 4096 x 14336 179 us, 1.35 PFLOP/s (a ninth of the tiles' rows is padding), with GELU and the saved z 214: the
+// Many rows: 4096 8-bit rows of 7168 x 4096 take 118 us, 2.0 PFLOP/s, 8192 205 us, 2.3 PFLOP/s: the additions and the
+// way from product to additions and back bound it, and 256 tiles are 3.4 rounds of 76 pairs.  2051
+// BF16 rows of 4096 x 14336 168 us, 1.4 PFLOP/s (a ninth of the tiles' rows is padding), with GELU and the saved z 206: the
 // end of a tile, which nothing overlaps.  Few rows, in a captured graph with cold caches: 1 8-bit row of 4096 x 14336 14 us,
 // 61 BF16 rows of 7168 x 4096 16: the first codes' way and the split's join, not the codes' rate.
 #include <cooperative_groups.h>
@@ -173,6 +173,131 @@ __device__ __forceinline__ void finish(const Out& o, const uint64_t (&sums)[8], 
     }
 }
 
+// The same for a warp's columns n0 .. n0 + 31 and n0 + 128 .. n0 + 159 of 32 rows where all lies on 16 bytes; without
+// kMore a bias at most and BF16 rows.  The products of a tile run two steps on while its results leave, so what
+// `finish` asks of every element cost 1400 to 2200 clocks a 16 columns: 8192 8-bit rows of 7168 x 4096 217 us with it, 205
+// with this, 2051 BF16 rows of 4096 x 14336 179 and 168, with GELU and z 214 and 206.  In a kernel without `finish`: beside it
+// the sums of the loop spilled.
+bool is_whole(const Out& o)
+{
+    return o.vec_y && o.N % 16 == 0 && (!o.bias || o.vec_bias) && (!o.residual || o.vec_r) && (!o.pre || o.vec_pre);
+}
+template <bool kMore>
+__device__ __forceinline__ void finish_whole(const Out& o, const float (&sums)[2][32], int64_t first, int lane, int rows, int64_t n0,
+                                             uint8_t* stage)
+{
+    const int r = lane >> 1;
+    const bool upper = r < rows, lower = r + 16 < rows;
+    uint4* put = reinterpret_cast<uint4*>(stage + lane * kStagePitch);
+    const uint4* get = reinterpret_cast<const uint4*>(stage + r * kStagePitch + (lane & 1) * 16);
+    const uint4* get_lower = reinterpret_cast<const uint4*>(stage + (r + 16) * kStagePitch + (lane & 1) * 16);
+    // 32 bytes a row, two lanes each
+    auto leave = [&](const uint4& w0, const uint4& w1, uint8_t* to, int64_t pitch) {
+        put[0] = w0, put[1] = w1;
+        __syncwarp();
+        if (upper) *reinterpret_cast<uint4*>(to + r * pitch + (lane & 1) * 16) = *get;
+        if (lower) *reinterpret_cast<uint4*>(to + (r + 16) * pitch + (lane & 1) * 16) = *get_lower;
+        __syncwarp();
+    };
+    // 64 bytes a row, 16 rows at a time, four lanes each
+    auto leave_floats = [&](const float (&v)[16], float* to, int64_t ld) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (lane >> 4 == h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float4*>(stage + (lane & 15) * 80 + i * 16) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int at = i * 8 + (lane >> 2), row = h * 16 + at;
+                if (row < rows)
+                    *reinterpret_cast<float4*>(to + row * ld + (lane & 3) * 4) = *reinterpret_cast<const float4*>(stage + at * 80 + (lane & 3) * 16);
+            }
+            __syncwarp();
+        }
+    };
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int64_t c = n0 + q / 2 * 128 + q % 2 * 16;
+        if (c >= o.N) break;  // with the whole warp
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = sums[q / 2][q % 2 * 16 + j];
+        if (o.bias)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 b = __ldg(reinterpret_cast<const float4*>(o.bias + c) + j);
+                v[4 * j] += b.x, v[4 * j + 1] += b.y, v[4 * j + 2] += b.z, v[4 * j + 3] += b.w;
+            }
+        if constexpr (kMore) {
+            if (o.pre) leave_floats(v, o.pre + first * o.N + c, o.N);
+            if (o.act == FP8Z1_ACT_SILU)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = activate(v[j], FP8Z1_ACT_SILU);
+            else if (o.act != FP8Z1_ACT_NONE)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = activate(v[j], FP8Z1_ACT_GELU_TANH);
+            if (o.residual && lane < rows) {
+                const uint4* p = reinterpret_cast<const uint4*>(o.residual + (first + lane) * o.ld_r + c);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 u = p[i];
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
+                        v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+                    }
+                }
+            }
+            if (o.f32) {
+                leave_floats(v, static_cast<float*>(o.y) + first * o.ld_y + c, o.ld_y);
+                continue;
+            }
+        }
+        uint32_t u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            u[j] = *reinterpret_cast<const uint32_t*>(&two);
+        }
+        leave(make_uint4(u[0], u[1], u[2], u[3]), make_uint4(u[4], u[5], u[6], u[7]),
+              reinterpret_cast<uint8_t*>(static_cast<bf16*>(o.y) + first * o.ld_y + c), o.ld_y * 2);
+    }
+}
+
+// And for FP32 rows of any alignment with a bias at most: 16 columns of 16 rows at a time, 16 lanes a row.  1001 rows of
+// 4096 to 50001 logits: 280 us, with `finish` 305.
+__device__ __forceinline__ void finish_odd(const Out& o, const float (&sums)[2][32], int64_t first, int lane, int rows, int64_t n0,
+                                           uint8_t* stage)
+{
+    const int r = lane >> 4, k = lane & 15;
+    const float* get = reinterpret_cast<const float*>(stage + r * 80 + k * 4);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int64_t c = n0 + q / 2 * 128 + q % 2 * 16;
+        if (c >= o.N) break;  // with the whole warp
+        const bool in = c + k < o.N;
+        const float b = o.bias && in ? __ldg(o.bias + c + k) : 0.0f;
+        float* to = static_cast<float*>(o.y) + (first + r) * o.ld_y + c + k;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (r == h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float* v = &sums[q / 2][q % 2 * 16 + 4 * i];
+                    *reinterpret_cast<float4*>(stage + k * 80 + i * 16) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i, to += 2 * o.ld_y)
+                if (in && h * 16 + 2 * i + r < rows) *to = get[i * 40] + b;
+            __syncwarp();
+        }
+    }
+}
+
 // ---- many rows ------------------------------------------------------------------------------
 
 constexpr int kCols = 256;
@@ -185,7 +310,7 @@ struct Many {
     static constexpr uint32_t kSmem = kStages * kStageBytes + 1024 + 256 + 8192 + 16 * 32 * kStagePitch;
 };
 
-template <int kTerms, bool kKMajor>
+template <int kTerms, bool kKMajor, bool kWhole>
 __global__ void __launch_bounds__(kManyThreads, 1)
 many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ CUtensorMap map_lo,
             const __grid_constant__ CUtensorMap map_w, const __grid_constant__ Args a)
@@ -390,14 +515,25 @@ many_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ 
                 for (int j = 0; j < 64; ++j) sums[j / 32][j % 32] = NAN;
             const int64_t first = (int64_t)m * 256 + sub * 128 + (warp & 3) * 32;  // row of the warp
             const int rows = (int)min(max(a.o.T - first, (int64_t)0), (int64_t)32);
+            const int64_t n0 = (int64_t)n * kCols + group * 32;
+            const bool plain = a.o.act == FP8Z1_ACT_NONE && !a.o.residual && !a.o.pre;
+            if constexpr (kWhole) {
+                if (plain && !a.o.f32)
+                    finish_whole<false>(a.o, sums, first, lane, rows, n0, stage);
+                else
+                    finish_whole<true>(a.o, sums, first, lane, rows, n0, stage);
+            } else if (plain && a.o.f32) {
+                finish_odd(a.o, sums, first, lane, rows, n0, stage);
+            } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t n0 = (int64_t)n * kCols + q / 2 * 128 + group * 32 + q % 2 * 16;
-                if (n0 >= a.o.N || rows == 0) continue;  // with the whole warp
-                uint64_t v[8];  // in pairs they need no registers of their own
+                for (int q = 0; q < 4; ++q) {
+                    const int64_t c = n0 + q / 2 * 128 + q % 2 * 16;
+                    if (c >= a.o.N || rows == 0) continue;  // with the whole warp
+                    uint64_t v[8];  // in pairs they need no registers of their own
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = pair(sums[q / 2][q % 2 * 16 + 2 * j], sums[q / 2][q % 2 * 16 + 2 * j + 1]);
-                finish(a.o, v, first, lane, rows, n0, stage);
+                    for (int j = 0; j < 8; ++j) v[j] = pair(sums[q / 2][q % 2 * 16 + 2 * j], sums[q / 2][q % 2 * 16 + 2 * j + 1]);
+                    finish(a.o, v, first, lane, rows, c, stage);
+                }
             }
         }
     }
@@ -690,8 +826,9 @@ int launch_many(const Rows& x, const Weight& w, Args a, cudaStream_t s)
     a.n_tiles = (int32_t)ceil_div(a.o.N, kCols);
     for (int t = 0; t < 2; ++t)
         a.idesc[t] = instruction_of(256, kCols, false, !kKMajor, t && x.lo_format == Lo::kE5M2, 0);
-    return ffn::launch_persistent<many_kernel<kTerms, kKMajor>, 2>(kManyThreads, Many<kTerms>::kSmem,
-                                                                    (int64_t)a.m_tiles * a.n_tiles, s, hi, lo, wm, a);
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+    return is_whole(a.o) ? ffn::launch_persistent<many_kernel<kTerms, kKMajor, true>, 2>(kManyThreads, Many<kTerms>::kSmem, tiles, s, hi, lo, wm, a)
+                         : ffn::launch_persistent<many_kernel<kTerms, kKMajor, false>, 2>(kManyThreads, Many<kTerms>::kSmem, tiles, s, hi, lo, wm, a);
 }
 
 // CTAs along K: as few rounds of K steps as the SMs' CTAs need, a CTA's start and end worth 4 of them.

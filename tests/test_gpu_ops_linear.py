@@ -155,6 +155,20 @@ def test_result_over_the_residual(tokens):
     assert got is s["residual"] and torch.equal(got, want)
 
 
+@pytest.mark.parametrize("x", ["bf16", "fp8"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bias,act,residual", [(False, None, False), (True, None, False), (True, "silu", True), (False, "gelu_tanh", False)])
+@pytest.mark.parametrize("rows,cols,transposed,pad", [(1024, 4112, False, 0), (1024, 4112, False, 16), (1024, 4112, False, 3),
+                                                      (4105, 1024, True, 0), (4105, 1024, True, 1)])
+def test_ends_of_large_tiles(rows, cols, transposed, pad, bias, act, residual, dtype, x):
+    """Enough rows and columns for the widest tiles, the last ones cut off; results on 16 bytes, and not."""
+    s = make(2051, rows, cols, transposed, rows + pad, x)
+    outer = rows if transposed else cols
+    out = torch.full((2051, outer + pad), 7.0, dtype=dtype, device="cuda")
+    forward(s, transposed, act, bias, residual, dtype, save=act is not None, out=out[:, :outer])
+    assert (out[:, outer:] == 7.0).all()
+
+
 def test_other_rows_do_not_matter():
     """An infinity, a NaN, and the largest and smallest numbers leave the other rows' results as they were."""
     for tokens in (6, 300):
