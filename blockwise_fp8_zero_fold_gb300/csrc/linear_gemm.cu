@@ -584,7 +584,7 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
     cg::cluster_group cluster = cg::this_cluster();
 
     const int warp = of_warp((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    // the rows' tiles outermost, in one dimension of the grid: another holds 65535
+    // the rows' tiles outermost, in one dimension of the grid (another would hold 65535, whatever the rule below takes)
     const int tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits, m = tile / a.n_tiles, n = tile - m * a.n_tiles;
     const int token0 = m * kN;
     const int k0 = a.k_blocks * split / a.splits, k1 = a.k_blocks * (split + 1) / a.splits;
@@ -863,7 +863,7 @@ int launch_few(const Rows& x, const Weight& w, Args a, cudaStream_t s)
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
-    c.gridDim = dim3((unsigned)((int64_t)a.n_tiles * a.splits * a.m_tiles));  // below 2^31: more than 128 columns take it for few rows alone
+    c.gridDim = dim3((unsigned)((int64_t)a.n_tiles * a.splits * a.m_tiles));
     c.blockDim = dim3(S::kThreads);
     c.dynamicSmemBytes = S::kSmem;
     c.stream = s;
@@ -878,15 +878,16 @@ int launch_few(const Rows& x, const Weight& w, Args a, cudaStream_t s)
 }
 
 // Whether CTAs of 128 columns by 128 rows take less time than pairs with 256 x 256.  A step of K takes both about
-// as long, 0.7 us of BF16 rows and 0.48 of 8-bit ones, so the rounds of the SMs decide; a round's start and end are worth 4
-// and 6 steps.  Measured, us of few and many: 512 rows of 7168 x 4096 42 and 42, 256 29 and 41, 1001 82 and 46; 200 of
-// 4096 x 14336 59 and 30; 2051 of 4096 x 1024 31 and 32, x 2048 56 and 33.
+// as long, so the rounds of the SMs decide; a round's start and end are worth 4 steps.  Measured, us of few and many, BF16
+// rows and 8-bit ones: 512 rows of 7168 x 4096 42 and 40, 30 and 32; 256 29 and 39, 22 and 31; 1001 82 and 44, 58 and 32; 200 of
+// 4096 x 14336 59 and 28, 50 and 22; 1001 of 4096 x 1024 23 and 27, 17 and 19, 2051 32 and 30, 21 and 20; 4096 of 1024 x 512
+// 16 and 15, 12 and 9.
 bool few_tiles(int64_t T, int64_t N, int64_t k_blocks)
 {
     const int64_t tiles = ceil_div(T, 128) * ceil_div(N, 128);
     const int n = splits_of(tiles, kSms, k_blocks);
     return ceil_div(tiles * n, kSms) * (ceil_div(k_blocks, n) + 4) <
-           ceil_div(ceil_div(T, 256) * ceil_div(N, 256), kSms / 2) * (k_blocks + 6);
+           ceil_div(ceil_div(T, 256) * ceil_div(N, 256), kSms / 2) * (k_blocks + 4);
 }
 
 template <int kTerms, bool kKMajor>
