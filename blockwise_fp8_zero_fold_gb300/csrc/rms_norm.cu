@@ -16,6 +16,7 @@
 // their gradient 90 us, 5.2 TB/s, and 4 us for the columns' sums.  32 rows 3 us from a captured graph.  2003 rows of
 // 4097 FP32, single elements: 15 and 26 us, the gradient at 3.8 TB/s, bound by its instructions.
 #include <algorithm>
+#include <mutex>
 
 #include "ops_common.cuh"
 #include "tc.cuh"
@@ -373,6 +374,16 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const GradArgs a)
 // groups of the other warps take them in turn.  Bulk copies move whole 16 bytes on 16-byte
 // boundaries; what a row has before its first and behind its last such boundary is read where it lies.
 
+//
+// A wait that runs out ends its group's use of the ring: no stage is given back whose copies did not come, so
+// that no barrier is filled twice; the group's dx from that row on and d_weight are NaN.  The copying thread
+// leaves when all that it sent has come.
+
+__device__ unsigned g_timeouts;
+#if FP8Z1_CHECKED
+__device__ unsigned g_stall;  // of the first CTA's first row, bit 0: it is never copied, 1: a warp does not give it back
+#endif
+
 constexpr int kMostStages = 8, kMostGroups = 8;
 
 struct Ring {
@@ -457,11 +468,19 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_ring_kernel(const GradA
         if (tid != 0) return;
         int slot = 0;
         uint32_t phase = 0;
+        bool ok = true, again = false;  // whether every stage has been filled
         for (int64_t row = blockIdx.x; r.stages && row < a.rows; row += gridDim.x) {
-            if (!tc::bar_wait(bar_empty + 8 * slot, phase ^ 1)) break;  // the readers' waits run out too
-            fetch<T>(r, row, a.dim, tc::smem_addr(stages) + slot * stage_bytes, bar_full + 8 * slot);
-            if (++slot == r.stages) slot = 0, phase ^= 1;
+            ok = tc::bar_wait(bar_empty + 8 * slot, phase ^ 1);
+            if (!ok) break;  // the readers' waits run out too
+#if FP8Z1_CHECKED
+            if (!(g_stall & 1 && row == 0))
+#endif
+                fetch<T>(r, row, a.dim, tc::smem_addr(stages) + slot * stage_bytes, bar_full + 8 * slot);
+            if (++slot == r.stages) slot = 0, phase ^= 1, again = true;
         }
+        // the copies in flight end before the CTA does, whatever became of the readers
+        for (int i = 0; i < (again ? r.stages : slot); ++i) ok &= tc::bar_wait(bar_full + 8 * i, i < slot ? phase : phase ^ 1);
+        if (!ok) atomicAdd(&g_timeouts, 1u);
         return;
     }
     float dw[kE];
@@ -469,24 +488,30 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_ring_kernel(const GradA
     for (int j = 0; j < kE; ++j) dw[j] = 0.0f;
     int slot = group, odd = 0;
     uint32_t phase = 0;
-    for (int64_t row = blockIdx.x + (int64_t)group * gridDim.x; row < a.rows; row += (int64_t)r.groups * gridDim.x) {
-        const bool ok = r.stages == 0 || tc::bar_wait(bar_full + 8 * slot, phase);
+    bool lost = false;  // a wait of the group ran out
+    const int rows = (int)a.rows;  // and a step more, within 2^31
+    int row = blockIdx.x + group * gridDim.x;
+    for (; row < rows && !lost; row += r.groups * gridDim.x) {
+        const bool ok = r.stages == 0 || tc::bar_wait_warp(bar_full + 8 * slot, phase);
+        if (!ok && (tid & 31) == 0) atomicAdd(&g_timeouts, 1u);
         const uint8_t* stage = stages + slot * stage_bytes;
         Held<T, kE> s, d;
         take<kE, kVec, T>(s, r, a.s, a.ld_s, 0, row, a.dim, stage, tid);
         take<kE, kVec, T>(d, r, a.dy, a.ld_dy, 1, row, a.dim, stage, tid);
+        float squares = 0.0f;
         auto sums = [&](float2 v, int again) {
             v = warp_sum(v);
-            if (!ok) v.x = NAN;  // a copy that never came
+            if (!ok) v.x = -INFINITY;  // a copy that never came: the row becomes NaN, and no squares have this sum
             // two rows' sums lie side by side: one barrier a row
             float2* mine = part[group][again ? 2 : odd];
             if ((tid & 31) == 0) mine[tid >> 5] = v;
             asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(r.threads) : "memory");
             v = mine[0];
             for (int w = 1; w < warps; ++w) v.x += mine[w].x, v.y += mine[w].y;
+            squares = v.x;
             return v;
         };
-        const T* more = static_cast<const T*>(a.d_total) + row * a.ld_t;
+        const T* more = static_cast<const T*>(a.d_total) + (int64_t)row * a.ld_t;
         const Span<T> span(more, a.dim);
         const T* here = reinterpret_cast<const T*>(stage + 2 * r.pitch + (reinterpret_cast<uintptr_t>(more) & 15));
         grad_row<T, kE, kVec>(a, row, tid, r.threads, s, d, weight, dw, sums, [&](int c, float(&v)[kPiece<kVec>]) {
@@ -509,12 +534,21 @@ __global__ void __launch_bounds__(kThreads, 1) norm_grad_ring_kernel(const GradA
 #pragma unroll
             for (int i = 0; i < kPiece<kVec>; ++i) v[i] += t[i];
         });
+        if (!(squares >= 0.0f)) {  // or the row's own NaN
+            for (int w = 0; w < warps; ++w) lost |= part[group][odd][w].x < 0.0f;
+            if (lost) continue;  // with the whole group, to the end
+        }
         __syncwarp();
-        if (r.stages && (tid & 31) == 0) tc::bar_arrive(bar_empty + 8 * slot);
+#if FP8Z1_CHECKED
+        if (!(g_stall & 2 && row == 0 && tid == 0))
+#endif
+            if (r.stages && (tid & 31) == 0) tc::bar_arrive(bar_empty + 8 * slot);
         odd ^= 1;
         slot += r.groups;
         if (slot >= r.stages) slot -= r.stages, phase ^= 1;
     }
+    for (; row < rows; row += r.groups * gridDim.x)  // what a lost group did not come to
+        for (int c = tid; c < a.dim; c += r.threads) static_cast<T*>(a.dx)[(int64_t)row * a.ld_dx + c] = from_float<T>(NAN);
 #pragma unroll
     for (int j = 0; j < kE; ++j) {
         const int c = column<kVec>(j, tid, r.threads);
@@ -744,4 +778,33 @@ extern "C" int fp8z1_rms_norm_grad(int64_t rows, int64_t dim, const void* dy, in
     }
     if (st != FP8Z1_OK) return st;
     return launch_column_sum(a.part, parts, dim, d_weight, s);
+}
+
+extern "C" int fp8z1_rms_norm_timeouts(uint32_t* count)
+{
+    if (!count) return FP8Z1_EINVAL;
+    // the devices' counters only grow, so that no count is lost between a read and a reset
+    static std::mutex lock;
+    static uint32_t seen[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return FP8Z1_ECUDA;
+    std::lock_guard<std::mutex> hold(lock);
+    unsigned n = 0;
+    if (cudaMemcpyFromSymbol(&n, g_timeouts, 4) != cudaSuccess) {
+        cudaGetLastError();
+        return FP8Z1_ECUDA;
+    }
+    *count = n - seen[dev];
+    seen[dev] = n;
+    return FP8Z1_OK;
+}
+
+extern "C" int fp8z1_checked_rms_norm_stall(uint32_t kernels)
+{
+#if FP8Z1_CHECKED
+    return cudaMemcpyToSymbol(g_stall, &kernels, 4) == cudaSuccess ? FP8Z1_OK : FP8Z1_ECUDA;
+#else
+    (void)kernels;
+    return FP8Z1_EINVAL;
+#endif
 }

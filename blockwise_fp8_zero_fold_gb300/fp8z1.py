@@ -160,6 +160,8 @@ _SIGS = {
     "fp8z1_rms_norm_grad_workspace": (C.c_int, [C.c_int64, C.c_int64, C.POINTER(C.c_int64)]),
     "fp8z1_rms_norm_grad": (C.c_int, [C.c_int64, C.c_int64, _P, C.c_int32, C.c_int64, _P, C.c_int64, _P, C.c_float, _P,
                                       C.c_int64, _P, C.c_int64, _P, _P, _P]),
+    "fp8z1_rms_norm_timeouts": (C.c_int, [C.POINTER(C.c_uint32)]),
+    "fp8z1_checked_rms_norm_stall": (C.c_int, [C.c_uint32]),
     "fp8z1_route": (C.c_int, [_P, C.c_int32, C.c_int64, C.c_int64, C.c_int64, _P, _P, _P]),
     "fp8z1_dispatch": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.c_int64, _P, C.c_int32, C.c_int64, _P, _P, _P,
                                  C.c_int64, _P]),
@@ -664,6 +666,18 @@ def fp8z1_rms_norm_grad(rows: int, dim: int, dy, type_: int, ld_dy: int, total, 
                                     ld_dt, _at(dx), ld_dx, _at(d_weight), _at(workspace), _stream(stream))
     if st:
         raise Fp8z1Error(st, "fp8z1_rms_norm_grad")
+
+
+def fp8z1_rms_norm_timeouts() -> int:
+    """Warps of the norm's gradient that gave up waiting since the last call (synchronous; 0 in all normal use)."""
+    n = C.c_uint32()
+    _check(lib().fp8z1_rms_norm_timeouts(C.byref(n)), "fp8z1_rms_norm_timeouts")
+    return n.value
+
+
+def fp8z1_checked_rms_norm_stall(kernels: int):
+    """Test hook of the checked library, as ``fp8z1_checked_ffn_stall``."""
+    _check(lib().fp8z1_checked_rms_norm_stall(kernels), "fp8z1_checked_rms_norm_stall")
 
 
 def fp8z1_route(ids, id_bytes: int, tokens: int, top: int, experts: int, offsets, place, stream=None):

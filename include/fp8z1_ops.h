@@ -198,6 +198,14 @@ int fp8z1_rms_norm_grad(int64_t rows, int64_t dim, const void* dy, int32_t type,
                         int64_t ld_total, const float* weight, float eps, const void* d_total, int64_t ld_dt, void* dx,
                         int64_t ld_dx, float* d_weight, void* workspace, void* stream);
 
+/* As fp8z1_ffn_timeouts, of the norm's gradient, whose rows of more than 1024 columns are copied ahead to its
+ * warps: a copy that does not come leaves NaN in its rows of dx and in d_weight. */
+int fp8z1_rms_norm_timeouts(uint32_t* count);
+
+/* As fp8z1_checked_ffn_stall.  Bits: of the first CTA's first row, 1 it is never copied, 2 a warp does
+ * not give its place back to the next one. */
+int fp8z1_checked_rms_norm_stall(uint32_t kernels);
+
 /* ---- routing ------------------------------------------------------------------------- */
 
 /* Sorts the choices (t, j), 0 <= t < tokens, 0 <= j < top, by their expert ids[t, j]
