@@ -375,6 +375,9 @@ __global__ void __launch_bounds__(256) norm_grad_kernel(const GradArgs a)
 // boundaries; what a row has before its first and behind its last such boundary is read where it lies.
 
 //
+// A stage is always the same group's.  Copies come in any order: a group that took over another's stage could look
+// for its second row there before the first has come, and a barrier that is a phase behind passes for filled.
+//
 // A wait that runs out ends its group's use of the ring: no stage is given back whose copies did not come, so
 // that no barrier is filled twice; the group's dx from that row on and d_weight are NaN.  The copying thread
 // leaves when all that it sent has come.
@@ -384,7 +387,8 @@ __device__ unsigned g_timeouts;
 __device__ unsigned g_stall;  // of the first CTA's first row, bit 0: it is never copied, 1: a warp does not give it back
 #endif
 
-constexpr int kMostStages = 8, kMostGroups = 8;
+constexpr int kMostStages = 16, kMostGroups = 8;
+constexpr int kBarriers = 16 * kMostStages;  // bytes: full, empty [kMostStages]
 
 struct Ring {
     const void* in[3];
@@ -448,11 +452,11 @@ __device__ __forceinline__ void take(Held<T, kE>& v, const Ring& r, const void* 
 template <class T, int kE, bool kVec, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1) norm_grad_ring_kernel(const GradArgs a, const Ring r)
 {
-    extern __shared__ __align__(128) uint8_t smem[];  // full, empty [kMostStages], the weight, stages
-    __shared__ float2 part[kMostGroups][3][32];
+    extern __shared__ __align__(128) uint8_t smem[];  // barriers, the weight, stages
+    __shared__ float2 part[kMostGroups][3][32];  // 6144 bytes
     const uint32_t bar_full = tc::smem_addr(smem), bar_empty = bar_full + 8 * kMostStages;
-    float* weight = reinterpret_cast<float*>(smem + 128);
-    uint8_t* stages = smem + 128 + (a.dim + 3) / 4 * 16;
+    float* weight = reinterpret_cast<float*>(smem + kBarriers);
+    uint8_t* stages = smem + kBarriers + (a.dim + 3) / 4 * 16;
     const int stage_bytes = r.n * r.pitch, warps = r.threads >> 5;
     const int group = threadIdx.x / r.threads, tid = threadIdx.x - group * r.threads;
     if (threadIdx.x == 0) {
@@ -607,9 +611,10 @@ int shape_ring(Ring& r, int64_t dim, int size, int each)  // bytes of shared mem
     r.threads = threads_of(dim, each);
     r.groups = ring_groups(dim, each);
     r.pitch = (int)ceil_div(dim * size + 16, 16) * 16;
-    const int fixed = 128 + (int)ceil_div(dim, 4) * 16, stage = r.n * r.pitch;
+    const int fixed = kBarriers + (int)ceil_div(dim, 4) * 16, stage = r.n * r.pitch;
     r.stages = std::min(kMostStages, (kRingSmem - fixed - 6144) / stage);
-    if (r.stages < 2 || r.stages < r.groups || r.threads > 480) r.stages = 0;
+    r.stages -= r.stages % r.groups;  // every stage is one group's: see above
+    if (r.stages < 2 || r.threads > 480) r.stages = 0;
     return fixed + r.stages * stage;
 }
 

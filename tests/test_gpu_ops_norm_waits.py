@@ -66,3 +66,12 @@ def test_what_a_wait_belongs_to_is_nan(lib, stall, more, dim, dtype):
     again = run()
     torch.cuda.synchronize()
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw) and F.fp8z1_rms_norm_timeouts() == 0
+
+
+# 7, 5, 5, 3, 3 groups, which the 16 places, or the 8 that there would be room for, do not go round evenly
+@pytest.mark.parametrize("dim,dtype", [(2048, torch.bfloat16), (3064, torch.bfloat16), (1025, torch.float32), (2049, torch.float32),
+                                       (4096, torch.bfloat16)])
+@pytest.mark.parametrize("more", [False, True])
+def test_a_place_is_one_groups_own_nan(lib, more, dim, dtype):
+    """A group does not take a row for its own in a place whose copy, another group's, has not come."""
+    test_what_a_wait_belongs_to_is_nan(lib, NEVER_COPIED, more, dim, dtype)
