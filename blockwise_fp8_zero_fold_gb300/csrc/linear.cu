@@ -399,6 +399,15 @@ extern "C" int fp8z1_linear(const fp8z1_linear_dims* dims, const void* x, int64_
     if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(bias, 4) || !aligned(residual, 2) || !aligned(y, y_size) ||
         !aligned(pre, 4) || (fp8 ? !aligned(x, 16) || ld_x % 16 || !aligned(x_scale, 4) : !aligned(x, 2) || !aligned(workspace, 256)))
         return FP8Z1_EALIGN;
+    {
+        const Area out = {y, d.T, N * y_size, ld_y * y_size}, z = dense(pre, d.T * N * 4), r = {residual, d.T, N * 2, ld_residual * 2};
+        const Area read[] = {dense(codes, d.R * d.C), dense(scales, ceil_div(d.R, 128) * ceil_div(d.C, 128) * 4), dense(bias, N * 4),
+                             {fp8 ? x : nullptr, d.T, K, ld_x}, dense(fp8 ? x_scale : nullptr, d.T * ceil_div(K, 128) * 4)};
+        for (const Area& a : read)
+            if (overlap(out, a) || overlap(z, a)) return FP8Z1_EINVAL;
+        // a tile's residual is read when others' results may be there
+        if (overlap(out, z) || overlap(z, r) || (d.y_type == FP8Z1_BF16 ? !same_or_apart(out, r) : overlap(out, r))) return FP8Z1_EINVAL;
+    }
     NvtxRange range("fp8z1_linear");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Rows rows = {};
@@ -468,6 +477,16 @@ extern "C" int fp8z1_linear_grad(const fp8z1_linear_dims* dims, const void* dy, 
     if (!aligned(dy, dy_size) || (d_weight && !aligned(x, 2)) || (dx && (!aligned(dx, 2) || !aligned(codes, 16) || !aligned(scales, 4))) ||
         !aligned(pre, 4) || !aligned(workspace, 256))
         return FP8Z1_EALIGN;
+    {
+        const Area to_x = {dx, d.T, K * 2, ld_dx * 2}, to_w = dense(d_weight, d.R * d.C * 4), to_b = dense(d_bias, N * 4);
+        const Area xs = {x, d.T, K * 2, ld_x * 2}, dys = {dy, d.T, N * dy_size, ld_dy * dy_size};
+        if (overlap(to_x, to_w) || overlap(to_x, to_b) || overlap(to_w, to_b) || overlap(to_x, dense(codes, d.R * d.C)) ||
+            overlap(to_x, dense(scales, ceil_div(d.R, 128) * ceil_div(d.C, 128) * 4)))
+            return FP8Z1_EINVAL;
+        // d_weight comes after dx, of x and (where dz is dy itself) of dy
+        if (d_weight && (overlap(to_x, xs) || (d.exact() && (overlap(to_x, dys) || overlap(to_w, xs) || overlap(to_w, dys)))))
+            return FP8Z1_EINVAL;
+    }
     NvtxRange range("fp8z1_linear_grad");
     Backward b;
     Cut c(workspace);

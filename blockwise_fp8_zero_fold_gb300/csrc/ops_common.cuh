@@ -55,6 +55,34 @@ bool allow_smem(int bytes)
 // out[c] = sum over i < n of part[i, c], [n, cols] FP32, in a fixed order (rms_norm.cu).
 int launch_column_sum(const float* part, int n, int64_t cols, float* out, cudaStream_t s);
 
+// The memory of `n` rows of `bytes` each, `ld` bytes apart (p NULL: none).
+struct Area {
+    const void* p;
+    int64_t n, bytes, ld;
+};
+inline Area dense(const void* p, int64_t bytes) { return Area{p, 1, bytes, bytes}; }
+
+// Whether two share a byte.  Rows of one stride may lie between the other's rows, as columns of one buffer; of several
+// strides they count as shared wherever one begins before the other's end.
+inline bool overlap(Area a, Area b)
+{
+    if (!a.p || !b.p || a.n < 1 || b.n < 1 || a.bytes < 1 || b.bytes < 1) return false;
+    const auto begin = [](const Area& x) { return (unsigned __int128)reinterpret_cast<uintptr_t>(x.p); };
+    const auto end = [&](const Area& x) { return begin(x) + (unsigned __int128)(x.n - 1) * (unsigned __int128)x.ld + x.bytes; };
+    if (end(a) <= begin(b) || end(b) <= begin(a)) return false;
+    if (a.n == 1) a.ld = b.ld;
+    if (b.n == 1) b.ld = a.ld;
+    if (a.ld != b.ld || (a.n == 1 && b.n == 1)) return true;
+    const int64_t to = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % a.ld;
+    const int64_t at = to < 0 ? to + a.ld : to;  // of b's rows, from the start of one of a's
+    return at < a.bytes || at + b.bytes > a.ld;
+}
+// Whether b is a, or shares nothing with it.
+inline bool same_or_apart(const Area& a, const Area& b)
+{
+    return (a.p == b.p && a.n == b.n && a.bytes == b.bytes && (a.ld == b.ld || a.n == 1)) || !overlap(a, b);
+}
+
 // The SM count of the current device (0 when it cannot be read).
 inline int sm_count_here()
 {

@@ -269,7 +269,8 @@ int fp8z1_linear_sizes(const fp8z1_linear_dims* dims, int64_t* forward_bytes, in
  * fp8z1_rms_norm writes them (x_scale is not read for BF16).  codes: 16-byte aligned.
  * bias: FP32 [width of y] or NULL; residual: BF16 or NULL; pre: NULL, or FP32 [tokens, width of
  * y] dense for z, which fp8z1_linear_grad reads.  y may be residual itself where both are BF16
- * of one stride.  Sums are FP32 over exact products of the codes and x (BF16 x down to 2^-13
+ * of one stride; else a result shares no memory with the other or with what the product reads (EINVAL;
+ * BF16 x has been read before).  Sums are FP32 over exact products of the codes and x (BF16 x down to 2^-13
  * of the largest of its 128 neighbours, to 2^-21 of that below); they repeat bit for
  * bit, and may change in their last places when other rows join.  An infinity or NaN in a row
  * of x leaves that row of y without finite numbers.  tokens == 0 enqueues nothing.
@@ -283,7 +284,8 @@ int fp8z1_linear(const fp8z1_linear_dims* dims, const void* x, int64_t ld_x, con
  *   sum over the rows of dz, FP32.
  * Each may be NULL, not all.  `pre`: z of the forward pass (not read without activation).
  * The residual's gradient is dy.  dy of `y_type`, dx: any alignment and stride; d_weight 16-byte
- * aligned.  dz is dy itself, exact, for BF16 dy without activation; else it is rounded for dx to 9
+ * aligned.  The results share no memory with one another, dx none with the weight nor, where d_weight is
+ * wanted, with x and (BF16 dy without activation, which d_weight's products read too) dy (EINVAL).  dz is dy itself, exact, for BF16 dy without activation; else it is rounded for dx to 9
  * significant bits (BF16 has 8) or 2^-17 of the largest of its 128 neighbours.  d_weight
  * and d_bias carry FP32 accuracy, d_weight every column of dz relative to its own size (x: what
  * lies above 2^-31 of the largest of 256 rows x 128 columns); every element is written.

@@ -1,0 +1,51 @@
+"""Results in memory that a call's inputs lie in too, where that is right: in their place, and between their rows."""
+import pytest
+import torch
+
+from blockwise_fp8_zero_fold_gb300 import fp8z1 as F
+from blockwise_fp8_zero_fold_gb300 import ops
+from tests import _more as M
+from tests import _ops as R
+from tests._gpu import lib  # noqa: F401
+
+pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("lib")]
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def beside(*tensors):
+    """The same tensors as columns of one buffer."""
+    both = torch.cat(tensors, 1)
+    return torch.split(both, [t.shape[1] for t in tensors], 1)
+
+
+def product(tokens, seed):
+    g = M.gen(seed)
+    codes, scale = R.fp8_weight(g, 256, 256)
+    x, r, dy = (torch.randn(tokens, 256, generator=g, device="cuda").bfloat16() for _ in range(3))
+    return codes, scale, x, r, dy
+
+
+@pytest.mark.parametrize("tokens", [1, 30, 700])
+def test_product(tokens):
+    codes, scale, x, r, _ = product(tokens, tokens)
+    want = ops.linear(x, codes, scale, residual=r)
+    xs, rs, out = beside(x, r, torch.zeros_like(x))
+    assert torch.equal(ops.linear(xs, codes, scale, residual=rs, out=out), want) and torch.equal(xs, x) and torch.equal(rs, r)
+    assert torch.equal(ops.linear(xs, codes, scale, residual=rs, out=rs), want) and torch.equal(xs, x)
+    # BF16 rows have been read when the first result is written
+    assert torch.equal(ops.linear(xs, codes, scale, residual=r, out=xs), want)
+
+
+@pytest.mark.parametrize("tokens", [1, 30, 700])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_products_gradients(tokens, act):
+    """dx in dy's place where d_weight is not wanted, or dz is not dy itself."""
+    codes, scale, x, r, dy = product(tokens, tokens)
+    _, pre = ops.linear(x, codes, scale, activation=act, save=True)
+    want = ops.linear_grad(dy, x, codes, scale, activation=act, pre=pre, bias=True)
+    d = F.fp8z1_linear_dims(tokens, 256, 256, 0, F.ACT_SILU if act else F.ACT_NONE, F.BF16, F.BF16)
+    ws = torch.empty(F.fp8z1_linear_sizes(d)[1], dtype=torch.uint8, device="cuda")
+    dx, dw, db = dy.clone(), torch.empty_like(want[1]) if act else None, torch.empty_like(want[2])
+    F.fp8z1_linear_grad(d, dx, 256, x, 256, codes, scale, pre, dx, 256, dw, db, ws, torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(dx, want[0]) and torch.equal(db, want[2]) and (dw is None or torch.equal(dw, want[1]))

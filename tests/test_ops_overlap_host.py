@@ -1,0 +1,49 @@
+"""Results over what a call still reads are refused: no GPU.
+
+Device pointers are stand-ins (host memory): a call that the library refuses touches none of them."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from blockwise_fp8_zero_fold_gb300 import build as fp8build
+from blockwise_fp8_zero_fold_gb300 import fp8z1 as F
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    fp8build.build()
+    return F.lib()
+
+
+_MEM = np.zeros(1 << 22, np.uint8)
+P = (_MEM.ctypes.data + 255) & ~255  # 256-byte aligned
+AT = [P + (i << 18) for i in range(15)]  # 256 KB apart: buffers that share nothing
+
+# 40 rows through a weight of 64 x 64
+DIMS = dict(tokens=40, rows=64, cols=64, transposed=0, activation=F.ACT_NONE, x_type=F.BF16, y_type=F.BF16)
+X, XS, CODES, SCALES, BIAS, RES, Y, PRE, WS, DY, DX, DW, DB = AT[:13]
+LINEAR = dict(x=X, ld_x=64, xs=XS, codes=CODES, scales=SCALES, bias=BIAS, r=RES, ld_r=64, y=Y, ld_y=64, pre=PRE, ws=WS, stream=None)
+FP8, F32, SILU = dict(x_type=F.E4M3), dict(y_type=F.F32), dict(activation=F.ACT_SILU)
+
+
+@pytest.mark.parametrize("dims,change", [
+    ({}, dict(pre=Y)), ({}, dict(pre=Y + 40 * 64 * 2 - 4)), ({}, dict(pre=RES)), ({}, dict(y=RES + 128)), ({}, dict(y=RES - 128)),
+    ({}, dict(y=RES, ld_y=72)), ({}, dict(y=RES + 64, ld_y=128, ld_r=128)), (F32, dict(y=RES)), (F32, dict(y=RES + 64)),
+    ({}, dict(y=CODES)), ({}, dict(y=CODES - 64)), ({}, dict(y=SCALES)), ({}, dict(y=BIAS + 64)), ({}, dict(pre=CODES)),
+    ({}, dict(pre=BIAS)), (FP8, dict(y=X)), (FP8, dict(y=X + 1024)), (FP8, dict(y=XS)), (FP8, dict(pre=XS))])
+def test_product(dims, change):
+    d = F.fp8z1_linear_dims(*{**DIMS, **dims}.values())
+    assert F.lib().fp8z1_linear(C.byref(d), *{**LINEAR, **change}.values()) == F.EINVAL
+
+
+LGRAD = dict(dy=DY, ld_dy=64, x=X, ld_x=64, codes=CODES, scales=SCALES, pre=PRE, dx=DX, ld_dx=64, dw=DW, db=DB, ws=WS, stream=None)
+
+
+@pytest.mark.parametrize("dims,change", [
+    ({}, dict(dx=X)), ({}, dict(dx=X + 128)), ({}, dict(dx=DY)), ({}, dict(dx=DY - 2)), (SILU, dict(dx=X)), (F32, dict(dx=X)),
+    ({}, dict(dw=DX)), ({}, dict(dx=DW + 64 * 64 * 4 - 2)), ({}, dict(db=DW + 64)), ({}, dict(db=DX)), ({}, dict(dw=X)),
+    ({}, dict(dw=DY)), ({}, dict(dx=CODES)), ({}, dict(dx=SCALES)), ({}, dict(dx=CODES, dw=None))])
+def test_products_gradients(dims, change):
+    d = F.fp8z1_linear_dims(*{**DIMS, **dims}.values())
+    assert F.lib().fp8z1_linear_grad(C.byref(d), *{**LGRAD, **change}.values()) == F.EINVAL
