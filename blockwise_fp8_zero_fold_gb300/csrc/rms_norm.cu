@@ -718,6 +718,18 @@ extern "C" int fp8z1_rms_norm(int64_t rows, int64_t dim, const void* x, int32_t 
     if (!aligned(x, size) || !aligned(residual, size) || !aligned(total, size) || !aligned(y, size) ||
         !aligned(weight, 4) || !aligned(scales, 4))
         return FP8Z1_EALIGN;
+    {
+        const Area in[] = {{x, rows, dim * size, ld_x * size}, {residual, rows, dim * size, ld_r * size}};
+        const Area out[] = {{total, rows, dim * size, ld_total * size}, {y, rows, dim * size, ld_y * size}};
+        const Area bits[] = {dense(codes, rows * dim), dense(scales, rows * ceil_div(dim, 128) * 4)}, w = dense(weight, dim * 4);
+        if (overlap(out[0], out[1]) || overlap(bits[0], bits[1])) return FP8Z1_EINVAL;
+        // a row is whole in registers before its results leave, others are not
+        for (int i = 0; i < 2; ++i)
+            for (int j = 0; j < 2; ++j)
+                if (!same_or_apart(out[i], in[j]) || overlap(bits[i], in[j]) || overlap(bits[i], out[j])) return FP8Z1_EINVAL;
+        for (int i = 0; i < 2; ++i)
+            if (overlap(out[i], w) || overlap(bits[i], w)) return FP8Z1_EINVAL;
+    }
     NvtxRange range("fp8z1_rms_norm");
     const bool vec = dim % 8 == 0 && fits(x, ld_x, size) && fits(residual, ld_r, size) && fits(total, ld_total, size) &&
                      fits(y, ld_y, size) && aligned(weight, 16) && aligned(codes, 8);
@@ -758,6 +770,11 @@ extern "C" int fp8z1_rms_norm_grad(int64_t rows, int64_t dim, const void* dy, in
     if (!aligned(dy, size) || !aligned(total, size) || !aligned(d_total, size) || !aligned(dx, size) ||
         !aligned(weight, 4) || !aligned(workspace, 256))
         return FP8Z1_EALIGN;
+    const Area to = {dx, rows, dim * size, ld_dx * size};
+    if (overlap(to, dense(weight, dim * 4)) || overlap(to, dense(d_weight, dim * 4)) ||
+        !same_or_apart(to, Area{dy, rows, dim * size, ld_dy * size}) || !same_or_apart(to, Area{total, rows, dim * size, ld_total * size}) ||
+        !same_or_apart(to, Area{d_total, rows, dim * size, ld_dt * size}))
+        return FP8Z1_EINVAL;
     NvtxRange range("fp8z1_rms_norm_grad");
     const bool vec = dim % 8 == 0 && fits(dy, ld_dy, size) && fits(total, ld_total, size) && fits(d_total, ld_dt, size) &&
                      fits(dx, ld_dx, size) && aligned(weight, 16);

@@ -173,7 +173,8 @@ int fp8z1_distill(const void* logits, int32_t type, int64_t ld, int64_t rows, in
  * below 2^-117 are 0, with a scale of 1.  `y` or `codes` may be NULL (codes and scales together),
  * not both.
  * x, residual, total, y: `type`, rows of `dim` elements, ld >= dim apart; total and y may be
- * x or residual themselves, not each other.  weight: FP32 [dim].  Any alignment of the element types;
+ * x or residual themselves (of one stride); else a result shares no memory with another one or
+ * with what the norm reads (EINVAL).  weight: FP32 [dim].  Any alignment of the element types;
  * dim and strides of whole 16 bytes on 16-byte boundaries are moved 8 elements at a time.
  * No row is too large: squares beyond FP32 are summed scaled down.  An infinity or NaN
  * leaves its row without finite numbers (but 0 where a finite element meets an infinity's norm).
@@ -191,7 +192,8 @@ int fp8z1_rms_norm_grad_workspace(int64_t rows, int64_t dim, int64_t* bytes);
  *   g = dy * weight,  h = s * rstd,  dx = rstd * (g - h * mean_j(g_j h_j)) + d_total,
  *   d_weight = sum over the rows of dy * h   (FP32 [dim], every element written).
  * dx is the gradient of x and of the residual; d_total (NULL: none) is what reaches s past the
- * norm.  dy, total, d_total, dx: `type`; dx may be dy or d_total itself.  Sums are FP32 in a
+ * norm.  dy, total, d_total, dx: `type`; dx may be dy, total or d_total itself (of one stride); else
+ * it shares no memory with them, weight or d_weight (EINVAL).  Sums are FP32 in a
  * fixed order: results repeat bit for bit.
  * Errors: as fp8z1_rms_norm; EALIGN (workspace: 256 bytes). */
 int fp8z1_rms_norm_grad(int64_t rows, int64_t dim, const void* dy, int32_t type, int64_t ld_dy, const void* total,

@@ -49,3 +49,22 @@ def test_products_gradients(tokens, act):
     dx, dw, db = dy.clone(), torch.empty_like(want[1]) if act else None, torch.empty_like(want[2])
     F.fp8z1_linear_grad(d, dx, 256, x, 256, codes, scale, pre, dx, 256, dw, db, ws, torch.cuda.current_stream().cuda_stream)
     assert torch.equal(dx, want[0]) and torch.equal(db, want[2]) and (dw is None or torch.equal(dw, want[1]))
+
+
+@pytest.mark.parametrize("rows", [1, 5, 900])
+@pytest.mark.parametrize("dim", [96, 1536, 2001])
+def test_norm(rows, dim):
+    g = M.gen(dim)
+    x, r, dy, dt = (torch.randn(rows, dim, generator=g, device="cuda").bfloat16() for _ in range(4))
+    w = torch.rand(dim, generator=g, device="cuda") + 0.5
+    y, total = ops.rms_norm(x, w, residual=r)
+    dx, dw = ops.rms_norm_grad(dy, total, w, d_total=dt)
+    xs, rs, ys, ts = beside(x, r, torch.zeros_like(x), torch.zeros_like(x))
+    got = ops.rms_norm(xs, w, residual=rs, out=ys, total=ts)
+    assert torch.equal(got[0], y) and torch.equal(got[1], total) and torch.equal(xs, x) and torch.equal(rs, r)
+    got = ops.rms_norm(xs, w, residual=rs, out=rs, total=xs)
+    assert torch.equal(got[0], y) and torch.equal(got[1], total)
+    for k in range(4):
+        dys, ss, dts, more = beside(dy, total, dt, torch.zeros_like(x))
+        got = ops.rms_norm_grad(dys, ss, w, d_total=dts, dx=(dys, ss, dts, more)[k])
+        assert torch.equal(got[0], dx) and torch.equal(got[1], dw)

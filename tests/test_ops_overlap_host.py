@@ -47,3 +47,27 @@ LGRAD = dict(dy=DY, ld_dy=64, x=X, ld_x=64, codes=CODES, scales=SCALES, pre=PRE,
 def test_products_gradients(dims, change):
     d = F.fp8z1_linear_dims(*{**DIMS, **dims}.values())
     assert F.lib().fp8z1_linear_grad(C.byref(d), *{**LGRAD, **change}.values()) == F.EINVAL
+
+
+NORM = dict(rows=40, dim=64, x=X, type=F.BF16, ld_x=64, r=RES, ld_r=64, w=BIAS, eps=1e-6, total=DX, ld_t=64, y=Y, ld_y=64, codes=CODES,
+            scales=SCALES, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(total=Y), dict(total=Y + 128), dict(total=X + 128), dict(y=X + 128), dict(y=X - 2), dict(total=RES + 2),
+    dict(y=RES - 64 * 2 * 39), dict(y=X, ld_y=72), dict(total=RES, ld_r=72), dict(y=X + 64, ld_x=128, ld_y=128), dict(codes=X),
+    dict(codes=RES + 64), dict(codes=Y), dict(codes=DX), dict(scales=X), dict(scales=CODES + 64), dict(scales=Y), dict(y=BIAS),
+    dict(total=BIAS), dict(codes=BIAS), dict(scales=BIAS + 32)])
+def test_norm(change):
+    assert F.lib().fp8z1_rms_norm(*{**NORM, **change}.values()) == F.EINVAL
+
+
+GRAD = dict(rows=40, dim=64, dy=DY, type=F.BF16, ld_dy=64, s=X, ld_s=64, w=BIAS, eps=1e-6, dt=RES, ld_dt=64, dx=DX, ld_dx=64, dw=DB, ws=WS,
+            stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(dx=DY + 128), dict(dx=DY, ld_dx=72), dict(dx=X - 128), dict(dx=X, ld_s=80), dict(dx=RES + 2), dict(dx=RES, ld_dt=128),
+    dict(dx=BIAS), dict(dx=DB - 64)])
+def test_norms_gradient(change):
+    assert F.lib().fp8z1_rms_norm_grad(*{**GRAD, **change}.values()) == F.EINVAL
