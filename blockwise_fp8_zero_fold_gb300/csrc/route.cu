@@ -491,6 +491,11 @@ extern "C" int fp8z1_route(const void* ids, int32_t id_bytes, int64_t tokens, in
     const int64_t n = tokens * top;
     if (!offsets || (n && (!ids || !place)) || (id_bytes != 4 && id_bytes != 8)) return FP8Z1_EINVAL;
     if (!aligned(ids, id_bytes) || !aligned(offsets, 4) || !aligned(place, 4)) return FP8Z1_EALIGN;
+    {
+        // long runs of choices are read twice, and ranks wait in `place` between
+        const Area in = dense(n ? ids : nullptr, n * id_bytes), at = dense(n ? place : nullptr, n * 4), ends = dense(offsets, (experts + 1) * 4);
+        if (overlap(in, at) || overlap(in, ends) || overlap(at, ends)) return FP8Z1_EINVAL;
+    }
     NvtxRange range("fp8z1_route");
     // one CTA up to 4096 choices (a cluster's barriers cost as much as four steps), then up to 8 CTAs of 32 warps
     const int ctas = (int)std::min<int64_t>(8, std::max<int64_t>(1, ceil_div(n, 4096)));
@@ -530,7 +535,11 @@ extern "C" int fp8z1_dispatch(int64_t tokens, int64_t top, int64_t experts, int6
     if (!x || !offsets || !place || !rows || ld_x < dim || ld_rows < dim) return FP8Z1_EINVAL;
     const int64_t size = type == FP8Z1_F32 ? 4 : 2, bytes = dim * size;
     if (!aligned(x, size) || !aligned(rows, size) || !aligned(offsets, 4) || !aligned(place, 4)) return FP8Z1_EALIGN;
-    if (rows == x) return FP8Z1_EINVAL;  // tokens read what others have written
+    // tokens read what others have written
+    const Area to = {rows, tokens * top, bytes, ld_rows * size};
+    if (overlap(to, Area{x, tokens, bytes, ld_x * size}) || overlap(to, dense(offsets, (experts + 1) * 4)) ||
+        overlap(to, dense(place, tokens * top * 4)))
+        return FP8Z1_EINVAL;
     NvtxRange range("fp8z1_dispatch");
     RowArgs a = {};
     a.tokens = tokens;
@@ -561,7 +570,11 @@ extern "C" int fp8z1_combine(int64_t tokens, int64_t top, int64_t dim, const voi
     const int64_t size = type == FP8Z1_F32 ? 4 : 2;
     if (!aligned(rows, size) || !aligned(residual, size) || !aligned(y, size) || !aligned(place, 4) || !aligned(weight, 4))
         return FP8Z1_EALIGN;
-    if (y == rows) return FP8Z1_EINVAL;  // tokens read what others have written
+    // tokens read what others have written; a token its own residual
+    const Area to = {y, tokens, dim * size, ld_y * size};
+    if (overlap(to, Area{rows, tokens * top, dim * size, ld_rows * size}) || overlap(to, dense(place, tokens * top * 4)) ||
+        overlap(to, dense(weight, tokens * top * 4)) || !same_or_apart(to, Area{residual, tokens, dim * size, ld_residual * size}))
+        return FP8Z1_EINVAL;
     NvtxRange range("fp8z1_combine");
     RowArgs a = {};
     a.tokens = tokens;
@@ -596,7 +609,13 @@ extern "C" int fp8z1_combine_grad(int64_t tokens, int64_t top, int64_t experts, 
     if (!aligned(dy, size) || !aligned(rows, size) || !aligned(d_rows, size) || !aligned(offsets, 4) || !aligned(place, 4) ||
         !aligned(weight, 4) || !aligned(d_weight, 4))
         return FP8Z1_EALIGN;
-    if (d_rows == dy) return FP8Z1_EINVAL;  // tokens read what others have written
+    // tokens read what others have written; a choice its own row and weight
+    const Area to = {d_rows, tokens * top, dim * size, ld_d * size}, got = {rows, tokens * top, dim * size, ld_rows * size},
+               from = {dy, tokens, dim * size, ld_dy * size}, at = dense(place, tokens * top * 4), w = dense(weight, tokens * top * 4),
+               to_w = dense(d_weight, tokens * top * 4), ends = dense(offsets, (experts + 1) * 4);
+    if (overlap(to, from) || !same_or_apart(to, got) || overlap(to, at) || overlap(to, w) || overlap(to, to_w) || overlap(to, ends) ||
+        overlap(to_w, from) || overlap(to_w, got) || overlap(to_w, at) || overlap(to_w, ends) || !same_or_apart(to_w, w))
+        return FP8Z1_EINVAL;
     NvtxRange range("fp8z1_combine_grad");
     RowArgs a = {};
     a.tokens = tokens;

@@ -217,22 +217,23 @@ int fp8z1_checked_rms_norm_stall(uint32_t kernels);
  *   place [tokens, top]: the row of choice (t, j), -1 where there is none.
  * An expert's rows are in the order of the choices; an expert may be chosen twice by a
  * token and has two rows then.  tokens == 0 writes the offsets alone.
- * Errors: EINVAL (null, tokens < 0, tokens * top > 2^30, top outside 1 .. 64, experts
+ * Errors: EINVAL (null, a result over the other or over ids, tokens < 0, tokens * top > 2^30, top outside 1 .. 64, experts
  * outside 1 .. 1024, id_bytes), EALIGN, ECUDA. */
 int fp8z1_route(const void* ids, int32_t id_bytes, int64_t tokens, int64_t top, int64_t experts, int32_t* offsets,
                 int32_t* place, void* stream);
 
 /* rows[place[t, j]] = x[t], bit for bit; rows from offsets[experts] to tokens * top are
  * cleared.  x: [tokens, dim], rows: [tokens * top, dim], both `type`.  tokens == 0 enqueues
- * nothing.  Errors: EINVAL (as fp8z1_route, dim outside 1 .. 2^23, type, strides, rows == x), EALIGN,
- * ECUDA. */
+ * nothing.  Errors: EINVAL (as fp8z1_route, dim outside 1 .. 2^23, type, strides, rows sharing
+ * memory with what the call reads), EALIGN, ECUDA. */
 int fp8z1_dispatch(int64_t tokens, int64_t top, int64_t experts, int64_t dim, const void* x, int32_t type, int64_t ld_x,
                    const int32_t* offsets, const int32_t* place, void* rows, int64_t ld_rows, void* stream);
 
 /* y[t] = residual[t] + sum_j weight[t, j] * rows[place[t, j]] over the choices that have a
  * row, in FP32 in the order of j, the residual last, rounded once to `type`.  weight: FP32
  * [tokens, top], NULL for 1 (which is fp8z1_dispatch's gradient); residual NULL: none; y may
- * be residual itself, not rows (EINVAL).  Errors: as fp8z1_dispatch. */
+ * be residual itself (of one stride); else it shares no memory with what the call reads.  Errors: as
+ * fp8z1_dispatch. */
 int fp8z1_combine(int64_t tokens, int64_t top, int64_t dim, const void* rows, int32_t type, int64_t ld_rows,
                   const int32_t* place, const float* weight, const void* residual, int64_t ld_residual, void* y,
                   int64_t ld_y, void* stream);
@@ -240,7 +241,9 @@ int fp8z1_combine(int64_t tokens, int64_t top, int64_t dim, const void* rows, in
 /* The gradients of sum(dy * y) of fp8z1_combine:
  *   d_rows[place[t, j]] = weight[t, j] * dy[t]  (rows from offsets[experts] on are cleared),
  *   d_weight[t, j] = sum over the columns of dy[t] * rows[place[t, j]], FP32, 0 without a row.
- * The residual's is dy.  Results repeat bit for bit.  Errors: as fp8z1_dispatch (d_rows == dy). */
+ * The residual's is dy.  d_rows may be rows itself (of one stride) and d_weight weight; else a result
+ * shares no memory with the other or with what the call reads.  Results repeat bit for bit.  Errors: as
+ * fp8z1_dispatch. */
 int fp8z1_combine_grad(int64_t tokens, int64_t top, int64_t experts, int64_t dim, const void* dy, int32_t type,
                        int64_t ld_dy, const void* rows, int64_t ld_rows, const int32_t* offsets, const int32_t* place,
                        const float* weight, void* d_rows, int64_t ld_d, float* d_weight, void* stream);

@@ -68,3 +68,35 @@ def test_norm(rows, dim):
         dys, ss, dts, more = beside(dy, total, dt, torch.zeros_like(x))
         got = ops.rms_norm_grad(dys, ss, w, d_total=dts, dx=(dys, ss, dts, more)[k])
         assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+
+
+@pytest.mark.parametrize("dim", [64, 1001])
+@pytest.mark.parametrize("tokens", [1, 200])
+def test_rows(tokens, dim):
+    g = M.gen(dim)
+    top, experts = 3, 7
+    r = ops.route(torch.randint(-1, experts, (tokens, top), generator=g, device="cuda"), experts)
+    x, res, dy = (torch.randn(tokens, dim, generator=g, device="cuda").bfloat16() for _ in range(3))
+    rows = torch.randn(tokens * top, dim, generator=g, device="cuda").bfloat16()
+    w = torch.rand(tokens, top, generator=g, device="cuda")
+    got, y, d = ops.dispatch(x, r), ops.combine(rows, r, w, residual=res), ops.combine_grad(dy, rows, r, w)
+    # tokens' rows and the experts' as columns of one buffer
+    wide = torch.zeros(tokens * top, 3 * dim, dtype=BF16, device="cuda")
+    xs, out, ys = wide[:tokens, :dim], wide[:, dim:2 * dim], wide[:tokens, 2 * dim:]
+    xs.copy_(x)
+    assert torch.equal(ops.dispatch(xs, r, out=out), got) and torch.equal(xs, x)
+    out.copy_(rows)
+    xs.copy_(res)
+    assert torch.equal(ops.combine(out, r, w, residual=xs, out=ys), y) and torch.equal(out, rows) and torch.equal(xs, res)
+    assert torch.equal(ops.combine(out, r, w, residual=xs, out=xs), y) and torch.equal(out, rows)
+    xs.copy_(dy)
+    again = ops.combine_grad(xs, out, r, w, out=out)  # in the rows' place
+    assert torch.equal(again[0], d[0]) and torch.equal(again[1], d[1]) and torch.equal(xs, dy)
+    # behind one another in one buffer
+    long = torch.zeros(tokens * (top + 1), dim, dtype=BF16, device="cuda")
+    long[:tokens] = x
+    assert torch.equal(ops.dispatch(long[:tokens], r, out=long[tokens:]), got)
+    with pytest.raises(F.Fp8z1Error):
+        ops.dispatch(long[:tokens], r, out=long[tokens - 1:-1])
+    with pytest.raises(F.Fp8z1Error):
+        ops.combine(rows, r, w, out=rows[tokens:2 * tokens])

@@ -71,3 +71,44 @@ GRAD = dict(rows=40, dim=64, dy=DY, type=F.BF16, ld_dy=64, s=X, ld_s=64, w=BIAS,
     dict(dx=BIAS), dict(dx=DB - 64)])
 def test_norms_gradient(change):
     assert F.lib().fp8z1_rms_norm_grad(*{**GRAD, **change}.values()) == F.EINVAL
+
+
+ROUTE = dict(ids=X, id_bytes=4, tokens=40, top=2, experts=8, offsets=SCALES, place=Y, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(place=X), dict(place=X + 316), dict(id_bytes=8, place=X + 320), dict(offsets=X + 64), dict(offsets=Y + 16), dict(place=SCALES + 32),
+    dict(place=SCALES - 316)])
+def test_route(change):
+    assert F.lib().fp8z1_route(*{**ROUTE, **change}.values()) == F.EINVAL
+
+
+DISPATCH = dict(tokens=40, top=2, experts=8, dim=64, x=X, type=F.BF16, ld_x=64, offsets=SCALES, place=BIAS, rows=Y, ld_rows=64, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(rows=X), dict(rows=X + 128 * 39), dict(rows=X - 128 * 79), dict(rows=X + 128, ld_x=96, ld_rows=96), dict(rows=SCALES),
+    dict(rows=BIAS + 64)])
+def test_dispatch(change):
+    assert F.lib().fp8z1_dispatch(*{**DISPATCH, **change}.values()) == F.EINVAL
+
+
+COMBINE = dict(tokens=40, top=2, dim=64, rows=X, type=F.BF16, ld_rows=64, place=BIAS, w=DW, r=RES, ld_r=64, y=Y, ld_y=64, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(y=X), dict(y=X + 40 * 128), dict(y=X + 79 * 128), dict(y=X - 39 * 128), dict(y=RES + 128), dict(y=RES, ld_r=72), dict(y=BIAS),
+    dict(y=DW + 64)])
+def test_combine(change):
+    assert F.lib().fp8z1_combine(*{**COMBINE, **change}.values()) == F.EINVAL
+
+
+CGRAD = dict(tokens=40, top=2, experts=8, dim=64, dy=DY, type=F.BF16, ld_dy=64, rows=X, ld_rows=64, offsets=SCALES, place=BIAS, w=DW, d=DX,
+             ld_d=64, dw=DB, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(d=DY), dict(d=DY + 39 * 128), dict(d=DY - 79 * 128), dict(d=X + 128), dict(d=X, ld_rows=72), dict(d=BIAS), dict(d=DW), dict(d=DB),
+    dict(d=SCALES), dict(dw=DY), dict(dw=X + 64), dict(dw=BIAS), dict(dw=SCALES), dict(dw=DW + 4)])
+def test_combines_gradient(change):
+    assert F.lib().fp8z1_combine_grad(*{**CGRAD, **change}.values()) == F.EINVAL
