@@ -50,10 +50,13 @@ __device__ __forceinline__ float gate_argument(float z, int act)
 {
     return act == FP8Z1_ACT_SILU ? z : kGelu * __fmaf_rn(kCubic * z * z, z, z);
 }
+// kFine: for FP32 results.  __expf is off by more units the larger |c| is (some 100 at 80, 2^-17: nothing beside a BF16
+// rounding), expf by one at most.
+template <bool kFine>
 __device__ __forceinline__ float activate(float z, int act)
 {
     if (act == FP8Z1_ACT_NONE) return z;
-    const float c = gate_argument(z, act), t = __expf(-fabsf(c));
+    const float c = gate_argument(z, act), t = kFine ? expf(-fabsf(c)) : __expf(-fabsf(c));
     return z * __fdividef(c < 0.0f ? t : 1.0f, 1.0f + t);
 }
 // The activation's derivative: s + z s (1 - s) c', the second term 0 where t is.
