@@ -344,14 +344,14 @@ def _norm(x, weight, residual, eps, fp8, out, total, stream):
             ld_t = _fits(total, shape, dtype, dev, dim, "total")
     elif total is not None:
         _bad("total is the sum with a residual")
-    y = codes = None
+    y, codes = out, None
+    if out is not None:
+        ld_y = _fits(out, shape, dtype, dev, dim, "out")
     if fp8:
         codes = out = _new(shape, torch.float8_e4m3fn, dev, other)
         scale = _new((*shape[:-1], (dim + 127) // 128), torch.float32, dev, other)
     elif out is None:
         y = out = _new(shape, dtype, dev, other)
-    else:
-        y, ld_y = out, _fits(out, shape, dtype, dev, dim, "out")
     F.fp8z1_rms_norm(x.numel() // dim if dim else 0, dim, x, kind, ld_x, residual, ld_r, weight, eps, total, ld_t, y, ld_y,
                      codes, scale, raw)
     return out, scale, total
@@ -368,11 +368,12 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.
 
 
 def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
-                 total: Optional[torch.Tensor] = None, stream=None):
+                 out: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None, stream=None):
     """``rms_norm`` in 8 bits: (codes, scale), E4M3 codes (float8_e4m3fn) and a float32
     scale for every 128 columns, [*, ceil(dim / 128)]; with ``residual`` (codes,
-    scale, s)."""
-    codes, scale, total = _norm(x, weight, residual, eps, True, None, total, stream)
+    scale, s).  ``out`` takes the result in x's type as well, which ``linear_grad`` needs
+    where the product before it took the codes."""
+    codes, scale, total = _norm(x, weight, residual, eps, True, out, total, stream)
     return (codes, scale) if residual is None else (codes, scale, total)
 
 
