@@ -597,8 +597,8 @@ extern "C" int fp8z1_linear_timeouts(uint32_t* count)
 extern "C" int fp8z1_checked_linear_stall(uint32_t kernels)
 {
 #if FP8Z1_CHECKED
-    const int st = stall_product(kernels & 3);
-    return st == FP8Z1_OK ? stall_wgrad(kernels >> 2) : st;
+    const int st = stall_product(kernels);
+    return st == FP8Z1_OK ? stall_wgrad(kernels >> 2 & 3) : st;
 #else
     (void)kernels;
     return FP8Z1_EINVAL;

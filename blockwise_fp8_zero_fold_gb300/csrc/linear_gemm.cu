@@ -25,6 +25,8 @@
 // 61 BF16 rows of 7168 x 4096 16: the first codes' way and the split's join, not the codes' rate.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "linear.cuh"
 
 namespace fp8z1 {
@@ -39,6 +41,7 @@ namespace cg = cooperative_groups;
 __device__ unsigned g_timeouts;
 #if FP8Z1_CHECKED
 __device__ unsigned g_stall;  // bit 0: many rows, 1: few rows: the first CTA does not announce its first sums
+std::atomic<bool> g_all_few{false};  // every product by the kernel of few rows
 #endif
 
 constexpr uint32_t kOperand = 128 * 128;  // bytes of a 128 x 128 operand tile
@@ -588,7 +591,8 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
     cg::cluster_group cluster = cg::this_cluster();
 
     const int warp = of_warp((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    // the rows' tiles outermost, in one dimension of the grid (another would hold 65535, whatever the rule below takes)
+    // the rows' tiles outermost, in one dimension of the grid (another would hold 65535; the rule below takes some 1600 at
+    // most for K up to 11000, and a larger K leaves no memory for 65535: its gain is a part of a round of the SMs)
     const int tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits, m = tile / a.n_tiles, n = tile - m * a.n_tiles;
     const int token0 = m * kN;
     const int k0 = a.k_blocks * split / a.splits, k1 = a.k_blocks * (split + 1) / a.splits;
@@ -900,6 +904,9 @@ int launch(const Rows& x, const Weight& w, const Args& a, cudaStream_t s)
     if (x.T <= 16) return launch_few<kTerms, 16, kKMajor>(x, w, a, s);
     if (x.T <= 32) return launch_few<kTerms, 32, kKMajor>(x, w, a, s);
     if (x.T <= 64) return launch_few<kTerms, 64, kKMajor>(x, w, a, s);
+#if FP8Z1_CHECKED
+    if (g_all_few.load(std::memory_order_relaxed)) return launch_few<kTerms, 128, kKMajor>(x, w, a, s);
+#endif
     if (x.T <= 128 || few_tiles(x.T, a.o.N, a.k_blocks)) return launch_few<kTerms, 128, kKMajor>(x, w, a, s);
     return launch_many<kTerms, kKMajor>(x, w, a, s);
 }
@@ -932,6 +939,8 @@ int read_timeouts_product(unsigned* n)
 #if FP8Z1_CHECKED
 int stall_product(unsigned kernels)
 {
+    g_all_few.store(kernels >> 4 & 1, std::memory_order_relaxed);
+    kernels &= 3;
     return cudaMemcpyToSymbol(g_stall, &kernels, 4) == cudaSuccess ? FP8Z1_OK : FP8Z1_ECUDA;
 }
 #endif

@@ -304,7 +304,7 @@ int fp8z1_linear_grad(const fp8z1_linear_dims* dims, const void* dy, int64_t ld_
 int fp8z1_linear_timeouts(uint32_t* count);
 
 /* As fp8z1_checked_ffn_stall.  Bits: 1 products of many rows, 2 of few, 4 d_weight, 8 d_weight of a
- * transposed weight. */
+ * transposed weight; 16 stalls nothing, but lets the kernel of few rows make every product. */
 int fp8z1_checked_linear_stall(uint32_t kernels);
 
 #ifdef __cplusplus
