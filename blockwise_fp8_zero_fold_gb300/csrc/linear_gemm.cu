@@ -129,7 +129,7 @@ __device__ __forceinline__ void finish(const Out& o, const uint64_t (&sums)[8], 
         }
         if (o.act != FP8Z1_ACT_NONE)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = activate<true>(v[j], o.act);  // for BF16 rows too: two of it here cost 5 %
+            for (int j = 0; j < 8; ++j) v[j] = activate(v[j], o.act);
         if (o.residual && here) {
             const bf16* p = o.residual + row * o.ld_r + c;
             if (whole && o.vec_r) {
@@ -235,16 +235,12 @@ __device__ __forceinline__ void finish_whole(const Out& o, const float (&sums)[2
             }
         if constexpr (kMore) {
             if (o.pre) leave_floats(v, o.pre + first * o.N + c, o.N);
-            if (o.act != FP8Z1_ACT_NONE && o.f32) {
+            if (o.act == FP8Z1_ACT_SILU)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = activate<true>(v[j], o.act);
-            } else if (o.act == FP8Z1_ACT_SILU) {
+                for (int j = 0; j < 16; ++j) v[j] = activate(v[j], FP8Z1_ACT_SILU);
+            else if (o.act != FP8Z1_ACT_NONE)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = activate<false>(v[j], FP8Z1_ACT_SILU);
-            } else if (o.act != FP8Z1_ACT_NONE) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = activate<false>(v[j], FP8Z1_ACT_GELU_TANH);
-            }
+                for (int j = 0; j < 16; ++j) v[j] = activate(v[j], FP8Z1_ACT_GELU_TANH);
             if (o.residual && lane < rows) {
                 const uint4* p = reinterpret_cast<const uint4*>(o.residual + (first + lane) * o.ld_r + c);
 #pragma unroll
@@ -763,7 +759,7 @@ few_kernel(const __grid_constant__ CUtensorMap map_hi, const __grid_constant__ C
         if (row >= o.T || col >= o.N) return;
         z += bias;
         if (o.pre) o.pre[row * o.N + col] = z;
-        float v = o.f32 ? activate<true>(z, o.act) : activate<false>(z, o.act);
+        float v = activate(z, o.act);
         if (o.residual) v += to_float(o.residual[row * o.ld_r + col]);
         if (o.f32)
             static_cast<float*>(o.y)[row * o.ld_y + col] = v;

@@ -30,3 +30,16 @@ def test_small_results_keep_their_bits(tokens, rows, cols, transposed, act, lo, 
     # less than 2^-20.  c of GELU: two constants and four operations, 6 of 2^-24 relative to c, and exp passes |c| times that on.
     tol = 2.0**-20 + (0 if act == "silu" else 6 * 2.0**-24 * c.abs())
     assert ((y.double() - want).abs() <= tol * want.abs() + 1e-44).all()
+
+
+@pytest.mark.parametrize("tokens", [5, 700])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_same_bits_in_rows_of_any_stride(tokens, act, dtype):
+    g = M.gen(tokens)
+    codes, scale = R.fp8_weight(g, 256, 20480)
+    x = torch.randn(tokens, 256, generator=g, device="cuda").bfloat16()
+    y = ops.linear(x, codes, scale, activation=act, dtype=dtype)
+    for pad, at in ((1, 0), (0, 1), (8, 0)):
+        out = M.strided(torch.zeros_like(y), pad, at)
+        assert torch.equal(ops.linear(x, codes, scale, activation=act, dtype=dtype, out=out), y)
