@@ -5,8 +5,8 @@
 // Backward: dz = dy act'(z) to pairs, its columns' sums; dx, a product with the weight turned;
 //           d_weight, of dy and x as they lie when dz is dy in BF16, else of FP16 terms.
 //
-// 2051 rows of 4096 to 14336 with a bias and GELU: pairs 9 us and product 194; dz 97, dx 156, x's FP16 terms beside
-// them, d_weight 302, the bias's gradient 4.
+// 2051 rows of 4096 to 14336 with a bias, GELU and z saved: pairs 9 us and product 202; dz 96, dx 161, x's FP16 terms
+// (24 for 2048 rows of 7168; they start when dx has ended), d_weight 306, the bias's gradient 4.
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -117,8 +117,8 @@ struct DzArgs {
 // from its one read on: pairs for dx (a row's 128 share a scale), FP16 terms for d_weight
 // (a column's 256 do: two CTAs tell each other their largest), the columns' sums.  The terms: a
 // column's largest number is brought to 2^14, so that columns of small numbers keep their 22
-// bits beside large ones.  2051 rows of 14336 with an activation take 97 us, 3.6 TB/s (256 rows by a CTA of 1024
-// threads, which loads and stores by turns, 123).
+// bits beside large ones.  2051 rows of 14336 with an activation take 96 us, 3.6 TB/s (256 rows by a CTA of 1024
+// threads, which loads and stores by turns, 123); its 64 registers spill 15 of BF16 dy's.
 constexpr int kDzRows = kTall / 2;
 template <class D, bool kAct, bool kTerms>
 __global__ void __launch_bounds__(512, 2) dz_kernel(const DzArgs a)
@@ -175,6 +175,8 @@ __global__ void __launch_bounds__(512, 2) dz_kernel(const DzArgs a)
         for (int r = 0; r < 8; ++r) {
             if (r0 + r >= a.T) break;
             const float amax = fmaxf(fmaxf(fabsf(v[r][0]), fabsf(v[r][1])), fmaxf(fabsf(v[r][2]), fabsf(v[r][3])));
+            // FP32 dz in two E4M3 terms: 9 bits, one more than a BF16 gradient would hand to dx's product, and dx is off by
+            // 1.8e-3 of its norm (its own rounding 1.66e-3).  A third term would make that product half as long again.
             const PairScale ps = pair_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
             uint32_t h0, l0, h1, l1;
             pair_encode<kExact ? Lo::kE5M2 : Lo::kE4M3>(v[r][0], v[r][1], ps.up, h0, l0);

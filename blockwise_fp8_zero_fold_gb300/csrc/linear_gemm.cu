@@ -18,10 +18,10 @@
 // the columns': the products' time follows the rows, and the codes are what is read.  K is
 // split over a cluster's CTAs, whose sums are added in shared memory in their order.
 //
-// Many rows: 4096 8-bit rows of 7168 x 4096 take 118 us, 2.0 PFLOP/s, 8192 205 us, 2.3 PFLOP/s: the additions and the
+// Many rows: 4096 8-bit rows of 7168 x 4096 take 120 us, 2.0 PFLOP/s, 8192 207 us, 2.3 PFLOP/s: the additions and the
 // way from product to additions and back bound it, and 256 tiles are 3.4 rounds of 76 pairs.  2051
-// BF16 rows of 4096 x 14336 168 us, 1.4 PFLOP/s (a ninth of the tiles' rows is padding), with GELU and the saved z 206: the
-// end of a tile, which nothing overlaps.  Few rows, in a captured graph with cold caches: 1 8-bit row of 4096 x 14336 14 us,
+// BF16 rows of 4096 x 14336 169 us with the 9 of their pairs, 1.4 PFLOP/s (a ninth of the tiles' rows is padding), with GELU
+// and the saved z 215: the end of a tile, which nothing overlaps.  Few rows, in a captured graph with cold caches: 1 8-bit row of 4096 x 14336 14 us,
 // 61 BF16 rows of 7168 x 4096 16: the first codes' way and the split's join, not the codes' rate.
 #include <cooperative_groups.h>
 
@@ -179,7 +179,7 @@ __device__ __forceinline__ void finish(const Out& o, const uint64_t (&sums)[8], 
 // The same for a warp's columns n0 .. n0 + 31 and n0 + 128 .. n0 + 159 of 32 rows where all lies on 16 bytes; without
 // kMore a bias at most and BF16 rows.  The products of a tile run two steps on while its results leave, so what
 // `finish` asks of every element cost 1400 to 2200 clocks a 16 columns: 8192 8-bit rows of 7168 x 4096 217 us with it, 205
-// with this, 2051 BF16 rows of 4096 x 14336 179 and 168, with GELU and z 214 and 206.  In a kernel without `finish`: beside it
+// with this, 2051 BF16 rows of 4096 x 14336 179 and 168, with GELU by __expf and z 214 and 206.  In a kernel without `finish`: beside it
 // the sums of the loop spilled.
 bool is_whole(const Out& o)
 {

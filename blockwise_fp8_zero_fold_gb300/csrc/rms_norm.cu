@@ -13,7 +13,7 @@
 // registers alone hold too few bytes under way (159 us for 8192 rows of 7168).
 //
 // With rows of 7168 BF16: 16384 with a residual to 8 bits 133 us, 6.2 TB/s; 8192 forward 66 us, 7.1 TB/s,
-// their gradient 90 us, 5.2 TB/s, and 4 us for the columns' sums.  32 rows 3 us from a captured graph.  2003 rows of
+// their gradient 91 us, 5.2 TB/s, and 4 us for the columns' sums.  32 rows 3 us from a captured graph.  2003 rows of
 // 4097 FP32, single elements: 15 and 26 us, the gradient at 3.8 TB/s, bound by its instructions.
 #include <algorithm>
 #include <mutex>
@@ -595,9 +595,11 @@ constexpr int kWarpDim = 1024;  // up to here a warp has a row
 int threads_of(int64_t dim, int each) { return (int)ceil_div(dim, each * 32) * 32; }
 // The gradient's ring: a CTA an SM, of 15 warps and the one that copies, for 128 registers a thread; as many elements a
 // thread as they hold of three inputs and the weight's sums (groups of 28 warps at 8 elements took 120 us for 8192 rows
-// of 7168 BF16, two of 14 at 16 with spilled registers 189, this 90).  Single elements 16, as 32 spill: 8192 rows of 7169
-// BF16 329 us, at 16 147.  19 warps and 96 registers where they hold two rows and 15 one: 2003 rows of 4097 FP32 33 us
-// for 38, 8192 of BF16 83 for 132; of other widths they spill (7169 FP32 187 for 128) or gain nothing.
+// of 7168 BF16, two of 14 at 16 with spilled registers 189, this 91).  Single elements 16, as 32 spill some 80 registers:
+// 8192 rows of 7169 BF16 329 us, at 16 150; beyond 7680, where 15 warps no longer hold a row at 16, they take 32 all the
+// same (4096 rows of 7681 BF16 189 us, of 16383 215).  19 warps and 96 registers where they hold two rows and 15 one, from
+// 3585 to 4608: 2003 rows of 4097 FP32 32 us for 38, 8192 of BF16 86 for 132; single FP32 elements spill 13 registers
+// there, other widths more (7169 FP32 187 for 128), or gain nothing.
 constexpr int kRingSmem = 224 * 1024;
 int ring_each(int64_t dim, int size, bool vec) { return dim > 7680 || (size == 2 && vec) ? 32 : 16; }
 int ring_groups(int64_t dim, int each)
