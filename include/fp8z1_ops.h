@@ -294,7 +294,7 @@ int fp8z1_linear(const fp8z1_linear_dims* dims, const void* x, int64_t ld_x, con
  * significant bits (BF16 has 8) or 2^-17 of the largest of its 128 neighbours.  d_weight
  * and d_bias are FP32 sums of dz as it is, d_weight of every column relative to its own size (x: what
  * lies above 2^-31 of the largest of 256 rows x 128 columns): each 256 rows' sum is within 7e-7 of its
- * norm, and these are added one after the other (8 million rows: 1e-5).  Every element is written.
+ * norm, and these are added one after the other (3e-6 at 8 million rows).  Every element is written.
  * Errors: EINVAL (E4M3 x too), EALIGN (workspace: 256 bytes), ECUDA. */
 int fp8z1_linear_grad(const fp8z1_linear_dims* dims, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
                       const uint8_t* codes, const float* scales, const float* pre, void* dx, int64_t ld_dx,
